@@ -32,6 +32,8 @@ ORDERS = {"head_first": ORDER_HEAD_FIRST, "block_first": ORDER_BLOCK_FIRST,
 # forward tile schemes, OR-ed into tile_order (0: the library's choice)
 FWD_SINGLE_CTA = 0x100
 FWD_CTA_PAIR = 0x200
+# frequency rules of rope_freqs
+ROPE_RULES = {"plain": 0, "linear": 1, "base": 2, "by_parts": 3}
 SCHEMES = {"auto": 0, "single": FWD_SINGLE_CTA, "pair": FWD_CTA_PAIR}
 
 # Every symbol include/attn.h declares, with (restype, argtypes).
@@ -42,6 +44,9 @@ _LL = ctypes.c_longlong
 _SZ = ctypes.c_size_t
 _IP = ctypes.POINTER(ctypes.c_int)
 _FP = ctypes.POINTER(ctypes.c_float)
+_D = ctypes.c_double
+_DP = ctypes.POINTER(ctypes.c_double)
+_LLP = ctypes.POINTER(ctypes.c_longlong)
 SIGNATURES = {
     "attn_fwd": (_I, [_P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _F, _I, _P]),
     "attn_fwd_ex": (_I, [_P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _F, _I, _I, _P]),
@@ -60,6 +65,9 @@ SIGNATURES = {
     "attn_decode_varlen": (_I, [_P, _P, _P, _P, _P, _I, _I, _I, _I, _F, _I, _P, _SZ, _P]),
     "attn_decode_varlen_workspace_bytes": (_SZ, [_I, _I, _I, _I]),
     "attn_decode_num_splits": (_I, [_I, _I, _I, _I]),
+    "attn_rope": (_I, [_P, _P, _P, _P, _P, _LL, _P, _I, _I, _I, _I, _I, _I, _I, _F, _I, _LLP, _P]),
+    "attn_rope_freqs": (_I, [_DP, _I, _D, _I, _D, _D, _D, _D]),
+    "attn_rope_append": (_I, [_P] * 13 + [_I] * 7 + [_F, _I, _LLP, _P]),
     "attn_tile_map": (_I, [_I, _I, _I, _I, _I, _I, _LL, _IP, _IP, _IP]),
     "attn_tile_map_die_split": (_I, [_I, _I, _I, _I, _I, _I, _LL, _IP, _IP, _IP]),
     "attn_bwd_tile_map": (_I, [_I, _I, _I, _I, _I, _I, _LL, _IP, _IP, _IP]),
@@ -326,7 +334,162 @@ def attn_version() -> int:
     return int(lib().attn_version())
 
 
+def _strides(*triples):
+    """Host array of (batch, head, token) element strides, or None (contiguous)."""
+    flat = [x for t in triples for x in t]
+    return (ctypes.c_longlong * len(flat))(*flat)
+
+
+def attn_rope(q, q_out, k, k_out, positions, position_stride, inv_freq, B, Hq, Hkv, N, d, rotary_dim, interleaved,
+              out_scale, inverse, strides=None, stream=None) -> int:
+    return lib().attn_rope(_ptr(q), _ptr(q_out), _ptr(k), _ptr(k_out), _ptr(positions), position_stride,
+                           _ptr(inv_freq), B, Hq, Hkv, N, d, rotary_dim, int(bool(interleaved)), out_scale,
+                           int(bool(inverse)), strides, _stream(stream))
+
+
+def attn_rope_append(q, q_out, k, v, kcache, vcache, seqlens, start_pos, new_lens, seqlens_out, cache_pos, weights,
+                     inv_freq, B, Hq, Hkv, T, d, rotary_dim, interleaved, out_scale, max_seqlen, strides=None,
+                     stream=None) -> int:
+    return lib().attn_rope_append(_ptr(q), _ptr(q_out), _ptr(k), _ptr(v), _ptr(kcache), _ptr(vcache), _ptr(seqlens),
+                                  _ptr(start_pos), _ptr(new_lens), _ptr(seqlens_out), _ptr(cache_pos), _ptr(weights),
+                                  _ptr(inv_freq), B, Hq, Hkv, T, d, rotary_dim, int(bool(interleaved)), out_scale,
+                                  max_seqlen, strides, _stream(stream))
+
+
+def attn_rope_freqs(rotary_dim, base=10000.0, rule=0, factor=1.0, low=1.0, high=4.0, trained_len=8192.0):
+    """List of rotary_dim / 2 frequencies (radians per position) by one of ROPE_RULES."""
+    buf = (ctypes.c_double * max(int(rotary_dim) // 2, 1))()
+    check(lib().attn_rope_freqs(buf, int(rotary_dim), base, int(rule), factor, low, high, trained_len),
+          "attn_rope_freqs")
+    return list(buf)
+
+
 # ----------------------------------------------------------- torch helpers
+def _expect(what, t, name, dtype, shape, device, packed=True):
+    """Refuse (ATTN_ERR_ARG) a tensor that the call cannot take as it is: its
+    address alone would not tell the library."""
+    if (t.dtype is dtype and tuple(t.shape) == tuple(shape) and t.device == device and t.is_cuda
+            and (t.is_contiguous() if packed else t.stride(-1) == 1)):
+        return
+    raise AttnError(ATTN_ERR_ARG, f"{what}: {name} has to be {dtype} {tuple(shape)} on {device}"
+                                  f"{', contiguous' if packed else ', with contiguous columns'} and on a GPU "
+                                  f"(got {t.dtype} {tuple(t.shape)} on {t.device}, strides {tuple(t.stride())})")
+
+
+class _on:
+    """The tensors' device as the current one for the length of a call; free
+    when it is current already."""
+
+    def __init__(self, device):
+        import torch
+        self._guard = None if device.index == torch.cuda.current_device() else torch.cuda.device(device)
+
+    def __enter__(self):
+        if self._guard is not None:
+            self._guard.__enter__()
+
+    def __exit__(self, *exc):
+        if self._guard is not None:
+            self._guard.__exit__(*exc)
+
+
+def rope_freqs(rotary_dim, base=10000.0, rule="plain", factor=1.0, low=1.0, high=4.0, trained_len=8192.0,
+               device=None):
+    """The frequencies of attn_rope_freqs as an fp64 CUDA tensor, for `rope`
+    and `rope_append` (make it once and keep it)."""
+    import torch
+    f = attn_rope_freqs(rotary_dim, base, ROPE_RULES[rule], factor, low, high, trained_len)
+    return torch.tensor(f, dtype=torch.float64, device="cuda" if device is None else device)
+
+
+def rope(q, k, inv_freq, positions=None, interleaved=False, out_scale=1.0, out=None, inverse=False, stream=None):
+    """Rotate ``[B, H, N, d]`` bf16 CUDA tensors (any strides with contiguous
+    columns, so a fused projection's views too) by attn_rope; `k` may be None.
+    `positions` is ``[N]`` or ``[B, N]`` int32, or None for 0..N-1; rotary_dim
+    is twice the length of `inv_freq`.  Returns ``(q_out, k_out)``: contiguous
+    tensors as attn_fwd takes them, or `out`, which may be ``(q, k)``."""
+    import torch
+    if q.dim() != 4 or (k is not None and k.dim() != 4):
+        raise AttnError(ATTN_ERR_ARG, "rope: q and k have to be [B, H, N, d]")
+    (B, Hq, N, d), dev, Hkv = q.shape, q.device, 0
+    bf16 = torch.bfloat16
+    _expect("rope", q, "q", bf16, q.shape, dev, packed=False)
+    if k is not None:
+        Hkv = k.shape[1]
+        _expect("rope", k, "k", bf16, (B, Hkv, N, d), dev, packed=False)
+    _expect("rope", inv_freq, "inv_freq", torch.float64, (inv_freq.numel(),), dev)
+    per_entry = 0
+    if positions is not None:
+        per_entry = N if positions.dim() == 2 else 0
+        _expect("rope", positions, "positions", torch.int32, (B, N) if per_entry else (N,), dev)
+    if out is None:
+        q_out = torch.empty((B, Hq, N, d), dtype=bf16, device=dev)
+        k_out = None if k is None else torch.empty((B, Hkv, N, d), dtype=bf16, device=dev)
+    else:
+        q_out, k_out = out
+        _expect("rope", q_out, "q_out", bf16, q.shape, dev, packed=False)
+        if (k is None) != (k_out is None):
+            raise AttnError(ATTN_ERR_ARG, "rope: out has to hold k_out exactly where there is a k")
+        if k is not None:
+            _expect("rope", k_out, "k_out", bf16, k.shape, dev, packed=False)
+    none = (0, 0, 0)
+    with _on(dev):
+        check(attn_rope(q, q_out, k, k_out, positions, per_entry, inv_freq, B, Hq, Hkv, N, d, 2 * inv_freq.numel(),
+                        interleaved, out_scale, inverse,
+                        _strides(q.stride()[:3], q_out.stride()[:3], none if k is None else k.stride()[:3],
+                                 none if k is None else k_out.stride()[:3]), stream), "attn_rope")
+    return q_out, k_out
+
+
+def rope_backward(dq, dk, inv_freq, positions=None, interleaved=False, out_scale=1.0, out=None, stream=None):
+    """Gradients of `rope` (the arguments it was called with): from those of
+    its outputs to those of its inputs; returns ``(dq_in, dk_in)``."""
+    return rope(dq, dk, inv_freq, positions, interleaved, out_scale, out, True, stream)
+
+
+def rope_append(q, k, v, kcache, vcache, seqlens, inv_freq=None, start_pos=None, new_lens=None, interleaved=False,
+                out_scale=1.0, cache_pos=None, weights=None, q_out=None, seqlens_out=None, stream=None):
+    """Rotate the new tokens' q ``[B, Hq, T, d]`` and append their rotated k
+    and their v ``[B, Hkv, T, d]`` (any strides with contiguous columns) to the
+    caches by attn_rope_append; without `inv_freq` nothing is rotated.
+    Allocates the outputs that are not given; returns ``(q_out,
+    seqlens_out)``."""
+    import torch
+    if q.dim() != 4 or kcache.dim() != 4:
+        raise AttnError(ATTN_ERR_ARG, "rope_append: q has to be [B, Hq, T, d], the caches [B, Hkv, max_seqlen, d]")
+    (B, Hq, T, d), dev, Hkv, s_max = q.shape, q.device, kcache.shape[1], kcache.shape[2]
+    bf16, i32, what = torch.bfloat16, torch.int32, "rope_append"
+    _expect(what, q, "q", bf16, q.shape, dev, packed=False)
+    _expect(what, k, "k", bf16, (B, Hkv, T, d), dev, packed=False)
+    _expect(what, v, "v", bf16, (B, Hkv, T, d), dev, packed=False)
+    _expect(what, kcache, "kcache", bf16, (B, Hkv, s_max, d), dev)
+    _expect(what, vcache, "vcache", bf16, (B, Hkv, s_max, d), dev)
+    for name, t in (("seqlens", seqlens), ("start_pos", start_pos), ("new_lens", new_lens),
+                    ("seqlens_out", seqlens_out)):
+        if t is not None:
+            _expect(what, t, name, i32, (B,), dev)
+    rotary_dim = 0
+    if inv_freq is not None:
+        rotary_dim = 2 * inv_freq.numel()
+        _expect(what, inv_freq, "inv_freq", torch.float64, (rotary_dim // 2,), dev)
+    if cache_pos is not None:
+        _expect(what, cache_pos, "cache_pos", i32, (B, Hkv, s_max), dev)
+    if weights is not None:
+        _expect(what, weights, "weights", torch.float32, (B, Hkv, s_max), dev)
+    if q_out is None:
+        q_out = torch.empty((B, Hq, T, d), dtype=bf16, device=dev)
+    else:
+        _expect(what, q_out, "q_out", bf16, q.shape, dev, packed=False)
+    if seqlens_out is None:
+        seqlens_out = torch.empty_like(seqlens)
+    with _on(dev):
+        check(attn_rope_append(q, q_out, k, v, kcache, vcache, seqlens, start_pos, new_lens, seqlens_out, cache_pos,
+                               weights, inv_freq, B, Hq, Hkv, T, d, rotary_dim, interleaved, out_scale, s_max,
+                               _strides(q.stride()[:3], q_out.stride()[:3], k.stride()[:3], v.stride()[:3]), stream),
+              "attn_rope_append")
+    return q_out, seqlens_out
+
+
 def forward(q, k, v, causal=False, scale=None, tile_order=ORDER_HEAD_FIRST, with_lse=True,
             stream=None):
     """Allocate outputs and run attn_fwd_ex on ``[B, H, N, d]`` bf16 CUDA tensors."""

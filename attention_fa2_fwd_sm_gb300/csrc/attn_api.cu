@@ -594,6 +594,145 @@ int attn_decode_noalloc(const void *q, const void *kcache, const void *vcache, c
                        scratch, cap, stream);
 }
 
+// Rotary positions.  The two tables of strides hold (batch, head, token) per
+// tensor; a stride of a dimension of extent 1 is never used and set to 0.
+static bool rope_strides(const long long *s, bool output, int B, int H, int N, int d, long long *out) {
+    const long long extent[3] = {B, H, N};
+    const long long packed[3] = {(long long)H * N * d, (long long)N * d, d};
+    for (int i = 0; i < 3; ++i) {
+        long long v = s ? s[i] : packed[i];
+        if (extent[i] == 1) v = 0;
+        else if (v % 8 || v < (output ? d : 0) || v >= (1LL << 40)) return false;
+        out[i] = v;
+    }
+    return true;
+}
+
+static int rope_tensor(RopeTensor *t, const void *in, void *out, const long long *in_s, const long long *out_s, int B,
+                       int H, int N, int d) {
+    long long a[3], b[3];
+    if (!aligned16(in) || !aligned16(out)) return ATTN_ERR_ARG;
+    if (!rope_strides(in_s, false, B, H, N, d, a) || !rope_strides(out_s, true, B, H, N, d, b)) return ATTN_ERR_ARG;
+    if (in == out && (a[0] != b[0] || a[1] != b[1] || a[2] != b[2])) return ATTN_ERR_ARG;
+    t->in = static_cast<const __nv_bfloat16 *>(in);
+    t->out = static_cast<__nv_bfloat16 *>(out);
+    t->in_b = a[0], t->in_h = a[1], t->in_n = a[2];
+    t->out_b = b[0], t->out_h = b[1], t->out_n = b[2];
+    t->heads = H;
+    return ATTN_OK;
+}
+
+static bool aligned4(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
+static int rope_common(const double *inv_freq, int B, int Hq, int N, int d, int rotary_dim, float out_scale,
+                       int min_rotary) {
+    if (B <= 0 || Hq <= 0 || N <= 0) return ATTN_ERR_ARG;
+    if (d <= 0 || d % 8 || d > 512) return ATTN_ERR_UNSUPPORTED;
+    if (rotary_dim < min_rotary || rotary_dim > d || rotary_dim % 2) return ATTN_ERR_ARG;
+    if (rotary_dim > 0 && (!inv_freq || (reinterpret_cast<uintptr_t>(inv_freq) & 7u))) return ATTN_ERR_ARG;
+    if (!std::isfinite(out_scale)) return ATTN_ERR_ARG;
+    return ATTN_OK;
+}
+
+int attn_rope(const void *q, void *q_out, const void *k, void *k_out, const int *positions, long long position_stride,
+              const double *inv_freq, int B, int Hq, int Hkv, int N, int d, int rotary_dim, int interleaved,
+              float out_scale, int inverse, const long long *strides, attn_stream_t stream) {
+    int rc = rope_common(inv_freq, B, Hq, N, d, rotary_dim, out_scale, 2);
+    if (rc != ATTN_OK) return rc;
+    if (!aligned4(positions) || position_stride < 0 || (!k != !k_out) || (k && Hkv <= 0)) return ATTN_ERR_ARG;
+    RopeLaunch a;
+    rc = rope_tensor(&a.t[0], q, q_out, strides, strides ? strides + 3 : nullptr, B, Hq, N, d);
+    if (rc == ATTN_OK && k)
+        rc = rope_tensor(&a.t[1], k, k_out, strides ? strides + 6 : nullptr, strides ? strides + 9 : nullptr, B, Hkv, N, d);
+    if (rc != ATTN_OK) return rc;
+    a.inv_freq = inv_freq;
+    a.pos = positions;
+    a.pos_stride = position_stride;
+    a.B = B;
+    a.N = N;
+    a.d = d;
+    a.rotary_dim = rotary_dim;
+    a.interleaved = interleaved ? 1 : 0;
+    a.inverse = inverse ? 1 : 0;
+    a.out_scale = out_scale;
+    a.num_sms = current_num_sms();
+    if (a.num_sms <= 0) return note_cuda_error(cudaErrorNoDevice, "device query");
+    return rope_launch(a, reinterpret_cast<cudaStream_t>(stream));
+}
+
+int attn_rope_freqs(double *inv_freq, int rotary_dim, double base, int rule, double factor, double low, double high,
+                    double trained_len) {
+    if (!inv_freq || rotary_dim < 2 || rotary_dim % 2 || !(base > 1.0) || !std::isfinite(base)) return ATTN_ERR_ARG;
+    if (rule < ATTN_ROPE_PLAIN || rule > ATTN_ROPE_BY_PARTS) return ATTN_ERR_ARG;
+    if (rule != ATTN_ROPE_PLAIN && (!(factor > 0.0) || !std::isfinite(factor))) return ATTN_ERR_ARG;
+    if (rule == ATTN_ROPE_BASE) {
+        if (rotary_dim < 4) return ATTN_ERR_ARG;
+        base *= std::pow(factor, double(rotary_dim) / (rotary_dim - 2));
+    }
+    if (rule == ATTN_ROPE_BY_PARTS && (!(low < high) || !std::isfinite(high - low) || !(trained_len > 0.0) || !std::isfinite(trained_len)))
+        return ATTN_ERR_ARG;
+    for (int i = 0; i < rotary_dim / 2; ++i) {
+        double f = std::pow(base, -2.0 * i / rotary_dim);
+        if (rule == ATTN_ROPE_LINEAR) f /= factor;
+        if (rule == ATTN_ROPE_BY_PARTS) {
+            double g = (trained_len * f / 6.283185307179586476925 - low) / (high - low);
+            g = g < 0.0 ? 0.0 : (g > 1.0 ? 1.0 : g);
+            f *= g + (1.0 - g) / factor;
+        }
+        inv_freq[i] = f;
+    }
+    return ATTN_OK;
+}
+
+static bool ints_overlap(const int *a, const int *b, int n) { return a && b && a < b + n && b < a + n; }
+
+int attn_rope_append(const void *q, void *q_out, const void *k, const void *v, void *kcache, void *vcache,
+                     const int *seqlens, const int *start_pos, const int *new_lens, int *seqlens_out, int *cache_pos,
+                     float *weights, const double *inv_freq, int B, int Hq, int Hkv, int T, int d, int rotary_dim,
+                     int interleaved, float out_scale, int max_seqlen, const long long *strides, attn_stream_t stream) {
+    int rc = rope_common(inv_freq, B, Hq, T, d, rotary_dim, out_scale, 0);
+    if (rc != ATTN_OK) return rc;
+    if (Hkv <= 0 || max_seqlen <= 0 || !seqlens) return ATTN_ERR_ARG;
+    for (const void *ptr : {(const void *)seqlens, (const void *)start_pos, (const void *)new_lens,
+                            (const void *)seqlens_out, (const void *)cache_pos, (const void *)weights})
+        if (!aligned4(ptr)) return ATTN_ERR_ARG;
+    if (ints_overlap(seqlens_out, seqlens, B) || ints_overlap(seqlens_out, start_pos, B) ||
+        ints_overlap(seqlens_out, new_lens, B))
+        return ATTN_ERR_ARG;
+    if (!aligned16(kcache) || !aligned16(vcache) || kcache == vcache) return ATTN_ERR_ARG;
+    const long long row = (long long)max_seqlen * d;
+    if ((double)B * Hkv * (double)row >= 9.0e18) return ATTN_ERR_ARG;
+    RopeLaunch a;
+    rc = rope_tensor(&a.t[0], q, q_out, strides, strides ? strides + 3 : nullptr, B, Hq, T, d);
+    // The caches' strides are their own, so they are set apart from the inputs'.
+    for (int i = 1; rc == ATTN_OK && i < 3; ++i) {
+        rc = rope_tensor(&a.t[i], i == 1 ? k : v, i == 1 ? kcache : vcache, strides ? strides + 3 + 3 * i : nullptr,
+                         nullptr, B, Hkv, T, d);
+        a.t[i].out_b = Hkv * row;
+        a.t[i].out_h = row;
+        a.t[i].out_n = d;
+    }
+    if (rc != ATTN_OK) return rc;
+    a.inv_freq = inv_freq;
+    a.pos = start_pos;
+    a.B = B;
+    a.N = T;
+    a.d = d;
+    a.rotary_dim = rotary_dim;
+    a.interleaved = interleaved ? 1 : 0;
+    a.out_scale = out_scale;
+    a.append = true;
+    a.lens = seqlens;
+    a.new_lens = new_lens;
+    a.lens_out = seqlens_out;
+    a.cache_pos = cache_pos;
+    a.weights = weights;
+    a.max_seqlen = max_seqlen;
+    a.num_sms = current_num_sms();
+    if (a.num_sms <= 0) return note_cuda_error(cudaErrorNoDevice, "device query");
+    return rope_launch(a, reinterpret_cast<cudaStream_t>(stream));
+}
+
 int attn_device_status(attn_stream_t stream) {
     if (cudaStreamSynchronize(reinterpret_cast<cudaStream_t>(stream)) != cudaSuccess)
         return ATTN_ERR_CUDA;

@@ -5,6 +5,7 @@
 #include <cstddef>
 #include <cstdint>
 #include <cuda.h>
+#include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
 namespace attn {
@@ -124,6 +125,30 @@ struct FwdSplitLaunch {
     int num_sms;
 };
 int fwd_split_launch(const FwdSplitLaunch &a, cudaStream_t stream);
+
+// Rotary positions (rope_sm103.cu).  Element strides of one tensor
+// [B, heads, N, d] (d contiguous) on its way in and out; heads = 0: absent.
+struct RopeTensor {
+    const __nv_bfloat16 *in = nullptr;
+    __nv_bfloat16 *out = nullptr;
+    long long in_b = 0, in_h = 0, in_n = 0, out_b = 0, out_h = 0, out_n = 0;
+    int heads = 0;
+};
+struct RopeLaunch {
+    RopeTensor t[3];  // q, k; appending also v (copied), with k and v going to the caches' rows
+    const double *inv_freq;
+    const int *pos;  // rope: [B, N], pos_stride a batch entry (null: 0..N-1); append: [B] (null: the lengths)
+    long long pos_stride = 0;
+    int B, N, d, rotary_dim, interleaved, inverse = 0;
+    float out_scale;
+    bool append = false;
+    const int *lens = nullptr, *new_lens = nullptr;
+    int *lens_out = nullptr, *cache_pos = nullptr;
+    float *weights = nullptr;
+    int max_seqlen = 0;
+    int num_sms;
+};
+int rope_launch(const RopeLaunch &a, cudaStream_t stream);
 int decode_launch(const DecodeLaunch &a, cudaStream_t stream);
 int bwd_launch(const BwdLaunch &a, cudaStream_t stream);
 

@@ -27,8 +27,8 @@
  *  - Return value: ATTN_OK (0) or one of the negative ATTN_ERR_* codes.
  *    attn_strerror() gives a message for each.
  *  - CUDA graphs: the launches of attn_fwd, attn_fwd_ex, attn_fwd_host,
- *    attn_bwd and the decode entry points can be captured into a CUDA graph
- *    on `stream` and replayed; a replay reads what the buffers hold at replay
+ *    attn_bwd, the decode entry points, attn_rope and attn_rope_append can be
+ *    captured into a CUDA graph on `stream` and replayed; a replay reads what the buffers hold at replay
  *    time (the ragged decode's seqlens included: it plans on the device).
  *    Make one ordinary call per device first (it sets up per-device state:
  *    kernel attributes, scratch addresses, the die map, the host-copy
@@ -403,6 +403,99 @@ size_t attn_decode_workspace_bytes(int B, int Hq, int d, int num_splits);
  * least 4096 keys and the grid stays within 4 CTAs per SM.  Returns a value >= 1 (or a negative
  * error code for bad arguments).  Queries the current device's SM count once. */
 int attn_decode_num_splits(int B, int Hq, int Hkv, int max_seqlen);
+
+/*
+ * Rotary positions.  For a token at position p, pair i of a head's first
+ * rotary_dim columns is turned by the angle a = p * inv_freq[i]:
+ *     (x, y) -> out_scale * (x cos a - y sin a, y cos a + x sin a),
+ * i = 0 .. rotary_dim / 2 - 1.  interleaved = 0: pair i is columns (i,
+ * i + rotary_dim / 2); interleaved != 0: columns (2 i, 2 i + 1).  Columns from
+ * rotary_dim on are copied unchanged.  inverse != 0 turns by -a, which is the
+ * gradient: if y = rope(x), then dx = rope(dy) with inverse set and the same
+ * out_scale.  Angles are reduced exactly (64-bit fixed-point turns), so far
+ * positions lose nothing; arithmetic is fp32, rounded to bf16 once.
+ *   q, q_out   [B, Hq,  N, d]  bf16
+ *   k, k_out   [B, Hkv, N, d]  bf16; both NULL when there is only q (Hkv is
+ *              then ignored)
+ *   positions  [B, N] int32 device array, position_stride elements from one
+ *              batch entry to the next (0: one row for all of them), or NULL:
+ *              token n has position n.  Any int32 value, negative ones too.
+ *   inv_freq   [rotary_dim / 2] fp64 device array, radians per position,
+ *              8-byte aligned (attn_rope_freqs fills one on the host).
+ *              Magnitudes below 2^54; other values count as 0.
+ *   strides    HOST array of 12 element strides, or NULL for contiguous
+ *              tensors: (batch, head, token) of q, q_out, k, k_out.  Columns
+ *              are contiguous; every stride is a multiple of 8; a stride of
+ *              an input may be 0 (broadcast), one of an output is at least d.
+ *              The strides of a dimension of extent 1 are ignored.
+ *   d a multiple of 8, at most 512; rotary_dim even, 2 <= rotary_dim <= d.
+ *   q_out == q (k_out == k) works in place where the strides are equal too;
+ *   any other overlap of an output with an input or an output is not allowed.
+ * One kernel on `stream`.
+ */
+int attn_rope(const void *q, void *q_out, const void *k, void *k_out, const int *positions,
+              long long position_stride, const double *inv_freq, int B, int Hq, int Hkv, int N, int d,
+              int rotary_dim, int interleaved, float out_scale, int inverse, const long long *strides,
+              attn_stream_t stream);
+
+/* Frequency rules of attn_rope_freqs.  With f_i = base^(-2 i / rotary_dim):
+ *  PLAIN     f_i
+ *  LINEAR    f_i / factor (positions squeezed by factor)
+ *  BASE      base multiplied by factor^(r / (r - 2)), r = rotary_dim: the
+ *            slowest pair is stretched by factor, the fastest not at all
+ *  BY_PARTS  f_i (g + (1 - g) / factor), g = clamp((t_i - low) / (high - low),
+ *            0, 1), t_i = trained_len * f_i / (2 pi): pairs that turn at least
+ *            `high` times over the trained length keep their frequency, those
+ *            that turn at most `low` times are stretched by factor */
+enum attn_rope_rule {
+    ATTN_ROPE_PLAIN = 0,
+    ATTN_ROPE_LINEAR = 1,
+    ATTN_ROPE_BASE = 2,
+    ATTN_ROPE_BY_PARTS = 3
+};
+
+/* Fill inv_freq (HOST array of rotary_dim / 2 doubles) by one of the rules.
+ * base > 1; factor > 0 (ignored by PLAIN); low < high and trained_len > 0 for
+ * BY_PARTS (ignored otherwise); BASE needs rotary_dim >= 4.  Pure host code.
+ * Returns ATTN_OK or ATTN_ERR_ARG. */
+int attn_rope_freqs(double *inv_freq, int rotary_dim, double base, int rule, double factor, double low, double high,
+                    double trained_len);
+
+/*
+ * Rotary positions for T new tokens per sequence on their way into a decode
+ * cache: q is rotated into q_out, k rotated and v copied into the caches'
+ * rows behind each sequence's last.  T = 1 is a decode step, larger T a chunk
+ * of a prompt.
+ *   q, q_out   [B, Hq,  T, d]  bf16;  k, v  [B, Hkv, T, d]  bf16
+ *   kcache, vcache  [B, Hkv, max_seqlen, d]  bf16, contiguous: row
+ *              seqlens[b] + t receives token t
+ *   seqlens    [B] int32: keys cached so far (values are clamped to
+ *              [0, max_seqlen])
+ *   start_pos  [B] int32 position of token 0 (token t: start_pos[b] + t), or
+ *              NULL: the clamped seqlens[b].  Differs from seqlens once keys
+ *              have been evicted.
+ *   new_lens   [B] int32 tokens of each sequence that enter the cache (a
+ *              padded batch; clamped to [0, T]), or NULL: all T.  q is rotated
+ *              for all T tokens.
+ *   Tokens whose row would lie at or past max_seqlen are not stored.
+ *   seqlens_out [B] int32, min(seqlens[b] + new_lens[b], max_seqlen), or NULL;
+ *              must not overlap seqlens (or start_pos, new_lens).
+ *   cache_pos  [B, Hkv, max_seqlen] int32, or NULL: receives the position of
+ *              every stored key.  weights  [B, Hkv, max_seqlen] fp32, or NULL:
+ *              receives 0 for every stored key.  (attn_cache_evict reads
+ *              both.)
+ *   inv_freq, interleaved, out_scale as in attn_rope; rotary_dim may be 0
+ *   (inv_freq NULL): keys and values are then only copied in.
+ *   strides    HOST array of 12 element strides, or NULL: (batch, head, token)
+ *              of q, q_out, k, v, as in attn_rope.
+ * No other row of the caches, cache_pos or weights is touched.  q_out == q is
+ * allowed as in attn_rope.  One kernel on `stream`.
+ */
+int attn_rope_append(const void *q, void *q_out, const void *k, const void *v, void *kcache, void *vcache,
+                     const int *seqlens, const int *start_pos, const int *new_lens, int *seqlens_out,
+                     int *cache_pos, float *weights, const double *inv_freq, int B, int Hq, int Hkv, int T, int d,
+                     int rotary_dim, int interleaved, float out_scale, int max_seqlen, const long long *strides,
+                     attn_stream_t stream);
 
 /* Host-side view of the forward scheduler: unit `unit` of the order maps to
  * (*b, *h, *m) where m is the index of a 256-row block.  Pure host code; the

@@ -1,0 +1,110 @@
+"""CPU-only checks of the decode-cache entry points (rotary positions,
+shared-prefix decode, eviction): refusals come from the host before any CUDA
+call, the host-side rules agree with their definitions, and the torch helpers
+refuse tensors whose addresses alone would not tell.  No kernel runs."""
+import ctypes
+import math
+
+import pytest
+import torch
+
+import attention_fa2_fwd_sm_gb300 as attn
+from attention_fa2_fwd_sm_gb300 import _build
+
+A16 = 0x10000  # a fake 16-byte-aligned address: never dereferenced by these calls
+ARG, UNSUP, WS = attn.ATTN_ERR_ARG, attn.ATTN_ERR_UNSUPPORTED, attn.ATTN_ERR_WORKSPACE
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _built():
+    _build.build()
+    attn.lib()
+
+
+def strides(*v):
+    return (ctypes.c_longlong * 12)(*v)
+
+
+PACKED = (2 * 16 * 64, 16 * 64, 64)  # B = 3, H = 2, N = 16, d = 64
+
+
+def _rope(**kw):
+    a = dict(q=A16, q_out=A16 + 4096, k=A16 + 8192, k_out=A16 + 16384, pos=None, pos_stride=0, freqs=A16, B=3, Hq=2,
+             Hkv=2, N=16, d=64, r=64, inter=0, scale=1.0, inverse=0, strides=None)
+    a.update(kw)
+    return attn.attn_rope(*a.values(), stream=0)
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(q=None), ARG), (dict(q=A16 + 8), ARG), (dict(q_out=None), ARG), (dict(k_out=None), ARG), (dict(k=None), ARG),
+    (dict(k_out=A16 + 2), ARG), (dict(B=0), ARG), (dict(Hq=0), ARG), (dict(Hkv=0), ARG), (dict(N=-1), ARG),
+    (dict(N=0), ARG), (dict(pos=A16 + 2), ARG), (dict(pos_stride=-1), ARG), (dict(freqs=None), ARG),
+    (dict(freqs=A16 + 4), ARG), (dict(r=0), ARG), (dict(r=63), ARG), (dict(r=66), ARG),
+    (dict(scale=float("nan")), ARG), (dict(scale=float("inf")), ARG), (dict(d=60, r=32), UNSUP), (dict(d=0), UNSUP),
+    (dict(d=520, r=64), UNSUP),
+    (dict(strides=strides(*PACKED, *PACKED, *PACKED, PACKED[0], PACKED[1], 60)), ARG),   # not a multiple of 8
+    (dict(strides=strides(*PACKED, PACKED[0], PACKED[1], 0, *PACKED, *PACKED)), ARG),    # an output laid over itself
+    (dict(strides=strides(-8, 64, 64, *PACKED, *PACKED, *PACKED)), ARG),
+    (dict(strides=strides(1 << 40, 64, 64, *PACKED, *PACKED, *PACKED)), ARG),
+    (dict(q_out=A16, strides=strides(*PACKED, 2 * PACKED[0], PACKED[1], 64, *PACKED, *PACKED)), ARG),  # in place, moved
+])
+def test_rope_refusals(kw, code):
+    assert _rope(**kw) == code
+
+
+def _append(**kw):
+    a = dict(q=A16, q_out=A16 + 4096, k=A16, v=A16, kc=A16, vc=A16 + 16, lens=A16, start=None, new=None, out=A16 + 64,
+             cache_pos=None, weights=None, freqs=A16, B=3, Hq=2, Hkv=2, T=1, d=64, r=64, inter=0, scale=1.0, S=16,
+             strides=None)
+    a.update(kw)
+    return attn.attn_rope_append(*a.values(), stream=0)
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(q=None), ARG), (dict(k=A16 + 8), ARG), (dict(v=None), ARG), (dict(kc=None), ARG), (dict(vc=A16), ARG),
+    (dict(vc=A16 + 4), ARG), (dict(lens=None), ARG), (dict(lens=A16 + 1), ARG), (dict(out=A16), ARG),
+    (dict(out=A16 + 8), ARG), (dict(start=A16 + 64), ARG), (dict(new=A16 + 72), ARG), (dict(cache_pos=A16 + 2), ARG),
+    (dict(weights=A16 + 3), ARG), (dict(S=0), ARG), (dict(T=0), ARG), (dict(Hkv=0), ARG), (dict(r=-2), ARG),
+    (dict(r=64, freqs=None), ARG), (dict(r=130, d=128), ARG), (dict(d=12), UNSUP), (dict(scale=-float("inf")), ARG),
+])
+def test_append_refusals(kw, code):
+    assert _append(**kw) == code
+
+
+def test_frequency_rules():
+    r, base, L = 64, 10000.0, 4096.0
+    plain = [base ** (-2 * i / r) for i in range(r // 2)]
+    close = lambda a, b: all(math.isclose(x, y, rel_tol=1e-14) for x, y in zip(a, b)) and len(a) == len(b)
+    assert close(attn.attn_rope_freqs(r, base), plain)
+    assert close(attn.attn_rope_freqs(r, base, 1, 8.0), [f / 8 for f in plain])
+    stretched = attn.attn_rope_freqs(r, base, 2, 8.0)
+    assert stretched[0] == 1.0 and math.isclose(stretched[-1], plain[-1] / 8, rel_tol=1e-12)
+    parts = attn.attn_rope_freqs(r, base, 3, 8.0, 1.0, 4.0, L)
+    want = []
+    for f in plain:
+        g = min(max((L * f / (2 * math.pi) - 1) / 3, 0.0), 1.0)
+        want.append(f * (g + (1 - g) / 8))
+    assert close(parts, want) and parts[0] == plain[0] and math.isclose(parts[-1], plain[-1] / 8, rel_tol=1e-14)
+
+
+@pytest.mark.parametrize("args", [
+    (0,), (7,), (64, 1.0), (64, float("nan")), (64, 1e4, 4), (64, 1e4, -1), (64, 1e4, 1, 0.0), (64, 1e4, 1, float("inf")),
+    (2, 1e4, 2, 8.0), (64, 1e4, 3, 8.0, 4.0, 1.0), (64, 1e4, 3, 8.0, 1.0, 4.0, 0.0)])
+def test_frequency_refusals(args):
+    with pytest.raises(attn.AttnError) as e:
+        attn.attn_rope_freqs(*args)
+    assert e.value.code == ARG
+
+
+def test_rope_helpers_refuse_what_an_address_does_not_tell():
+    z = lambda *s, dtype=torch.bfloat16: torch.zeros(s, dtype=dtype)
+    f = z(32, dtype=torch.float64)
+    for call in (lambda: attn.rope(z(1, 2, 3, 64), None, f),                       # on the CPU
+                 lambda: attn.rope(z(2, 3, 64), None, f),
+                 lambda: attn.rope(z(1, 2, 3, 64, dtype=torch.float16), None, f),
+                 lambda: attn.rope_append(z(1, 2, 1, 64), z(1, 2, 1, 64), z(1, 2, 1, 64), z(1, 2, 9, 64), z(1, 2, 9, 64),
+                                          z(1, dtype=torch.int32), f),
+                 lambda: attn.rope_append(z(1, 2, 64), None, None, z(1, 2, 9, 64), None, None)):
+        with pytest.raises(attn.AttnError) as e:
+            call()
+        assert e.value.code == ARG
