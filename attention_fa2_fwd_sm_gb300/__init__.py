@@ -128,7 +128,7 @@ def _ptr(t):
 def _stream(stream):
     if stream is None:
         import torch
-        return torch.cuda.current_stream().cuda_stream
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
@@ -334,10 +334,7 @@ def attn_version() -> int:
     return int(lib().attn_version())
 
 
-def _strides(*triples):
-    """Host array of (batch, head, token) element strides, or None (contiguous)."""
-    flat = [x for t in triples for x in t]
-    return (ctypes.c_longlong * len(flat))(*flat)
+_Strides = _LL * 12  # (batch, head, token) element strides of four tensors
 
 
 def attn_rope(q, q_out, k, k_out, positions, position_stride, inv_freq, B, Hq, Hkv, N, d, rotary_dim, interleaved,
@@ -365,32 +362,52 @@ def attn_rope_freqs(rotary_dim, base=10000.0, rule=0, factor=1.0, low=1.0, high=
 
 
 # ----------------------------------------------------------- torch helpers
-def _expect(what, t, name, dtype, shape, device, packed=True):
-    """Refuse (ATTN_ERR_ARG) a tensor that the call cannot take as it is: its
+def _fits(t, dtype, shape, gpu):
+    """A contiguous tensor of this type and shape on this GPU."""
+    return t.dtype is dtype and t.shape == shape and t.get_device() == gpu and t.is_contiguous()
+
+
+def _fits_rows(t, dtype, shape, gpu):
+    """The same with any strides, columns contiguous."""
+    return t.dtype is dtype and t.shape == shape and t.get_device() == gpu and t.stride(-1) == 1
+
+
+def _refuse(what, name, t, dtype, shape):
+    """ATTN_ERR_ARG for a tensor that the call cannot take as it is: its
     address alone would not tell the library."""
-    if (t.dtype is dtype and tuple(t.shape) == tuple(shape) and t.device == device and t.is_cuda
-            and (t.is_contiguous() if packed else t.stride(-1) == 1)):
-        return
-    raise AttnError(ATTN_ERR_ARG, f"{what}: {name} has to be {dtype} {tuple(shape)} on {device}"
-                                  f"{', contiguous' if packed else ', with contiguous columns'} and on a GPU "
-                                  f"(got {t.dtype} {tuple(t.shape)} on {t.device}, strides {tuple(t.stride())})")
+    raise AttnError(ATTN_ERR_ARG, f"{what}: {name} has to be {dtype} {tuple(shape)}, on the GPU of the first tensor, with "
+                                  f"contiguous rows (got {t.dtype} {tuple(t.shape)} on {t.device}, strides {t.stride()})")
 
 
-class _on:
-    """The tensors' device as the current one for the length of a call; free
-    when it is current already."""
+def _gpu_of(what, t):
+    gpu = t.get_device()
+    if gpu < 0:
+        raise AttnError(ATTN_ERR_ARG, f"{what}: the tensors have to be on a GPU")
+    return gpu
 
-    def __init__(self, device):
-        import torch
-        self._guard = None if device.index == torch.cuda.current_device() else torch.cuda.device(device)
 
-    def __enter__(self):
-        if self._guard is not None:
-            self._guard.__enter__()
+def _elsewhere(what, gpu, stream):
+    """None when a call on GPU `gpu` and `stream` is one on the current device
+    and stream; else the context that makes it one.  Outputs and workspaces
+    that the helpers allocate then belong to the stream that writes them."""
+    import torch
+    if stream is None:
+        return None if gpu == torch.cuda.current_device() else torch.cuda.device(gpu)
+    if isinstance(stream, int):
+        stream = torch.cuda.ExternalStream(stream, device=gpu) if stream else torch.cuda.default_stream(gpu)
+    if stream.device.index != gpu:
+        raise AttnError(ATTN_ERR_ARG, f"{what}: the stream belongs to {stream.device}, the tensors to cuda:{gpu}")
+    return torch.cuda.stream(stream)
 
-    def __exit__(self, *exc):
-        if self._guard is not None:
-            self._guard.__exit__(*exc)
+
+def _workspace(what, workspace, nbytes, like, gpu):
+    """A workspace of nbytes: the caller's, or a new one."""
+    import torch
+    if workspace is None:
+        return torch.empty(max(nbytes, 16), dtype=torch.uint8, device=like.device), nbytes
+    if workspace.get_device() != gpu or not workspace.is_contiguous():
+        raise AttnError(ATTN_ERR_WORKSPACE, f"{what}: the workspace has to be contiguous and on the tensors' GPU")
+    return workspace, workspace.numel() * workspace.element_size()
 
 
 def rope_freqs(rotary_dim, base=10000.0, rule="plain", factor=1.0, low=1.0, high=4.0, trained_len=8192.0,
@@ -409,35 +426,44 @@ def rope(q, k, inv_freq, positions=None, interleaved=False, out_scale=1.0, out=N
     is twice the length of `inv_freq`.  Returns ``(q_out, k_out)``: contiguous
     tensors as attn_fwd takes them, or `out`, which may be ``(q, k)``."""
     import torch
+    what, bf16 = "rope", torch.bfloat16
+    gpu = _gpu_of(what, q)
+    there = _elsewhere(what, gpu, stream)
+    if there is not None:
+        with there:
+            return rope(q, k, inv_freq, positions, interleaved, out_scale, out, inverse)
     if q.dim() != 4 or (k is not None and k.dim() != 4):
         raise AttnError(ATTN_ERR_ARG, "rope: q and k have to be [B, H, N, d]")
-    (B, Hq, N, d), dev, Hkv = q.shape, q.device, 0
-    bf16 = torch.bfloat16
-    _expect("rope", q, "q", bf16, q.shape, dev, packed=False)
-    if k is not None:
-        Hkv = k.shape[1]
-        _expect("rope", k, "k", bf16, (B, Hkv, N, d), dev, packed=False)
-    _expect("rope", inv_freq, "inv_freq", torch.float64, (inv_freq.numel(),), dev)
+    B, Hq, N, d = q.shape
+    pairs = inv_freq.numel()
+    _fits_rows(q, bf16, q.shape, gpu) or _refuse(what, "q", q, bf16, q.shape)
+    _fits(inv_freq, torch.float64, (pairs,), gpu) or _refuse(what, "inv_freq", inv_freq, torch.float64, (pairs,))
     per_entry = 0
     if positions is not None:
-        per_entry = N if positions.dim() == 2 else 0
-        _expect("rope", positions, "positions", torch.int32, (B, N) if per_entry else (N,), dev)
-    if out is None:
-        q_out = torch.empty((B, Hq, N, d), dtype=bf16, device=dev)
-        k_out = None if k is None else torch.empty((B, Hkv, N, d), dtype=bf16, device=dev)
+        shape = (N,)
+        if positions.dim() == 2:
+            per_entry, shape = N, (B, N)
+        _fits(positions, torch.int32, shape, gpu) or _refuse(what, "positions", positions, torch.int32, shape)
+    q_out, k_out = (None, None) if out is None else out
+    if out is not None and (q_out is None or (k is None) != (k_out is None)):
+        raise AttnError(ATTN_ERR_ARG, "rope: out has to hold q_out, and k_out exactly where there is a k")
+    if q_out is None:
+        q_out = torch.empty((B, Hq, N, d), dtype=bf16, device=q.device)
     else:
-        q_out, k_out = out
-        _expect("rope", q_out, "q_out", bf16, q.shape, dev, packed=False)
-        if (k is None) != (k_out is None):
-            raise AttnError(ATTN_ERR_ARG, "rope: out has to hold k_out exactly where there is a k")
-        if k is not None:
-            _expect("rope", k_out, "k_out", bf16, k.shape, dev, packed=False)
-    none = (0, 0, 0)
-    with _on(dev):
-        check(attn_rope(q, q_out, k, k_out, positions, per_entry, inv_freq, B, Hq, Hkv, N, d, 2 * inv_freq.numel(),
-                        interleaved, out_scale, inverse,
-                        _strides(q.stride()[:3], q_out.stride()[:3], none if k is None else k.stride()[:3],
-                                 none if k is None else k_out.stride()[:3]), stream), "attn_rope")
+        _fits_rows(q_out, bf16, q.shape, gpu) or _refuse(what, "q_out", q_out, bf16, q.shape)
+    Hkv, ks, kos = 0, (0, 0, 0, 1), (0, 0, 0, 1)
+    if k is not None:
+        Hkv = k.shape[1]
+        shape = (B, Hkv, N, d)
+        _fits_rows(k, bf16, shape, gpu) or _refuse(what, "k", k, bf16, shape)
+        if k_out is None:
+            k_out = torch.empty(shape, dtype=bf16, device=q.device)
+        else:
+            _fits_rows(k_out, bf16, shape, gpu) or _refuse(what, "k_out", k_out, bf16, shape)
+        ks, kos = k.stride(), k_out.stride()
+    rc = attn_rope(q, q_out, k, k_out, positions, per_entry, inv_freq, B, Hq, Hkv, N, d, 2 * pairs, interleaved,
+                   out_scale, inverse, _Strides(*q.stride()[:3], *q_out.stride()[:3], *ks[:3], *kos[:3]))
+    check(rc, "attn_rope")
     return q_out, k_out
 
 
@@ -455,38 +481,46 @@ def rope_append(q, k, v, kcache, vcache, seqlens, inv_freq=None, start_pos=None,
     Allocates the outputs that are not given; returns ``(q_out,
     seqlens_out)``."""
     import torch
+    what, bf16, i32 = "rope_append", torch.bfloat16, torch.int32
+    gpu = _gpu_of(what, q)
+    there = _elsewhere(what, gpu, stream)
+    if there is not None:
+        with there:
+            return rope_append(q, k, v, kcache, vcache, seqlens, inv_freq, start_pos, new_lens, interleaved, out_scale,
+                               cache_pos, weights, q_out, seqlens_out)
     if q.dim() != 4 or kcache.dim() != 4:
         raise AttnError(ATTN_ERR_ARG, "rope_append: q has to be [B, Hq, T, d], the caches [B, Hkv, max_seqlen, d]")
-    (B, Hq, T, d), dev, Hkv, s_max = q.shape, q.device, kcache.shape[1], kcache.shape[2]
-    bf16, i32, what = torch.bfloat16, torch.int32, "rope_append"
-    _expect(what, q, "q", bf16, q.shape, dev, packed=False)
-    _expect(what, k, "k", bf16, (B, Hkv, T, d), dev, packed=False)
-    _expect(what, v, "v", bf16, (B, Hkv, T, d), dev, packed=False)
-    _expect(what, kcache, "kcache", bf16, (B, Hkv, s_max, d), dev)
-    _expect(what, vcache, "vcache", bf16, (B, Hkv, s_max, d), dev)
-    for name, t in (("seqlens", seqlens), ("start_pos", start_pos), ("new_lens", new_lens),
-                    ("seqlens_out", seqlens_out)):
-        if t is not None:
-            _expect(what, t, name, i32, (B,), dev)
+    B, Hq, T, d = q.shape
+    Hkv, s_max = kcache.shape[1], kcache.shape[2]
+    new, cache, per_key = (B, Hkv, T, d), (B, Hkv, s_max, d), (B, Hkv, s_max)
+    _fits_rows(q, bf16, q.shape, gpu) or _refuse(what, "q", q, bf16, q.shape)
+    _fits_rows(k, bf16, new, gpu) or _refuse(what, "k", k, bf16, new)
+    _fits_rows(v, bf16, new, gpu) or _refuse(what, "v", v, bf16, new)
+    _fits(kcache, bf16, cache, gpu) or _refuse(what, "kcache", kcache, bf16, cache)
+    _fits(vcache, bf16, cache, gpu) or _refuse(what, "vcache", vcache, bf16, cache)
+    _fits(seqlens, i32, (B,), gpu) or _refuse(what, "seqlens", seqlens, i32, (B,))
+    start_pos is None or _fits(start_pos, i32, (B,), gpu) or _refuse(what, "start_pos", start_pos, i32, (B,))
+    new_lens is None or _fits(new_lens, i32, (B,), gpu) or _refuse(what, "new_lens", new_lens, i32, (B,))
+    cache_pos is None or _fits(cache_pos, i32, per_key, gpu) or _refuse(what, "cache_pos", cache_pos, i32, per_key)
+    weights is None or _fits(weights, torch.float32, per_key, gpu) or _refuse(what, "weights", weights, torch.float32,
+                                                                              per_key)
     rotary_dim = 0
     if inv_freq is not None:
-        rotary_dim = 2 * inv_freq.numel()
-        _expect(what, inv_freq, "inv_freq", torch.float64, (rotary_dim // 2,), dev)
-    if cache_pos is not None:
-        _expect(what, cache_pos, "cache_pos", i32, (B, Hkv, s_max), dev)
-    if weights is not None:
-        _expect(what, weights, "weights", torch.float32, (B, Hkv, s_max), dev)
+        pairs = inv_freq.numel()
+        rotary_dim = 2 * pairs
+        _fits(inv_freq, torch.float64, (pairs,), gpu) or _refuse(what, "inv_freq", inv_freq, torch.float64, (pairs,))
     if q_out is None:
-        q_out = torch.empty((B, Hq, T, d), dtype=bf16, device=dev)
+        q_out = torch.empty((B, Hq, T, d), dtype=bf16, device=q.device)
     else:
-        _expect(what, q_out, "q_out", bf16, q.shape, dev, packed=False)
+        _fits_rows(q_out, bf16, q.shape, gpu) or _refuse(what, "q_out", q_out, bf16, q.shape)
     if seqlens_out is None:
         seqlens_out = torch.empty_like(seqlens)
-    with _on(dev):
-        check(attn_rope_append(q, q_out, k, v, kcache, vcache, seqlens, start_pos, new_lens, seqlens_out, cache_pos,
-                               weights, inv_freq, B, Hq, Hkv, T, d, rotary_dim, interleaved, out_scale, s_max,
-                               _strides(q.stride()[:3], q_out.stride()[:3], k.stride()[:3], v.stride()[:3]), stream),
-              "attn_rope_append")
+    else:
+        _fits(seqlens_out, i32, (B,), gpu) or _refuse(what, "seqlens_out", seqlens_out, i32, (B,))
+    rc = attn_rope_append(q, q_out, k, v, kcache, vcache, seqlens, start_pos, new_lens, seqlens_out, cache_pos, weights,
+                          inv_freq, B, Hq, Hkv, T, d, rotary_dim, interleaved, out_scale, s_max,
+                          _Strides(*q.stride()[:3], *q_out.stride()[:3], *k.stride()[:3], *v.stride()[:3]))
+    check(rc, "attn_rope_append")
     return q_out, seqlens_out
 
 
