@@ -68,6 +68,9 @@ SIGNATURES = {
     "attn_rope": (_I, [_P, _P, _P, _P, _P, _LL, _P, _I, _I, _I, _I, _I, _I, _I, _F, _I, _LLP, _P]),
     "attn_rope_freqs": (_I, [_DP, _I, _D, _I, _D, _D, _D, _D]),
     "attn_rope_append": (_I, [_P] * 13 + [_I] * 7 + [_F, _I, _LLP, _P]),
+    "attn_decode_prefix": (_I, [_P] * 9 + [_I] * 5 + [_F, _I, _P, _SZ, _P]),
+    "attn_decode_prefix_workspace_bytes": (_SZ, [_I] * 7),
+    "attn_decode_prefix_segment": (_I, [_I] * 7 + [_IP]),
     "attn_tile_map": (_I, [_I, _I, _I, _I, _I, _I, _LL, _IP, _IP, _IP]),
     "attn_tile_map_die_split": (_I, [_I, _I, _I, _I, _I, _I, _LL, _IP, _IP, _IP]),
     "attn_bwd_tile_map": (_I, [_I, _I, _I, _I, _I, _I, _LL, _IP, _IP, _IP]),
@@ -353,6 +356,27 @@ def attn_rope_append(q, q_out, k, v, kcache, vcache, seqlens, start_pos, new_len
                                   max_seqlen, strides, _stream(stream))
 
 
+def attn_decode_prefix(q, kprefix, vprefix, kcache, vcache, seqlens, o, lse, weights, B, Hq, Hkv, P, d, scale,
+                       max_seqlen, workspace, workspace_bytes, stream=None) -> int:
+    return lib().attn_decode_prefix(_ptr(q), _ptr(kprefix), _ptr(vprefix), _ptr(kcache), _ptr(vcache), _ptr(seqlens),
+                                    _ptr(o), _ptr(lse), _ptr(weights), B, Hq, Hkv, P, d, scale, max_seqlen,
+                                    _ptr(workspace), workspace_bytes, _stream(stream))
+
+
+def attn_decode_prefix_workspace_bytes(B, Hq, Hkv, P, d, max_seqlen, with_weights=False) -> int:
+    return lib().attn_decode_prefix_workspace_bytes(B, Hq, Hkv, P, d, max_seqlen, int(bool(with_weights)))
+
+
+def attn_decode_prefix_segment(B, Hq, Hkv, P, num_sms, cta, i):
+    """(KV head, unit, first key block, blocks, slot) of CTA `cta`'s i-th piece
+    of the prefix phase, or None when it has no i-th piece."""
+    out = (ctypes.c_int * 5)()
+    rc = lib().attn_decode_prefix_segment(B, Hq, Hkv, P, num_sms, cta, i, out)
+    if rc < 0:
+        check(rc, "attn_decode_prefix_segment")
+    return tuple(out) if rc else None
+
+
 def attn_rope_freqs(rotary_dim, base=10000.0, rule=0, factor=1.0, low=1.0, high=4.0, trained_len=8192.0):
     """List of rotary_dim / 2 frequencies (radians per position) by one of ROPE_RULES."""
     buf = (ctypes.c_double * max(int(rotary_dim) // 2, 1))()
@@ -522,6 +546,57 @@ def rope_append(q, k, v, kcache, vcache, seqlens, inv_freq=None, start_pos=None,
                           _Strides(*q.stride()[:3], *q_out.stride()[:3], *k.stride()[:3], *v.stride()[:3]))
     check(rc, "attn_rope_append")
     return q_out, seqlens_out
+
+
+def decode_prefix(q, kprefix, vprefix, kcache, vcache, seqlens, scale=None, weights=None, workspace=None,
+                  with_lse=True, stream=None):
+    """One decode step by attn_decode_prefix: q ``[B, Hq, d]`` over a prefix
+    ``[Hkv, P, d]`` that the batch shares (None: none) and the sequences' own
+    caches ``[B, Hkv, max_seqlen, d]`` (None: none).  `weights` ``[B, Hkv,
+    max_seqlen]`` fp32, where given, is added to in place.  Allocates the outputs,
+    and a workspace when none is given (attn_decode_prefix_workspace_bytes says
+    how large one has to be); returns ``(o, lse, workspace)``."""
+    import torch
+    what, bf16 = "decode_prefix", torch.bfloat16
+    gpu = _gpu_of(what, q)
+    there = _elsewhere(what, gpu, stream)
+    if there is not None:
+        with there:
+            return decode_prefix(q, kprefix, vprefix, kcache, vcache, seqlens, scale, weights, workspace, with_lse)
+    if q.dim() != 3 or (kcache is not None and kcache.dim() != 4) or (kprefix is not None and kprefix.dim() != 3):
+        raise AttnError(ATTN_ERR_ARG, "decode_prefix: q has to be [B, Hq, d], the prefix [Hkv, P, d], the caches "
+                                      "[B, Hkv, max_seqlen, d]")
+    B, Hq, d = q.shape
+    P = s_max = Hkv = 0
+    _fits(q, bf16, q.shape, gpu) or _refuse(what, "q", q, bf16, q.shape)
+    if kcache is not None:
+        Hkv, s_max = kcache.shape[1], kcache.shape[2]
+        shape = (B, Hkv, s_max, d)
+        _fits(kcache, bf16, shape, gpu) or _refuse(what, "kcache", kcache, bf16, shape)
+        _fits(vcache, bf16, shape, gpu) or _refuse(what, "vcache", vcache, bf16, shape)
+        _fits(seqlens, torch.int32, (B,), gpu) or _refuse(what, "seqlens", seqlens, torch.int32, (B,))
+    if kprefix is not None:
+        Hkv, P = (Hkv or kprefix.shape[0]), kprefix.shape[1]
+        shape = (Hkv, P, d)
+        _fits(kprefix, bf16, shape, gpu) or _refuse(what, "kprefix", kprefix, bf16, shape)
+        _fits(vprefix, bf16, shape, gpu) or _refuse(what, "vprefix", vprefix, bf16, shape)
+    if weights is not None:
+        shape = (B, Hkv, s_max)
+        _fits(weights, torch.float32, shape, gpu) or _refuse(what, "weights", weights, torch.float32, shape)
+    nbytes = attn_decode_prefix_workspace_bytes(B, Hq, Hkv, P, d, s_max, weights is not None)
+    workspace, nbytes = _workspace(what, workspace, nbytes, q, gpu)
+    o = torch.empty_like(q)
+    lse = torch.empty((B, Hq), dtype=torch.float32, device=q.device) if with_lse else None
+    rc = attn_decode_prefix(q, kprefix, vprefix, kcache, vcache, seqlens, o, lse, weights, B, Hq, Hkv, P, d,
+                            d ** -0.5 if scale is None else scale, s_max, workspace, nbytes)
+    check(rc, "attn_decode_prefix")
+    return o, lse, workspace
+
+
+def decode_weighted(q, kcache, vcache, seqlens, weights, scale=None, workspace=None, with_lse=True, stream=None):
+    """A decode step that adds to `weights` what every cached key receives:
+    `decode_prefix` without a prefix."""
+    return decode_prefix(q, None, None, kcache, vcache, seqlens, scale, weights, workspace, with_lse, stream)
 
 
 def forward(q, k, v, causal=False, scale=None, tile_order=ORDER_HEAD_FIRST, with_lse=True,

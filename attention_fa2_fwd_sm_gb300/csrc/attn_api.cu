@@ -14,6 +14,7 @@
 #include "../../include/attn.h"
 #include "attn_internal.h"
 #include "dkdv_order.cuh"
+#include "prefix_order.cuh"
 #include "tile_order.cuh"
 
 namespace attn {
@@ -70,12 +71,12 @@ int note_cuda_error(cudaError_t e, const char *where) {
 }
 
 bool encode_bf16_3d(CUtensorMap *map, const void *base, uint64_t dim0, uint64_t dim1, uint64_t dim2,
-                    uint32_t box0, uint32_t box1) {
+                    uint32_t box0, uint32_t box1, uint32_t box2) {
     EncodeTiledFn fn = encode_fn();
     if (!fn) return false;
     const cuuint64_t dims[3] = {dim0, dim1, dim2};
     const cuuint64_t strides[2] = {dim0 * 2, dim0 * dim1 * 2};
-    const cuuint32_t box[3] = {box0, box1, 1};
+    const cuuint32_t box[3] = {box0, box1, box2};
     const cuuint32_t estr[3] = {1, 1, 1};
     return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(base), dims, strides, box,
               estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
@@ -733,15 +734,88 @@ int attn_rope_append(const void *q, void *q_out, const void *k, const void *v, v
     return rope_launch(a, reinterpret_cast<cudaStream_t>(stream));
 }
 
+static int decode_prefix_sizes(int B, int Hq, int Hkv, int P, int d, int max_seqlen) {
+    if (B <= 0 || Hq <= 0 || Hkv <= 0 || P < 0 || max_seqlen < 0 || Hq % Hkv) return ATTN_ERR_ARG;
+    if (P == 0 && max_seqlen == 0) return ATTN_ERR_ARG;
+    if (d != 64 && d != 128) return ATTN_ERR_UNSUPPORTED;
+    if (Hq / Hkv > kDecodeMaxGroup) return ATTN_ERR_UNSUPPORTED;
+    if (Hkv > 65535 || (long long)B * Hq > 0x7fffffffLL) return ATTN_ERR_ARG;
+    // tensor-map limits, and the work list's total of keys stays below 2^62
+    if ((long long)max_seqlen * d * 2 >= (1LL << 39) || (long long)P * d * 2 >= (1LL << 39)) return ATTN_ERR_ARG;
+    if ((double)B * (double)max_seqlen * (double)Hkv >= 4.0e18) return ATTN_ERR_ARG;
+    return ATTN_OK;
+}
+
+size_t attn_decode_prefix_workspace_bytes(int B, int Hq, int Hkv, int P, int d, int max_seqlen, int with_weights) {
+    if (decode_prefix_sizes(B, Hq, Hkv, P, d, max_seqlen) != ATTN_OK) return 0;
+    const int sms = current_num_sms();
+    PrefixLayout l;
+    if (sms <= 0 || !decode_prefix_layout(B, Hq, Hkv, P, d, max_seqlen, with_weights != 0, sms, &l)) return 0;
+    return l.bytes;
+}
+
+int attn_decode_prefix(const void *q, const void *kprefix, const void *vprefix, const void *kcache, const void *vcache,
+                       const int *seqlens, void *o, float *lse, float *weights, int B, int Hq, int Hkv, int P, int d,
+                       float scale, int max_seqlen, void *workspace, size_t workspace_bytes, attn_stream_t stream) {
+    const int rc = decode_prefix_sizes(B, Hq, Hkv, P, d, max_seqlen);
+    if (rc != ATTN_OK) return rc;
+    if (!aligned16(q) || !aligned16(o) || !aligned4(lse) || !aligned4(weights)) return ATTN_ERR_ARG;
+    if (P > 0 && (!aligned16(kprefix) || !aligned16(vprefix))) return ATTN_ERR_ARG;
+    if (max_seqlen > 0 && (!aligned16(kcache) || !aligned16(vcache) || !seqlens || !aligned4(seqlens)))
+        return ATTN_ERR_ARG;
+    if (weights && max_seqlen == 0) return ATTN_ERR_ARG;
+    if (!(scale > 0.f) || !std::isfinite(scale)) return ATTN_ERR_ARG;
+    if (!workspace || !aligned16(workspace)) return ATTN_ERR_WORKSPACE;
+    const int sms = current_num_sms();
+    if (sms <= 0) return note_cuda_error(cudaErrorNoDevice, "device query");
+    PrefixLayout l;
+    if (!decode_prefix_layout(B, Hq, Hkv, P, d, max_seqlen, weights != nullptr, sms, &l)) return ATTN_ERR_ARG;
+    if (workspace_bytes < l.bytes) return ATTN_ERR_WORKSPACE;
+    DecodePrefixLaunch a;
+    a.q = q;
+    a.kprefix = kprefix;
+    a.vprefix = vprefix;
+    a.kcache = kcache;
+    a.vcache = vcache;
+    a.seqlens = seqlens;
+    a.o = o;
+    a.lse = lse;
+    a.weights = weights;
+    a.B = B;
+    a.Hq = Hq;
+    a.Hkv = Hkv;
+    a.P = P;
+    a.d = d;
+    a.max_seqlen = max_seqlen;
+    a.scale = scale;
+    a.workspace = static_cast<char *>(workspace);
+    a.wait_ns = (unsigned long long)g_wait_ns.load();
+    a.num_sms = sms;
+    return decode_prefix_launch(a, reinterpret_cast<cudaStream_t>(stream));
+}
+
+int attn_decode_prefix_segment(int B, int Hq, int Hkv, int P, int num_sms, int cta, int i, int *out) {
+    PrefixOrder o;
+    if (!out || P <= 0 || num_sms <= 0 || i < 0 || decode_prefix_sizes(B, Hq, Hkv, P, 128, 0) != ATTN_OK ||
+        !prefix_order(&o, B, Hq / Hkv, Hkv, P, num_sms) || cta < 0 || cta >= o.grid)
+        return ATTN_ERR_ARG;
+    const long long u = prefix_start(o, cta, i);
+    if (u < 0) return 0;
+    const PrefixSegment s = prefix_segment(o, cta, u);
+    const int v[5] = {s.g, s.m, s.j0, s.n, s.slot};
+    for (int k = 0; k < 5; ++k) out[k] = v[k];
+    return 1;
+}
+
 int attn_device_status(attn_stream_t stream) {
     if (cudaStreamSynchronize(reinterpret_cast<cudaStream_t>(stream)) != cudaSuccess)
         return ATTN_ERR_CUDA;
-    int a = 0, b = 0, c = 0, e = 0, f = 0;
+    int a = 0, b = 0, c = 0, e = 0, f = 0, g = 0;
     if (fwd_take_status(&a) != cudaSuccess || decode_take_status(&b) != cudaSuccess ||
         bwd_take_status(&c) != cudaSuccess || fwd_pair_take_status(&e) != cudaSuccess ||
-        fwd_split_take_status(&f) != cudaSuccess)
+        fwd_split_take_status(&f) != cudaSuccess || decode_prefix_take_status(&g) != cudaSuccess)
         return ATTN_ERR_CUDA;
-    return (a | b | c | e | f) ? ATTN_ERR_TIMEOUT : ATTN_OK;
+    return (a | b | c | e | f | g) ? ATTN_ERR_TIMEOUT : ATTN_OK;
 }
 
 }  // extern "C"

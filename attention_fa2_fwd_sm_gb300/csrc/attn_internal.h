@@ -150,6 +150,30 @@ struct RopeLaunch {
 };
 int rope_launch(const RopeLaunch &a, cudaStream_t stream);
 int decode_launch(const DecodeLaunch &a, cudaStream_t stream);
+
+// Decode over a shared prefix and the sequences' own keys
+// (decode_prefix_sm103.cu).  Byte offsets of the workspace's parts: the own
+// keys' work list, their partials and the prefix's, and the scores.
+struct PrefixLayout {
+    size_t plan, own_o, own_lse, pre_o, pre_lse, scores, bytes;
+    int own_items;  // capacity of the work list
+};
+struct DecodePrefixLaunch {
+    const void *q, *kprefix, *vprefix, *kcache, *vcache;
+    const int *seqlens;
+    void *o;
+    float *lse, *weights;  // may be null
+    int B, Hq, Hkv, P, d, max_seqlen;
+    float scale;
+    char *workspace;
+    unsigned long long wait_ns;
+    int num_sms;
+};
+// False when the sizes are outside what the launches can count.
+bool decode_prefix_layout(int B, int Hq, int Hkv, int P, int d, int max_seqlen, bool weights, int num_sms,
+                          PrefixLayout *l);
+int decode_prefix_launch(const DecodePrefixLaunch &a, cudaStream_t stream);
+cudaError_t decode_prefix_take_status(int *bits);
 int bwd_launch(const BwdLaunch &a, cudaStream_t stream);
 
 // Size of the built-in scratch array used by attn_decode_noalloc.
@@ -180,9 +204,9 @@ cudaError_t decode_take_status(int *bits);
 cudaError_t bwd_take_status(int *bits);
 
 // Tiled bf16 tensor map over a 3-D row-major tensor [dim2][dim1][dim0]
-// (dim0 contiguous), box {box0, box1, 1}, 128-byte swizzle, zero fill out of
+// (dim0 contiguous), box {box0, box1, box2}, 128-byte swizzle, zero fill out of
 // bounds.  Returns false if the driver rejects it.
 bool encode_bf16_3d(CUtensorMap *map, const void *base, uint64_t dim0, uint64_t dim1,
-                    uint64_t dim2, uint32_t box0, uint32_t box1);
+                    uint64_t dim2, uint32_t box0, uint32_t box1, uint32_t box2 = 1);
 
 }  // namespace attn

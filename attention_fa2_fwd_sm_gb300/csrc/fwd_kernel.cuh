@@ -33,10 +33,11 @@
 // rewritten (the same result up to rounding, since l and O always share the
 // reference maximum).
 //
-// The kernel is one template over the unit mapping, instantiated by two
+// The kernel is one template over the unit mapping, instantiated by three
 // translation units: fwd_sm103.cu (the tile orders, and the grouped causal
-// GQA mapping) and fwd_splitkv_sm103.cu (each head's keys cut into ranges,
-// fp32 partials per range).  The mappings are compile-time variants, so each
+// GQA mapping), fwd_splitkv_sm103.cu (each head's keys cut into ranges,
+// fp32 partials per range) and decode_prefix_sm103.cu (one query row per batch
+// entry and head against a prefix that the batch shares).  The mappings are compile-time variants, so each
 // instantiation carries only its own mapping's code; each translation unit
 // has its own copy of the work counters and the status word below.
 #pragma once
@@ -47,6 +48,7 @@
 #include <cmath>
 
 #include "attn_internal.h"
+#include "prefix_order.cuh"
 #include "sm103_ptx.cuh"
 #include "tile_order.cuh"
 
@@ -124,6 +126,14 @@ struct SplitParams : Params {
     int splits, chunk_blocks;
 };
 
+// Parameters of a shared prefix's launch: the rows of a tile are (batch entry,
+// query head of the group) pairs, N is the prefix's length and causal is 0.
+struct PrefixParams : Params {
+    float *part_o;    // [slots][B * Hq][D] fp32
+    float *part_lse;  // [slots][B * Hq] fp32, log2 units (-inf when empty)
+    PrefixOrder po;
+};
+
 struct UnitWork {
     int b, h, kvh;
     int row0[kNT];
@@ -140,7 +150,9 @@ struct UnitWork {
 //                CTAs running at the same time stream one range of one K/V
 //                head.  Inside a range: query head, then row block
 //                (descending when causal, longest first).
-enum UnitMap : int { kMapOrder = 0, kMapGrouped = 1, kMapSplit = 2 };
+//   kMapPrefix   decode rows over a shared prefix: the segments of
+//                prefix_order.cuh; row0 is a tile's first batch entry.
+enum UnitMap : int { kMapOrder = 0, kMapGrouped = 1, kMapSplit = 2, kMapPrefix = 3 };
 
 // Parameter block of each mapping.
 template <int kMap>
@@ -150,6 +162,11 @@ struct ParamsOf {
 template <>
 struct ParamsOf<kMapSplit> {
     using type = SplitParams;
+};
+
+template <>
+struct ParamsOf<kMapPrefix> {
+    using type = PrefixParams;
 };
 
 // A unit's work under mapping kMap: s is its key range and jb the range's
@@ -163,10 +180,29 @@ template <>
 struct MappedWork<kMapSplit> : UnitWork {
     int s, jb;
 };
+template <>
+struct MappedWork<kMapPrefix> : UnitWork {
+    int s, jb;
+};
 
 template <int kMap>
 __device__ __forceinline__ MappedWork<kMap> unit_work(const typename ParamsOf<kMap>::type &p, long long u) {
-    if constexpr (kMap == kMapSplit) {
+    if constexpr (kMap == kMapPrefix) {
+        MappedWork<kMap> w;
+        const PrefixSegment seg = prefix_segment(p.po, blockIdx.x, u);
+        w.b = 0;
+        w.kvh = seg.g;
+        w.h = seg.g * p.G;
+        w.s = seg.slot;
+        w.jb = seg.j0;
+        w.nmax = seg.n;
+#pragma unroll
+        for (int tt = 0; tt < kNT; ++tt) {
+            w.row0[tt] = (seg.m * kNT + tt) * p.po.rb;
+            w.nkv[tt] = w.row0[tt] < p.B ? seg.n : 0;
+        }
+        return w;
+    } else if constexpr (kMap == kMapSplit) {
         MappedWork<kMap> w;
         const int nkv_all = (p.N + kBlockN - 1) / kBlockN;
         w.nmax = 0;
@@ -295,6 +331,18 @@ __global__ void __launch_bounds__(kThreads, 1)
         *abort_flag = 0;
         fence_mbar_init();
     }
+    if constexpr (kMap == kMapPrefix) {
+        // The own keys' grid behind this one reads nothing that it writes.
+        griddep_launch_dependents();
+        // Tile rows that no box covers: zero once, so that their scores (which
+        // nobody stores) stay finite and take the common softmax path.
+        const int rows = p.po.rb * p.G;
+        const int units = (kTileM - rows) * 8;  // 16-byte units of one 64-column chunk
+        for (int i = threadIdx.x; i < kNT * C::kChunks * units; i += kThreads)
+            *reinterpret_cast<uint4 *>(sQ + (i / units) * C::kChunkBytes + rows * 128 + (i % units) * 16) =
+                make_uint4(0, 0, 0, 0);
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    }
     if (warp == 0 && lane == 0) {
         tma_prefetch_desc(&tmQ);
         tma_prefetch_desc(&tmK);
@@ -329,7 +377,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             for (long long qi = 0; ok; ++qi) {
                 // Publish the next unit to the other roles (two-entry queue).
-                const long long u = fetch_unit(p, qi, my_die);
+                long long u;
+                if constexpr (kMap == kMapPrefix) u = prefix_start(p.po, blockIdx.x, int(qi));
+                else u = fetch_unit(p, qi, my_die);
                 const int qs = int(qi & 1);
                 if (qi >= 2 && !mbar_wait_bounded(bar(C::kBarUQEmpty + qs), uint32_t(((qi >> 1) - 1) & 1),
                                                   p.wait_ns, abort_flag, status)) {
@@ -347,10 +397,18 @@ __global__ void __launch_bounds__(kThreads, 1)
                                                p.wait_ns, abort_flag, status);
                     if (!ok) break;
                     const uint32_t qb = bar(C::kBarQFull + t);
-                    mbar_arrive_expect_tx(qb, C::kQBytes);
-                    for (int c = 0; c < C::kChunks; ++c)
-                        tma_load_3d(smem_u32(sQ + t * C::kQBytes + c * C::kChunkBytes), &tmQ, qb,
-                                    c * 64, w.row0[t], w.b * p.Hq + w.h);
+                    if constexpr (kMap == kMapPrefix) {
+                        // box: rb batch entries x G heads x 64 columns, rows of 128 bytes one after another
+                        mbar_arrive_expect_tx(qb, p.po.rb * p.G * 128 * C::kChunks);
+                        for (int c = 0; c < C::kChunks; ++c)
+                            tma_load_3d(smem_u32(sQ + t * C::kQBytes + c * C::kChunkBytes), &tmQ, qb, c * 64, w.h,
+                                        w.row0[t]);
+                    } else {
+                        mbar_arrive_expect_tx(qb, C::kQBytes);
+                        for (int c = 0; c < C::kChunks; ++c)
+                            tma_load_3d(smem_u32(sQ + t * C::kQBytes + c * C::kChunkBytes), &tmQ, qb,
+                                        c * 64, w.row0[t], w.b * p.Hq + w.h);
+                    }
                     ++q_loads[t];
                 }
                 for (int j = 0; ok && j < w.nmax; ++j) {
@@ -683,7 +741,27 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (!ok) break;
             ++o_waits;
             tc_fence_after();
-            if constexpr (kMap == kMapSplit) {
+            if constexpr (kMap == kMapPrefix) {
+                const float inv_l = l_run > 0.f ? 1.f / l_run : 0.f;
+                const int be = w.row0[t] + r / p.G;  // batch entry of this row
+                const bool row_ok = r < p.po.rb * p.G && be < p.B;
+                const size_t prow = row_ok ? ((size_t)w.s * p.B + be) * p.Hq + w.h + r % p.G : 0;
+                float *orow = p.part_o + prow * D;
+#pragma unroll
+                for (int c = 0; c < D / 32; ++c) {
+                    uint32_t ov[32];
+                    tmem_ld32(tO + c * 32, ov);
+                    tmem_wait_ld();
+                    if (row_ok) {
+#pragma unroll
+                        for (int g = 0; g < 8; ++g)
+                            *reinterpret_cast<float4 *>(orow + c * 32 + g * 4) = make_float4(
+                                __uint_as_float(ov[4 * g]) * inv_l, __uint_as_float(ov[4 * g + 1]) * inv_l,
+                                __uint_as_float(ov[4 * g + 2]) * inv_l, __uint_as_float(ov[4 * g + 3]) * inv_l);
+                    }
+                }
+                if (row_ok) p.part_lse[prow] = l_run > 0.f ? m_run + __log2f(l_run) : -INFINITY;
+            } else if constexpr (kMap == kMapSplit) {
                 const float inv_l = l_run > 0.f ? 1.f / l_run : 0.f;
                 const bool row_ok = row < p.N;
                 const size_t prow =

@@ -497,6 +497,53 @@ int attn_rope_append(const void *q, void *q_out, const void *k, const void *v, v
                      int rotary_dim, int interleaved, float out_scale, int max_seqlen, const long long *strides,
                      attn_stream_t stream);
 
+/*
+ * Decode for a batch whose sequences share a prefix (one query row per
+ * sequence and query head), optionally adding up the attention weight that
+ * every cached key receives.  Sequence b attends the P keys of the prefix and
+ * the first seqlens[b] keys of its own cache:
+ *     s_j = scale * <q, k_j>,  L = log(sum_j exp(s_j)) over both,
+ *     o = sum_j exp(s_j - L) v_j,  lse = L,
+ *     weights[b, g, j] += sum over the Hq / Hkv query heads that read KV head
+ *                         g of exp(s_j - L),  j < seqlens[b] (own keys only).
+ * The prefix's keys are read once for the whole batch, as matrix products over
+ * all the rows that read a KV head.
+ *   q, o       [B, Hq, d]                bf16
+ *   kprefix, vprefix  [Hkv, P, d]        bf16; P = 0 (NULL): no prefix, which
+ *              makes this attn_decode with weights
+ *   kcache, vcache  [B, Hkv, max_seqlen, d]  bf16; max_seqlen = 0 (NULL): no
+ *              own keys
+ *   seqlens    [B] int32, clamped to [0, max_seqlen]; NULL where max_seqlen
+ *              is 0.  A sequence with no key at all gets o = 0, lse = -inf.
+ *   lse        [B, Hq] fp32 (natural log), or NULL
+ *   weights    [B, Hkv, max_seqlen] fp32, read and written, or NULL.  Entries
+ *              at or past seqlens[b] are left as they were.  No atomics:
+ *              equal calls give equal bits.
+ *   d in {64, 128}; 1 <= Hq / Hkv <= 16; P or max_seqlen > 0;
+ *   ceil(5 SMs / 3 / Hkv) + B <= 65535.
+ *   workspace  at least attn_decode_prefix_workspace_bytes(...) bytes, 16-byte
+ *              aligned; with weights it also holds the scores, 4 * B * Hq *
+ *              max_seqlen bytes.  Nothing in it outlives the call.
+ * Up to three kernels run on `stream`, with no host synchronisation: the
+ * prefix's partials, the own keys' partials (work list made on the device from
+ * seqlens), and the merge with the weights.
+ */
+int attn_decode_prefix(const void *q, const void *kprefix, const void *vprefix, const void *kcache,
+                       const void *vcache, const int *seqlens, void *o, float *lse, float *weights, int B, int Hq,
+                       int Hkv, int P, int d, float scale, int max_seqlen, void *workspace, size_t workspace_bytes,
+                       attn_stream_t stream);
+
+/* Workspace bytes attn_decode_prefix needs on the current device (0 for sizes
+ * that it refuses, or when the device cannot be queried). */
+size_t attn_decode_prefix_workspace_bytes(int B, int Hq, int Hkv, int P, int d, int max_seqlen, int with_weights);
+
+/* Host-side view of the prefix phase: the i-th piece of work of CTA `cta` on a
+ * GPU of num_sms SMs, as out[5] = {KV head, unit of up to 256 query rows, first
+ * 128-key block, blocks, partial's slot}.  Returns 1, 0 when that CTA has no
+ * i-th piece, or ATTN_ERR_ARG (sizes, or cta outside the grid).  Pure host
+ * code; the same functions run inside the kernel. */
+int attn_decode_prefix_segment(int B, int Hq, int Hkv, int P, int num_sms, int cta, int i, int *out);
+
 /* Host-side view of the forward scheduler: unit `unit` of the order maps to
  * (*b, *h, *m) where m is the index of a 256-row block.  Pure host code; the
  * same function runs inside the kernel.  Orders 0-2 only (the die-split order

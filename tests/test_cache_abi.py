@@ -108,3 +108,75 @@ def test_rope_helpers_refuse_what_an_address_does_not_tell():
         with pytest.raises(attn.AttnError) as e:
             call()
         assert e.value.code == ARG
+
+
+# ------------------------------------------------------ shared-prefix decode
+def _prefix(**kw):
+    a = dict(q=A16, kp=A16, vp=A16, kc=A16, vc=A16, lens=A16, o=A16, lse=None, w=None, B=2, Hq=4, Hkv=2, P=100, d=64,
+             scale=0.125, S=32, ws=A16, nbytes=1 << 40)
+    a.update(kw)
+    return attn.attn_decode_prefix(*a.values(), stream=0)
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(q=None), ARG), (dict(q=A16 + 8), ARG), (dict(o=None), ARG), (dict(kp=None), ARG), (dict(vp=A16 + 2), ARG),
+    (dict(kc=None), ARG), (dict(vc=A16 + 8), ARG), (dict(lens=None), ARG), (dict(lens=A16 + 2), ARG),
+    (dict(lse=A16 + 1), ARG), (dict(w=A16 + 2), ARG), (dict(w=A16, S=0), ARG), (dict(P=0, S=0), ARG), (dict(P=-1), ARG),
+    (dict(S=-1), ARG), (dict(B=0), ARG), (dict(Hq=3), ARG), (dict(scale=0.0), ARG), (dict(scale=float("nan")), ARG),
+    (dict(d=56), UNSUP), (dict(d=256), UNSUP), (dict(Hq=34, Hkv=2), UNSUP), (dict(ws=None), WS), (dict(ws=A16 + 8), WS),
+    (dict(P=0, kp=None, vp=None, kc=None), ARG), (dict(S=0, kc=None, vc=None, lens=None, ws=None), WS),
+])
+def test_decode_prefix_refusals(kw, code):
+    assert _prefix(**kw) == code
+
+
+@pytest.mark.parametrize("sms", [152, 8, 1])
+@pytest.mark.parametrize("B,Hq,Hkv,P", [
+    (1, 1, 1, 1), (1, 8, 1, 129), (4, 8, 2, 500), (32, 64, 8, 8192), (128, 64, 8, 32768), (7, 40, 8, 5001),
+    (300, 16, 16, 1000), (2000, 64, 4, 700), (1000, 15, 1, 257), (5000, 16, 1, 300)])
+def test_prefix_segments_cover_every_block_once(B, Hq, Hkv, P, sms):
+    """Every (KV head, unit, key block) belongs to one segment; a row's slots are 0, 1, ... without gaps; no CTA has more
+    than about its equal share of blocks; the grid is at most one CTA per SM."""
+    G, nblk = Hq // Hkv, -(-P // 128)
+    units = (-(-B // (128 // G)) + 1) // 2
+    seen, slots, load = {}, {}, []
+    cta = 0
+    while True:
+        try:
+            first = attn.attn_decode_prefix_segment(B, Hq, Hkv, P, sms, cta, 0)
+        except attn.AttnError:
+            break
+        assert first is not None
+        mine, i = 0, 0
+        while (s := attn.attn_decode_prefix_segment(B, Hq, Hkv, P, sms, cta, i)) is not None:
+            g, m, j0, n, slot = s
+            assert n > 0 and 0 <= g < Hkv and 0 <= m < units and j0 + n <= nblk
+            for j in range(j0, j0 + n):
+                assert (g, m, j) not in seen
+                seen[g, m, j] = cta
+            slots.setdefault((g, m), set()).add(slot)
+            mine, i = mine + n, i + 1
+        load.append(mine)
+        cta += 1
+    assert cta <= sms
+    assert len(seen) == Hkv * units * nblk
+    for s in slots.values():
+        assert s == set(range(len(s)))
+    assert max(load) <= -(-Hkv * units * nblk // max(1, int(0.9 * sms))) + units
+
+
+def test_prefix_segment_refusals():
+    for args in [(0, 4, 2, 100, 152, 0, 0), (2, 4, 2, 0, 152, 0, 0), (2, 4, 2, 100, 0, 0, 0), (2, 4, 2, 100, 152, -1, 0),
+                 (2, 4, 2, 100, 152, 152, 0), (2, 4, 2, 100, 152, 0, -1)]:
+        with pytest.raises(attn.AttnError):
+            attn.attn_decode_prefix_segment(*args)
+
+
+def test_decode_helpers_refuse_what_an_address_does_not_tell():
+    z = lambda *s, dtype=torch.bfloat16: torch.zeros(s, dtype=dtype)
+    n = z(1, dtype=torch.int32)
+    for call in (lambda: attn.decode_prefix(z(1, 2, 64), z(2, 5, 64), z(2, 5, 64), z(1, 2, 9, 64), z(1, 2, 9, 64), n),
+                 lambda: attn.decode_weighted(z(1, 2, 64), z(1, 2, 9, 64), z(1, 2, 9, 64), n, z(1, 2, 9))):
+        with pytest.raises(attn.AttnError) as e:
+            call()
+        assert e.value.code == ARG
