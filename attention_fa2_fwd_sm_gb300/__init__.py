@@ -71,6 +71,8 @@ SIGNATURES = {
     "attn_decode_prefix": (_I, [_P] * 9 + [_I] * 5 + [_F, _I, _P, _SZ, _P]),
     "attn_decode_prefix_workspace_bytes": (_SZ, [_I] * 7),
     "attn_decode_prefix_segment": (_I, [_I] * 7 + [_IP]),
+    "attn_cache_evict": (_I, [_P] * 11 + [_I] * 7 + [_P, _SZ, _P]),
+    "attn_cache_evict_workspace_bytes": (_SZ, [_I] * 5),
     "attn_tile_map": (_I, [_I, _I, _I, _I, _I, _I, _LL, _IP, _IP, _IP]),
     "attn_tile_map_die_split": (_I, [_I, _I, _I, _I, _I, _I, _LL, _IP, _IP, _IP]),
     "attn_bwd_tile_map": (_I, [_I, _I, _I, _I, _I, _I, _LL, _IP, _IP, _IP]),
@@ -377,6 +379,19 @@ def attn_decode_prefix_segment(B, Hq, Hkv, P, num_sms, cta, i):
     return tuple(out) if rc else None
 
 
+def attn_cache_evict(kcache, vcache, weights, cache_pos, seqlens, cur_pos, kout, vout, weights_out, pos_out,
+                     seqlens_out, B, Hkv, d, max_seqlen, out_seqlen, keep, recent, workspace, workspace_bytes,
+                     stream=None) -> int:
+    return lib().attn_cache_evict(_ptr(kcache), _ptr(vcache), _ptr(weights), _ptr(cache_pos), _ptr(seqlens),
+                                  _ptr(cur_pos), _ptr(kout), _ptr(vout), _ptr(weights_out), _ptr(pos_out),
+                                  _ptr(seqlens_out), B, Hkv, d, max_seqlen, out_seqlen, keep, recent, _ptr(workspace),
+                                  workspace_bytes, _stream(stream))
+
+
+def attn_cache_evict_workspace_bytes(B, Hkv, max_seqlen, keep, in_place) -> int:
+    return lib().attn_cache_evict_workspace_bytes(B, Hkv, max_seqlen, keep, int(bool(in_place)))
+
+
 def attn_rope_freqs(rotary_dim, base=10000.0, rule=0, factor=1.0, low=1.0, high=4.0, trained_len=8192.0):
     """List of rotary_dim / 2 frequencies (radians per position) by one of ROPE_RULES."""
     buf = (ctypes.c_double * max(int(rotary_dim) // 2, 1))()
@@ -597,6 +612,59 @@ def decode_weighted(q, kcache, vcache, seqlens, weights, scale=None, workspace=N
     """A decode step that adds to `weights` what every cached key receives:
     `decode_prefix` without a prefix."""
     return decode_prefix(q, None, None, kcache, vcache, seqlens, scale, weights, workspace, with_lse, stream)
+
+
+def cache_evict(kcache, vcache, weights, seqlens, keep, recent=0, cache_pos=None, cur_pos=None, out=None,
+                seqlens_out=None, workspace=None, stream=None):
+    """Keep `keep` keys of every head's cache ``[B, Hkv, max_seqlen, d]`` by
+    attn_cache_evict: the `recent` latest, then the heaviest by `weights` ``[B,
+    Hkv, max_seqlen]`` fp32.  In place, unless `out` is a dict of tensors to
+    write instead: ``kcache`` and ``vcache`` ``[B, Hkv, slots, d]``, optionally
+    ``weights``, ``cache_pos`` ``[B, Hkv, slots]`` and ``seqlens``.  Allocates
+    the new lengths and the workspace where they are not given; returns
+    ``(seqlens_out, workspace)`` (`workspace` is None where none is needed)."""
+    import torch
+    what, bf16, i32, f32 = "cache_evict", torch.bfloat16, torch.int32, torch.float32
+    gpu = _gpu_of(what, kcache)
+    there = _elsewhere(what, gpu, stream)
+    if there is not None:
+        with there:
+            return cache_evict(kcache, vcache, weights, seqlens, keep, recent, cache_pos, cur_pos, out, seqlens_out,
+                               workspace)
+    if kcache.dim() != 4:
+        raise AttnError(ATTN_ERR_ARG, "cache_evict: the caches have to be [B, Hkv, max_seqlen, d]")
+    B, Hkv, s_max, d = kcache.shape
+    cache, per_key = kcache.shape, (B, Hkv, s_max)
+    _fits(kcache, bf16, cache, gpu) or _refuse(what, "kcache", kcache, bf16, cache)
+    _fits(vcache, bf16, cache, gpu) or _refuse(what, "vcache", vcache, bf16, cache)
+    _fits(weights, f32, per_key, gpu) or _refuse(what, "weights", weights, f32, per_key)
+    _fits(seqlens, i32, (B,), gpu) or _refuse(what, "seqlens", seqlens, i32, (B,))
+    cache_pos is None or _fits(cache_pos, i32, per_key, gpu) or _refuse(what, "cache_pos", cache_pos, i32, per_key)
+    cur_pos is None or _fits(cur_pos, i32, (B,), gpu) or _refuse(what, "cur_pos", cur_pos, i32, (B,))
+    kout, vout, wout, pout, s_out = kcache, vcache, weights, cache_pos, s_max
+    if out is not None:
+        kout, vout, wout, pout = out["kcache"], out["vcache"], out.get("weights"), out.get("cache_pos")
+        if seqlens_out is None:
+            seqlens_out = out.get("seqlens")
+        if kout.dim() != 4:
+            raise AttnError(ATTN_ERR_ARG, "cache_evict: out's caches have to be [B, Hkv, slots, d]")
+        s_out = kout.shape[2]
+        shape, per_slot = (B, Hkv, s_out, d), (B, Hkv, s_out)
+        _fits(kout, bf16, shape, gpu) or _refuse(what, "out's kcache", kout, bf16, shape)
+        _fits(vout, bf16, shape, gpu) or _refuse(what, "out's vcache", vout, bf16, shape)
+        wout is None or _fits(wout, f32, per_slot, gpu) or _refuse(what, "out's weights", wout, f32, per_slot)
+        pout is None or _fits(pout, i32, per_slot, gpu) or _refuse(what, "out's cache_pos", pout, i32, per_slot)
+    if seqlens_out is None:
+        seqlens_out = torch.empty_like(seqlens)
+    else:
+        _fits(seqlens_out, i32, (B,), gpu) or _refuse(what, "seqlens_out", seqlens_out, i32, (B,))
+    nbytes = attn_cache_evict_workspace_bytes(B, Hkv, s_max, keep, kout.data_ptr() == kcache.data_ptr())
+    if nbytes or workspace is not None:
+        workspace, nbytes = _workspace(what, workspace, nbytes, kcache, gpu)
+    rc = attn_cache_evict(kcache, vcache, weights, cache_pos, seqlens, cur_pos, kout, vout, wout, pout, seqlens_out, B,
+                          Hkv, d, s_max, s_out, keep, recent, workspace, nbytes)
+    check(rc, "attn_cache_evict")
+    return seqlens_out, workspace
 
 
 def forward(q, k, v, causal=False, scale=None, tile_order=ORDER_HEAD_FIRST, with_lse=True,

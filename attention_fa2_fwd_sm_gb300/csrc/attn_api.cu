@@ -807,6 +807,86 @@ int attn_decode_prefix_segment(int B, int Hq, int Hkv, int P, int num_sms, int c
     return 1;
 }
 
+size_t attn_cache_evict_workspace_bytes(int B, int Hkv, int max_seqlen, int keep, int in_place) {
+    if (B <= 0 || Hkv <= 0 || max_seqlen <= 0 || keep <= 0 || (long long)B * Hkv > 0x7fffffffLL) return 0;
+    EvictLaunch a = {};
+    a.B = B;
+    a.Hkv = Hkv;
+    a.max_seqlen = max_seqlen;
+    a.keep = keep;
+    a.kout = in_place ? nullptr : &a;  // in place: the same address as kcache
+    return evict_workspace_bytes(a);
+}
+
+// Whether [a, a + n) and [b, b + m) share a byte.
+static bool bytes_overlap(const void *a, size_t n, const void *b, size_t m) {
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+    return a && b && x < y + m && y < x + n;
+}
+
+int attn_cache_evict(const void *kcache, const void *vcache, const float *weights, const int *cache_pos,
+                     const int *seqlens, const int *cur_pos, void *kout, void *vout, float *weights_out, int *pos_out,
+                     int *seqlens_out, int B, int Hkv, int d, int max_seqlen, int out_seqlen, int keep, int recent,
+                     void *workspace, size_t workspace_bytes, attn_stream_t stream) {
+    if (B <= 0 || Hkv <= 0 || max_seqlen <= 0 || out_seqlen <= 0 || keep <= 0 || keep > out_seqlen || recent < 0 ||
+        recent > keep)
+        return ATTN_ERR_ARG;
+    if (d <= 0 || d % 8 || d > 512) return ATTN_ERR_UNSUPPORTED;
+    if ((long long)B * Hkv > 0x7fffffffLL || max_seqlen > (1 << 30)) return ATTN_ERR_ARG;
+    const size_t rows = (size_t)B * Hkv;
+    if ((double)rows * (max_seqlen > out_seqlen ? max_seqlen : out_seqlen) * d >= 4.0e18) return ATTN_ERR_ARG;
+    if (!aligned16(kcache) || !aligned16(vcache) || !aligned16(kout) || !aligned16(vout)) return ATTN_ERR_ARG;
+    if (!weights || !seqlens) return ATTN_ERR_ARG;
+    for (const void *ptr : {(const void *)weights, (const void *)cache_pos, (const void *)seqlens, (const void *)cur_pos,
+                            (const void *)weights_out, (const void *)pos_out, (const void *)seqlens_out})
+        if (!aligned4(ptr)) return ATTN_ERR_ARG;
+    if (ints_overlap(seqlens_out, seqlens, B) || ints_overlap(seqlens_out, cur_pos, B)) return ATTN_ERR_ARG;
+    const bool in_place = kout == kcache;
+    if (in_place) {
+        if (vout != vcache || weights_out != weights || pos_out != cache_pos || out_seqlen != max_seqlen || kout == vout)
+            return ATTN_ERR_ARG;
+    } else {
+        // An output may overlap no input and no other output.
+        const size_t in4 = rows * max_seqlen * 4, out4 = rows * out_seqlen * 4;
+        const size_t in = rows * max_seqlen * d * 2, out = rows * out_seqlen * d * 2;
+        const struct {
+            const void *p;
+            size_t n;
+        } ins[] = {{kcache, in}, {vcache, in}, {weights, in4}, {cache_pos, in4}},
+          outs[] = {{kout, out}, {vout, out}, {weights_out, out4}, {pos_out, out4}};
+        for (int i = 0; i < 4; ++i)
+            for (int j = 0; j < 4; ++j)
+                if (bytes_overlap(outs[i].p, outs[i].n, ins[j].p, ins[j].n) ||
+                    (j < i && bytes_overlap(outs[i].p, outs[i].n, outs[j].p, outs[j].n)))
+                    return ATTN_ERR_ARG;
+    }
+    EvictLaunch a;
+    a.kcache = kcache;
+    a.vcache = vcache;
+    a.weights = weights;
+    a.cache_pos = cache_pos;
+    a.seqlens = seqlens;
+    a.cur_pos = cur_pos;
+    a.kout = kout;
+    a.vout = vout;
+    a.weights_out = weights_out;
+    a.pos_out = pos_out;
+    a.seqlens_out = seqlens_out;
+    a.B = B;
+    a.Hkv = Hkv;
+    a.d = d;
+    a.max_seqlen = max_seqlen;
+    a.out_seqlen = out_seqlen;
+    a.keep = keep;
+    a.recent = recent;
+    a.workspace = static_cast<char *>(workspace);
+    const size_t need = evict_workspace_bytes(a);
+    if (need > 0 && (!workspace || !aligned16(workspace) || workspace_bytes < need)) return ATTN_ERR_WORKSPACE;
+    a.num_sms = current_num_sms();
+    if (a.num_sms <= 0) return note_cuda_error(cudaErrorNoDevice, "device query");
+    return evict_launch(a, reinterpret_cast<cudaStream_t>(stream));
+}
+
 int attn_device_status(attn_stream_t stream) {
     if (cudaStreamSynchronize(reinterpret_cast<cudaStream_t>(stream)) != cudaSuccess)
         return ATTN_ERR_CUDA;

@@ -149,6 +149,21 @@ struct RopeLaunch {
     int num_sms;
 };
 int rope_launch(const RopeLaunch &a, cudaStream_t stream);
+
+// Eviction by weight (evict_sm103.cu); in place when kout == kcache.
+struct EvictLaunch {
+    const void *kcache, *vcache;
+    const float *weights;
+    const int *cache_pos, *seqlens, *cur_pos;  // cache_pos: null is the slot; cur_pos: null is the last slot
+    void *kout, *vout;
+    float *weights_out;               // may be null out of place
+    int *pos_out, *seqlens_out;       // may be null
+    int B, Hkv, d, max_seqlen, out_seqlen, keep, recent;
+    char *workspace;
+    int num_sms;
+};
+size_t evict_workspace_bytes(const EvictLaunch &a);
+int evict_launch(const EvictLaunch &a, cudaStream_t stream);
 int decode_launch(const DecodeLaunch &a, cudaStream_t stream);
 
 // Decode over a shared prefix and the sequences' own keys

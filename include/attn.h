@@ -27,8 +27,8 @@
  *  - Return value: ATTN_OK (0) or one of the negative ATTN_ERR_* codes.
  *    attn_strerror() gives a message for each.
  *  - CUDA graphs: the launches of attn_fwd, attn_fwd_ex, attn_fwd_host,
- *    attn_bwd, the decode entry points, attn_rope and attn_rope_append can be
- *    captured into a CUDA graph on `stream` and replayed; a replay reads what the buffers hold at replay
+ *    attn_bwd, the decode entry points, attn_rope, attn_rope_append and
+ *    attn_cache_evict can be captured into a CUDA graph on `stream` and replayed; a replay reads what the buffers hold at replay
  *    time (the ragged decode's seqlens included: it plans on the device).
  *    Make one ordinary call per device first (it sets up per-device state:
  *    kernel attributes, scratch addresses, the die map, the host-copy
@@ -543,6 +543,48 @@ size_t attn_decode_prefix_workspace_bytes(int B, int Hq, int Hkv, int P, int d, 
  * i-th piece, or ATTN_ERR_ARG (sizes, or cta outside the grid).  Pure host
  * code; the same functions run inside the kernel. */
 int attn_decode_prefix_segment(int B, int Hq, int Hkv, int P, int num_sms, int cta, int i, int *out);
+
+/*
+ * Eviction from a decode cache by accumulated attention weight (the weights
+ * that attn_decode_prefix adds up).  Every KV head of every sequence with more
+ * than `keep` keys keeps `keep` of them: first the recent ones (cache_pos >
+ * cur_pos[b] - recent), then those of the largest weight; among equals the
+ * lowest slot is kept.  Kept keys in slots below `keep` stay there; the i-th
+ * slot below `keep` whose key goes receives the i-th kept key from the slots at
+ * or past `keep`, in slot order, with its value, weight and position.  (The
+ * order of the keys means nothing to attention.)  A sequence with at most
+ * `keep` keys keeps them all.
+ *   kcache, vcache  [B, Hkv, max_seqlen, d] bf16
+ *   weights    [B, Hkv, max_seqlen] fp32.  NaN counts as below every number.
+ *   cache_pos  [B, Hkv, max_seqlen] int32 position of every key (as
+ *              attn_rope_append writes them), or NULL: the slot.  Needed once
+ *              keys have been evicted, since slots then no longer tell.
+ *   seqlens    [B] int32, clamped to [0, max_seqlen]
+ *   cur_pos    [B] int32, position of the newest token, or NULL: the clamped
+ *              seqlens[b] - 1
+ *   kout, vout, weights_out, pos_out  receive the first min(seqlens[b], keep)
+ *              slots.  In place: all four equal to the inputs, out_seqlen ==
+ *              max_seqlen; slots from `keep` on are left as they were.
+ *              Otherwise [B, Hkv, out_seqlen, ...] arrays that overlap no
+ *              input, where weights_out and pos_out may be NULL; slots past
+ *              the kept ones are left as they were.
+ *   seqlens_out [B] int32, min(seqlens[b], keep), or NULL; must not overlap
+ *              seqlens or cur_pos
+ *   1 <= keep <= out_seqlen; 0 <= recent <= keep; d a multiple of 8, at most
+ *   512; B * Hkv < 2^31; max_seqlen <= 2^30.
+ *   workspace  at least attn_cache_evict_workspace_bytes(...) bytes, 16-byte
+ *              aligned (may be NULL when that is 0)
+ * One or two kernels on `stream`; results do not depend on any order of
+ * execution.
+ */
+int attn_cache_evict(const void *kcache, const void *vcache, const float *weights, const int *cache_pos,
+                     const int *seqlens, const int *cur_pos, void *kout, void *vout, float *weights_out, int *pos_out,
+                     int *seqlens_out, int B, int Hkv, int d, int max_seqlen, int out_seqlen, int keep, int recent,
+                     void *workspace, size_t workspace_bytes, attn_stream_t stream);
+
+/* Workspace bytes attn_cache_evict needs (0 for bad sizes, and in place where
+ * max_seqlen - keep <= 64).  Pure host code. */
+size_t attn_cache_evict_workspace_bytes(int B, int Hkv, int max_seqlen, int keep, int in_place);
 
 /* Host-side view of the forward scheduler: unit `unit` of the order maps to
  * (*b, *h, *m) where m is the index of a 256-row block.  Pure host code; the

@@ -180,3 +180,37 @@ def test_decode_helpers_refuse_what_an_address_does_not_tell():
         with pytest.raises(attn.AttnError) as e:
             call()
         assert e.value.code == ARG
+
+
+# ----------------------------------------------------------------- eviction
+def _evict(**kw):
+    M = 1 << 24  # far apart: nothing overlaps
+    a = dict(kc=M, vc=2 * M, w=3 * M, pos=4 * M, lens=A16, cur=None, ko=M, vo=2 * M, wo=3 * M, po=4 * M, lo=A16 + 64,
+             B=2, Hkv=2, d=64, S=512, So=512, keep=100, recent=10, ws=A16, nbytes=1 << 30)
+    a.update(kw)
+    return attn.attn_cache_evict(*a.values(), stream=0)
+
+
+OUT = dict(ko=5 << 24, vo=6 << 24, wo=7 << 24, po=8 << 24)
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(kc=None), ARG), (dict(vc=8), ARG), (dict(w=None), ARG), (dict(lens=None), ARG), (dict(lens=A16 + 1), ARG),
+    (dict(cur=A16 + 2), ARG), (dict(lo=A16), ARG), (dict(lo=A16 + 4), ARG), (dict(cur=A16 + 64), ARG), (dict(B=0), ARG),
+    (dict(S=0), ARG), (dict(keep=0), ARG), (dict(keep=513), ARG), (dict(recent=101), ARG), (dict(recent=-1), ARG),
+    (dict(d=60), UNSUP), (dict(d=520), UNSUP), (dict(So=600), ARG), (dict(vo=9 << 24), ARG), (dict(wo=None), ARG),
+    (dict(po=None), ARG), (dict(S=(1 << 30) + 1, So=(1 << 30) + 1), ARG), (dict(ws=None), WS), (dict(ws=A16 + 8), WS),
+    (dict(nbytes=64), WS),
+    (dict(OUT, vo=5 << 24), ARG), (dict(OUT, ko=(1 << 24) + 4096), ARG), (dict(OUT, wo=3 << 24), ARG),
+    (dict(OUT, po=(7 << 24) + 64), ARG), (dict(OUT, nbytes=64), WS),
+])
+def test_evict_refusals(kw, code):
+    assert _evict(**kw) == code
+
+
+def test_evict_workspace():
+    ws = attn.attn_cache_evict_workspace_bytes
+    assert ws(2, 2, 164, 100, True) == 0 and ws(2, 2, 165, 100, True) > 0  # few slots past the kept ones: one kernel
+    assert ws(2, 2, 164, 100, False) >= 4 * 4 * (100 + 2 * 64)
+    assert ws(0, 2, 300, 100, True) == ws(2, 0, 300, 100, True) == ws(2, 2, 0, 100, True) == ws(2, 2, 300, 0, True) == 0
+    assert ws(2, 2, 80, 100, False) >= 4 * 4 * 80  # a cache below the bound is only copied
