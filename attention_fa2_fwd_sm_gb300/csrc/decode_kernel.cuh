@@ -131,69 +131,71 @@ __device__ __forceinline__ uint32_t mask_pair(uint32_t r, int k_lo, int n_valid)
     return r;
 }
 
-// Work item `item` of the own keys' grid, found by the whole CTA: T = total
-// keys, chunk C = max(min_chunk, ceil(T * Hkv / target) rounded up to 64),
-// sequence b in ceil(len_b / C) items numbered consecutively.  Returns false
-// when there is no such item.  The CTA of (item 0, KV head 0) writes the
-// plan's head, and each KV head 0 CTA its item.  (A plan kernel ahead of the
-// grid would cost a launch; the lengths of a batch are a few hundred bytes.)
+// Work item `item` of the own keys' grid: T = total keys, chunk C =
+// max(min_chunk, ceil(T * Hkv / target) rounded up to 64), sequence b in
+// ceil(len_b / C) items numbered consecutively.  Returns false when there is no
+// such item.  The CTA of (item 0, KV head 0) writes the plan's head, and each
+// KV head 0 CTA its item.  Every warp does the whole search by itself, from the
+// lengths in registers for up to 256 sequences: no plan kernel ahead of the
+// grid (a launch) and no barriers.
 __device__ __forceinline__ bool own_item(const OwnParams &p, int item, int g, int &b, int &lo, int &hi) {
-    __shared__ long long part[kThreads / 32];
-    __shared__ int found[2];
-    const int t = threadIdx.x, lane = t & 31, w = t >> 5;
-    const int per = (p.B + kThreads - 1) / kThreads;
-    const int b0 = min(t * per, p.B), b1 = min(b0 + per, p.B);
-    auto len_of = [&](int i) { return min(max(p.seqlens[i], 0), p.max_seqlen); };
-    auto block_scan = [&](long long v, long long &total) {
-        long long x = v;
+    constexpr int kRound = 8;  // groups of 32 sequences whose lengths are loaded together
+    const int lane = threadIdx.x & 31;
+    int len[kRound];
+    auto load = [&](int first) {
 #pragma unroll
-        for (int off = 1; off < 32; off <<= 1) {
-            const long long y = __shfl_up_sync(0xffffffffu, x, off);
-            if (lane >= off) x += y;
+        for (int k = 0; k < kRound; ++k) {
+            const int i = first + 32 * k + lane;
+            len[k] = i < p.B ? min(max(p.seqlens[i], 0), p.max_seqlen) : 0;
         }
-        __syncthreads();
-        if (lane == 31) part[w] = x;
-        __syncthreads();
-        long long before = 0;
-        total = 0;
-        for (int i = 0; i < kThreads / 32; ++i) {
-            if (i < w) before += part[i];
-            total += part[i];
-        }
-        return before + x - v;
     };
-    if (t == 0) found[0] = -1;
-    long long keys = 0, T = 0, count = 0, mine = 0;
-    for (int i = b0; i < b1; ++i) keys += len_of(i);
-    block_scan(keys, T);
+    long long T = 0;
+    for (int first = 0; first < p.B; first += 32 * kRound) {
+        load(first);
+#pragma unroll
+        for (int k = 0; k < kRound; ++k) T += len[k];
+    }
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) T += __shfl_xor_sync(0xffffffffu, T, off);
     long long c = (T * p.Hkv + p.target - 1) / p.target;
     c = (c + kChunkGranule - 1) / kChunkGranule * kChunkGranule;
-    const int C = int(min(max(c, (long long)p.min_chunk), 0x40000000LL));
-    for (int i = b0; i < b1; ++i) mine += (len_of(i) + C - 1) / C;
-    int first = int(block_scan(mine, count));
-    const bool head = item == 0 && g == 0;
-    if (head && t == 0) {
-        p.plan_out[0] = int(count);
-        p.plan_out[1] = C;
-    }
-    for (int i = b0; i < b1; ++i) {
-        const int n = (len_of(i) + C - 1) / C;
-        if (head) {
-            p.plan_out[2 + i] = first;
-            p.plan_out[2 + p.B + i] = n;
+    const unsigned C = unsigned(min(max(c, (long long)p.min_chunk), 0x40000000LL));
+    const bool head = item == 0 && g == 0 && threadIdx.x < 32;
+    int count = 0;  // items of the sequences before
+    b = -1;
+    for (int first = 0; first < p.B && (head || b < 0); first += 32 * kRound) {
+        if (p.B > 32 * kRound) load(first);
+#pragma unroll
+        for (int k = 0; k < kRound; ++k) {
+            if (first + 32 * k >= p.B) break;
+            const int n = int((unsigned(len[k]) + C - 1) / C);
+            int upto = n;
+#pragma unroll
+            for (int off = 1; off < 32; off <<= 1) {
+                const int y = __shfl_up_sync(0xffffffffu, upto, off);
+                if (lane >= off) upto += y;
+            }
+            const int mine = count + upto - n;  // first item of this lane's sequence
+            const uint32_t hit = __ballot_sync(0xffffffffu, item >= mine && item < mine + n);
+            if (hit) {
+                const int at = __ffs(hit) - 1;
+                b = first + 32 * k + at;
+                lo = (item - __shfl_sync(0xffffffffu, mine, at)) * int(C);
+                hi = min(lo + int(C), __shfl_sync(0xffffffffu, len[k], at));
+            }
+            if (head && first + 32 * k + lane < p.B) {
+                p.plan_out[2 + first + 32 * k + lane] = mine;
+                p.plan_out[2 + p.B + first + 32 * k + lane] = n;
+            }
+            count += __shfl_sync(0xffffffffu, upto, 31);
         }
-        if (item >= first && item < first + n) {
-            found[0] = i;
-            found[1] = item - first;
-        }
-        first += n;
     }
-    __syncthreads();
-    b = found[0];
+    if (head && lane == 0) {
+        p.plan_out[0] = count;
+        p.plan_out[1] = int(C);
+    }
     if (b < 0) return false;
-    lo = found[1] * C;
-    hi = min(lo + C, len_of(b));
-    if (g == 0 && t == 0) {
+    if (g == 0 && threadIdx.x == 0) {
         int *it = p.plan_out + plan_items_offset(p.B) + 3 * item;
         it[0] = b;
         it[1] = lo;
@@ -229,6 +231,10 @@ __global__ void __launch_bounds__(kThreads)
     int b, lo, hi;
     if constexpr (kOwn) {
         griddep_launch_dependents();  // the finishing grid may be scheduled now
+        if (threadIdx.x == kConsumerWarps * 32) {
+            tma_prefetch_desc(&tmK);
+            tma_prefetch_desc(&tmV);
+        }
         if (!own_item(p, split, g, b, lo, hi)) {
             griddep_wait();
             return;
@@ -461,20 +467,21 @@ __global__ void __launch_bounds__(kThreads)
 #pragma unroll
         for (int w = 0; w < kConsumerWarps; ++w) M = fmaxf(M, cm[w * kMaxGroup + row]);
         float wsum = 0.f, osum = 0.f;
-        if (M != -INFINITY) {
+        if (kOwn || M != -INFINITY) {
+            const float ref = kOwn && M == -INFINITY ? 0.f : M;
 #pragma unroll
             for (int w = 0; w < kConsumerWarps; ++w) {
-                const float f = fast_exp2(cm[w * kMaxGroup + row] - M);
+                const float f = fast_exp2(cm[w * kMaxGroup + row] - ref);
                 wsum += f * cl[w * kMaxGroup + row];
                 osum += f * cw[(w * kMaxGroup + row) * D + col];
             }
         }
         const float o = wsum > 0.f ? osum / wsum : 0.f;
         const int h = g * G + row;
-        if constexpr (kOwn) {  // log2 units, as the scores
+        if constexpr (kOwn) {  // log2 units, as the scores; NaN stays NaN
             const size_t pi = (size_t)split * p.Hq + h;
-            p.ws_o[pi * D + col] = o;
-            if (col == 0) p.ws_lse[pi] = wsum > 0.f ? M + __log2f(wsum) : -INFINITY;
+            p.ws_o[pi * D + col] = wsum == 0.f ? 0.f : osum / wsum;
+            if (col == 0) p.ws_lse[pi] = wsum == 0.f ? -INFINITY : M + __log2f(wsum);
         } else if (p.plan) {
             const size_t pi = (size_t)split * p.Hq + h;
             p.ws_o[pi * D + col] = o;

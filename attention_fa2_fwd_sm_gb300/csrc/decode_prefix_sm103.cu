@@ -75,95 +75,158 @@ __device__ __forceinline__ RowParts row_parts(const FinishParams &p, int b, int 
     return r;
 }
 
-// Maximum and sum of 2^(lse_i - maximum) over a row's partials, by one warp.
-__device__ __forceinline__ void warp_total(const RowParts &r, int lane, float &top, float &sum) {
-    top = -INFINITY;
-    for (int i = lane; i < r.n; i += 32) top = fmaxf(top, r.lse(i));
+// Maximum and sum of 2^(lse_i - maximum) over a row's partials, by one warp;
+// w0 is 2^(lse_lane - maximum).
+__device__ __forceinline__ void warp_total(const RowParts &r, int lane, float &top, float &sum, float &w0) {
+    const float l0 = lane < r.n ? r.lse(lane) : -INFINITY;
+    top = l0;
+    for (int i = lane + 32; i < r.n; i += 32) top = fmaxf(top, r.lse(i));
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
-    sum = 0.f;
-    if (top != -INFINITY)
-        for (int i = lane; i < r.n; i += 32) sum += fast_exp2(r.lse(i) - top);
+    const float ref = top == -INFINITY ? 0.f : top;
+    sum = w0 = fast_exp2(l0 - ref);
+    for (int i = lane + 32; i < r.n; i += 32) sum += fast_exp2(r.lse(i) - ref);
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
 }
 
-// Grid: first a CTA for every (b, h), whose four warps take every fourth
-// partial of the row; then, with weights, one for every 1024 keys of every own
-// item of every KV head.
-template <int D>
+template <int kCols>
+struct Cols {
+    float v[kCols];
+};
+template <int kCols>
+__device__ __forceinline__ Cols<kCols> load_cols(const float *p) {
+    Cols<kCols> c;
+    if constexpr (kCols == 4) {
+        const float4 x = *reinterpret_cast<const float4 *>(p);
+        c.v[0] = x.x, c.v[1] = x.y, c.v[2] = x.z, c.v[3] = x.w;
+    } else {
+        const float2 x = *reinterpret_cast<const float2 *>(p);
+        c.v[0] = x.x, c.v[1] = x.y;
+    }
+    return c;
+}
+
+// Grid: first the rows (b, h), each by kWarps warps of a CTA; then, with
+// weights, a CTA for every 1024 keys of every own item of every KV head.
+// A row's chain is what bounds the merge: its counts, then its partials' L, then
+// their outputs.  The outputs do not depend on the L's, so the first eight of
+// each warp are loaded before L is known.  One warp a row when there are rows
+// enough to fill the GPU with; four take turns of eight partials when not.
+template <int D, int kWarps>
 __global__ void __launch_bounds__(kFinishThreads) finish_kernel(const FinishParams p) {
     constexpr int kCols = D / 32;  // columns of a lane
-    __shared__ float acc_sh[kFinishThreads / 32][D];
+    constexpr int kAhead = 8;
+    __shared__ float acc_sh[kWarps > 1 ? kFinishThreads / 32 : 1][D];
     __shared__ float lse_sh[dec::kMaxGroup];
     griddep_wait();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int rows = p.B * p.Hq;
-    if (int(blockIdx.x) < rows) {
-        const int row = blockIdx.x, b = row / p.Hq, h = row % p.Hq;
+    constexpr int kRows = kFinishThreads / 32 / kWarps;
+    const int row_ctas = (rows + kRows - 1) / kRows;
+    if (int(blockIdx.x) < row_ctas) {
+        const int row = blockIdx.x * kRows + warp / kWarps, q = warp % kWarps;
+        if (row >= rows) return;  // with kWarps > 1 a CTA is one row
+        const int b = row / p.Hq, h = row - b * p.Hq;
         const RowParts r = row_parts(p, b, h);
-        float top, sum;
-        warp_total(r, lane, top, sum);
-        float acc[kCols] = {};
         const size_t pre_step = (size_t)rows * D, own_step = (size_t)p.Hq * D;
         const float *pre = p.pre_o + (size_t)row * D + lane * kCols;
         const float *own = p.own_o + (p.plan ? ((size_t)p.plan[2 + b] * p.Hq + h) * D : 0) + lane * kCols;
-        if (top != -INFINITY) {
-#pragma unroll 4
-            for (int i = warp; i < r.n; i += kFinishThreads / 32) {
-                const float w = fast_exp2(r.lse(i) - top);
-                const float *src = i < r.n_pre ? pre + i * pre_step : own + (i - r.n_pre) * own_step;
-                if constexpr (kCols == 4) {
-                    const float4 v = *reinterpret_cast<const float4 *>(src);
-                    acc[0] += w * v.x, acc[1] += w * v.y, acc[2] += w * v.z, acc[3] += w * v.w;
-                } else {
-                    const float2 v = *reinterpret_cast<const float2 *>(src);
-                    acc[0] += w * v.x, acc[1] += w * v.y;
+        auto part = [&](int i) { return i < r.n_pre ? pre + i * pre_step : own + (i - r.n_pre) * own_step; };
+        Cols<kCols> v[kAhead];
+        auto fetch = [&](int i0) {
+#pragma unroll
+            for (int k = 0; k < kAhead; ++k)
+                if (i0 + k < r.n) v[k] = load_cols<kCols>(part(i0 + k));
+        };
+        fetch(q * kAhead);
+        float top, sum, w0;
+        warp_total(r, lane, top, sum, w0);
+        float acc[kCols] = {};
+        for (int i0 = q * kAhead; i0 < r.n; i0 += kAhead * kWarps) {
+            if (i0 > q * kAhead) fetch(i0);
+#pragma unroll
+            for (int k = 0; k < kAhead; ++k) {
+                const int i = i0 + k;
+                float w = __shfl_sync(0xffffffffu, w0, i & 31);
+                if (i < r.n) {
+                    if (i >= 32) w = fast_exp2(r.lse(i) - (top == -INFINITY ? 0.f : top));
+                    if (w != 0.f)  // an empty partial adds nothing
+#pragma unroll
+                        for (int c = 0; c < kCols; ++c) acc[c] += w * v[k].v[c];
                 }
             }
         }
+        if constexpr (kWarps > 1) {
 #pragma unroll
-        for (int c = 0; c < kCols; ++c) acc_sh[warp][lane * kCols + c] = acc[c];
-        __syncthreads();
-        if (threadIdx.x < D) {
-            float v = 0.f;
+            for (int c = 0; c < kCols; ++c) acc_sh[warp][lane * kCols + c] = acc[c];
+            __syncthreads();
+            if (warp > 0) return;
 #pragma unroll
-            for (int w = 0; w < kFinishThreads / 32; ++w) v += acc_sh[w][threadIdx.x];
-            p.o[(size_t)row * D + threadIdx.x] = __float2bfloat16_rn(sum > 0.f ? v / sum : 0.f);
+            for (int c = 0; c < kCols; ++c)
+                for (int w = 1; w < kWarps; ++w) acc[c] += acc_sh[w][lane * kCols + c];
         }
-        if (threadIdx.x == 0 && p.lse)
-            p.lse[row] = sum > 0.f ? (top + log2f(sum)) * 0.69314718055994531f : -INFINITY;
+        const float inv = sum == 0.f ? 0.f : 1.f / sum;  // NaN stays NaN
+        uint32_t packed[kCols / 2];
+#pragma unroll
+        for (int c = 0; c < kCols / 2; ++c) packed[c] = pack_bf16x2(acc[2 * c] * inv, acc[2 * c + 1] * inv);
+        __nv_bfloat16 *o = p.o + (size_t)row * D + lane * kCols;
+        if constexpr (kCols == 4) *reinterpret_cast<uint2 *>(o) = make_uint2(packed[0], packed[1]);
+        else *reinterpret_cast<uint32_t *>(o) = packed[0];
+        if (lane == 0 && p.lse) p.lse[row] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * 0.69314718055994531f;
         return;
     }
     // ------------------------------------------------------------- weights
-    long long i = (long long)blockIdx.x - rows;
-    const int sub = int(i % p.subs);
+    int i = int(blockIdx.x) - row_ctas;
+    const int sub = i % p.subs;
     i /= p.subs;
-    const int g = int(i % p.Hkv), item = int(i / p.Hkv);
+    const int g = i % p.Hkv, item = i / p.Hkv;
     if (item >= p.plan[0]) return;
     const int *it = p.plan + dec::plan_items_offset(p.B) + 3 * item;
     const int b = it[0], lo = it[1] + sub * kWeightKeys, hi = min(it[2], lo + kWeightKeys);
     if (lo >= hi) return;
     for (int h = warp; h < p.G; h += kFinishThreads / 32) {
-        float top, sum;
-        warp_total(row_parts(p, b, g * p.G + h), lane, top, sum);
+        float top, sum, w0;
+        warp_total(row_parts(p, b, g * p.G + h), lane, top, sum, w0);
         if (lane == 0) lse_sh[h] = top + log2f(sum);
     }
     __syncthreads();
     const size_t base = (size_t)(b * p.Hkv + g) * p.max_seqlen;
-    for (int j = lo + threadIdx.x; j < hi; j += kFinishThreads) {
-        const float *s = p.scores + (base + j) * p.G;
-        float w = 0.f;
+    constexpr int kKeys = 4;  // keys of a thread in flight
+    for (int j0 = lo + threadIdx.x; j0 < hi; j0 += kKeys * kFinishThreads) {
+        float old[kKeys], w[kKeys] = {};
+#pragma unroll
+        for (int k = 0; k < kKeys; ++k) {
+            const int j = j0 + k * kFinishThreads;
+            if (j < hi) old[k] = p.weights[base + j];
+        }
         if (p.G % 4 == 0) {
             for (int h = 0; h < p.G; h += 4) {
-                const float4 x = *reinterpret_cast<const float4 *>(s + h);
-                w += (fast_exp2(x.x - lse_sh[h]) + fast_exp2(x.y - lse_sh[h + 1])) +
-                     (fast_exp2(x.z - lse_sh[h + 2]) + fast_exp2(x.w - lse_sh[h + 3]));
+                float4 x[kKeys];
+#pragma unroll
+                for (int k = 0; k < kKeys; ++k) {
+                    const int j = j0 + k * kFinishThreads;
+                    if (j < hi) x[k] = __ldcs(reinterpret_cast<const float4 *>(p.scores + (base + j) * p.G + h));
+                }
+#pragma unroll
+                for (int k = 0; k < kKeys; ++k)
+                    if (j0 + k * kFinishThreads < hi)
+                        w[k] += (fast_exp2(x[k].x - lse_sh[h]) + fast_exp2(x[k].y - lse_sh[h + 1])) +
+                                (fast_exp2(x[k].z - lse_sh[h + 2]) + fast_exp2(x[k].w - lse_sh[h + 3]));
             }
         } else {
-            for (int h = 0; h < p.G; ++h) w += fast_exp2(s[h] - lse_sh[h]);
+            for (int h = 0; h < p.G; ++h)
+#pragma unroll
+                for (int k = 0; k < kKeys; ++k) {
+                    const int j = j0 + k * kFinishThreads;
+                    if (j < hi) w[k] += fast_exp2(p.scores[(base + j) * p.G + h] - lse_sh[h]);
+                }
         }
-        p.weights[base + j] += w;
+#pragma unroll
+        for (int k = 0; k < kKeys; ++k) {
+            const int j = j0 + k * kFinishThreads;
+            if (j < hi) p.weights[base + j] = old[k] + w[k];
+        }
     }
 }
 
@@ -200,11 +263,11 @@ int launch_prefix(const DecodePrefixLaunch &a, const PrefixOrder &po, float *par
         if (fa.numRegs != fwd::kLaunchRegs || fa.maxThreadsPerBlock < fwd::kThreads)
             return note_cuda_error(cudaErrorInvalidConfiguration,
                                    "fwd_kernel (prefix) register count differs from the setmaxnreg split");
-        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes);
+        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes + fwd::kTurnBytes);
         if (e != cudaSuccess) return note_cuda_error(e, "cudaFuncSetAttribute(fwd_kernel, prefix)");
         if (dev >= 0) attr_set[dev] = true;
     }
-    kernel<<<dim3(unsigned(po.grid)), dim3(fwd::kThreads), C::kSmemBytes, stream>>>(mq, mk, mv, p);
+    kernel<<<dim3(unsigned(po.grid)), dim3(fwd::kThreads), C::kSmemBytes + fwd::kTurnBytes, stream>>>(mq, mk, mv, p);
     const cudaError_t e = cudaGetLastError();
     return e == cudaSuccess ? 0 : note_cuda_error(e, "fwd_kernel (prefix) launch");
 }
@@ -272,7 +335,10 @@ int launch_all(const DecodePrefixLaunch &a, cudaStream_t stream) {
         return ATTN_ERR_ARG;
     float *pre_o = reinterpret_cast<float *>(a.workspace + l.pre_o);
     float *pre_lse = reinterpret_cast<float *>(a.workspace + l.pre_lse);
-    long long grid = (long long)a.B * a.Hq;
+    // Four warps a row while a warp a row would leave SMs short of two CTAs.
+    const long long rows = (long long)a.B * a.Hq;
+    const bool wide = rows < 8LL * a.num_sms;
+    long long grid = wide ? rows : (rows + kFinishThreads / 32 - 1) / (kFinishThreads / 32);
     if (a.weights) {
         f.subs = int((own_max_chunk(a.B, a.Hkv, a.max_seqlen, a.num_sms) + kWeightKeys - 1) / kWeightKeys);
         grid += (long long)l.own_items * a.Hkv * f.subs;
@@ -302,7 +368,8 @@ int launch_all(const DecodePrefixLaunch &a, cudaStream_t stream) {
     f.G = G;
     f.P = a.P;
     f.max_seqlen = a.max_seqlen;
-    const cudaError_t e = dec::launch_programmatic(finish_kernel<D>, dim3(unsigned(grid)), dim3(kFinishThreads), 0,
+    auto finish = wide ? finish_kernel<D, kFinishThreads / 32> : finish_kernel<D, 1>;
+    const cudaError_t e = dec::launch_programmatic(finish, dim3(unsigned(grid)), dim3(kFinishThreads), 0,
                                                    stream, f);
     return e == cudaSuccess ? 0 : note_cuda_error(e, "finish_kernel launch");
 }

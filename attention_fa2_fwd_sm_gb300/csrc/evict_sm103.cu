@@ -9,16 +9,24 @@
 // fewest rows: one per evicted key, instead of everything behind it.  No slot is
 // both read and written, so rows move in place and in parallel.
 //
-// select_kernel, a CTA a row: each key becomes a 32-bit rank whose unsigned order
-// is the order above (recent keys highest), kept in shared memory; a radix
-// select finds the keep-th largest rank in four 8-bit passes; two ballot passes
-// over the slots in order number the ties, the holes and the fillers.  The
-// histogram has a column per lane, so a warp's 32 increments never meet in one
-// bank although most weights share their exponent bits.  Work: 8 bytes a key
-// from HBM, then shared memory only.
+// select_kernel, one row a cluster of 1, 2, 4 or 8 CTAs, a contiguous range of
+// slots each: every key becomes a 32-bit rank whose unsigned order is the order
+// above (recent keys highest), kept in shared memory.  A radix select finds the
+// keep-th largest rank in four 8-bit passes: the CTAs count digits, exchange
+// their 256 counts through distributed shared memory and each take the same
+// digit; the second pass also gathers the ranks that still qualify, a few per
+// cent, so that the last two passes are short.  Two ballot sweeps over the slots
+// in order then number the holes and the fillers.  The histogram has a column
+// per lane, so a warp's 32 increments never meet in one bank although most
+// weights share their exponent bits.  What bounds it is one SM's instruction
+// rate (32K keys on one SM: 47 us with seven full passes), hence the cluster
+// where there are fewer rows than SMs.
+// Where at most kFewMoves keys go, the smallest are found one after the other
+// instead.
 // move_kernel: 2 * 2 d bytes a row each way, HBM-bound.  Where a cache has at
 // most kFusedMoves slots past `keep` (a decode loop that evicts what it appends)
 // the selecting CTA moves its rows itself and the second launch falls away.
+#include <cooperative_groups.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -32,18 +40,18 @@
 namespace attn {
 namespace evict {
 
-constexpr int kThreads = 1024;
-constexpr int kWarps = kThreads / 32;
 constexpr int kHistBytes = 256 * 32 * 4;
-constexpr int kMaxKeys = 48 * 1024;  // ranks that fit in shared memory; longer rows are read again each pass
+constexpr int kListKeys = 4096;       // ranks that the second pass may gather
+constexpr int kMaxKeys = 44 * 1024;  // of one CTA: ranks that fit in shared memory; longer ranges are read again each pass
 constexpr int kFusedMoves = 64;
+constexpr int kFewMoves = 8;
 
 struct Params {
     EvictLaunch a;
     int *head;     // [rows][2]: keys to move, n
     int *src;      // [rows][slots]: in place the fillers, else the source of every slot
     int *holes;    // [rows][gaps]
-    int slots, gaps, in_place;
+    int slots, gaps, in_place, cluster;
 };
 
 // Larger is kept longer.  NaN ranks below every number; -0 equals +0.
@@ -63,12 +71,13 @@ struct Row {
 };
 
 // Exclusive prefix of one value per warp, and the total.
+template <int kWarps>
 __device__ __forceinline__ int warp_offsets(int v, int *sh, int &total) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     __syncthreads();
     if (lane == 0) sh[warp] = v;
     __syncthreads();
-    int x = sh[lane];
+    int x = lane < kWarps ? sh[lane] : 0;
 #pragma unroll
     for (int off = 1; off < 32; off <<= 1) {
         const int y = __shfl_up_sync(0xffffffffu, x, off);
@@ -96,21 +105,46 @@ __device__ __forceinline__ void move_scalars(const EvictLaunch &a, long long row
     if (a.pos_out) a.pos_out[o] = a.cache_pos ? a.cache_pos[i] : from;
 }
 
-template <bool kShared, bool kFused>
+// Calls f(slot, rank) for the slots of [i0, i1) that this thread visits, `step`
+// apart, kBatch loads at a time.
+template <int kBatch, typename Load, typename F>
+__device__ __forceinline__ void visit(int i0, int i1, int step, Load load, F f) {
+    for (int i = i0; i < i1; i += kBatch * step) {
+        uint32_t x[kBatch];
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k)
+            if (i + k * step < i1) x[k] = load(i + k * step);
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k)
+            if (i + k * step < i1) f(i + k * step, x[k]);
+    }
+}
+
+// A cluster selects the kept keys of one row.  kFused: a single CTA, which also
+// moves them.
+template <bool kShared, bool kFused, int kThreads>
 __global__ void __launch_bounds__(kThreads) select_kernel(const Params p) {
+    namespace cg = cooperative_groups;
+    constexpr int kWarps = kThreads / 32;
     extern __shared__ uint32_t smem[];
     uint32_t *hist = smem;               // [256][32]
-    uint32_t *ranks = smem + 256 * 32;   // [n], when they fit
+    uint32_t *list = smem + 256 * 32;    // [kListKeys] gathered ranks
+    uint32_t *ranks = list + kListKeys;  // [keys of this CTA], when they fit
     __shared__ int part[kWarps];
+    __shared__ int counts[2][256];       // digit counts of this CTA (in turns: the others may still read the last)
+    __shared__ int totals[4];            // ties; holes and fillers; entries of the list
     __shared__ uint32_t found[2];        // the digit, and how many are above it
-    __shared__ int fused_holes[kFused ? kFusedMoves : 1], fused_src[kFused ? kFusedMoves : 1];
+    __shared__ unsigned long long least[kWarps];
+    __shared__ int fused_holes[kFused ? kFusedMoves : 1], fused_src[kFused ? kFusedMoves : 1], fused_moves;
     const EvictLaunch &a = p.a;
-    const long long row = blockIdx.x;
+    const cg::cluster_group cluster = cg::this_cluster();
+    const int peers = kFused ? 1 : p.cluster, peer = kFused ? 0 : int(cluster.block_rank());
+    const long long row = blockIdx.x / peers;
     const int b = int(row / a.Hkv), t = threadIdx.x, warp = t >> 5, lane = t & 31;
     if constexpr (!kFused) griddep_launch_dependents();
     const int n = min(max(a.seqlens[b], 0), a.max_seqlen);
     const int kept = min(n, a.keep);
-    if (t == 0) {
+    if (t == 0 && peer == 0) {
         if (a.seqlens_out && row == (long long)b * a.Hkv) a.seqlens_out[b] = kept;
         if constexpr (!kFused) p.head[2 * row + 1] = n;
     }
@@ -118,9 +152,9 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const Params p) {
     int *holes = kFused ? fused_holes : p.holes + row * p.gaps;
     if (n <= a.keep) {  // nothing to evict
         if constexpr (!kFused) {
-            if (t == 0) p.head[2 * row] = 0;
+            if (t == 0 && peer == 0) p.head[2 * row] = 0;
             if (!p.in_place)
-                for (int i = t; i < n; i += kThreads) src[i] = i;
+                for (int i = peer * kThreads + t; i < n; i += peers * kThreads) src[i] = i;
         }
         return;
     }
@@ -128,86 +162,202 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const Params p) {
     r.w = a.weights + row * a.max_seqlen;
     r.pos = a.cache_pos ? a.cache_pos + row * a.max_seqlen : nullptr;
     r.after = (long long)(a.cur_pos ? a.cur_pos[b] : n - 1) - a.recent;
-    auto rank = [&](int i) { return kShared ? ranks[i] : r.rank(i); };
+    // This CTA's slots.
+    const int chunk = ((n + peers - 1) / peers + 31) / 32 * 32;
+    const int lo = min(peer * chunk, n), hi = min(lo + chunk, n);
+    auto global_rank = [&](int i) { return r.rank(i); };
+    auto rank = [&](int i) { return kShared ? ranks[i - lo] : r.rank(i); };
+    auto cluster_sync = [&]() {
+        if (peers > 1) cluster.sync();
+        else __syncthreads();
+    };
+    int moves = 0;
 
-    // Radix select of the keep-th largest rank: `value` collects its digits,
-    // `want` counts down to its place among the ranks that share them.
-    uint32_t value = 0;
-    int want = a.keep;
-    for (int shift = 24; shift >= 0; shift -= 8) {
-        for (int i = t; i < 256 * 32; i += kThreads) hist[i] = 0;
-        __syncthreads();
-        const uint32_t mask = shift == 24 ? 0u : 0xffffffffu << (shift + 8);
-        for (int i = t; i < n; i += kThreads) {
-            uint32_t x;
-            if (kShared && shift == 24) ranks[i] = x = r.rank(i);
-            else x = rank(i);
-            if ((x & mask) == value) atomicAdd(&hist[(x >> shift & 255u) * 32 + lane], 1u);
+    if (kFused && n - a.keep <= kFewMoves) {
+        // A few keys go: find the smallest (rank, slot from the end), then the
+        // next one, a pass each.
+        if constexpr (kShared)
+            visit<8>(t, n, kThreads, global_rank, [&](int i, uint32_t x) { ranks[i] = x; });  // each thread its own
+        unsigned long long last = 0;
+        for (int e = 0; e < n - a.keep; ++e) {
+            unsigned long long low = ~0ull;
+            visit<8>(t, n, kThreads, rank, [&](int i, uint32_t x) {
+                const unsigned long long key = (unsigned long long)x << 32 | uint32_t(~i);
+                if ((e == 0 || key > last) && key < low) low = key;
+            });
+#pragma unroll
+            for (int off = 16; off > 0; off >>= 1) {
+                const unsigned long long y = __shfl_xor_sync(0xffffffffu, low, off);
+                low = y < low ? y : low;
+            }
+            if (lane == 0) least[warp] = low;
+            __syncthreads();
+            low = least[lane % kWarps];
+#pragma unroll
+            for (int off = kWarps / 2; off > 0; off >>= 1) {
+                const unsigned long long y = __shfl_xor_sync(0xffffffffu, low, off);
+                low = y < low ? y : low;
+            }
+            last = low;
+            if (t == 0) fused_src[e] = int(~uint32_t(low));  // evicted slots for now
+            __syncthreads();
+        }
+        if (t == 0) {
+            // Holes: the evicted slots below keep, in order.  Fillers: the slots past it that stay.
+            int gone[kFewMoves];
+            const int count = n - a.keep;
+            unsigned past = 0;
+            for (int e = 0; e < count; ++e) {
+                const int s = fused_src[e];
+                if (s >= a.keep) {
+                    past |= 1u << (s - a.keep);
+                    continue;
+                }
+                int at = moves++;
+                for (; at > 0 && gone[at - 1] > s; --at) gone[at] = gone[at - 1];
+                gone[at] = s;
+            }
+            for (int e = 0, f = 0; e < count; ++e)
+                if (!(past >> e & 1)) fused_src[f++] = a.keep + e;
+            for (int m = 0; m < moves; ++m) fused_holes[m] = gone[m];
+            fused_moves = moves;
         }
         __syncthreads();
-        // Column sums: warp w owns the 8 digits below 256 - 8 w, highest first.
-        int count[8], sum = 0;
+        moves = fused_moves;
+    } else {
+        // Radix select of the keep-th largest rank: `value` collects its digits,
+        // `want` counts down to its place among the ranks that share them.
+        uint32_t value = 0;
+        int want = a.keep;
+        bool gathered = false;  // the list holds every rank that still qualifies
+        if (t == 0) totals[3] = 0;
+        for (int shift = 24; shift >= 0; shift -= 8) {
+            for (int i = t; i < 256 * 32; i += kThreads) hist[i] = 0;
+            __syncthreads();
+            const uint32_t mask = shift == 24 ? 0u : 0xffffffffu << (shift + 8);
+            auto count = [&](uint32_t x) { atomicAdd(&hist[(x >> shift & 255u) * 32 + lane], 1u); };
+            if (shift == 24) {
+                visit<8>(lo + t, hi, kThreads, global_rank, [&](int i, uint32_t x) {
+                    if (kShared) ranks[i - lo] = x;
+                    count(x);
+                });
+            } else if (gathered) {
+                visit<4>(t, totals[3], kThreads, [&](int i) { return list[i]; },
+                         [&](int, uint32_t x) { if ((x & mask) == value) count(x); });
+            } else {
+                visit<8>(lo + t, hi, kThreads, rank, [&](int, uint32_t x) {
+                    if ((x & mask) != value) return;
+                    count(x);
+                    if (shift == 16) {
+                        const cg::coalesced_group some = cg::coalesced_threads();
+                        int at = 0;
+                        if (some.thread_rank() == 0) at = atomicAdd(&totals[3], int(some.size()));
+                        at = some.shfl(at, 0) + int(some.thread_rank());
+                        if (at < kListKeys) list[at] = x;
+                    }
+                });
+            }
+            __syncthreads();
+            if (shift == 16) gathered = totals[3] <= kListKeys;
+            // Column sums of this CTA, then over the cluster: warp w owns kDigits digits from 255 - kDigits w down.
+            constexpr int kDigits = 256 / kWarps;
+            int *mine = counts[shift >> 3 & 1];
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-            int c = int(hist[(255 - 8 * warp - k) * 32 + lane]);
+            for (int k = 0; k < kDigits; ++k) {
+                const int digit = 255 - kDigits * warp - k;
+                const int c = __reduce_add_sync(0xffffffffu, int(hist[digit * 32 + lane]));
+                if (lane == 0) mine[digit] = c;
+            }
+            cluster_sync();
+            // Lane k of a warp holds its k-th digit, highest first.
+            int c = 0;
+            if (lane < kDigits) {
+                const int digit = 255 - kDigits * warp - lane;
+                if (peers > 1)
+                    for (int q = 0; q < peers; ++q) c += cluster.map_shared_rank(mine, q)[digit];
+                else
+                    c = mine[digit];
+            }
+            int total, upto = c;
 #pragma unroll
-            for (int off = 16; off > 0; off >>= 1) c += __shfl_xor_sync(0xffffffffu, c, off);
-            count[k] = c;
-            sum += c;
-        }
-        int total;
-        int above = warp_offsets(sum, part, total);
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {
-            if (lane == 0 && above < want && above + count[k] >= want) {
-                found[0] = uint32_t(255 - 8 * warp - k);
+            for (int off = 1; off < 32; off <<= 1) {
+                const int y = __shfl_up_sync(0xffffffffu, upto, off);
+                if (lane >= off) upto += y;
+            }
+            const int above = warp_offsets<kWarps>(__shfl_sync(0xffffffffu, upto, 31), part, total) + upto - c;
+            if (lane < kDigits && above < want && above + c >= want) {
+                found[0] = uint32_t(255 - kDigits * warp - lane);
                 found[1] = uint32_t(above);
             }
-            above += count[k];
+            __syncthreads();
+            value |= found[0] << shift;
+            want -= int(found[1]);
         }
-        __syncthreads();
-        value |= found[0] << shift;
-        want -= int(found[1]);
-    }
 
-    // Slots in order, a contiguous range a warp.  Ties keep the first `want`.
-    const int range = (n + kWarps * 32 - 1) / (kWarps * 32) * 32;
-    const int i0 = min(warp * range, n), i1 = min(i0 + range, n);
-    const uint32_t below = (1u << lane) - 1;
-    int ties = 0, total;
-    for (int i = i0; i < i1; i += 32)
-        ties += __popc(__ballot_sync(0xffffffffu, i + lane < i1 && rank(i + lane) == value));
-    const int ties0 = warp_offsets(ties, part, total);
-    // Pass 0 counts the warp's holes and fillers, pass 1 writes them down.
-    int hole = 0, fill = 0, moves = 0;
-    for (int pass = 0; pass < 2; ++pass) {
-        int tie = ties0;
-        for (int i = i0; i < i1; i += 32) {
-            const int s = i + lane;
-            const uint32_t x = s < i1 ? rank(s) : 0;
-            const bool same = s < i1 && x == value;
-            const uint32_t same_mask = __ballot_sync(0xffffffffu, same);
-            const bool keep = s < i1 && (x > value || (same && tie + __popc(same_mask & below) < want));
-            tie += __popc(same_mask);
-            const bool is_hole = s < i1 && s < a.keep && !keep, is_fill = keep && s >= a.keep;
-            const uint32_t hm = __ballot_sync(0xffffffffu, is_hole), fm = __ballot_sync(0xffffffffu, is_fill);
-            if (pass == 1) {
-                if (is_hole) holes[hole + __popc(hm & below)] = s;
-                if (is_fill) {
-                    const int f = fill + __popc(fm & below);
-                    // Out of place the fillers wait behind the holes for src to be complete.
-                    if (p.in_place) src[f] = s;
-                    else holes[p.gaps / 2 + f] = s;
-                }
-                if (!p.in_place && s < a.keep && !is_hole && s < i1) src[s] = s;
+        // Slots in order, a contiguous range a warp.  Of the ranks equal to `value` the first `want` are kept.
+        const int range = (hi - lo + kWarps * 32 - 1) / (kWarps * 32) * 32;
+        const int i0 = min(lo + warp * range, hi), i1 = min(i0 + range, hi);
+        const uint32_t below = (1u << lane) - 1;
+        constexpr int kBatch = 4;
+        auto sweep = [&](auto f) {  // f(slot, rank, inside) by whole warps, in order
+            for (int i = i0; i < i1; i += kBatch * 32) {
+                uint32_t x[kBatch];
+#pragma unroll
+                for (int k = 0; k < kBatch; ++k) x[k] = i + k * 32 + lane < i1 ? rank(i + k * 32 + lane) : 0;
+#pragma unroll
+                for (int k = 0; k < kBatch; ++k)
+                    if (i + k * 32 < i1) f(i + k * 32 + lane, x[k], i + k * 32 + lane < i1);
             }
+        };
+        // First sweep: keys above `value` and ties, below `keep` and past it.
+        int up[2] = {0, 0}, tie[2] = {0, 0};
+        sweep([&](int s, uint32_t x, bool in) {
+            const bool past = s >= a.keep;
+            up[0] += __popc(__ballot_sync(0xffffffffu, in && x > value && !past));
+            up[1] += __popc(__ballot_sync(0xffffffffu, in && x > value && past));
+            tie[0] += __popc(__ballot_sync(0xffffffffu, in && x == value && !past));
+            tie[1] += __popc(__ballot_sync(0xffffffffu, in && x == value && past));
+        });
+        // Ties ahead of this warp's, then the holes and fillers ahead: within
+        // the CTA, and over the lower CTAs of the cluster.
+        auto offset = [&](int v, int slot, int &total) {
+            int at = warp_offsets<kWarps>(v, part, total);
+            if (peers > 1) {
+                if (t == 0) totals[slot] = total;
+                cluster.sync();
+                total = 0;
+                for (int q = 0; q < peers; ++q) {
+                    const int x = cluster.map_shared_rank(totals, q)[slot];
+                    at += q < peer ? x : 0;
+                    total += x;
+                }
+            }
+            return at;
+        };
+        int total;
+        int ties = offset(tie[0] + tie[1], 0, total);
+        const int left = max(want - ties, 0);  // ties that this warp may keep
+        const int mine_below = max(min(i1, a.keep) - i0, 0);
+        const int kept0 = up[0] + min(tie[0], left), kept1 = up[1] + min(tie[1], max(left - tie[0], 0));
+        int hole = offset(mine_below - kept0, 1, moves);
+        int fill = offset(kept1, 2, total);
+        sweep([&](int s, uint32_t x, bool in) {
+            const uint32_t same = __ballot_sync(0xffffffffu, in && x == value);
+            const bool keep = in && (x > value || (x == value && ties + __popc(same & below) < want));
+            ties += __popc(same);
+            const bool is_hole = in && s < a.keep && !keep, is_fill = keep && s >= a.keep;
+            const uint32_t hm = __ballot_sync(0xffffffffu, is_hole), fm = __ballot_sync(0xffffffffu, is_fill);
+            if (is_hole) holes[hole + __popc(hm & below)] = s;
+            if (is_fill) {
+                const int f = fill + __popc(fm & below);
+                // Out of place the fillers wait behind the holes for src to be complete.
+                if (p.in_place) src[f] = s;
+                else holes[p.gaps / 2 + f] = s;
+            }
+            if (!p.in_place && in && s < a.keep && !is_hole) src[s] = s;
             hole += __popc(hm);
             fill += __popc(fm);
-        }
-        if (pass == 0) {
-            hole = warp_offsets(hole, part, moves);
-            fill = warp_offsets(fill, part, total);
-        }
+        });
     }
     if constexpr (kFused) {
         __syncthreads();
@@ -218,45 +368,62 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const Params p) {
             if (u == 0) move_scalars(a, row, src[m], holes[m]);
         }
     } else {
-        if (t == 0) p.head[2 * row] = moves;
-        if (!p.in_place) {
-            __syncthreads();
-            for (int i = t; i < moves; i += kThreads) src[holes[i]] = holes[p.gaps / 2 + i];
-        }
+        if (t == 0 && peer == 0) p.head[2 * row] = moves;
+        // The lists are complete, and no CTA leaves while another may read its shared memory.
+        __threadfence();
+        cluster_sync();
+        if (!p.in_place)
+            for (int i = peer * kThreads + t; i < moves; i += peers * kThreads) src[holes[i]] = holes[p.gaps / 2 + i];
     }
 }
 
 constexpr int kMoveThreads = 256;
-constexpr int kMoveRows = 32;  // cache rows of one CTA's turn
-constexpr int kMoveBatch = 4;  // 16-byte units a thread has in flight
+constexpr int kMoveRows = 64;  // cache rows of one CTA's turn
+constexpr int kMoveBatch = 8;  // 16-byte units a thread has in flight
 
-// Grid-stride over (row, 32 moved keys).
+// Grid-stride over (row, 64 moved keys).  kUnits: 16-byte units of a key and its
+// value (d / 4) where that divides the CTA, so that a thread keeps one unit and
+// steps over keys without a division; 0: any d.
+template <int kUnits>
 __global__ void __launch_bounds__(kMoveThreads) move_kernel(const Params p, long long turns, int per_row) {
     griddep_wait();
     const EvictLaunch &a = p.a;
-    const int units = a.d / 4;
+    const int units = kUnits ? kUnits : a.d / 4, half = units / 2;
     for (long long turn = blockIdx.x; turn < turns; turn += gridDim.x) {
         const long long row = turn / per_row;
         const int first = int(turn - row * per_row) * kMoveRows;
         const int count = p.in_place ? p.head[2 * row] : min(p.head[2 * row + 1], a.keep);
-        const int items = min(kMoveRows, count - first) * units;
+        const int keys = min(kMoveRows, count - first);
         const int *src = p.src + row * p.slots + first, *to = p.holes + row * p.gaps + first;
-        for (int i0 = threadIdx.x; i0 < items; i0 += kMoveBatch * kMoveThreads) {
-            uint4 v[kMoveBatch];
+        if (int(threadIdx.x) < keys)
+            move_scalars(a, row, src[threadIdx.x], p.in_place ? to[threadIdx.x] : first + int(threadIdx.x));
+        if constexpr (kUnits > 0) {
+            constexpr int kStep = kMoveThreads / kUnits;
+            const int u = threadIdx.x % kUnits, m0 = threadIdx.x / kUnits;
+            const bool key = u < half;
+            const char *in = static_cast<const char *>(key ? a.kcache : a.vcache) +
+                             row * a.max_seqlen * (half * 16) + (key ? u : u - half) * 16;
+            char *out = static_cast<char *>(key ? a.kout : a.vout) + row * a.out_seqlen * (half * 16) +
+                        (key ? u : u - half) * 16;
 #pragma unroll
-            for (int k = 0; k < kMoveBatch; ++k) {
-                const int i = i0 + k * kMoveThreads;
-                if (i < items) v[k] = load_unit(a, row, src[i / units], i % units);
-            }
+            for (int m1 = 0; m1 < kMoveRows; m1 += kMoveBatch * kStep) {
+                uint4 v[kMoveBatch];
 #pragma unroll
-            for (int k = 0; k < kMoveBatch; ++k) {
-                const int i = i0 + k * kMoveThreads;
-                if (i < items) {
-                    const int m = i / units, u = i % units;
-                    const int dst = p.in_place ? to[m] : first + m;
-                    store_unit(a, row, dst, u, v[k]);
-                    if (u == 0) move_scalars(a, row, src[m], dst);
+                for (int k = 0; k < kMoveBatch; ++k) {
+                    const int m = m0 + m1 + k * kStep;
+                    if (m < keys) v[k] = __ldcs(reinterpret_cast<const uint4 *>(in + (long long)src[m] * (half * 16)));
                 }
+#pragma unroll
+                for (int k = 0; k < kMoveBatch; ++k) {
+                    const int m = m0 + m1 + k * kStep;
+                    if (m < keys)
+                        *reinterpret_cast<uint4 *>(out + (long long)(p.in_place ? to[m] : first + m) * (half * 16)) = v[k];
+                }
+            }
+        } else {
+            for (int i = threadIdx.x; i < keys * units; i += kMoveThreads) {
+                const int m = i / units, u = i % units;
+                store_unit(a, row, p.in_place ? to[m] : first + m, u, load_unit(a, row, src[m], u));
             }
         }
     }
@@ -288,17 +455,29 @@ Layout layout(const EvictLaunch &a) {
 
 template <bool kShared, bool kFused>
 cudaError_t launch_select(const Params &p, size_t smem, cudaStream_t stream) {
-    auto kernel = select_kernel<kShared, kFused>;
+    // Fused rows are those of a decode loop, many and short: several CTAs an SM.
+    constexpr int kThreads = kFused ? 512 : 1024;
+    auto kernel = select_kernel<kShared, kFused, kThreads>;
     static bool attr_set[kMaxDevices] = {};
     const int dev = slot_for_device();
     if (dev < 0 || !attr_set[dev]) {
         const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                                   kHistBytes + (kShared ? kMaxKeys * 4 : 0));
+                                                   kHistBytes + (kListKeys + (kShared ? kMaxKeys : 0)) * 4);
         if (e != cudaSuccess) return e;
         if (dev >= 0) attr_set[dev] = true;
     }
-    kernel<<<dim3(unsigned(p.a.B * p.a.Hkv)), dim3(kThreads), smem, stream>>>(p);
-    return cudaGetLastError();
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(unsigned(p.a.B) * unsigned(p.a.Hkv) * unsigned(p.cluster));
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = unsigned(p.cluster);
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = p.cluster > 1 ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, kernel, p);
 }
 
 }  // namespace evict
@@ -318,8 +497,15 @@ int evict_launch(const EvictLaunch &a, cudaStream_t stream) {
         p.src = reinterpret_cast<int *>(a.workspace + l.src);
         p.holes = reinterpret_cast<int *>(a.workspace + l.holes);
     }
-    const bool shared = a.max_seqlen <= kMaxKeys;
-    const size_t smem = kHistBytes + (shared ? (size_t)a.max_seqlen * 4 : 0);
+    // CTAs a row: while every row's cluster still has its SMs to itself and a
+    // CTA 2048 keys or more (below that the exchanges cost what the split saves).
+    const long long rows = (long long)a.B * a.Hkv;
+    p.cluster = 1;
+    if (!l.fused)
+        while (p.cluster < 8 && rows * p.cluster * 2 <= a.num_sms && a.max_seqlen / (p.cluster * 2) >= 2048) p.cluster *= 2;
+    const int keys = ((a.max_seqlen + p.cluster - 1) / p.cluster + 31) / 32 * 32;
+    const bool shared = keys <= kMaxKeys;
+    const size_t smem = kHistBytes + (kListKeys + (shared ? (size_t)keys : 0)) * 4;
     cudaError_t e = l.fused ? (shared ? launch_select<true, true>(p, smem, stream)
                                       : launch_select<false, true>(p, smem, stream))
                             : (shared ? launch_select<true, false>(p, smem, stream)
@@ -327,9 +513,13 @@ int evict_launch(const EvictLaunch &a, cudaStream_t stream) {
     if (e != cudaSuccess) return note_cuda_error(e, "select_kernel launch");
     if (l.fused || l.slots == 0) return 0;
     const int per_row = (l.slots + kMoveRows - 1) / kMoveRows;
-    const long long turns = (long long)a.B * a.Hkv * per_row;
-    const long long grid = turns < 8LL * a.num_sms ? turns : 8LL * a.num_sms;
-    e = dec::launch_programmatic(move_kernel, dim3(unsigned(grid)), dim3(kMoveThreads), 0, stream, p, turns, per_row);
+    const long long turns = rows * per_row;
+    // In place the number of moves is known on the device only, and most turns
+    // may be empty: a fixed grid walks them.  Out of place every turn is work.
+    const long long most = p.in_place ? 8LL * a.num_sms : 0x7fffffffLL;
+    const long long grid = turns < most ? turns : most;
+    auto move = a.d == 128 ? move_kernel<32> : (a.d == 64 ? move_kernel<16> : move_kernel<0>);
+    e = dec::launch_programmatic(move, dim3(unsigned(grid)), dim3(kMoveThreads), 0, stream, p, turns, per_row);
     return e == cudaSuccess ? 0 : note_cuda_error(e, "move_kernel launch");
 }
 

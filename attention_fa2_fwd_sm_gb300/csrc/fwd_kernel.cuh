@@ -85,6 +85,10 @@ constexpr int kCtrlRegs = 120;  // the warp-wide MMA issue loop spills at 104
 constexpr int kSoftmaxRegs = 192;
 static_assert(128 * kCtrlRegs + 256 * kSoftmaxRegs <= kThreads * kLaunchRegs, "register split");
 constexpr int kTmemCols = 512;
+// Shared memory of the prefix mapping's epilogue, behind everything else: 32
+// rows of 16 columns (20 words apart) for each softmax warp.
+constexpr int kTurnStride = 20, kTurnFloats = 32 * kTurnStride;
+constexpr int kTurnBytes = 8 * kTurnFloats * 4 + 16;
 
 template <int D>
 struct Cfg {
@@ -189,7 +193,7 @@ template <int kMap>
 __device__ __forceinline__ MappedWork<kMap> unit_work(const typename ParamsOf<kMap>::type &p, long long u) {
     if constexpr (kMap == kMapPrefix) {
         MappedWork<kMap> w;
-        const PrefixSegment seg = prefix_segment(p.po, blockIdx.x, u);
+        const PrefixSegment seg = prefix_segment(p.po, blockIdx.x, int(u));
         w.b = 0;
         w.kvh = seg.g;
         w.h = seg.g * p.G;
@@ -742,25 +746,50 @@ __global__ void __launch_bounds__(kThreads, 1)
             ++o_waits;
             tc_fence_after();
             if constexpr (kMap == kMapPrefix) {
-                const float inv_l = l_run > 0.f ? 1.f / l_run : 0.f;
-                const int be = w.row0[t] + r / p.G;  // batch entry of this row
-                const bool row_ok = r < p.po.rb * p.G && be < p.B;
-                const size_t prow = row_ok ? ((size_t)w.s * p.B + be) * p.Hq + w.h + r % p.G : 0;
-                float *orow = p.part_o + prow * D;
+                const float inv_l = l_run == 0.f ? 0.f : 1.f / l_run;  // NaN stays NaN
+                // A thread holds a row; stores straight from there would put 16
+                // bytes into each of 32 lines (10,000 clocks for the 128 KB of a
+                // unit).  The warp turns 32 rows x 16 columns at a time through
+                // its own 2.5 KB of shared memory (rows 20 words apart: no bank
+                // conflicts on the way in), so that four lanes write 64
+                // consecutive bytes.
+                const int first = quarter * 32 + (lane >> 2);  // this lane's rows to store: first + 8 k
+                const size_t slot0 = (size_t)w.s * p.B;
+                auto prow_of = [&](int rr) {  // the partial of tile row rr, or -1
+                    const int be = w.row0[t] + rr / p.G;
+                    return rr < p.po.rb * p.G && be < p.B ? (long long)((slot0 + be) * p.Hq + w.h + rr % p.G) : -1;
+                };
+                long long to[4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) to[k] = prow_of(first + 8 * k);
+                float *turn = reinterpret_cast<float *>(smem + (C::kSmemBytes - 1024 + 15) / 16 * 16) + (warp - 4) * kTurnFloats;
 #pragma unroll
                 for (int c = 0; c < D / 32; ++c) {
                     uint32_t ov[32];
                     tmem_ld32(tO + c * 32, ov);
                     tmem_wait_ld();
-                    if (row_ok) {
 #pragma unroll
-                        for (int g = 0; g < 8; ++g)
-                            *reinterpret_cast<float4 *>(orow + c * 32 + g * 4) = make_float4(
-                                __uint_as_float(ov[4 * g]) * inv_l, __uint_as_float(ov[4 * g + 1]) * inv_l,
-                                __uint_as_float(ov[4 * g + 2]) * inv_l, __uint_as_float(ov[4 * g + 3]) * inv_l);
+                    for (int half = 0; half < 2; ++half) {
+                        __syncwarp();
+#pragma unroll
+                        for (int g = 0; g < 4; ++g) {
+                            const int i = half * 16 + g * 4;
+                            *reinterpret_cast<float4 *>(turn + lane * kTurnStride + g * 4) = make_float4(
+                                __uint_as_float(ov[i]) * inv_l, __uint_as_float(ov[i + 1]) * inv_l,
+                                __uint_as_float(ov[i + 2]) * inv_l, __uint_as_float(ov[i + 3]) * inv_l);
+                        }
+                        __syncwarp();
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            const float4 v = *reinterpret_cast<const float4 *>(
+                                turn + (8 * k + (lane >> 2)) * kTurnStride + (lane & 3) * 4);
+                            if (to[k] >= 0)
+                                *reinterpret_cast<float4 *>(p.part_o + to[k] * D + c * 32 + half * 16 + (lane & 3) * 4) = v;
+                        }
                     }
                 }
-                if (row_ok) p.part_lse[prow] = l_run > 0.f ? m_run + __log2f(l_run) : -INFINITY;
+                const long long mine = prow_of(r);
+                if (mine >= 0) p.part_lse[mine] = l_run == 0.f ? -INFINITY : m_run + __log2f(l_run);
             } else if constexpr (kMap == kMapSplit) {
                 const float inv_l = l_run > 0.f ? 1.f / l_run : 0.f;
                 const bool row_ok = row < p.N;

@@ -35,7 +35,7 @@ struct PrefixOrder {
     int lockstep;
     int per;       // key blocks of a CTA's share
     int grid, slots;
-    long long total;  // key blocks over all rows of the order
+    unsigned total;  // key blocks over all rows of the order; below 2^31, as every product below
 };
 
 // One piece of work: key blocks [j0, j0 + n) of unit m of KV head g.
@@ -46,29 +46,29 @@ struct PrefixSegment {
 ATTN_HD int prefix_row(const PrefixOrder &o, int g, int m) { return o.lockstep ? g : g * o.mt + m; }
 
 // Shares that touch row `row` of the order: the first one and their number.
-ATTN_HD int prefix_first(const PrefixOrder &o, int row) { return int((long long)row * o.nblk / o.per); }
+ATTN_HD int prefix_first(const PrefixOrder &o, int row) { return int(unsigned(row) * unsigned(o.nblk) / unsigned(o.per)); }
 ATTN_HD int prefix_parts(const PrefixOrder &o, int row) {
-    return int((((long long)row + 1) * o.nblk - 1) / o.per) - prefix_first(o, row) + 1;
+    return int((unsigned(row + 1) * unsigned(o.nblk) - 1) / unsigned(o.per)) - prefix_first(o, row) + 1;
 }
 
 // First key block of CTA `cta`'s i-th segment in the order's linear space, or -1.
-ATTN_HD long long prefix_start(const PrefixOrder &o, int cta, int i) {
-    const long long lo = (long long)(o.lockstep ? cta / o.mt : cta) * o.per;
-    const long long hi = lo + o.per < o.total ? lo + o.per : o.total;
-    const long long u = i == 0 ? lo : (lo / o.nblk + i) * o.nblk;
-    return u < hi ? u : -1;
+ATTN_HD int prefix_start(const PrefixOrder &o, int cta, int i) {
+    const unsigned lo = unsigned(o.lockstep ? cta / o.mt : cta) * unsigned(o.per);
+    const unsigned hi = lo + o.per < o.total ? lo + o.per : o.total;
+    const unsigned u = i == 0 ? lo : (lo / unsigned(o.nblk) + i) * unsigned(o.nblk);
+    return u < hi ? int(u) : -1;
 }
 
-ATTN_HD PrefixSegment prefix_segment(const PrefixOrder &o, int cta, long long u) {
+ATTN_HD PrefixSegment prefix_segment(const PrefixOrder &o, int cta, int u) {
     const int share = o.lockstep ? cta / o.mt : cta;
-    const int row = int(u / o.nblk);
+    const int row = int(unsigned(u) / unsigned(o.nblk));
     PrefixSegment s;
     s.m = o.lockstep ? cta % o.mt : row % o.mt;
     s.g = o.lockstep ? row : row / o.mt;
-    s.j0 = int(u - (long long)row * o.nblk);
-    const long long end = (long long)(share + 1) * o.per;
-    const long long left = (end < o.total ? end : o.total) - u;
-    s.n = left < o.nblk - s.j0 ? int(left) : o.nblk - s.j0;
+    s.j0 = u - row * o.nblk;
+    const unsigned end = unsigned(share + 1) * unsigned(o.per);
+    const int left = int((end < o.total ? end : o.total) - unsigned(u));
+    s.n = left < o.nblk - s.j0 ? left : o.nblk - s.j0;
     s.slot = share - prefix_first(o, row);
     return s;
 }
@@ -82,10 +82,11 @@ inline bool prefix_order(PrefixOrder *o, int B, int G, int Hkv, int P, int num_s
     const int groups = num_sms / o->mt;
     o->lockstep = 10LL * groups * o->mt >= 9LL * num_sms;
     const int shares = o->lockstep ? groups : num_sms;
-    o->total = (long long)Hkv * o->nblk * (o->lockstep ? 1 : o->mt);
-    if (o->total >= (1LL << 31)) return false;
-    o->per = int((o->total + shares - 1) / shares);
-    const int used = int((o->total + o->per - 1) / o->per);
+    const long long total = (long long)Hkv * o->nblk * (o->lockstep ? 1 : o->mt);
+    if (total >= (1LL << 30)) return false;
+    o->total = unsigned(total);
+    o->per = int((total + shares - 1) / shares);
+    const int used = int((total + o->per - 1) / o->per);
     o->grid = used * (o->lockstep ? o->mt : 1);
     o->slots = 0;
     for (int row = 0; row < Hkv * (o->lockstep ? 1 : o->mt); ++row) {

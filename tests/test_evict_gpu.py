@@ -136,6 +136,16 @@ def test_long_rows(attn, in_place, S, keep):
     check(attn, weights_of("few values", (2, 1, S)), [S - 1, keep + 5], keep, 0, in_place=in_place)
 
 
+@pytest.mark.parametrize("in_place", [True, False])
+@pytest.mark.parametrize("kind", ["plain", "few values", "equal", "odd"])
+@pytest.mark.parametrize("B,H,S,keep", [(1, 2, 20001, 7000), (3, 8, 9000, 8000), (5, 9, 5000, 33), (1, 1, 17000, 16990)])
+def test_rows_shared_by_several_ctas(attn, B, H, S, keep, kind, in_place):
+    """Few long rows: a cluster of CTAs a row, one of whose ranges holds the last kept slot; lengths that leave
+    some of them without a key."""
+    lens = [S, keep + 1, S - 1, 40, (S + keep) // 2][:B]
+    check(attn, weights_of(kind, (B, H, S), 7), lens, keep, 12, in_place=in_place, slack=1)
+
+
 def test_captured_loop_with_appends(attn):
     """A captured decode step on a bounded cache (append, evict), replayed: the lengths go round in device memory, positions
     advance, and every replay equals the eager step."""
