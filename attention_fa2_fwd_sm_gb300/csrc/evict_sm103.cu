@@ -42,7 +42,7 @@ namespace evict {
 
 constexpr int kHistBytes = 256 * 32 * 4;
 constexpr int kListKeys = 4096;       // ranks that the second pass may gather
-constexpr int kMaxKeys = 44 * 1024;  // of one CTA: ranks that fit in shared memory; longer ranges are read again each pass
+constexpr int kMaxKeys = 43 * 1024;  // of one CTA: ranks that fit in shared memory; longer ranges are read again each pass
 constexpr int kFusedMoves = 64;
 constexpr int kFewMoves = 8;
 
@@ -132,7 +132,9 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const Params p) {
     uint32_t *ranks = list + kListKeys;  // [keys of this CTA], when they fit
     __shared__ int part[kWarps];
     __shared__ int counts[2][256];       // digit counts of this CTA (in turns: the others may still read the last)
-    __shared__ int totals[4];            // ties; holes and fillers; entries of the list
+    __shared__ int totals[4];            // this CTA's tallies
+    __shared__ int tally[4][32];         // of each warp: kept below and past `keep`, ties below and past
+    __shared__ int listed;               // entries of the list
     __shared__ uint32_t found[2];        // the digit, and how many are above it
     __shared__ unsigned long long least[kWarps];
     __shared__ int fused_holes[kFused ? kFusedMoves : 1], fused_src[kFused ? kFusedMoves : 1], fused_moves;
@@ -230,7 +232,7 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const Params p) {
         uint32_t value = 0;
         int want = a.keep;
         bool gathered = false;  // the list holds every rank that still qualifies
-        if (t == 0) totals[3] = 0;
+        if (t == 0) listed = 0;
         for (int shift = 24; shift >= 0; shift -= 8) {
             for (int i = t; i < 256 * 32; i += kThreads) hist[i] = 0;
             __syncthreads();
@@ -242,7 +244,7 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const Params p) {
                     count(x);
                 });
             } else if (gathered) {
-                visit<4>(t, totals[3], kThreads, [&](int i) { return list[i]; },
+                visit<4>(t, listed, kThreads, [&](int i) { return list[i]; },
                          [&](int, uint32_t x) { if ((x & mask) == value) count(x); });
             } else {
                 visit<8>(lo + t, hi, kThreads, rank, [&](int, uint32_t x) {
@@ -251,14 +253,14 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const Params p) {
                     if (shift == 16) {
                         const cg::coalesced_group some = cg::coalesced_threads();
                         int at = 0;
-                        if (some.thread_rank() == 0) at = atomicAdd(&totals[3], int(some.size()));
+                        if (some.thread_rank() == 0) at = atomicAdd(&listed, int(some.size()));
                         at = some.shfl(at, 0) + int(some.thread_rank());
                         if (at < kListKeys) list[at] = x;
                     }
                 });
             }
             __syncthreads();
-            if (shift == 16) gathered = totals[3] <= kListKeys;
+            if (shift == 16) gathered = listed <= kListKeys;
             // Column sums of this CTA, then over the cluster: warp w owns kDigits digits from 255 - kDigits w down.
             constexpr int kDigits = 256 / kWarps;
             int *mine = counts[shift >> 3 & 1];
@@ -273,10 +275,15 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const Params p) {
             int c = 0;
             if (lane < kDigits) {
                 const int digit = 255 - kDigits * warp - lane;
-                if (peers > 1)
-                    for (int q = 0; q < peers; ++q) c += cluster.map_shared_rank(mine, q)[digit];
-                else
+                if (peers > 1) {
+                    int theirs[8];
+#pragma unroll
+                    for (int q = 0; q < 8; ++q) theirs[q] = q < peers ? cluster.map_shared_rank(mine, q)[digit] : 0;
+#pragma unroll
+                    for (int q = 0; q < 8; ++q) c += theirs[q];
+                } else {
                     c = mine[digit];
+                }
             }
             int total, upto = c;
 #pragma unroll
@@ -318,29 +325,63 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const Params p) {
             tie[0] += __popc(__ballot_sync(0xffffffffu, in && x == value && !past));
             tie[1] += __popc(__ballot_sync(0xffffffffu, in && x == value && past));
         });
-        // Ties ahead of this warp's, then the holes and fillers ahead: within
-        // the CTA, and over the lower CTAs of the cluster.
-        auto offset = [&](int v, int slot, int &total) {
-            int at = warp_offsets<kWarps>(v, part, total);
-            if (peers > 1) {
-                if (t == 0) totals[slot] = total;
-                cluster.sync();
-                total = 0;
-                for (int q = 0; q < peers; ++q) {
-                    const int x = cluster.map_shared_rank(totals, q)[slot];
-                    at += q < peer ? x : 0;
-                    total += x;
-                }
+        // Where this warp's ties, holes and fillers start.  Slots go up with the
+        // warp and with the CTA, and within either the ties below `keep` come
+        // before those past it, so four counts of every warp and of every CTA
+        // say all of it: one exchange.
+        if (lane == 0) {
+            tally[0][warp] = up[0], tally[1][warp] = up[1];
+            tally[2][warp] = tie[0], tally[3][warp] = tie[1];
+        }
+        __syncthreads();
+        int mine[4];  // lane w: the counts of warp w
+#pragma unroll
+        for (int k = 0; k < 4; ++k) mine[k] = lane < kWarps ? tally[k][lane] : 0;
+        auto scan = [&](int v) {  // sum over the lanes up to this one
+#pragma unroll
+            for (int off = 1; off < 32; off <<= 1) {
+                const int y = __shfl_up_sync(0xffffffffu, v, off);
+                if (lane >= off) v += y;
             }
-            return at;
+            return v;
         };
-        int total;
-        int ties = offset(tie[0] + tie[1], 0, total);
-        const int left = max(want - ties, 0);  // ties that this warp may keep
-        const int mine_below = max(min(i1, a.keep) - i0, 0);
-        const int kept0 = up[0] + min(tie[0], left), kept1 = up[1] + min(tie[1], max(left - tie[0], 0));
-        int hole = offset(mine_below - kept0, 1, moves);
-        int fill = offset(kept1, 2, total);
+        int ties = 0, hole = 0, fill = 0;  // ahead of this CTA, then of this warp
+        if (peers > 1) {
+            if (warp == 0)
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const int sum = __reduce_add_sync(0xffffffffu, mine[k]);
+                    if (lane == 0) totals[k] = sum;
+                }
+            cluster.sync();
+            int theirs[8][4];
+#pragma unroll
+            for (int q = 0; q < 8; ++q)
+#pragma unroll
+                for (int k = 0; k < 4; ++k) theirs[q][k] = q < peers ? cluster.map_shared_rank(totals, q)[k] : 0;
+            int t0 = 0;  // ties ahead of CTA q
+#pragma unroll
+            for (int q = 0; q < 8; ++q) {
+                if (q >= peers) break;
+                if (q < peer) fill += theirs[q][1] + min(theirs[q][3], max(want - t0 - theirs[q][2], 0));
+                if (q == peer) ties = t0, hole = moves;
+                const int left = max(want - t0, 0), start = min(q * chunk, n);
+                moves += max(min(min(start + chunk, n), a.keep) - start, 0) - theirs[q][0] - min(theirs[q][2], left);
+                t0 += theirs[q][2] + theirs[q][3];
+            }
+        }
+        {
+            const int upto = scan(mine[2] + mine[3]);
+            const int left = max(want - ties - (upto - mine[2] - mine[3]), 0);
+            const int s0 = min(lo + lane * range, hi);
+            const int gaps = lane < kWarps ? max(min(min(s0 + range, hi), a.keep) - s0, 0) - mine[0] - min(mine[2], left) : 0;
+            const int fills = mine[1] + min(mine[3], max(left - mine[2], 0));
+            const int gaps_upto = scan(gaps), fills_upto = scan(fills);
+            if (peers == 1) moves = __shfl_sync(0xffffffffu, gaps_upto, 31);
+            ties += __shfl_sync(0xffffffffu, upto - mine[2] - mine[3], warp);
+            hole += __shfl_sync(0xffffffffu, gaps_upto - gaps, warp);
+            fill += __shfl_sync(0xffffffffu, fills_upto - fills, warp);
+        }
         sweep([&](int s, uint32_t x, bool in) {
             const uint32_t same = __ballot_sync(0xffffffffu, in && x == value);
             const bool keep = in && (x > value || (x == value && ties + __popc(same & below) < want));
