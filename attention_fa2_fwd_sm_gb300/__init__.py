@@ -418,20 +418,16 @@ def _refuse(what, name, t, dtype, shape):
                                   f"contiguous rows (got {t.dtype} {tuple(t.shape)} on {t.device}, strides {t.stride()})")
 
 
-def _gpu_of(what, t):
-    gpu = t.get_device()
+def _elsewhere(what, gpu, stream):
+    """The context that makes `stream` (or GPU `gpu`'s current one) the current
+    stream.  The helpers below call themselves inside it unless it is current
+    already, so the outputs and workspaces that they allocate belong to the
+    stream that writes them."""
+    import torch
     if gpu < 0:
         raise AttnError(ATTN_ERR_ARG, f"{what}: the tensors have to be on a GPU")
-    return gpu
-
-
-def _elsewhere(what, gpu, stream):
-    """None when a call on GPU `gpu` and `stream` is one on the current device
-    and stream; else the context that makes it one.  Outputs and workspaces
-    that the helpers allocate then belong to the stream that writes them."""
-    import torch
     if stream is None:
-        return None if gpu == torch.cuda.current_device() else torch.cuda.device(gpu)
+        return torch.cuda.device(gpu)
     if isinstance(stream, int):
         stream = torch.cuda.ExternalStream(stream, device=gpu) if stream else torch.cuda.default_stream(gpu)
     if stream.device.index != gpu:
@@ -439,14 +435,11 @@ def _elsewhere(what, gpu, stream):
     return torch.cuda.stream(stream)
 
 
-def _workspace(what, workspace, nbytes, like, gpu):
-    """A workspace of nbytes: the caller's, or a new one."""
-    import torch
-    if workspace is None:
-        return torch.empty(max(nbytes, 16), dtype=torch.uint8, device=like.device), nbytes
+def _held(what, workspace, gpu):
+    """Bytes of the caller's workspace."""
     if workspace.get_device() != gpu or not workspace.is_contiguous():
         raise AttnError(ATTN_ERR_WORKSPACE, f"{what}: the workspace has to be contiguous and on the tensors' GPU")
-    return workspace, workspace.numel() * workspace.element_size()
+    return workspace.nbytes
 
 
 def rope_freqs(rotary_dim, base=10000.0, rule="plain", factor=1.0, low=1.0, high=4.0, trained_len=8192.0,
@@ -466,10 +459,9 @@ def rope(q, k, inv_freq, positions=None, interleaved=False, out_scale=1.0, out=N
     tensors as attn_fwd takes them, or `out`, which may be ``(q, k)``."""
     import torch
     what, bf16 = "rope", torch.bfloat16
-    gpu = _gpu_of(what, q)
-    there = _elsewhere(what, gpu, stream)
-    if there is not None:
-        with there:
+    gpu = q.get_device()
+    if stream is not None or gpu < 0 or gpu != torch._C._cuda_getDevice():
+        with _elsewhere(what, gpu, stream):
             return rope(q, k, inv_freq, positions, interleaved, out_scale, out, inverse)
     if q.dim() != 4 or (k is not None and k.dim() != 4):
         raise AttnError(ATTN_ERR_ARG, "rope: q and k have to be [B, H, N, d]")
@@ -500,9 +492,13 @@ def rope(q, k, inv_freq, positions=None, interleaved=False, out_scale=1.0, out=N
         else:
             _fits_rows(k_out, bf16, shape, gpu) or _refuse(what, "k_out", k_out, bf16, shape)
         ks, kos = k.stride(), k_out.stride()
-    rc = attn_rope(q, q_out, k, k_out, positions, per_entry, inv_freq, B, Hq, Hkv, N, d, 2 * pairs, interleaved,
-                   out_scale, inverse, _Strides(*q.stride()[:3], *q_out.stride()[:3], *ks[:3], *kos[:3]))
-    check(rc, "attn_rope")
+    rc = lib().attn_rope(q.data_ptr(), q_out.data_ptr(), None if k is None else k.data_ptr(),
+                         None if k is None else k_out.data_ptr(), None if positions is None else positions.data_ptr(),
+                         per_entry, inv_freq.data_ptr(), B, Hq, Hkv, N, d, 2 * pairs, interleaved, out_scale, inverse,
+                         _Strides(*q.stride()[:3], *q_out.stride()[:3], *ks[:3], *kos[:3]),
+                         torch._C._cuda_getCurrentRawStream(gpu))
+    if rc:
+        check(rc, "attn_rope")
     return q_out, k_out
 
 
@@ -521,10 +517,9 @@ def rope_append(q, k, v, kcache, vcache, seqlens, inv_freq=None, start_pos=None,
     seqlens_out)``."""
     import torch
     what, bf16, i32 = "rope_append", torch.bfloat16, torch.int32
-    gpu = _gpu_of(what, q)
-    there = _elsewhere(what, gpu, stream)
-    if there is not None:
-        with there:
+    gpu = q.get_device()
+    if stream is not None or gpu < 0 or gpu != torch._C._cuda_getDevice():
+        with _elsewhere(what, gpu, stream):
             return rope_append(q, k, v, kcache, vcache, seqlens, inv_freq, start_pos, new_lens, interleaved, out_scale,
                                cache_pos, weights, q_out, seqlens_out)
     if q.dim() != 4 or kcache.dim() != 4:
@@ -556,10 +551,17 @@ def rope_append(q, k, v, kcache, vcache, seqlens, inv_freq=None, start_pos=None,
         seqlens_out = torch.empty_like(seqlens)
     else:
         _fits(seqlens_out, i32, (B,), gpu) or _refuse(what, "seqlens_out", seqlens_out, i32, (B,))
-    rc = attn_rope_append(q, q_out, k, v, kcache, vcache, seqlens, start_pos, new_lens, seqlens_out, cache_pos, weights,
-                          inv_freq, B, Hq, Hkv, T, d, rotary_dim, interleaved, out_scale, s_max,
-                          _Strides(*q.stride()[:3], *q_out.stride()[:3], *k.stride()[:3], *v.stride()[:3]))
-    check(rc, "attn_rope_append")
+    rc = lib().attn_rope_append(q.data_ptr(), q_out.data_ptr(), k.data_ptr(), v.data_ptr(), kcache.data_ptr(),
+                                vcache.data_ptr(), seqlens.data_ptr(), None if start_pos is None else start_pos.data_ptr(),
+                                None if new_lens is None else new_lens.data_ptr(), seqlens_out.data_ptr(),
+                                None if cache_pos is None else cache_pos.data_ptr(),
+                                None if weights is None else weights.data_ptr(),
+                                None if inv_freq is None else inv_freq.data_ptr(), B, Hq, Hkv, T, d, rotary_dim,
+                                interleaved, out_scale, s_max,
+                                _Strides(*q.stride()[:3], *q_out.stride()[:3], *k.stride()[:3], *v.stride()[:3]),
+                                torch._C._cuda_getCurrentRawStream(gpu))
+    if rc:
+        check(rc, "attn_rope_append")
     return q_out, seqlens_out
 
 
@@ -573,10 +575,9 @@ def decode_prefix(q, kprefix, vprefix, kcache, vcache, seqlens, scale=None, weig
     how large one has to be); returns ``(o, lse, workspace)``."""
     import torch
     what, bf16 = "decode_prefix", torch.bfloat16
-    gpu = _gpu_of(what, q)
-    there = _elsewhere(what, gpu, stream)
-    if there is not None:
-        with there:
+    gpu = q.get_device()
+    if stream is not None or gpu < 0 or gpu != torch._C._cuda_getDevice():
+        with _elsewhere(what, gpu, stream):
             return decode_prefix(q, kprefix, vprefix, kcache, vcache, seqlens, scale, weights, workspace, with_lse)
     if q.dim() != 3 or (kcache is not None and kcache.dim() != 4) or (kprefix is not None and kprefix.dim() != 3):
         raise AttnError(ATTN_ERR_ARG, "decode_prefix: q has to be [B, Hq, d], the prefix [Hkv, P, d], the caches "
@@ -598,13 +599,21 @@ def decode_prefix(q, kprefix, vprefix, kcache, vcache, seqlens, scale=None, weig
     if weights is not None:
         shape = (B, Hkv, s_max)
         _fits(weights, torch.float32, shape, gpu) or _refuse(what, "weights", weights, torch.float32, shape)
-    nbytes = attn_decode_prefix_workspace_bytes(B, Hq, Hkv, P, d, s_max, weights is not None)
-    workspace, nbytes = _workspace(what, workspace, nbytes, q, gpu)
+    if workspace is None:
+        nbytes = attn_decode_prefix_workspace_bytes(B, Hq, Hkv, P, d, s_max, weights is not None)
+        workspace = torch.empty(max(nbytes, 16), dtype=torch.uint8, device=q.device)
+    else:
+        nbytes = _held(what, workspace, gpu)
     o = torch.empty_like(q)
     lse = torch.empty((B, Hq), dtype=torch.float32, device=q.device) if with_lse else None
-    rc = attn_decode_prefix(q, kprefix, vprefix, kcache, vcache, seqlens, o, lse, weights, B, Hq, Hkv, P, d,
-                            d ** -0.5 if scale is None else scale, s_max, workspace, nbytes)
-    check(rc, "attn_decode_prefix")
+    prefix = (None, None) if kprefix is None else (kprefix.data_ptr(), vprefix.data_ptr())
+    own = (None, None, None) if kcache is None else (kcache.data_ptr(), vcache.data_ptr(), seqlens.data_ptr())
+    rc = lib().attn_decode_prefix(q.data_ptr(), *prefix, *own, o.data_ptr(), lse.data_ptr() if with_lse else None,
+                                  None if weights is None else weights.data_ptr(), B, Hq, Hkv, P, d,
+                                  d ** -0.5 if scale is None else scale, s_max, workspace.data_ptr(), nbytes,
+                                  torch._C._cuda_getCurrentRawStream(gpu))
+    if rc:
+        check(rc, "attn_decode_prefix")
     return o, lse, workspace
 
 
@@ -625,10 +634,9 @@ def cache_evict(kcache, vcache, weights, seqlens, keep, recent=0, cache_pos=None
     ``(seqlens_out, workspace)`` (`workspace` is None where none is needed)."""
     import torch
     what, bf16, i32, f32 = "cache_evict", torch.bfloat16, torch.int32, torch.float32
-    gpu = _gpu_of(what, kcache)
-    there = _elsewhere(what, gpu, stream)
-    if there is not None:
-        with there:
+    gpu = kcache.get_device()
+    if stream is not None or gpu < 0 or gpu != torch._C._cuda_getDevice():
+        with _elsewhere(what, gpu, stream):
             return cache_evict(kcache, vcache, weights, seqlens, keep, recent, cache_pos, cur_pos, out, seqlens_out,
                                workspace)
     if kcache.dim() != 4:
@@ -658,12 +666,21 @@ def cache_evict(kcache, vcache, weights, seqlens, keep, recent=0, cache_pos=None
         seqlens_out = torch.empty_like(seqlens)
     else:
         _fits(seqlens_out, i32, (B,), gpu) or _refuse(what, "seqlens_out", seqlens_out, i32, (B,))
-    nbytes = attn_cache_evict_workspace_bytes(B, Hkv, s_max, keep, kout.data_ptr() == kcache.data_ptr())
-    if nbytes or workspace is not None:
-        workspace, nbytes = _workspace(what, workspace, nbytes, kcache, gpu)
-    rc = attn_cache_evict(kcache, vcache, weights, cache_pos, seqlens, cur_pos, kout, vout, wout, pout, seqlens_out, B,
-                          Hkv, d, s_max, s_out, keep, recent, workspace, nbytes)
-    check(rc, "attn_cache_evict")
+    if workspace is not None:
+        nbytes = _held(what, workspace, gpu)
+    else:
+        nbytes = attn_cache_evict_workspace_bytes(B, Hkv, s_max, keep, kout.data_ptr() == kcache.data_ptr())
+        if nbytes:
+            workspace = torch.empty(nbytes, dtype=torch.uint8, device=kcache.device)
+    rc = lib().attn_cache_evict(kcache.data_ptr(), vcache.data_ptr(), weights.data_ptr(),
+                                None if cache_pos is None else cache_pos.data_ptr(), seqlens.data_ptr(),
+                                None if cur_pos is None else cur_pos.data_ptr(), kout.data_ptr(), vout.data_ptr(),
+                                None if wout is None else wout.data_ptr(), None if pout is None else pout.data_ptr(),
+                                seqlens_out.data_ptr(), B, Hkv, d, s_max, s_out, keep, recent,
+                                None if workspace is None else workspace.data_ptr(), nbytes,
+                                torch._C._cuda_getCurrentRawStream(gpu))
+    if rc:
+        check(rc, "attn_cache_evict")
     return seqlens_out, workspace
 
 
