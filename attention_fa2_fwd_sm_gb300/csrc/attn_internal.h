@@ -168,10 +168,10 @@ int decode_launch(const DecodeLaunch &a, cudaStream_t stream);
 
 // Decode over a shared prefix and the sequences' own keys
 // (decode_prefix_sm103.cu).  Byte offsets of the workspace's parts: the own
-// keys' work list, their partials and the prefix's, and the scores.
+// keys' plan, their partials and the prefix's, the scores and the rows' L.
 struct PrefixLayout {
-    size_t plan, own_o, own_lse, pre_o, pre_lse, scores, bytes;
-    int own_items;  // capacity of the work list
+    size_t plan, own_o, own_lse, pre_o, pre_lse, scores, row_lse, bytes;
+    int own_ctas;
 };
 struct DecodePrefixLaunch {
     const void *q, *kprefix, *vprefix, *kcache, *vcache;

@@ -6,18 +6,18 @@
 //     s_j = scale <q, k_j>,  L = log sum_j exp(s_j),  o = sum_j exp(s_j - L) v_j,
 //     weights[b, g, j] += sum over the group's heads of exp(s_j - L)  (own keys).
 // Softmax partials over disjoint sets of keys merge exactly: (o_i, L_i) give
-// L = log sum_i exp(L_i) and o = sum_i exp(L_i - L) o_i.  So three kernels:
+// L = log sum_i exp(L_i) and o = sum_i exp(L_i - L) o_i.  So three kernels, or four:
 //
 //   1. Prefix: fwd_kernel<D, kMapPrefix> (fwd_kernel.cuh).  For one KV head the
 //      B * G query rows are a matrix, and S = Q K^T and P V are matrix products
 //      whose keys are read once for the whole batch: tcgen05, 128 rows a tile
 //      whatever B * G is, since even a tile of one row outruns HBM.  Shares of
 //      key blocks as in prefix_order.cuh.
-//   2. Own keys: decode_kernel<D, S, true> (decode_kernel.cuh), HBM-bound; with
-//      weights it also writes the scores (4 G bytes a key beside 4 d read).
-//      Launched programmatically, it fills SMs as the prefix's CTAs leave.
-//   3. Finish: merges the partials of every row and, with weights, turns the
-//      scores into weights now that L is known.
+//   2. Own keys: own_kernel<D> (own_keys.cuh), HBM-bound; with weights it also
+//      writes the scores (4 G bytes a key beside 4 d read).  Launched
+//      programmatically, it fills SMs as the prefix's CTAs leave.
+//   3. Merge: the partials of every row.
+//   4. With weights: the scores become weights now that L is known.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -25,52 +25,66 @@
 
 #include "../../include/attn.h"
 #include "attn_internal.h"
-#include "decode_kernel.cuh"
+#include "decode_tile.cuh"
 #include "fwd_kernel.cuh"
+#include "own_keys.cuh"
 #include "prefix_order.cuh"
 
 namespace attn {
 
 namespace {
 
-// Own keys: about 5/3 CTAs an SM in all and no chunk below kOwnMinChunk keys, as
-// the ragged decode's plan.
-constexpr int kOwnMinChunk = 512;
-long long own_target(int sms) { return (5LL * sms) / 3 > 0 ? (5LL * sms) / 3 : 1; }
+constexpr int kMergeThreads = 128, kWeightThreads = 256;
+constexpr int kWeightCtasPerSm = 8;
+constexpr int kMinWeightKeys = 256;  // of one CTA
 
-constexpr int kFinishThreads = 128;
-constexpr int kWeightKeys = 1024;  // keys of one finishing CTA
-
-struct FinishParams {
-    const int *plan;  // null: no own keys
-    const float *own_o, *own_lse, *pre_o, *pre_lse, *scores;
+struct MergeParams {
+    const long long *plan;  // own_keys.cuh; null: no own keys
+    const int *seqlens;
+    const float *own_o, *own_lse, *pre_o, *pre_lse;
     __nv_bfloat16 *o;
-    float *lse, *weights;
-    int B, Hq, Hkv, G, P, max_seqlen, subs;
+    float *lse, *row_lse;  // natural log, and log2 units for the weights; either may be null
+    int B, Hq, Hkv, G, P, max_seqlen;
     PrefixOrder po;
 };
 
-// The partials of row (b, h): those of the prefix, then those of b's own items.
+struct WeightParams {
+    const long long *plan;
+    const int *seqlens;
+    const float *scores, *row_lse;
+    float *weights;
+    int B, Hkv, G, max_seqlen;
+};
+
+// The partials of row (b, h): those of the prefix, then those of b's own keys.
 struct RowParts {
     const float *pre, *own;  // log-sum-exps, log2 units
-    size_t pre_stride, own_stride;
-    int n_pre, n;
+    size_t own_first;        // number of the first own partial
+    int pre_stride, own_stride, n_pre, n;
     __device__ __forceinline__ float lse(int i) const {
-        return i < n_pre ? pre[i * pre_stride] : own[(i - n_pre) * own_stride];
+        return i < n_pre ? pre[(size_t)i * pre_stride] : own[(size_t)(i - n_pre) * own_stride];
     }
 };
 
-__device__ __forceinline__ RowParts row_parts(const FinishParams &p, int b, int h) {
+__device__ __forceinline__ RowParts row_parts(const MergeParams &p, int b, int h) {
     RowParts r;
     r.n_pre = r.n = 0;
-    r.pre_stride = (size_t)p.B * p.Hq;
-    r.own_stride = p.Hq;
+    r.pre_stride = p.B * p.Hq;
+    r.own_stride = p.G;
+    r.own_first = 0;
     r.pre = p.pre_lse + (size_t)b * p.Hq + h;
-    r.own = p.own_lse + h;
-    if (p.P > 0) r.n = r.n_pre = prefix_parts(p.po, prefix_row(p.po, h / p.G, b / p.po.rb / 2));
+    r.own = p.own_lse;
+    const int g = h / p.G;
+    if (p.P > 0) r.n = r.n_pre = prefix_parts(p.po, prefix_row(p.po, g, b / p.po.rb / 2));
     if (p.plan) {
-        r.own += (size_t)p.plan[2 + b] * p.Hq;
-        r.n += p.plan[2 + p.B + b];
+        const int len = own::length_of(p.seqlens, p.max_seqlen, b);
+        const long long S = p.plan[0], off = p.plan[2 + b] + (long long)g * len;
+        if (len > 0) {
+            const long long first = own::quotient(off, S);
+            r.own_first = size_t(first) + b * p.Hkv + g;
+            r.n += int(own::quotient(off + len - 1, S) - first) + 1;
+        }
+        r.own += r.own_first * p.G + (h - g * p.G);
     }
     return r;
 }
@@ -107,126 +121,154 @@ __device__ __forceinline__ Cols<kCols> load_cols(const float *p) {
     return c;
 }
 
-// Grid: first the rows (b, h), each by kWarps warps of a CTA; then, with
-// weights, a CTA for every 1024 keys of every own item of every KV head.
-// A row's chain is what bounds the merge: its counts, then its partials' L, then
+// A row (b, h) by kWarps warps of a CTA.  A row's chain is what bounds the merge: its counts, then its partials' L, then
 // their outputs.  The outputs do not depend on the L's, so the first eight of
 // each warp are loaded before L is known.  One warp a row when there are rows
 // enough to fill the GPU with; four take turns of eight partials when not.
 template <int D, int kWarps>
-__global__ void __launch_bounds__(kFinishThreads) finish_kernel(const FinishParams p) {
+__global__ void __launch_bounds__(kMergeThreads) merge_kernel(const MergeParams p) {
     constexpr int kCols = D / 32;  // columns of a lane
     constexpr int kAhead = 8;
-    __shared__ float acc_sh[kWarps > 1 ? kFinishThreads / 32 : 1][D];
-    __shared__ float lse_sh[dec::kMaxGroup];
+    __shared__ float acc_sh[kWarps > 1 ? kMergeThreads / 32 : 1][D];
     griddep_wait();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int rows = p.B * p.Hq;
-    constexpr int kRows = kFinishThreads / 32 / kWarps;
-    const int row_ctas = (rows + kRows - 1) / kRows;
-    if (int(blockIdx.x) < row_ctas) {
-        const int row = blockIdx.x * kRows + warp / kWarps, q = warp % kWarps;
-        if (row >= rows) return;  // with kWarps > 1 a CTA is one row
-        const int b = row / p.Hq, h = row - b * p.Hq;
-        const RowParts r = row_parts(p, b, h);
-        const size_t pre_step = (size_t)rows * D, own_step = (size_t)p.Hq * D;
-        const float *pre = p.pre_o + (size_t)row * D + lane * kCols;
-        const float *own = p.own_o + (p.plan ? ((size_t)p.plan[2 + b] * p.Hq + h) * D : 0) + lane * kCols;
-        auto part = [&](int i) { return i < r.n_pre ? pre + i * pre_step : own + (i - r.n_pre) * own_step; };
-        Cols<kCols> v[kAhead];
-        auto fetch = [&](int i0) {
+    constexpr int kRows = kMergeThreads / 32 / kWarps;
+    const int row = blockIdx.x * kRows + warp / kWarps, q = warp % kWarps;
+    if (row >= rows) return;  // with kWarps > 1 a CTA is one row
+    const int b = row / p.Hq, h = row - b * p.Hq;
+    const RowParts r = row_parts(p, b, h);
+    const size_t pre_step = (size_t)rows * D, own_step = (size_t)p.G * D;
+    const float *pre = p.pre_o + (size_t)row * D + lane * kCols;
+    const float *own = p.own_o + (r.own_first * p.G + h % p.G) * D + lane * kCols;
+    auto part = [&](int i) { return i < r.n_pre ? pre + i * pre_step : own + (i - r.n_pre) * own_step; };
+    Cols<kCols> v[kAhead];
+    auto fetch = [&](int i0) {
 #pragma unroll
-            for (int k = 0; k < kAhead; ++k)
-                if (i0 + k < r.n) v[k] = load_cols<kCols>(part(i0 + k));
-        };
-        fetch(q * kAhead);
-        float top, sum, w0;
-        warp_total(r, lane, top, sum, w0);
-        float acc[kCols] = {};
-        for (int i0 = q * kAhead; i0 < r.n; i0 += kAhead * kWarps) {
-            if (i0 > q * kAhead) fetch(i0);
+        for (int k = 0; k < kAhead; ++k)
+            if (i0 + k < r.n) v[k] = load_cols<kCols>(part(i0 + k));
+    };
+    fetch(q * kAhead);
+    float top, sum, w0;
+    warp_total(r, lane, top, sum, w0);
+    float acc[kCols] = {};
+    for (int i0 = q * kAhead; i0 < r.n; i0 += kAhead * kWarps) {
+        if (i0 > q * kAhead) fetch(i0);
 #pragma unroll
-            for (int k = 0; k < kAhead; ++k) {
-                const int i = i0 + k;
-                float w = __shfl_sync(0xffffffffu, w0, i & 31);
-                if (i < r.n) {
-                    if (i >= 32) w = fast_exp2(r.lse(i) - (top == -INFINITY ? 0.f : top));
-                    if (w != 0.f)  // an empty partial adds nothing
+        for (int k = 0; k < kAhead; ++k) {
+            const int i = i0 + k;
+            float w = __shfl_sync(0xffffffffu, w0, i & 31);
+            if (i < r.n) {
+                if (i >= 32) w = fast_exp2(r.lse(i) - (top == -INFINITY ? 0.f : top));
+                if (w != 0.f)  // an empty partial adds nothing
 #pragma unroll
-                        for (int c = 0; c < kCols; ++c) acc[c] += w * v[k].v[c];
-                }
+                    for (int c = 0; c < kCols; ++c) acc[c] += w * v[k].v[c];
             }
         }
-        if constexpr (kWarps > 1) {
-#pragma unroll
-            for (int c = 0; c < kCols; ++c) acc_sh[warp][lane * kCols + c] = acc[c];
-            __syncthreads();
-            if (warp > 0) return;
-#pragma unroll
-            for (int c = 0; c < kCols; ++c)
-                for (int w = 1; w < kWarps; ++w) acc[c] += acc_sh[w][lane * kCols + c];
-        }
-        const float inv = sum == 0.f ? 0.f : 1.f / sum;  // NaN stays NaN
-        uint32_t packed[kCols / 2];
-#pragma unroll
-        for (int c = 0; c < kCols / 2; ++c) packed[c] = pack_bf16x2(acc[2 * c] * inv, acc[2 * c + 1] * inv);
-        __nv_bfloat16 *o = p.o + (size_t)row * D + lane * kCols;
-        if constexpr (kCols == 4) *reinterpret_cast<uint2 *>(o) = make_uint2(packed[0], packed[1]);
-        else *reinterpret_cast<uint32_t *>(o) = packed[0];
-        if (lane == 0 && p.lse) p.lse[row] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * 0.69314718055994531f;
-        return;
     }
-    // ------------------------------------------------------------- weights
-    int i = int(blockIdx.x) - row_ctas;
-    const int sub = i % p.subs;
-    i /= p.subs;
-    const int g = i % p.Hkv, item = i / p.Hkv;
-    if (item >= p.plan[0]) return;
-    const int *it = p.plan + dec::plan_items_offset(p.B) + 3 * item;
-    const int b = it[0], lo = it[1] + sub * kWeightKeys, hi = min(it[2], lo + kWeightKeys);
-    if (lo >= hi) return;
-    for (int h = warp; h < p.G; h += kFinishThreads / 32) {
-        float top, sum, w0;
-        warp_total(row_parts(p, b, g * p.G + h), lane, top, sum, w0);
-        if (lane == 0) lse_sh[h] = top + log2f(sum);
+    if constexpr (kWarps > 1) {
+#pragma unroll
+        for (int c = 0; c < kCols; ++c) acc_sh[warp][lane * kCols + c] = acc[c];
+        __syncthreads();
+        if (warp > 0) return;
+#pragma unroll
+        for (int c = 0; c < kCols; ++c)
+            for (int w = 1; w < kWarps; ++w) acc[c] += acc_sh[w][lane * kCols + c];
     }
-    __syncthreads();
-    const size_t base = (size_t)(b * p.Hkv + g) * p.max_seqlen;
-    constexpr int kKeys = 4;  // keys of a thread in flight
-    for (int j0 = lo + threadIdx.x; j0 < hi; j0 += kKeys * kFinishThreads) {
-        float old[kKeys], w[kKeys] = {};
+    const float inv = sum == 0.f ? 0.f : 1.f / sum;  // NaN stays NaN
+    uint32_t packed[kCols / 2];
 #pragma unroll
-        for (int k = 0; k < kKeys; ++k) {
-            const int j = j0 + k * kFinishThreads;
-            if (j < hi) old[k] = p.weights[base + j];
-        }
-        if (p.G % 4 == 0) {
-            for (int h = 0; h < p.G; h += 4) {
-                float4 x[kKeys];
+    for (int c = 0; c < kCols / 2; ++c) packed[c] = pack_bf16x2(acc[2 * c] * inv, acc[2 * c + 1] * inv);
+    __nv_bfloat16 *o = p.o + (size_t)row * D + lane * kCols;
+    if constexpr (kCols == 4) *reinterpret_cast<uint2 *>(o) = make_uint2(packed[0], packed[1]);
+    else *reinterpret_cast<uint32_t *>(o) = packed[0];
+    if (lane == 0) {
+        const float L = sum == 0.f ? -INFINITY : top + log2f(sum);
+        if (p.lse) p.lse[row] = L * 0.69314718055994531f;
+        if (p.row_lse) p.row_lse[row] = L;
+    }
+}
+
+// The weights of n neighbouring keys of one KV head's row, G = 4 kQuads: a thread
+// takes one float4 of a key's G scores (a warp's loads are 512 consecutive bytes)
+// and kQuads neighbours add up.
+template <int kQuads>
+__device__ __forceinline__ void add_weights(const float *scores, const float *lse, float *weights, int n) {
+    constexpr int kBatch = 8, kStep = kWeightThreads / kQuads;
+    const int quad = threadIdx.x % kQuads, key0 = threadIdx.x / kQuads;
+    const float4 *src = reinterpret_cast<const float4 *>(scores) + quad;
+    const float L[4] = {lse[4 * quad], lse[4 * quad + 1], lse[4 * quad + 2], lse[4 * quad + 3]};
+    for (int j0 = 0; j0 < n; j0 += kBatch * kStep) {
+        float4 x[kBatch];
+        float old[kBatch];
 #pragma unroll
-                for (int k = 0; k < kKeys; ++k) {
-                    const int j = j0 + k * kFinishThreads;
-                    if (j < hi) x[k] = __ldcs(reinterpret_cast<const float4 *>(p.scores + (base + j) * p.G + h));
-                }
-#pragma unroll
-                for (int k = 0; k < kKeys; ++k)
-                    if (j0 + k * kFinishThreads < hi)
-                        w[k] += (fast_exp2(x[k].x - lse_sh[h]) + fast_exp2(x[k].y - lse_sh[h + 1])) +
-                                (fast_exp2(x[k].z - lse_sh[h + 2]) + fast_exp2(x[k].w - lse_sh[h + 3]));
+        for (int k = 0; k < kBatch; ++k) {
+            const int j = j0 + key0 + k * kStep;
+            if (j < n) {
+                x[k] = __ldcs(src + (size_t)j * kQuads);
+                if (quad == 0) old[k] = weights[j];
             }
-        } else {
-            for (int h = 0; h < p.G; ++h)
-#pragma unroll
-                for (int k = 0; k < kKeys; ++k) {
-                    const int j = j0 + k * kFinishThreads;
-                    if (j < hi) w[k] += fast_exp2(p.scores[(base + j) * p.G + h] - lse_sh[h]);
-                }
         }
 #pragma unroll
-        for (int k = 0; k < kKeys; ++k) {
-            const int j = j0 + k * kFinishThreads;
-            if (j < hi) p.weights[base + j] = old[k] + w[k];
+        for (int k = 0; k < kBatch; ++k) {
+            const int j = j0 + key0 + k * kStep;
+            float w = 0.f;
+            if (j < n)
+                w = (fast_exp2(x[k].x - L[0]) + fast_exp2(x[k].y - L[1])) +
+                    (fast_exp2(x[k].z - L[2]) + fast_exp2(x[k].w - L[3]));
+#pragma unroll
+            for (int off = 1; off < kQuads; off <<= 1) w += __shfl_xor_sync(0xffffffffu, w, off);
+            if (j < n && quad == 0) weights[j] = old[k] + w;
         }
+    }
+}
+
+// CTAs with equal shares of the own keys in the numbering of own_keys.cuh.
+// Bound by the scores' traffic (4 G bytes a key, most of it from L2).
+// kQuads: G / 4 where that is a power of two, else 0.
+template <int kQuads>
+__global__ void __launch_bounds__(kWeightThreads) weight_kernel(const WeightParams p) {
+    griddep_wait();
+    const int lane = threadIdx.x & 31;
+    const long long total = p.plan[1];
+    const long long share = max((long long)kMinWeightKeys, own::quotient(total + gridDim.x - 1, gridDim.x));
+    const long long lo = blockIdx.x * share;
+    if (lo >= total) return;
+    // The last sequence that starts at or before lo (of several, the one with keys).
+    int b = -1;
+    for (int first = 0; first < p.B; first += 256) {
+        int n = 0;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            const int i = first + 32 * k + lane;
+            n += __popc(__ballot_sync(0xffffffffu, i < p.B && p.plan[2 + i] <= lo));
+        }
+        b += n;
+        if (n < 256) break;
+    }
+    own::Place at;
+    const long long rem = lo - p.plan[2 + b];
+    at.b = b;
+    at.len = own::length_of(p.seqlens, p.max_seqlen, b);
+    at.g = int(own::quotient(rem, at.len));
+    at.j = int(rem - (long long)at.g * at.len);
+    at.left = min(share, total - lo);
+    while (true) {
+        const int n = at.keys(), row = at.b * p.Hkv + at.g;
+        const size_t key = (size_t)row * p.max_seqlen + at.j;
+        const float *scores = p.scores + key * p.G, *lse = p.row_lse + (size_t)row * p.G;
+        float *weights = p.weights + key;
+        if constexpr (kQuads > 0)
+            add_weights<kQuads>(scores, lse, weights, n);
+        else
+            for (int j = threadIdx.x; j < n; j += kWeightThreads) {
+                float w = 0.f;
+                for (int h = 0; h < p.G; ++h) w += fast_exp2(scores[(size_t)j * p.G + h] - lse[h]);
+                weights[j] += w;
+            }
+        at.left -= n;
+        if (at.left == 0) return;
+        at.next(p.seqlens, p.max_seqlen, p.Hkv);
     }
 }
 
@@ -274,18 +316,21 @@ int launch_prefix(const DecodePrefixLaunch &a, const PrefixOrder &po, float *par
 
 template <int D>
 int launch_own(const DecodePrefixLaunch &a, const PrefixLayout &l, bool behind_prefix, cudaStream_t stream) {
-    constexpr int S = dec::kBaseStages<D>;
-    using C = dec::Cfg<D, S>;
-    CUtensorMap mk, mv;
-    const uint64_t planes = uint64_t(a.B) * a.Hkv;
-    if (!encode_bf16_3d(&mk, a.kcache, D, uint64_t(a.max_seqlen), planes, 64, dec::kKeysPerStage) ||
-        !encode_bf16_3d(&mv, a.vcache, D, uint64_t(a.max_seqlen), planes, 64, dec::kKeysPerStage))
+    using C = own::Cfg<D>;
+    CUtensorMap mk, mv, mk16, mv16;
+    const uint64_t planes = uint64_t(a.B) * a.Hkv, keys = uint64_t(a.max_seqlen);
+    if (!encode_bf16_3d(&mk, a.kcache, D, keys, planes, 64, dec::kKeysPerStage) ||
+        !encode_bf16_3d(&mv, a.vcache, D, keys, planes, 64, dec::kKeysPerStage) ||
+        !encode_bf16_3d(&mk16, a.kcache, D, keys, planes, 64, 16) ||
+        !encode_bf16_3d(&mv16, a.vcache, D, keys, planes, 64, 16))
         return note_cuda_error(cudaErrorInvalidValue, "cuTensorMapEncodeTiled (own keys)");
-    dec::OwnParams p = {};
+    own::Params p = {};
     p.q = static_cast<const __nv_bfloat16 *>(a.q);
     p.seqlens = a.seqlens;
-    p.ws_o = reinterpret_cast<float *>(a.workspace + l.own_o);
-    p.ws_lse = reinterpret_cast<float *>(a.workspace + l.own_lse);
+    p.part_o = reinterpret_cast<float *>(a.workspace + l.own_o);
+    p.part_lse = reinterpret_cast<float *>(a.workspace + l.own_lse);
+    p.scores = a.weights ? reinterpret_cast<float *>(a.workspace + l.scores) : nullptr;
+    p.plan = reinterpret_cast<long long *>(a.workspace + l.plan);
     p.B = a.B;
     p.Hq = a.Hq;
     p.Hkv = a.Hkv;
@@ -293,85 +338,83 @@ int launch_own(const DecodePrefixLaunch &a, const PrefixLayout &l, bool behind_p
     p.max_seqlen = a.max_seqlen;
     p.scale_log2 = a.scale * 1.4426950408889634f;
     p.wait_ns = a.wait_ns;
-    p.plan_out = reinterpret_cast<int *>(a.workspace + l.plan);
-    p.scores = a.weights ? reinterpret_cast<float *>(a.workspace + l.scores) : nullptr;
-    p.target = own_target(a.num_sms);
-    p.min_chunk = kOwnMinChunk;
-    auto kernel = dec::decode_kernel<D, S, true>;
+    auto kernel = own::own_kernel<D>;
     static bool attr_set[kMaxDevices] = {};
     const int dev = slot_for_device();
     if (dev < 0 || !attr_set[dev]) {
         const cudaError_t e =
             cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes);
-        if (e != cudaSuccess) return note_cuda_error(e, "cudaFuncSetAttribute(decode_kernel, own keys)");
+        if (e != cudaSuccess) return note_cuda_error(e, "cudaFuncSetAttribute(own_kernel)");
         if (dev >= 0) attr_set[dev] = true;
     }
-    const dim3 grid(unsigned(a.Hkv), unsigned(l.own_items), 1);
+    const dim3 grid(unsigned(l.own_ctas)), block(dec::kThreads);
     cudaError_t e;
     if (behind_prefix) {
-        e = dec::launch_programmatic(kernel, grid, dim3(dec::kThreads), C::kSmemBytes, stream, mk, mv, p);
+        e = dec::launch_programmatic(kernel, grid, block, C::kSmemBytes, stream, mk, mv, mk16, mv16, p);
     } else {
-        kernel<<<grid, dim3(dec::kThreads), C::kSmemBytes, stream>>>(mk, mv, p);
+        kernel<<<grid, block, C::kSmemBytes, stream>>>(mk, mv, mk16, mv16, p);
         e = cudaGetLastError();
     }
-    return e == cudaSuccess ? 0 : note_cuda_error(e, "decode_kernel launch (own keys)");
-}
-
-// Longest chunk that own_item can choose for these sizes.
-long long own_max_chunk(int B, int Hkv, int max_seqlen, int sms) {
-    const long long t = own_target(sms);
-    long long c = ((long long)B * max_seqlen * Hkv + t - 1) / t;
-    c = (c + dec::kChunkGranule - 1) / dec::kChunkGranule * dec::kChunkGranule;
-    if (c < kOwnMinChunk) c = kOwnMinChunk;
-    return c < max_seqlen ? c : max_seqlen;
+    return e == cudaSuccess ? 0 : note_cuda_error(e, "own_kernel launch");
 }
 
 template <int D>
 int launch_all(const DecodePrefixLaunch &a, cudaStream_t stream) {
     PrefixLayout l;
-    FinishParams f = {};
+    MergeParams m = {};
     const int G = a.Hq / a.Hkv;
     if (!decode_prefix_layout(a.B, a.Hq, a.Hkv, a.P, a.d, a.max_seqlen, a.weights != nullptr, a.num_sms, &l))
         return ATTN_ERR_ARG;
     float *pre_o = reinterpret_cast<float *>(a.workspace + l.pre_o);
     float *pre_lse = reinterpret_cast<float *>(a.workspace + l.pre_lse);
-    // Four warps a row while a warp a row would leave SMs short of two CTAs.
-    const long long rows = (long long)a.B * a.Hq;
-    const bool wide = rows < 8LL * a.num_sms;
-    long long grid = wide ? rows : (rows + kFinishThreads / 32 - 1) / (kFinishThreads / 32);
-    if (a.weights) {
-        f.subs = int((own_max_chunk(a.B, a.Hkv, a.max_seqlen, a.num_sms) + kWeightKeys - 1) / kWeightKeys);
-        grid += (long long)l.own_items * a.Hkv * f.subs;
-    }
-    if (grid > 0x7fffffffLL) return ATTN_ERR_ARG;  // before anything is launched
     if (a.P > 0) {
-        prefix_order(&f.po, a.B, G, a.Hkv, a.P, a.num_sms);
-        const int rc = launch_prefix<D>(a, f.po, pre_o, pre_lse, stream);
+        prefix_order(&m.po, a.B, G, a.Hkv, a.P, a.num_sms);
+        const int rc = launch_prefix<D>(a, m.po, pre_o, pre_lse, stream);
         if (rc) return rc;
     }
     if (a.max_seqlen > 0) {
         const int rc = launch_own<D>(a, l, a.P > 0, stream);
         if (rc) return rc;
-        f.plan = reinterpret_cast<const int *>(a.workspace + l.plan);
+        m.plan = reinterpret_cast<const long long *>(a.workspace + l.plan);
+        m.seqlens = a.seqlens;
     }
-    f.own_o = reinterpret_cast<const float *>(a.workspace + l.own_o);
-    f.own_lse = reinterpret_cast<const float *>(a.workspace + l.own_lse);
-    f.pre_o = pre_o;
-    f.pre_lse = pre_lse;
-    f.scores = reinterpret_cast<const float *>(a.workspace + l.scores);
-    f.o = static_cast<__nv_bfloat16 *>(a.o);
-    f.lse = a.lse;
-    f.weights = a.weights;
-    f.B = a.B;
-    f.Hq = a.Hq;
-    f.Hkv = a.Hkv;
-    f.G = G;
-    f.P = a.P;
-    f.max_seqlen = a.max_seqlen;
-    auto finish = wide ? finish_kernel<D, kFinishThreads / 32> : finish_kernel<D, 1>;
-    const cudaError_t e = dec::launch_programmatic(finish, dim3(unsigned(grid)), dim3(kFinishThreads), 0,
-                                                   stream, f);
-    return e == cudaSuccess ? 0 : note_cuda_error(e, "finish_kernel launch");
+    m.own_o = reinterpret_cast<const float *>(a.workspace + l.own_o);
+    m.own_lse = reinterpret_cast<const float *>(a.workspace + l.own_lse);
+    m.pre_o = pre_o;
+    m.pre_lse = pre_lse;
+    m.o = static_cast<__nv_bfloat16 *>(a.o);
+    m.lse = a.lse;
+    m.row_lse = a.weights ? reinterpret_cast<float *>(a.workspace + l.row_lse) : nullptr;
+    m.B = a.B;
+    m.Hq = a.Hq;
+    m.Hkv = a.Hkv;
+    m.G = G;
+    m.P = a.P;
+    m.max_seqlen = a.max_seqlen;
+    // Four warps a row while a warp a row would leave SMs short of two CTAs.
+    constexpr int kWarps = kMergeThreads / 32;
+    const long long rows = (long long)a.B * a.Hq;
+    const bool wide = rows < 2LL * kWarps * a.num_sms;
+    auto merge = wide ? merge_kernel<D, kWarps> : merge_kernel<D, 1>;
+    cudaError_t e = dec::launch_programmatic(merge, dim3(unsigned(wide ? rows : (rows + kWarps - 1) / kWarps)),
+                                             dim3(kMergeThreads), 0, stream, m);
+    if (e != cudaSuccess) return note_cuda_error(e, "merge_kernel launch");
+    if (!a.weights) return 0;
+    WeightParams w = {};
+    w.plan = m.plan;
+    w.seqlens = a.seqlens;
+    w.scores = reinterpret_cast<const float *>(a.workspace + l.scores);
+    w.row_lse = m.row_lse;
+    w.weights = a.weights;
+    w.B = a.B;
+    w.Hkv = a.Hkv;
+    w.G = G;
+    w.max_seqlen = a.max_seqlen;
+    const long long most = ((long long)a.B * a.Hkv * a.max_seqlen + kMinWeightKeys - 1) / kMinWeightKeys;
+    const long long ctas = most < kWeightCtasPerSm * a.num_sms ? most : kWeightCtasPerSm * a.num_sms;
+    auto weigh = G == 4 ? weight_kernel<1> : G == 8 ? weight_kernel<2> : G == 16 ? weight_kernel<4> : weight_kernel<0>;
+    e = dec::launch_programmatic(weigh, dim3(unsigned(ctas)), dim3(kWeightThreads), 0, stream, w);
+    return e == cudaSuccess ? 0 : note_cuda_error(e, "weight_kernel launch");
 }
 
 }  // namespace
@@ -382,21 +425,23 @@ bool decode_prefix_layout(int B, int Hq, int Hkv, int P, int d, int max_seqlen, 
     const size_t rows = (size_t)B * Hq;
     PrefixOrder po = {};
     if (P > 0 && !prefix_order(&po, B, Hq / Hkv, Hkv, P, num_sms)) return false;
-    const long long items = max_seqlen > 0 ? (own_target(num_sms) + Hkv - 1) / Hkv + B : 0;
-    if (items > 65535) return false;  // grid.y of the own keys' launch
-    l->own_items = int(items);
+    const long long keys = (long long)B * Hkv * max_seqlen, most = (keys + own::kMinShare - 1) / own::kMinShare;
+    const long long ctas = most < own::kCtasPerSm * num_sms ? most : own::kCtasPerSm * num_sms;
+    const size_t parts = max_seqlen > 0 ? (size_t)ctas + (size_t)B * Hkv : 0;
+    l->own_ctas = int(ctas);
     size_t at = 0;
     auto take = [&](size_t n) {
         const size_t here = at;
         at += up(n);
         return here;
     };
-    l->plan = take(items ? (size_t)(2 + 2LL * B + 3 * items) * sizeof(int) : 0);
-    l->own_o = take((size_t)items * Hq * d * sizeof(float));
-    l->own_lse = take((size_t)items * Hq * sizeof(float));
+    l->plan = take(max_seqlen > 0 ? (size_t)(2 + B) * sizeof(long long) : 0);
+    l->own_o = take(parts * (Hq / Hkv) * d * sizeof(float));
+    l->own_lse = take(parts * (Hq / Hkv) * sizeof(float));
     l->pre_o = take((size_t)po.slots * rows * d * sizeof(float));
     l->pre_lse = take((size_t)po.slots * rows * sizeof(float));
     l->scores = take(weights ? rows * max_seqlen * sizeof(float) : 0);
+    l->row_lse = take(weights ? rows * sizeof(float) : 0);
     l->bytes = at;
     return true;
 }
@@ -406,12 +451,12 @@ int decode_prefix_launch(const DecodePrefixLaunch &a, cudaStream_t stream) {
 }
 
 cudaError_t decode_prefix_take_status(int *bits) {
-    int zero = 0, fwd_bits = 0, dec_bits = 0;
+    int zero = 0, fwd_bits = 0, own_bits = 0;
     cudaError_t e = cudaMemcpyFromSymbol(&fwd_bits, g_fwd_status, sizeof(int));
-    if (e == cudaSuccess) e = cudaMemcpyFromSymbol(&dec_bits, g_decode_status, sizeof(int));
+    if (e == cudaSuccess) e = cudaMemcpyFromSymbol(&own_bits, g_own_status, sizeof(int));
     if (e == cudaSuccess) e = cudaMemcpyToSymbol(g_fwd_status, &zero, sizeof(int));
-    if (e == cudaSuccess) e = cudaMemcpyToSymbol(g_decode_status, &zero, sizeof(int));
-    *bits = fwd_bits | dec_bits;
+    if (e == cudaSuccess) e = cudaMemcpyToSymbol(g_own_status, &zero, sizeof(int));
+    *bits = fwd_bits | own_bits;
     return e;
 }
 

@@ -34,7 +34,7 @@
 
 #include "../../include/attn.h"
 #include "attn_internal.h"
-#include "decode_kernel.cuh"
+#include "decode_tile.cuh"
 #include "sm103_ptx.cuh"
 
 namespace attn {

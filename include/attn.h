@@ -519,14 +519,13 @@ int attn_rope_append(const void *q, void *q_out, const void *k, const void *v, v
  *   weights    [B, Hkv, max_seqlen] fp32, read and written, or NULL.  Entries
  *              at or past seqlens[b] are left as they were.  No atomics:
  *              equal calls give equal bits.
- *   d in {64, 128}; 1 <= Hq / Hkv <= 16; P or max_seqlen > 0;
- *   ceil(5 SMs / 3 / Hkv) + B <= 65535.
+ *   d in {64, 128}; 1 <= Hq / Hkv <= 16; P or max_seqlen > 0.
  *   workspace  at least attn_decode_prefix_workspace_bytes(...) bytes, 16-byte
  *              aligned; with weights it also holds the scores, 4 * B * Hq *
  *              max_seqlen bytes.  Nothing in it outlives the call.
- * Up to three kernels run on `stream`, with no host synchronisation: the
- * prefix's partials, the own keys' partials (work list made on the device from
- * seqlens), and the merge with the weights.
+ * Up to four kernels run on `stream`, with no host synchronisation: the
+ * prefix's partials, the own keys' partials (shared out on the device by
+ * seqlens), the merge, and the weights.
  */
 int attn_decode_prefix(const void *q, const void *kprefix, const void *vprefix, const void *kcache,
                        const void *vcache, const int *seqlens, void *o, float *lse, float *weights, int B, int Hq,
