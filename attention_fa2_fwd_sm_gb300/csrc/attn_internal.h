@@ -170,7 +170,7 @@ int decode_launch(const DecodeLaunch &a, cudaStream_t stream);
 // (decode_prefix_sm103.cu).  Byte offsets of the workspace's parts: the own
 // keys' plan, their partials and the prefix's, the scores and the rows' L.
 struct PrefixLayout {
-    size_t plan, own_o, own_lse, pre_o, pre_lse, scores, row_lse, bytes;
+    size_t plan, own_rows, own_o, own_lse, pre_o, pre_lse, scores, row_lse, bytes;
     int own_ctas;
 };
 struct DecodePrefixLaunch {

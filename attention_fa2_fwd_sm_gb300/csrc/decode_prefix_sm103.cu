@@ -35,11 +35,12 @@ namespace attn {
 namespace {
 
 constexpr int kMergeThreads = 128, kWeightThreads = 256;
+constexpr int kWideWarps = 16;  // of one row, where there are few
 constexpr int kWeightCtasPerSm = 8;
 constexpr int kMinWeightKeys = 256;  // of one CTA
 
 struct MergeParams {
-    const long long *plan;  // own_keys.cuh; null: no own keys
+    const int2 *own_rows;  // own_keys.cuh; null: no own keys
     const int *seqlens;
     const float *own_o, *own_lse, *pre_o, *pre_lse;
     __nv_bfloat16 *o;
@@ -76,15 +77,13 @@ __device__ __forceinline__ RowParts row_parts(const MergeParams &p, int b, int h
     r.own = p.own_lse;
     const int g = h / p.G;
     if (p.P > 0) r.n = r.n_pre = prefix_parts(p.po, prefix_row(p.po, g, b / p.po.rb / 2));
-    if (p.plan) {
-        const int len = own::length_of(p.seqlens, p.max_seqlen, b);
-        const long long S = p.plan[0], off = p.plan[2 + b] + (long long)g * len;
-        if (len > 0) {
-            const long long first = own::quotient(off, S);
-            r.own_first = size_t(first) + b * p.Hkv + g;
-            r.n += int(own::quotient(off + len - 1, S) - first) + 1;
+    if (p.own_rows) {
+        const int2 own = p.own_rows[b * p.Hkv + g];  // not written for a sequence without keys
+        if (p.seqlens[b] > 0) {
+            r.own_first = own.x;
+            r.n += own.y;
+            r.own += r.own_first * p.G + (h - g * p.G);
         }
-        r.own += r.own_first * p.G + (h - g * p.G);
     }
     return r;
 }
@@ -126,14 +125,14 @@ __device__ __forceinline__ Cols<kCols> load_cols(const float *p) {
 // each warp are loaded before L is known.  One warp a row when there are rows
 // enough to fill the GPU with; four take turns of eight partials when not.
 template <int D, int kWarps>
-__global__ void __launch_bounds__(kMergeThreads) merge_kernel(const MergeParams p) {
+__global__ void __launch_bounds__(kWarps > 1 ? kWarps * 32 : kMergeThreads) merge_kernel(const MergeParams p) {
     constexpr int kCols = D / 32;  // columns of a lane
     constexpr int kAhead = 8;
-    __shared__ float acc_sh[kWarps > 1 ? kMergeThreads / 32 : 1][D];
+    __shared__ float acc_sh[kWarps][D];
     griddep_wait();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int rows = p.B * p.Hq;
-    constexpr int kRows = kMergeThreads / 32 / kWarps;
+    constexpr int kRows = kWarps > 1 ? 1 : kMergeThreads / 32;
     const int row = blockIdx.x * kRows + warp / kWarps, q = warp % kWarps;
     if (row >= rows) return;  // with kWarps > 1 a CTA is one row
     const int b = row / p.Hq, h = row - b * p.Hq;
@@ -171,9 +170,10 @@ __global__ void __launch_bounds__(kMergeThreads) merge_kernel(const MergeParams 
         for (int c = 0; c < kCols; ++c) acc_sh[warp][lane * kCols + c] = acc[c];
         __syncthreads();
         if (warp > 0) return;
+        const int used = min(kWarps, (r.n + kAhead - 1) / kAhead);  // warps that had a partial
+        for (int w = 1; w < used; ++w)
 #pragma unroll
-        for (int c = 0; c < kCols; ++c)
-            for (int w = 1; w < kWarps; ++w) acc[c] += acc_sh[w][lane * kCols + c];
+            for (int c = 0; c < kCols; ++c) acc[c] += acc_sh[w][lane * kCols + c];
     }
     const float inv = sum == 0.f ? 0.f : 1.f / sum;  // NaN stays NaN
     uint32_t packed[kCols / 2];
@@ -331,11 +331,13 @@ int launch_own(const DecodePrefixLaunch &a, const PrefixLayout &l, bool behind_p
     p.part_lse = reinterpret_cast<float *>(a.workspace + l.own_lse);
     p.scores = a.weights ? reinterpret_cast<float *>(a.workspace + l.scores) : nullptr;
     p.plan = reinterpret_cast<long long *>(a.workspace + l.plan);
+    p.rows = reinterpret_cast<int2 *>(a.workspace + l.own_rows);
     p.B = a.B;
     p.Hq = a.Hq;
     p.Hkv = a.Hkv;
     p.G = a.Hq / a.Hkv;
     p.max_seqlen = a.max_seqlen;
+    p.narrow = planes * keys < (1ull << 29);
     p.scale_log2 = a.scale * 1.4426950408889634f;
     p.wait_ns = a.wait_ns;
     auto kernel = own::own_kernel<D>;
@@ -375,7 +377,7 @@ int launch_all(const DecodePrefixLaunch &a, cudaStream_t stream) {
     if (a.max_seqlen > 0) {
         const int rc = launch_own<D>(a, l, a.P > 0, stream);
         if (rc) return rc;
-        m.plan = reinterpret_cast<const long long *>(a.workspace + l.plan);
+        m.own_rows = reinterpret_cast<const int2 *>(a.workspace + l.own_rows);
         m.seqlens = a.seqlens;
     }
     m.own_o = reinterpret_cast<const float *>(a.workspace + l.own_o);
@@ -391,17 +393,18 @@ int launch_all(const DecodePrefixLaunch &a, cudaStream_t stream) {
     m.G = G;
     m.P = a.P;
     m.max_seqlen = a.max_seqlen;
-    // Four warps a row while a warp a row would leave SMs short of two CTAs.
-    constexpr int kWarps = kMergeThreads / 32;
+    // A warp a row where the rows fill the SMs; few rows get more warps, and the
+    // fewest, whose partials can be many, sixteen.
     const long long rows = (long long)a.B * a.Hq;
-    const bool wide = rows < 2LL * kWarps * a.num_sms;
-    auto merge = wide ? merge_kernel<D, kWarps> : merge_kernel<D, 1>;
-    cudaError_t e = dec::launch_programmatic(merge, dim3(unsigned(wide ? rows : (rows + kWarps - 1) / kWarps)),
-                                             dim3(kMergeThreads), 0, stream, m);
+    const int warps = rows >= 8LL * a.num_sms ? 1 : (rows >= a.num_sms ? 4 : kWideWarps);
+    auto merge = warps == 1 ? merge_kernel<D, 1> : (warps == 4 ? merge_kernel<D, 4> : merge_kernel<D, kWideWarps>);
+    const int per_cta = warps == 1 ? kMergeThreads / 32 : 1;
+    cudaError_t e = dec::launch_programmatic(merge, dim3(unsigned((rows + per_cta - 1) / per_cta)),
+                                             dim3(warps == 1 ? kMergeThreads : warps * 32), 0, stream, m);
     if (e != cudaSuccess) return note_cuda_error(e, "merge_kernel launch");
     if (!a.weights) return 0;
     WeightParams w = {};
-    w.plan = m.plan;
+    w.plan = reinterpret_cast<const long long *>(a.workspace + l.plan);
     w.seqlens = a.seqlens;
     w.scores = reinterpret_cast<const float *>(a.workspace + l.scores);
     w.row_lse = m.row_lse;
@@ -436,6 +439,7 @@ bool decode_prefix_layout(int B, int Hq, int Hkv, int P, int d, int max_seqlen, 
         return here;
     };
     l->plan = take(max_seqlen > 0 ? (size_t)(2 + B) * sizeof(long long) : 0);
+    l->own_rows = take(max_seqlen > 0 ? (size_t)B * Hkv * sizeof(int2) : 0);
     l->own_o = take(parts * (Hq / Hkv) * d * sizeof(float));
     l->own_lse = take(parts * (Hq / Hkv) * sizeof(float));
     l->pre_o = take((size_t)po.slots * rows * d * sizeof(float));

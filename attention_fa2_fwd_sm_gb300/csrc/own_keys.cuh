@@ -39,7 +39,7 @@ namespace own {
 
 using namespace dec;
 
-constexpr int kMinShare = 128;  // keys: two stages
+constexpr int kMinShare = 64;  // keys: one stage
 constexpr int kCtasPerSm = 2;
 
 template <int D>
@@ -64,7 +64,9 @@ struct Params {
     float *part_o, *part_lse;  // [partial][G][D], [partial][G] (log2 units)
     float *scores;             // [B, Hkv, max_seqlen, G] log2 units, or null
     long long *plan;           // {S, T Hkv, first key of each sequence in the numbering}
+    int2 *rows;                // [B * Hkv] first partial and number of partials (rows with keys only)
     int B, Hq, Hkv, G, max_seqlen;
+    int narrow;  // fewer than 2^29 keys in the caches
     float scale_log2;
     unsigned long long wait_ns;
 };
@@ -94,7 +96,9 @@ __device__ __forceinline__ long long quotient(long long a, long long b) {
 }
 
 // Where CTA `cta` of `ctas` starts (left = 0: it has no share).  All lanes of
-// the calling warp; `write`: also write the plan down.
+// the calling warp; `write`: also write the plan down.  Int: wide enough for the
+// number of keys, so that the common case scans and divides in 32 bits.
+template <typename Int>
 __device__ __forceinline__ Place find_share(const Params &p, int cta, int ctas, bool write) {
     constexpr int kRound = 8;  // groups of 32 sequences whose lengths are loaded together
     const int lane = threadIdx.x & 31;
@@ -106,7 +110,7 @@ __device__ __forceinline__ Place find_share(const Params &p, int cta, int ctas, 
             len[k] = i < p.B ? length_of(p.seqlens, p.max_seqlen, i) : 0;
         }
     };
-    long long T = 0;
+    Int T = 0;
     for (int first = 0; first < p.B; first += 32 * kRound) {
         load(first);
 #pragma unroll
@@ -114,39 +118,39 @@ __device__ __forceinline__ Place find_share(const Params &p, int cta, int ctas, 
     }
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) T += __shfl_xor_sync(0xffffffffu, T, off);
-    T *= p.Hkv;
-    long long S = (quotient(T + ctas - 1, ctas) + kKeysPerStage - 1) / kKeysPerStage * kKeysPerStage;
+    T *= Int(p.Hkv);
+    Int S = ((T + Int(ctas) - 1) / Int(ctas) + kKeysPerStage - 1) / kKeysPerStage * kKeysPerStage;
     if (S < kMinShare) S = kMinShare;
-    const long long lo = cta * S;
+    const Int lo = Int(cta) * S;
     if (write && lane == 0) {
-        p.plan[0] = S;
-        p.plan[1] = T;
+        p.plan[0] = (long long)S;
+        p.plan[1] = (long long)T;
     }
-    Place at = {0, 0, 0, 0, lo < T ? min(S, T - lo) : 0};
-    long long before = 0;  // keys of the sequences before, over all KV heads
+    Place at = {0, 0, 0, 0, lo < T ? (long long)min(S, T - lo) : 0};
+    Int before = 0;  // keys of the sequences before, over all KV heads
     bool searching = at.left > 0;
     for (int first = 0; first < p.B && (write || searching); first += 32 * kRound) {
         if (p.B > 32 * kRound) load(first);
 #pragma unroll
         for (int k = 0; k < kRound; ++k) {
             if (first + 32 * k >= p.B) break;
-            const long long n = (long long)len[k] * p.Hkv;
-            long long upto = n;
+            const Int n = Int(len[k]) * Int(p.Hkv);
+            Int upto = n;
 #pragma unroll
             for (int off = 1; off < 32; off <<= 1) {
-                const long long y = __shfl_up_sync(0xffffffffu, upto, off);
+                const Int y = __shfl_up_sync(0xffffffffu, upto, off);
                 if (lane >= off) upto += y;
             }
-            const long long base = before + upto - n;
-            if (write && first + 32 * k + lane < p.B) p.plan[2 + first + 32 * k + lane] = base;
+            const Int base = before + upto - n;
+            if (write && first + 32 * k + lane < p.B) p.plan[2 + first + 32 * k + lane] = (long long)base;
             const uint32_t hit = __ballot_sync(0xffffffffu, searching && lo >= base && lo < base + n);
             if (hit) {
                 const int src = __ffs(hit) - 1;
-                const long long rem = lo - __shfl_sync(0xffffffffu, base, src);
+                const Int rem = lo - __shfl_sync(0xffffffffu, base, src);
                 at.b = first + 32 * k + src;
                 at.len = __shfl_sync(0xffffffffu, len[k], src);
-                at.g = int(quotient(rem, at.len));
-                at.j = int(rem - (long long)at.g * at.len);
+                at.g = int(rem / Int(at.len));
+                at.j = int(rem - Int(at.g) * Int(at.len));
                 searching = false;
             }
             before += __shfl_sync(0xffffffffu, upto, 31);
@@ -160,7 +164,7 @@ __device__ __forceinline__ void consumer_sync() {
 }
 
 template <int D>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, kCtasPerSm)
     own_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                const __grid_constant__ CUtensorMap tmK16, const __grid_constant__ CUtensorMap tmV16, const Params p) {
     using C = Cfg<D>;
@@ -189,13 +193,18 @@ __global__ void __launch_bounds__(kThreads)
         tma_prefetch_desc(&tmK);
         tma_prefetch_desc(&tmV);
     }
-    Place at = find_share(p, blockIdx.x, gridDim.x, blockIdx.x == 0 && warp == 0);
+    const bool write = blockIdx.x == 0 && warp == 0;
+    // (CTAs + 1) shares stay below 2^31 where the caches' keys stay below 2^29: a share is at most twice its equal part or kMinShare.
+    Place at = p.narrow ? find_share<unsigned>(p, blockIdx.x, gridDim.x, write)
+                        : find_share<long long>(p, blockIdx.x, gridDim.x, write);
     __syncthreads();
     if (at.left == 0) {
         griddep_wait();
         return;
     }
 
+    // Share, where a row can go on behind it (a longer one holds every row's rest; the last may be shorter).
+    const unsigned share = unsigned(min(at.left, 0x40000000LL));
     long long fills = 0;  // ring fills issued (producer) or used (consumers)
     if (warp == kConsumerWarps) {
         // ------------------------------------------------------------ producer
@@ -244,17 +253,22 @@ __global__ void __launch_bounds__(kThreads)
         const int gq = lane >> 2, tq = lane & 3;
         const float sl2 = p.scale_log2;
         bool ok = true;
-        while (true) {
-            const int n = at.keys(), row = at.b * p.Hkv + at.g;
-            // Q fragments (A operand, rows = query heads of the group, k = head dim).
-            uint32_t qa[D / 16][4];
+        // Q fragments (A operand, rows = query heads of the group, k = head dim).
+        uint32_t qa[D / 16][4];
+        auto load_q = [&](int row) {
+            const __nv_bfloat16 *q = p.q + ((size_t)row * p.G + gq) * D + tq * 2;
 #pragma unroll
             for (int ks = 0; ks < D / 16; ++ks)
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int h = gq + ((i & 1) ? 8 : 0), col = ks * 16 + tq * 2 + ((i & 2) ? 8 : 0);
-                    qa[ks][i] = h < p.G ? *reinterpret_cast<const uint32_t *>(p.q + ((size_t)row * p.G + h) * D + col) : 0u;
-                }
+                for (int i = 0; i < 4; ++i)
+                    qa[ks][i] = gq + ((i & 1) ? 8 : 0) < p.G
+                                    ? *reinterpret_cast<const uint32_t *>(q + ((i & 1) ? 8 * D : 0) + ks * 16 + ((i & 2) ? 8 : 0))
+                                    : 0u;
+        };
+        load_q(at.b * p.Hkv + at.g);
+        while (true) {
+            const int n = at.keys(), row = at.b * p.Hkv + at.g, len = at.len;
+            const bool first_of_row = at.j == 0;
             float m_st[2] = {-INFINITY, -INFINITY}, l_st[2] = {0.f, 0.f};
             float acc[D / 8][4];
 #pragma unroll
@@ -344,30 +358,42 @@ __global__ void __launch_bounds__(kThreads)
                 if (lane == 0) mbar_arrive(smem_u32(bars + C::kStages + s));
             }
 
+            // On to the next segment: its queries arrive while this one is finished.
+            at.left -= n;
+            if (at.left > 0) {
+                at.next(p.seqlens, p.max_seqlen, p.Hkv);
+                load_q(at.b * p.Hkv + at.g);
+            }
+
             // The four warps' states become the segment's partial, 32 columns at a time.
+            const bool high = p.G > 8;  // rows 8..15 are in use
 #pragma unroll
             for (int r = 0; r < 2; ++r) {
                 float l = l_st[r];
                 l += __shfl_xor_sync(0xffffffffu, l, 1);
                 l += __shfl_xor_sync(0xffffffffu, l, 2);
-                if (tq == 0) state[warp * kMaxGroup + gq + 8 * r] = make_float2(m_st[r], l);
+                if (tq == 0 && (r == 0 || high)) state[warp * kMaxGroup + gq + 8 * r] = make_float2(m_st[r], l);
             }
             consumer_sync();
-            float f[2];
+            float f[2] = {0.f, 0.f};
 #pragma unroll
             for (int r = 0; r < 2; ++r) {
                 float top = -INFINITY;
+                if (r == 1 && !high) break;
 #pragma unroll
                 for (int w = 0; w < kConsumerWarps; ++w) top = fmaxf(top, state[w * kMaxGroup + gq + 8 * r].x);
                 f[r] = fast_exp2(m_st[r] - (top == -INFINITY ? 0.f : top));
             }
             const size_t part = (size_t)blockIdx.x + row;
+            if (first_of_row && threadIdx.x == 0)
+                p.rows[row] = make_int2(int(part), 1 + int((unsigned(len - n) + share - 1) / share));
             // A thread stores column `col` of rows row0, row0 + 4, ...: their sums once, ahead of the columns.
             const int col = threadIdx.x & 31, row0 = threadIdx.x >> 5;
             float inv[kMaxGroup / 4];
 #pragma unroll
             for (int k = 0; k < kMaxGroup / 4; ++k) {
                 const int h = row0 + 4 * k;
+                if (h >= p.G) break;
                 float top = -INFINITY, sum = 0.f;
 #pragma unroll
                 for (int w = 0; w < kConsumerWarps; ++w) top = fmaxf(top, state[w * kMaxGroup + h].x);
@@ -378,7 +404,7 @@ __global__ void __launch_bounds__(kThreads)
                     sum += fast_exp2(st.x - ref) * st.y;
                 }
                 inv[k] = sum == 0.f ? 0.f : 1.f / sum;  // NaN stays NaN
-                if (ok && h < p.G && col == 0) p.part_lse[part * p.G + h] = sum == 0.f ? -INFINITY : top + __log2f(sum);
+                if (ok && col == 0) p.part_lse[part * p.G + h] = sum == 0.f ? -INFINITY : top + __log2f(sum);
             }
 #pragma unroll
             for (int c = 0; c < D / 32; ++c) {
@@ -387,22 +413,23 @@ __global__ void __launch_bounds__(kThreads)
                 for (int u = 0; u < 4; ++u) {
                     const float(&a)[4] = acc[4 * c + u];
                     *reinterpret_cast<float2 *>(mine + u * 8) = make_float2(a[0] * f[0], a[1] * f[0]);
-                    *reinterpret_cast<float2 *>(mine + 8 * C::kTurnStride + u * 8) = make_float2(a[2] * f[1], a[3] * f[1]);
+                    if (high)
+                        *reinterpret_cast<float2 *>(mine + 8 * C::kTurnStride + u * 8) =
+                            make_float2(a[2] * f[1], a[3] * f[1]);
                 }
                 consumer_sync();
 #pragma unroll
                 for (int k = 0; k < kMaxGroup / 4; ++k) {
                     const int h = row0 + 4 * k;
+                    if (h >= p.G) break;
                     float v = 0.f;
 #pragma unroll
                     for (int w = 0; w < kConsumerWarps; ++w) v += turn[(w * kMaxGroup + h) * C::kTurnStride + col];
-                    if (ok && h < p.G) p.part_o[(part * p.G + h) * D + c * 32 + col] = v * inv[k];
+                    if (ok) p.part_o[(part * p.G + h) * D + c * 32 + col] = v * inv[k];
                 }
                 consumer_sync();
             }
-            at.left -= n;
             if (at.left == 0) break;
-            at.next(p.seqlens, p.max_seqlen, p.Hkv);
         }
     }
     __syncthreads();

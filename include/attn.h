@@ -519,7 +519,7 @@ int attn_rope_append(const void *q, void *q_out, const void *k, const void *v, v
  *   weights    [B, Hkv, max_seqlen] fp32, read and written, or NULL.  Entries
  *              at or past seqlens[b] are left as they were.  No atomics:
  *              equal calls give equal bits.
- *   d in {64, 128}; 1 <= Hq / Hkv <= 16; P or max_seqlen > 0.
+ *   d in {64, 128}; 1 <= Hq / Hkv <= 16; P or max_seqlen > 0; max_seqlen <= 2^30.
  *   workspace  at least attn_decode_prefix_workspace_bytes(...) bytes, 16-byte
  *              aligned; with weights it also holds the scores, 4 * B * Hq *
  *              max_seqlen bytes.  Nothing in it outlives the call.
