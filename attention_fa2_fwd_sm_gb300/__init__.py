@@ -70,7 +70,7 @@ SIGNATURES = {
     "attn_rope_append": (_I, [_P] * 13 + [_I] * 7 + [_F, _I, _LLP, _P]),
     "attn_decode_prefix": (_I, [_P] * 9 + [_I] * 5 + [_F, _I, _P, _SZ, _P]),
     "attn_decode_prefix_workspace_bytes": (_SZ, [_I] * 7),
-    "attn_decode_prefix_segment": (_I, [_I] * 7 + [_IP]),
+    "attn_decode_prefix_segment": (_I, [_I] * 6 + [_LL] + [_I] * 3 + [_IP]),
     "attn_cache_evict": (_I, [_P] * 11 + [_I] * 7 + [_P, _SZ, _P]),
     "attn_cache_evict_workspace_bytes": (_SZ, [_I] * 5),
     "attn_tile_map": (_I, [_I, _I, _I, _I, _I, _I, _LL, _IP, _IP, _IP]),
@@ -369,11 +369,12 @@ def attn_decode_prefix_workspace_bytes(B, Hq, Hkv, P, d, max_seqlen, with_weight
     return lib().attn_decode_prefix_workspace_bytes(B, Hq, Hkv, P, d, max_seqlen, int(bool(with_weights)))
 
 
-def attn_decode_prefix_segment(B, Hq, Hkv, P, num_sms, cta, i):
-    """(KV head, unit, first key block, blocks, slot) of CTA `cta`'s i-th piece
-    of the prefix phase, or None when it has no i-th piece."""
-    out = (ctypes.c_int * 5)()
-    rc = lib().attn_decode_prefix_segment(B, Hq, Hkv, P, num_sms, cta, i, out)
+def attn_decode_prefix_segment(B, Hq, Hkv, P, d, max_seqlen, own_keys, num_sms, cta, i):
+    """(KV head, unit, first key block, blocks, partial, its rows' last partial)
+    of CTA `cta`'s i-th piece of the prefix phase, or None when it has no i-th
+    piece."""
+    out = (ctypes.c_int * 6)()
+    rc = lib().attn_decode_prefix_segment(B, Hq, Hkv, P, d, max_seqlen, own_keys, num_sms, cta, i, out)
     if rc < 0:
         check(rc, "attn_decode_prefix_segment")
     return tuple(out) if rc else None

@@ -17,7 +17,8 @@ CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libattn.so")
 SOURCES = ["attn_api.cu", "fwd_sm103.cu", "fwd_pair_sm103.cu", "fwd_splitkv_sm103.cu", "fwd_host.cu", "decode_sm103.cu", "die_map.cu", "bwd_sm103.cu",
-           "rope_sm103.cu", "decode_prefix_sm103.cu", "evict_sm103.cu"]
+           "rope_sm103.cu", "decode_prefix_sm103.cu", "own_keys_sm103.cu",
+           "evict_sm103.cu"]
 HEADERS = ["attn_internal.h", "fwd_kernel.cuh", "decode_tile.cuh", "own_keys.cuh", "prefix_order.cuh", "sm103_ptx.cuh", "tile_order.cuh", "dkdv_order.cuh"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-O2",

@@ -794,16 +794,23 @@ int attn_decode_prefix(const void *q, const void *kprefix, const void *vprefix, 
     return decode_prefix_launch(a, reinterpret_cast<cudaStream_t>(stream));
 }
 
-int attn_decode_prefix_segment(int B, int Hq, int Hkv, int P, int num_sms, int cta, int i, int *out) {
+int attn_decode_prefix_segment(int B, int Hq, int Hkv, int P, int d, int max_seqlen, long long own_keys, int num_sms,
+                               int cta, int i, int *out) {
     PrefixOrder o;
-    if (!out || P <= 0 || num_sms <= 0 || i < 0 || decode_prefix_sizes(B, Hq, Hkv, P, 128, 0) != ATTN_OK ||
-        !prefix_order(&o, B, Hq / Hkv, Hkv, P, num_sms) || cta < 0 || cta >= o.grid)
+    if (!out || P <= 0 || num_sms <= 0 || i < 0 || own_keys < 0 ||
+        decode_prefix_sizes(B, Hq, Hkv, P, d, max_seqlen) != ATTN_OK ||
+        !prefix_order(&o, B, Hq / Hkv, Hkv, P, d, own_ctas(B, Hkv, P, max_seqlen, num_sms), num_sms) || cta < 0 ||
+        cta >= prefix_grid(o))
         return ATTN_ERR_ARG;
-    const long long u = prefix_start(o, cta, i);
+    const PrefixShares s = prefix_shares(o, own_keys * Hkv);
+    const int share = prefix_share(o, cta);
+    const unsigned hi = prefix_begin(o, s, share + 1);
+    const int u = prefix_start(o, prefix_begin(o, s, share), hi, i);
     if (u < 0) return 0;
-    const PrefixSegment s = prefix_segment(o, cta, u);
-    const int v[5] = {s.g, s.m, s.j0, s.n, s.slot};
-    for (int k = 0; k < 5; ++k) out[k] = v[k];
+    const PrefixSegment seg = prefix_segment(o, hi, cta, u);
+    const int last = prefix_holder(o, s, unsigned(seg.row + 1) * o.nblk - 1);
+    const int v[6] = {seg.g, seg.m, seg.j0, seg.n, share + seg.row, last + seg.row};
+    for (int k = 0; k < 6; ++k) out[k] = v[k];
     return 1;
 }
 
@@ -890,12 +897,13 @@ int attn_cache_evict(const void *kcache, const void *vcache, const float *weight
 int attn_device_status(attn_stream_t stream) {
     if (cudaStreamSynchronize(reinterpret_cast<cudaStream_t>(stream)) != cudaSuccess)
         return ATTN_ERR_CUDA;
-    int a = 0, b = 0, c = 0, e = 0, f = 0, g = 0;
+    int a = 0, b = 0, c = 0, e = 0, f = 0, g = 0, h = 0;
     if (fwd_take_status(&a) != cudaSuccess || decode_take_status(&b) != cudaSuccess ||
         bwd_take_status(&c) != cudaSuccess || fwd_pair_take_status(&e) != cudaSuccess ||
-        fwd_split_take_status(&f) != cudaSuccess || decode_prefix_take_status(&g) != cudaSuccess)
+        fwd_split_take_status(&f) != cudaSuccess || decode_prefix_take_status(&g) != cudaSuccess ||
+        own_take_status(&h) != cudaSuccess)
         return ATTN_ERR_CUDA;
-    return (a | b | c | e | f | g) ? ATTN_ERR_TIMEOUT : ATTN_OK;
+    return (a | b | c | e | f | g | h) ? ATTN_ERR_TIMEOUT : ATTN_OK;
 }
 
 }  // extern "C"

@@ -170,7 +170,7 @@ int decode_launch(const DecodeLaunch &a, cudaStream_t stream);
 // (decode_prefix_sm103.cu).  Byte offsets of the workspace's parts: the own
 // keys' plan, their partials and the prefix's, the scores and the rows' L.
 struct PrefixLayout {
-    size_t plan, own_rows, own_o, own_lse, pre_o, pre_lse, scores, row_lse, bytes;
+    size_t plan, own_rows, own_o, own_lse, pre_rows, pre_o, pre_lse, scores, row_lse, bytes;
     int own_ctas;
 };
 struct DecodePrefixLaunch {
@@ -184,11 +184,15 @@ struct DecodePrefixLaunch {
     unsigned long long wait_ns;
     int num_sms;
 };
+// CTAs (one an SM) of the own keys' kernel: half of the SMs beside a prefix.
+int own_ctas(int B, int Hkv, int P, int max_seqlen, int num_sms);
 // False when the sizes are outside what the launches can count.
 bool decode_prefix_layout(int B, int Hq, int Hkv, int P, int d, int max_seqlen, bool weights, int num_sms,
                           PrefixLayout *l);
 int decode_prefix_launch(const DecodePrefixLaunch &a, cudaStream_t stream);
+int own_launch(const DecodePrefixLaunch &a, const PrefixLayout &l, cudaStream_t stream);  // its own keys' part
 cudaError_t decode_prefix_take_status(int *bits);
+cudaError_t own_take_status(int *bits);
 int bwd_launch(const BwdLaunch &a, cudaStream_t stream);
 
 // Size of the built-in scratch array used by attn_decode_noalloc.

@@ -14,8 +14,10 @@
 //      whatever B * G is, since even a tile of one row outruns HBM.  Shares of
 //      key blocks as in prefix_order.cuh.
 //   2. Own keys: own_kernel<D> (own_keys.cuh), HBM-bound; with weights it also
-//      writes the scores (4 G bytes a key beside 4 d read).  Launched
-//      programmatically, it fills SMs as the prefix's CTAs leave.
+//      writes the scores (4 G bytes a key beside 4 d read).
+//      It is launched first, on half of the SMs, and the prefix's kernel
+//      programmatically behind it, so that both run at once: the one waits for
+//      memory, the other for the tensor cores.
 //   3. Merge: the partials of every row.
 //   4. With weights: the scores become weights now that L is known.
 #include <cuda_bf16.h>
@@ -45,7 +47,8 @@ struct MergeParams {
     const float *own_o, *own_lse, *pre_o, *pre_lse;
     __nv_bfloat16 *o;
     float *lse, *row_lse;  // natural log, and log2 units for the weights; either may be null
-    int B, Hq, Hkv, G, P, max_seqlen;
+    const int2 *pre_rows;  // null: no prefix
+    int B, Hq, Hkv, G;
     PrefixOrder po;
 };
 
@@ -59,46 +62,48 @@ struct WeightParams {
 
 // The partials of row (b, h): those of the prefix, then those of b's own keys.
 struct RowParts {
-    const float *pre, *own;  // log-sum-exps, log2 units
-    size_t own_first;        // number of the first own partial
+    size_t pre, own;  // row of the first one in each array of partials
     int pre_stride, own_stride, n_pre, n;
-    __device__ __forceinline__ float lse(int i) const {
-        return i < n_pre ? pre[(size_t)i * pre_stride] : own[(size_t)(i - n_pre) * own_stride];
+    __device__ __forceinline__ size_t row(int i) const {
+        return i < n_pre ? pre + (size_t)i * pre_stride : own + (size_t)(i - n_pre) * own_stride;
     }
 };
 
 __device__ __forceinline__ RowParts row_parts(const MergeParams &p, int b, int h) {
-    RowParts r;
-    r.n_pre = r.n = 0;
-    r.pre_stride = p.B * p.Hq;
-    r.own_stride = p.G;
-    r.own_first = 0;
-    r.pre = p.pre_lse + (size_t)b * p.Hq + h;
-    r.own = p.own_lse;
-    const int g = h / p.G;
-    if (p.P > 0) r.n = r.n_pre = prefix_parts(p.po, prefix_row(p.po, g, b / p.po.rb / 2));
-    if (p.own_rows) {
-        const int2 own = p.own_rows[b * p.Hkv + g];  // not written for a sequence without keys
-        if (p.seqlens[b] > 0) {
-            r.own_first = own.x;
-            r.n += own.y;
-            r.own += r.own_first * p.G + (h - g * p.G);
-        }
+    RowParts r = {};
+    const int g = h / p.G, j = h - g * p.G;
+    int2 pre = make_int2(0, 0), own = pre;
+    if (p.pre_rows) {
+        const int tile = b / p.po.rb, m = tile / 2;
+        pre = p.pre_rows[prefix_row(p.po, g, m)];
+        r.pre_stride = p.po.id_rows;
+        // In lockstep the units of a partial number lie one behind the other.
+        r.pre = (size_t)(b - (p.po.lockstep ? 0 : 2 * m * p.po.rb)) * p.G + j;
     }
+    if (p.own_rows) {
+        own = p.own_rows[b * p.Hkv + g];  // not written for a sequence without keys
+        if (p.seqlens[b] <= 0) own = make_int2(0, 0);
+        r.own_stride = p.G;
+    }
+    r.pre += (size_t)pre.x * p.po.id_rows;
+    r.own = (size_t)own.x * p.G + j;
+    r.n_pre = pre.y;
+    r.n = pre.y + own.y;
     return r;
 }
 
 // Maximum and sum of 2^(lse_i - maximum) over a row's partials, by one warp;
 // w0 is 2^(lse_lane - maximum).
-__device__ __forceinline__ void warp_total(const RowParts &r, int lane, float &top, float &sum, float &w0) {
-    const float l0 = lane < r.n ? r.lse(lane) : -INFINITY;
+template <typename Lse>
+__device__ __forceinline__ void warp_total(const RowParts &r, Lse lse, int lane, float &top, float &sum, float &w0) {
+    const float l0 = lane < r.n ? lse(lane) : -INFINITY;
     top = l0;
-    for (int i = lane + 32; i < r.n; i += 32) top = fmaxf(top, r.lse(i));
+    for (int i = lane + 32; i < r.n; i += 32) top = fmaxf(top, lse(i));
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
     const float ref = top == -INFINITY ? 0.f : top;
     sum = w0 = fast_exp2(l0 - ref);
-    for (int i = lane + 32; i < r.n; i += 32) sum += fast_exp2(r.lse(i) - ref);
+    for (int i = lane + 32; i < r.n; i += 32) sum += fast_exp2(lse(i) - ref);
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
 }
@@ -137,10 +142,8 @@ __global__ void __launch_bounds__(kWarps > 1 ? kWarps * 32 : kMergeThreads) merg
     if (row >= rows) return;  // with kWarps > 1 a CTA is one row
     const int b = row / p.Hq, h = row - b * p.Hq;
     const RowParts r = row_parts(p, b, h);
-    const size_t pre_step = (size_t)rows * D, own_step = (size_t)p.G * D;
-    const float *pre = p.pre_o + (size_t)row * D + lane * kCols;
-    const float *own = p.own_o + (r.own_first * p.G + h % p.G) * D + lane * kCols;
-    auto part = [&](int i) { return i < r.n_pre ? pre + i * pre_step : own + (i - r.n_pre) * own_step; };
+    auto part = [&](int i) { return (i < r.n_pre ? p.pre_o : p.own_o) + r.row(i) * D + lane * kCols; };
+    auto lse = [&](int i) { return (i < r.n_pre ? p.pre_lse : p.own_lse)[r.row(i)]; };
     Cols<kCols> v[kAhead];
     auto fetch = [&](int i0) {
 #pragma unroll
@@ -149,7 +152,7 @@ __global__ void __launch_bounds__(kWarps > 1 ? kWarps * 32 : kMergeThreads) merg
     };
     fetch(q * kAhead);
     float top, sum, w0;
-    warp_total(r, lane, top, sum, w0);
+    warp_total(r, lse, lane, top, sum, w0);
     float acc[kCols] = {};
     for (int i0 = q * kAhead; i0 < r.n; i0 += kAhead * kWarps) {
         if (i0 > q * kAhead) fetch(i0);
@@ -158,7 +161,7 @@ __global__ void __launch_bounds__(kWarps > 1 ? kWarps * 32 : kMergeThreads) merg
             const int i = i0 + k;
             float w = __shfl_sync(0xffffffffu, w0, i & 31);
             if (i < r.n) {
-                if (i >= 32) w = fast_exp2(r.lse(i) - (top == -INFINITY ? 0.f : top));
+                if (i >= 32) w = fast_exp2(lse(i) - (top == -INFINITY ? 0.f : top));
                 if (w != 0.f)  // an empty partial adds nothing
 #pragma unroll
                     for (int c = 0; c < kCols; ++c) acc[c] += w * v[k].v[c];
@@ -273,8 +276,7 @@ __global__ void __launch_bounds__(kWeightThreads) weight_kernel(const WeightPara
 }
 
 template <int D>
-int launch_prefix(const DecodePrefixLaunch &a, const PrefixOrder &po, float *part_o, float *part_lse,
-                  cudaStream_t stream) {
+int launch_prefix(const DecodePrefixLaunch &a, const PrefixLayout &l, const PrefixOrder &po, cudaStream_t stream) {
     using C = fwd::Cfg<D>;
     CUtensorMap mq, mk, mv;
     const int G = a.Hq / a.Hkv;
@@ -283,8 +285,11 @@ int launch_prefix(const DecodePrefixLaunch &a, const PrefixOrder &po, float *par
         !encode_bf16_3d(&mv, a.vprefix, D, uint64_t(a.P), uint64_t(a.Hkv), 64, fwd::kBlockN))
         return note_cuda_error(cudaErrorInvalidValue, "cuTensorMapEncodeTiled (shared prefix)");
     fwd::PrefixParams p = {};
-    p.part_o = part_o;
-    p.part_lse = part_lse;
+    p.part_o = reinterpret_cast<float *>(a.workspace + l.pre_o);
+    p.part_lse = reinterpret_cast<float *>(a.workspace + l.pre_lse);
+    p.rows = reinterpret_cast<int2 *>(a.workspace + l.pre_rows);
+    p.seqlens = a.max_seqlen > 0 ? a.seqlens : nullptr;
+    p.max_seqlen = a.max_seqlen;
     p.po = po;
     p.B = a.B;
     p.N = a.P;
@@ -305,59 +310,20 @@ int launch_prefix(const DecodePrefixLaunch &a, const PrefixOrder &po, float *par
         if (fa.numRegs != fwd::kLaunchRegs || fa.maxThreadsPerBlock < fwd::kThreads)
             return note_cuda_error(cudaErrorInvalidConfiguration,
                                    "fwd_kernel (prefix) register count differs from the setmaxnreg split");
-        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes + fwd::kTurnBytes);
+        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes + fwd::kPrefixSmemBytes);
         if (e != cudaSuccess) return note_cuda_error(e, "cudaFuncSetAttribute(fwd_kernel, prefix)");
         if (dev >= 0) attr_set[dev] = true;
     }
-    kernel<<<dim3(unsigned(po.grid)), dim3(fwd::kThreads), C::kSmemBytes + fwd::kTurnBytes, stream>>>(mq, mk, mv, p);
-    const cudaError_t e = cudaGetLastError();
-    return e == cudaSuccess ? 0 : note_cuda_error(e, "fwd_kernel (prefix) launch");
-}
-
-template <int D>
-int launch_own(const DecodePrefixLaunch &a, const PrefixLayout &l, bool behind_prefix, cudaStream_t stream) {
-    using C = own::Cfg<D>;
-    CUtensorMap mk, mv, mk16, mv16;
-    const uint64_t planes = uint64_t(a.B) * a.Hkv, keys = uint64_t(a.max_seqlen);
-    if (!encode_bf16_3d(&mk, a.kcache, D, keys, planes, 64, dec::kKeysPerStage) ||
-        !encode_bf16_3d(&mv, a.vcache, D, keys, planes, 64, dec::kKeysPerStage) ||
-        !encode_bf16_3d(&mk16, a.kcache, D, keys, planes, 64, 16) ||
-        !encode_bf16_3d(&mv16, a.vcache, D, keys, planes, 64, 16))
-        return note_cuda_error(cudaErrorInvalidValue, "cuTensorMapEncodeTiled (own keys)");
-    own::Params p = {};
-    p.q = static_cast<const __nv_bfloat16 *>(a.q);
-    p.seqlens = a.seqlens;
-    p.part_o = reinterpret_cast<float *>(a.workspace + l.own_o);
-    p.part_lse = reinterpret_cast<float *>(a.workspace + l.own_lse);
-    p.scores = a.weights ? reinterpret_cast<float *>(a.workspace + l.scores) : nullptr;
-    p.plan = reinterpret_cast<long long *>(a.workspace + l.plan);
-    p.rows = reinterpret_cast<int2 *>(a.workspace + l.own_rows);
-    p.B = a.B;
-    p.Hq = a.Hq;
-    p.Hkv = a.Hkv;
-    p.G = a.Hq / a.Hkv;
-    p.max_seqlen = a.max_seqlen;
-    p.narrow = planes * keys < (1ull << 29);
-    p.scale_log2 = a.scale * 1.4426950408889634f;
-    p.wait_ns = a.wait_ns;
-    auto kernel = own::own_kernel<D>;
-    static bool attr_set[kMaxDevices] = {};
-    const int dev = slot_for_device();
-    if (dev < 0 || !attr_set[dev]) {
-        const cudaError_t e =
-            cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes);
-        if (e != cudaSuccess) return note_cuda_error(e, "cudaFuncSetAttribute(own_kernel)");
-        if (dev >= 0) attr_set[dev] = true;
-    }
-    const dim3 grid(unsigned(l.own_ctas)), block(dec::kThreads);
+    const dim3 grid(unsigned(prefix_grid(po))), block(fwd::kThreads);
+    constexpr size_t smem = C::kSmemBytes + fwd::kPrefixSmemBytes;
     cudaError_t e;
-    if (behind_prefix) {
-        e = dec::launch_programmatic(kernel, grid, block, C::kSmemBytes, stream, mk, mv, mk16, mv16, p);
+    if (a.max_seqlen > 0) {  // behind the own keys' kernel, beside it on the GPU
+        e = dec::launch_programmatic(kernel, grid, block, smem, stream, mq, mk, mv, p);
     } else {
-        kernel<<<grid, block, C::kSmemBytes, stream>>>(mk, mv, mk16, mv16, p);
+        kernel<<<grid, block, smem, stream>>>(mq, mk, mv, p);
         e = cudaGetLastError();
     }
-    return e == cudaSuccess ? 0 : note_cuda_error(e, "own_kernel launch");
+    return e == cudaSuccess ? 0 : note_cuda_error(e, "fwd_kernel (prefix) launch");
 }
 
 template <int D>
@@ -367,23 +333,22 @@ int launch_all(const DecodePrefixLaunch &a, cudaStream_t stream) {
     const int G = a.Hq / a.Hkv;
     if (!decode_prefix_layout(a.B, a.Hq, a.Hkv, a.P, a.d, a.max_seqlen, a.weights != nullptr, a.num_sms, &l))
         return ATTN_ERR_ARG;
-    float *pre_o = reinterpret_cast<float *>(a.workspace + l.pre_o);
-    float *pre_lse = reinterpret_cast<float *>(a.workspace + l.pre_lse);
-    if (a.P > 0) {
-        prefix_order(&m.po, a.B, G, a.Hkv, a.P, a.num_sms);
-        const int rc = launch_prefix<D>(a, m.po, pre_o, pre_lse, stream);
-        if (rc) return rc;
-    }
     if (a.max_seqlen > 0) {
-        const int rc = launch_own<D>(a, l, a.P > 0, stream);
+        const int rc = own_launch(a, l, stream);
         if (rc) return rc;
         m.own_rows = reinterpret_cast<const int2 *>(a.workspace + l.own_rows);
         m.seqlens = a.seqlens;
     }
+    if (a.P > 0) {
+        prefix_order(&m.po, a.B, G, a.Hkv, a.P, a.d, l.own_ctas, a.num_sms);
+        const int rc = launch_prefix<D>(a, l, m.po, stream);
+        if (rc) return rc;
+        m.pre_rows = reinterpret_cast<const int2 *>(a.workspace + l.pre_rows);
+    }
     m.own_o = reinterpret_cast<const float *>(a.workspace + l.own_o);
     m.own_lse = reinterpret_cast<const float *>(a.workspace + l.own_lse);
-    m.pre_o = pre_o;
-    m.pre_lse = pre_lse;
+    m.pre_o = reinterpret_cast<const float *>(a.workspace + l.pre_o);
+    m.pre_lse = reinterpret_cast<const float *>(a.workspace + l.pre_lse);
     m.o = static_cast<__nv_bfloat16 *>(a.o);
     m.lse = a.lse;
     m.row_lse = a.weights ? reinterpret_cast<float *>(a.workspace + l.row_lse) : nullptr;
@@ -391,8 +356,6 @@ int launch_all(const DecodePrefixLaunch &a, cudaStream_t stream) {
     m.Hq = a.Hq;
     m.Hkv = a.Hkv;
     m.G = G;
-    m.P = a.P;
-    m.max_seqlen = a.max_seqlen;
     // A warp a row where the rows fill the SMs; few rows get more warps, and the
     // fewest, whose partials can be many, sixteen.
     const long long rows = (long long)a.B * a.Hq;
@@ -422,16 +385,22 @@ int launch_all(const DecodePrefixLaunch &a, cudaStream_t stream) {
 
 }  // namespace
 
+int own_ctas(int B, int Hkv, int P, int max_seqlen, int num_sms) {
+    const long long keys = (long long)B * Hkv * max_seqlen, most = (keys + own::kMinShare - 1) / own::kMinShare;
+    const int sms = P > 0 && num_sms > 1 ? num_sms / 2 : num_sms;
+    return int(most < sms ? most : sms);
+}
+
 bool decode_prefix_layout(int B, int Hq, int Hkv, int P, int d, int max_seqlen, bool weights, int num_sms,
                           PrefixLayout *l) {
     auto up = [](size_t n) { return (n + 255) / 256 * 256; };
     const size_t rows = (size_t)B * Hq;
+    l->own_ctas = own_ctas(B, Hkv, P, max_seqlen, num_sms);
     PrefixOrder po = {};
-    if (P > 0 && !prefix_order(&po, B, Hq / Hkv, Hkv, P, num_sms)) return false;
-    const long long keys = (long long)B * Hkv * max_seqlen, most = (keys + own::kMinShare - 1) / own::kMinShare;
-    const long long ctas = most < own::kCtasPerSm * num_sms ? most : own::kCtasPerSm * num_sms;
-    const size_t parts = max_seqlen > 0 ? (size_t)ctas + (size_t)B * Hkv : 0;
-    l->own_ctas = int(ctas);
+    if (P > 0 && !prefix_order(&po, B, Hq / Hkv, Hkv, P, d, l->own_ctas, num_sms)) return false;
+    const size_t parts = max_seqlen > 0 ? (size_t)l->own_ctas + (size_t)B * Hkv : 0;
+    const size_t pre = (size_t)po.ids * po.id_rows;
+    if (parts > 0x7fffffff) return false;
     size_t at = 0;
     auto take = [&](size_t n) {
         const size_t here = at;
@@ -442,8 +411,9 @@ bool decode_prefix_layout(int B, int Hq, int Hkv, int P, int d, int max_seqlen, 
     l->own_rows = take(max_seqlen > 0 ? (size_t)B * Hkv * sizeof(int2) : 0);
     l->own_o = take(parts * (Hq / Hkv) * d * sizeof(float));
     l->own_lse = take(parts * (Hq / Hkv) * sizeof(float));
-    l->pre_o = take((size_t)po.slots * rows * d * sizeof(float));
-    l->pre_lse = take((size_t)po.slots * rows * sizeof(float));
+    l->pre_rows = take((size_t)po.rows * sizeof(int2));
+    l->pre_o = take(pre * d * sizeof(float));
+    l->pre_lse = take(pre * sizeof(float));
     l->scores = take(weights ? rows * max_seqlen * sizeof(float) : 0);
     l->row_lse = take(weights ? rows * sizeof(float) : 0);
     l->bytes = at;
@@ -455,13 +425,10 @@ int decode_prefix_launch(const DecodePrefixLaunch &a, cudaStream_t stream) {
 }
 
 cudaError_t decode_prefix_take_status(int *bits) {
-    int zero = 0, fwd_bits = 0, own_bits = 0;
-    cudaError_t e = cudaMemcpyFromSymbol(&fwd_bits, g_fwd_status, sizeof(int));
-    if (e == cudaSuccess) e = cudaMemcpyFromSymbol(&own_bits, g_own_status, sizeof(int));
-    if (e == cudaSuccess) e = cudaMemcpyToSymbol(g_fwd_status, &zero, sizeof(int));
-    if (e == cudaSuccess) e = cudaMemcpyToSymbol(g_own_status, &zero, sizeof(int));
-    *bits = fwd_bits | own_bits;
-    return e;
+    int zero = 0;
+    cudaError_t e = cudaMemcpyFromSymbol(bits, g_fwd_status, sizeof(int));
+    if (e != cudaSuccess) return e;
+    return cudaMemcpyToSymbol(g_fwd_status, &zero, sizeof(int));
 }
 
 }  // namespace attn

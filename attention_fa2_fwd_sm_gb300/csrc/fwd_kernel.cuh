@@ -85,10 +85,10 @@ constexpr int kCtrlRegs = 120;  // the warp-wide MMA issue loop spills at 104
 constexpr int kSoftmaxRegs = 192;
 static_assert(128 * kCtrlRegs + 256 * kSoftmaxRegs <= kThreads * kLaunchRegs, "register split");
 constexpr int kTmemCols = 512;
-// Shared memory of the prefix mapping's epilogue, behind everything else: 32
-// rows of 16 columns (20 words apart) for each softmax warp.
+// Shared memory of the prefix mapping, behind everything else: 32 rows of 16
+// columns (20 words apart) for each softmax warp's epilogue, and a PrefixRange.
 constexpr int kTurnStride = 20, kTurnFloats = 32 * kTurnStride;
-constexpr int kTurnBytes = 8 * kTurnFloats * 4 + 16;
+constexpr int kPrefixSmemBytes = 8 * kTurnFloats * 4 + 16 + 32;  // alignment, and the CTA's share
 
 template <int D>
 struct Cfg {
@@ -109,6 +109,9 @@ struct Cfg {
     // data, barriers, TMEM address, abort flag, two-entry unit queue, align slack
     static constexpr int kSmemBytes = kDataBytes + kNumBars * 8 + 32 + 1024;
 };
+
+template <int D>
+constexpr int kPrefixSmemOffset = (Cfg<D>::kSmemBytes - 1024 + 15) / 16 * 16;
 
 struct Params {
     __nv_bfloat16 *o;
@@ -133,9 +136,19 @@ struct SplitParams : Params {
 // Parameters of a shared prefix's launch: the rows of a tile are (batch entry,
 // query head of the group) pairs, N is the prefix's length and causal is 0.
 struct PrefixParams : Params {
-    float *part_o;    // [slots][B * Hq][D] fp32
-    float *part_lse;  // [slots][B * Hq] fp32, log2 units (-inf when empty)
+    float *part_o;    // [ids][id_rows][D] fp32
+    float *part_lse;  // [ids][id_rows] fp32, log2 units (-inf when empty)
+    int2 *rows;       // [rows of the order] first partial and number of partials
+    const int *seqlens;  // the own keys' lengths (null: none)
+    int max_seqlen;
     PrefixOrder po;
+};
+
+// A CTA's share of a prefix launch (shared memory, set up before the roles part).
+struct PrefixRange {
+    PrefixShares shares;
+    unsigned lo, hi;
+    int share;
 };
 
 struct UnitWork {
@@ -186,18 +199,22 @@ struct MappedWork<kMapSplit> : UnitWork {
 };
 template <>
 struct MappedWork<kMapPrefix> : UnitWork {
-    int s, jb;
+    int s, jb;  // s: the partial number
+    int row, m;
 };
 
 template <int kMap>
-__device__ __forceinline__ MappedWork<kMap> unit_work(const typename ParamsOf<kMap>::type &p, long long u) {
+__device__ __forceinline__ MappedWork<kMap> unit_work(const typename ParamsOf<kMap>::type &p, long long u,
+                                                      const PrefixRange *range) {
     if constexpr (kMap == kMapPrefix) {
         MappedWork<kMap> w;
-        const PrefixSegment seg = prefix_segment(p.po, blockIdx.x, int(u));
+        const PrefixSegment seg = prefix_segment(p.po, range->hi, blockIdx.x, int(u));
         w.b = 0;
         w.kvh = seg.g;
         w.h = seg.g * p.G;
-        w.s = seg.slot;
+        w.s = range->share + seg.row;
+        w.row = seg.row;
+        w.m = seg.m;
         w.jb = seg.j0;
         w.nmax = seg.n;
 #pragma unroll
@@ -335,9 +352,25 @@ __global__ void __launch_bounds__(kThreads, 1)
         *abort_flag = 0;
         fence_mbar_init();
     }
+    PrefixRange *prefix_range = nullptr;
     if constexpr (kMap == kMapPrefix) {
-        // The own keys' grid behind this one reads nothing that it writes.
-        griddep_launch_dependents();
+        prefix_range = reinterpret_cast<PrefixRange *>(smem + kPrefixSmemOffset<D> + 8 * kTurnFloats * 4);
+        if (warp == 2) {
+            long long keys = 0;
+            if (p.seqlens)
+                for (int i = lane; i < p.B; i += 32) keys += min(max(p.seqlens[i], 0), p.max_seqlen);
+#pragma unroll
+            for (int off = 16; off > 0; off >>= 1) keys += __shfl_xor_sync(0xffffffffu, keys, off);
+            if (lane == 0) {
+                PrefixRange r;
+                r.shares = prefix_shares(p.po, keys * p.Hkv);
+                r.share = prefix_share(p.po, blockIdx.x);
+                r.lo = prefix_begin(p.po, r.shares, r.share);
+                r.hi = prefix_begin(p.po, r.shares, r.share + 1);
+                *prefix_range = r;
+            }
+        }
+        griddep_launch_dependents();  // the merge waits for this grid to end
         // Tile rows that no box covers: zero once, so that their scores (which
         // nobody stores) stay finite and take the common softmax path.
         const int rows = p.po.rb * p.G;
@@ -382,7 +415,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (long long qi = 0; ok; ++qi) {
                 // Publish the next unit to the other roles (two-entry queue).
                 long long u;
-                if constexpr (kMap == kMapPrefix) u = prefix_start(p.po, blockIdx.x, int(qi));
+                if constexpr (kMap == kMapPrefix) u = prefix_start(p.po, prefix_range->lo, prefix_range->hi, int(qi));
                 else u = fetch_unit(p, qi, my_die);
                 const int qs = int(qi & 1);
                 if (qi >= 2 && !mbar_wait_bounded(bar(C::kBarUQEmpty + qs), uint32_t(((qi >> 1) - 1) & 1),
@@ -393,7 +426,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 unit_q[qs] = int(u);
                 mbar_arrive(bar(C::kBarUQFull + qs));
                 if (u < 0) break;
-                const auto w = unit_work<kMap>(p, u);
+                const auto w = unit_work<kMap>(p, u, prefix_range);
                 for (int t = 0; t < kNT && ok; ++t) {
                     if (w.nkv[t] == 0) continue;
                     if (q_loads[t] > 0)
@@ -530,7 +563,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const long long u = __shfl_sync(0xffffffffu, int(unit_q[qs]), 0);
                 mbar_arrive_elect(bar(C::kBarUQEmpty + qs));
                 if (u < 0) break;
-                const auto w = unit_work<kMap>(p, u);
+                const auto w = unit_work<kMap>(p, u, prefix_range);
                 if constexpr (kMap == kMapSplit) {
                     // A causal unit whose rows all lie before its key range has
                     // no block to visit (the producer loads nothing for it).
@@ -627,7 +660,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             __syncwarp();
             mbar_arrive_elect(bar(C::kBarUQEmpty + qs));
             if (u < 0) break;
-            const auto w = unit_work<kMap>(p, u);
+            const auto w = unit_work<kMap>(p, u, prefix_range);
             const long long f0 = kv_base;  // K_j at ring position f0 + 2j
             kv_base += 2 * (long long)w.nmax;
             const int nkv = w.nkv[t];
@@ -754,15 +787,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                 // conflicts on the way in), so that four lanes write 64
                 // consecutive bytes.
                 const int first = quarter * 32 + (lane >> 2);  // this lane's rows to store: first + 8 k
-                const size_t slot0 = (size_t)w.s * p.B;
-                auto prow_of = [&](int rr) {  // the partial of tile row rr, or -1
-                    const int be = w.row0[t] + rr / p.G;
-                    return rr < p.po.rb * p.G && be < p.B ? (long long)((slot0 + be) * p.Hq + w.h + rr % p.G) : -1;
-                };
-                long long to[4];
-#pragma unroll
-                for (int k = 0; k < 4; ++k) to[k] = prow_of(first + 8 * k);
-                float *turn = reinterpret_cast<float *>(smem + (C::kSmemBytes - 1024 + 15) / 16 * 16) + (warp - 4) * kTurnFloats;
+                const int limit = min(p.po.rb, p.B - w.row0[t]) * p.G;  // rows of the tile in use
+                const size_t base = (size_t)w.s * p.po.id_rows + (p.po.lockstep ? w.m * p.po.unit_rows : 0) +
+                                    t * (p.po.unit_rows / kNT);
+                if (t == 0 && r == 0 && w.jb == 0 && (w.m == 0 || !p.po.lockstep)) {
+                    const int last = prefix_holder(p.po, prefix_range->shares, unsigned(w.row + 1) * p.po.nblk - 1);
+                    p.rows[w.row] = make_int2(w.s, last - prefix_range->share + 1);
+                }
+                float *turn = reinterpret_cast<float *>(smem + kPrefixSmemOffset<D>) + (warp - 4) * kTurnFloats;
 #pragma unroll
                 for (int c = 0; c < D / 32; ++c) {
                     uint32_t ov[32];
@@ -783,13 +815,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                         for (int k = 0; k < 4; ++k) {
                             const float4 v = *reinterpret_cast<const float4 *>(
                                 turn + (8 * k + (lane >> 2)) * kTurnStride + (lane & 3) * 4);
-                            if (to[k] >= 0)
-                                *reinterpret_cast<float4 *>(p.part_o + to[k] * D + c * 32 + half * 16 + (lane & 3) * 4) = v;
+                            if (first + 8 * k < limit)
+                                *reinterpret_cast<float4 *>(p.part_o + (base + first + 8 * k) * D + c * 32 + half * 16 +
+                                                            (lane & 3) * 4) = v;
                         }
                     }
                 }
-                const long long mine = prow_of(r);
-                if (mine >= 0) p.part_lse[mine] = l_run == 0.f ? -INFINITY : m_run + __log2f(l_run);
+                if (r < limit) p.part_lse[base + r] = l_run == 0.f ? -INFINITY : m_run + __log2f(l_run);
             } else if constexpr (kMap == kMapSplit) {
                 const float inv_l = l_run > 0.f ? 1.f / l_run : 0.f;
                 const bool row_ok = row < p.N;
@@ -853,6 +885,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_after();
         tmem_dealloc(tmem_base, kTmemCols);
     }
+    // The own keys' grid ahead: whoever waits for this grid has waited for it too.
+    if constexpr (kMap == kMapPrefix) griddep_wait();
     if (threadIdx.x == 0 && p.order != kNaiveHeadFirst) {
         // Every CTA has fetched its last unit before it gets here, so the last
         // CTA to arrive may reset the launch's counters for the next user.

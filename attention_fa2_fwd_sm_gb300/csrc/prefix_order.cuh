@@ -4,16 +4,27 @@
 //
 // The B * G query rows that read KV head g are packed into 128-row MMA tiles of
 // `rb` whole batch entries each (rb * G <= 128), two tiles a unit, `mt` units a
-// head; each has to visit all nblk key blocks of the prefix.  Equal shares of
-// key blocks go to as many CTAs as there are SMs, whatever the head count:
+// head; each has to visit all nblk key blocks of the prefix.  Shares of key
+// blocks go to as many CTAs as there are SMs, whatever the head count:
 //   lockstep  every group of mt CTAs takes one share of the (head, key block)
 //             space, a CTA per unit, so the CTAs that run side by side read the
 //             same key blocks at the same time and all but one find them in L2;
 //   linear    the share is cut from the (head, unit, key block) space.
 // Lockstep unless it would leave more than a tenth of the SMs idle (mt near the
-// SM count).  A CTA's share is one segment per head (or unit) that it touches;
-// each segment writes one partial per query row.  A row's partials are numbered
-// by CTA: slot 0 is the first CTA that touches it.
+// SM count).  A row below is a head (lockstep) or a unit of a head (linear).
+//
+// The prefix is bound by the tensor cores, the sequences' own keys by HBM, so
+// the two run at the same time on different SMs: the own keys' kernel, ahead on
+// the stream, holds `own` SMs (half of them already draw HBM's full rate), the
+// first `early` shares start at once on the others, and the `late` ones wait for
+// its SMs.  So that all end together, a late share is shorter by what the own
+// keys take, tau key blocks' worth of time, estimated from their number T:
+//     early a + late b = total,  b = a - tau  (b = 0 where a <= tau).
+// The shares depend on the lengths alone, so results do not depend on timing.
+//
+// A CTA's share is one segment per row that it touches; each segment writes one
+// partial per query row, numbered share + row (both go up along the shares, one
+// of them at every cut): the numbers are distinct, a row's consecutive.
 #pragma once
 
 #include <cstdint>
@@ -33,48 +44,84 @@ struct PrefixOrder {
     int nblk;      // key blocks of the prefix
     int rb, mt;    // batch entries per tile; units (two tiles) per KV head
     int lockstep;
-    int per;       // key blocks of a CTA's share
-    int grid, slots;
-    unsigned total;  // key blocks over all rows of the order; below 2^31, as every product below
+    int early, late;  // shares
+    int unit_rows;    // query rows of a unit, its last tile full
+    int id_rows;      // query rows of a partial number
+    int ids;          // partial numbers
+    int rows;         // rows of the order
+    unsigned total;   // key blocks over all of them; below 2^30, as every product below
+    unsigned own_cost;  // key blocks' worth of time of one own key and KV head, in 2^-32
+};
+
+// Lengths of the early and the late shares.
+struct PrefixShares {
+    unsigned a, b;
 };
 
 // One piece of work: key blocks [j0, j0 + n) of unit m of KV head g.
 struct PrefixSegment {
-    int g, m, j0, n, slot;
+    int g, m, j0, n, row;
 };
 
+ATTN_HD int prefix_grid(const PrefixOrder &o) { return (o.early + o.late) * (o.lockstep ? o.mt : 1); }
+ATTN_HD int prefix_share(const PrefixOrder &o, int cta) { return o.lockstep ? cta / o.mt : cta; }
 ATTN_HD int prefix_row(const PrefixOrder &o, int g, int m) { return o.lockstep ? g : g * o.mt + m; }
 
-// Shares that touch row `row` of the order: the first one and their number.
-ATTN_HD int prefix_first(const PrefixOrder &o, int row) { return int(unsigned(row) * unsigned(o.nblk) / unsigned(o.per)); }
-ATTN_HD int prefix_parts(const PrefixOrder &o, int row) {
-    return int((unsigned(row + 1) * unsigned(o.nblk) - 1) / unsigned(o.per)) - prefix_first(o, row) + 1;
+// T: own keys over all KV heads.
+ATTN_HD PrefixShares prefix_shares(const PrefixOrder &o, long long T) {
+    const unsigned e = unsigned(o.early), l = unsigned(o.late);
+    // (own_cost is below 2^18, and no memory holds 2^44 keys)
+    const unsigned long long wide = (unsigned long long)(T < (1LL << 44) ? T : (1LL << 44)) * o.own_cost >> 32;
+    const unsigned tau = wide < (1u << 30) ? unsigned(wide) : (1u << 30);
+    PrefixShares s;
+    s.a = (o.total + e - 1) / e;
+    s.b = 0;
+    if (l > 0 && s.a > tau) {
+        s.a = unsigned((o.total + (unsigned long long)l * tau + e + l - 1) / (e + l));
+        s.b = e * s.a >= o.total ? 0 : (o.total - e * s.a + l - 1) / l;
+    }
+    return s;
 }
 
-// First key block of CTA `cta`'s i-th segment in the order's linear space, or -1.
-ATTN_HD int prefix_start(const PrefixOrder &o, int cta, int i) {
-    const unsigned lo = unsigned(o.lockstep ? cta / o.mt : cta) * unsigned(o.per);
-    const unsigned hi = lo + o.per < o.total ? lo + o.per : o.total;
+// First key block of a share in the order's space; a share may be empty.
+ATTN_HD unsigned prefix_begin(const PrefixOrder &o, const PrefixShares &s, int share) {
+    const unsigned x = unsigned(share), e = unsigned(o.early);
+    const unsigned at = x <= e ? x * s.a : e * s.a + (x - e) * s.b;
+    return at < o.total ? at : o.total;
+}
+// The share that holds key block x.
+ATTN_HD int prefix_holder(const PrefixOrder &o, const PrefixShares &s, unsigned x) {
+    const unsigned early = unsigned(o.early) * s.a;
+    return int(x < early ? x / s.a : unsigned(o.early) + (x - early) / s.b);
+}
+
+// First key block of the i-th segment of a share [lo, hi), or -1.
+ATTN_HD int prefix_start(const PrefixOrder &o, unsigned lo, unsigned hi, int i) {
     const unsigned u = i == 0 ? lo : (lo / unsigned(o.nblk) + i) * unsigned(o.nblk);
     return u < hi ? int(u) : -1;
 }
 
-ATTN_HD PrefixSegment prefix_segment(const PrefixOrder &o, int cta, int u) {
-    const int share = o.lockstep ? cta / o.mt : cta;
-    const int row = int(unsigned(u) / unsigned(o.nblk));
+ATTN_HD PrefixSegment prefix_segment(const PrefixOrder &o, unsigned hi, int cta, int u) {
     PrefixSegment s;
-    s.m = o.lockstep ? cta % o.mt : row % o.mt;
-    s.g = o.lockstep ? row : row / o.mt;
-    s.j0 = u - row * o.nblk;
-    const unsigned end = unsigned(share + 1) * unsigned(o.per);
-    const int left = int((end < o.total ? end : o.total) - unsigned(u));
+    s.row = int(unsigned(u) / unsigned(o.nblk));
+    s.m = o.lockstep ? cta % o.mt : s.row % o.mt;
+    s.g = o.lockstep ? s.row : s.row / o.mt;
+    s.j0 = u - s.row * o.nblk;
+    const int left = int(hi - unsigned(u));
     s.n = left < o.nblk - s.j0 ? left : o.nblk - s.j0;
-    s.slot = share - prefix_first(o, row);
     return s;
 }
 
-// False when the problem is outside the order's 32-bit counters.
-inline bool prefix_order(PrefixOrder *o, int B, int G, int Hkv, int P, int num_sms) {
+// Measured: one key block of a unit takes about 1.5 us with two tiles and 1.05
+// us with one (d = 128; 1.3 and 0.9 at d = 64), and the own keys arrive at 6.4 TB/s.
+inline unsigned prefix_own_cost(int d, bool two_tiles) {
+    const double block_us = d == 128 ? (two_tiles ? 1.5 : 1.05) : (two_tiles ? 1.3 : 0.9);
+    return unsigned(4.0 * d / 6.4e6 / block_us * 4294967296.0);
+}
+
+// `own`: SMs that the own keys' kernel holds (0: none).  False when the problem
+// is outside the order's 32-bit counters.
+inline bool prefix_order(PrefixOrder *o, int B, int G, int Hkv, int P, int d, int own, int num_sms) {
     o->nblk = (P + kPrefixBlock - 1) / kPrefixBlock;
     o->rb = kPrefixTileRows / G;
     const int tiles = (B + o->rb - 1) / o->rb;
@@ -82,17 +129,18 @@ inline bool prefix_order(PrefixOrder *o, int B, int G, int Hkv, int P, int num_s
     const int groups = num_sms / o->mt;
     o->lockstep = 10LL * groups * o->mt >= 9LL * num_sms;
     const int shares = o->lockstep ? groups : num_sms;
-    const long long total = (long long)Hkv * o->nblk * (o->lockstep ? 1 : o->mt);
+    const long long rows = (long long)Hkv * (o->lockstep ? 1 : o->mt), total = rows * o->nblk;
     if (total >= (1LL << 30)) return false;
     o->total = unsigned(total);
-    o->per = int((total + shares - 1) / shares);
-    const int used = int((total + o->per - 1) / o->per);
-    o->grid = used * (o->lockstep ? o->mt : 1);
-    o->slots = 0;
-    for (int row = 0; row < Hkv * (o->lockstep ? 1 : o->mt); ++row) {
-        const int n = prefix_parts(*o, row);
-        if (n > o->slots) o->slots = n;
-    }
+    o->rows = int(rows);
+    o->early = o->lockstep ? (num_sms - own) / o->mt : num_sms - own;
+    if (o->early < 1) o->early = 1;
+    if (o->early > total) o->early = int(total);
+    o->late = total > o->early && shares > o->early ? shares - o->early : 0;
+    o->unit_rows = 2 * o->rb * G;
+    o->id_rows = o->unit_rows * (o->lockstep ? o->mt : 1);
+    o->ids = o->early + o->late + o->rows;
+    o->own_cost = prefix_own_cost(d, tiles > 1);
     return true;
 }
 

@@ -536,12 +536,15 @@ int attn_decode_prefix(const void *q, const void *kprefix, const void *vprefix, 
  * that it refuses, or when the device cannot be queried). */
 size_t attn_decode_prefix_workspace_bytes(int B, int Hq, int Hkv, int P, int d, int max_seqlen, int with_weights);
 
-/* Host-side view of the prefix phase: the i-th piece of work of CTA `cta` on a
- * GPU of num_sms SMs, as out[5] = {KV head, unit of up to 256 query rows, first
- * 128-key block, blocks, partial's slot}.  Returns 1, 0 when that CTA has no
- * i-th piece, or ATTN_ERR_ARG (sizes, or cta outside the grid).  Pure host
- * code; the same functions run inside the kernel. */
-int attn_decode_prefix_segment(int B, int Hq, int Hkv, int P, int num_sms, int cta, int i, int *out);
+/* Host-side view of the prefix phase of attn_decode_prefix on a GPU of num_sms
+ * SMs, when the sequences hold own_keys keys in all: the i-th piece of work of
+ * CTA `cta` as out[6] = {KV head, unit of up to 256 query rows, first 128-key
+ * block, blocks, number of its partial, number of its rows' last partial}.
+ * Returns 1, 0 when that CTA has no i-th piece, or ATTN_ERR_ARG (sizes, or cta
+ * outside the grid).  Pure host code; the same functions run inside the
+ * kernel. */
+int attn_decode_prefix_segment(int B, int Hq, int Hkv, int P, int d, int max_seqlen, long long own_keys, int num_sms,
+                               int cta, int i, int *out);
 
 /*
  * Eviction from a decode cache by accumulated attention weight (the weights

@@ -131,45 +131,61 @@ def test_decode_prefix_refusals(kw, code):
 
 
 @pytest.mark.parametrize("sms", [152, 8, 1])
-@pytest.mark.parametrize("B,Hq,Hkv,P", [
-    (1, 1, 1, 1), (1, 8, 1, 129), (4, 8, 2, 500), (32, 64, 8, 8192), (128, 64, 8, 32768), (7, 40, 8, 5001),
-    (300, 16, 16, 1000), (2000, 64, 4, 700), (1000, 15, 1, 257), (5000, 16, 1, 300)])
-def test_prefix_segments_cover_every_block_once(B, Hq, Hkv, P, sms):
-    """Every (KV head, unit, key block) belongs to one segment; a row's slots are 0, 1, ... without gaps; no CTA has more
-    than about its equal share of blocks; the grid is at most one CTA per SM."""
+@pytest.mark.parametrize("S,keys", [(0, 0), (1000, 0), (1000, 1.0), (1000, 0.3), (50000, 1.0)])
+@pytest.mark.parametrize("B,Hq,Hkv,P,d", [
+    (1, 1, 1, 1, 64), (1, 8, 1, 129, 128), (4, 8, 2, 500, 64), (32, 64, 8, 8192, 128), (128, 64, 8, 32768, 128),
+    (7, 40, 8, 5001, 128), (300, 16, 16, 1000, 64), (2000, 64, 4, 700, 64), (1000, 15, 1, 257, 128), (5000, 16, 1, 300, 128)])
+def test_prefix_segments_cover_every_block_once(B, Hq, Hkv, P, d, S, keys, sms):
+    """Whatever the own keys' number: every (KV head, unit, key block) belongs to one segment; a unit's partials are numbered
+    without gaps up to the one that every segment names as the last; no two segments of a unit share a number."""
     G, nblk = Hq // Hkv, -(-P // 128)
     units = (-(-B // (128 // G)) + 1) // 2
-    seen, slots, load = {}, {}, []
+    seen, numbers, last, load = {}, {}, {}, []
     cta = 0
     while True:
+        mine, i = 0, 0
         try:
-            first = attn.attn_decode_prefix_segment(B, Hq, Hkv, P, sms, cta, 0)
+            while (s := attn.attn_decode_prefix_segment(B, Hq, Hkv, P, d, S, int(keys * B * S), sms, cta, i)) is not None:
+                g, m, j0, n, part, end = s
+                assert n > 0 and 0 <= g < Hkv and 0 <= m < units and j0 + n <= nblk
+                for j in range(j0, j0 + n):
+                    assert (g, m, j) not in seen
+                    seen[g, m, j] = cta
+                numbers.setdefault((g, m), []).append(part)
+                assert last.setdefault((g, m), end) == end
+                mine, i = mine + n, i + 1
         except attn.AttnError:
             break
-        assert first is not None
-        mine, i = 0, 0
-        while (s := attn.attn_decode_prefix_segment(B, Hq, Hkv, P, sms, cta, i)) is not None:
-            g, m, j0, n, slot = s
-            assert n > 0 and 0 <= g < Hkv and 0 <= m < units and j0 + n <= nblk
-            for j in range(j0, j0 + n):
-                assert (g, m, j) not in seen
-                seen[g, m, j] = cta
-            slots.setdefault((g, m), set()).add(slot)
-            mine, i = mine + n, i + 1
         load.append(mine)
         cta += 1
-    assert cta <= sms
+    assert 0 < cta <= max(sms, units)
     assert len(seen) == Hkv * units * nblk
-    for s in slots.values():
-        assert s == set(range(len(s)))
-    assert max(load) <= -(-Hkv * units * nblk // max(1, int(0.9 * sms))) + units
+    for unit, parts in numbers.items():
+        assert sorted(parts) == list(range(min(parts), last[unit] + 1))
+    assert len({(p, u[1]) for u, parts in numbers.items() for p in parts}) == sum(map(len, numbers.values()))
+    if S == 0:  # nothing beside it: equal shares
+        assert max(load) <= -(-Hkv * units * nblk // max(1, int(0.9 * sms))) + units
+
+
+def test_prefix_shares_leave_room_for_the_own_keys():
+    """The more own keys, the less falls to the CTAs that start behind them."""
+    late = []
+    for own in (0, 20000, 60000, 100000, 10 ** 7):
+        n = 0
+        for cta in range(76, 152):
+            i = 0
+            while (s := attn.attn_decode_prefix_segment(128, 64, 8, 32768, 128, 1024, own, 152, cta, i)) is not None:
+                n, i = n + s[3], i + 1
+        late.append(n)
+    assert late == sorted(late, reverse=True) and late[0] > late[2] > 0 and late[-1] == 0
 
 
 def test_prefix_segment_refusals():
-    for args in [(0, 4, 2, 100, 152, 0, 0), (2, 4, 2, 0, 152, 0, 0), (2, 4, 2, 100, 0, 0, 0), (2, 4, 2, 100, 152, -1, 0),
-                 (2, 4, 2, 100, 152, 152, 0), (2, 4, 2, 100, 152, 0, -1)]:
+    ok = dict(B=2, Hq=4, Hkv=2, P=100, d=128, S=10, own=5, sms=152, cta=0, i=0)
+    assert attn.attn_decode_prefix_segment(*ok.values()) == (0, 0, 0, 1, 0, 0)
+    for kw in (dict(B=0), dict(P=0), dict(sms=0), dict(cta=-1), dict(cta=152), dict(i=-1), dict(own=-1), dict(d=96), dict(S=-1)):
         with pytest.raises(attn.AttnError):
-            attn.attn_decode_prefix_segment(*args)
+            attn.attn_decode_prefix_segment(*dict(ok, **kw).values())
 
 
 def test_decode_helpers_refuse_what_an_address_does_not_tell():
