@@ -13,7 +13,7 @@ namespace attn {
 
 namespace own {
 
-constexpr int kMinShare = 64;  // keys: one stage
+constexpr int kMinShare = 32;  // keys: two warps of a stage
 
 __device__ __forceinline__ int length_of(const int *seqlens, int max_seqlen, int b) {
     return min(max(seqlens[b], 0), max_seqlen);

@@ -5,7 +5,7 @@
 // memory busy is that no CTA ever has less to do than another and that its ring
 // never runs dry, so the kernel is persistent and its share exact: with T keys
 // in all, numbered by (sequence, KV head, key), CTA c takes keys [c S, (c + 1) S),
-// S = max(kMinShare, ceil(T Hkv / CTAs) rounded up to 64), however they fall on
+// S = ceil(T Hkv / CTAs) rounded up (find_share), however they fall on
 // the sequences; a share is cut into segments at the ends of the sequences' heads,
 // and the TMA warp runs ahead over those ends while the other warps finish a
 // segment.  (One CTA a chunk, as in the ragged decode: 81 us on 128 sequences of
@@ -18,11 +18,18 @@
 // the shares and one of them at every cut, so the numbers are distinct, a row's
 // are consecutive, and there are at most CTAs + B * Hkv of them.
 //
-// The arithmetic of a stage is the decode kernel's (decode_sm103.cu): four warps
-// of 16 keys each, m16n8k16 MMAs with the group's query heads on M, a running
-// maximum and sum a warp.  A stage takes four warps about 1400 clocks, mostly
-// latency, so two groups of four take turns: one CTA an SM then draws HBM's full
-// rate from half of the SMs, and the prefix's kernel has the others.
+// A stage is 64 keys, 16 a warp.  Up to 8 query heads a KV head (kWide false) they
+// are the N dimension of m16n8k16 MMAs: S^T = K Q^T and O^T = V^T P^T, keys and
+// then columns of V on M, so that no row of an MMA is idle; P^T gets from the one
+// layout to the other by movmatrix.  9 to 16 heads are the M dimension as in
+// decode_sm103.cu.  Heads on N take half the MMAs and half the accumulator
+// registers, which lets three groups of four warps take turns with the stages
+// instead of two; a stage takes its warps about a thousand clocks, mostly latency,
+// and one CTA an SM has to draw HBM's full rate from half of the SMs, because the
+// prefix's kernel has the others.
+// A ring slot always belongs to the same group: a group that skipped a slot's
+// phase could take the phase after it for complete, since a barrier tells its
+// phases apart by parity alone.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -42,23 +49,31 @@ namespace own {
 
 using namespace dec;
 
-constexpr int kGroups = 2, kWarps = kGroups * kConsumerWarps;  // consumer warps: a group takes every other stage
-constexpr int kOwnThreads = (kWarps + 1) * 32;
+// out = in^T for the 8 x 8 matrix of b16 whose row r is in lanes 4r .. 4r + 3.
+__device__ __forceinline__ uint32_t transpose_8x8(uint32_t in) {
+    uint32_t out;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(out) : "r"(in));
+    return out;
+}
 
-template <int D>
+template <int D, bool kWide>
 struct Cfg {
-    static constexpr int kStages = D == 128 ? 6 : 12;  // even: a slot always belongs to the same group
+    static constexpr int kGroups = kWide ? 2 : 3, kWarps = kGroups * kConsumerWarps;  // consumer warps
+    static constexpr int kThreads = (kWarps + 1) * 32;
+    static constexpr int kStages = D == 128 ? 6 : 12;
+    static_assert(kStages % kGroups == 0, "a slot belongs to one group");
     static constexpr int kChunks = D / 64;
     static constexpr int kChunkBytes = kKeysPerStage * 128;
     static constexpr int kTileBytes = kKeysPerStage * D * 2;
     static constexpr int kStageBytes = 2 * kTileBytes;
     static constexpr int kRingBytes = kStages * kStageBytes;
-    // Combine area: 16 rows of 32 columns (40 words apart: no bank conflicts)
-    // and (maximum, sum) per row for each consumer warp.
-    static constexpr int kTurnStride = 40;
-    static constexpr int kTurnBytes = kWarps * kMaxGroup * kTurnStride * 4;
-    static constexpr int kStateBytes = kWarps * kMaxGroup * 8;
+    // Combine area of a consumer warp: kRows heads of kCols columns, kStride
+    // words apart (no bank conflicts on the way in), and (maximum, sum) a head.
+    static constexpr int kRows = kWide ? 16 : 8, kCols = kWide ? 32 : 64, kStride = kWide ? 40 : 68;
+    static constexpr int kTurnBytes = kWarps * kRows * kStride * 4;
+    static constexpr int kStateBytes = kWarps * kRows * 8;
     static constexpr int kSmemBytes = kRingBytes + kTurnBytes + kStateBytes + 2 * kStages * 8 + 16 + 1024;
+    static_assert(kSmemBytes <= 227 * 1024, "shared memory");
 };
 
 struct Params {
@@ -98,8 +113,10 @@ __device__ __forceinline__ Place find_share(const Params &p, int cta, int ctas, 
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) T += __shfl_xor_sync(0xffffffffu, T, off);
     T *= Int(p.Hkv);
-    Int S = ((T + Int(ctas) - 1) / Int(ctas) + kKeysPerStage - 1) / kKeysPerStage * kKeysPerStage;
-    if (S < kMinShare) S = kMinShare;
+    Int S = (T + Int(ctas) - 1) / Int(ctas);
+    // Whole stages where there are keys enough; few keys are better spread.
+    const Int unit = S > 4 * kKeysPerStage ? Int(kKeysPerStage) : Int(kMinShare);
+    S = S == 0 ? unit : (S + unit - 1) / unit * unit;
     const Int lo = Int(cta) * S;
     if (write && lane == 0) {
         p.plan[0] = (long long)S;
@@ -138,19 +155,198 @@ __device__ __forceinline__ Place find_share(const Params &p, int cta, int ctas, 
     return at;
 }
 
+template <int kWarps>
 __device__ __forceinline__ void consumer_sync() {
     asm volatile("bar.sync 1, %0;" ::"n"(kWarps * 32) : "memory");
 }
 
+// One segment's running state in a consumer warp: the maxima and (per lane) sums
+// of the two heads that this lane's scores belong to, and the output
+// accumulators.  kWide: heads gq and gq + 8, acc[c] = O[heads][8 c ..]; else heads
+// 2 tq and 2 tq + 1, acc[c] = O^T[16 c ..][heads].
+template <int D, bool kWide>
+struct State {
+    static constexpr int kTiles = kWide ? D / 8 : D / 16;
+    float m[2], l[2], acc[kTiles][4];
+    __device__ __forceinline__ void clear() {
+        m[0] = m[1] = -INFINITY;
+        l[0] = l[1] = 0.f;
+#pragma unroll
+        for (int c = 0; c < kTiles; ++c)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) acc[c][i] = 0.f;
+    }
+    // acc[c][i] belongs to head index head(i).
+    static __device__ __forceinline__ constexpr int head(int i) { return kWide ? i >> 1 : i & 1; }
+    // The maxima move to at least mx; returns the exponents' offsets.
+    __device__ __forceinline__ void raise(const float (&mx)[2], float (&offset)[2]) {
+        float corr[2];
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+            const float m_new = fmaxf(m[r], mx[r]);
+            corr[r] = m_new == -INFINITY ? 1.f : fast_exp2(m[r] - m_new);
+            m[r] = m_new;
+            offset[r] = m_new == -INFINITY ? 0.f : -m_new;
+            l[r] *= corr[r];
+        }
+        if (__any_sync(0xffffffffu, corr[0] != 1.f || corr[1] != 1.f)) {
+#pragma unroll
+            for (int c = 0; c < kTiles; ++c)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) acc[c][i] *= corr[head(i)];
+        }
+    }
+};
+
+// Query heads of one KV head as MMA operands.
+template <int D, bool kWide>
+struct Queries {
+    static constexpr int kRegs = kWide ? 4 : 2;
+    uint32_t v[D / 16][kRegs];
+    __device__ __forceinline__ void load(const Params &p, int row) {
+        const int gq = (threadIdx.x & 31) >> 2, tq = threadIdx.x & 3;
+        const __nv_bfloat16 *q = p.q + ((size_t)row * p.G + gq) * D + tq * 2;
+#pragma unroll
+        for (int ks = 0; ks < D / 16; ++ks)
+#pragma unroll
+            for (int i = 0; i < kRegs; ++i) {
+                // kWide: A operand, registers (head gq, gq + 8) x (columns, columns + 8); else B, columns, columns + 8.
+                const int up = kWide ? i & 1 : 0, right = kWide ? i >> 1 : i;
+                v[ks][i] = gq + 8 * up < p.G ? *reinterpret_cast<const uint32_t *>(q + 8 * up * D + ks * 16 + 8 * right) : 0u;
+            }
+    }
+};
+
+// 16 keys of a stage, rows key0 .. key0 + 15 of the tiles at kt and vt, of which
+// n_valid (1..16) belong to the segment; `scores`: where the first one's go, or null.
 template <int D>
-__global__ void __launch_bounds__(kOwnThreads, 1)
+__device__ __forceinline__ void add_keys(State<D, true> &st, const Queries<D, true> &q, uint32_t kt, uint32_t vt, int key0,
+                                         int n_valid, float sl2, int G, float *scores) {
+    const int lane = threadIdx.x & 31, gq = lane >> 2, tq = lane & 3, sub = lane >> 3, rr = lane & 7;
+    float sc[2][4] = {};
+    {
+        const int key = key0 + ((sub & 2) ? 8 : 0) + rr;
+#pragma unroll
+        for (int ks = 0; ks < D / 16; ++ks) {
+            uint32_t b0, b1, b2, b3;
+            ldsm_x4(tile_unit_addr(kt, key, 2 * ks + (sub & 1)), b0, b1, b2, b3);
+            mma_bf16_16816(sc[0], q.v[ks], b0, b1);
+            mma_bf16_16816(sc[1], q.v[ks], b2, b3);
+        }
+    }
+    // Scores in log2 units, masked past the segment's end.
+    float mx[2] = {-INFINITY, -INFINITY}, offset[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const int kl = h * 8 + tq * 2 + (e & 1), hq = gq + ((e & 2) ? 8 : 0);
+            const bool in = kl < n_valid;
+            sc[h][e] = in ? sc[h][e] * sl2 : -INFINITY;
+            mx[e >> 1] = fmaxf(mx[e >> 1], sc[h][e]);
+            if (scores && in && hq < G) scores[kl * G + hq] = sc[h][e];
+        }
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+        mx[r] = fmaxf(mx[r], __shfl_xor_sync(0xffffffffu, mx[r], 1));
+        mx[r] = fmaxf(mx[r], __shfl_xor_sync(0xffffffffu, mx[r], 2));
+    }
+    st.raise(mx, offset);
+    uint32_t pa[4];
+#pragma unroll
+    for (int r = 0; r < 2; ++r)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const float p0 = fast_exp2(sc[h][2 * r] + offset[r]), p1 = fast_exp2(sc[h][2 * r + 1] + offset[r]);
+            st.l[r] += p0 + p1;
+            pa[2 * h + r] = pack_bf16x2(p0, p1);  // rounded to bf16 for the product with V
+        }
+    const int key = key0 + ((sub & 1) ? 8 : 0) + rr;
+#pragma unroll
+    for (int c = 0; c < D / 16; ++c) {
+        uint32_t b0, b1, b2, b3;
+        ldsm_x4_t(tile_unit_addr(vt, key, 2 * c + (sub >> 1)), b0, b1, b2, b3);
+        if (n_valid < 16) {
+            b0 = mask_pair(b0, 2 * tq, n_valid);
+            b1 = mask_pair(b1, 8 + 2 * tq, n_valid);
+            b2 = mask_pair(b2, 2 * tq, n_valid);
+            b3 = mask_pair(b3, 8 + 2 * tq, n_valid);
+        }
+        mma_bf16_16816(st.acc[2 * c], pa, b0, b1);
+        mma_bf16_16816(st.acc[2 * c + 1], pa, b2, b3);
+    }
+}
+
+template <int D>
+__device__ __forceinline__ void add_keys(State<D, false> &st, const Queries<D, false> &q, uint32_t kt, uint32_t vt, int key0,
+                                         int n_valid, float sl2, int G, float *scores) {
+    const int lane = threadIdx.x & 31, gq = lane >> 2, tq = lane & 3, sub = lane >> 3, rr = lane & 7;
+    float sa[4] = {}, sb[4] = {};  // two chains of MMAs, over the even and the odd steps
+    {
+        const int key = key0 + ((sub & 1) ? 8 : 0) + rr;
+#pragma unroll
+        for (int ks = 0; ks < D / 16; ++ks) {
+            uint32_t a[4];
+            ldsm_x4(tile_unit_addr(kt, key, 2 * ks + (sub >> 1)), a[0], a[1], a[2], a[3]);
+            mma_bf16_16816(ks & 1 ? sb : sa, a, q.v[ks][0], q.v[ks][1]);
+        }
+    }
+    // sa: (key gq, heads 2tq and 2tq + 1), (key gq + 8, the same), in log2 units, masked past the segment's end.
+    float mx[2], offset[2];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) sa[e] = gq + 8 * (e >> 1) < n_valid ? (sa[e] + sb[e]) * sl2 : -INFINITY;
+    if (scores) {
+        float *to = scores + gq * G + 2 * tq;
+#pragma unroll
+        for (int k = 0; k < 2; ++k, to += 8 * G)
+            if (gq + 8 * k < n_valid) {
+                if ((G & 1) == 0) {
+                    if (2 * tq < G) *reinterpret_cast<float2 *>(to) = make_float2(sa[2 * k], sa[2 * k + 1]);
+                } else {
+                    if (2 * tq < G) to[0] = sa[2 * k];
+                    if (2 * tq + 1 < G) to[1] = sa[2 * k + 1];
+                }
+            }
+    }
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+        mx[r] = fmaxf(sa[r], sa[2 + r]);
+#pragma unroll
+        for (int off = 4; off < 32; off <<= 1) mx[r] = fmaxf(mx[r], __shfl_xor_sync(0xffffffffu, mx[r], off));
+    }
+    st.raise(mx, offset);
+    float pr[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        pr[e] = fast_exp2(sa[e] + offset[e & 1]);
+        st.l[e & 1] += pr[e];
+    }
+    // P^T (keys x heads) as the B operand; rounded to bf16 for the product with V.
+    const uint32_t b0 = transpose_8x8(pack_bf16x2(pr[0], pr[1])), b1 = transpose_8x8(pack_bf16x2(pr[2], pr[3]));
+    const int key = key0 + ((sub & 2) ? 8 : 0) + rr;
+#pragma unroll
+    for (int c = 0; c < D / 16; ++c) {
+        uint32_t a[4];
+        ldsm_x4_t(tile_unit_addr(vt, key, 2 * c + (sub & 1)), a[0], a[1], a[2], a[3]);
+        if (n_valid < 16) {
+            a[0] = mask_pair(a[0], 2 * tq, n_valid);
+            a[1] = mask_pair(a[1], 2 * tq, n_valid);
+            a[2] = mask_pair(a[2], 8 + 2 * tq, n_valid);
+            a[3] = mask_pair(a[3], 8 + 2 * tq, n_valid);
+        }
+        mma_bf16_16816(st.acc[c], a, b0, b1);
+    }
+}
+
+template <int D, bool kWide>
+__global__ void __launch_bounds__(Cfg<D, kWide>::kThreads, 1)
     own_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                const __grid_constant__ CUtensorMap tmK16, const __grid_constant__ CUtensorMap tmV16, const Params p) {
-    using C = Cfg<D>;
+    using C = Cfg<D, kWide>;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    float *turn = reinterpret_cast<float *>(smem + C::kRingBytes);                          // [warp][16][40]
-    float2 *state = reinterpret_cast<float2 *>(smem + C::kRingBytes + C::kTurnBytes);       // [warp][16]
+    float *turn = reinterpret_cast<float *>(smem + C::kRingBytes);                     // [warp][kRows][kStride]
+    float2 *state = reinterpret_cast<float2 *>(smem + C::kRingBytes + C::kTurnBytes);  // [warp][kRows]
     uint64_t *bars = reinterpret_cast<uint64_t *>(smem + C::kRingBytes + C::kTurnBytes + C::kStateBytes);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(bars + 2 * C::kStages);
     int *status = &g_own_status;
@@ -165,12 +361,12 @@ __global__ void __launch_bounds__(kOwnThreads, 1)
         *abort_flag = 0;
         fence_mbar_init();
     }
-    if (threadIdx.x == kWarps * 32) {
+    if (threadIdx.x == C::kWarps * 32) {
         tma_prefetch_desc(&tmK);
         tma_prefetch_desc(&tmV);
     }
     const bool write = blockIdx.x == 0 && warp == 0;
-    // (CTAs + 1) shares stay below 2^31 where the caches' keys stay below 2^29: a share is at most twice its equal part or kMinShare.
+    // (CTAs + 1) shares stay below 2^31 where the caches' keys stay below 2^29.
     Place at = p.narrow ? find_share<unsigned>(p, blockIdx.x, gridDim.x, write)
                         : find_share<long long>(p, blockIdx.x, gridDim.x, write);
     __syncthreads();
@@ -179,7 +375,7 @@ __global__ void __launch_bounds__(kOwnThreads, 1)
     // Share, where a row can go on behind it (a longer one holds every row's rest; the last may be shorter).
     const unsigned share = unsigned(min(at.left, 0x40000000LL));
     long long fills = 0;  // ring fills issued (producer) or used (consumers)
-    if (warp == kWarps) {
+    if (warp == C::kWarps) {
         // ------------------------------------------------------------ producer
         if (lane == 0) {
             bool ok = true;
@@ -214,6 +410,7 @@ __global__ void __launch_bounds__(kOwnThreads, 1)
                     }
                     ++fills;
                 }
+                if (!ok) break;
                 at.left -= n;
                 if (at.left == 0) break;
                 at.next(p.seqlens, p.max_seqlen, p.Hkv);
@@ -224,110 +421,26 @@ __global__ void __launch_bounds__(kOwnThreads, 1)
         // A warp whose wait ran out does no more work but still meets the others
         // at every barrier of the segments ahead.
         const int gq = lane >> 2, tq = lane & 3;
-        const float sl2 = p.scale_log2;
         const int group = warp / kConsumerWarps, slice = warp % kConsumerWarps;  // of the stages; of a stage's keys
         bool ok = true;
-        // Q fragments (A operand, rows = query heads of the group, k = head dim).
-        uint32_t qa[D / 16][4];
-        auto load_q = [&](int row) {
-            const __nv_bfloat16 *q = p.q + ((size_t)row * p.G + gq) * D + tq * 2;
-#pragma unroll
-            for (int ks = 0; ks < D / 16; ++ks)
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    qa[ks][i] = gq + ((i & 1) ? 8 : 0) < p.G
-                                    ? *reinterpret_cast<const uint32_t *>(q + ((i & 1) ? 8 * D : 0) + ks * 16 + ((i & 2) ? 8 : 0))
-                                    : 0u;
-        };
-        load_q(at.b * p.Hkv + at.g);
+        Queries<D, kWide> q;
+        q.load(p, at.b * p.Hkv + at.g);
+        State<D, kWide> st;
         while (true) {
             const int n = at.keys(), row = at.b * p.Hkv + at.g, len = at.len;
             const bool first_of_row = at.j == 0;
-            float m_st[2] = {-INFINITY, -INFINITY}, l_st[2] = {0.f, 0.f};
-            float acc[D / 8][4];
-#pragma unroll
-            for (int c = 0; c < D / 8; ++c)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) acc[c][i] = 0.f;
+            st.clear();
+            float *scores = p.scores ? p.scores + ((size_t)row * p.max_seqlen + at.j + slice * 16) * p.G : nullptr;
             for (int i = 0; ok && i < n; i += kKeysPerStage, ++fills) {
-                if (int(fills & 1) != group) continue;
+                if (int(fills % C::kGroups) != group) continue;
                 const int s = int(fills % C::kStages);
                 ok = mbar_wait_warp(smem_u32(bars + s), (fills / C::kStages) & 1, p.wait_ns, abort_flag, status);
                 if (!ok) break;
                 const int n_valid = min(16, n - i - slice * 16);  // keys of this warp
                 if (n_valid > 0) {
-                    const uint32_t kt = smem_u32(smem + s * C::kStageBytes), vt = kt + C::kTileBytes;
-                    const int sub = lane >> 3, rr = lane & 7;
-                    float sc[2][4] = {};
-                    {
-                        const int key = slice * 16 + ((sub & 2) ? 8 : 0) + rr;
-#pragma unroll
-                        for (int ks = 0; ks < D / 16; ++ks) {
-                            uint32_t b0, b1, b2, b3;
-                            ldsm_x4(tile_unit_addr(kt, key, 2 * ks + (sub & 1)), b0, b1, b2, b3);
-                            mma_bf16_16816(sc[0], qa[ks], b0, b1);
-                            mma_bf16_16816(sc[1], qa[ks], b2, b3);
-                        }
-                    }
-                    // Scores in log2 units, masked past the segment's end.
-                    float x[2][4];
-#pragma unroll
-                    for (int h = 0; h < 2; ++h)
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            const int kl = h * 8 + tq * 2 + (e & 1);
-                            x[h][e] = kl < n_valid ? sc[h][e] * sl2 : -INFINITY;
-                        }
-                    if (p.scores) {
-                        float *to = p.scores + ((size_t)row * p.max_seqlen + at.j + i + slice * 16) * p.G;
-#pragma unroll
-                        for (int h = 0; h < 2; ++h)
-#pragma unroll
-                            for (int e = 0; e < 4; ++e) {
-                                const int kl = h * 8 + tq * 2 + (e & 1), hq = gq + ((e & 2) ? 8 : 0);
-                                if (kl < n_valid && hq < p.G) to[kl * p.G + hq] = x[h][e];
-                            }
-                    }
-                    uint32_t pa[4];
-                    float corr[2];
-#pragma unroll
-                    for (int r = 0; r < 2; ++r) {  // rows gq (e = 0, 1) and gq + 8 (e = 2, 3)
-                        float mx = fmaxf(fmaxf(x[0][2 * r], x[0][2 * r + 1]), fmaxf(x[1][2 * r], x[1][2 * r + 1]));
-                        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-                        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-                        const float m_new = fmaxf(m_st[r], mx);
-                        corr[r] = m_new == -INFINITY ? 1.f : fast_exp2(m_st[r] - m_new);
-                        m_st[r] = m_new;
-                        const float nm = m_new == -INFINITY ? 0.f : -m_new;
-                        const float p00 = fast_exp2(x[0][2 * r] + nm), p01 = fast_exp2(x[0][2 * r + 1] + nm);
-                        const float p10 = fast_exp2(x[1][2 * r] + nm), p11 = fast_exp2(x[1][2 * r + 1] + nm);
-                        l_st[r] = l_st[r] * corr[r] + (p00 + p01 + p10 + p11);
-                        pa[r] = pack_bf16x2(p00, p01);      // keys 2tq..: rounded to bf16 for the product with V
-                        pa[2 + r] = pack_bf16x2(p10, p11);  // keys 8 + 2tq..
-                    }
-#pragma unroll
-                    for (int c = 0; c < D / 8; ++c) {
-                        acc[c][0] *= corr[0];
-                        acc[c][1] *= corr[0];
-                        acc[c][2] *= corr[1];
-                        acc[c][3] *= corr[1];
-                    }
-                    {
-                        const int key = slice * 16 + ((sub & 1) ? 8 : 0) + rr;
-#pragma unroll
-                        for (int c = 0; c < D / 16; ++c) {
-                            uint32_t b0, b1, b2, b3;
-                            ldsm_x4_t(tile_unit_addr(vt, key, 2 * c + (sub >> 1)), b0, b1, b2, b3);
-                            if (n_valid < 16) {
-                                b0 = mask_pair(b0, 2 * tq, n_valid);
-                                b1 = mask_pair(b1, 8 + 2 * tq, n_valid);
-                                b2 = mask_pair(b2, 2 * tq, n_valid);
-                                b3 = mask_pair(b3, 8 + 2 * tq, n_valid);
-                            }
-                            mma_bf16_16816(acc[2 * c], pa, b0, b1);
-                            mma_bf16_16816(acc[2 * c + 1], pa, b2, b3);
-                        }
-                    }
+                    const uint32_t kt = smem_u32(smem + s * C::kStageBytes);
+                    add_keys<D>(st, q, kt, kt + C::kTileBytes, slice * 16, n_valid, p.scale_log2, p.G,
+                                scores ? scores + (size_t)i * p.G : nullptr);
                 }
                 __syncwarp();
                 if (lane == 0) mbar_arrive(smem_u32(bars + C::kStages + s));
@@ -337,78 +450,111 @@ __global__ void __launch_bounds__(kOwnThreads, 1)
             at.left -= n;
             if (at.left > 0) {
                 at.next(p.seqlens, p.max_seqlen, p.Hkv);
-                load_q(at.b * p.Hkv + at.g);
+                q.load(p, at.b * p.Hkv + at.g);
             }
 
-            // The warps' states become the segment's partial, 32 columns at a time.
-            const bool high = p.G > 8;  // rows 8..15 are in use
+            // The warps' states become the segment's partial, kCols columns at a time.
 #pragma unroll
             for (int r = 0; r < 2; ++r) {
-                float l = l_st[r];
-                l += __shfl_xor_sync(0xffffffffu, l, 1);
-                l += __shfl_xor_sync(0xffffffffu, l, 2);
-                if (tq == 0 && (r == 0 || high)) state[warp * kMaxGroup + gq + 8 * r] = make_float2(m_st[r], l);
+                float l = st.l[r];
+                if constexpr (kWide) {
+                    l += __shfl_xor_sync(0xffffffffu, l, 1);
+                    l += __shfl_xor_sync(0xffffffffu, l, 2);
+                    if (tq == 0) state[warp * C::kRows + gq + 8 * r] = make_float2(st.m[r], l);
+                } else {
+#pragma unroll
+                    for (int off = 4; off < 32; off <<= 1) l += __shfl_xor_sync(0xffffffffu, l, off);
+                    if (gq == 0) state[warp * C::kRows + 2 * tq + r] = make_float2(st.m[r], l);
+                }
             }
-            consumer_sync();
-            float f[2] = {0.f, 0.f};
+            consumer_sync<C::kWarps>();
+            float f[2];
 #pragma unroll
             for (int r = 0; r < 2; ++r) {
+                const int h = kWide ? gq + 8 * r : 2 * tq + r;
                 float top = -INFINITY;
-                if (r == 1 && !high) break;
 #pragma unroll
-                for (int w = 0; w < kWarps; ++w) top = fmaxf(top, state[w * kMaxGroup + gq + 8 * r].x);
-                f[r] = fast_exp2(m_st[r] - (top == -INFINITY ? 0.f : top));
+                for (int w = 0; w < C::kWarps; ++w) top = fmaxf(top, state[w * C::kRows + h].x);
+                f[r] = fast_exp2(st.m[r] - (top == -INFINITY ? 0.f : top));
             }
             const size_t part = (size_t)blockIdx.x + row;
             if (first_of_row && threadIdx.x == 0)
                 p.rows[row] = make_int2(int(part), 1 + int((unsigned(len - n) + share - 1) / share));
-            // A thread stores column `col` of rows row0 and row0 + 8: their sums once, ahead of the columns.
-            const int col = threadIdx.x & 31, row0 = threadIdx.x >> 5;
-            float inv[kMaxGroup / kWarps];
+            // Warps 0..7 store head `warp` (and `warp` + 8).
+            constexpr int kStores = C::kRows / 8;
+            float inv[kStores];
+            if (warp < 8) {
 #pragma unroll
-            for (int k = 0; k < kMaxGroup / kWarps; ++k) {
-                const int h = row0 + kWarps * k;
-                if (h >= p.G) break;
-                float top = -INFINITY, sum = 0.f;
+                for (int k = 0; k < kStores; ++k) {
+                    const int h = warp + 8 * k;
+                    inv[k] = 0.f;
+                    if (h >= p.G) break;
+                    float top = -INFINITY, sum = 0.f;
 #pragma unroll
-                for (int w = 0; w < kWarps; ++w) top = fmaxf(top, state[w * kMaxGroup + h].x);
-                const float ref = top == -INFINITY ? 0.f : top;
+                    for (int w = 0; w < C::kWarps; ++w) top = fmaxf(top, state[w * C::kRows + h].x);
+                    const float ref = top == -INFINITY ? 0.f : top;
 #pragma unroll
-                for (int w = 0; w < kWarps; ++w) {
-                    const float2 st = state[w * kMaxGroup + h];
-                    sum += fast_exp2(st.x - ref) * st.y;
+                    for (int w = 0; w < C::kWarps; ++w) {
+                        const float2 x = state[w * C::kRows + h];
+                        sum += fast_exp2(x.x - ref) * x.y;
+                    }
+                    inv[k] = sum == 0.f ? 0.f : 1.f / sum;  // NaN stays NaN
+                    if (ok && lane == 0) p.part_lse[part * p.G + h] = sum == 0.f ? -INFINITY : top + __log2f(sum);
                 }
-                inv[k] = sum == 0.f ? 0.f : 1.f / sum;  // NaN stays NaN
-                if (ok && col == 0) p.part_lse[part * p.G + h] = sum == 0.f ? -INFINITY : top + __log2f(sum);
             }
 #pragma unroll
-            for (int c = 0; c < D / 32; ++c) {
-                float *mine = turn + (warp * kMaxGroup + gq) * C::kTurnStride + tq * 2;
+            for (int c0 = 0; c0 < D; c0 += C::kCols) {
+                float *mine = turn + warp * C::kRows * C::kStride;
+                if constexpr (kWide) {
 #pragma unroll
-                for (int u = 0; u < 4; ++u) {
-                    const float(&a)[4] = acc[4 * c + u];
-                    *reinterpret_cast<float2 *>(mine + u * 8) = make_float2(a[0] * f[0], a[1] * f[0]);
-                    if (high)
-                        *reinterpret_cast<float2 *>(mine + 8 * C::kTurnStride + u * 8) =
-                            make_float2(a[2] * f[1], a[3] * f[1]);
+                    for (int u = 0; u < C::kCols / 8; ++u) {
+                        const float(&a)[4] = st.acc[c0 / 8 + u];
+                        float *to = mine + gq * C::kStride + u * 8 + tq * 2;
+                        *reinterpret_cast<float2 *>(to) = make_float2(a[0] * f[0], a[1] * f[0]);
+                        *reinterpret_cast<float2 *>(to + 8 * C::kStride) = make_float2(a[2] * f[1], a[3] * f[1]);
+                    }
+                } else {
+#pragma unroll
+                    for (int u = 0; u < C::kCols / 16; ++u) {
+                        const float(&a)[4] = st.acc[c0 / 16 + u];
+                        float *to = mine + 2 * tq * C::kStride + u * 16 + gq;
+                        to[0] = a[0] * f[0];
+                        to[C::kStride] = a[1] * f[1];
+                        to[8] = a[2] * f[0];
+                        to[C::kStride + 8] = a[3] * f[1];
+                    }
                 }
-                consumer_sync();
+                consumer_sync<C::kWarps>();
+                if (warp < 8) {
 #pragma unroll
-                for (int k = 0; k < kMaxGroup / kWarps; ++k) {
-                    const int h = row0 + kWarps * k;
-                    if (h >= p.G) break;
-                    float v = 0.f;
+                    for (int k = 0; k < kStores; ++k) {
+                        const int h = warp + 8 * k;
+                        if (h >= p.G) break;
+                        float *to = p.part_o + (part * p.G + h) * D + c0;
+                        if constexpr (kWide) {
+                            float v = 0.f;
 #pragma unroll
-                    for (int w = 0; w < kWarps; ++w) v += turn[(w * kMaxGroup + h) * C::kTurnStride + col];
-                    if (ok) p.part_o[(part * p.G + h) * D + c * 32 + col] = v * inv[k];
+                            for (int w = 0; w < C::kWarps; ++w) v += turn[(w * C::kRows + h) * C::kStride + lane];
+                            if (ok) to[lane] = v * inv[k];
+                        } else {
+                            float2 v = make_float2(0.f, 0.f);
+#pragma unroll
+                            for (int w = 0; w < C::kWarps; ++w) {
+                                const float2 x = *reinterpret_cast<const float2 *>(turn + (w * C::kRows + h) * C::kStride + 2 * lane);
+                                v.x += x.x;
+                                v.y += x.y;
+                            }
+                            if (ok) *reinterpret_cast<float2 *>(to + 2 * lane) = make_float2(v.x * inv[k], v.y * inv[k]);
+                        }
+                    }
                 }
-                consumer_sync();
+                consumer_sync<C::kWarps>();
             }
             if (at.left == 0) break;
         }
     }
     __syncthreads();
-    if (*abort_flag && warp == kWarps && lane == 0) {
+    if (*abort_flag && warp == C::kWarps && lane == 0) {
         // A wait ran out.  Before the CTA exits, wait (bounded, with a fixed
         // limit) for the copies of the last fill of every ring slot so that none
         // is still writing shared memory.
@@ -420,9 +566,9 @@ __global__ void __launch_bounds__(kOwnThreads, 1)
     }
 }
 
-template <int D>
+template <int D, bool kWide>
 int launch(const DecodePrefixLaunch &a, const PrefixLayout &l, cudaStream_t stream) {
-    using C = Cfg<D>;
+    using C = Cfg<D, kWide>;
     CUtensorMap mk, mv, mk16, mv16;
     const uint64_t planes = uint64_t(a.B) * a.Hkv, keys = uint64_t(a.max_seqlen);
     if (!encode_bf16_3d(&mk, a.kcache, D, keys, planes, 64, kKeysPerStage) ||
@@ -446,7 +592,7 @@ int launch(const DecodePrefixLaunch &a, const PrefixLayout &l, cudaStream_t stre
     p.narrow = planes * keys < (1ull << 29);
     p.scale_log2 = a.scale * 1.4426950408889634f;
     p.wait_ns = a.wait_ns;
-    auto kernel = own_kernel<D>;
+    auto kernel = own_kernel<D, kWide>;
     static bool attr_set[kMaxDevices] = {};
     const int dev = slot_for_device();
     if (dev < 0 || !attr_set[dev]) {
@@ -455,7 +601,7 @@ int launch(const DecodePrefixLaunch &a, const PrefixLayout &l, cudaStream_t stre
         if (e != cudaSuccess) return note_cuda_error(e, "cudaFuncSetAttribute(own_kernel)");
         if (dev >= 0) attr_set[dev] = true;
     }
-    kernel<<<dim3(unsigned(l.own_ctas)), dim3(kOwnThreads), C::kSmemBytes, stream>>>(mk, mv, mk16, mv16, p);
+    kernel<<<dim3(unsigned(l.own_ctas)), dim3(C::kThreads), C::kSmemBytes, stream>>>(mk, mv, mk16, mv16, p);
     const cudaError_t e = cudaGetLastError();
     return e == cudaSuccess ? 0 : note_cuda_error(e, "own_kernel launch");
 }
@@ -463,7 +609,9 @@ int launch(const DecodePrefixLaunch &a, const PrefixLayout &l, cudaStream_t stre
 }  // namespace own
 
 int own_launch(const DecodePrefixLaunch &a, const PrefixLayout &l, cudaStream_t stream) {
-    return a.d == 64 ? own::launch<64>(a, l, stream) : own::launch<128>(a, l, stream);
+    const bool wide = a.Hq / a.Hkv > 8;
+    if (a.d == 64) return wide ? own::launch<64, true>(a, l, stream) : own::launch<64, false>(a, l, stream);
+    return wide ? own::launch<128, true>(a, l, stream) : own::launch<128, false>(a, l, stream);
 }
 
 cudaError_t own_take_status(int *bits) {

@@ -113,10 +113,13 @@ ATTN_HD PrefixSegment prefix_segment(const PrefixOrder &o, unsigned hi, int cta,
 }
 
 // Measured: one key block of a unit takes about 1.5 us with two tiles and 1.05
-// us with one (d = 128; 1.3 and 0.9 at d = 64), and the own keys arrive at 6.4 TB/s.
+// us with one (d = 128; 1.3 and 0.9 at d = 64), and half of the SMs draw the own
+// keys at 4 TB/s in segments of some hundred keys (5.5 TB/s in long ones).  At
+// 6.4 TB/s here, 128 x (32K shared + 512 .. 1024 own) keys took 173 us, at 4 TB/s
+// 163, one phase after the other 176; 32 x (8K + 256 .. 512) 54, 42 and 46 us.
 inline unsigned prefix_own_cost(int d, bool two_tiles) {
     const double block_us = d == 128 ? (two_tiles ? 1.5 : 1.05) : (two_tiles ? 1.3 : 0.9);
-    return unsigned(4.0 * d / 6.4e6 / block_us * 4294967296.0);
+    return unsigned(4.0 * d / 4.0e6 / block_us * 4294967296.0);
 }
 
 // `own`: SMs that the own keys' kernel holds (0: none).  False when the problem
