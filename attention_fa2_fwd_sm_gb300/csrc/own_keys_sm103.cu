@@ -89,24 +89,26 @@ struct Params {
     unsigned long long wait_ns;
 };
 
+// The lengths of 256 sequences from `first` on, over the lanes of a warp.
+constexpr int kRound = 8;
+__device__ __forceinline__ void load_lengths(const Params &p, int first, int (&len)[kRound]) {
+#pragma unroll
+    for (int k = 0; k < kRound; ++k) {
+        const int i = first + 32 * k + int(threadIdx.x & 31);
+        len[k] = i < p.B ? length_of(p.seqlens, p.max_seqlen, i) : 0;
+    }
+}
+
 // Where CTA `cta` of `ctas` starts (left = 0: it has no share).  All lanes of
 // the calling warp; `write`: also write the plan down.  Int: wide enough for the
 // number of keys, so that the common case scans and divides in 32 bits.
+// `len` holds load_lengths(0), which the caller has had time to wait for.
 template <typename Int>
-__device__ __forceinline__ Place find_share(const Params &p, int cta, int ctas, bool write) {
-    constexpr int kRound = 8;  // groups of 32 sequences whose lengths are loaded together
+__device__ __forceinline__ Place find_share(const Params &p, int (&len)[kRound], int cta, int ctas, bool write) {
     const int lane = threadIdx.x & 31;
-    int len[kRound];
-    auto load = [&](int first) {
-#pragma unroll
-        for (int k = 0; k < kRound; ++k) {
-            const int i = first + 32 * k + lane;
-            len[k] = i < p.B ? length_of(p.seqlens, p.max_seqlen, i) : 0;
-        }
-    };
     Int T = 0;
     for (int first = 0; first < p.B; first += 32 * kRound) {
-        load(first);
+        if (first > 0) load_lengths(p, first, len);
 #pragma unroll
         for (int k = 0; k < kRound; ++k) T += len[k];
     }
@@ -126,7 +128,7 @@ __device__ __forceinline__ Place find_share(const Params &p, int cta, int ctas, 
     Int before = 0;  // keys of the sequences before, over all KV heads
     bool searching = at.left > 0;
     for (int first = 0; first < p.B && (write || searching); first += 32 * kRound) {
-        if (p.B > 32 * kRound) load(first);
+        if (p.B > 32 * kRound) load_lengths(p, first, len);
 #pragma unroll
         for (int k = 0; k < kRound; ++k) {
             if (first + 32 * k >= p.B) break;
@@ -353,6 +355,8 @@ __global__ void __launch_bounds__(Cfg<D, kWide>::kThreads, 1)
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
     griddep_launch_dependents();  // the prefix's grid, which reads nothing from here, may take the other SMs
+    int lengths[kRound];
+    load_lengths(p, 0, lengths);
     if (threadIdx.x == 0) {
         for (int s = 0; s < C::kStages; ++s) {
             mbar_init(smem_u32(bars + s), 1);                            // full
@@ -367,14 +371,14 @@ __global__ void __launch_bounds__(Cfg<D, kWide>::kThreads, 1)
     }
     const bool write = blockIdx.x == 0 && warp == 0;
     // (CTAs + 1) shares stay below 2^31 where the caches' keys stay below 2^29.
-    Place at = p.narrow ? find_share<unsigned>(p, blockIdx.x, gridDim.x, write)
-                        : find_share<long long>(p, blockIdx.x, gridDim.x, write);
+    Place at = p.narrow ? find_share<unsigned>(p, lengths, blockIdx.x, gridDim.x, write)
+                        : find_share<long long>(p, lengths, blockIdx.x, gridDim.x, write);
     __syncthreads();
     if (at.left == 0) return;
 
     // Share, where a row can go on behind it (a longer one holds every row's rest; the last may be shorter).
     const unsigned share = unsigned(min(at.left, 0x40000000LL));
-    long long fills = 0;  // ring fills issued (producer) or used (consumers)
+    int slot = 0, round = 0;  // of the ring's next stage to issue (producer) or use (consumers)
     if (warp == C::kWarps) {
         // ------------------------------------------------------------ producer
         if (lane == 0) {
@@ -382,8 +386,7 @@ __global__ void __launch_bounds__(Cfg<D, kWide>::kThreads, 1)
             while (ok) {
                 const int n = at.keys(), plane = at.b * p.Hkv + at.g;
                 for (int i = 0; i < n; i += kKeysPerStage) {
-                    const int s = int(fills % C::kStages);
-                    const long long round = fills / C::kStages;
+                    const int s = slot;
                     ok = round == 0 || mbar_wait_bounded(smem_u32(bars + C::kStages + s), (round - 1) & 1, p.wait_ns,
                                                          abort_flag, status);
                     if (!ok) break;
@@ -408,7 +411,7 @@ __global__ void __launch_bounds__(Cfg<D, kWide>::kThreads, 1)
                                 tma_load_3d(to + C::kTileBytes, &tmV16, fb, c * 64, key + 16 * w, plane);
                             }
                     }
-                    ++fills;
+                    if (++slot == C::kStages) slot = 0, ++round;
                 }
                 if (!ok) break;
                 at.left -= n;
@@ -431,10 +434,11 @@ __global__ void __launch_bounds__(Cfg<D, kWide>::kThreads, 1)
             const bool first_of_row = at.j == 0;
             st.clear();
             float *scores = p.scores ? p.scores + ((size_t)row * p.max_seqlen + at.j + slice * 16) * p.G : nullptr;
-            for (int i = 0; ok && i < n; i += kKeysPerStage, ++fills) {
-                if (int(fills % C::kGroups) != group) continue;
-                const int s = int(fills % C::kStages);
-                ok = mbar_wait_warp(smem_u32(bars + s), (fills / C::kStages) & 1, p.wait_ns, abort_flag, status);
+            for (int i = 0; ok && i < n; i += kKeysPerStage) {
+                const int s = slot, phase = round & 1;
+                if (++slot == C::kStages) slot = 0, ++round;
+                if (s % C::kGroups != group) continue;
+                ok = mbar_wait_warp(smem_u32(bars + s), phase, p.wait_ns, abort_flag, status);
                 if (!ok) break;
                 const int n_valid = min(16, n - i - slice * 16);  // keys of this warp
                 if (n_valid > 0) {
@@ -468,40 +472,37 @@ __global__ void __launch_bounds__(Cfg<D, kWide>::kThreads, 1)
                 }
             }
             consumer_sync<C::kWarps>();
+            // Lane l of every warp: the maximum and sum of head l % kRows over the
+            // warps, each of the 32 / kRows lanes of a head over some of them.
+            constexpr int kPer = C::kWarps * C::kRows / 32;
+            float2 theirs[kPer];
+            float top = -INFINITY, sum = 0.f;
+#pragma unroll
+            for (int k = 0; k < kPer; ++k) {
+                theirs[k] = state[lane + 32 * k];  // [warp][head] flat
+                top = fmaxf(top, theirs[k].x);
+            }
+#pragma unroll
+            for (int off = C::kRows; off < 32; off <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
+            const float ref = top == -INFINITY ? 0.f : top;
+#pragma unroll
+            for (int k = 0; k < kPer; ++k) sum += fast_exp2(theirs[k].x - ref) * theirs[k].y;
+#pragma unroll
+            for (int off = C::kRows; off < 32; off <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
+            const float over = sum == 0.f ? 0.f : 1.f / sum;  // NaN stays NaN
             float f[2];
 #pragma unroll
-            for (int r = 0; r < 2; ++r) {
-                const int h = kWide ? gq + 8 * r : 2 * tq + r;
-                float top = -INFINITY;
-#pragma unroll
-                for (int w = 0; w < C::kWarps; ++w) top = fmaxf(top, state[w * C::kRows + h].x);
-                f[r] = fast_exp2(st.m[r] - (top == -INFINITY ? 0.f : top));
-            }
+            for (int r = 0; r < 2; ++r) f[r] = fast_exp2(st.m[r] - __shfl_sync(0xffffffffu, ref, kWide ? gq + 8 * r : 2 * tq + r));
             const size_t part = (size_t)blockIdx.x + row;
             if (first_of_row && threadIdx.x == 0)
                 p.rows[row] = make_int2(int(part), 1 + int((unsigned(len - n) + share - 1) / share));
+            if (ok && warp == 0 && lane < p.G)
+                p.part_lse[part * p.G + lane] = sum == 0.f ? -INFINITY : top + __log2f(sum);
             // Warps 0..7 store head `warp` (and `warp` + 8).
             constexpr int kStores = C::kRows / 8;
             float inv[kStores];
-            if (warp < 8) {
 #pragma unroll
-                for (int k = 0; k < kStores; ++k) {
-                    const int h = warp + 8 * k;
-                    inv[k] = 0.f;
-                    if (h >= p.G) break;
-                    float top = -INFINITY, sum = 0.f;
-#pragma unroll
-                    for (int w = 0; w < C::kWarps; ++w) top = fmaxf(top, state[w * C::kRows + h].x);
-                    const float ref = top == -INFINITY ? 0.f : top;
-#pragma unroll
-                    for (int w = 0; w < C::kWarps; ++w) {
-                        const float2 x = state[w * C::kRows + h];
-                        sum += fast_exp2(x.x - ref) * x.y;
-                    }
-                    inv[k] = sum == 0.f ? 0.f : 1.f / sum;  // NaN stays NaN
-                    if (ok && lane == 0) p.part_lse[part * p.G + h] = sum == 0.f ? -INFINITY : top + __log2f(sum);
-                }
-            }
+            for (int k = 0; k < kStores; ++k) inv[k] = __shfl_sync(0xffffffffu, over, (warp + 8 * k) & 31);
 #pragma unroll
             for (int c0 = 0; c0 < D; c0 += C::kCols) {
                 float *mine = turn + warp * C::kRows * C::kStride;
@@ -559,10 +560,12 @@ __global__ void __launch_bounds__(Cfg<D, kWide>::kThreads, 1)
         // limit) for the copies of the last fill of every ring slot so that none
         // is still writing shared memory.
         volatile int no_abort = 0;
-        for (long long i = fills > C::kStages ? fills - C::kStages : 0; i < fills; ++i)
-            if (!mbar_wait_bounded(smem_u32(bars + i % C::kStages), (i / C::kStages) & 1, 1000000000ull, &no_abort,
-                                   status))
+        for (int s = 0; s < C::kStages; ++s) {
+            const int last = s < slot ? round : round - 1;  // round of this slot's last fill
+            if (last >= 0 &&
+                !mbar_wait_bounded(smem_u32(bars + s), last & 1, 1000000000ull, &no_abort, status))
                 atomicOr(status, kStatusDrainTimeout);
+        }
     }
 }
 
