@@ -112,6 +112,7 @@ SHAPES = [
     (8, 8, 8, 129, 100, 128), (9, 10, 2, 700, 33, 64), (5, 28, 4, 1000, 257, 128), (3, 48, 3, 300, 1200, 128),
     (8, 32, 2, 0, 3000, 64), (8, 64, 8, 2500, 513, 128), (30, 40, 8, 333, 70, 128), (130, 10, 2, 400, 40, 64),
     (260, 16, 1, 515, 20, 128), (300, 4, 4, 200, 9, 64), (70, 12, 1, 140, 200, 128), (1, 64, 8, 0, 8000, 128),
+    (2, 16, 2, 20000, 70, 64), (16, 64, 8, 6000, 90, 128), (3, 2, 1, 40001, 5, 128), (17, 8, 1, 25000, 300, 128),
 ]
 
 
