@@ -385,8 +385,11 @@ int launch_all(const DecodePrefixLaunch &a, cudaStream_t stream) {
 
 }  // namespace
 
-int own_ctas(int B, int Hkv, int P, int max_seqlen, int num_sms) {
-    const long long keys = (long long)B * Hkv * max_seqlen, most = (keys + own::kMinShare - 1) / own::kMinShare;
+int own_groups(int G) { return G > 8 ? 2 : 3; }
+
+int own_ctas(int B, int G, int Hkv, int P, int max_seqlen, int num_sms) {
+    const long long keys = (long long)B * Hkv * max_seqlen;
+    const long long cta = own::kMinShare * own_groups(G), most = (keys + cta - 1) / cta;
     const int sms = P > 0 && num_sms > 1 ? num_sms / 2 : num_sms;
     return int(most < sms ? most : sms);
 }
@@ -395,10 +398,10 @@ bool decode_prefix_layout(int B, int Hq, int Hkv, int P, int d, int max_seqlen, 
                           PrefixLayout *l) {
     auto up = [](size_t n) { return (n + 255) / 256 * 256; };
     const size_t rows = (size_t)B * Hq;
-    l->own_ctas = own_ctas(B, Hkv, P, max_seqlen, num_sms);
+    l->own_ctas = own_ctas(B, Hq / Hkv, Hkv, P, max_seqlen, num_sms);
     PrefixOrder po = {};
     if (P > 0 && !prefix_order(&po, B, Hq / Hkv, Hkv, P, d, l->own_ctas, num_sms)) return false;
-    const size_t parts = max_seqlen > 0 ? (size_t)l->own_ctas + (size_t)B * Hkv : 0;
+    const size_t parts = max_seqlen > 0 ? (size_t)l->own_ctas * own_groups(Hq / Hkv) + (size_t)B * Hkv : 0;
     const size_t pre = (size_t)po.ids * po.id_rows;
     if (parts > 0x7fffffff) return false;
     size_t at = 0;

@@ -2,34 +2,33 @@
 // prefix: one query row per query head, ragged lengths, softmax partials out.
 //
 // HBM-bound: 4 d bytes a key and KV head, each read once.  What keeps the
-// memory busy is that no CTA ever has less to do than another and that its ring
-// never runs dry, so the kernel is persistent and its share exact: with T keys
-// in all, numbered by (sequence, KV head, key), CTA c takes keys [c S, (c + 1) S),
-// S = ceil(T Hkv / CTAs) rounded up (find_share), however they fall on
-// the sequences; a share is cut into segments at the ends of the sequences' heads,
-// and the TMA warp runs ahead over those ends while the other warps finish a
-// segment.  (One CTA a chunk, as in the ragged decode: 81 us on 128 sequences of
-// 512 to 1024 keys, 8 KV heads, d = 128, and up to 255 us on 32 of 8K to 16K,
-// where 1.26 waves of equal chunks left SMs idle.)  The lengths are on the device;
-// every warp finds its place in them by itself, from registers for up to 256
-// sequences.
+// memory busy is that no part of the GPU ever has less to do than another and
+// that the rings never run dry, so the kernel is persistent and its shares are
+// exact.  An SM holds one CTA of two or three groups: four warps that compute, one
+// that issues TMA loads, a ring and barriers of their own.  With T keys in all,
+// numbered by (sequence, KV head, key), group c takes keys [c S, (c + 1) S), S =
+// ceil(T Hkv / groups) rounded up (find_share), however they fall on the sequences; a
+// share is cut into segments at the ends of the sequences' heads, the group's TMA
+// warp runs ahead over those ends while its other warps finish a segment, and the
+// SM's other groups are not held up by either.  (One CTA a chunk, as in the ragged
+// decode: 81 us on 128 sequences of 512 to 1024 keys, 8 KV heads, d = 128, and up to
+// 255 us on 32 of 8K to 16K, where 1.26 waves of equal chunks left SMs idle.)  The
+// lengths are on the device; every warp finds its place in them by itself, from
+// registers for up to 256 sequences.
 //
 // Segment partials are numbered c + (row b * Hkv + g): both numbers go up along
 // the shares and one of them at every cut, so the numbers are distinct, a row's
-// are consecutive, and there are at most CTAs + B * Hkv of them.
+// are consecutive, and there are at most groups + B * Hkv of them.
 //
 // A stage is 64 keys, 16 a warp.  Up to 8 query heads a KV head (kWide false) they
 // are the N dimension of m16n8k16 MMAs: S^T = K Q^T and O^T = V^T P^T, keys and
 // then columns of V on M, so that no row of an MMA is idle; P^T gets from the one
 // layout to the other by movmatrix.  9 to 16 heads are the M dimension as in
 // decode_sm103.cu.  Heads on N take half the MMAs and half the accumulator
-// registers, which lets three groups of four warps take turns with the stages
-// instead of two; a stage takes its warps about a thousand clocks, mostly latency,
-// and one CTA an SM has to draw HBM's full rate from half of the SMs, because the
-// prefix's kernel has the others.
-// A ring slot always belongs to the same group: a group that skipped a slot's
-// phase could take the phase after it for complete, since a barrier tells its
-// phases apart by parity alone.
+// registers, which lets three groups share an SM instead of two; a stage takes its
+// group about 1600 clocks, mostly latency, and one CTA an SM has to draw HBM's full
+// rate from half of the SMs, because the prefix's kernel has the others.  An SM
+// ingests at most about 45 bytes a clock.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -59,20 +58,19 @@ __device__ __forceinline__ uint32_t transpose_8x8(uint32_t in) {
 template <int D, bool kWide>
 struct Cfg {
     static constexpr int kGroups = kWide ? 2 : 3, kWarps = kGroups * kConsumerWarps;  // consumer warps
-    static constexpr int kThreads = (kWarps + 1) * 32;
-    static constexpr int kStages = D == 128 ? 6 : 12;
-    static_assert(kStages % kGroups == 0, "a slot belongs to one group");
+    static constexpr int kThreads = (kWarps + kGroups) * 32;
+    static constexpr int kStages = (D == 128 ? 6 : 12) / kGroups;  // of a group's ring
     static constexpr int kChunks = D / 64;
     static constexpr int kChunkBytes = kKeysPerStage * 128;
     static constexpr int kTileBytes = kKeysPerStage * D * 2;
     static constexpr int kStageBytes = 2 * kTileBytes;
-    static constexpr int kRingBytes = kStages * kStageBytes;
+    static constexpr int kRingBytes = kGroups * kStages * kStageBytes;
     // Combine area of a consumer warp: kRows heads of kCols columns, kStride
     // words apart (no bank conflicts on the way in), and (maximum, sum) a head.
     static constexpr int kRows = kWide ? 16 : 8, kCols = kWide ? 32 : 64, kStride = kWide ? 40 : 68;
     static constexpr int kTurnBytes = kWarps * kRows * kStride * 4;
     static constexpr int kStateBytes = kWarps * kRows * 8;
-    static constexpr int kSmemBytes = kRingBytes + kTurnBytes + kStateBytes + 2 * kStages * 8 + 16 + 1024;
+    static constexpr int kSmemBytes = kRingBytes + kTurnBytes + kStateBytes + kGroups * 2 * kStages * 8 + 16 + 1024;
     static_assert(kSmemBytes <= 227 * 1024, "shared memory");
 };
 
@@ -99,7 +97,7 @@ __device__ __forceinline__ void load_lengths(const Params &p, int first, int (&l
     }
 }
 
-// Where CTA `cta` of `ctas` starts (left = 0: it has no share).  All lanes of
+// Where group `cta` of `ctas` starts (left = 0: it has no share).  All lanes of
 // the calling warp; `write`: also write the plan down.  Int: wide enough for the
 // number of keys, so that the common case scans and divides in 32 bits.
 // `len` holds load_lengths(0), which the caller has had time to wait for.
@@ -157,9 +155,9 @@ __device__ __forceinline__ Place find_share(const Params &p, int (&len)[kRound],
     return at;
 }
 
-template <int kWarps>
-__device__ __forceinline__ void consumer_sync() {
-    asm volatile("bar.sync 1, %0;" ::"n"(kWarps * 32) : "memory");
+// Among the four computing warps of a group.
+__device__ __forceinline__ void group_sync(int group) {
+    asm volatile("bar.sync %0, %1;" ::"r"(1 + group), "n"(kConsumerWarps * 32) : "memory");
 }
 
 // One segment's running state in a consumer warp: the maxima and (per lane) sums
@@ -347,21 +345,30 @@ __global__ void __launch_bounds__(Cfg<D, kWide>::kThreads, 1)
     using C = Cfg<D, kWide>;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    float *turn = reinterpret_cast<float *>(smem + C::kRingBytes);                     // [warp][kRows][kStride]
-    float2 *state = reinterpret_cast<float2 *>(smem + C::kRingBytes + C::kTurnBytes);  // [warp][kRows]
-    uint64_t *bars = reinterpret_cast<uint64_t *>(smem + C::kRingBytes + C::kTurnBytes + C::kStateBytes);
-    volatile int *abort_flag = reinterpret_cast<volatile int *>(bars + 2 * C::kStages);
+    float *turns = reinterpret_cast<float *>(smem + C::kRingBytes);                     // [group][warp][kRows][kStride]
+    float2 *states = reinterpret_cast<float2 *>(smem + C::kRingBytes + C::kTurnBytes);  // [group][warp][kRows]
+    uint64_t *barriers = reinterpret_cast<uint64_t *>(smem + C::kRingBytes + C::kTurnBytes + C::kStateBytes);
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(barriers + C::kGroups * 2 * C::kStages);
     int *status = &g_own_status;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    // Computing warps first, then a TMA warp for every group.
+    const bool loads = warp >= C::kWarps;
+    const int group = loads ? warp - C::kWarps : warp / kConsumerWarps, slice = warp % kConsumerWarps;
+    const int part0 = blockIdx.x * C::kGroups + group;  // the group's number in the grid
+    uint8_t *ring = smem + group * C::kStages * C::kStageBytes;
+    uint64_t *bars = barriers + group * 2 * C::kStages;  // full, then empty
+    float *turn = turns + group * kConsumerWarps * C::kRows * C::kStride;
+    float2 *state = states + group * kConsumerWarps * C::kRows;
 
     griddep_launch_dependents();  // the prefix's grid, which reads nothing from here, may take the other SMs
     int lengths[kRound];
     load_lengths(p, 0, lengths);
     if (threadIdx.x == 0) {
-        for (int s = 0; s < C::kStages; ++s) {
-            mbar_init(smem_u32(bars + s), 1);                            // full
-            mbar_init(smem_u32(bars + C::kStages + s), kConsumerWarps);  // empty: the group that used it
-        }
+        for (int g = 0; g < C::kGroups; ++g)
+            for (int s = 0; s < C::kStages; ++s) {
+                mbar_init(smem_u32(barriers + (2 * g) * C::kStages + s), 1);                   // full
+                mbar_init(smem_u32(barriers + (2 * g + 1) * C::kStages + s), kConsumerWarps);  // empty
+            }
         *abort_flag = 0;
         fence_mbar_init();
     }
@@ -370,16 +377,16 @@ __global__ void __launch_bounds__(Cfg<D, kWide>::kThreads, 1)
         tma_prefetch_desc(&tmV);
     }
     const bool write = blockIdx.x == 0 && warp == 0;
-    // (CTAs + 1) shares stay below 2^31 where the caches' keys stay below 2^29.
-    Place at = p.narrow ? find_share<unsigned>(p, lengths, blockIdx.x, gridDim.x, write)
-                        : find_share<long long>(p, lengths, blockIdx.x, gridDim.x, write);
+    // (groups + 1) shares stay below 2^31 where the caches' keys stay below 2^29.
+    Place at = p.narrow ? find_share<unsigned>(p, lengths, part0, gridDim.x * C::kGroups, write)
+                        : find_share<long long>(p, lengths, part0, gridDim.x * C::kGroups, write);
     __syncthreads();
-    if (at.left == 0) return;
+    if (at.left == 0) return;  // whole warps; nothing below waits for all of the CTA
 
     // Share, where a row can go on behind it (a longer one holds every row's rest; the last may be shorter).
     const unsigned share = unsigned(min(at.left, 0x40000000LL));
     int slot = 0, round = 0;  // of the ring's next stage to issue (producer) or use (consumers)
-    if (warp == C::kWarps) {
+    if (loads) {
         // ------------------------------------------------------------ producer
         if (lane == 0) {
             bool ok = true;
@@ -390,7 +397,7 @@ __global__ void __launch_bounds__(Cfg<D, kWide>::kThreads, 1)
                     ok = round == 0 || mbar_wait_bounded(smem_u32(bars + C::kStages + s), (round - 1) & 1, p.wait_ns,
                                                          abort_flag, status);
                     if (!ok) break;
-                    const uint32_t fb = smem_u32(bars + s), kt = smem_u32(smem + s * C::kStageBytes);
+                    const uint32_t fb = smem_u32(bars + s), kt = smem_u32(ring + s * C::kStageBytes);
                     const int key = at.j + i;
                     if (n - i >= kKeysPerStage) {
                         mbar_arrive_expect_tx(fb, C::kStageBytes);
@@ -418,13 +425,22 @@ __global__ void __launch_bounds__(Cfg<D, kWide>::kThreads, 1)
                 if (at.left == 0) break;
                 at.next(p.seqlens, p.max_seqlen, p.Hkv);
             }
+            // Whatever becomes of the other warps, this one leaves only when the
+            // last fill of every slot has landed (bounded, by a second at least), so
+            // that no copy writes shared memory when the CTA is gone.
+            volatile int no_abort = 0;
+            const uint64_t limit = p.wait_ns > 1000000000ull ? p.wait_ns : 1000000000ull;
+            for (int s = 0; s < C::kStages; ++s) {
+                const int last = s < slot ? round : round - 1;  // round of this slot's last fill
+                if (last >= 0 && !mbar_wait_bounded(smem_u32(bars + s), last & 1, limit, &no_abort, status))
+                    atomicOr(status, kStatusDrainTimeout);
+            }
         }
     } else {
         // ------------------------------------------------------------ consumer
         // A warp whose wait ran out does no more work but still meets the others
         // at every barrier of the segments ahead.
         const int gq = lane >> 2, tq = lane & 3;
-        const int group = warp / kConsumerWarps, slice = warp % kConsumerWarps;  // of the stages; of a stage's keys
         bool ok = true;
         Queries<D, kWide> q;
         q.load(p, at.b * p.Hkv + at.g);
@@ -437,12 +453,11 @@ __global__ void __launch_bounds__(Cfg<D, kWide>::kThreads, 1)
             for (int i = 0; ok && i < n; i += kKeysPerStage) {
                 const int s = slot, phase = round & 1;
                 if (++slot == C::kStages) slot = 0, ++round;
-                if (s % C::kGroups != group) continue;
                 ok = mbar_wait_warp(smem_u32(bars + s), phase, p.wait_ns, abort_flag, status);
                 if (!ok) break;
                 const int n_valid = min(16, n - i - slice * 16);  // keys of this warp
                 if (n_valid > 0) {
-                    const uint32_t kt = smem_u32(smem + s * C::kStageBytes);
+                    const uint32_t kt = smem_u32(ring + s * C::kStageBytes);
                     add_keys<D>(st, q, kt, kt + C::kTileBytes, slice * 16, n_valid, p.scale_log2, p.G,
                                 scores ? scores + (size_t)i * p.G : nullptr);
                 }
@@ -464,17 +479,17 @@ __global__ void __launch_bounds__(Cfg<D, kWide>::kThreads, 1)
                 if constexpr (kWide) {
                     l += __shfl_xor_sync(0xffffffffu, l, 1);
                     l += __shfl_xor_sync(0xffffffffu, l, 2);
-                    if (tq == 0) state[warp * C::kRows + gq + 8 * r] = make_float2(st.m[r], l);
+                    if (tq == 0) state[slice * C::kRows + gq + 8 * r] = make_float2(st.m[r], l);
                 } else {
 #pragma unroll
                     for (int off = 4; off < 32; off <<= 1) l += __shfl_xor_sync(0xffffffffu, l, off);
-                    if (gq == 0) state[warp * C::kRows + 2 * tq + r] = make_float2(st.m[r], l);
+                    if (gq == 0) state[slice * C::kRows + 2 * tq + r] = make_float2(st.m[r], l);
                 }
             }
-            consumer_sync<C::kWarps>();
+            group_sync(group);
             // Lane l of every warp: the maximum and sum of head l % kRows over the
             // warps, each of the 32 / kRows lanes of a head over some of them.
-            constexpr int kPer = C::kWarps * C::kRows / 32;
+            constexpr int kPer = kConsumerWarps * C::kRows / 32;
             float2 theirs[kPer];
             float top = -INFINITY, sum = 0.f;
 #pragma unroll
@@ -493,19 +508,19 @@ __global__ void __launch_bounds__(Cfg<D, kWide>::kThreads, 1)
             float f[2];
 #pragma unroll
             for (int r = 0; r < 2; ++r) f[r] = fast_exp2(st.m[r] - __shfl_sync(0xffffffffu, ref, kWide ? gq + 8 * r : 2 * tq + r));
-            const size_t part = (size_t)blockIdx.x + row;
-            if (first_of_row && threadIdx.x == 0)
+            const size_t part = (size_t)part0 + row;
+            if (first_of_row && slice == 0 && lane == 0)
                 p.rows[row] = make_int2(int(part), 1 + int((unsigned(len - n) + share - 1) / share));
-            if (ok && warp == 0 && lane < p.G)
+            if (ok && slice == 0 && lane < p.G)
                 p.part_lse[part * p.G + lane] = sum == 0.f ? -INFINITY : top + __log2f(sum);
-            // Warps 0..7 store head `warp` (and `warp` + 8).
-            constexpr int kStores = C::kRows / 8;
+            // A warp stores heads `slice`, `slice` + 4, ...
+            constexpr int kStores = C::kRows / kConsumerWarps;
             float inv[kStores];
 #pragma unroll
-            for (int k = 0; k < kStores; ++k) inv[k] = __shfl_sync(0xffffffffu, over, (warp + 8 * k) & 31);
+            for (int k = 0; k < kStores; ++k) inv[k] = __shfl_sync(0xffffffffu, over, slice + kConsumerWarps * k);
 #pragma unroll
             for (int c0 = 0; c0 < D; c0 += C::kCols) {
-                float *mine = turn + warp * C::kRows * C::kStride;
+                float *mine = turn + slice * C::kRows * C::kStride;
                 if constexpr (kWide) {
 #pragma unroll
                     for (int u = 0; u < C::kCols / 8; ++u) {
@@ -525,46 +540,31 @@ __global__ void __launch_bounds__(Cfg<D, kWide>::kThreads, 1)
                         to[C::kStride + 8] = a[3] * f[1];
                     }
                 }
-                consumer_sync<C::kWarps>();
-                if (warp < 8) {
+                group_sync(group);
 #pragma unroll
-                    for (int k = 0; k < kStores; ++k) {
-                        const int h = warp + 8 * k;
-                        if (h >= p.G) break;
-                        float *to = p.part_o + (part * p.G + h) * D + c0;
-                        if constexpr (kWide) {
-                            float v = 0.f;
+                for (int k = 0; k < kStores; ++k) {
+                    const int h = slice + kConsumerWarps * k;
+                    if (h >= p.G) break;
+                    float *to = p.part_o + (part * p.G + h) * D + c0;
+                    if constexpr (kWide) {
+                        float v = 0.f;
 #pragma unroll
-                            for (int w = 0; w < C::kWarps; ++w) v += turn[(w * C::kRows + h) * C::kStride + lane];
-                            if (ok) to[lane] = v * inv[k];
-                        } else {
-                            float2 v = make_float2(0.f, 0.f);
+                        for (int w = 0; w < kConsumerWarps; ++w) v += turn[(w * C::kRows + h) * C::kStride + lane];
+                        if (ok) to[lane] = v * inv[k];
+                    } else {
+                        float2 v = make_float2(0.f, 0.f);
 #pragma unroll
-                            for (int w = 0; w < C::kWarps; ++w) {
-                                const float2 x = *reinterpret_cast<const float2 *>(turn + (w * C::kRows + h) * C::kStride + 2 * lane);
-                                v.x += x.x;
-                                v.y += x.y;
-                            }
-                            if (ok) *reinterpret_cast<float2 *>(to + 2 * lane) = make_float2(v.x * inv[k], v.y * inv[k]);
+                        for (int w = 0; w < kConsumerWarps; ++w) {
+                            const float2 x = *reinterpret_cast<const float2 *>(turn + (w * C::kRows + h) * C::kStride + 2 * lane);
+                            v.x += x.x;
+                            v.y += x.y;
                         }
+                        if (ok) *reinterpret_cast<float2 *>(to + 2 * lane) = make_float2(v.x * inv[k], v.y * inv[k]);
                     }
                 }
-                consumer_sync<C::kWarps>();
+                group_sync(group);
             }
             if (at.left == 0) break;
-        }
-    }
-    __syncthreads();
-    if (*abort_flag && warp == C::kWarps && lane == 0) {
-        // A wait ran out.  Before the CTA exits, wait (bounded, with a fixed
-        // limit) for the copies of the last fill of every ring slot so that none
-        // is still writing shared memory.
-        volatile int no_abort = 0;
-        for (int s = 0; s < C::kStages; ++s) {
-            const int last = s < slot ? round : round - 1;  // round of this slot's last fill
-            if (last >= 0 &&
-                !mbar_wait_bounded(smem_u32(bars + s), last & 1, 1000000000ull, &no_abort, status))
-                atomicOr(status, kStatusDrainTimeout);
         }
     }
 }
