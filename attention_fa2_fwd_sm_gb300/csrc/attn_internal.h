@@ -184,9 +184,9 @@ struct DecodePrefixLaunch {
     unsigned long long wait_ns;
     int num_sms;
 };
-// CTAs (one an SM) of the own keys' kernel, half of the SMs beside a prefix, and
-// the groups of a CTA, which have a share each.
-int own_ctas(int B, int G, int Hkv, int P, int max_seqlen, int num_sms);
+// CTAs (one an SM) of the own keys' kernel, and the groups of a CTA, which have a
+// share each.
+int own_ctas(int B, int G, int Hkv, int P, int d, int max_seqlen, int num_sms);
 int own_groups(int G);
 // False when the sizes are outside what the launches can count.
 bool decode_prefix_layout(int B, int Hq, int Hkv, int P, int d, int max_seqlen, bool weights, int num_sms,

@@ -15,7 +15,7 @@
 //      key blocks as in prefix_order.cuh.
 //   2. Own keys: own_kernel<D> (own_keys.cuh), HBM-bound; with weights it also
 //      writes the scores (4 G bytes a key beside 4 d read).
-//      It is launched first, on half of the SMs, and the prefix's kernel
+//      It is launched first, on some of the SMs, and the prefix's kernel
 //      programmatically behind it, so that both run at once: the one waits for
 //      memory, the other for the tensor cores.
 //   3. Merge: the partials of every row.
@@ -387,18 +387,19 @@ int launch_all(const DecodePrefixLaunch &a, cudaStream_t stream) {
 
 int own_groups(int G) { return G > 8 ? 2 : 3; }
 
-int own_ctas(int B, int G, int Hkv, int P, int max_seqlen, int num_sms) {
+int own_ctas(int B, int G, int Hkv, int P, int d, int max_seqlen, int num_sms) {
+    if (max_seqlen <= 0) return 0;
     const long long keys = (long long)B * Hkv * max_seqlen;
-    const long long cta = own::kMinShare * own_groups(G), most = (keys + cta - 1) / cta;
-    const int sms = P > 0 && num_sms > 1 ? num_sms / 2 : num_sms;
-    return int(most < sms ? most : sms);
+    const long long cta = own::kMinShare * own_groups(G), ctas = (keys + cta - 1) / cta;
+    const int most = int(ctas < num_sms ? ctas : num_sms);
+    return P > 0 ? prefix_own_sms(B, G, Hkv, P, d, max_seqlen, most, num_sms) : most;
 }
 
 bool decode_prefix_layout(int B, int Hq, int Hkv, int P, int d, int max_seqlen, bool weights, int num_sms,
                           PrefixLayout *l) {
     auto up = [](size_t n) { return (n + 255) / 256 * 256; };
     const size_t rows = (size_t)B * Hq;
-    l->own_ctas = own_ctas(B, Hq / Hkv, Hkv, P, max_seqlen, num_sms);
+    l->own_ctas = own_ctas(B, Hq / Hkv, Hkv, P, d, max_seqlen, num_sms);
     PrefixOrder po = {};
     if (P > 0 && !prefix_order(&po, B, Hq / Hkv, Hkv, P, d, l->own_ctas, num_sms)) return false;
     const size_t parts = max_seqlen > 0 ? (size_t)l->own_ctas * own_groups(Hq / Hkv) + (size_t)B * Hkv : 0;

@@ -27,8 +27,8 @@
 // decode_sm103.cu.  Heads on N take half the MMAs and half the accumulator
 // registers, which lets three groups share an SM instead of two; a stage takes its
 // group about 1600 clocks, mostly latency, and one CTA an SM has to draw HBM's full
-// rate from half of the SMs, because the prefix's kernel has the others.  An SM
-// ingests at most about 45 bytes a clock.
+// rate from part of the SMs (about 100 GB/s each), because the prefix's kernel has
+// the others.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 

@@ -15,9 +15,8 @@
 //
 // The prefix is bound by the tensor cores, the sequences' own keys by HBM, so
 // the two run at the same time on different SMs: the own keys' kernel, ahead on
-// the stream, holds `own` SMs (half of them already draw HBM's full rate), the
-// first `early` shares start at once on the others, and the `late` ones wait for
-// its SMs.  So that all end together, a late share is shorter by what the own
+// the stream, holds `own` SMs (prefix_own_sms), the first `early` shares start at
+// once on the others, and the `late` ones wait for its SMs.  So that all end together, a late share is shorter by what the own
 // keys take, tau key blocks' worth of time, estimated from their number T:
 //     early a + late b = total,  b = a - tau  (b = 0 where a <= tau).
 // The shares depend on the lengths alone, so results do not depend on timing.
@@ -70,8 +69,8 @@ ATTN_HD int prefix_row(const PrefixOrder &o, int g, int m) { return o.lockstep ?
 // T: own keys over all KV heads.
 ATTN_HD PrefixShares prefix_shares(const PrefixOrder &o, long long T) {
     const unsigned e = unsigned(o.early), l = unsigned(o.late);
-    // (own_cost is below 2^18, and no memory holds 2^44 keys)
-    const unsigned long long wide = (unsigned long long)(T < (1LL << 44) ? T : (1LL << 44)) * o.own_cost >> 32;
+    // (no memory holds 2^38 keys, and own_cost is below 2^26)
+    const unsigned long long wide = (unsigned long long)(T < (1LL << 38) ? T : (1LL << 38)) * o.own_cost >> 32;
     const unsigned tau = wide < (1u << 30) ? unsigned(wide) : (1u << 30);
     PrefixShares s;
     s.a = (o.total + e - 1) / e;
@@ -112,14 +111,31 @@ ATTN_HD PrefixSegment prefix_segment(const PrefixOrder &o, unsigned hi, int cta,
     return s;
 }
 
-// Measured: one key block of a unit takes about 1.5 us with two tiles and 1.05
-// us with one (d = 128; 1.3 and 0.9 at d = 64), and half of the SMs draw the own
-// keys at 4 TB/s in segments of some hundred keys (5.5 TB/s in long ones).  At
-// 6.4 TB/s here, 128 x (32K shared + 512 .. 1024 own) keys took 173 us, at 4 TB/s
-// 163, one phase after the other 176; 32 x (8K + 256 .. 512) 54, 42 and 46 us.
-inline unsigned prefix_own_cost(int d, bool two_tiles) {
-    const double block_us = d == 128 ? (two_tiles ? 1.5 : 1.05) : (two_tiles ? 1.3 : 0.9);
-    return unsigned(4.0 * d / 4.0e6 / block_us * 4294967296.0);
+// Measured rates.  A unit's key block takes this many microseconds, with two tiles
+// and with one:
+inline double prefix_block_us(int d, bool two_tiles) { return d == 128 ? (two_tiles ? 1.55 : 1.2) : (two_tiles ? 1.37 : 1.0); }
+// The own keys' kernel draws this many bytes a microsecond on `own` SMs (segments
+// of 768 keys; 20% more in long ones), up to what HBM gives.
+inline double prefix_own_rate(int d, int G, int own) {
+    const double sm = (d == 128 ? (G > 8 ? 52.0 : 100.0) : (G > 8 ? 38.0 : 80.0)) * 1e3;
+    return own * sm < 6.0e6 ? own * sm : 6.0e6;
+}
+
+// SMs for the own keys' kernel beside a prefix, `most` at most: in proportion to
+// what the two have to do if the caches are three quarters full, so that in the
+// usual case no share has to wait, and leaving whole groups of mt.  128 x (32K
+// shared + 512 .. 1024 own) keys: 24 SMs 190 us, 32 153, 40 139, 48 149, 64 174 (with
+// the shares' balance; the two phases one after the other 176).
+inline int prefix_own_sms(int B, int G, int Hkv, int P, int d, int max_seqlen, int most, int num_sms) {
+    const int rb = kPrefixTileRows / G, tiles = (B + rb - 1) / rb, mt = (tiles + 1) / 2;
+    const double own = 0.75 * B * Hkv * (double)max_seqlen * 4 * d / prefix_own_rate(d, G, 1);
+    const double prefix = (double)Hkv * mt * ((P + kPrefixBlock - 1) / kPrefixBlock) * prefix_block_us(d, tiles > 1);
+    int left = int(num_sms * (prefix / (own + prefix)) + 0.5);  // SMs that the prefix starts on
+    left = mt < num_sms ? (left + mt / 2) / mt * mt : left;
+    if (left < (mt < num_sms ? mt : 1)) left = mt < num_sms ? mt : 1;
+    int sms = num_sms - left;
+    if (sms < 1) sms = 1;
+    return sms < most ? sms : most;
 }
 
 // `own`: SMs that the own keys' kernel holds (0: none).  False when the problem
@@ -143,7 +159,7 @@ inline bool prefix_order(PrefixOrder *o, int B, int G, int Hkv, int P, int d, in
     o->unit_rows = 2 * o->rb * G;
     o->id_rows = o->unit_rows * (o->lockstep ? o->mt : 1);
     o->ids = o->early + o->late + o->rows;
-    o->own_cost = prefix_own_cost(d, tiles > 1);
+    o->own_cost = own > 0 ? unsigned(4.0 * d / prefix_own_rate(d, G, own) / prefix_block_us(d, tiles > 1) * 4294967296.0) : 0u;
     return true;
 }
 

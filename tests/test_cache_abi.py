@@ -168,16 +168,20 @@ def test_prefix_segments_cover_every_block_once(B, Hq, Hkv, P, d, S, keys, sms):
 
 
 def test_prefix_shares_leave_room_for_the_own_keys():
-    """The more own keys, the less falls to the CTAs that start behind them."""
-    late = []
+    """The more own keys, the less falls to the CTAs that start behind them; all CTAs at or above some number start behind them."""
+    loads = []
     for own in (0, 20000, 60000, 100000, 10 ** 7):
-        n = 0
-        for cta in range(76, 152):
-            i = 0
+        load = []
+        for cta in range(152):
+            n = i = 0
             while (s := attn.attn_decode_prefix_segment(128, 64, 8, 32768, 128, 1024, own, 152, cta, i)) is not None:
                 n, i = n + s[3], i + 1
-        late.append(n)
-    assert late == sorted(late, reverse=True) and late[0] > late[2] > 0 and late[-1] == 0
+            load.append(n)
+        loads.append(load)
+    late = [sum(x[120:]) for x in loads]
+    assert late == sorted(late, reverse=True) and late[0] > late[1] > 0 and late[-1] == 0
+    assert len({n for n in loads[0][:148]}) == 1  # nothing own: equal shares (the last one takes the rest)
+    assert all(sum(x) == 4 * 8 * 256 for x in loads)
 
 
 def test_prefix_segment_refusals():
