@@ -37,7 +37,6 @@ namespace attn {
 namespace {
 
 constexpr int kMergeThreads = 128, kWeightThreads = 256;
-constexpr int kWideWarps = 16;  // of one row, where there are few
 constexpr int kWeightCtasPerSm = 8;
 constexpr int kMinWeightKeys = 256;  // of one CTA
 
@@ -69,24 +68,40 @@ struct RowParts {
     }
 };
 
-__device__ __forceinline__ RowParts row_parts(const MergeParams &p, int b, int h) {
-    RowParts r = {};
-    const int g = h / p.G, j = h - g * p.G;
-    int2 pre = make_int2(0, 0), own = pre;
+// Where to find the two, from the indices alone.
+struct RowPlace {
+    int b, j, pre_row, own_row;
+    size_t pre;
+};
+
+__device__ __forceinline__ RowPlace row_place(const MergeParams &p, int row) {
+    RowPlace r;
+    r.b = row / p.Hq;
+    const int h = row - r.b * p.Hq, g = h / p.G;
+    r.j = h - g * p.G;
+    r.own_row = r.b * p.Hkv + g;
+    r.pre = r.pre_row = 0;
     if (p.pre_rows) {
-        const int tile = b / p.po.rb, m = tile / 2;
-        pre = p.pre_rows[prefix_row(p.po, g, m)];
-        r.pre_stride = p.po.id_rows;
+        const int m = r.b / p.po.rb / 2;
+        r.pre_row = prefix_row(p.po, g, m);
         // In lockstep the units of a partial number lie one behind the other.
-        r.pre = (size_t)(b - (p.po.lockstep ? 0 : 2 * m * p.po.rb)) * p.G + j;
+        r.pre = (size_t)(r.b - (p.po.lockstep ? 0 : 2 * m * p.po.rb)) * p.G + r.j;
     }
+    return r;
+}
+
+__device__ __forceinline__ RowParts row_parts(const MergeParams &p, const RowPlace &at) {
+    RowParts r = {};
+    int2 pre = make_int2(0, 0), own = pre;
+    if (p.pre_rows) pre = p.pre_rows[at.pre_row];
     if (p.own_rows) {
-        own = p.own_rows[b * p.Hkv + g];  // not written for a sequence without keys
-        if (p.seqlens[b] <= 0) own = make_int2(0, 0);
-        r.own_stride = p.G;
+        own = p.own_rows[at.own_row];  // not written for a sequence without keys
+        if (p.seqlens[at.b] <= 0) own = make_int2(0, 0);
     }
-    r.pre += (size_t)pre.x * p.po.id_rows;
-    r.own = (size_t)own.x * p.G + j;
+    r.pre_stride = p.po.id_rows;
+    r.own_stride = p.G;
+    r.pre = at.pre + (size_t)pre.x * p.po.id_rows;
+    r.own = (size_t)own.x * p.G + at.j;
     r.n_pre = pre.y;
     r.n = pre.y + own.y;
     return r;
@@ -125,23 +140,22 @@ __device__ __forceinline__ Cols<kCols> load_cols(const float *p) {
     return c;
 }
 
-// A row (b, h) by kWarps warps of a CTA.  A row's chain is what bounds the merge: its counts, then its partials' L, then
-// their outputs.  The outputs do not depend on the L's, so the first eight of
-// each warp are loaded before L is known.  One warp a row when there are rows
-// enough to fill the GPU with; four take turns of eight partials when not.
-template <int D, int kWarps>
+// A row (b, h) by kWarps warps of a CTA.  A row's chain is what bounds the merge:
+// its counts, then its partials' L, then their outputs.  The outputs do not depend
+// on the L's, so the first kAhead of each warp are loaded before L is known, and
+// what follows from the indices alone is done before the wait.
+template <int D, int kWarps, int kAhead>
 __global__ void __launch_bounds__(kWarps > 1 ? kWarps * 32 : kMergeThreads) merge_kernel(const MergeParams p) {
     constexpr int kCols = D / 32;  // columns of a lane
-    constexpr int kAhead = 8;
     __shared__ float acc_sh[kWarps][D];
-    griddep_wait();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int rows = p.B * p.Hq;
     constexpr int kRows = kWarps > 1 ? 1 : kMergeThreads / 32;
     const int row = blockIdx.x * kRows + warp / kWarps, q = warp % kWarps;
-    if (row >= rows) return;  // with kWarps > 1 a CTA is one row
-    const int b = row / p.Hq, h = row - b * p.Hq;
-    const RowParts r = row_parts(p, b, h);
+    if (row >= rows) return;  // with kWarps > 1 a CTA is one row (no thread of it leaves)
+    const RowPlace at = row_place(p, row);
+    griddep_wait();
+    const RowParts r = row_parts(p, at);
     auto part = [&](int i) { return (i < r.n_pre ? p.pre_o : p.own_o) + r.row(i) * D + lane * kCols; };
     auto lse = [&](int i) { return (i < r.n_pre ? p.pre_lse : p.own_lse)[r.row(i)]; };
     Cols<kCols> v[kAhead];
@@ -356,11 +370,15 @@ int launch_all(const DecodePrefixLaunch &a, cudaStream_t stream) {
     m.Hq = a.Hq;
     m.Hkv = a.Hkv;
     m.G = G;
-    // A warp a row where the rows fill the SMs; few rows get more warps, and the
-    // fewest, whose partials can be many, sixteen.
+    // Warps a row by what the rows leave of an SM's.  Whole calls, in us, by warps a
+    // row (1, 2, 4, 16): 8192 rows 88, 91, 95, 141; 2048 rows with some 12 partials
+    // 37, 36, 38, 49; 512 rows 18, 17, 16, 19; 64 rows with 57 partials 30, 22, 17, 12.
     const long long rows = (long long)a.B * a.Hq;
-    const int warps = rows >= 8LL * a.num_sms ? 1 : (rows >= a.num_sms ? 4 : kWideWarps);
-    auto merge = warps == 1 ? merge_kernel<D, 1> : (warps == 4 ? merge_kernel<D, 4> : merge_kernel<D, kWideWarps>);
+    const int warps = rows >= 24LL * a.num_sms ? 1 : rows >= 8LL * a.num_sms ? 2 : rows >= a.num_sms ? 4 : 16;
+    auto merge = warps == 1   ? merge_kernel<D, 1, 8>
+                 : warps == 2 ? merge_kernel<D, 2, 4>
+                 : warps == 4 ? merge_kernel<D, 4, 4>
+                              : merge_kernel<D, 16, 4>;
     const int per_cta = warps == 1 ? kMergeThreads / 32 : 1;
     cudaError_t e = dec::launch_programmatic(merge, dim3(unsigned((rows + per_cta - 1) / per_cta)),
                                              dim3(warps == 1 ? kMergeThreads : warps * 32), 0, stream, m);

@@ -20,6 +20,9 @@
 // keys take, tau key blocks' worth of time, estimated from their number T:
 //     early a + late b = total,  b = a - tau  (b = 0 where a <= tau).
 // The shares depend on the lengths alone, so results do not depend on timing.
+// Where nothing is left for the late ones and it makes no share much longer, every
+// row gets a whole number of shares (`aligned` of them): a share that goes on in
+// the next row pays for a second start and end.
 //
 // A CTA's share is one segment per row that it touches; each segment writes one
 // partial per query row, numbered share + row (both go up along the shares, one
@@ -52,9 +55,9 @@ struct PrefixOrder {
     unsigned own_cost;  // key blocks' worth of time of one own key and KV head, in 2^-32
 };
 
-// Lengths of the early and the late shares.
+// Lengths of the early and the late shares; aligned: shares per row, or 0.
 struct PrefixShares {
-    unsigned a, b;
+    unsigned a, b, aligned;
 };
 
 // One piece of work: key blocks [j0, j0 + n) of unit m of KV head g.
@@ -79,17 +82,31 @@ ATTN_HD PrefixShares prefix_shares(const PrefixOrder &o, long long T) {
         s.a = unsigned((o.total + (unsigned long long)l * tau + e + l - 1) / (e + l));
         s.b = e * s.a >= o.total ? 0 : (o.total - e * s.a + l - 1) / l;
     }
+    s.aligned = 0;
+    const unsigned rows = unsigned(o.rows), nblk = unsigned(o.nblk);
+    if (s.b == 0 && e >= rows) {
+        const unsigned a = (nblk + e / rows - 1) / (e / rows);
+        if (a <= s.a + s.a / 8) {
+            s.a = a;
+            s.aligned = (nblk + a - 1) / a;
+        }
+    }
     return s;
 }
 
 // First key block of a share in the order's space; a share may be empty.
 ATTN_HD unsigned prefix_begin(const PrefixOrder &o, const PrefixShares &s, int share) {
     const unsigned x = unsigned(share), e = unsigned(o.early);
+    if (s.aligned) {
+        const unsigned row = x / s.aligned, in = (x - row * s.aligned) * s.a;
+        return row < unsigned(o.rows) ? row * unsigned(o.nblk) + in : o.total;
+    }
     const unsigned at = x <= e ? x * s.a : e * s.a + (x - e) * s.b;
     return at < o.total ? at : o.total;
 }
 // The share that holds key block x.
 ATTN_HD int prefix_holder(const PrefixOrder &o, const PrefixShares &s, unsigned x) {
+    if (s.aligned) return int(x / unsigned(o.nblk) * s.aligned + x % unsigned(o.nblk) / s.a);
     const unsigned early = unsigned(o.early) * s.a;
     return int(x < early ? x / s.a : unsigned(o.early) + (x - early) / s.b);
 }
@@ -115,9 +132,9 @@ ATTN_HD PrefixSegment prefix_segment(const PrefixOrder &o, unsigned hi, int cta,
 // and with one:
 inline double prefix_block_us(int d, bool two_tiles) { return d == 128 ? (two_tiles ? 1.55 : 1.2) : (two_tiles ? 1.37 : 1.0); }
 // The own keys' kernel draws this many bytes a microsecond on `own` SMs (segments
-// of 768 keys; 20% more in long ones), up to what HBM gives.
+// of 768 keys; a third more in long ones), up to what HBM gives.
 inline double prefix_own_rate(int d, int G, int own) {
-    const double sm = (d == 128 ? (G > 8 ? 52.0 : 100.0) : (G > 8 ? 38.0 : 80.0)) * 1e3;
+    const double sm = (d == 128 ? (G > 8 ? 52.0 : 90.0) : (G > 8 ? 38.0 : 75.0)) * 1e3;
     return own * sm < 6.0e6 ? own * sm : 6.0e6;
 }
 
