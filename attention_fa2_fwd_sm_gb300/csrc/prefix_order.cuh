@@ -128,14 +128,18 @@ ATTN_HD PrefixSegment prefix_segment(const PrefixOrder &o, unsigned hi, int cta,
     return s;
 }
 
-// Measured rates.  A unit's key block takes this many microseconds, with two tiles
-// and with one:
-inline double prefix_block_us(int d, bool two_tiles) { return d == 128 ? (two_tiles ? 1.55 : 1.2) : (two_tiles ? 1.37 : 1.0); }
-// The own keys' kernel draws this many bytes a microsecond on `own` SMs (segments
-// of 768 keys; a third more in long ones), up to what HBM gives.
+// Measured rates.  The own keys' kernel draws this many bytes a microsecond on
+// `own` SMs (segments of 768 keys; a third more in long ones), up to what HBM gives.
+constexpr double kHbmRate = 6.0e6;
 inline double prefix_own_rate(int d, int G, int own) {
     const double sm = (d == 128 ? (G > 8 ? 52.0 : 90.0) : (G > 8 ? 38.0 : 75.0)) * 1e3;
-    return own * sm < 6.0e6 ? own * sm : 6.0e6;
+    return own * sm < kHbmRate ? own * sm : kHbmRate;
+}
+// A unit's key block takes this many microseconds, with two tiles and with one;
+// twice that beside own keys that take all of HBM's rate.
+inline double prefix_block_us(int d, bool two_tiles, double own_rate) {
+    const double us = d == 128 ? (two_tiles ? 1.55 : 1.2) : (two_tiles ? 1.37 : 1.0);
+    return own_rate < kHbmRate ? us : 2 * us;
 }
 
 // SMs for the own keys' kernel beside a prefix, `most` at most: in proportion to
@@ -146,8 +150,12 @@ inline double prefix_own_rate(int d, int G, int own) {
 inline int prefix_own_sms(int B, int G, int Hkv, int P, int d, int max_seqlen, int most, int num_sms) {
     const int rb = kPrefixTileRows / G, tiles = (B + rb - 1) / rb, mt = (tiles + 1) / 2;
     const double own = 0.75 * B * Hkv * (double)max_seqlen * 4 * d / prefix_own_rate(d, G, 1);
-    const double prefix = (double)Hkv * mt * ((P + kPrefixBlock - 1) / kPrefixBlock) * prefix_block_us(d, tiles > 1);
-    int left = int(num_sms * (prefix / (own + prefix)) + 0.5);  // SMs that the prefix starts on
+    int left = num_sms;  // SMs that the prefix starts on
+    for (int i = 0; i < 2; ++i) {  // at first as if the own keys left bandwidth over
+        const double prefix = (double)Hkv * mt * ((P + kPrefixBlock - 1) / kPrefixBlock) *
+                              prefix_block_us(d, tiles > 1, prefix_own_rate(d, G, num_sms - left));
+        left = int(num_sms * (prefix / (own + prefix)) + 0.5);
+    }
     left = mt < num_sms ? (left + mt / 2) / mt * mt : left;
     if (left < (mt < num_sms ? mt : 1)) left = mt < num_sms ? mt : 1;
     int sms = num_sms - left;
@@ -176,7 +184,7 @@ inline bool prefix_order(PrefixOrder *o, int B, int G, int Hkv, int P, int d, in
     o->unit_rows = 2 * o->rb * G;
     o->id_rows = o->unit_rows * (o->lockstep ? o->mt : 1);
     o->ids = o->early + o->late + o->rows;
-    o->own_cost = own > 0 ? unsigned(4.0 * d / prefix_own_rate(d, G, own) / prefix_block_us(d, tiles > 1) * 4294967296.0) : 0u;
+    o->own_cost = own > 0 ? unsigned(4.0 * d / prefix_own_rate(d, G, own) / prefix_block_us(d, tiles > 1, prefix_own_rate(d, G, own)) * 4294967296.0) : 0u;
     return true;
 }
 
