@@ -12,15 +12,16 @@
 // select_kernel, one row a cluster of 1, 2, 4 or 8 CTAs, a contiguous range of
 // slots each: every key becomes a 32-bit rank whose unsigned order is the order
 // above (recent keys highest), kept in shared memory.  A radix select finds the
-// keep-th largest rank in four 8-bit passes: the CTAs count digits, exchange
-// their 256 counts through distributed shared memory and each take the same
-// digit; the second pass also gathers the ranks that still qualify, a few per
-// cent, so that the last two passes are short.  Two ballot sweeps over the slots
-// in order then number the holes and the fillers.  The histogram has a column
-// per lane, so a warp's 32 increments never meet in one bank although most
-// weights share their exponent bits.  What bounds it is one SM's instruction
-// rate (32K keys on one SM: 47 us with seven full passes), hence the cluster
-// where there are fewer rows than SMs.
+// keep-th largest rank by 8-bit digits: the CTAs count digits, exchange their 256
+// counts through distributed shared memory and each take the same digit; the
+// second pass also gathers the ranks that still qualify, a few per cent, and the
+// handful that share 16 bits after it are compared with one another (two more
+// passes over the gathered ones where there are more).  Two ballot sweeps over the
+// slots in order then number the holes and the fillers.  The histogram has a
+// column per lane, so a warp's 32 increments never meet in one bank although most
+// weights share their exponent bits.  What bounds it is one SM's instruction rate
+// and the exchanges' latency (32 rows of 32K keys: 47 us on an SM a row with seven
+// full passes, 21 on four), hence the cluster where there are fewer rows than SMs.
 // Where at most kFewMoves keys go, the smallest are found one after the other
 // instead.
 // move_kernel: 2 * 2 d bytes a row each way, HBM-bound.  Where a cache has at
@@ -42,7 +43,8 @@ namespace evict {
 
 constexpr int kHistBytes = 256 * 32 * 4;
 constexpr int kListKeys = 4096;       // ranks that the second pass may gather
-constexpr int kMaxKeys = 43 * 1024;  // of one CTA: ranks that fit in shared memory; longer ranges are read again each pass
+constexpr int kMaxKeys = 42 * 1024;  // of one CTA: ranks that fit in shared memory; longer ranges are read again each pass
+constexpr int kFinalKeys = 128;        // ranks with the same upper half that are compared directly
 constexpr int kFusedMoves = 64;
 constexpr int kFewMoves = 8;
 
@@ -133,9 +135,12 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const Params p) {
     __shared__ int part[kWarps];
     __shared__ int counts[2][256];       // digit counts of this CTA (in turns: the others may still read the last)
     __shared__ int totals[4];            // this CTA's tallies
+    __shared__ int theirs[8][4];         // those of the cluster's
     __shared__ int tally[4][32];         // of each warp: kept below and past `keep`, ties below and past
     __shared__ int listed;               // entries of the list
-    __shared__ uint32_t found[2];        // the digit, and how many are above it
+    __shared__ uint32_t found[3];        // the digit, how many are above it, how many have it
+    __shared__ uint32_t finals[kFinalKeys], every[kFinalKeys];  // of this CTA; of the cluster
+    __shared__ int final_count;
     __shared__ unsigned long long least[kWarps];
     __shared__ int fused_holes[kFused ? kFusedMoves : 1], fused_src[kFused ? kFusedMoves : 1], fused_moves;
     const EvictLaunch &a = p.a;
@@ -232,7 +237,7 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const Params p) {
         uint32_t value = 0;
         int want = a.keep;
         bool gathered = false;  // the list holds every rank that still qualifies
-        if (t == 0) listed = 0;
+        if (t == 0) listed = final_count = 0;
         for (int shift = 24; shift >= 0; shift -= 8) {
             for (int i = t; i < 256 * 32; i += kThreads) hist[i] = 0;
             __syncthreads();
@@ -246,18 +251,33 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const Params p) {
             } else if (gathered) {
                 visit<4>(t, listed, kThreads, [&](int i) { return list[i]; },
                          [&](int, uint32_t x) { if ((x & mask) == value) count(x); });
-            } else {
-                visit<8>(lo + t, hi, kThreads, rank, [&](int, uint32_t x) {
-                    if ((x & mask) != value) return;
-                    count(x);
-                    if (shift == 16) {
-                        const cg::coalesced_group some = cg::coalesced_threads();
-                        int at = 0;
-                        if (some.thread_rank() == 0) at = atomicAdd(&listed, int(some.size()));
-                        at = some.shfl(at, 0) + int(some.thread_rank());
-                        if (at < kListKeys) list[at] = x;
+            } else if (shift == 16) {
+                // Whole warps, eight keys a lane: one reservation in the list for all of them.
+                for (int i0 = lo + warp * 32; i0 < hi; i0 += 8 * kThreads) {
+                    uint32_t x[8], some[8];
+                    int total = 0;
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) x[k] = i0 + k * kThreads + lane < hi ? rank(i0 + k * kThreads + lane) : ~value;
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) {
+                        some[k] = __ballot_sync(0xffffffffu, (x[k] & mask) == value);
+                        total += __popc(some[k]);
                     }
-                });
+                    int at = 0;
+                    if (lane == 0 && total > 0) at = atomicAdd(&listed, total);
+                    at = __shfl_sync(0xffffffffu, at, 0);
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) {
+                        if (some[k] >> lane & 1) {
+                            count(x[k]);
+                            const int to = at + __popc(some[k] & ((1u << lane) - 1));
+                            if (to < kListKeys) list[to] = x[k];
+                        }
+                        at += __popc(some[k]);
+                    }
+                }
+            } else {
+                visit<8>(lo + t, hi, kThreads, rank, [&](int, uint32_t x) { if ((x & mask) == value) count(x); });
             }
             __syncthreads();
             if (shift == 16) gathered = listed <= kListKeys;
@@ -295,10 +315,53 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const Params p) {
             if (lane < kDigits && above < want && above + c >= want) {
                 found[0] = uint32_t(255 - kDigits * warp - lane);
                 found[1] = uint32_t(above);
+                found[2] = uint32_t(c);
             }
             __syncthreads();
             value |= found[0] << shift;
             want -= int(found[1]);
+            if (shift == 16 && found[2] <= kFinalKeys) {
+                // So few share 16 bits that they are compared with one another: one
+                // exchange instead of two.
+                const int left = int(found[2]);
+                auto pick = [&](int, uint32_t x) {
+                    if ((x & 0xffff0000u) == value) finals[atomicAdd(&final_count, 1)] = x;
+                };
+                if (gathered) visit<4>(t, listed, kThreads, [&](int i) { return list[i]; }, pick);
+                else visit<8>(lo + t, hi, kThreads, rank, pick);
+                cluster_sync();
+                if (t < left) {
+                    uint32_t x = 0;
+                    if (peers > 1) {
+                        int i = t;
+                        for (int q = 0; q < peers; ++q) {
+                            const int n_q = *cluster.map_shared_rank(&final_count, q);
+                            if (i < n_q) {
+                                x = cluster.map_shared_rank(finals, q)[i];
+                                break;
+                            }
+                            i -= n_q;
+                        }
+                    } else {
+                        x = finals[t];
+                    }
+                    every[t] = x;
+                }
+                __syncthreads();
+                if (t < left) {
+                    const uint32_t x = every[t];
+                    int more = 0, same = 0;
+                    for (int i = 0; i < left; ++i) more += every[i] > x, same += every[i] == x;
+                    if (more < want && more + same >= want) {  // one value: equal threads write equal numbers
+                        found[0] = x;
+                        found[1] = uint32_t(more);
+                    }
+                }
+                __syncthreads();
+                value = found[0];
+                want -= int(found[1]);
+                break;
+            }
         }
 
         // Slots in order, a contiguous range a warp.  Of the ranks equal to `value` the first `want` are kept.
@@ -354,15 +417,11 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const Params p) {
                     if (lane == 0) totals[k] = sum;
                 }
             cluster.sync();
-            int theirs[8][4];
-#pragma unroll
-            for (int q = 0; q < 8; ++q)
-#pragma unroll
-                for (int k = 0; k < 4; ++k) theirs[q][k] = q < peers ? cluster.map_shared_rank(totals, q)[k] : 0;
+            if (warp == 0)  // a lane a number; the other warps read the copy
+                theirs[lane >> 2][lane & 3] = (lane >> 2) < peers ? cluster.map_shared_rank(totals, lane >> 2)[lane & 3] : 0;
+            __syncthreads();
             int t0 = 0;  // ties ahead of CTA q
-#pragma unroll
-            for (int q = 0; q < 8; ++q) {
-                if (q >= peers) break;
+            for (int q = 0; q < peers; ++q) {
                 if (q < peer) fill += theirs[q][1] + min(theirs[q][3], max(want - t0 - theirs[q][2], 0));
                 if (q == peer) ties = t0, hole = moves;
                 const int left = max(want - t0, 0), start = min(q * chunk, n);
