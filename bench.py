@@ -904,6 +904,79 @@ def run_decode_varlen(args):
         torch.cuda.empty_cache()
 
 
+def run_decode_cache(args):
+    """The decode-cache operators (GQA Hq=64, Hkv=8, d=128), one JSON line per
+    workload: a decode step over a shared prefix against attn_decode on caches
+    that hold a copy of it (which reads the prefix once per user), the weights'
+    cost on top of a decode step, a bounded cache's append and eviction, and the
+    rotary positions of a prompt.  Between calls the L2 is flushed."""
+    import torch
+
+    import attention_fa2_fwd_sm_gb300 as attn
+    from attention_fa2_fwd_sm_gb300 import _build
+    from synthetic_inputs import decode_inputs, normal_bf16, prefill_inputs
+    _build.build()
+    dev = torch.device("cuda", 0)
+    torch.cuda.set_device(dev)
+    peaks, _ = load_peaks()
+    stream = torch.cuda.current_stream(dev)
+    flush = _l2_flush_buffer(torch, dev)
+    Hq, Hkv, d = 64, 8, 128
+
+    def timed(fn):
+        for _ in range(args.warmup):
+            fn()
+        return round(_time_calls(torch, fn, args.steps, flush, stream) * 1e3, 2)
+
+    def line(workload, nbytes, **us):
+        print(json.dumps({"mode": "decode-cache", "workload": workload, "Hq": Hq, "Hkv": Hkv, "d": d, "bytes": nbytes,
+                          "hbm_floor_us": round(nbytes / peaks["hbm_gbs"] / 1e3, 2), **us}), flush=True)
+
+    for B, P, S in ((8, 2048, 256), (32, 8192, 512), (128, 32768, 1024)):
+        q, kc, vc = decode_inputs(90, B, Hq, Hkv, S, d, dev)
+        kp, vp = normal_bf16((Hkv, P, d), 91, dev), normal_bf16((Hkv, P, d), 92, dev)
+        seq = torch.linspace(S // 2, S, B, device=dev).to(torch.int32)
+        ws = attn.decode_prefix(q, kp, vp, kc, vc, seq)[2]
+        us = {"prefix_us": timed(lambda: attn.decode_prefix(q, kp, vp, kc, vc, seq, workspace=ws))}
+        keys = int(seq.sum())
+        if B <= 32:  # the copies of a longer prefix would fill the GPU's memory
+            wk = torch.cat((kp[None].expand(B, -1, -1, -1), kc), 2).contiguous()
+            wv = torch.cat((vp[None].expand(B, -1, -1, -1), vc), 2).contiguous()
+            _, wd, sp = attn.decode(q, wk, wv, seq + P)
+            us["copied_prefix_us"] = timed(lambda: attn.decode(q, wk, wv, seq + P, num_splits=sp, workspace=wd))
+            del wk, wv
+        line(f"{B} users, {P} shared + {S // 2}..{S} own keys", 4 * d * Hkv * (P + keys) + 4 * B * Hq * d, **us)
+
+    for B, S in ((1, 8192), (32, 16384)):
+        q, kc, vc = decode_inputs(93, B, Hq, Hkv, S, d, dev)
+        seq = torch.full((B,), S, dtype=torch.int32, device=dev)
+        w = torch.zeros((B, Hkv, S), device=dev)
+        ws = attn.decode_weighted(q, kc, vc, seq, w)[2]
+        _, wd, sp = attn.decode(q, kc, vc, seq)
+        line(f"{B} users, {S} keys, weights counted", (4 * d + 8) * Hkv * B * S + 4 * B * Hq * d,
+             weighted_us=timed(lambda: attn.decode_weighted(q, kc, vc, seq, w, workspace=ws)),
+             decode_us=timed(lambda: attn.decode(q, kc, vc, seq, num_splits=sp, workspace=wd)))
+        del kc, vc, w, ws
+
+    B, keep, S = 32, 4096, 4104
+    q, kc, vc = decode_inputs(94, B, Hq, Hkv, S, d, dev)
+    k = normal_bf16((B, Hkv, 1, d), 95, dev)
+    w = torch.rand((B, Hkv, S), device=dev)
+    pos = torch.arange(S, dtype=torch.int32, device=dev).expand(B, Hkv, S).contiguous()
+    lens = torch.full((B,), keep, dtype=torch.int32, device=dev)
+    lens2, cur, f = torch.empty_like(lens), lens - 1, attn.rope_freqs(d)
+
+    def step():
+        cur.add_(1)
+        attn.rope_append(q[:, :, None], k, k, kc, vc, lens, f, start_pos=cur, cache_pos=pos, weights=w, seqlens_out=lens2)
+        attn.cache_evict(kc, vc, w, lens2, keep, 256, cache_pos=pos, cur_pos=cur, seqlens_out=lens)
+
+    line(f"{B} users, a token in and the lightest of {keep} keys out", 8 * B * Hkv * (keep + 1), append_evict_us=timed(step))
+    q, kp, _ = prefill_inputs(96, 1, Hq, Hkv, 8192, d, dev)
+    out = (torch.empty_like(q), torch.empty_like(kp))
+    line("rotary positions of a prompt of 8192", 4 * (Hq + Hkv) * 8192 * d, rope_us=timed(lambda: attn.rope(q, kp, f, out=out)))
+
+
 def run_bwd_sweep(args):
     """Backward configurations (MHA, GQA causal and non-causal, DeepSeek-like
     d=56 causal) in the head-first and block-first orders; one JSON line per
@@ -972,7 +1045,7 @@ def main():
     ap.add_argument("--impl", default="gb300", choices=["gb300", "reference"])
     ap.add_argument("--mode", default="step",
                     choices=["step", "decode-sweep", "decode-one", "decode-floor", "decode-varlen", "fwd-sweep", "fwd-one",
-                             "fwd-splitkv",
+                             "fwd-splitkv", "decode-cache",
                              "bwd-one", "bwd-sweep", "die-map"],
                     help="step: the contract's one-line benchmark; the sweeps print one line "
                          "per configuration; fwd-one times one forward configuration")
@@ -1011,6 +1084,8 @@ def main():
         return run_decode_one(args)
     if args.mode == "decode-varlen":
         return run_decode_varlen(args)
+    if args.mode == "decode-cache":
+        return run_decode_cache(args)
     if args.mode == "decode-floor":
         return run_decode_floor(args)
     if args.mode == "fwd-splitkv":
