@@ -739,7 +739,7 @@ static int decode_prefix_sizes(int B, int Hq, int Hkv, int P, int d, int max_seq
     if (P == 0 && max_seqlen == 0) return ATTN_ERR_ARG;
     if (d != 64 && d != 128) return ATTN_ERR_UNSUPPORTED;
     if (Hq / Hkv > kDecodeMaxGroup) return ATTN_ERR_UNSUPPORTED;
-    if (Hkv > 65535 || (long long)B * Hq > 0x7fffffffLL || max_seqlen > (1 << 30)) return ATTN_ERR_ARG;
+    if (Hkv > 65535 || (long long)B * Hq > (1 << 30) || max_seqlen > (1 << 30) || P > (1 << 30)) return ATTN_ERR_ARG;
     // tensor-map limits, and the work list's total of keys stays below 2^62
     if ((long long)max_seqlen * d * 2 >= (1LL << 39) || (long long)P * d * 2 >= (1LL << 39)) return ATTN_ERR_ARG;
     if ((double)B * (double)max_seqlen * (double)Hkv >= 4.0e18) return ATTN_ERR_ARG;

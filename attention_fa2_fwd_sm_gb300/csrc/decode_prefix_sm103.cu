@@ -206,6 +206,10 @@ __global__ void __launch_bounds__(kWarps > 1 ? kWarps * 32 : kMergeThreads) merg
     }
 }
 
+// What to subtract from a row's scores: a row whose scores are all -inf has no
+// softmax, adds nothing, and leaves 2^(-inf - inf) = 0 instead of NaN.
+__device__ __forceinline__ float weight_ref(float L) { return L == -INFINITY ? INFINITY : L; }
+
 // The weights of n neighbouring keys of one KV head's row, G = 4 kQuads: a thread
 // takes one float4 of a key's G scores (a warp's loads are 512 consecutive bytes)
 // and kQuads neighbours add up.
@@ -214,7 +218,8 @@ __device__ __forceinline__ void add_weights(const float *scores, const float *ls
     constexpr int kBatch = 8, kStep = kWeightThreads / kQuads;
     const int quad = threadIdx.x % kQuads, key0 = threadIdx.x / kQuads;
     const float4 *src = reinterpret_cast<const float4 *>(scores) + quad;
-    const float L[4] = {lse[4 * quad], lse[4 * quad + 1], lse[4 * quad + 2], lse[4 * quad + 3]};
+    const float L[4] = {weight_ref(lse[4 * quad]), weight_ref(lse[4 * quad + 1]), weight_ref(lse[4 * quad + 2]),
+                        weight_ref(lse[4 * quad + 3])};
     for (int j0 = 0; j0 < n; j0 += kBatch * kStep) {
         float4 x[kBatch];
         float old[kBatch];
@@ -280,7 +285,7 @@ __global__ void __launch_bounds__(kWeightThreads) weight_kernel(const WeightPara
         else
             for (int j = threadIdx.x; j < n; j += kWeightThreads) {
                 float w = 0.f;
-                for (int h = 0; h < p.G; ++h) w += fast_exp2(scores[(size_t)j * p.G + h] - lse[h]);
+                for (int h = 0; h < p.G; ++h) w += fast_exp2(scores[(size_t)j * p.G + h] - weight_ref(lse[h]));
                 weights[j] += w;
             }
         at.left -= n;

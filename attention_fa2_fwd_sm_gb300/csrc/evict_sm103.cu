@@ -20,13 +20,17 @@
 // slots in order then number the holes and the fillers.  The histogram has a
 // column per lane, so a warp's 32 increments never meet in one bank although most
 // weights share their exponent bits.  What bounds it is one SM's instruction rate
-// and the exchanges' latency (32 rows of 32K keys: 47 us on an SM a row with seven
-// full passes, 21 on four), hence the cluster where there are fewer rows than SMs.
+// and the exchanges' latency (32 rows of 32K keys that need no moving: 40 us on an
+// SM a row, 26 on four), hence the cluster where there are fewer rows than SMs.
+// Without the direct comparison 29 us; without the gathering 0.1 to 0.7 us more.
 // Where at most kFewMoves keys go, the smallest are found one after the other
-// instead.
-// move_kernel: 2 * 2 d bytes a row each way, HBM-bound.  Where a cache has at
-// most kFusedMoves slots past `keep` (a decode loop that evicts what it appends)
-// the selecting CTA moves its rows itself and the second launch falls away.
+// instead (256 rows of 4K keys, 1, 2, 4, 8 of them: 8.3, 10.3, 13.7, 21 us; by the
+// radix select 16).
+// move_kernel: 2 * 2 d bytes a row each way, HBM-bound (32 rows of 8000 keys to a
+// new cache: 40 us, 6.6 TB/s).  Where a cache has at most kFusedMoves slots past
+// `keep` (a decode loop that evicts what it appends) the selecting CTA moves its
+// rows itself and the second launch falls away (256 rows, 1 key of 4K: 8.3 us, 25
+// with two launches; 64 keys of 4K 18 and 29; 16 of 16K in 64 rows 23 and 22).
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -46,7 +50,7 @@ constexpr int kListKeys = 4096;       // ranks that the second pass may gather
 constexpr int kMaxKeys = 42 * 1024;  // of one CTA: ranks that fit in shared memory; longer ranges are read again each pass
 constexpr int kFinalKeys = 128;        // ranks with the same upper half that are compared directly
 constexpr int kFusedMoves = 64;
-constexpr int kFewMoves = 8;
+constexpr int kFewMoves = 4;
 
 struct Params {
     EvictLaunch a;
@@ -553,10 +557,8 @@ Layout layout(const EvictLaunch &a) {
     return l;
 }
 
-template <bool kShared, bool kFused>
+template <bool kShared, bool kFused, int kThreads>
 cudaError_t launch_select(const Params &p, size_t smem, cudaStream_t stream) {
-    // Fused rows are those of a decode loop, many and short: several CTAs an SM.
-    constexpr int kThreads = kFused ? 512 : 1024;
     auto kernel = select_kernel<kShared, kFused, kThreads>;
     static bool attr_set[kMaxDevices] = {};
     const int dev = slot_for_device();
@@ -598,18 +600,27 @@ int evict_launch(const EvictLaunch &a, cudaStream_t stream) {
         p.holes = reinterpret_cast<int *>(a.workspace + l.holes);
     }
     // CTAs a row: while every row's cluster still has its SMs to itself and a
-    // CTA 2048 keys or more (below that the exchanges cost what the split saves).
+    // CTA 2048 keys or more.  In us, with 1, 2, 4 and 8 CTAs a row: 8 rows of 16K
+    // keys 27, 23, 21, 19; 8 of 128K 245, 140, 52, 39; 16 of 8K 21, 20, 18, 20; 8 of
+    // 4K 15.6, 16.5 with two (an exchange costs what it saves).
     const long long rows = (long long)a.B * a.Hkv;
     p.cluster = 1;
-    if (!l.fused)
+    if (!l.fused && a.max_seqlen >= 8192)
         while (p.cluster < 8 && rows * p.cluster * 2 <= a.num_sms && a.max_seqlen / (p.cluster * 2) >= 2048) p.cluster *= 2;
     const int keys = ((a.max_seqlen + p.cluster - 1) / p.cluster + 31) / 32 * 32;
     const bool shared = keys <= kMaxKeys;
     const size_t smem = kHistBytes + (kListKeys + (shared ? (size_t)keys : 0)) * 4;
-    cudaError_t e = l.fused ? (shared ? launch_select<true, true>(p, smem, stream)
-                                      : launch_select<false, true>(p, smem, stream))
-                            : (shared ? launch_select<true, false>(p, smem, stream)
-                                      : launch_select<false, false>(p, smem, stream));
+    // Threads: a CTA with few keys spends its time at barriers, which are cheaper with
+    // 512 threads (2048 keys of each of 64 CTAs 19.0 us, 20.6 with 1024), one with many
+    // on its keys (8K of 128 CTAs 32.5 and 30.6; one key of 64 rows of 8K by the fused
+    // form 11.0 and 8.2).  More fused rows than SMs share an SM with 512 threads, up to
+    // some length (one key of 256 rows: 4K keys 8.3 and 11.6, 8K 12.4 and 15.1, 16K 33 and 23).
+    const bool many = keys > (l.fused && rows > a.num_sms ? 12288 : 4096);
+    auto select = l.fused ? (!shared ? launch_select<false, true, 1024> : many ? launch_select<true, true, 1024>
+                                                                               : launch_select<true, true, 512>)
+                          : (!shared ? launch_select<false, false, 1024> : many ? launch_select<true, false, 1024>
+                                                                                : launch_select<true, false, 512>);
+    cudaError_t e = select(p, smem, stream);
     if (e != cudaSuccess) return note_cuda_error(e, "select_kernel launch");
     if (l.fused || l.slots == 0) return 0;
     const int per_row = (l.slots + kMoveRows - 1) / kMoveRows;

@@ -21,6 +21,10 @@
 // else of size moves, so HBM.  A thread owns one 8-column unit of one token
 // (in the half layout its partner unit too), computes that unit's sines once
 // and applies them to up to kMaxHeads heads, whose loads it issues together.
+// 8192 tokens, 64 + 8 heads, d = 128 (302 MB): 48.4 us, 6.2 TB/s; one head a
+// thread 100 us (the sines), 4 or 16 heads 48.5, loads of 2 or 8 heads at a time
+// 49.0 and 48.6.  2048 tokens, 32 + 8 heads: 8.9 us in blocks of 128 threads, 10.3
+// in blocks of 256, whose last wave is the coarser.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -31,7 +35,7 @@
 namespace attn {
 namespace rope {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 128;
 constexpr int kMaxHeads = 8;   // heads a thread visits with one set of sines
 constexpr int kBatch = 4;      // heads whose loads are in flight together
 constexpr int kMaxPairs = 256; // rotary_dim <= 512
@@ -247,15 +251,17 @@ int rope_launch(const RopeLaunch &a, cudaStream_t stream) {
     p.scale = a.out_scale;
     p.sign = a.inverse ? -1.f : 1.f;
     const long long gx = (p.tokens * p.items + kThreads - 1) / kThreads;
-    // Heads per thread: as many as share the sines while the grid still has
-    // four blocks per SM; a short call takes one head a thread.
+    // Heads per thread: as many as share the sines while the grid still has two
+    // blocks per SM; a short call takes one head a thread.  In us, one head and
+    // eight: 64 tokens of 8 + 2 heads 3.4 and 4.1; 128 x 1 token of 64 + 8 heads 4.4
+    // and 4.8; 2048 tokens of 32 + 8 heads 16.4 and 8.9.
     int per = kMaxHeads;
     auto grid_y = [&](int c) {
         long long y = 0;
         for (const auto &t : a.t) y += (t.heads + c - 1) / c;
         return y;
     };
-    while (per > 1 && gx * grid_y(per) < 4LL * a.num_sms) per /= 2;
+    while (per > 1 && gx * grid_y(per) < 2LL * a.num_sms && grid_y(per / 2) <= 65535) per /= 2;
     p.heads_per_chunk = per;
     for (int i = 0; i < 3; ++i) {
         p.t[i] = a.t[i];

@@ -28,8 +28,9 @@
  *    attn_strerror() gives a message for each.
  *  - CUDA graphs: the launches of attn_fwd, attn_fwd_ex, attn_fwd_host,
  *    attn_bwd, the decode entry points, attn_rope, attn_rope_append and
- *    attn_cache_evict can be captured into a CUDA graph on `stream` and replayed; a replay reads what the buffers hold at replay
- *    time (the ragged decode's seqlens included: it plans on the device).
+ *    attn_cache_evict can be captured into a CUDA graph on `stream` and
+ *    replayed; a replay reads what the buffers hold at replay time (seqlens
+ *    included: the ragged decode and attn_decode_prefix plan on the device).
  *    Make one ordinary call per device first (it sets up per-device state:
  *    kernel attributes, scratch addresses, the die map, the host-copy
  *    streams).  The persistent forward and backward kernels take one of 64
@@ -514,12 +515,14 @@ int attn_rope_append(const void *q, void *q_out, const void *k, const void *v, v
  *   kcache, vcache  [B, Hkv, max_seqlen, d]  bf16; max_seqlen = 0 (NULL): no
  *              own keys
  *   seqlens    [B] int32, clamped to [0, max_seqlen]; NULL where max_seqlen
- *              is 0.  A sequence with no key at all gets o = 0, lse = -inf.
+ *              is 0.  A sequence with no key at all (or none whose score is
+ *              above -inf) gets o = 0, lse = -inf and adds no weight.
  *   lse        [B, Hq] fp32 (natural log), or NULL
  *   weights    [B, Hkv, max_seqlen] fp32, read and written, or NULL.  Entries
  *              at or past seqlens[b] are left as they were.  No atomics:
  *              equal calls give equal bits.
- *   d in {64, 128}; 1 <= Hq / Hkv <= 16; P or max_seqlen > 0; max_seqlen <= 2^30.
+ *   d in {64, 128}; 1 <= Hq / Hkv <= 16; P or max_seqlen > 0; max_seqlen, P and
+ *   B * Hq at most 2^30.
  *   workspace  at least attn_decode_prefix_workspace_bytes(...) bytes, 16-byte
  *              aligned; with weights it also holds the scores, 4 * B * Hq *
  *              max_seqlen bytes.  Nothing in it outlives the call.

@@ -125,6 +125,7 @@ def _prefix(**kw):
     (dict(S=-1), ARG), (dict(B=0), ARG), (dict(Hq=3), ARG), (dict(scale=0.0), ARG), (dict(scale=float("nan")), ARG),
     (dict(d=56), UNSUP), (dict(d=256), UNSUP), (dict(Hq=34, Hkv=2), UNSUP), (dict(ws=None), WS), (dict(ws=A16 + 8), WS),
     (dict(P=0, kp=None, vp=None, kc=None), ARG), (dict(S=0, kc=None, vc=None, lens=None, ws=None), WS),
+    (dict(P=(1 << 30) + 1), ARG), (dict(S=(1 << 30) + 1), ARG), (dict(B=(1 << 28) + 1, Hq=4, Hkv=4), ARG),
 ])
 def test_decode_prefix_refusals(kw, code):
     assert _prefix(**kw) == code

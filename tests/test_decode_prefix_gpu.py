@@ -248,6 +248,58 @@ def test_caches_past_two_to_the_31_elements(attn):
     torch.cuda.empty_cache()
 
 
+def test_more_than_two_to_the_29_keys_in_the_caches(attn):
+    """Lengths are then scanned in 64 bits; K and V are one tensor, and most of it is never read."""
+    B, Hq, Hkv, S, d = 600, 2, 1, (1 << 29) // 600 + 1, 64
+    if torch.cuda.mem_get_info()[0] < 90 << 30:
+        pytest.skip("needs 90 GB")
+    kc = torch.empty((B, Hkv, S, d), dtype=torch.bfloat16, device=DEV)
+    kc[:, :, :512] = normal_bf16((B, Hkv, 512, d), 203, DEV)
+    q = normal_bf16((B, Hq, d), 204, DEV)
+    kp, vp = (normal_bf16((Hkv, 200, d), 205 + i, DEV) for i in range(2))
+    lens = torch.randint(-3, 70, (B,), generator=torch.Generator().manual_seed(206)).tolist()
+    lens[300], lens[-1] = 512, 511
+    seq = torch.tensor(lens, dtype=torch.int32, device=DEV)
+    w = torch.zeros((B, Hkv, S), device=DEV)
+    o, lse, _ = attn.decode_prefix(q, kp, vp, kc, kc, seq, weights=w)
+    torch.cuda.synchronize()
+    assert attn.attn_device_status() == attn.ATTN_OK
+    near = kc[:, :, :512]
+    ro, rl, rw, to, e, tw = reference(q, kp, vp, near, near, lens, d ** -0.5)
+    assert torch.all((o.double().cpu() - ro).abs() <= to)
+    assert torch.all((lse.double().cpu() - rl).abs() <= e)
+    assert torch.all((w[:, :, :512].double().cpu() - rw).abs() <= tw + 2.0 ** -24 * rw)
+    assert not w[:, :, 512:].any()
+    del kc, near, w
+    torch.cuda.empty_cache()
+
+
+@pytest.mark.parametrize("G,d", [(1, 64), (4, 128), (8, 64), (16, 128)])
+def test_scores_of_minus_infinity(attn, G, d):
+    """Keys whose score is -inf add nothing; a sequence with no others gets o = 0, lse = -inf and no weight."""
+    B, Hkv, S = 3, 2, 300
+    q, _, _, kc, vc = inputs(B, G * Hkv, Hkv, 0, S, d, 230)
+    q[..., 0] = 1
+    gone = torch.zeros(B, S, dtype=torch.bool)
+    gone[0] = True
+    gone[1, torch.randperm(S, generator=torch.Generator().manual_seed(231))[:200]] = True
+    kc[:, :, :, 0] = torch.where(gone.to(DEV)[:, None], -math.inf, kc[:, :, :, 0].float()).bfloat16()
+    seq = torch.tensor([S, S, S], dtype=torch.int32, device=DEV)
+    w = torch.ones((B, Hkv, S), device=DEV)
+    o, lse, _ = attn.decode_weighted(q, kc, vc, seq, w)
+    torch.cuda.synchronize()
+    assert attn.attn_device_status() == attn.ATTN_OK
+    assert torch.all(o[0] == 0) and torch.all(lse[0] == -math.inf)
+    assert torch.all(w.cpu()[gone[:, None].expand(B, Hkv, S)] == 1)
+    for b in (1, 2):
+        left = (~gone[b]).nonzero()[:, 0].to(DEV)
+        n = len(left)
+        ro, rl, rw, to, e, tw = reference(q[b:b + 1], None, None, kc[b:b + 1, :, left], vc[b:b + 1, :, left], [n], d ** -0.5)
+        assert torch.all((o[b].double().cpu() - ro[0]).abs() <= to[0])
+        assert torch.all((lse[b].double().cpu() - rl[0]).abs() <= e[0])
+        assert torch.all((w[b][:, left].double().cpu() - 1 - rw[0]).abs() <= tw[0] + 2.0 ** -24 * (1 + rw[0]))
+
+
 def test_wait_limit_is_reported_and_recovered(attn):
     q, kp, vp, kc, vc = inputs(4, 16, 2, 3000, 1500, 128, 210)
     lens = [1500, 0, 17, 900]
