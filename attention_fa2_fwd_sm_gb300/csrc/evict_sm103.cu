@@ -20,17 +20,18 @@
 // slots in order then number the holes and the fillers.  The histogram has a
 // column per lane, so a warp's 32 increments never meet in one bank although most
 // weights share their exponent bits.  What bounds it is one SM's instruction rate
-// and the exchanges' latency (32 rows of 32K keys that need no moving: 40 us on an
-// SM a row, 26 on four), hence the cluster where there are fewer rows than SMs.
-// Without the direct comparison 29 us; without the gathering 0.1 to 0.7 us more.
+// and the exchanges' latency (32 rows of 32K keys that need no moving: 29 us on an
+// SM a row, 18.5 on four), hence the cluster where there are fewer rows than SMs.
+// Without the direct comparison 22 us; without the gathering 0 to 0.7 us more, 3 on
+// 8 rows of 128K.
 // Where at most kFewMoves keys go, the smallest are found one after the other
-// instead (256 rows of 4K keys, 1, 2, 4, 8 of them: 8.3, 10.3, 13.7, 21 us; by the
-// radix select 16).
+// instead (256 rows of 4K keys, 1, 2, 4, 8 of them: 6.9, 8.9, 13.0, 21.2 us; by the
+// radix select 13.7).
 // move_kernel: 2 * 2 d bytes a row each way, HBM-bound (32 rows of 8000 keys to a
-// new cache: 40 us, 6.6 TB/s).  Where a cache has at most kFusedMoves slots past
-// `keep` (a decode loop that evicts what it appends) the selecting CTA moves its
-// rows itself and the second launch falls away (256 rows, 1 key of 4K: 8.3 us, 25
-// with two launches; 64 keys of 4K 18 and 29; 16 of 16K in 64 rows 23 and 22).
+// new cache: 273 MB, 41 us, 6.6 TB/s).  Where a cache has at most kFusedMoves slots
+// past `keep` (a decode loop that evicts what it appends) the selecting CTA moves
+// its rows itself and the second launch falls away (256 rows, 1 key of 4K: 6.9 us,
+// 22.7 with two launches; 64 keys of 4K 17.4 and 26; 16 of 16K in 64 rows 18.4 and 19).
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -55,8 +56,8 @@ constexpr int kFewMoves = 4;
 struct Params {
     EvictLaunch a;
     int *head;     // [rows][2]: keys to move, n
-    int *src;      // [rows][slots]: in place the fillers, else the source of every slot
-    int *holes;    // [rows][gaps]
+    int *src;      // [rows][slots]: in place the fillers, else the source of every slot: another slot, or ~i for fillers[i]
+    int *holes;    // [rows][gaps]: in place the holes, else the fillers
     int slots, gaps, in_place, cluster;
 };
 
@@ -67,13 +68,16 @@ __device__ __forceinline__ uint32_t rank_of(float w) {
     return u & 0x80000000u ? ~u : u | 0x80000000u;
 }
 
+struct Key {
+    float w;
+    int pos;
+};
 struct Row {
     const float *w;
     const int *pos;
     long long after;  // positions past this one are recent
-    __device__ __forceinline__ uint32_t rank(int i) const {
-        return (long long)(pos ? pos[i] : i) > after ? 0xffffffffu : rank_of(w[i]);
-    }
+    __device__ __forceinline__ Key key(int i) const { return {w[i], pos ? pos[i] : i}; }
+    __device__ __forceinline__ uint32_t rank(Key k) const { return (long long)k.pos > after ? 0xffffffffu : rank_of(k.w); }
 };
 
 // Exclusive prefix of one value per warp, and the total.
@@ -111,15 +115,16 @@ __device__ __forceinline__ void move_scalars(const EvictLaunch &a, long long row
     if (a.pos_out) a.pos_out[o] = a.cache_pos ? a.cache_pos[i] : from;
 }
 
-// Calls f(slot, rank) for the slots of [i0, i1) that this thread visits, `step`
-// apart, kBatch loads at a time.
+// Calls f(slot, load(slot)) for the slots of [i0, i1) that this thread visits, `step`
+// apart, kBatch loads at a time.  None of them is conditional (past the end they
+// repeat the last slot), so that all are on their way together: the first pass over
+// 8K keys a CTA takes 3.1 us instead of 4.9.
 template <int kBatch, typename Load, typename F>
 __device__ __forceinline__ void visit(int i0, int i1, int step, Load load, F f) {
     for (int i = i0; i < i1; i += kBatch * step) {
-        uint32_t x[kBatch];
+        decltype(load(0)) x[kBatch];
 #pragma unroll
-        for (int k = 0; k < kBatch; ++k)
-            if (i + k * step < i1) x[k] = load(i + k * step);
+        for (int k = 0; k < kBatch; ++k) x[k] = load(min(i + k * step, i1 - 1));
 #pragma unroll
         for (int k = 0; k < kBatch; ++k)
             if (i + k * step < i1) f(i + k * step, x[k]);
@@ -153,7 +158,10 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const Params p) {
     const long long row = blockIdx.x / peers;
     const int b = int(row / a.Hkv), t = threadIdx.x, warp = t >> 5, lane = t & 31;
     if constexpr (!kFused) griddep_launch_dependents();
-    const int n = min(max(a.seqlens[b], 0), a.max_seqlen);
+    const int listed_keys = a.seqlens[b], newest = a.cur_pos ? a.cur_pos[b] : 0;
+    if constexpr (!kFused)  // for the first digit, while the loads are on their way
+        for (int i = t; i < 256 * 32; i += kThreads) hist[i] = 0;
+    const int n = min(max(listed_keys, 0), a.max_seqlen);
     const int kept = min(n, a.keep);
     if (t == 0 && peer == 0) {
         if (a.seqlens_out && row == (long long)b * a.Hkv) a.seqlens_out[b] = kept;
@@ -172,12 +180,12 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const Params p) {
     Row r;
     r.w = a.weights + row * a.max_seqlen;
     r.pos = a.cache_pos ? a.cache_pos + row * a.max_seqlen : nullptr;
-    r.after = (long long)(a.cur_pos ? a.cur_pos[b] : n - 1) - a.recent;
+    r.after = (long long)(a.cur_pos ? newest : n - 1) - a.recent;
     // This CTA's slots.
     const int chunk = ((n + peers - 1) / peers + 31) / 32 * 32;
     const int lo = min(peer * chunk, n), hi = min(lo + chunk, n);
-    auto global_rank = [&](int i) { return r.rank(i); };
-    auto rank = [&](int i) { return kShared ? ranks[i - lo] : r.rank(i); };
+    auto key = [&](int i) { return r.key(i); };
+    auto rank = [&](int i) { return kShared ? ranks[i - lo] : r.rank(r.key(i)); };
     auto cluster_sync = [&]() {
         if (peers > 1) cluster.sync();
         else __syncthreads();
@@ -188,7 +196,7 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const Params p) {
         // A few keys go: find the smallest (rank, slot from the end), then the
         // next one, a pass each.
         if constexpr (kShared)
-            visit<8>(t, n, kThreads, global_rank, [&](int i, uint32_t x) { ranks[i] = x; });  // each thread its own
+            visit<8>(t, n, kThreads, key, [&](int i, Key k) { ranks[i] = r.rank(k); });  // each thread its own
         unsigned long long last = 0;
         for (int e = 0; e < n - a.keep; ++e) {
             unsigned long long low = ~0ull;
@@ -243,12 +251,14 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const Params p) {
         bool gathered = false;  // the list holds every rank that still qualifies
         if (t == 0) listed = final_count = 0;
         for (int shift = 24; shift >= 0; shift -= 8) {
-            for (int i = t; i < 256 * 32; i += kThreads) hist[i] = 0;
+            if (kFused || shift < 24)
+                for (int i = t; i < 256 * 32; i += kThreads) hist[i] = 0;
             __syncthreads();
             const uint32_t mask = shift == 24 ? 0u : 0xffffffffu << (shift + 8);
             auto count = [&](uint32_t x) { atomicAdd(&hist[(x >> shift & 255u) * 32 + lane], 1u); };
             if (shift == 24) {
-                visit<8>(lo + t, hi, kThreads, global_rank, [&](int i, uint32_t x) {
+                visit<8>(lo + t, hi, kThreads, key, [&](int i, Key k) {
+                    const uint32_t x = r.rank(k);
                     if (kShared) ranks[i - lo] = x;
                     count(x);
                 });
@@ -373,25 +383,26 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const Params p) {
         const int i0 = min(lo + warp * range, hi), i1 = min(i0 + range, hi);
         const uint32_t below = (1u << lane) - 1;
         constexpr int kBatch = 4;
-        auto sweep = [&](auto f) {  // f(slot, rank, inside) by whole warps, in order
-            for (int i = i0; i < i1; i += kBatch * 32) {
+        const int mid = min(max(a.keep, i0), i1);  // slots past `keep` from here on
+        auto sweep = [&](int from, int to, auto f) {  // f(slot, rank, inside) by whole warps, in order
+            for (int i = from; i < to; i += kBatch * 32) {
                 uint32_t x[kBatch];
 #pragma unroll
-                for (int k = 0; k < kBatch; ++k) x[k] = i + k * 32 + lane < i1 ? rank(i + k * 32 + lane) : 0;
+                for (int k = 0; k < kBatch; ++k) x[k] = rank(min(i + k * 32 + lane, to - 1));
 #pragma unroll
                 for (int k = 0; k < kBatch; ++k)
-                    if (i + k * 32 < i1) f(i + k * 32 + lane, x[k], i + k * 32 + lane < i1);
+                    if (i + k * 32 < to) f(i + k * 32 + lane, x[k], i + k * 32 + lane < to);
             }
         };
         // First sweep: keys above `value` and ties, below `keep` and past it.
         int up[2] = {0, 0}, tie[2] = {0, 0};
-        sweep([&](int s, uint32_t x, bool in) {
-            const bool past = s >= a.keep;
-            up[0] += __popc(__ballot_sync(0xffffffffu, in && x > value && !past));
-            up[1] += __popc(__ballot_sync(0xffffffffu, in && x > value && past));
-            tie[0] += __popc(__ballot_sync(0xffffffffu, in && x == value && !past));
-            tie[1] += __popc(__ballot_sync(0xffffffffu, in && x == value && past));
-        });
+        sweep(i0, mid, [&](int, uint32_t x, bool in) { up[0] += in && x > value, tie[0] += in && x == value; });
+        sweep(mid, i1, [&](int, uint32_t x, bool in) { up[1] += in && x > value, tie[1] += in && x == value; });
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            up[k] = __reduce_add_sync(0xffffffffu, up[k]);
+            tie[k] = __reduce_add_sync(0xffffffffu, tie[k]);
+        }
         // Where this warp's ties, holes and fillers start.  Slots go up with the
         // warp and with the CTA, and within either the ties below `keep` come
         // before those past it, so four counts of every warp and of every CTA
@@ -424,6 +435,7 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const Params p) {
             if (warp == 0)  // a lane a number; the other warps read the copy
                 theirs[lane >> 2][lane & 3] = (lane >> 2) < peers ? cluster.map_shared_rank(totals, lane >> 2)[lane & 3] : 0;
             __syncthreads();
+            cluster.barrier_arrive();  // this CTA has read all that it will of the others
             int t0 = 0;  // ties ahead of CTA q
             for (int q = 0; q < peers; ++q) {
                 if (q < peer) fill += theirs[q][1] + min(theirs[q][3], max(want - t0 - theirs[q][2], 0));
@@ -445,22 +457,29 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const Params p) {
             hole += __shfl_sync(0xffffffffu, gaps_upto - gaps, warp);
             fill += __shfl_sync(0xffffffffu, fills_upto - fills, warp);
         }
-        sweep([&](int s, uint32_t x, bool in) {
+        auto stays = [&](uint32_t x, bool in) {
             const uint32_t same = __ballot_sync(0xffffffffu, in && x == value);
-            const bool keep = in && (x > value || (x == value && ties + __popc(same & below) < want));
-            ties += __popc(same);
-            const bool is_hole = in && s < a.keep && !keep, is_fill = keep && s >= a.keep;
-            const uint32_t hm = __ballot_sync(0xffffffffu, is_hole), fm = __ballot_sync(0xffffffffu, is_fill);
-            if (is_hole) holes[hole + __popc(hm & below)] = s;
-            if (is_fill) {
-                const int f = fill + __popc(fm & below);
-                // Out of place the fillers wait behind the holes for src to be complete.
-                if (p.in_place) src[f] = s;
-                else holes[p.gaps / 2 + f] = s;
+            bool yes = in && x > value;
+            if (same) {
+                yes |= (same >> lane & 1) && ties + __popc(same & below) < want;
+                ties += __popc(same);
             }
-            if (!p.in_place && in && s < a.keep && !is_hole) src[s] = s;
-            hole += __popc(hm);
-            fill += __popc(fm);
+            return yes;
+        };
+        sweep(i0, mid, [&](int s, uint32_t x, bool in) {
+            const bool gone = !stays(x, in) && in;
+            const uint32_t all = __ballot_sync(0xffffffffu, gone);
+            const int at = hole + __popc(all & below);
+            hole += __popc(all);
+            if (!p.in_place && in) src[s] = gone ? ~at : s;
+            if (p.in_place && gone) holes[at] = s;
+        });
+        int *fillers = p.in_place ? src : holes;
+        sweep(mid, i1, [&](int s, uint32_t x, bool in) {
+            const bool filler = stays(x, in);
+            const uint32_t all = __ballot_sync(0xffffffffu, filler);
+            if (filler) fillers[fill + __popc(all & below)] = s;
+            fill += __popc(all);
         });
     }
     if constexpr (kFused) {
@@ -473,11 +492,7 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const Params p) {
         }
     } else {
         if (t == 0 && peer == 0) p.head[2 * row] = moves;
-        // The lists are complete, and no CTA leaves while another may read its shared memory.
-        __threadfence();
-        cluster_sync();
-        if (!p.in_place)
-            for (int i = peer * kThreads + t; i < moves; i += peers * kThreads) src[holes[i]] = holes[p.gaps / 2 + i];
+        if (peers > 1) cluster.barrier_wait();  // no CTA leaves while another may read its shared memory
     }
 }
 
@@ -485,22 +500,28 @@ constexpr int kMoveThreads = 256;
 constexpr int kMoveRows = 64;  // cache rows of one CTA's turn
 constexpr int kMoveBatch = 8;  // 16-byte units a thread has in flight
 
-// Grid-stride over (row, 64 moved keys).  kUnits: 16-byte units of a key and its
+// `per_row` CTAs a row, each every per_row-th kMoveRows of its moved keys.  kUnits: 16-byte units of a key and its
 // value (d / 4) where that divides the CTA, so that a thread keeps one unit and
 // steps over keys without a division; 0: any d.
 template <int kUnits>
-__global__ void __launch_bounds__(kMoveThreads) move_kernel(const Params p, long long turns, int per_row) {
+__global__ void __launch_bounds__(kMoveThreads) move_kernel(const Params p, int per_row) {
+    __shared__ int from[kMoveRows], to[kMoveRows];
     griddep_wait();
     const EvictLaunch &a = p.a;
     const int units = kUnits ? kUnits : a.d / 4, half = units / 2;
-    for (long long turn = blockIdx.x; turn < turns; turn += gridDim.x) {
-        const long long row = turn / per_row;
-        const int first = int(turn - row * per_row) * kMoveRows;
-        const int count = p.in_place ? p.head[2 * row] : min(p.head[2 * row + 1], a.keep);
+    const long long row = blockIdx.x / per_row;
+    const int count = p.in_place ? p.head[2 * row] : min(p.head[2 * row + 1], a.keep);
+    for (int first = int(blockIdx.x % per_row) * kMoveRows; first < count; first += per_row * kMoveRows) {
         const int keys = min(kMoveRows, count - first);
-        const int *src = p.src + row * p.slots + first, *to = p.holes + row * p.gaps + first;
-        if (int(threadIdx.x) < keys)
-            move_scalars(a, row, src[threadIdx.x], p.in_place ? to[threadIdx.x] : first + int(threadIdx.x));
+        if (int(threadIdx.x) < keys) {
+            const int m = first + threadIdx.x, *list = p.holes + row * p.gaps;
+            int s = p.src[row * p.slots + m];
+            if (s < 0) s = list[~s];
+            from[threadIdx.x] = s;
+            to[threadIdx.x] = p.in_place ? list[m] : m;
+        }
+        __syncthreads();
+        if (int(threadIdx.x) < keys) move_scalars(a, row, from[threadIdx.x], to[threadIdx.x]);
         if constexpr (kUnits > 0) {
             constexpr int kStep = kMoveThreads / kUnits;
             const int u = threadIdx.x % kUnits, m0 = threadIdx.x / kUnits;
@@ -515,21 +536,22 @@ __global__ void __launch_bounds__(kMoveThreads) move_kernel(const Params p, long
 #pragma unroll
                 for (int k = 0; k < kMoveBatch; ++k) {
                     const int m = m0 + m1 + k * kStep;
-                    if (m < keys) v[k] = __ldcs(reinterpret_cast<const uint4 *>(in + (long long)src[m] * (half * 16)));
+                    if (m < keys) v[k] = __ldcs(reinterpret_cast<const uint4 *>(in + (long long)from[m] * (half * 16)));
                 }
 #pragma unroll
                 for (int k = 0; k < kMoveBatch; ++k) {
                     const int m = m0 + m1 + k * kStep;
                     if (m < keys)
-                        *reinterpret_cast<uint4 *>(out + (long long)(p.in_place ? to[m] : first + m) * (half * 16)) = v[k];
+                        *reinterpret_cast<uint4 *>(out + (long long)to[m] * (half * 16)) = v[k];
                 }
             }
         } else {
             for (int i = threadIdx.x; i < keys * units; i += kMoveThreads) {
                 const int m = i / units, u = i % units;
-                store_unit(a, row, p.in_place ? to[m] : first + m, u, load_unit(a, row, src[m], u));
+                store_unit(a, row, to[m], u, load_unit(a, row, from[m], u));
             }
         }
+        __syncthreads();  // the lists are free for the next turn
     }
 }
 
@@ -549,7 +571,7 @@ Layout layout(const EvictLaunch &a) {
     l.fused = in_place && past <= kFusedMoves;
     if (l.fused) return l;
     l.slots = in_place ? most : (a.keep < a.max_seqlen ? a.keep : a.max_seqlen);
-    l.gaps = in_place ? most : 2 * most;
+    l.gaps = most;
     l.head = 0;
     l.src = up(rows * 2 * sizeof(int));
     l.holes = l.src + up(rows * l.slots * sizeof(int));
@@ -601,8 +623,8 @@ int evict_launch(const EvictLaunch &a, cudaStream_t stream) {
     }
     // CTAs a row: while every row's cluster still has its SMs to itself and a
     // CTA 2048 keys or more.  In us, with 1, 2, 4 and 8 CTAs a row: 8 rows of 16K
-    // keys 27, 23, 21, 19; 8 of 128K 245, 140, 52, 39; 16 of 8K 21, 20, 18, 20; 8 of
-    // 4K 15.6, 16.5 with two (an exchange costs what it saves).
+    // keys 18.5, 17.1, 15.1, 15.1; 8 of 128K 197, 114, 36, 25; 16 of 8K 14.4, 14.4, 13.7,
+    // 16.4; 8 of 4K 11.7, and 13.7 with eight (an exchange costs what it saves).
     const long long rows = (long long)a.B * a.Hkv;
     p.cluster = 1;
     if (!l.fused && a.max_seqlen >= 8192)
@@ -611,11 +633,12 @@ int evict_launch(const EvictLaunch &a, cudaStream_t stream) {
     const bool shared = keys <= kMaxKeys;
     const size_t smem = kHistBytes + (kListKeys + (shared ? (size_t)keys : 0)) * 4;
     // Threads: a CTA with few keys spends its time at barriers, which are cheaper with
-    // 512 threads (2048 keys of each of 64 CTAs 19.0 us, 20.6 with 1024), one with many
-    // on its keys (8K of 128 CTAs 32.5 and 30.6; one key of 64 rows of 8K by the fused
-    // form 11.0 and 8.2).  More fused rows than SMs share an SM with 512 threads, up to
-    // some length (one key of 256 rows: 4K keys 8.3 and 11.6, 8K 12.4 and 15.1, 16K 33 and 23).
-    const bool many = keys > (l.fused && rows > a.num_sms ? 12288 : 4096);
+    // 512 threads (2048 keys of each of 64 CTAs 15.1 us, 16.5 with 1024), one with many
+    // on its keys (8K of 128 CTAs 19.2 and 18.5; one key of 64 rows of 8K by the fused
+    // form 7.5 and 6.9).  Two of more rows than SMs share an SM with 512 threads, up to
+    // some length (256 rows of 8K 21 and 26; one key of 256 rows of 4K 6.9 and 9.6, of 8K
+    // 8.9 and 11.6, of 16K 18.6 and 15.8).
+    const bool many = keys > (rows > a.num_sms ? 12288 : 4096);
     auto select = l.fused ? (!shared ? launch_select<false, true, 1024> : many ? launch_select<true, true, 1024>
                                                                                : launch_select<true, true, 512>)
                           : (!shared ? launch_select<false, false, 1024> : many ? launch_select<true, false, 1024>
@@ -623,14 +646,13 @@ int evict_launch(const EvictLaunch &a, cudaStream_t stream) {
     cudaError_t e = select(p, smem, stream);
     if (e != cudaSuccess) return note_cuda_error(e, "select_kernel launch");
     if (l.fused || l.slots == 0) return 0;
-    const int per_row = (l.slots + kMoveRows - 1) / kMoveRows;
-    const long long turns = rows * per_row;
-    // In place the number of moves is known on the device only, and most turns
-    // may be empty: a fixed grid walks them.  Out of place every turn is work.
-    const long long most = p.in_place ? 8LL * a.num_sms : 0x7fffffffLL;
-    const long long grid = turns < most ? turns : most;
+    // In place the number of moves is known on the device only and may be far from
+    // the most: as many CTAs as the GPU holds.  Out of place the most is usual.
+    long long per_row = (l.slots + kMoveRows - 1) / kMoveRows;
+    const long long most = p.in_place ? (8LL * a.num_sms + rows - 1) / rows : 0x7fffffffLL / rows;
+    if (per_row > most) per_row = most;
     auto move = a.d == 128 ? move_kernel<32> : (a.d == 64 ? move_kernel<16> : move_kernel<0>);
-    e = dec::launch_programmatic(move, dim3(unsigned(grid)), dim3(kMoveThreads), 0, stream, p, turns, per_row);
+    e = dec::launch_programmatic(move, dim3(unsigned(rows * per_row)), dim3(kMoveThreads), 0, stream, p, int(per_row));
     return e == cudaSuccess ? 0 : note_cuda_error(e, "move_kernel launch");
 }
 
