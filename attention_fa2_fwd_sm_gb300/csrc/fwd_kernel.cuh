@@ -37,9 +37,10 @@
 // translation units: fwd_sm103.cu (the tile orders, and the grouped causal
 // GQA mapping), fwd_splitkv_sm103.cu (each head's keys cut into ranges,
 // fp32 partials per range) and decode_prefix_sm103.cu (one query row per batch
-// entry and head against a prefix that the batch shares).  The mappings are compile-time variants, so each
-// instantiation carries only its own mapping's code; each translation unit
-// has its own copy of the work counters and the status word below.
+// entry and head against a prefix that the batch shares).  The mappings are
+// compile-time variants, so each instantiation carries only its own mapping's
+// code; each translation unit has its own copy of the work counters and the
+// status word below.
 #pragma once
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -200,7 +201,7 @@ struct MappedWork<kMapSplit> : UnitWork {
 template <>
 struct MappedWork<kMapPrefix> : UnitWork {
     int s, jb;  // s: the partial number
-    int row, m;
+    int m;
 };
 
 template <int kMap>
@@ -213,7 +214,6 @@ __device__ __forceinline__ MappedWork<kMap> unit_work(const typename ParamsOf<kM
         w.kvh = seg.g;
         w.h = seg.g * p.G;
         w.s = range->share + seg.row;
-        w.row = seg.row;
         w.m = seg.m;
         w.jb = seg.j0;
         w.nmax = seg.n;
@@ -395,6 +395,24 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t tmem_base = *tmem_slot;
 
     int *status = &g_fwd_status;
+
+    // Where the merge finds the rows that this CTA's share begins: from the shares
+    // alone and whatever becomes of the work, so that a launch whose waits run out
+    // leaves the merge with wrong numbers but no wrong addresses.
+    if constexpr (kMap == kMapPrefix) {
+        if (warp == 3) {
+            for (int i = lane;; i += 32) {
+                const int u = prefix_start(p.po, prefix_range->lo, prefix_range->hi, i);
+                if (u < 0) break;
+                const PrefixSegment seg = prefix_segment(p.po, prefix_range->hi, blockIdx.x, u);
+                if (seg.j0 == 0 && (seg.m == 0 || !p.po.lockstep)) {
+                    const int last = prefix_holder(p.po, prefix_range->shares, unsigned(seg.row + 1) * p.po.nblk - 1);
+                    p.rows[seg.row] = make_int2(prefix_range->share + seg.row, last - prefix_range->share + 1);
+                }
+            }
+            __syncwarp();
+        }
+    }
 
     // Each role runs inside the branch that set its register limit, so the
     // compiler allocates each role's code under that role's limit.
@@ -790,10 +808,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int limit = min(p.po.rb, p.B - w.row0[t]) * p.G;  // rows of the tile in use
                 const size_t base = (size_t)w.s * p.po.id_rows + (p.po.lockstep ? w.m * p.po.unit_rows : 0) +
                                     t * (p.po.unit_rows / kNT);
-                if (t == 0 && r == 0 && w.jb == 0 && (w.m == 0 || !p.po.lockstep)) {
-                    const int last = prefix_holder(p.po, prefix_range->shares, unsigned(w.row + 1) * p.po.nblk - 1);
-                    p.rows[w.row] = make_int2(w.s, last - prefix_range->share + 1);
-                }
                 float *turn = reinterpret_cast<float *>(smem + kPrefixSmemOffset<D>) + (warp - 4) * kTurnFloats;
 #pragma unroll
                 for (int c = 0; c < D / 32; ++c) {

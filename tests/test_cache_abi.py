@@ -232,6 +232,6 @@ def test_evict_refusals(kw, code):
 def test_evict_workspace():
     ws = attn.attn_cache_evict_workspace_bytes
     assert ws(2, 2, 164, 100, True) == 0 and ws(2, 2, 165, 100, True) > 0  # few slots past the kept ones: one kernel
-    assert ws(2, 2, 164, 100, False) >= 4 * 4 * (100 + 2 * 64)
+    assert ws(2, 2, 164, 100, False) >= 4 * 4 * (100 + 64)  # a source for every slot, and the fillers
     assert ws(0, 2, 300, 100, True) == ws(2, 0, 300, 100, True) == ws(2, 2, 0, 100, True) == ws(2, 2, 300, 0, True) == 0
     assert ws(2, 2, 80, 100, False) >= 4 * 4 * 80  # a cache below the bound is only copied

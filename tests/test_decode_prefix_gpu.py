@@ -314,6 +314,27 @@ def test_wait_limit_is_reported_and_recovered(attn):
     run_and_check(attn, q, kp, vp, kc, vc, lens)
 
 
+@pytest.mark.parametrize("B,Hq,Hkv,P,S,d", [
+    (4, 16, 2, 3000, 1500, 128), (300, 8, 1, 700, 20, 64), (2, 8, 2, 900, 0, 128), (3, 8, 8, 0, 700, 64), (64, 64, 8, 4000, 90, 128),
+])
+def test_a_launch_that_gave_up_stays_in_bounds(attn, B, Hq, Hkv, P, S, d):
+    """With no time to wait the phases leave early.  What the merge and the weights
+    read out of the workspace as numbers and positions is there all the same."""
+    q, kp, vp, kc, vc = inputs(B, Hq, Hkv, P, S, d, 240)
+    lens = lens_for(B, S) if S else []
+    seq = torch.tensor(lens, dtype=torch.int32, device=DEV) if S else None
+    w = torch.zeros((B, Hkv, S), device=DEV) if S else None
+    ws = torch.full((attn.attn_decode_prefix_workspace_bytes(B, Hq, Hkv, P, d, S, bool(S)),), 0x7f, dtype=torch.uint8, device=DEV)
+    old = attn.attn_set_wait_timeout_ns(0)
+    try:
+        attn.decode_prefix(q, kp, vp, kc, vc, seq, weights=w, workspace=ws)
+        torch.cuda.synchronize()
+        assert attn.attn_device_status() == attn.ATTN_ERR_TIMEOUT
+    finally:
+        attn.attn_set_wait_timeout_ns(old)
+    run_and_check(attn, q, kp, vp, kc, vc, lens, workspace=ws)
+
+
 def test_helper_refusals(attn):
     q, kp, vp, kc, vc = inputs(2, 8, 2, 100, 16, 64, 220)
     seq = torch.tensor([1, 2], dtype=torch.int32, device=DEV)
