@@ -11,6 +11,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "libattn.so")
@@ -46,7 +47,6 @@ _IP = ctypes.POINTER(ctypes.c_int)
 _FP = ctypes.POINTER(ctypes.c_float)
 _D = ctypes.c_double
 _DP = ctypes.POINTER(ctypes.c_double)
-_LLP = ctypes.POINTER(ctypes.c_longlong)
 SIGNATURES = {
     "attn_fwd": (_I, [_P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _F, _I, _P]),
     "attn_fwd_ex": (_I, [_P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _F, _I, _I, _P]),
@@ -65,9 +65,9 @@ SIGNATURES = {
     "attn_decode_varlen": (_I, [_P, _P, _P, _P, _P, _I, _I, _I, _I, _F, _I, _P, _SZ, _P]),
     "attn_decode_varlen_workspace_bytes": (_SZ, [_I, _I, _I, _I]),
     "attn_decode_num_splits": (_I, [_I, _I, _I, _I]),
-    "attn_rope": (_I, [_P, _P, _P, _P, _P, _LL, _P, _I, _I, _I, _I, _I, _I, _I, _F, _I, _LLP, _P]),
+    "attn_rope": (_I, [_P, _P, _P, _P, _P, _LL, _P, _I, _I, _I, _I, _I, _I, _I, _F, _I, _P, _P]),
     "attn_rope_freqs": (_I, [_DP, _I, _D, _I, _D, _D, _D, _D]),
-    "attn_rope_append": (_I, [_P] * 13 + [_I] * 7 + [_F, _I, _LLP, _P]),
+    "attn_rope_append": (_I, [_P] * 13 + [_I] * 7 + [_F, _I, _P, _P]),
     "attn_decode_prefix": (_I, [_P] * 9 + [_I] * 5 + [_F, _I, _P, _SZ, _P]),
     "attn_decode_prefix_workspace_bytes": (_SZ, [_I] * 7),
     "attn_decode_prefix_segment": (_I, [_I] * 6 + [_LL] + [_I] * 3 + [_IP]),
@@ -339,7 +339,7 @@ def attn_version() -> int:
     return int(lib().attn_version())
 
 
-_Strides = _LL * 12  # (batch, head, token) element strides of four tensors
+_strides = struct.Struct("12q").pack  # a host array: (batch, head, token) element strides of four tensors
 
 
 def attn_rope(q, q_out, k, k_out, positions, position_stride, inv_freq, B, Hq, Hkv, N, d, rotary_dim, interleaved,
@@ -404,19 +404,20 @@ def attn_rope_freqs(rotary_dim, base=10000.0, rule=0, factor=1.0, low=1.0, high=
 # ----------------------------------------------------------- torch helpers
 def _fits(t, dtype, shape, gpu):
     """A contiguous tensor of this type and shape on this GPU."""
-    return t.dtype is dtype and t.shape == shape and t.get_device() == gpu and t.is_contiguous()
+    return t is not None and t.dtype is dtype and t.shape == shape and t.get_device() == gpu and t.is_contiguous()
 
 
 def _fits_rows(t, dtype, shape, gpu):
     """The same with any strides, columns contiguous."""
-    return t.dtype is dtype and t.shape == shape and t.get_device() == gpu and t.stride(-1) == 1
+    return t is not None and t.dtype is dtype and t.shape == shape and t.get_device() == gpu and t.stride(-1) == 1
 
 
 def _refuse(what, name, t, dtype, shape):
     """ATTN_ERR_ARG for a tensor that the call cannot take as it is: its
     address alone would not tell the library."""
+    got = "None" if t is None else f"{t.dtype} {tuple(t.shape)} on {t.device}, strides {t.stride()}"
     raise AttnError(ATTN_ERR_ARG, f"{what}: {name} has to be {dtype} {tuple(shape)}, on the GPU of the first tensor, with "
-                                  f"contiguous rows (got {t.dtype} {tuple(t.shape)} on {t.device}, strides {t.stride()})")
+                                  f"contiguous rows (got {got})")
 
 
 def _elsewhere(what, gpu, stream):
@@ -480,7 +481,7 @@ def rope(q, k, inv_freq, positions=None, interleaved=False, out_scale=1.0, out=N
     if out is not None and (q_out is None or (k is None) != (k_out is None)):
         raise AttnError(ATTN_ERR_ARG, "rope: out has to hold q_out, and k_out exactly where there is a k")
     if q_out is None:
-        q_out = torch.empty((B, Hq, N, d), dtype=bf16, device=q.device)
+        q_out = torch.empty_like(q, memory_format=torch.contiguous_format)
     else:
         _fits_rows(q_out, bf16, q.shape, gpu) or _refuse(what, "q_out", q_out, bf16, q.shape)
     Hkv, ks, kos = 0, (0, 0, 0, 1), (0, 0, 0, 1)
@@ -489,14 +490,14 @@ def rope(q, k, inv_freq, positions=None, interleaved=False, out_scale=1.0, out=N
         shape = (B, Hkv, N, d)
         _fits_rows(k, bf16, shape, gpu) or _refuse(what, "k", k, bf16, shape)
         if k_out is None:
-            k_out = torch.empty(shape, dtype=bf16, device=q.device)
+            k_out = torch.empty_like(k, memory_format=torch.contiguous_format)
         else:
             _fits_rows(k_out, bf16, shape, gpu) or _refuse(what, "k_out", k_out, bf16, shape)
         ks, kos = k.stride(), k_out.stride()
     rc = lib().attn_rope(q.data_ptr(), q_out.data_ptr(), None if k is None else k.data_ptr(),
                          None if k is None else k_out.data_ptr(), None if positions is None else positions.data_ptr(),
                          per_entry, inv_freq.data_ptr(), B, Hq, Hkv, N, d, 2 * pairs, interleaved, out_scale, inverse,
-                         _Strides(*q.stride()[:3], *q_out.stride()[:3], *ks[:3], *kos[:3]),
+                         _strides(*q.stride()[:3], *q_out.stride()[:3], *ks[:3], *kos[:3]),
                          torch._C._cuda_getCurrentRawStream(gpu))
     if rc:
         check(rc, "attn_rope")
@@ -545,7 +546,7 @@ def rope_append(q, k, v, kcache, vcache, seqlens, inv_freq=None, start_pos=None,
         rotary_dim = 2 * pairs
         _fits(inv_freq, torch.float64, (pairs,), gpu) or _refuse(what, "inv_freq", inv_freq, torch.float64, (pairs,))
     if q_out is None:
-        q_out = torch.empty((B, Hq, T, d), dtype=bf16, device=q.device)
+        q_out = torch.empty_like(q, memory_format=torch.contiguous_format)
     else:
         _fits_rows(q_out, bf16, q.shape, gpu) or _refuse(what, "q_out", q_out, bf16, q.shape)
     if seqlens_out is None:
@@ -559,7 +560,7 @@ def rope_append(q, k, v, kcache, vcache, seqlens, inv_freq=None, start_pos=None,
                                 None if weights is None else weights.data_ptr(),
                                 None if inv_freq is None else inv_freq.data_ptr(), B, Hq, Hkv, T, d, rotary_dim,
                                 interleaved, out_scale, s_max,
-                                _Strides(*q.stride()[:3], *q_out.stride()[:3], *k.stride()[:3], *v.stride()[:3]),
+                                _strides(*q.stride()[:3], *q_out.stride()[:3], *k.stride()[:3], *v.stride()[:3]),
                                 torch._C._cuda_getCurrentRawStream(gpu))
     if rc:
         check(rc, "attn_rope_append")
@@ -586,6 +587,8 @@ def decode_prefix(q, kprefix, vprefix, kcache, vcache, seqlens, scale=None, weig
     B, Hq, d = q.shape
     P = s_max = Hkv = 0
     _fits(q, bf16, q.shape, gpu) or _refuse(what, "q", q, bf16, q.shape)
+    if (kcache is None) != (vcache is None) or (kprefix is None) != (vprefix is None):
+        raise AttnError(ATTN_ERR_ARG, "decode_prefix: keys and values go together")
     if kcache is not None:
         Hkv, s_max = kcache.shape[1], kcache.shape[2]
         shape = (B, Hkv, s_max, d)

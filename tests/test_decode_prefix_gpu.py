@@ -349,6 +349,9 @@ def test_helper_refusals(attn):
         (lambda: attn.decode_prefix(q, kp, vp, None, None, None, weights=kc), attn.ATTN_ERR_ARG),
         (lambda: attn.decode_prefix(q, kp, vp, kc, vc, seq, workspace=small), attn.ATTN_ERR_WORKSPACE),
         (lambda: attn.decode_prefix(q, kp, vp, kc, vc, seq, scale=-1.0), attn.ATTN_ERR_ARG),
+        (lambda: attn.decode_prefix(q, kp, None, kc, vc, seq), attn.ATTN_ERR_ARG),
+        (lambda: attn.decode_prefix(q, kp, vp, None, vc, seq), attn.ATTN_ERR_ARG),
+        (lambda: attn.decode_prefix(q, kp, vp, kc, vc, None), attn.ATTN_ERR_ARG),
     ]:
         with pytest.raises(attn.AttnError) as e:
             call()
