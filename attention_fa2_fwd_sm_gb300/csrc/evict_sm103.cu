@@ -28,7 +28,7 @@
 // instead (256 rows of 4K keys, 1, 2, 4, 8 of them: 6.9, 8.9, 13.0, 21.2 us; by the
 // radix select 13.7).
 // move_kernel: 2 * 2 d bytes a row each way, HBM-bound (32 rows of 8000 keys to a
-// new cache: 273 MB, 41 us, 6.6 TB/s).  Where a cache has at most kFusedMoves slots
+// new cache: 262 MB, 42 us, 6.2 TB/s).  Where a cache has at most kFusedMoves slots
 // past `keep` (a decode loop that evicts what it appends) the selecting CTA moves
 // its rows itself and the second launch falls away (256 rows, 1 key of 4K: 6.9 us,
 // 22.7 with two launches; 64 keys of 4K 17.4 and 26; 16 of 16K in 64 rows 18.4 and 19).

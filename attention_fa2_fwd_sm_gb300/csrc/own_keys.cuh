@@ -13,7 +13,9 @@ namespace attn {
 
 namespace own {
 
-constexpr int kMinShare = 32;  // keys: two warps of a stage
+// Keys: two warps of a stage.  A step of 8 KV heads of 64 keys, of 300, of 3000: with 32
+// 9.6, 9.6, 11.6 us, with 64 11.0, 9.6, 10.3, with 128 13.7, 10.3, 11.0.
+constexpr int kMinShare = 32;
 
 __device__ __forceinline__ int length_of(const int *seqlens, int max_seqlen, int b) {
     return min(max(seqlens[b], 0), max_seqlen);

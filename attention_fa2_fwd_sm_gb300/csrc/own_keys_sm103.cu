@@ -10,11 +10,11 @@
 // ceil(T Hkv / groups) rounded up (find_share), however they fall on the sequences; a
 // share is cut into segments at the ends of the sequences' heads, the group's TMA
 // warp runs ahead over those ends while its other warps finish a segment, and the
-// SM's other groups are not held up by either.  (One CTA a chunk, as in the ragged
-// decode: 81 us on 128 sequences of 512 to 1024 keys, 8 KV heads, d = 128, and up to
-// 255 us on 32 of 8K to 16K, where 1.26 waves of equal chunks left SMs idle.)  The
-// lengths are on the device; every warp finds its place in them by itself, from
-// registers for up to 256 sequences.
+// SM's other groups are not held up by either.  128 sequences of 512 to 1024 keys, 64
+// heads, 8 KV heads, d = 128: 72 us with the merge, 5.6 TB/s; 32 of 8K to 16K: 225 us,
+// 7.1 TB/s.  (One CTA a chunk, as in the ragged decode: 81 us, and up to 255, where
+// 1.26 waves of equal chunks left SMs idle.)  The lengths are on the device; every
+// warp finds its place in them by itself, from registers for up to 256 sequences.
 //
 // Segment partials are numbered c + (row b * Hkv + g): both numbers go up along
 // the shares and one of them at every cut, so the numbers are distinct, a row's
@@ -27,8 +27,9 @@
 // decode_sm103.cu.  Heads on N take half the MMAs and half the accumulator
 // registers, which lets three groups share an SM instead of two; a stage takes its
 // group about 1600 clocks, mostly latency, and one CTA an SM has to draw HBM's full
-// rate from part of the SMs (about 100 GB/s each), because the prefix's kernel has
-// the others.
+// rate from part of the SMs, because the prefix's kernel has the others: 90 GB/s an
+// SM with up to 8 heads on N, 52 with them on M.  (On all SMs 72 and 74 us for the 128
+// sequences above, 225 and 230 for the 32.)
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 

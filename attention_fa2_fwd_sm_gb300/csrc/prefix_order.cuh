@@ -16,8 +16,9 @@
 // The prefix is bound by the tensor cores, the sequences' own keys by HBM, so
 // the two run at the same time on different SMs: the own keys' kernel, ahead on
 // the stream, holds `own` SMs (prefix_own_sms), the first `early` shares start at
-// once on the others, and the `late` ones wait for its SMs.  So that all end together, a late share is shorter by what the own
-// keys take, tau key blocks' worth of time, estimated from their number T:
+// once on the others, and the `late` ones wait for its SMs.  So that all end
+// together, a late share is shorter by what the own keys take, tau key blocks'
+// worth of time, estimated from their number T:
 //     early a + late b = total,  b = a - tau  (b = 0 where a <= tau).
 // The shares depend on the lengths alone, so results do not depend on timing.
 // Where nothing is left for the late ones and it makes no share much longer, every
@@ -184,7 +185,8 @@ inline bool prefix_order(PrefixOrder *o, int B, int G, int Hkv, int P, int d, in
     o->unit_rows = 2 * o->rb * G;
     o->id_rows = o->unit_rows * (o->lockstep ? o->mt : 1);
     o->ids = o->early + o->late + o->rows;
-    o->own_cost = own > 0 ? unsigned(4.0 * d / prefix_own_rate(d, G, own) / prefix_block_us(d, tiles > 1, prefix_own_rate(d, G, own)) * 4294967296.0) : 0u;
+    const double rate = prefix_own_rate(d, G, own);
+    o->own_cost = own > 0 ? unsigned(4.0 * d / rate / prefix_block_us(d, tiles > 1, rate) * 4294967296.0) : 0u;
     return true;
 }
 
