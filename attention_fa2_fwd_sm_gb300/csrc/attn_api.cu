@@ -641,6 +641,7 @@ int attn_rope(const void *q, void *q_out, const void *k, void *k_out, const int 
     int rc = rope_common(inv_freq, B, Hq, N, d, rotary_dim, out_scale, 2);
     if (rc != ATTN_OK) return rc;
     if (!aligned4(positions) || position_stride < 0 || (!k != !k_out) || (k && Hkv <= 0)) return ATTN_ERR_ARG;
+    if (k && (q_out == k || k_out == q || q_out == k_out)) return ATTN_ERR_ARG;
     RopeLaunch a;
     rc = rope_tensor(&a.t[0], q, q_out, strides, strides ? strides + 3 : nullptr, B, Hq, N, d);
     if (rc == ATTN_OK && k)
@@ -701,6 +702,9 @@ int attn_rope_append(const void *q, void *q_out, const void *k, const void *v, v
         ints_overlap(seqlens_out, new_lens, B))
         return ATTN_ERR_ARG;
     if (!aligned16(kcache) || !aligned16(vcache) || kcache == vcache) return ATTN_ERR_ARG;
+    for (const void *cache : {(const void *)kcache, (const void *)vcache})
+        if (cache == k || cache == v || cache == q || cache == q_out) return ATTN_ERR_ARG;
+    if (q_out == k || q_out == v) return ATTN_ERR_ARG;
     const long long row = (long long)max_seqlen * d;
     if ((double)B * Hkv * (double)row >= 9.0e18) return ATTN_ERR_ARG;
     RopeLaunch a;
@@ -797,7 +801,7 @@ int attn_decode_prefix(const void *q, const void *kprefix, const void *vprefix, 
 int attn_decode_prefix_segment(int B, int Hq, int Hkv, int P, int d, int max_seqlen, long long own_keys, int num_sms,
                                int cta, int i, int *out) {
     PrefixOrder o;
-    if (!out || P <= 0 || num_sms <= 0 || i < 0 || own_keys < 0 ||
+    if (!out || P <= 0 || num_sms <= 0 || num_sms > (1 << 20) || i < 0 || own_keys < 0 ||
         decode_prefix_sizes(B, Hq, Hkv, P, d, max_seqlen) != ATTN_OK ||
         !prefix_order(&o, B, Hq / Hkv, Hkv, P, d, own_ctas(B, Hq / Hkv, Hkv, P, d, max_seqlen, num_sms), num_sms) || cta < 0 ||
         cta >= prefix_grid(o))

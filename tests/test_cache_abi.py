@@ -47,13 +47,17 @@ def _rope(**kw):
     (dict(strides=strides(-8, 64, 64, *PACKED, *PACKED, *PACKED)), ARG),
     (dict(strides=strides(1 << 40, 64, 64, *PACKED, *PACKED, *PACKED)), ARG),
     (dict(q_out=A16, strides=strides(*PACKED, 2 * PACKED[0], PACKED[1], 64, *PACKED, *PACKED)), ARG),  # in place, moved
+    (dict(q_out=A16 + 8192), ARG), (dict(k_out=A16), ARG), (dict(k_out=A16 + 4096), ARG),     # one tensor laid over another
 ])
 def test_rope_refusals(kw, code):
     assert _rope(**kw) == code
 
 
+KC, VC = A16 + (1 << 20), A16 + (2 << 20)
+
+
 def _append(**kw):
-    a = dict(q=A16, q_out=A16 + 4096, k=A16, v=A16, kc=A16, vc=A16 + 16, lens=A16, start=None, new=None, out=A16 + 64,
+    a = dict(q=A16, q_out=A16 + 4096, k=A16 + 8192, v=A16 + 16384, kc=KC, vc=VC, lens=A16, start=None, new=None, out=A16 + 64,
              cache_pos=None, weights=None, freqs=A16, B=3, Hq=2, Hkv=2, T=1, d=64, r=64, inter=0, scale=1.0, S=16,
              strides=None)
     a.update(kw)
@@ -61,8 +65,9 @@ def _append(**kw):
 
 
 @pytest.mark.parametrize("kw,code", [
-    (dict(q=None), ARG), (dict(k=A16 + 8), ARG), (dict(v=None), ARG), (dict(kc=None), ARG), (dict(vc=A16), ARG),
-    (dict(vc=A16 + 4), ARG), (dict(lens=None), ARG), (dict(lens=A16 + 1), ARG), (dict(out=A16), ARG),
+    (dict(q=None), ARG), (dict(k=A16 + 8), ARG), (dict(v=None), ARG), (dict(kc=None), ARG), (dict(vc=KC), ARG),
+    (dict(vc=VC + 4), ARG), (dict(k=KC), ARG), (dict(v=KC), ARG), (dict(v=VC), ARG), (dict(q=KC), ARG), (dict(q_out=VC), ARG),
+    (dict(q_out=A16 + 8192), ARG), (dict(q_out=A16 + 16384), ARG), (dict(lens=None), ARG), (dict(lens=A16 + 1), ARG), (dict(out=A16), ARG),
     (dict(out=A16 + 8), ARG), (dict(start=A16 + 64), ARG), (dict(new=A16 + 72), ARG), (dict(cache_pos=A16 + 2), ARG),
     (dict(weights=A16 + 3), ARG), (dict(S=0), ARG), (dict(T=0), ARG), (dict(Hkv=0), ARG), (dict(r=-2), ARG),
     (dict(r=64, freqs=None), ARG), (dict(r=130, d=128), ARG), (dict(d=12), UNSUP), (dict(scale=-float("inf")), ARG),

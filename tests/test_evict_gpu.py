@@ -129,7 +129,8 @@ def test_positions(attn, in_place):
 
 
 @pytest.mark.parametrize("in_place,S,keep", [(True, 50001, 49990), (True, 60000, 20000), (False, 70000, 30001),
-                                             (False, 43008, 100), (True, 43009, 43000)])
+                                             (False, 43008, 100), (True, 43009, 43000), (True, 400001, 150000),
+                                             (False, 350000, 349000)])
 def test_long_rows(attn, in_place, S, keep):
     """Rows whose ranks fit in shared memory just so, and rows that do not."""
     check(attn, weights_of("plain", (1, 2, S)), [S], keep, 100, in_place=in_place)
