@@ -23,7 +23,8 @@
 // The shares depend on the lengths alone, so results do not depend on timing.
 // Where nothing is left for the late ones and it makes no share much longer, every
 // row gets a whole number of shares (`aligned` of them): a share that goes on in
-// the next row pays for a second start and end.
+// the next row pays for a second start and end (32 x (8K + 256 .. 512) keys 36.8 us,
+// 41.5 without).
 //
 // A CTA's share is one segment per row that it touches; each segment writes one
 // partial per query row, numbered share + row (both go up along the shares, one
@@ -146,8 +147,10 @@ inline double prefix_block_us(int d, bool two_tiles, double own_rate) {
 // SMs for the own keys' kernel beside a prefix, `most` at most: in proportion to
 // what the two have to do if the caches are three quarters full, so that in the
 // usual case no share has to wait, and leaving whole groups of mt.  128 x (32K
-// shared + 512 .. 1024 own) keys: 24 SMs 190 us, 32 153, 40 139, 48 149, 64 174 (with
-// the shares' balance; the two phases one after the other 176).
+// shared + 512 .. 1024 own) keys: 24 SMs 191 us, 32 153, 40 138, 48 143, 64 147, 104 172
+// (with the shares' balance; the two phases one after the other 176); 32 x (8K + 256
+// .. 512): 24 SMs 44, 32 37, 40 36.5, 48 34.5, 56 37, 76 45, 36.8 with the choice made
+// here; 64 x (8K + 256 .. 512) 69, 56, 49, 46, 46, 56, and 50.7.
 inline int prefix_own_sms(int B, int G, int Hkv, int P, int d, int max_seqlen, int most, int num_sms) {
     const int rb = kPrefixTileRows / G, tiles = (B + rb - 1) / rb, mt = (tiles + 1) / 2;
     const double own = 0.75 * B * Hkv * (double)max_seqlen * 4 * d / prefix_own_rate(d, G, 1);
