@@ -623,6 +623,85 @@ static int rope_tensor(RopeTensor *t, const void *in, void *out, const long long
     return ATTN_OK;
 }
 
+// A bf16 tensor [B, heads, N, d] by its strides, in units of 8 elements (16
+// bytes), which base, strides and rows are multiples of; heads = 0: absent.
+struct Rows {
+    const void *p = nullptr;
+    long long s[3] = {}, n[3] = {};
+    long long d = 0;
+    __int128 span = 0;  // from the first row to the last
+    Rows(const void *base, const long long (&strides)[3], int B, int H, int N, int cols) : p(H > 0 ? base : nullptr), d(cols / 8) {
+        const int extent[3] = {B, H, N};
+        for (int i = 0; i < 3; ++i) {
+            s[i] = strides[i] / 8, n[i] = extent[i];
+            span += (__int128)s[i] * (n[i] - 1);
+        }
+    }
+    bool same(const Rows &o) const {
+        if (p != o.p || d != o.d) return false;
+        for (int i = 0; i < 3; ++i)
+            if (n[i] != o.n[i] || (n[i] > 1 && s[i] != o.s[i])) return false;
+        return true;
+    }
+};
+
+// One dimension of the distance between an element of one tensor and an
+// element of another: it adds s * y, lo <= y <= hi.
+struct Reach {
+    __int128 s, lo, hi;
+};
+
+// Whether the distances at + sum s_i y_i meet (-width, width); the dimensions
+// by falling stride, so that after each only the few y_i are left that the
+// smaller ones can make up for.  `budget` bounds the search: strides that do
+// not nest can leave many, and such tensors pass for apart.
+static bool meets(const Reach *dim, int n, __int128 at, __int128 width, int *budget) {
+    if (--*budget < 0) return false;
+    if (n == 0) return at > -width && at < width;
+    __int128 lo = 0, hi = 0;  // what the smaller strides can add
+    for (int i = 1; i < n; ++i) lo += dim[i].s * dim[i].lo, hi += dim[i].s * dim[i].hi;
+    // -width < at + s y + [lo, hi] < width
+    const __int128 s = dim[0].s;
+    auto floor_div = [&](__int128 x) { return x >= 0 ? x / s : -((-x + s - 1) / s); };
+    __int128 first = floor_div(-width - at - hi) + 1, last = -floor_div(-(width - at - lo)) - 1;
+    if (first < dim[0].lo) first = dim[0].lo;
+    if (last > dim[0].hi) last = dim[0].hi;
+    for (__int128 y = first; y <= last && *budget >= 0; ++y)
+        if (meets(dim + 1, n - 1, at + s * y, width, budget)) return true;
+    return false;
+}
+
+// Whether the two share an element.  Views of one fused projection interleave
+// without sharing any, so their address ranges do not tell.
+static bool share_elements(const Rows &a, const Rows &b) {
+    if (!a.p || !b.p) return false;
+    // Rows of the same width meet where they start less than it apart.
+    const __int128 apart = ((__int128)reinterpret_cast<uintptr_t>(a.p) - (__int128)reinterpret_cast<uintptr_t>(b.p)) / 16;
+    if (apart + a.span <= -a.d || apart - b.span >= a.d) return false;
+    Reach dim[6];
+    int n = 0;
+    auto add = [&](long long s, long long lo, long long hi) {
+        if (s == 0 || lo == hi) return;
+        for (int i = 0; i < n; ++i)
+            if (dim[i].s == s) {
+                dim[i].lo += lo, dim[i].hi += hi;
+                return;
+            }
+        int i = n++;
+        for (; i > 0 && dim[i - 1].s < s; --i) dim[i] = dim[i - 1];
+        dim[i] = {s, lo, hi};
+    };
+    for (int i = 0; i < 3; ++i) {
+        add(a.s[i], 0, a.n[i] - 1);
+        add(b.s[i], 1 - b.n[i], 0);
+    }
+    int budget = 2000;
+    return meets(dim, n, apart, a.d, &budget);
+}
+
+static Rows rows_in(const RopeTensor &t, int B, int N, int d) { return Rows(t.in, {t.in_b, t.in_h, t.in_n}, B, t.heads, N, d); }
+static Rows rows_out(const RopeTensor &t, int B, int N, int d) { return Rows(t.out, {t.out_b, t.out_h, t.out_n}, B, t.heads, N, d); }
+
 static bool aligned4(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 
 static int rope_common(const double *inv_freq, int B, int Hq, int N, int d, int rotary_dim, float out_scale,
@@ -641,12 +720,17 @@ int attn_rope(const void *q, void *q_out, const void *k, void *k_out, const int 
     int rc = rope_common(inv_freq, B, Hq, N, d, rotary_dim, out_scale, 2);
     if (rc != ATTN_OK) return rc;
     if (!aligned4(positions) || position_stride < 0 || (!k != !k_out) || (k && Hkv <= 0)) return ATTN_ERR_ARG;
-    if (k && (q_out == k || k_out == q || q_out == k_out)) return ATTN_ERR_ARG;
     RopeLaunch a;
     rc = rope_tensor(&a.t[0], q, q_out, strides, strides ? strides + 3 : nullptr, B, Hq, N, d);
     if (rc == ATTN_OK && k)
         rc = rope_tensor(&a.t[1], k, k_out, strides ? strides + 6 : nullptr, strides ? strides + 9 : nullptr, B, Hkv, N, d);
     if (rc != ATTN_OK) return rc;
+    for (int i = 0; i < 2; ++i)
+        for (int j = 0; j < 2; ++j) {
+            const Rows in = rows_in(a.t[i], B, N, d), out = rows_out(a.t[j], B, N, d);
+            if (!(i == j && in.same(out)) && share_elements(in, out)) return ATTN_ERR_ARG;
+        }
+    if (share_elements(rows_out(a.t[0], B, N, d), rows_out(a.t[1], B, N, d))) return ATTN_ERR_ARG;
     a.inv_freq = inv_freq;
     a.pos = positions;
     a.pos_stride = position_stride;
@@ -701,10 +785,7 @@ int attn_rope_append(const void *q, void *q_out, const void *k, const void *v, v
     if (ints_overlap(seqlens_out, seqlens, B) || ints_overlap(seqlens_out, start_pos, B) ||
         ints_overlap(seqlens_out, new_lens, B))
         return ATTN_ERR_ARG;
-    if (!aligned16(kcache) || !aligned16(vcache) || kcache == vcache) return ATTN_ERR_ARG;
-    for (const void *cache : {(const void *)kcache, (const void *)vcache})
-        if (cache == k || cache == v || cache == q || cache == q_out) return ATTN_ERR_ARG;
-    if (q_out == k || q_out == v) return ATTN_ERR_ARG;
+    if (!aligned16(kcache) || !aligned16(vcache)) return ATTN_ERR_ARG;
     const long long row = (long long)max_seqlen * d;
     if ((double)B * Hkv * (double)row >= 9.0e18) return ATTN_ERR_ARG;
     RopeLaunch a;
@@ -718,6 +799,16 @@ int attn_rope_append(const void *q, void *q_out, const void *k, const void *v, v
         a.t[i].out_n = d;
     }
     if (rc != ATTN_OK) return rc;
+    // The outputs: q_out (which may be q) and all of both caches.
+    const Rows rotated = rows_out(a.t[0], B, T, d), caches[2] = {rows_out(a.t[1], B, max_seqlen, d), rows_out(a.t[2], B, max_seqlen, d)};
+    for (int i = 0; i < 3; ++i) {
+        const Rows in = rows_in(a.t[i], B, T, d);
+        if ((i > 0 || !in.same(rotated)) && share_elements(in, rotated)) return ATTN_ERR_ARG;
+        for (const Rows &cache : caches)
+            if (share_elements(in, cache)) return ATTN_ERR_ARG;
+    }
+    if (share_elements(rotated, caches[0]) || share_elements(rotated, caches[1]) || share_elements(caches[0], caches[1]))
+        return ATTN_ERR_ARG;
     a.inv_freq = inv_freq;
     a.pos = start_pos;
     a.B = B;

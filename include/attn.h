@@ -431,7 +431,10 @@ int attn_decode_num_splits(int B, int Hq, int Hkv, int max_seqlen);
  *              The strides of a dimension of extent 1 are ignored.
  *   d a multiple of 8, at most 512; rotary_dim even, 2 <= rotary_dim <= d.
  *   q_out == q (k_out == k) works in place where the strides are equal too;
- *   any other overlap of an output with an input or an output is not allowed.
+ *   any other overlap of an output with an input or an output of q and k is
+ *   not allowed and refused (views that interleave without sharing an element,
+ *   as those of one fused projection do, do not overlap; strides that do not
+ *   nest are taken on trust).
  * One kernel on `stream`.
  */
 int attn_rope(const void *q, void *q_out, const void *k, void *k_out, const int *positions,
@@ -490,7 +493,9 @@ int attn_rope_freqs(double *inv_freq, int rotary_dim, double base, int rule, dou
  *   strides    HOST array of 12 element strides, or NULL: (batch, head, token)
  *              of q, q_out, k, v, as in attn_rope.
  * No other row of the caches, cache_pos or weights is touched.  q_out == q is
- * allowed as in attn_rope.  One kernel on `stream`.
+ * allowed as in attn_rope; q_out, kcache and vcache may otherwise overlap neither
+ * each other nor q, k or v, whichever rows the lengths name (refused as in
+ * attn_rope).  One kernel on `stream`.
  */
 int attn_rope_append(const void *q, void *q_out, const void *k, const void *v, void *kcache, void *vcache,
                      const int *seqlens, const int *start_pos, const int *new_lens, int *seqlens_out,

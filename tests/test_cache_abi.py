@@ -76,6 +76,34 @@ def test_append_refusals(kw, code):
     assert _append(**kw) == code
 
 
+CACHE_ROWS = (2 * 16 * 64, 16 * 64, 64)  # strides of a [3, 2, T, 64] view of a cache of 16 rows
+NEW = (2 * 64, 64, 0)                    # those of [3, 2, 1, 64] tokens
+
+
+@pytest.mark.parametrize("kw", [
+    dict(q_out=A16 + 2048), dict(k_out=A16 + 128), dict(q_out=A16 + 8192 - 4096), dict(k_out=A16 + 12288 - 128),  # one row in the other
+    # q_out in the rows of q one token further; k_out in a gap of k that is too narrow for it
+    dict(q_out=A16 + 128, strides=strides(*PACKED, *PACKED, *PACKED, *PACKED)),
+    dict(q=A16, q_out=1 << 24, k=A16 + 2048, k_out=A16 + 2048 + 64,
+         strides=strides(4 * 64 * 16, 64, 4 * 64, *PACKED, 4 * 64 * 16, 64, 4 * 64, 4 * 64 * 16, 64, 4 * 64)),
+])
+def test_rope_refuses_partial_overlaps(kw):
+    """[3, 2, 16, 64] tensors are 12288 bytes; these share some of their rows."""
+    assert _rope(**dict(dict(q=A16, q_out=1 << 24, k=1 << 25, k_out=1 << 26), **kw)) == ARG
+
+
+@pytest.mark.parametrize("kw", [
+    # tokens that lie in a cache: its rows 3.., the last one's last element, the other cache
+    dict(k=KC + 3 * 128, strides=strides(*NEW, *NEW, *CACHE_ROWS, *NEW)), dict(v=KC + 3 * 128, strides=strides(*NEW, *NEW, *NEW, *CACHE_ROWS)),
+    dict(k=VC + 5 * 128, strides=strides(*NEW, *NEW, *CACHE_ROWS, *NEW)), dict(k=KC + 3 * 2 * 16 * 128 - 128), dict(q=VC - 640),
+    dict(q_out=KC + 128), dict(vc=KC + 3 * 2 * 16 * 128 - 16), dict(kc=VC + 16),  # the caches in each other
+    dict(q_out=A16 + 8192 + 128), dict(q_out=A16 + 16384 - 128), dict(q_out=A16 + 128),
+])
+def test_append_refuses_partial_overlaps(kw):
+    """Caches [3, 2, 16, 64] are 12288 bytes, new tokens [3, 2, 1, 64] 768."""
+    assert _append(**kw) == ARG
+
+
 def test_frequency_rules():
     r, base, L = 64, 10000.0, 4096.0
     plain = [base ** (-2 * i / r) for i in range(r // 2)]

@@ -302,3 +302,37 @@ def test_rows_past_two_to_the_31_elements(attn):
     assert torch.equal(vc[1, :, S - 1], v[1, :, 0]) and not kc[1, :, :S - 1].any() and not kc[0, :, :S - 2].any()
     del kc, vc
     torch.cuda.empty_cache()
+
+
+def test_views_that_interleave_do_not_overlap(attn):
+    """In place through one fused projection, whose q, k and v lie between one another: rotation and appending give what they give on separate
+    tensors, v stays; so do tensors in the two halves of one buffer's columns, and outputs behind inputs in one allocation."""
+    dev = torch.device("cuda")
+    B, Hq, Hkv, N, d = 3, 6, 2, 19, 64
+    f = freqs(d).to(dev)
+    qkv = normal_bf16((B, N, Hq + 2 * Hkv, d), 90, dev)
+    q, k, v = qkv.transpose(1, 2).split([Hq, Hkv, Hkv], dim=1)
+    want, kept = attn.rope(q, k, f), v.clone()
+    lens = torch.tensor([0, 4, 30], dtype=torch.int32, device=dev)
+    caches = [torch.zeros((B, Hkv, 40, d), dtype=torch.bfloat16, device=dev) for _ in range(4)]
+    q1, _ = attn.rope_append(q.clone(), k.clone(), v.clone(), *caches[:2], lens, f)
+    q2 = normal_bf16((B, N, Hq + 2 * Hkv, d), 90, dev)
+    qs, ks, vs = q2.transpose(1, 2).split([Hq, Hkv, Hkv], dim=1)
+    attn.rope_append(qs, ks, vs, *caches[2:], lens, f, q_out=qs)
+    assert torch.equal(qs, q1) and torch.equal(caches[0], caches[2]) and torch.equal(caches[1], caches[3])
+    attn.rope(q, k, f, out=(q, k))
+    assert torch.equal(q, want[0]) and torch.equal(k, want[1]) and torch.equal(v, kept)
+    both = normal_bf16((B, Hq, N, 2 * d), 91, dev)
+    a, b = both[..., :d], both[..., d:]
+    want = attn.rope(a, None, f)[0]
+    attn.rope(a, None, f, out=(b, None))
+    assert torch.equal(b, want)
+    pool = normal_bf16((2, B, Hq, N, d), 92, dev)
+    want = attn.rope(pool[0], None, f)[0]
+    attn.rope(pool[0], None, f, out=(pool[1], None))
+    assert torch.equal(pool[1], want)
+    # keys in every other token of a longer row of tokens, the outputs in those between them
+    rows = normal_bf16((B, Hkv, 2 * N, d), 93, dev)
+    want = attn.rope(q, rows[:, :, ::2], f)[1]
+    attn.rope(q, rows[:, :, ::2], f, out=(want.new_empty(q.shape), rows[:, :, 1::2]))
+    assert torch.equal(rows[:, :, 1::2], want)
