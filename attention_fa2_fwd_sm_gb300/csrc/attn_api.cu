@@ -894,7 +894,7 @@ int attn_decode_prefix_segment(int B, int Hq, int Hkv, int P, int d, int max_seq
     PrefixOrder o;
     if (!out || P <= 0 || num_sms <= 0 || num_sms > (1 << 20) || i < 0 || own_keys < 0 ||
         decode_prefix_sizes(B, Hq, Hkv, P, d, max_seqlen) != ATTN_OK ||
-        !prefix_order(&o, B, Hq / Hkv, Hkv, P, d, own_ctas(B, Hq / Hkv, Hkv, P, d, max_seqlen, num_sms), num_sms) || cta < 0 ||
+        !prefix_order(&o, B, Hq / Hkv, Hkv, P, d, max_seqlen, own_ctas(B, Hq / Hkv, Hkv, P, d, max_seqlen, num_sms), num_sms) || cta < 0 ||
         cta >= prefix_grid(o))
         return ATTN_ERR_ARG;
     const PrefixShares s = prefix_shares(o, own_keys * Hkv);

@@ -184,10 +184,8 @@ struct DecodePrefixLaunch {
     unsigned long long wait_ns;
     int num_sms;
 };
-// CTAs (one an SM) of the own keys' kernel, and the groups of a CTA, which have a
-// share each.
+// CTAs (one an SM) of the own keys' kernel.
 int own_ctas(int B, int G, int Hkv, int P, int d, int max_seqlen, int num_sms);
-int own_groups(int G);
 // False when the sizes are outside what the launches can count.
 bool decode_prefix_layout(int B, int Hq, int Hkv, int P, int d, int max_seqlen, bool weights, int num_sms,
                           PrefixLayout *l);

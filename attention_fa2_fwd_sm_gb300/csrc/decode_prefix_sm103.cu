@@ -365,7 +365,7 @@ int launch_all(const DecodePrefixLaunch &a, cudaStream_t stream) {
         m.seqlens = a.seqlens;
     }
     if (a.P > 0) {
-        prefix_order(&m.po, a.B, G, a.Hkv, a.P, a.d, l.own_ctas, a.num_sms);
+        prefix_order(&m.po, a.B, G, a.Hkv, a.P, a.d, a.max_seqlen, l.own_ctas, a.num_sms);
         const int rc = launch_prefix<D>(a, l, m.po, stream);
         if (rc) return rc;
         m.pre_rows = reinterpret_cast<const int2 *>(a.workspace + l.pre_rows);
@@ -414,8 +414,6 @@ int launch_all(const DecodePrefixLaunch &a, cudaStream_t stream) {
 
 }  // namespace
 
-int own_groups(int G) { return G > 8 ? 2 : 3; }
-
 int own_ctas(int B, int G, int Hkv, int P, int d, int max_seqlen, int num_sms) {
     if (max_seqlen <= 0) return 0;
     const long long keys = (long long)B * Hkv * max_seqlen;
@@ -430,7 +428,7 @@ bool decode_prefix_layout(int B, int Hq, int Hkv, int P, int d, int max_seqlen, 
     const size_t rows = (size_t)B * Hq;
     l->own_ctas = own_ctas(B, Hq / Hkv, Hkv, P, d, max_seqlen, num_sms);
     PrefixOrder po = {};
-    if (P > 0 && !prefix_order(&po, B, Hq / Hkv, Hkv, P, d, l->own_ctas, num_sms)) return false;
+    if (P > 0 && !prefix_order(&po, B, Hq / Hkv, Hkv, P, d, max_seqlen, l->own_ctas, num_sms)) return false;
     const size_t parts = max_seqlen > 0 ? (size_t)l->own_ctas * own_groups(Hq / Hkv) + (size_t)B * Hkv : 0;
     const size_t pre = (size_t)po.ids * po.id_rows;
     if (parts > 0x7fffffff) return false;

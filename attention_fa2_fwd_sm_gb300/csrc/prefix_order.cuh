@@ -54,7 +54,9 @@ struct PrefixOrder {
     int ids;          // partial numbers
     int rows;         // rows of the order
     unsigned total;   // key blocks over all of them; below 2^30, as every product below
-    unsigned own_cost;  // key blocks' worth of time of one own key and KV head, in 2^-32
+    // Key blocks' worth of time that the own keys' kernel takes for one key of one KV
+    // head, in 2^-32, and that it takes whatever the number of keys.
+    unsigned own_key, own_rows;
 };
 
 // Lengths of the early and the late shares; aligned: shares per row, or 0.
@@ -71,11 +73,12 @@ ATTN_HD int prefix_grid(const PrefixOrder &o) { return (o.early + o.late) * (o.l
 ATTN_HD int prefix_share(const PrefixOrder &o, int cta) { return o.lockstep ? cta / o.mt : cta; }
 ATTN_HD int prefix_row(const PrefixOrder &o, int g, int m) { return o.lockstep ? g : g * o.mt + m; }
 
-// T: own keys over all KV heads.
-ATTN_HD PrefixShares prefix_shares(const PrefixOrder &o, long long T) {
+// `keys`: own keys over all KV heads.
+ATTN_HD PrefixShares prefix_shares(const PrefixOrder &o, long long keys) {
     const unsigned e = unsigned(o.early), l = unsigned(o.late);
-    // (no memory holds 2^38 keys, and own_cost is below 2^26)
-    const unsigned long long wide = (unsigned long long)(T < (1LL << 38) ? T : (1LL << 38)) * o.own_cost >> 32;
+    // (no memory holds 2^38 keys, and own_key is below 2^26)
+    unsigned long long wide = (unsigned long long)(keys < (1LL << 38) ? keys : (1LL << 38)) * o.own_key >> 32;
+    if (keys > 0) wide += o.own_rows;
     const unsigned tau = wide < (1u << 30) ? unsigned(wide) : (1u << 30);
     PrefixShares s;
     s.a = (o.total + e - 1) / e;
@@ -130,12 +133,26 @@ ATTN_HD PrefixSegment prefix_segment(const PrefixOrder &o, unsigned hi, int cta,
     return s;
 }
 
-// Measured rates.  The own keys' kernel draws this many bytes a microsecond on
-// `own` SMs (segments of 768 keys; a third more in long ones), up to what HBM gives.
-constexpr double kHbmRate = 6.0e6;
-inline double prefix_own_rate(int d, int G, int own) {
-    const double sm = (d == 128 ? (G > 8 ? 52.0 : 90.0) : (G > 8 ? 38.0 : 75.0)) * 1e3;
-    return own * sm < kHbmRate ? own * sm : kHbmRate;
+// Groups of an own keys' CTA, which have a share each.
+inline int own_groups(int G) { return G > 8 ? 2 : 3; }
+
+// Measured times of the own keys' kernel beside the prefix's: a group of a CTA
+// takes `row` microseconds to start and end a segment and `key` for each of its
+// keys, so 3 KV heads of 768 keys at once come to 90 GB/s an SM (d = 128, up to
+// 8 heads a KV head), 3 of 12 keys to 7 GB/s.  All of its SMs together draw at
+// most what HBM gives.
+constexpr double kHbmRate = 6.0e6;  // bytes a microsecond
+struct OwnTimes {
+    double row, key;
+};
+inline OwnTimes prefix_own_times(int d, int G) {
+    if (d == 128) return G > 8 ? OwnTimes{3.6, 0.0150} : OwnTimes{2.5, 0.0138};
+    return G > 8 ? OwnTimes{1.9, 0.0110} : OwnTimes{1.55, 0.00825};
+}
+// Microseconds that `held` rows with `keys` keys in all keep one SM busy.
+inline double prefix_own_us(int d, int G, double held, double keys) {
+    const OwnTimes t = prefix_own_times(d, G);
+    return (held * t.row + keys * t.key) / own_groups(G);
 }
 // A unit's key block takes this many microseconds, with two tiles and with one;
 // twice that beside own keys that take all of HBM's rate.
@@ -144,24 +161,37 @@ inline double prefix_block_us(int d, bool two_tiles, double own_rate) {
     return own_rate < kHbmRate ? us : 2 * us;
 }
 
+// A late share starts when the own keys are done, and the microseconds until its
+// first product overlap nothing: without them 16 x (32K + 1K .. 2K) keys give late
+// shares of one block (58.5 us, 53.5).
+constexpr double kLateStart = 2.0;
+
+// Units in lockstep: whether that leaves at most a tenth of the SMs idle.
+ATTN_HD bool prefix_lockstep(int mt, int num_sms) { return 10LL * (num_sms / mt) * mt >= 9LL * num_sms; }
+
 // SMs for the own keys' kernel beside a prefix, `most` at most: in proportion to
-// what the two have to do if the caches are three quarters full, so that in the
-// usual case no share has to wait, and leaving whole groups of mt.  128 x (32K
-// shared + 512 .. 1024 own) keys: 24 SMs 191 us, 32 153, 40 138, 48 143, 64 147, 104 172
-// (with the shares' balance; the two phases one after the other 176); 32 x (8K + 256
-// .. 512): 24 SMs 44, 32 37, 40 36.5, 48 34.5, 56 37, 76 45, 36.8 with the choice made
-// here; 64 x (8K + 256 .. 512) 69, 56, 49, 46, 46, 56, and 50.7.
+// what the two have to do if the caches are three quarters full, and rounded up,
+// in lockstep until the prefix starts on whole groups of mt: with too few of them
+// the late shares wait for the own keys, with too many they just start sooner.
+// In us, by SMs: 128 x (32K shared + 512 .. 1024 own) keys: 24 193, 32 154, 40 (the
+// choice) 138, 48 148, 64 150, 104 171, and 176 with one phase behind the other;
+// 32 x (8K + 256 .. 512): 24 43, 32 35, 48 34, 64 37, 70 (the choice) 36, 76 42. Short
+// own lengths, where a row's start and end are all of its time: 128 x (32K + 8 .. 16)
+// 1 SM 958, 4 307, 12 (the choice) 148, 32 118; 32 x (8K + 8 .. 16) 4 84, 41 24.7;
+// 1216 x (8K + 32 .. 64) 1 SM 9350, 40 440, 76 (the choice) 354.
 inline int prefix_own_sms(int B, int G, int Hkv, int P, int d, int max_seqlen, int most, int num_sms) {
     const int rb = kPrefixTileRows / G, tiles = (B + rb - 1) / rb, mt = (tiles + 1) / 2;
-    const double own = 0.75 * B * Hkv * (double)max_seqlen * 4 * d / prefix_own_rate(d, G, 1);
+    const double held = (double)B * Hkv, keys = 0.75 * held * max_seqlen;
+    const double own = prefix_own_us(d, G, held, keys);
     int left = num_sms;  // SMs that the prefix starts on
     for (int i = 0; i < 2; ++i) {  // at first as if the own keys left bandwidth over
-        const double prefix = (double)Hkv * mt * ((P + kPrefixBlock - 1) / kPrefixBlock) *
-                              prefix_block_us(d, tiles > 1, prefix_own_rate(d, G, num_sms - left));
-        left = int(num_sms * (prefix / (own + prefix)) + 0.5);
+        const double rate = keys * 4 * d * (num_sms - left) / own;
+        const double prefix = (double)Hkv * mt * ((P + kPrefixBlock - 1) / kPrefixBlock) * prefix_block_us(d, tiles > 1, rate);
+        left = int(num_sms * (prefix / (own + prefix)));
     }
-    left = mt < num_sms ? (left + mt / 2) / mt * mt : left;
-    if (left < (mt < num_sms ? mt : 1)) left = mt < num_sms ? mt : 1;
+    const int whole = prefix_lockstep(mt, num_sms) ? mt : 1;
+    left = left / whole * whole;
+    if (left < whole) left = whole;
     int sms = num_sms - left;
     if (sms < 1) sms = 1;
     return sms < most ? sms : most;
@@ -169,13 +199,13 @@ inline int prefix_own_sms(int B, int G, int Hkv, int P, int d, int max_seqlen, i
 
 // `own`: SMs that the own keys' kernel holds (0: none).  False when the problem
 // is outside the order's 32-bit counters.
-inline bool prefix_order(PrefixOrder *o, int B, int G, int Hkv, int P, int d, int own, int num_sms) {
+inline bool prefix_order(PrefixOrder *o, int B, int G, int Hkv, int P, int d, int max_seqlen, int own, int num_sms) {
     o->nblk = (P + kPrefixBlock - 1) / kPrefixBlock;
     o->rb = kPrefixTileRows / G;
     const int tiles = (B + o->rb - 1) / o->rb;
     o->mt = (tiles + 1) / 2;
     const int groups = num_sms / o->mt;
-    o->lockstep = 10LL * groups * o->mt >= 9LL * num_sms;
+    o->lockstep = prefix_lockstep(o->mt, num_sms);
     const int shares = o->lockstep ? groups : num_sms;
     const long long rows = (long long)Hkv * (o->lockstep ? 1 : o->mt), total = rows * o->nblk;
     if (total >= (1LL << 30)) return false;
@@ -188,8 +218,17 @@ inline bool prefix_order(PrefixOrder *o, int B, int G, int Hkv, int P, int d, in
     o->unit_rows = 2 * o->rb * G;
     o->id_rows = o->unit_rows * (o->lockstep ? o->mt : 1);
     o->ids = o->early + o->late + o->rows;
-    const double rate = prefix_own_rate(d, G, own);
-    o->own_cost = own > 0 ? unsigned(4.0 * d / rate / prefix_block_us(d, tiles > 1, rate) * 4294967296.0) : 0u;
+    o->own_key = o->own_rows = 0;
+    if (own > 0) {
+        const double held = (double)B * Hkv, keys = 0.75 * held * max_seqlen;
+        const double rate = keys * 4 * d * own / prefix_own_us(d, G, held, keys);
+        const double block = prefix_block_us(d, tiles > 1, rate);
+        const OwnTimes t = prefix_own_times(d, G);
+        const double sms = own_groups(G) * own;
+        o->own_key = unsigned((rate < kHbmRate ? t.key / sms : 4.0 * d / kHbmRate) / block * 4294967296.0);
+        const double rows = ((rate < kHbmRate ? held * t.row / sms : 0.0) + kLateStart) / block;
+        o->own_rows = rows < 1e9 ? unsigned(rows + 0.5) : 1000000000u;
+    }
     return true;
 }
 

@@ -218,6 +218,42 @@ def test_prefix_shares_leave_room_for_the_own_keys():
     assert all(sum(x) == 4 * 8 * 256 for x in loads)
 
 
+OWN_US = {(128, False): (2.0, 0.0112), (128, True): (3.0, 0.0127), (64, False): (1.4, 0.0074), (64, True): (1.7, 0.0097)}
+
+
+def test_own_keys_get_the_sms_that_they_need(tmp_path):
+    """Beside a prefix the own keys' kernel gets its SMs from the sizes.  A group of one of its CTAs takes OWN_US (measured on
+    its own) for a row and for each key of it; at caches three quarters full that must not outlast the
+    prefix's work on the SMs that it starts on (which takes up to twice as long beside own keys at
+    HBM's rate), however short the caches are and however the prefix's groups divide the GPU."""
+    import os
+    import subprocess
+    src, exe = tmp_path / "sms.cpp", tmp_path / "sms"
+    csrc = os.path.join(os.path.dirname(attn.__file__), "csrc")
+    src.write_text('#include <cstdio>\n#include "prefix_order.cuh"\nint main() {\n    int B, G, H, P, d, S, most;\n'
+                   '    while (scanf("%d%d%d%d%d%d%d", &B, &G, &H, &P, &d, &S, &most) == 7)\n'
+                   '        printf("%d\\n", attn::prefix_own_sms(B, G, H, P, d, S, most, 152));\n}\n')
+    subprocess.run(["g++", "-std=c++17", "-O1", "-I", csrc, str(src), "-o", str(exe)], check=True)
+    cases = [(B, G, H, P, d, S) for B in (4, 16, 32, 64, 128, 300, 512, 1216, 2000) for G in (1, 8, 16) for H in (2, 8)
+             for P in (8192, 16384, 32768) for d in (64, 128) for S in (1, 16, 32, 40, 45, 48, 64, 128, 256, 1024)]
+    most = lambda B, G, H, S: min(152, -(-B * H * S // (32 * (2 if G > 8 else 3))))
+    lines = [" ".join(map(str, (*c, most(c[0], c[1], c[2], c[5])))) for c in cases]
+    out = subprocess.run([str(exe)], input="\n".join(lines), capture_output=True, text=True, check=True).stdout.split()
+    assert len(out) == len(cases)
+    for (B, G, H, P, d, S), sms in zip(cases, map(int, out)):
+        tiles = -(-B // (128 // G))
+        mt = (tiles + 1) // 2
+        row, key = OWN_US[d, G > 8]
+        own = B * H * (row + key * 0.75 * S) / (2 if G > 8 else 3) / sms
+        block = (1.37 if tiles > 1 else 1.0) if d == 64 else 1.55 if tiles > 1 else 1.2
+        lockstep = 10 * (152 // mt) * mt >= 9 * 152 if mt <= 152 else False
+        start = 152 - sms
+        if lockstep and start // mt == 1 or start <= 1 or sms >= most(B, G, H, S):
+            continue  # one group of the prefix is left, or every share of the own keys has a group
+        prefix = H * mt * -(-P // 128) * block / (start // mt * mt if lockstep else start)
+        assert own <= 2 * prefix, (B, G, H, P, d, S, sms, own, prefix)
+
+
 def test_prefix_segment_refusals():
     ok = dict(B=2, Hq=4, Hkv=2, P=100, d=128, S=10, own=5, sms=152, cta=0, i=0)
     assert attn.attn_decode_prefix_segment(*ok.values()) == (0, 0, 0, 1, 0, 0)
