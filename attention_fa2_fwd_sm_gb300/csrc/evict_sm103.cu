@@ -29,14 +29,16 @@
 // radix select 13.7).
 // move_kernel: 2 * 2 d bytes a row each way, HBM-bound (32 rows of 8000 keys to a
 // new cache: 262 MB, 42 us, 6.2 TB/s).  Where a cache has at most kFusedMoves slots
-// past `keep` (a decode loop that evicts what it appends) the selecting CTA moves
-// its rows itself and the second launch falls away (256 rows, 1 key of 4K: 6.9 us,
-// 22.7 with two launches; 64 keys of 4K 17.4 and 26; 16 of 16K in 64 rows 18.4 and 19).
+// past `keep` (a decode loop that evicts what it appends) the selecting CTA or
+// cluster moves its rows itself and the second launch falls away (256 rows, 1 key of
+// 4K: 5.7 us, 15.8 with two launches; 64 keys of 4K 12.5 and 15.8; 16 of 16K in 64 rows
+// 14.7 and 17.8; of 128K in 8 rows 20.4 and 21.8).
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
 #include <cmath>
+#include <type_traits>
 
 #include "../../include/attn.h"
 #include "attn_internal.h"
@@ -131,11 +133,14 @@ __device__ __forceinline__ void visit(int i0, int i1, int step, Load load, F f) 
     }
 }
 
-// A cluster selects the kept keys of one row.  kFused: a single CTA, which also
-// moves them.
-template <bool kShared, bool kFused, int kThreads>
+// Who moves the kept keys: move_kernel, or the CTA or the cluster that selects them.
+enum Mover { kLater = 0, kCta = 1, kCluster = 2 };
+
+// A cluster (kCta: a single CTA) selects the kept keys of one row.
+template <bool kShared, Mover kMover, int kThreads>
 __global__ void __launch_bounds__(kThreads) select_kernel(const Params p) {
     namespace cg = cooperative_groups;
+    constexpr bool kFused = kMover != kLater;
     constexpr int kWarps = kThreads / 32;
     extern __shared__ uint32_t smem[];
     uint32_t *hist = smem;               // [256][32]
@@ -150,11 +155,12 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const Params p) {
     __shared__ uint32_t found[3];        // the digit, how many are above it, how many have it
     __shared__ uint32_t finals[kFinalKeys], every[kFinalKeys];  // of this CTA; of the cluster
     __shared__ int final_count;
-    __shared__ unsigned long long least[kWarps];
+    __shared__ unsigned long long least[kWarps], least_here[2];
     __shared__ int fused_holes[kFused ? kFusedMoves : 1], fused_src[kFused ? kFusedMoves : 1], fused_moves;
+    __shared__ int gone_slots[kFewMoves];
     const EvictLaunch &a = p.a;
     const cg::cluster_group cluster = cg::this_cluster();
-    const int peers = kFused ? 1 : p.cluster, peer = kFused ? 0 : int(cluster.block_rank());
+    const int peers = kMover == kCta ? 1 : p.cluster, peer = kMover == kCta ? 0 : int(cluster.block_rank());
     const long long row = blockIdx.x / peers;
     const int b = int(row / a.Hkv), t = threadIdx.x, warp = t >> 5, lane = t & 31;
     if constexpr (!kFused) griddep_launch_dependents();
@@ -169,6 +175,7 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const Params p) {
     }
     int *src = kFused ? fused_src : p.src + row * p.slots;
     int *holes = kFused ? fused_holes : p.holes + row * p.gaps;
+    if constexpr (kMover == kCluster) src = cluster.map_shared_rank(src, 0), holes = cluster.map_shared_rank(holes, 0);
     if (n <= a.keep) {  // nothing to evict
         if constexpr (!kFused) {
             if (t == 0 && peer == 0) p.head[2 * row] = 0;
@@ -196,11 +203,11 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const Params p) {
         // A few keys go: find the smallest (rank, slot from the end), then the
         // next one, a pass each.
         if constexpr (kShared)
-            visit<8>(t, n, kThreads, key, [&](int i, Key k) { ranks[i] = r.rank(k); });  // each thread its own
+            visit<8>(lo + t, hi, kThreads, key, [&](int i, Key k) { ranks[i - lo] = r.rank(k); });  // each thread its own
         unsigned long long last = 0;
         for (int e = 0; e < n - a.keep; ++e) {
             unsigned long long low = ~0ull;
-            visit<8>(t, n, kThreads, rank, [&](int i, uint32_t x) {
+            visit<8>(lo + t, hi, kThreads, rank, [&](int i, uint32_t x) {
                 const unsigned long long key = (unsigned long long)x << 32 | uint32_t(~i);
                 if ((e == 0 || key > last) && key < low) low = key;
             });
@@ -217,17 +224,30 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const Params p) {
                 const unsigned long long y = __shfl_xor_sync(0xffffffffu, low, off);
                 low = y < low ? y : low;
             }
+            if constexpr (kMover == kCluster) {
+                // (In turns: the others may still read the last one.)
+                if (t == 0) least_here[e & 1] = low;
+                cluster.sync();
+                low = lane < peers ? *cluster.map_shared_rank(&least_here[e & 1], lane) : ~0ull;
+#pragma unroll
+                for (int off = 4; off > 0; off >>= 1) {
+                    const unsigned long long y = __shfl_xor_sync(0xffffffffu, low, off);
+                    low = y < low ? y : low;
+                }
+                low = __shfl_sync(0xffffffffu, low, 0);
+            }
             last = low;
-            if (t == 0) fused_src[e] = int(~uint32_t(low));  // evicted slots for now
+            if (t == 0) gone_slots[e] = int(~uint32_t(low));
             __syncthreads();
         }
+        if constexpr (kMover == kCluster) cluster.barrier_arrive();  // this CTA has read all that it will of the others
         if (t == 0) {
             // Holes: the evicted slots below keep, in order.  Fillers: the slots past it that stay.
             int gone[kFewMoves];
             const int count = n - a.keep;
             unsigned past = 0;
             for (int e = 0; e < count; ++e) {
-                const int s = fused_src[e];
+                const int s = gone_slots[e];
                 if (s >= a.keep) {
                     past |= 1u << (s - a.keep);
                     continue;
@@ -435,7 +455,7 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const Params p) {
             if (warp == 0)  // a lane a number; the other warps read the copy
                 theirs[lane >> 2][lane & 3] = (lane >> 2) < peers ? cluster.map_shared_rank(totals, lane >> 2)[lane & 3] : 0;
             __syncthreads();
-            cluster.barrier_arrive();  // this CTA has read all that it will of the others
+            if constexpr (!kFused) cluster.barrier_arrive();  // this CTA has read all that it will of the others
             int t0 = 0;  // ties ahead of CTA q
             for (int q = 0; q < peers; ++q) {
                 if (q < peer) fill += theirs[q][1] + min(theirs[q][3], max(want - t0 - theirs[q][2], 0));
@@ -481,15 +501,23 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const Params p) {
             if (filler) fillers[fill + __popc(all & below)] = s;
             fill += __popc(all);
         });
+        if constexpr (kMover == kCluster) {
+            // The first CTA has the lists; every other takes a copy.
+            cluster.sync();
+            if (peer > 0 && t < moves) fused_src[t] = src[t], fused_holes[t] = holes[t];
+            __syncthreads();
+            cluster.barrier_arrive();
+        }
     }
     if constexpr (kFused) {
         __syncthreads();
         const int units = a.d / 4;
-        for (int i = t; i < moves * units; i += kThreads) {
-            const int m = i / units, u = i % units;
-            store_unit(a, row, holes[m], u, load_unit(a, row, src[m], u));
-            if (u == 0) move_scalars(a, row, src[m], holes[m]);
+        for (int i = peer * kThreads + t; i < moves * units; i += peers * kThreads) {
+            const int m = i / units, u = i % units, from = fused_src[m], to = fused_holes[m];
+            store_unit(a, row, to, u, load_unit(a, row, from, u));
+            if (u == 0) move_scalars(a, row, from, to);
         }
+        if constexpr (kMover == kCluster) cluster.barrier_wait();
     } else {
         if (t == 0 && peer == 0) p.head[2 * row] = moves;
         if (peers > 1) cluster.barrier_wait();  // no CTA leaves while another may read its shared memory
@@ -579,9 +607,9 @@ Layout layout(const EvictLaunch &a) {
     return l;
 }
 
-template <bool kShared, bool kFused, int kThreads>
+template <bool kShared, Mover kMover, int kThreads>
 cudaError_t launch_select(const Params &p, size_t smem, cudaStream_t stream) {
-    auto kernel = select_kernel<kShared, kFused, kThreads>;
+    auto kernel = select_kernel<kShared, kMover, kThreads>;
     static bool attr_set[kMaxDevices] = {};
     const int dev = slot_for_device();
     if (dev < 0 || !attr_set[dev]) {
@@ -624,10 +652,12 @@ int evict_launch(const EvictLaunch &a, cudaStream_t stream) {
     // CTAs a row: while every row's cluster still has its SMs to itself and a
     // CTA 2048 keys or more.  In us, with 1, 2, 4 and 8 CTAs a row: 8 rows of 16K
     // keys 18.5, 17.1, 15.1, 15.1; 8 of 128K 197, 114, 36, 25; 16 of 8K 14.4, 14.4, 13.7,
-    // 16.4; 8 of 4K 11.7, and 13.7 with eight (an exchange costs what it saves).
+    // 16.4; 8 of 4K 11.7, and 13.7 with eight (an exchange costs what it saves).  The
+    // fused form, 16 keys of 8 rows: of 8K 10.4, 11.8, 11.6, 12.3; of 16K 14.6, 14.3, 12.2,
+    // 12.7; of 64K 72, 26.5, 19.0, 16.1; of 128K 136, 77, 27, 20.4.
     const long long rows = (long long)a.B * a.Hkv;
     p.cluster = 1;
-    if (!l.fused && a.max_seqlen >= 8192)
+    if (a.max_seqlen >= (l.fused ? 16384 : 8192))
         while (p.cluster < 8 && rows * p.cluster * 2 <= a.num_sms && a.max_seqlen / (p.cluster * 2) >= 2048) p.cluster *= 2;
     const int keys = ((a.max_seqlen + p.cluster - 1) / p.cluster + 31) / 32 * 32;
     const bool shared = keys <= kMaxKeys;
@@ -639,11 +669,15 @@ int evict_launch(const EvictLaunch &a, cudaStream_t stream) {
     // some length (256 rows of 8K 21 and 26; one key of 256 rows of 4K 6.9 and 9.6, of 8K
     // 8.9 and 11.6, of 16K 18.6 and 15.8).
     const bool many = keys > (rows > a.num_sms ? 12288 : 4096);
-    auto select = l.fused ? (!shared ? launch_select<false, true, 1024> : many ? launch_select<true, true, 1024>
-                                                                               : launch_select<true, true, 512>)
-                          : (!shared ? launch_select<false, false, 1024> : many ? launch_select<true, false, 1024>
-                                                                                : launch_select<true, false, 512>);
-    cudaError_t e = select(p, smem, stream);
+    auto select = [&](auto mover) {
+        constexpr Mover m = decltype(mover)::value;
+        return !shared ? launch_select<false, m, 1024>(p, smem, stream)
+               : many  ? launch_select<true, m, 1024>(p, smem, stream)
+                       : launch_select<true, m, 512>(p, smem, stream);
+    };
+    cudaError_t e = !l.fused        ? select(std::integral_constant<Mover, kLater>())
+                    : p.cluster > 1 ? select(std::integral_constant<Mover, kCluster>())
+                                    : select(std::integral_constant<Mover, kCta>());
     if (e != cudaSuccess) return note_cuda_error(e, "select_kernel launch");
     if (l.fused || l.slots == 0) return 0;
     // In place the number of moves is known on the device only and may be far from

@@ -147,6 +147,44 @@ def test_rows_shared_by_several_ctas(attn, B, H, S, keep, kind, in_place):
     check(attn, weights_of(kind, (B, H, S), 7), lens, keep, 12, in_place=in_place, slack=1)
 
 
+@pytest.mark.parametrize("kind", ["plain", "few values", "equal", "odd"])
+@pytest.mark.parametrize("B,H,S,past", [(3, 2, 16384, 1), (2, 8, 9001, 4), (5, 1, 20000, 5), (4, 2, 33000, 64), (1, 1, 60001, 33),
+                                        (2, 2, 180000, 3), (1, 2, 400000, 64)])
+def test_few_keys_of_long_rows_go(attn, B, H, S, past, kind):
+    """A bounded cache with few long rows, in place: the CTAs of a row select and move together.  From none to all of the
+    keys past the bound go; the lengths leave some of the CTAs without one."""
+    keep = S - past
+    lens = [S, keep + min(past, 2), keep, S - past // 2, 50][:B]
+    check(attn, weights_of(kind, (B, H, S), 11), lens, keep, 9, in_place=True)
+    g = torch.Generator().manual_seed(12)
+    pos = torch.stack([torch.randperm(2 * S, generator=g)[:S].to(torch.int32) for _ in range(B * H)]).view(B, H, S)
+    check(attn, weights_of("few values", (B, H, S), 13), lens, keep, S // 2, pos=pos, cur=torch.full((B,), 2 * S, dtype=torch.int32))
+
+
+def test_few_keys_of_long_rows_take_no_longer_than_many(attn):
+    """16 of 131072 keys of 8 rows go where the cache has 64 slots past the bound (one launch): with one CTA a row that
+    took 6 times as long as with 65 slots, where a cluster selects and a second launch moves."""
+    B, H, S, d = 1, 8, 1 << 17, 64
+    kc, vc = normal_bf16((B, H, S, d), 70, DEV), normal_bf16((B, H, S, d), 71, DEV)
+    w = weights_of("plain", (B, H, S), 14).to(DEV)
+    us = []
+    for past in (64, 65):
+        lens = torch.full((B,), S - past + 16, dtype=torch.int32, device=DEV)
+        out, ws = attn.cache_evict(kc, vc, w, lens, S - past, 8)
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            for _ in range(20):
+                attn.cache_evict(kc, vc, w, lens, S - past, 8, seqlens_out=out, workspace=ws)
+        ends = [torch.cuda.Event(enable_timing=True) for _ in range(6)]
+        ends[0].record()
+        for e in ends[1:]:
+            g.replay()
+            e.record()
+        torch.cuda.synchronize()
+        us.append(min(a.elapsed_time(b) for a, b in zip(ends, ends[1:])))
+    assert us[0] <= 2 * us[1], us
+
+
 def test_captured_loop_with_appends(attn):
     """A captured decode step on a bounded cache (append, evict), replayed: the lengths go round in device memory, positions
     advance, and every replay equals the eager step."""
