@@ -161,6 +161,32 @@ def test_few_keys_of_long_rows_go(attn, B, H, S, past, kind):
     check(attn, weights_of("few values", (B, H, S), 13), lens, keep, S // 2, pos=pos, cur=torch.full((B,), 2 * S, dtype=torch.int32))
 
 
+def timed(attn, B, H, S, keep, n, d=64):
+    """Milliseconds of 20 evictions in place of n - keep keys of every row (the weights decide, so each moves as many)."""
+    kc, vc = normal_bf16((B, H, S, d), 70, DEV), normal_bf16((B, H, S, d), 71, DEV)
+    w = weights_of("plain", (B, H, S), 14).to(DEV)
+    lens = torch.full((B,), n, dtype=torch.int32, device=DEV)
+    out, ws = attn.cache_evict(kc, vc, w, lens, keep, 8)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        for _ in range(20):
+            attn.cache_evict(kc, vc, w, lens, keep, 8, seqlens_out=out, workspace=ws)
+    ends = [torch.cuda.Event(enable_timing=True) for _ in range(6)]
+    ends[0].record()
+    for e in ends[1:]:
+        g.replay()
+        e.record()
+    torch.cuda.synchronize()
+    return min(a.elapsed_time(b) for a, b in zip(ends, ends[1:]))
+
+
+@pytest.mark.parametrize("fits,more", [(15, 16), (15, 19), (34, 38)])
+def test_one_row_more_does_not_wait_for_the_others(attn, fits, more):
+    """Clusters that do not all have SMs at once took a second wave: 16 rows of 64K keys 1.8 times as long as 15."""
+    S = 1 << 16
+    assert timed(attn, more, 1, S, S - 65, S) <= 1.4 * timed(attn, fits, 1, S, S - 65, S)
+
+
 def test_few_keys_of_long_rows_take_no_longer_than_many(attn):
     """16 of 131072 keys of 8 rows go where the cache has 64 slots past the bound (one launch): with one CTA a row that
     took 6 times as long as with 65 slots, where a cluster selects and a second launch moves."""
