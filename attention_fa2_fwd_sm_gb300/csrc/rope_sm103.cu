@@ -13,9 +13,11 @@
 // u = frac(f_i / 2 pi) 2^64, and the phase p u mod 2^64 is one integer product
 // that drops whole turns exactly.  Its top 32 bits, as a signed fraction of a
 // half turn, go to sincospif: the angle is off by 2^-24 of a half turn at any
-// position.  The conversion of f_i is integer arithmetic too (a 53-bit mantissa
-// times 2^66 / 2 pi): this GPU has few fp64 units, and eight conversions a
-// thread on them would take as long as the thread's memory traffic.
+// position (u itself by less than one unit, which makes 2^-33 turns of the
+// farthest).  The conversion of f_i is integer arithmetic too (a 53-bit mantissa
+// times 2^130 / 2 pi, 181 bits, so that u is right up to f_i = 2^54): this GPU has
+// few fp64 units, and eight conversions a thread on them would take as long as the
+// thread's memory traffic.
 //
 // What bounds it: every element is read and written once (4 bytes), nothing
 // else of size moves, so HBM.  A thread owns one 8-column unit of one token
@@ -60,11 +62,11 @@ struct Params {
     float scale, sign;
 };
 
-// 2^66 / (2 pi), rounded.
-constexpr unsigned long long kTurns = 0xA2F9836E4E44152Aull;
+// 2^130 / (2 pi), rounded: its upper and its lower 64 bits.
+constexpr unsigned long long kTurnsHi = 0xA2F9836E4E441529ull, kTurnsLo = 0xFC2757D1F534DDC1ull;
 
 // frac(f / 2 pi) in units of 2^-64 turns.  f = m 2^(e - 1075) with a 53-bit m,
-// so f / 2 pi * 2^64 = m kTurns 2^(e - 1077).  Frequencies from 2^54 up, and
+// so f / 2 pi * 2^64 = (m kTurns 2^-64) 2^(e - 1077).  Frequencies from 2^54 up, and
 // infinities and NaN, give 0: no position has a meaningful angle there.
 __device__ __forceinline__ unsigned long long turns_of(double f) {
     const unsigned long long bits = (unsigned long long)__double_as_longlong(f);
@@ -73,7 +75,9 @@ __device__ __forceinline__ unsigned long long turns_of(double f) {
     if (e) m |= 1ull << 52;
     const int shift = 1077 - (e ? e : 1);
     if (shift <= 0 || shift >= 128) return 0;
-    const unsigned long long lo = m * kTurns, hi = __umul64hi(m, kTurns);
+    // The upper 128 of the product's 192 bits.
+    const unsigned long long low = __umul64hi(m, kTurnsLo), lo = m * kTurnsHi + low;
+    const unsigned long long hi = __umul64hi(m, kTurnsHi) + (lo < low);
     const unsigned long long u = shift >= 64 ? hi >> (shift - 64) : (lo >> shift) | (hi << (64 - shift));
     return (long long)bits < 0 ? 0ull - u : u;
 }

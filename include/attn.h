@@ -413,8 +413,9 @@ int attn_decode_num_splits(int B, int Hq, int Hkv, int max_seqlen);
  * i + rotary_dim / 2); interleaved != 0: columns (2 i, 2 i + 1).  Columns from
  * rotary_dim on are copied unchanged.  inverse != 0 turns by -a, which is the
  * gradient: if y = rope(x), then dx = rope(dy) with inverse set and the same
- * out_scale.  Angles are reduced exactly (64-bit fixed-point turns), so far
- * positions lose nothing; arithmetic is fp32, rounded to bf16 once.
+ * out_scale.  Whole turns are dropped in 64-bit fixed point, off by less than
+ * |p| 2^-64 turns whatever the frequency, so far positions lose nothing;
+ * arithmetic is fp32, rounded to bf16 once.
  *   q, q_out   [B, Hq,  N, d]  bf16
  *   k, k_out   [B, Hkv, N, d]  bf16; both NULL when there is only q (Hkv is
  *              then ignored)

@@ -138,6 +138,29 @@ def test_far_positions_and_odd_frequencies(attn):
     assert torch.isfinite(y.float()).all()
 
 
+def test_high_frequencies_at_far_positions(attn):
+    """Up to 2^54 radians a position: besides the bound at the top the phase is off by less than |p| 2^-64 turns, 2^-33 at the farthest
+    position."""
+    getcontext().prec = 60
+    two_pi = 2 * Decimal("3.14159265358979323846264338327950288419716939937510582097494459")
+    dev = torch.device("cuda")
+    f = [2.0 ** 53, 2.0 ** 53 - 1, -(2.0 ** 54 - 2), 1e15, 12345678901.25, 2.0 ** 40 + 1, -7.5e12, 1e8 / 3, 2.0 ** 30, 10.5, 2.0 / 3, 1e-8]
+    pos = [2 ** 31 - 1, -2 ** 31, 1234567890, -77777, 4099, 1]
+    x = torch.zeros((1, 1, len(pos), 2 * len(f)), dtype=torch.bfloat16)
+    x[..., :len(f)] = 1.0
+    out, _ = attn.rope(x.to(dev), None, torch.tensor(f, dtype=torch.float64, device=dev),
+                       positions=torch.tensor(pos, dtype=torch.int32, device=dev))
+    out = out.cpu().double().numpy()[0, 0]
+    for n, p in enumerate(pos):
+        for i, w in enumerate(f):
+            t = Decimal(p) * Decimal(w) / two_pi
+            a = float((t - t.to_integral_value()) * two_pi)
+            slack = FP32 + abs(p) * 2.0 ** -64 * 6.2832
+            assert slack < 2.0 ** -19
+            assert abs(out[n, i] - np.cos(a)) <= STEP * abs(np.cos(a)) + slack, (p, w)
+            assert abs(out[n, len(f) + i] - np.sin(a)) <= STEP * abs(np.sin(a)) + slack, (p, w)
+
+
 @pytest.mark.parametrize("inter", [False, True])
 @pytest.mark.parametrize("r", [16, 20])
 def test_gradient_is_the_adjoint_and_matches_differences(attn, inter, r):
