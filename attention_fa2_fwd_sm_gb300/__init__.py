@@ -437,6 +437,17 @@ def _elsewhere(what, gpu, stream):
     return torch.cuda.stream(stream)
 
 
+def _lend(stream, *tensors):
+    """Tell the allocator that `stream` uses these tensors, so that none of them is
+    given away under its kernels when the caller lets go of it.  Not for a
+    stream that torch does not own: it may be gone by then."""
+    import torch
+    if isinstance(stream, torch.cuda.Stream) and not isinstance(stream, torch.cuda.ExternalStream):
+        for t in tensors:
+            if t is not None:
+                t.record_stream(stream)
+
+
 def _held(what, workspace, gpu):
     """Bytes of the caller's workspace."""
     if workspace.get_device() != gpu or not workspace.is_contiguous():
@@ -458,13 +469,21 @@ def rope(q, k, inv_freq, positions=None, interleaved=False, out_scale=1.0, out=N
     columns, so a fused projection's views too) by attn_rope; `k` may be None.
     `positions` is ``[N]`` or ``[B, N]`` int32, or None for 0..N-1; rotary_dim
     is twice the length of `inv_freq`.  Returns ``(q_out, k_out)``: contiguous
-    tensors as attn_fwd takes them, or `out`, which may be ``(q, k)``."""
+    tensors as attn_fwd takes them, or `out`, which may be ``(q, k)``.
+
+    `stream` (here and in the other decode-cache helpers): a torch stream, or
+    an address of one, other than the current one.  What the call allocates
+    belongs to it.  The inputs are kept for it by the allocator where the stream
+    is torch's own; the caller keeps them until the work is done where it is an
+    address or a torch.cuda.ExternalStream."""
     import torch
     what, bf16 = "rope", torch.bfloat16
     gpu = q.get_device()
     if stream is not None or gpu < 0 or gpu != torch._C._cuda_getDevice():
         with _elsewhere(what, gpu, stream):
-            return rope(q, k, inv_freq, positions, interleaved, out_scale, out, inverse)
+            got = rope(q, k, inv_freq, positions, interleaved, out_scale, out, inverse)
+        _lend(stream, q, k, inv_freq, positions, *(out or ()))
+        return got
     if q.dim() != 4 or (k is not None and k.dim() != 4):
         raise AttnError(ATTN_ERR_ARG, "rope: q and k have to be [B, H, N, d]")
     B, Hq, N, d = q.shape
@@ -522,8 +541,11 @@ def rope_append(q, k, v, kcache, vcache, seqlens, inv_freq=None, start_pos=None,
     gpu = q.get_device()
     if stream is not None or gpu < 0 or gpu != torch._C._cuda_getDevice():
         with _elsewhere(what, gpu, stream):
-            return rope_append(q, k, v, kcache, vcache, seqlens, inv_freq, start_pos, new_lens, interleaved, out_scale,
-                               cache_pos, weights, q_out, seqlens_out)
+            got = rope_append(q, k, v, kcache, vcache, seqlens, inv_freq, start_pos, new_lens, interleaved, out_scale,
+                              cache_pos, weights, q_out, seqlens_out)
+        _lend(stream, q, k, v, kcache, vcache, seqlens, inv_freq, start_pos, new_lens, cache_pos, weights, q_out,
+              seqlens_out)
+        return got
     if q.dim() != 4 or kcache.dim() != 4:
         raise AttnError(ATTN_ERR_ARG, "rope_append: q has to be [B, Hq, T, d], the caches [B, Hkv, max_seqlen, d]")
     B, Hq, T, d = q.shape
@@ -580,7 +602,9 @@ def decode_prefix(q, kprefix, vprefix, kcache, vcache, seqlens, scale=None, weig
     gpu = q.get_device()
     if stream is not None or gpu < 0 or gpu != torch._C._cuda_getDevice():
         with _elsewhere(what, gpu, stream):
-            return decode_prefix(q, kprefix, vprefix, kcache, vcache, seqlens, scale, weights, workspace, with_lse)
+            got = decode_prefix(q, kprefix, vprefix, kcache, vcache, seqlens, scale, weights, workspace, with_lse)
+        _lend(stream, q, kprefix, vprefix, kcache, vcache, seqlens if kcache is not None else None, weights, workspace)
+        return got
     if q.dim() != 3 or (kcache is not None and kcache.dim() != 4) or (kprefix is not None and kprefix.dim() != 3):
         raise AttnError(ATTN_ERR_ARG, "decode_prefix: q has to be [B, Hq, d], the prefix [Hkv, P, d], the caches "
                                       "[B, Hkv, max_seqlen, d]")
@@ -641,8 +665,11 @@ def cache_evict(kcache, vcache, weights, seqlens, keep, recent=0, cache_pos=None
     gpu = kcache.get_device()
     if stream is not None or gpu < 0 or gpu != torch._C._cuda_getDevice():
         with _elsewhere(what, gpu, stream):
-            return cache_evict(kcache, vcache, weights, seqlens, keep, recent, cache_pos, cur_pos, out, seqlens_out,
-                               workspace)
+            got = cache_evict(kcache, vcache, weights, seqlens, keep, recent, cache_pos, cur_pos, out, seqlens_out,
+                              workspace)
+        _lend(stream, kcache, vcache, weights, seqlens, cache_pos, cur_pos, seqlens_out, workspace,
+              *(out.values() if out is not None else ()))
+        return got
     if kcache.dim() != 4:
         raise AttnError(ATTN_ERR_ARG, "cache_evict: the caches have to be [B, Hkv, max_seqlen, d]")
     B, Hkv, s_max, d = kcache.shape

@@ -118,3 +118,50 @@ def test_training_through_the_rotation(attn):
     for got, want in ((dq, q64.grad), (dk, k64.grad), (dv, v64.grad)):
         rel = float((got.double().cpu() - want).norm() / want.norm())
         assert rel <= 1e-2 + 2 * 2.0 ** -8, rel
+
+
+def test_inputs_let_go_of_while_another_stream_uses_them(attn):
+    """Calls on a stream that is still busy, whose inputs are freed at once: what is allocated and filled with NaN meanwhile is other memory."""
+    B, Hq, Hkv, N, P, S, d = 2, 16, 4, 700, 300, 1000, 128
+    f, s = attn.rope_freqs(d), torch.cuda.Stream()
+
+    def tokens(seed, n):
+        return [normal_bf16((B, h, n, d), seed + i, DEV) for i, h in enumerate((Hq, Hkv, Hkv))]
+
+    def caches(seed):
+        w = torch.rand((B, Hkv, S), generator=torch.Generator().manual_seed(seed)).to(DEV)
+        return [normal_bf16((B, Hkv, S, d), seed + i, DEV) for i in range(2)] + [w, torch.full((B,), S - N, dtype=torch.int32, device=DEV)]
+
+    def rope():
+        q, k, _ = tokens(1, N)
+        return [q, k, f], lambda stream: attn.rope(q, k, f, stream=stream)
+
+    def append():
+        q, k, v = tokens(5, N)
+        kc, vc, _, n = caches(10)
+        return [q, k, v, kc, vc, n], lambda stream: attn.rope_append(q, k, v, kc, vc, n, f, stream=stream) + (kc, vc)
+
+    def decode():
+        q, kp, vp = (normal_bf16(x, 20 + i, DEV) for i, x in enumerate(((B, Hq, d), (Hkv, P, d), (Hkv, P, d))))
+        kc, vc, w, n = caches(25)
+        return [q, kp, vp, kc, vc, n], lambda stream: attn.decode_prefix(q, kp, vp, kc, vc, n, weights=w, stream=stream)[:2] + (w,)
+
+    def evict():
+        kc, vc, w, n = caches(30)
+        out = dict(kcache=torch.zeros_like(kc), vcache=torch.zeros_like(vc))
+        return [kc, vc, w, n], lambda stream: (attn.cache_evict(kc, vc, w, n, 100, 10, out=out, stream=stream)[0], *out.values())
+
+    for make in (rope, append, decode, evict):
+        want = make()[1](None)
+        inputs, call = make()
+        sizes = [(t.shape, t.dtype) for t in inputs if t is not f]
+        torch.cuda.synchronize()
+        with torch.cuda.stream(s):
+            torch.cuda._sleep(60_000_000)
+        got = call(s)
+        del inputs, call
+        other = [torch.empty(shape, dtype=dtype, device=DEV) for shape, dtype in sizes * 2]
+        for t in other:
+            t.fill_(float("nan") if t.dtype.is_floating_point else -1)
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, want)), make.__name__
