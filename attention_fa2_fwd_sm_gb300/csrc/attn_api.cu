@@ -944,24 +944,21 @@ int attn_cache_evict(const void *kcache, const void *vcache, const float *weight
         if (!aligned4(ptr)) return ATTN_ERR_ARG;
     if (ints_overlap(seqlens_out, seqlens, B) || ints_overlap(seqlens_out, cur_pos, B)) return ATTN_ERR_ARG;
     const bool in_place = kout == kcache;
-    if (in_place) {
-        if (vout != vcache || weights_out != weights || pos_out != cache_pos || out_seqlen != max_seqlen || kout == vout)
-            return ATTN_ERR_ARG;
-    } else {
-        // An output may overlap no input and no other output.
-        const size_t in4 = rows * max_seqlen * 4, out4 = rows * out_seqlen * 4;
-        const size_t in = rows * max_seqlen * d * 2, out = rows * out_seqlen * d * 2;
-        const struct {
-            const void *p;
-            size_t n;
-        } ins[] = {{kcache, in}, {vcache, in}, {weights, in4}, {cache_pos, in4}},
-          outs[] = {{kout, out}, {vout, out}, {weights_out, out4}, {pos_out, out4}};
-        for (int i = 0; i < 4; ++i)
-            for (int j = 0; j < 4; ++j)
-                if (bytes_overlap(outs[i].p, outs[i].n, ins[j].p, ins[j].n) ||
-                    (j < i && bytes_overlap(outs[i].p, outs[i].n, outs[j].p, outs[j].n)))
-                    return ATTN_ERR_ARG;
-    }
+    if (in_place && (vout != vcache || weights_out != weights || pos_out != cache_pos || out_seqlen != max_seqlen))
+        return ATTN_ERR_ARG;
+    // An output may overlap no other output and, but for its own in place, no input.
+    const size_t in4 = rows * max_seqlen * 4, out4 = rows * out_seqlen * 4;
+    const size_t in = rows * max_seqlen * d * 2, out = rows * out_seqlen * d * 2;
+    const struct {
+        const void *p;
+        size_t n;
+    } ins[] = {{kcache, in}, {vcache, in}, {weights, in4}, {cache_pos, in4}},
+      outs[] = {{kout, out}, {vout, out}, {weights_out, out4}, {pos_out, out4}};
+    for (int i = 0; i < 4; ++i)
+        for (int j = 0; j < 4; ++j)
+            if ((!(in_place && i == j) && bytes_overlap(outs[i].p, outs[i].n, ins[j].p, ins[j].n)) ||
+                (j < i && bytes_overlap(outs[i].p, outs[i].n, outs[j].p, outs[j].n)))
+                return ATTN_ERR_ARG;
     EvictLaunch a;
     a.kcache = kcache;
     a.vcache = vcache;

@@ -575,7 +575,8 @@ int attn_decode_prefix_segment(int B, int Hq, int Hkv, int P, int d, int max_seq
  *              seqlens[b] - 1
  *   kout, vout, weights_out, pos_out  receive the first min(seqlens[b], keep)
  *              slots.  In place: all four equal to the inputs, out_seqlen ==
- *              max_seqlen; slots from `keep` on are left as they were.
+ *              max_seqlen; slots from `keep` on are left as they were; the
+ *              four do not overlap each other.
  *              Otherwise [B, Hkv, out_seqlen, ...] arrays that overlap no
  *              input, where weights_out and pos_out may be NULL; slots past
  *              the kept ones are left as they were.

@@ -298,6 +298,14 @@ def test_evict_refusals(kw, code):
     assert _evict(**kw) == code
 
 
+@pytest.mark.parametrize("kw", [
+    dict(vc=(1 << 24) + 4096, vo=(1 << 24) + 4096), dict(vc=(1 << 24) - 262144 + 16, vo=(1 << 24) - 262144 + 16),
+    dict(w=(1 << 24) + 64, wo=(1 << 24) + 64), dict(pos=(2 << 24) + 64, po=(2 << 24) + 64), dict(pos=(3 << 24) + 8188, po=(3 << 24) + 8188)])
+def test_evict_refuses_partial_overlaps_in_place(kw):
+    """Caches of [2, 2, 512, 64] are 262144 bytes, weights and positions 8192."""
+    assert _evict(**kw) == ARG
+
+
 def test_evict_workspace():
     ws = attn.attn_cache_evict_workspace_bytes
     assert ws(2, 2, 164, 100, True) == 0 and ws(2, 2, 165, 100, True) > 0  # few slots past the kept ones: one kernel
