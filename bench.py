@@ -904,12 +904,38 @@ def run_decode_varlen(args):
         torch.cuda.empty_cache()
 
 
+def shared_prefix_calls(B, P, S, Hq, Hkv, d, dev, copies):
+    """A decode step of B users behind P shared keys, S / 2 to S own ones each, as
+    callables that launch that step and nothing else: by attn_decode_prefix and,
+    with ``copies``, by attn_decode and attn_decode_varlen on caches that hold a
+    copy of the prefix.  Returns ({name: callable}, own keys of all users)."""
+    import torch
+
+    import attention_fa2_fwd_sm_gb300 as attn
+    from synthetic_inputs import decode_inputs, normal_bf16
+    q, kc, vc = decode_inputs(90, B, Hq, Hkv, S, d, dev)
+    kp, vp = normal_bf16((Hkv, P, d), 91, dev), normal_bf16((Hkv, P, d), 92, dev)
+    seq = torch.linspace(S // 2, S, B, device=dev).to(torch.int32)
+    ws = attn.decode_prefix(q, kp, vp, kc, vc, seq)[2]
+    calls = {"prefix_us": lambda: attn.decode_prefix(q, kp, vp, kc, vc, seq, workspace=ws)}
+    if copies:
+        wk = torch.cat((kp[None].expand(B, -1, -1, -1), kc), 2).contiguous()
+        wv = torch.cat((vp[None].expand(B, -1, -1, -1), vc), 2).contiguous()
+        whole = seq + P
+        _, wd, sp = attn.decode(q, wk, wv, whole)
+        _, wr = attn.decode_varlen(q, wk, wv, whole)
+        calls["copied_prefix_us"] = lambda: attn.decode(q, wk, wv, whole, num_splits=sp, workspace=wd)
+        calls["copied_prefix_varlen_us"] = lambda: attn.decode_varlen(q, wk, wv, whole, workspace=wr)
+    return calls, int(seq.sum())
+
+
 def run_decode_cache(args):
     """The decode-cache operators (GQA Hq=64, Hkv=8, d=128), one JSON line per
-    workload: a decode step over a shared prefix against attn_decode on caches
-    that hold a copy of it (which reads the prefix once per user), the weights'
-    cost on top of a decode step, a bounded cache's append and eviction, and the
-    rotary positions of a prompt.  Between calls the L2 is flushed."""
+    workload: a decode step over a shared prefix against attn_decode and
+    attn_decode_varlen on caches that hold a copy of it (which read the prefix
+    once per user), the weights' cost on top of a decode step, a bounded cache's
+    append and eviction (with the positions' step), and the rotary positions of a
+    prompt.  Between calls the L2 is flushed."""
     import torch
 
     import attention_fa2_fwd_sm_gb300 as attn
@@ -933,18 +959,10 @@ def run_decode_cache(args):
                           "hbm_floor_us": round(nbytes / peaks["hbm_gbs"] / 1e3, 2), **us}), flush=True)
 
     for B, P, S in ((8, 2048, 256), (32, 8192, 512), (128, 32768, 1024)):
-        q, kc, vc = decode_inputs(90, B, Hq, Hkv, S, d, dev)
-        kp, vp = normal_bf16((Hkv, P, d), 91, dev), normal_bf16((Hkv, P, d), 92, dev)
-        seq = torch.linspace(S // 2, S, B, device=dev).to(torch.int32)
-        ws = attn.decode_prefix(q, kp, vp, kc, vc, seq)[2]
-        us = {"prefix_us": timed(lambda: attn.decode_prefix(q, kp, vp, kc, vc, seq, workspace=ws))}
-        keys = int(seq.sum())
-        if B <= 32:  # the copies of a longer prefix would fill the GPU's memory
-            wk = torch.cat((kp[None].expand(B, -1, -1, -1), kc), 2).contiguous()
-            wv = torch.cat((vp[None].expand(B, -1, -1, -1), vc), 2).contiguous()
-            _, wd, sp = attn.decode(q, wk, wv, seq + P)
-            us["copied_prefix_us"] = timed(lambda: attn.decode(q, wk, wv, seq + P, num_splits=sp, workspace=wd))
-            del wk, wv
+        # (the copies of a longer prefix would fill the GPU's memory)
+        calls, keys = shared_prefix_calls(B, P, S, Hq, Hkv, d, dev, B <= 32)
+        us = {name: timed(fn) for name, fn in calls.items()}
+        del calls
         line(f"{B} users, {P} shared + {S // 2}..{S} own keys", 4 * d * Hkv * (P + keys) + 4 * B * Hq * d, **us)
 
     for B, S in ((1, 8192), (32, 16384)):
