@@ -17,3 +17,12 @@ def oracle():
     import oracle as _oracle
     _oracle.build()
     return _oracle
+
+
+@pytest.fixture(scope="session", autouse=True)
+def _torch_exp_set_up():
+    """torch's fp64 exp on the CPU sets itself up at its first use.  Where that use is
+    spread over several threads, some processes get one thread's share off by 1e-10, which
+    the oracle's comparisons at 1e-12 see; so the first use has one thread."""
+    import torch
+    torch.exp(torch.linspace(-1, 1, 64, dtype=torch.float64))
