@@ -651,8 +651,8 @@ int evict_launch(const EvictLaunch &a, cudaStream_t stream) {
     }
     // CTAs a row: while every row's cluster still has its SMs to itself (a cluster
     // lies within one of the 8 parts of the GPU, each of which has half a cluster
-    // left over in the mean) and a CTA 2048 keys or more.  In us, with 1, 2, 4 and 8 CTAs a row: 8 rows of 16K
-    // keys 18.5, 17.1, 15.1, 15.1; 8 of 128K 197, 114, 36, 25; 16 of 8K 14.4, 14.4, 13.7,
+    // left over in the mean) and a CTA 2048 keys or more.  In us, with 1, 2, 4 and 8
+    // CTAs a row: 8 rows of 16K keys 18.5, 17.1, 15.1, 15.1; 8 of 128K 197, 114, 36, 25; 16 of 8K 14.4, 14.4, 13.7,
     // 16.4; 8 of 4K 11.7, and 13.7 with eight (an exchange costs what it saves).  The
     // fused form, 16 keys of 8 rows: of 8K 10.4, 11.8, 11.6, 12.3; of 16K 14.6, 14.3, 12.2,
     // 12.7; of 64K 72, 26.5, 19.0, 16.1; of 128K 136, 77, 27, 20.4.
@@ -684,7 +684,11 @@ int evict_launch(const EvictLaunch &a, cudaStream_t stream) {
     if (e != cudaSuccess) return note_cuda_error(e, "select_kernel launch");
     if (l.fused || l.slots == 0) return 0;
     // In place the number of moves is known on the device only and may be far from
-    // the most: as many CTAs as the GPU holds.  Out of place the most is usual.
+    // the most: about as many CTAs as the GPU holds.  Whole calls, in us, with 2, 8, 32
+    // CTAs an SM and with one for every kMoveRows slots: 128 rows of 32K keys to 16000
+    // (8190 of them move) 240, 215, 203, 204; 256 of 8K to 4096 115, 116, 108, 109; one key past
+    // 4096 in 256 rows of 8K slots 14.8, 15.4, 18.4, 26.8; 100 past 16000 in 128 of 32K 19.6,
+    // 19.5, 22.2, 38.7.  Out of place the most is usual.
     long long per_row = (l.slots + kMoveRows - 1) / kMoveRows;
     const long long most = p.in_place ? (8LL * a.num_sms + rows - 1) / rows : 0x7fffffffLL / rows;
     if (per_row > most) per_row = most;
