@@ -699,6 +699,27 @@ static bool share_elements(const Rows &a, const Rows &b) {
     return meets(dim, n, apart, a.d, &budget);
 }
 
+// Whether two rows of one tensor share an element (a stride that is smaller than
+// what the smaller strides span).
+static bool shares_with_itself(const Rows &a) {
+    if (!a.p) return false;
+    Reach dim[3];
+    int n = 0;
+    for (int k = 0; k < 3; ++k) {
+        if (a.n[k] < 2) continue;
+        if (a.s[k] < a.d) return true;
+        int i = n++;
+        for (; i > 0 && dim[i - 1].s < a.s[k]; --i) dim[i] = dim[i - 1];
+        dim[i] = {a.s[k], 1 - a.n[k], a.n[k] - 1};
+    }
+    int budget = 2000;
+    for (int i = 0; i < n; ++i) {  // the first dimension in which the two differ
+        dim[i].lo = 1;
+        if (meets(dim + i, n - i, 0, a.d, &budget)) return true;
+    }
+    return false;
+}
+
 static Rows rows_in(const RopeTensor &t, int B, int N, int d) { return Rows(t.in, {t.in_b, t.in_h, t.in_n}, B, t.heads, N, d); }
 static Rows rows_out(const RopeTensor &t, int B, int N, int d) { return Rows(t.out, {t.out_b, t.out_h, t.out_n}, B, t.heads, N, d); }
 
@@ -731,6 +752,7 @@ int attn_rope(const void *q, void *q_out, const void *k, void *k_out, const int 
             if (!(i == j && in.same(out)) && share_elements(in, out)) return ATTN_ERR_ARG;
         }
     if (share_elements(rows_out(a.t[0], B, N, d), rows_out(a.t[1], B, N, d))) return ATTN_ERR_ARG;
+    if (shares_with_itself(rows_out(a.t[0], B, N, d)) || shares_with_itself(rows_out(a.t[1], B, N, d))) return ATTN_ERR_ARG;
     a.inv_freq = inv_freq;
     a.pos = positions;
     a.pos_stride = position_stride;
@@ -807,7 +829,7 @@ int attn_rope_append(const void *q, void *q_out, const void *k, const void *v, v
         for (const Rows &cache : caches)
             if (share_elements(in, cache)) return ATTN_ERR_ARG;
     }
-    if (share_elements(rotated, caches[0]) || share_elements(rotated, caches[1]) || share_elements(caches[0], caches[1]))
+    if (shares_with_itself(rotated) || share_elements(rotated, caches[0]) || share_elements(rotated, caches[1]) || share_elements(caches[0], caches[1]))
         return ATTN_ERR_ARG;
     a.inv_freq = inv_freq;
     a.pos = start_pos;

@@ -432,8 +432,8 @@ int attn_decode_num_splits(int B, int Hq, int Hkv, int max_seqlen);
  *              The strides of a dimension of extent 1 are ignored.
  *   d a multiple of 8, at most 512; rotary_dim even, 2 <= rotary_dim <= d.
  *   q_out == q (k_out == k) works in place where the strides are equal too;
- *   any other overlap of an output with an input or an output of q and k is
- *   not allowed and refused (views that interleave without sharing an element,
+ *   any other overlap of an output with an input or an output of q and k, or
+ *   of its own rows, is not allowed and refused (views that interleave without sharing an element,
  *   as those of one fused projection do, do not overlap; strides that do not
  *   nest are taken on trust).
  * One kernel on `stream`.

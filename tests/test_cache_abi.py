@@ -76,6 +76,15 @@ def test_append_refusals(kw, code):
     assert _append(**kw) == code
 
 
+@pytest.mark.parametrize("s", [
+    (1024, 1024, 64), (1024, 64, 64), (64, 1024, 64), (1024, 64, 1024), (960, 2048, 64), (2048, 1000, 64), (1032, 512, 32)])
+def test_outputs_laid_over_themselves_are_refused(s):
+    """B = 3, H = 2, N = 16 (T = 16 with a cache of 40 rows), d = 64."""
+    assert _rope(q_out=1 << 26, k=None, k_out=None, strides=strides(*PACKED, *s, *PACKED, *PACKED)) == ARG
+    assert _rope(q_out=1 << 25, k_out=1 << 26, strides=strides(*PACKED, *PACKED, *PACKED, *s)) == ARG
+    assert _append(q_out=1 << 26, T=16, S=40, kc=1 << 27, vc=1 << 28, v=A16 + (1 << 20), strides=strides(*PACKED, *s, *PACKED, *PACKED)) == ARG
+
+
 CACHE_ROWS = (2 * 16 * 64, 16 * 64, 64)  # strides of a [3, 2, T, 64] view of a cache of 16 rows
 NEW = (2 * 64, 64, 0)                    # those of [3, 2, 1, 64] tokens
 
