@@ -20,10 +20,10 @@
 //      memory, the other for the tensor cores.
 //   3. Merge: the partials of every row.
 //   4. With weights: the scores become weights now that L is known.
-// 128 sequences, 32K shared + 512 .. 1024 own keys, 64 heads, 8 KV heads, d = 128: 141
-// us, where the prefix alone takes 101 (1365 TFLOP/s) and the own keys alone 72; 32 with
-// 8K + 256 .. 512: 34.5, alone 23.4 and 17.7.  32 of 8K to 16K own keys, no prefix: 225
-// us, with weights 277.
+// 128 sequences, 32K shared + 512 .. 1024 own keys, 64 heads, 8 KV heads, d = 128: 137 to
+// 142 us, where the prefix alone takes 100 (1370 TFLOP/s) and the own keys alone 72; 32
+// with 8K + 256 .. 512: 28 to 37 by the GPU, alone 22 and 18, with weights 43.  32 of 8K to
+// 16K own keys, no prefix: 227 us, with weights 281.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 

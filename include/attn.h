@@ -517,7 +517,12 @@ int attn_rope_append(const void *q, void *q_out, const void *k, const void *v, v
  * all the rows that read a KV head.
  *   q, o       [B, Hq, d]                bf16
  *   kprefix, vprefix  [Hkv, P, d]        bf16; P = 0 (NULL): no prefix, which
- *              makes this attn_decode with weights
+ *              makes this a decode over ragged caches, with weights if they are
+ *              wanted.  Without weights it does the work of attn_decode and
+ *              attn_decode_varlen: the choice for a ragged batch (us here, there and
+ *              there: 128 users of 512 .. 1024 keys 72, 71, 82; 32 of 8K .. 16K 227,
+ *              235, 250), while one user is attn_decode's (8192 keys 12.1, 11.1, 15.1)
+ *              and so are head groups and sizes that this refuses.
  *   kcache, vcache  [B, Hkv, max_seqlen, d]  bf16; max_seqlen = 0 (NULL): no
  *              own keys
  *   seqlens    [B] int32, clamped to [0, max_seqlen]; NULL where max_seqlen
@@ -531,7 +536,10 @@ int attn_rope_append(const void *q, void *q_out, const void *k, const void *v, v
  *   B * Hq at most 2^30.
  *   workspace  at least attn_decode_prefix_workspace_bytes(...) bytes, 16-byte
  *              aligned; with weights it also holds the scores, 4 * B * Hq *
- *              max_seqlen bytes.  Nothing in it outlives the call.
+ *              max_seqlen bytes.  Nothing in it outlives the call.  The scores
+ *              are by capacity, since the lengths are on the device: a cache
+ *              allocated far past its lengths pays for it in memory, and in
+ *              time for an SM division that takes it as three quarters full.
  * Up to four kernels run on `stream`, with no host synchronisation: the
  * prefix's partials, the own keys' partials (shared out on the device by
  * seqlens), the merge, and the weights.
