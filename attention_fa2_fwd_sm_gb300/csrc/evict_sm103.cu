@@ -652,12 +652,12 @@ int evict_launch(const EvictLaunch &a, cudaStream_t stream) {
     // CTAs a row: while every row's cluster still has its SMs to itself (a cluster
     // lies within one of the 8 parts of the GPU, each of which has half a cluster
     // left over in the mean) and a CTA 2048 keys or more.  In us, with 1, 2, 4 and 8
-    // CTAs a row: 8 rows of 16K keys 18.5, 17.1, 15.1, 15.1; 8 of 128K 197, 114, 36, 25; 16 of 8K 14.4, 14.4, 13.7,
-    // 16.4; 8 of 4K 11.7, and 13.7 with eight (an exchange costs what it saves).  The
-    // fused form, 16 keys of 8 rows: of 8K 10.4, 11.8, 11.6, 12.3; of 16K 14.6, 14.3, 12.2,
-    // 12.7; of 64K 72, 26.5, 19.0, 16.1; of 128K 136, 77, 27, 20.4.
-    // Where they do not all fit: 16 rows of 64K 75, 28.5, 20.7, 31.7 (15 rows 18.0 with
-    // eight); 38 rows of 64K 75, 28.8, 37.8 with one, two, four (36 rows 22.4).
+    // CTAs a row: 8 rows of 16K keys 18.5, 17.1, 15.1, 15.1; 8 of 128K 197, 114, 36, 25; 16
+    // of 8K 14.4, 14.4, 13.7, 16.4; 8 of 4K 11.7, and 13.7 with eight (an exchange costs
+    // what it saves).  The fused form, 16 keys of 8 rows: of 8K 10.4, 11.8, 11.6, 12.3; of
+    // 16K 14.6, 14.3, 12.2, 12.7; of 64K 72, 26.5, 19.0, 16.1; of 128K 136, 77, 27, 20.4.
+    // Where the clusters do not all fit: 16 rows of 64K 75, 28.5, 20.7, 31.7 (15 rows 18.0
+    // with eight); 38 rows of 64K 75, 28.8, 37.8 with one, two, four (36 rows 22.4).
     const long long rows = (long long)a.B * a.Hkv;
     p.cluster = 1;
     if (a.max_seqlen >= (l.fused ? 16384 : 8192))
