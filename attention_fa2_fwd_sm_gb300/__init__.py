@@ -68,6 +68,8 @@ SIGNATURES = {
     "attn_rope": (_I, [_P, _P, _P, _P, _P, _LL, _P, _I, _I, _I, _I, _I, _I, _I, _F, _I, _P, _P]),
     "attn_rope_freqs": (_I, [_DP, _I, _D, _I, _D, _D, _D, _D]),
     "attn_rope_append": (_I, [_P] * 13 + [_I] * 7 + [_F, _I, _P, _P]),
+    "attn_rope_axes": (_I, [_P] * 5 + [_LL, _LL, _I, _P, _P] + [_I] * 7 + [_F, _I, _P, _P]),
+    "attn_rope_axes_append": (_I, [_P] * 9 + [_LL, _LL, _I] + [_P] * 4 + [_I] * 7 + [_F, _I, _I, _I, _P, _P]),
     "attn_decode_prefix": (_I, [_P] * 9 + [_I] * 5 + [_F, _I, _P, _SZ, _P]),
     "attn_decode_prefix_workspace_bytes": (_SZ, [_I] * 7),
     "attn_decode_prefix_segment": (_I, [_I] * 6 + [_LL] + [_I] * 3 + [_IP]),
@@ -358,6 +360,23 @@ def attn_rope_append(q, q_out, k, v, kcache, vcache, seqlens, start_pos, new_len
                                   max_seqlen, strides, _stream(stream))
 
 
+def attn_rope_axes(q, q_out, k, k_out, positions, axis_stride, position_stride, num_axes, inv_freq, axes, B, Hq, Hkv, N,
+                   d, rotary_dim, interleaved, out_scale, inverse, strides=None, stream=None) -> int:
+    return lib().attn_rope_axes(_ptr(q), _ptr(q_out), _ptr(k), _ptr(k_out), _ptr(positions), axis_stride,
+                                position_stride, num_axes, _ptr(inv_freq), _ptr(axes), B, Hq, Hkv, N, d, rotary_dim,
+                                int(bool(interleaved)), out_scale, int(bool(inverse)), strides, _stream(stream))
+
+
+def attn_rope_axes_append(q, q_out, k, v, kpages, vpages, page_table, seqlens, positions, axis_stride, position_stride,
+                          num_axes, new_lens, seqlens_out, inv_freq, axes, B, Hq, Hkv, T, d, rotary_dim, interleaved,
+                          out_scale, num_pages, page_size, max_pages, strides=None, stream=None) -> int:
+    return lib().attn_rope_axes_append(_ptr(q), _ptr(q_out), _ptr(k), _ptr(v), _ptr(kpages), _ptr(vpages),
+                                       _ptr(page_table), _ptr(seqlens), _ptr(positions), axis_stride, position_stride,
+                                       num_axes, _ptr(new_lens), _ptr(seqlens_out), _ptr(inv_freq), _ptr(axes), B, Hq,
+                                       Hkv, T, d, rotary_dim, int(bool(interleaved)), out_scale, num_pages, page_size,
+                                       max_pages, strides, _stream(stream))
+
+
 def attn_decode_prefix(q, kprefix, vprefix, kcache, vcache, seqlens, o, lse, weights, B, Hq, Hkv, P, d, scale,
                        max_seqlen, workspace, workspace_bytes, stream=None) -> int:
     return lib().attn_decode_prefix(_ptr(q), _ptr(kprefix), _ptr(vprefix), _ptr(kcache), _ptr(vcache), _ptr(seqlens),
@@ -586,6 +605,165 @@ def rope_append(q, k, v, kcache, vcache, seqlens, inv_freq=None, start_pos=None,
                                 torch._C._cuda_getCurrentRawStream(gpu))
     if rc:
         check(rc, "attn_rope_append")
+    return q_out, seqlens_out
+
+
+def rope_sections(sections, cycled=False, device=None):
+    """The axis of every rotated pair as an int32 CUDA tensor, for `rope_axes`
+    and `rope_axes_append`: `sections` says how many pairs each axis has, in runs
+    one behind the other, or with `cycled` dealt out in turn while an axis has
+    pairs left.  (`rope_freqs` gives the pairs' frequencies.)"""
+    import torch
+    left = [int(n) for n in sections]
+    if not 1 <= len(left) <= 4 or min(left) < 0 or sum(left) == 0:
+        raise AttnError(ATTN_ERR_ARG, "rope_sections: one to four axes with pairs")
+    if cycled:
+        rounds = [[a for a, n in enumerate(left) if n > i] for i in range(max(left))]
+        axes = [a for r in rounds for a in r]
+    else:
+        axes = [a for a, n in enumerate(left) for _ in range(n)]
+    return torch.tensor(axes, dtype=torch.int32, device="cuda" if device is None else device)
+
+
+def _axes_positions(what, positions, axes, pairs, B, N, gpu):
+    """(axes in all, axis stride, batch stride) of positions [A, N], [A, B, N] or, without `axes`, [N], [B, N]."""
+    import torch
+    axes is None or _fits(axes, torch.int32, (pairs,), gpu) or _refuse(what, "axes", axes, torch.int32, (pairs,))
+    if positions is None:
+        return 1, 0, 0
+    lead = positions.shape[:1] if axes is not None else ()
+    per_entry = positions.dim() == len(lead) + 2
+    shape = (*lead, B, N) if per_entry else (*lead, N)
+    _fits(positions, torch.int32, shape, gpu) or _refuse(what, "positions", positions, torch.int32, shape)
+    return (lead[0] if lead else 1), (B * N if per_entry else N), (N if per_entry else 0)
+
+
+def rope_axes(q, k, inv_freq, axes, positions, interleaved=False, out_scale=1.0, out=None, inverse=False, stream=None):
+    """`rope` where a token has a position on each of several axes, by
+    attn_rope_axes: `positions` is ``[A, N]`` or ``[A, B, N]`` int32 and `axes` ``[rotary_dim
+    / 2]`` int32 names the axis of every pair (`rope_sections` makes one; None: a
+    single axis, positions ``[N]`` or ``[B, N]``)."""
+    import torch
+    what, bf16 = "rope_axes", torch.bfloat16
+    gpu = q.get_device()
+    if stream is not None or gpu < 0 or gpu != torch._C._cuda_getDevice():
+        with _elsewhere(what, gpu, stream):
+            got = rope_axes(q, k, inv_freq, axes, positions, interleaved, out_scale, out, inverse)
+        _lend(stream, q, k, inv_freq, axes, positions, *(out or ()))
+        return got
+    if q.dim() != 4 or (k is not None and k.dim() != 4):
+        raise AttnError(ATTN_ERR_ARG, "rope_axes: q and k have to be [B, H, N, d]")
+    B, Hq, N, d = q.shape
+    pairs = inv_freq.numel()
+    _fits_rows(q, bf16, q.shape, gpu) or _refuse(what, "q", q, bf16, q.shape)
+    _fits(inv_freq, torch.float64, (pairs,), gpu) or _refuse(what, "inv_freq", inv_freq, torch.float64, (pairs,))
+    if positions is None:
+        raise AttnError(ATTN_ERR_ARG, "rope_axes: positions are missing")
+    num_axes, axis_stride, per_entry = _axes_positions(what, positions, axes, pairs, B, N, gpu)
+    q_out, k_out = (None, None) if out is None else out
+    if out is not None and (q_out is None or (k is None) != (k_out is None)):
+        raise AttnError(ATTN_ERR_ARG, "rope_axes: out has to hold q_out, and k_out exactly where there is a k")
+    if q_out is None:
+        q_out = torch.empty_like(q, memory_format=torch.contiguous_format)
+    else:
+        _fits_rows(q_out, bf16, q.shape, gpu) or _refuse(what, "q_out", q_out, bf16, q.shape)
+    Hkv, ks, kos = 0, (0, 0, 0, 1), (0, 0, 0, 1)
+    if k is not None:
+        Hkv = k.shape[1]
+        shape = (B, Hkv, N, d)
+        _fits_rows(k, bf16, shape, gpu) or _refuse(what, "k", k, bf16, shape)
+        if k_out is None:
+            k_out = torch.empty_like(k, memory_format=torch.contiguous_format)
+        else:
+            _fits_rows(k_out, bf16, shape, gpu) or _refuse(what, "k_out", k_out, bf16, shape)
+        ks, kos = k.stride(), k_out.stride()
+    rc = lib().attn_rope_axes(q.data_ptr(), q_out.data_ptr(), None if k is None else k.data_ptr(),
+                              None if k is None else k_out.data_ptr(), positions.data_ptr(), axis_stride, per_entry,
+                              num_axes, inv_freq.data_ptr(), None if axes is None else axes.data_ptr(), B, Hq, Hkv, N, d,
+                              2 * pairs, interleaved, out_scale, inverse,
+                              _strides(*q.stride()[:3], *q_out.stride()[:3], *ks[:3], *kos[:3]),
+                              torch._C._cuda_getCurrentRawStream(gpu))
+    if rc:
+        check(rc, "attn_rope_axes")
+    return q_out, k_out
+
+
+def rope_axes_backward(dq, dk, inv_freq, axes, positions, interleaved=False, out_scale=1.0, out=None, stream=None):
+    """Gradients of `rope_axes` (the arguments it was called with): from those
+    of its outputs to those of its inputs; returns ``(dq_in, dk_in)``."""
+    return rope_axes(dq, dk, inv_freq, axes, positions, interleaved, out_scale, out, True, stream)
+
+
+def _paged(what, kcache, vcache, page_table, B, gpu):
+    """(Hkv, d, pages, page size, pages a sequence) of contiguous caches ``[B, Hkv, slots, d]`` or, with a table ``[B,
+    max_pages]``, pools of pages ``[pages, Hkv, page_size, d]``."""
+    import torch
+    bf16 = torch.bfloat16
+    if kcache is None or kcache.dim() != 4:
+        raise AttnError(ATTN_ERR_ARG, f"{what}: the caches have to be [B, Hkv, slots, d], or pages [pages, Hkv, page_size, d]")
+    pages, Hkv, page, d = shape = kcache.shape
+    _fits(kcache, bf16, shape, gpu) or _refuse(what, "kcache", kcache, bf16, shape)
+    _fits(vcache, bf16, shape, gpu) or _refuse(what, "vcache", vcache, bf16, shape)
+    if page_table is None:
+        if pages != B:
+            raise AttnError(ATTN_ERR_ARG, f"{what}: {pages} caches for {B} sequences, and no page table")
+        return Hkv, d, pages, page, 1
+    per = page_table.shape[-1]
+    _fits(page_table, torch.int32, (B, per), gpu) or _refuse(what, "page_table", page_table, torch.int32, (B, per))
+    return Hkv, d, pages, page, per
+
+
+def rope_axes_append(q, k, v, kcache, vcache, seqlens, inv_freq=None, axes=None, positions=None, page_table=None,
+                     new_lens=None, interleaved=False, out_scale=1.0, q_out=None, seqlens_out=None, stream=None):
+    """Rotate the new tokens' q ``[B, Hq, T, d]`` and append their rotated k
+    and their v ``[B, Hkv, T, d]`` by attn_rope_axes_append: to contiguous caches
+    ``[B, Hkv, slots, d]`` or, with `page_table` ``[B, max_pages]`` int32, to pages
+    ``[pages, Hkv, page_size, d]``.  `positions` and `axes` as in `rope_axes`;
+    without positions the tokens count on from `seqlens`.  Allocates the outputs that
+    are not given; returns ``(q_out, seqlens_out)``."""
+    import torch
+    what, bf16, i32 = "rope_axes_append", torch.bfloat16, torch.int32
+    gpu = q.get_device()
+    if stream is not None or gpu < 0 or gpu != torch._C._cuda_getDevice():
+        with _elsewhere(what, gpu, stream):
+            got = rope_axes_append(q, k, v, kcache, vcache, seqlens, inv_freq, axes, positions, page_table, new_lens,
+                                   interleaved, out_scale, q_out, seqlens_out)
+        _lend(stream, q, k, v, kcache, vcache, seqlens, inv_freq, axes, positions, page_table, new_lens, q_out, seqlens_out)
+        return got
+    if q.dim() != 4:
+        raise AttnError(ATTN_ERR_ARG, "rope_axes_append: q has to be [B, Hq, T, d]")
+    B, Hq, T, d = q.shape
+    Hkv, cols, pages, page, per = _paged(what, kcache, vcache, page_table, B, gpu)
+    new = (B, Hkv, T, cols)
+    _fits_rows(q, bf16, (B, Hq, T, cols), gpu) or _refuse(what, "q", q, bf16, (B, Hq, T, cols))
+    _fits_rows(k, bf16, new, gpu) or _refuse(what, "k", k, bf16, new)
+    _fits_rows(v, bf16, new, gpu) or _refuse(what, "v", v, bf16, new)
+    _fits(seqlens, i32, (B,), gpu) or _refuse(what, "seqlens", seqlens, i32, (B,))
+    new_lens is None or _fits(new_lens, i32, (B,), gpu) or _refuse(what, "new_lens", new_lens, i32, (B,))
+    pairs = 0
+    if inv_freq is not None:
+        pairs = inv_freq.numel()
+        _fits(inv_freq, torch.float64, (pairs,), gpu) or _refuse(what, "inv_freq", inv_freq, torch.float64, (pairs,))
+    num_axes, axis_stride, per_entry = _axes_positions(what, positions, axes, pairs, B, T, gpu)
+    if q_out is None:
+        q_out = torch.empty_like(q, memory_format=torch.contiguous_format)
+    else:
+        _fits_rows(q_out, bf16, q.shape, gpu) or _refuse(what, "q_out", q_out, bf16, q.shape)
+    if seqlens_out is None:
+        seqlens_out = torch.empty_like(seqlens)
+    else:
+        _fits(seqlens_out, i32, (B,), gpu) or _refuse(what, "seqlens_out", seqlens_out, i32, (B,))
+    rc = lib().attn_rope_axes_append(q.data_ptr(), q_out.data_ptr(), k.data_ptr(), v.data_ptr(), kcache.data_ptr(),
+                                     vcache.data_ptr(), None if page_table is None else page_table.data_ptr(),
+                                     seqlens.data_ptr(), None if positions is None else positions.data_ptr(), axis_stride,
+                                     per_entry, num_axes, None if new_lens is None else new_lens.data_ptr(),
+                                     seqlens_out.data_ptr(), None if inv_freq is None else inv_freq.data_ptr(),
+                                     None if axes is None else axes.data_ptr(), B, Hq, Hkv, T, d, 2 * pairs, interleaved,
+                                     out_scale, pages, page, per,
+                                     _strides(*q.stride()[:3], *q_out.stride()[:3], *k.stride()[:3], *v.stride()[:3]),
+                                     torch._C._cuda_getCurrentRawStream(gpu))
+    if rc:
+        check(rc, "attn_rope_axes_append")
     return q_out, seqlens_out
 
 

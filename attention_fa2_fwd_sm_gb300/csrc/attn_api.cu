@@ -723,6 +723,52 @@ static bool shares_with_itself(const Rows &a) {
 static Rows rows_in(const RopeTensor &t, int B, int N, int d) { return Rows(t.in, {t.in_b, t.in_h, t.in_n}, B, t.heads, N, d); }
 static Rows rows_out(const RopeTensor &t, int B, int N, int d) { return Rows(t.out, {t.out_b, t.out_h, t.out_n}, B, t.heads, N, d); }
 
+// The tensors of a rotation, and that no output is laid over what it must not be.
+static int rope_tensors(RopeLaunch *a, const void *q, void *q_out, const void *k, void *k_out, int B, int Hq, int Hkv, int N,
+                        int d, const long long *strides) {
+    int rc = rope_tensor(&a->t[0], q, q_out, strides, strides ? strides + 3 : nullptr, B, Hq, N, d);
+    if (rc == ATTN_OK && k)
+        rc = rope_tensor(&a->t[1], k, k_out, strides ? strides + 6 : nullptr, strides ? strides + 9 : nullptr, B, Hkv, N, d);
+    if (rc != ATTN_OK) return rc;
+    for (int i = 0; i < 2; ++i)
+        for (int j = 0; j < 2; ++j) {
+            const Rows in = rows_in(a->t[i], B, N, d), out = rows_out(a->t[j], B, N, d);
+            if (!(i == j && in.same(out)) && share_elements(in, out)) return ATTN_ERR_ARG;
+        }
+    if (share_elements(rows_out(a->t[0], B, N, d), rows_out(a->t[1], B, N, d))) return ATTN_ERR_ARG;
+    if (shares_with_itself(rows_out(a->t[0], B, N, d)) || shares_with_itself(rows_out(a->t[1], B, N, d))) return ATTN_ERR_ARG;
+    return ATTN_OK;
+}
+
+// The same for an append into caches [entries, Hkv, slots, d].
+static int append_tensors(RopeLaunch *a, const void *q, void *q_out, const void *k, const void *v, void *kcache,
+                          void *vcache, int B, int Hq, int Hkv, int T, int d, int entries, int slots,
+                          const long long *strides) {
+    const long long row = (long long)slots * d;
+    int rc = rope_tensor(&a->t[0], q, q_out, strides, strides ? strides + 3 : nullptr, B, Hq, T, d);
+    // The caches' strides are their own, so they are set apart from the inputs'.
+    for (int i = 1; rc == ATTN_OK && i < 3; ++i) {
+        rc = rope_tensor(&a->t[i], i == 1 ? k : v, i == 1 ? kcache : vcache, strides ? strides + 3 + 3 * i : nullptr,
+                         nullptr, B, Hkv, T, d);
+        a->t[i].out_b = Hkv * row;
+        a->t[i].out_h = row;
+        a->t[i].out_n = d;
+    }
+    if (rc != ATTN_OK) return rc;
+    // The outputs: q_out (which may be q) and all of both caches.
+    const Rows rotated = rows_out(a->t[0], B, T, d);
+    const Rows caches[2] = {rows_out(a->t[1], entries, slots, d), rows_out(a->t[2], entries, slots, d)};
+    for (int i = 0; i < 3; ++i) {
+        const Rows in = rows_in(a->t[i], B, T, d);
+        if ((i > 0 || !in.same(rotated)) && share_elements(in, rotated)) return ATTN_ERR_ARG;
+        for (const Rows &cache : caches)
+            if (share_elements(in, cache)) return ATTN_ERR_ARG;
+    }
+    if (shares_with_itself(rotated) || share_elements(rotated, caches[0]) || share_elements(rotated, caches[1]) || share_elements(caches[0], caches[1]))
+        return ATTN_ERR_ARG;
+    return ATTN_OK;
+}
+
 static bool aligned4(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 
 static int rope_common(const double *inv_freq, int B, int Hq, int N, int d, int rotary_dim, float out_scale,
@@ -742,17 +788,8 @@ int attn_rope(const void *q, void *q_out, const void *k, void *k_out, const int 
     if (rc != ATTN_OK) return rc;
     if (!aligned4(positions) || position_stride < 0 || (!k != !k_out) || (k && Hkv <= 0)) return ATTN_ERR_ARG;
     RopeLaunch a;
-    rc = rope_tensor(&a.t[0], q, q_out, strides, strides ? strides + 3 : nullptr, B, Hq, N, d);
-    if (rc == ATTN_OK && k)
-        rc = rope_tensor(&a.t[1], k, k_out, strides ? strides + 6 : nullptr, strides ? strides + 9 : nullptr, B, Hkv, N, d);
+    rc = rope_tensors(&a, q, q_out, k, k_out, B, Hq, Hkv, N, d, strides);
     if (rc != ATTN_OK) return rc;
-    for (int i = 0; i < 2; ++i)
-        for (int j = 0; j < 2; ++j) {
-            const Rows in = rows_in(a.t[i], B, N, d), out = rows_out(a.t[j], B, N, d);
-            if (!(i == j && in.same(out)) && share_elements(in, out)) return ATTN_ERR_ARG;
-        }
-    if (share_elements(rows_out(a.t[0], B, N, d), rows_out(a.t[1], B, N, d))) return ATTN_ERR_ARG;
-    if (shares_with_itself(rows_out(a.t[0], B, N, d)) || shares_with_itself(rows_out(a.t[1], B, N, d))) return ATTN_ERR_ARG;
     a.inv_freq = inv_freq;
     a.pos = positions;
     a.pos_stride = position_stride;
@@ -792,6 +829,12 @@ int attn_rope_freqs(double *inv_freq, int rotary_dim, double base, int rule, dou
     return ATTN_OK;
 }
 
+// Whether [a, a + n) and [b, b + m) share a byte.
+static bool bytes_overlap(const void *a, size_t n, const void *b, size_t m) {
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+    return a && b && x < y + m && y < x + n;
+}
+
 static bool ints_overlap(const int *a, const int *b, int n) { return a && b && a < b + n && b < a + n; }
 
 int attn_rope_append(const void *q, void *q_out, const void *k, const void *v, void *kcache, void *vcache,
@@ -811,26 +854,8 @@ int attn_rope_append(const void *q, void *q_out, const void *k, const void *v, v
     const long long row = (long long)max_seqlen * d;
     if ((double)B * Hkv * (double)row >= 9.0e18) return ATTN_ERR_ARG;
     RopeLaunch a;
-    rc = rope_tensor(&a.t[0], q, q_out, strides, strides ? strides + 3 : nullptr, B, Hq, T, d);
-    // The caches' strides are their own, so they are set apart from the inputs'.
-    for (int i = 1; rc == ATTN_OK && i < 3; ++i) {
-        rc = rope_tensor(&a.t[i], i == 1 ? k : v, i == 1 ? kcache : vcache, strides ? strides + 3 + 3 * i : nullptr,
-                         nullptr, B, Hkv, T, d);
-        a.t[i].out_b = Hkv * row;
-        a.t[i].out_h = row;
-        a.t[i].out_n = d;
-    }
+    rc = append_tensors(&a, q, q_out, k, v, kcache, vcache, B, Hq, Hkv, T, d, B, max_seqlen, strides);
     if (rc != ATTN_OK) return rc;
-    // The outputs: q_out (which may be q) and all of both caches.
-    const Rows rotated = rows_out(a.t[0], B, T, d), caches[2] = {rows_out(a.t[1], B, max_seqlen, d), rows_out(a.t[2], B, max_seqlen, d)};
-    for (int i = 0; i < 3; ++i) {
-        const Rows in = rows_in(a.t[i], B, T, d);
-        if ((i > 0 || !in.same(rotated)) && share_elements(in, rotated)) return ATTN_ERR_ARG;
-        for (const Rows &cache : caches)
-            if (share_elements(in, cache)) return ATTN_ERR_ARG;
-    }
-    if (shares_with_itself(rotated) || share_elements(rotated, caches[0]) || share_elements(rotated, caches[1]) || share_elements(caches[0], caches[1]))
-        return ATTN_ERR_ARG;
     a.inv_freq = inv_freq;
     a.pos = start_pos;
     a.B = B;
@@ -846,6 +871,106 @@ int attn_rope_append(const void *q, void *q_out, const void *k, const void *v, v
     a.cache_pos = cache_pos;
     a.weights = weights;
     a.max_seqlen = max_seqlen;
+    a.num_sms = current_num_sms();
+    if (a.num_sms <= 0) return note_cuda_error(cudaErrorNoDevice, "device query");
+    return rope_launch(a, reinterpret_cast<cudaStream_t>(stream));
+}
+
+// The caches of the paged calls (see attn.h): whether the sizes fit each other.
+static int paged_sizes(const int *page_table, int B, int Hkv, int num_pages, int page_size, int max_pages) {
+    if (B <= 0 || Hkv <= 0 || num_pages <= 0 || page_size <= 0 || max_pages <= 0) return ATTN_ERR_ARG;
+    if ((reinterpret_cast<uintptr_t>(page_table) & 3u) != 0) return ATTN_ERR_ARG;
+    if ((long long)page_size * max_pages > (1LL << 30)) return ATTN_ERR_ARG;
+    if ((long long)num_pages * Hkv > 0x7fffffffLL || (long long)B * Hkv > 0x7fffffffLL) return ATTN_ERR_ARG;
+    if (page_table) return page_size < 16 || page_size > 65536 || (page_size & (page_size - 1)) ? ATTN_ERR_ARG : ATTN_OK;
+    return num_pages != B || max_pages != 1 ? ATTN_ERR_ARG : ATTN_OK;
+}
+
+// log2 of the page size; one page a sequence: above every row.
+static int page_shift_of(const int *page_table, int page_size) {
+    int s = 0;
+    while (page_table && (1 << s) < page_size) ++s;
+    return page_table ? s : 30;
+}
+
+static int axes_common(const int *positions, long long axis_stride, long long position_stride, int num_axes,
+                       const int *axes) {
+    if (!aligned4(positions) || !aligned4(axes)) return ATTN_ERR_ARG;
+    if (axis_stride < 0 || position_stride < 0 || num_axes < 1 || num_axes > 4) return ATTN_ERR_ARG;
+    return ATTN_OK;
+}
+
+int attn_rope_axes(const void *q, void *q_out, const void *k, void *k_out, const int *positions, long long axis_stride,
+                   long long position_stride, int num_axes, const double *inv_freq, const int *axes, int B, int Hq,
+                   int Hkv, int N, int d, int rotary_dim, int interleaved, float out_scale, int inverse,
+                   const long long *strides, attn_stream_t stream) {
+    int rc = rope_common(inv_freq, B, Hq, N, d, rotary_dim, out_scale, 2);
+    if (rc == ATTN_OK) rc = axes_common(positions, axis_stride, position_stride, num_axes, axes);
+    if (rc != ATTN_OK) return rc;
+    if (!positions || (!k != !k_out) || (k && Hkv <= 0)) return ATTN_ERR_ARG;
+    RopeLaunch a;
+    rc = rope_tensors(&a, q, q_out, k, k_out, B, Hq, Hkv, N, d, strides);
+    if (rc != ATTN_OK) return rc;
+    a.inv_freq = inv_freq;
+    a.pos = positions;
+    a.pos_stride = position_stride;
+    a.axis_stride = axis_stride;
+    a.num_axes = num_axes;
+    a.axes = axes;
+    a.B = B;
+    a.N = N;
+    a.d = d;
+    a.rotary_dim = rotary_dim;
+    a.interleaved = interleaved ? 1 : 0;
+    a.inverse = inverse ? 1 : 0;
+    a.out_scale = out_scale;
+    a.num_sms = current_num_sms();
+    if (a.num_sms <= 0) return note_cuda_error(cudaErrorNoDevice, "device query");
+    return rope_launch(a, reinterpret_cast<cudaStream_t>(stream));
+}
+
+int attn_rope_axes_append(const void *q, void *q_out, const void *k, const void *v, void *kpages, void *vpages,
+                          const int *page_table, const int *seqlens, const int *positions, long long axis_stride,
+                          long long position_stride, int num_axes, const int *new_lens, int *seqlens_out,
+                          const double *inv_freq, const int *axes, int B, int Hq, int Hkv, int T, int d, int rotary_dim,
+                          int interleaved, float out_scale, int num_pages, int page_size, int max_pages,
+                          const long long *strides, attn_stream_t stream) {
+    int rc = rope_common(inv_freq, B, Hq, T, d, rotary_dim, out_scale, 0);
+    if (rc == ATTN_OK) rc = axes_common(positions, axis_stride, position_stride, num_axes, axes);
+    if (rc == ATTN_OK) rc = paged_sizes(page_table, B, Hkv, num_pages, page_size, max_pages);
+    if (rc != ATTN_OK) return rc;
+    if (!seqlens || !aligned4(seqlens) || !aligned4(new_lens) || !aligned4(seqlens_out)) return ATTN_ERR_ARG;
+    if (ints_overlap(seqlens_out, seqlens, B) || ints_overlap(seqlens_out, new_lens, B)) return ATTN_ERR_ARG;
+    if (seqlens_out && page_table &&
+        bytes_overlap(seqlens_out, size_t(B) * 4, page_table, size_t(B) * max_pages * 4))
+        return ATTN_ERR_ARG;
+    if (!aligned16(kpages) || !aligned16(vpages)) return ATTN_ERR_ARG;
+    const long long row = (long long)page_size * d;
+    if ((double)num_pages * Hkv * (double)row >= 9.0e18) return ATTN_ERR_ARG;
+    RopeLaunch a;
+    rc = append_tensors(&a, q, q_out, k, v, kpages, vpages, B, Hq, Hkv, T, d, num_pages, page_size, strides);
+    if (rc != ATTN_OK) return rc;
+    a.inv_freq = inv_freq;
+    a.pos = positions;
+    a.pos_stride = position_stride;
+    a.axis_stride = axis_stride;
+    a.num_axes = num_axes;
+    a.axes = axes;
+    a.table = page_table;
+    a.max_pages = max_pages;
+    a.num_pages = num_pages;
+    a.page_shift = page_shift_of(page_table, page_size);
+    a.B = B;
+    a.N = T;
+    a.d = d;
+    a.rotary_dim = rotary_dim;
+    a.interleaved = interleaved ? 1 : 0;
+    a.out_scale = out_scale;
+    a.append = true;
+    a.lens = seqlens;
+    a.new_lens = new_lens;
+    a.lens_out = seqlens_out;
+    a.max_seqlen = page_size * max_pages;
     a.num_sms = current_num_sms();
     if (a.num_sms <= 0) return note_cuda_error(cudaErrorNoDevice, "device query");
     return rope_launch(a, reinterpret_cast<cudaStream_t>(stream));
@@ -940,12 +1065,6 @@ size_t attn_cache_evict_workspace_bytes(int B, int Hkv, int max_seqlen, int keep
     a.keep = keep;
     a.kout = in_place ? nullptr : &a;  // in place: the same address as kcache
     return evict_workspace_bytes(a);
-}
-
-// Whether [a, a + n) and [b, b + m) share a byte.
-static bool bytes_overlap(const void *a, size_t n, const void *b, size_t m) {
-    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
-    return a && b && x < y + m && y < x + n;
 }
 
 int attn_cache_evict(const void *kcache, const void *vcache, const float *weights, const int *cache_pos,

@@ -146,6 +146,13 @@ struct RopeLaunch {
     int *lens_out = nullptr, *cache_pos = nullptr;
     float *weights = nullptr;
     int max_seqlen = 0;
+    // Several axes (num_axes > 0): pos is [axis][B][N], axis_stride and pos_stride apart (appending: null counts on from
+    // the lengths); out_b of the caches is a page's stride.
+    int num_axes = 0;
+    const int *axes = nullptr;   // axis of every pair (null: 0)
+    long long axis_stride = 0;
+    const int *table = nullptr;  // pages of every sequence (null: sequence b is page b)
+    int max_pages = 1, num_pages = 0, page_shift = 30;
     int num_sms;
 };
 int rope_launch(const RopeLaunch &a, cudaStream_t stream);
@@ -165,6 +172,35 @@ struct EvictLaunch {
 size_t evict_workspace_bytes(const EvictLaunch &a);
 int evict_launch(const EvictLaunch &a, cudaStream_t stream);
 int decode_launch(const DecodeLaunch &a, cudaStream_t stream);
+
+// The pages of a cache (pages_sm103.cu): tables, counts and copies.
+struct PagesLaunch {
+    int *table = nullptr, *table_out = nullptr, *refs = nullptr;
+    const int *seqlens = nullptr, *new_lens = nullptr, *parent = nullptr;
+    int *lens_out = nullptr, *info = nullptr;
+    void *kpages = nullptr, *vpages = nullptr;
+    int T = 0, layers = 1, B, Hkv = 1, d = 8, num_pages, page_size, max_pages;
+    char *workspace = nullptr;
+    int num_sms = 0;
+};
+size_t pages_workspace_bytes(int B, int num_pages);
+int pages_extend_launch(const PagesLaunch &a, cudaStream_t stream);
+int pages_fork_launch(const PagesLaunch &a, cudaStream_t stream);
+int pages_trim_launch(const PagesLaunch &a, cudaStream_t stream);
+int pages_compact_launch(const PagesLaunch &a, cudaStream_t stream);
+
+// Trees of drafted tokens (tree_sm103.cu): masks, and the accepted path's rows.
+struct TreeLaunch {
+    const int *parents = nullptr, *seqlens = nullptr, *draft_lens = nullptr, *last = nullptr;
+    unsigned long long *mask_out = nullptr;
+    const unsigned long long *mask = nullptr;
+    int *positions = nullptr, *lens_out = nullptr;
+    void *kpages = nullptr, *vpages = nullptr;
+    const int *table = nullptr;
+    int B, T, layers = 1, Hkv = 1, d = 8, num_pages = 0, page_size = 0, page_shift = 0, max_pages = 0;
+};
+int tree_mask_launch(const TreeLaunch &a, cudaStream_t stream);
+int tree_accept_launch(const TreeLaunch &a, cudaStream_t stream);
 
 // Decode over a shared prefix and the sequences' own keys
 // (decode_prefix_sm103.cu).  Byte offsets of the workspace's parts: the own

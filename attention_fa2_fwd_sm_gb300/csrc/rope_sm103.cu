@@ -27,6 +27,12 @@
 // thread 100 us (the sines), 4 or 16 heads 48.5, loads of 2 or 8 heads at a time
 // 49.0 and 48.6.  2048 tokens, 32 + 8 heads: 8.9 us in blocks of 128 threads, 10.3
 // in blocks of 256, whose last wave is the coarser.
+//
+// Several axes (kAxes): a token has up to four positions (time, height, width; the
+// depth in a tree) and pair i turns by the one that axes[i] names.  The phase of a
+// pair is then its own axis's product; nothing else changes, and nothing else is
+// read but 4 bytes an axis and token.  Appending by axes also looks the row's page
+// up: a row of a sequence is a row of one of its pages.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -41,6 +47,7 @@ constexpr int kThreads = 128;
 constexpr int kMaxHeads = 8;   // heads a thread visits with one set of sines
 constexpr int kBatch = 4;      // heads whose loads are in flight together
 constexpr int kMaxPairs = 256; // rotary_dim <= 512
+constexpr int kMaxAxes = 4;
 
 // Item layouts.  Vector items are 8 columns (16 bytes), half: 8 columns and
 // the 8 that they pair with; the pair forms take any even rotary_dim, one
@@ -60,6 +67,11 @@ struct Params {
     long long tokens;     // B * N
     int N, r, items, rot_items, max_seqlen;
     float scale, sign;
+    // kAxes
+    const int *axes;       // [r / 2] (null: all 0)
+    const int *table;      // [B, max_pages] (null: sequence b's only page is b)
+    long long axis_stride; // between the axes in pos
+    int num_axes, max_pages, num_pages, page_shift;
 };
 
 // 2^130 / (2 pi), rounded: its upper and its lower 64 bits.
@@ -115,10 +127,14 @@ __device__ __forceinline__ void turn_inter(uint4 &x, const float (&c)[8], const 
 }
 
 // Grid: x over (token, item), y over the head chunks of q, then k, then v.
-template <int kLayout, bool kAppend>
+template <int kLayout, bool kAppend, bool kAxes>
 __global__ void __launch_bounds__(kThreads) rope_kernel(const Params p) {
     __shared__ unsigned long long turns[kMaxPairs];
-    for (int i = threadIdx.x; i < p.r / 2; i += kThreads) turns[i] = turns_of(p.inv_freq[i]);
+    __shared__ int axis_of[kAxes ? kMaxPairs : 1];
+    for (int i = threadIdx.x; i < p.r / 2; i += kThreads) {
+        turns[i] = turns_of(p.inv_freq[i]);
+        if constexpr (kAxes) axis_of[i] = p.axes ? min(max(p.axes[i], 0), p.num_axes - 1) : 0;
+    }
     __syncthreads();
 
     const long long flat = (long long)blockIdx.x * kThreads + threadIdx.x;
@@ -133,17 +149,43 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const Params p) {
     const RopeTensor &t = p.t[which];
     const int h0 = chunk * p.heads_per_chunk, h1 = min(h0 + p.heads_per_chunk, t.heads);
 
-    int pos;
-    long long row = n;  // row of the output
+    int pos = 0, more[kMaxAxes - 1] = {};  // on axis 0 and on the others
+    long long row = n, entry = b;      // row of the output, and the batch entry or page that it is in
     bool store = true;
+    if constexpr (kAxes) {
+        if (p.pos) {
+            const int *at = p.pos + b * p.pos_stride + n;
+            pos = at[0];
+#pragma unroll
+            for (int a = 1; a < kMaxAxes; ++a)
+                if (a < p.num_axes) more[a - 1] = at[a * p.axis_stride];
+        }
+    }
+    auto pos_of = [&](int pair) {
+        if constexpr (!kAxes) return pos;
+        const int a = axis_of[pair];
+        return a == 0 ? pos : a == 1 ? more[0] : a == 2 ? more[1] : more[2];
+    };
     if constexpr (kAppend) {
         const int len = min(max(p.lens[b], 0), p.max_seqlen);
         const int added = p.new_lens ? min(max(p.new_lens[b], 0), p.N) : p.N;
-        pos = int(unsigned(p.pos ? p.pos[b] : len) + unsigned(n));
+        if constexpr (!kAxes) {
+            pos = int(unsigned(p.pos ? p.pos[b] : len) + unsigned(n));
+        } else if (!p.pos) {
+            pos = int(unsigned(len) + unsigned(n));
+            more[0] = more[1] = more[2] = pos;
+        }
         if (which > 0) {
             row = (long long)len + n;
             store = n < added && row < p.max_seqlen;
-            if (which == 1 && item == 0 && store) {
+            if constexpr (kAxes) {
+                if (store && p.table) {
+                    const int page = p.table[(long long)b * p.max_pages + (row >> p.page_shift)];
+                    store = page >= 0 && page < p.num_pages;
+                    entry = page;
+                }
+                row &= (1LL << p.page_shift) - 1;
+            } else if (which == 1 && item == 0 && store) {
                 for (int h = h0; h < h1; ++h) {
                     const long long at = ((long long)b * t.heads + h) * p.max_seqlen + row;
                     if (p.cache_pos) p.cache_pos[at] = pos;
@@ -154,19 +196,19 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const Params p) {
             p.lens_out[b] = int(min((long long)len + added, (long long)p.max_seqlen));
         }
         if (!store) return;
-    } else {
+    } else if constexpr (!kAxes) {
         pos = p.pos ? p.pos[b * p.pos_stride + n] : n;
     }
     const bool turn = item < p.rot_items && which < 2;
     const __nv_bfloat16 *src = t.in + b * t.in_b + n * t.in_n;
-    __nv_bfloat16 *dst = t.out + b * t.out_b + row * t.out_n;
+    __nv_bfloat16 *dst = t.out + entry * t.out_b + row * t.out_n;
 
     if constexpr (kLayout == kHalfVec || kLayout == kInterVec) {
         constexpr int kFreqs = kLayout == kHalfVec ? 8 : 4;
         float c[8], s[8];
         if (turn)
 #pragma unroll
-            for (int i = 0; i < kFreqs; ++i) sin_cos(turns[item * kFreqs + i], pos, p.sign, p.scale, c[i], s[i]);
+            for (int i = 0; i < kFreqs; ++i) sin_cos(turns[item * kFreqs + i], pos_of(item * kFreqs + i), p.sign, p.scale, c[i], s[i]);
         if (kLayout == kHalfVec && item < p.rot_items) {
             src += item * 8;
             dst += item * 8;
@@ -211,7 +253,7 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const Params p) {
         const bool split = kLayout == kHalfPair && item < p.rot_items;
         const int cx = split ? item : 2 * item, cy = split ? item + p.r / 2 : 2 * item + 1;
         float c = 1.f, s = 0.f;
-        if (turn) sin_cos(turns[item], pos, p.sign, p.scale, c, s);
+        if (turn) sin_cos(turns[item], pos_of(item), p.sign, p.scale, c, s);
         for (int h = h0; h < h1; ++h) {
             const __nv_bfloat16 *q = src + h * t.in_h;
             __nv_bfloat16 x = q[cx], y = q[cy];
@@ -224,6 +266,16 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const Params p) {
             w[cx] = x;
             w[cy] = y;
         }
+    }
+}
+
+template <bool kAppend, bool kAxes>
+auto kernel_of(int layout) {
+    switch (layout) {
+        case kHalfVec: return rope_kernel<kHalfVec, kAppend, kAxes>;
+        case kInterVec: return rope_kernel<kInterVec, kAppend, kAxes>;
+        case kHalfPair: return rope_kernel<kHalfPair, kAppend, kAxes>;
+        default: return rope_kernel<kInterPair, kAppend, kAxes>;
     }
 }
 
@@ -254,6 +306,13 @@ int rope_launch(const RopeLaunch &a, cudaStream_t stream) {
     p.max_seqlen = a.max_seqlen;
     p.scale = a.out_scale;
     p.sign = a.inverse ? -1.f : 1.f;
+    p.axes = a.axes;
+    p.table = a.table;
+    p.axis_stride = a.axis_stride;
+    p.num_axes = a.num_axes;
+    p.max_pages = a.max_pages;
+    p.num_pages = a.num_pages;
+    p.page_shift = a.page_shift;
     const long long gx = (p.tokens * p.items + kThreads - 1) / kThreads;
     // Heads per thread: as many as share the sines while the grid still has two
     // blocks per SM; a short call takes one head a thread.  In us, one head and
@@ -273,13 +332,8 @@ int rope_launch(const RopeLaunch &a, cudaStream_t stream) {
     }
     const long long gy = grid_y(per);
     if (gx > 0x7fffffffLL || gy > 65535) return ATTN_ERR_ARG;
-    void (*kernel)(Params) = nullptr;
-    switch (layout) {
-        case kHalfVec: kernel = a.append ? rope_kernel<kHalfVec, true> : rope_kernel<kHalfVec, false>; break;
-        case kInterVec: kernel = a.append ? rope_kernel<kInterVec, true> : rope_kernel<kInterVec, false>; break;
-        case kHalfPair: kernel = a.append ? rope_kernel<kHalfPair, true> : rope_kernel<kHalfPair, false>; break;
-        default: kernel = a.append ? rope_kernel<kInterPair, true> : rope_kernel<kInterPair, false>;
-    }
+    void (*kernel)(Params) = a.num_axes > 0 ? (a.append ? kernel_of<true, true>(layout) : kernel_of<false, true>(layout))
+                                            : (a.append ? kernel_of<true, false>(layout) : kernel_of<false, false>(layout));
     kernel<<<dim3(unsigned(gx), unsigned(gy)), kThreads, 0, stream>>>(p);
     const cudaError_t e = cudaGetLastError();
     return e == cudaSuccess ? 0 : note_cuda_error(e, "rope_kernel launch");

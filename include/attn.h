@@ -27,9 +27,9 @@
  *  - Return value: ATTN_OK (0) or one of the negative ATTN_ERR_* codes.
  *    attn_strerror() gives a message for each.
  *  - CUDA graphs: the launches of attn_fwd, attn_fwd_ex, attn_fwd_host,
- *    attn_bwd, the decode entry points, attn_rope, attn_rope_append and
- *    attn_cache_evict can be captured into a CUDA graph on `stream` and
- *    replayed; a replay reads what the buffers hold at replay time (seqlens
+ *    attn_bwd, the decode entry points, the attn_rope*, attn_tree* and
+ *    attn_pages* calls and attn_cache_evict can be captured into a CUDA graph on
+ *    `stream` and replayed; a replay reads what the buffers hold at replay time (seqlens
  *    included: the ragged decode and attn_decode_prefix plan on the device).
  *    Make one ordinary call per device first (it sets up per-device state:
  *    kernel attributes, scratch addresses, the die map, the host-copy
@@ -503,6 +503,63 @@ int attn_rope_append(const void *q, void *q_out, const void *k, const void *v, v
                      int *cache_pos, float *weights, const double *inv_freq, int B, int Hq, int Hkv, int T, int d,
                      int rotary_dim, int interleaved, float out_scale, int max_seqlen, const long long *strides,
                      attn_stream_t stream);
+
+/*
+ * Rotary positions with several axes: a token has num_axes positions (time,
+ * height and width of an image or a video; a drafted token's depth), and pair i
+ * turns by the one that its axis names,
+ *     a = positions[axes[i]] * inv_freq[i],
+ * otherwise as attn_rope, with the same gradient (inverse != 0).
+ *   positions  int32 device array: axis a, batch entry b, token n at
+ *              positions[a * axis_stride + b * position_stride + n]
+ *              (position_stride 0: one row for all of them)
+ *   num_axes   1 to 4
+ *   axes       [rotary_dim / 2] int32 device array, or NULL: all 0.  Values are
+ *              clamped to [0, num_axes - 1].
+ * Other arguments, what may overlap, and errors as attn_rope.  One kernel on
+ * `stream`.
+ */
+int attn_rope_axes(const void *q, void *q_out, const void *k, void *k_out, const int *positions, long long axis_stride,
+                   long long position_stride, int num_axes, const double *inv_freq, const int *axes, int B, int Hq,
+                   int Hkv, int N, int d, int rotary_dim, int interleaved, float out_scale, int inverse,
+                   const long long *strides, attn_stream_t stream);
+
+/*
+ * A cache in pages, as attn_rope_axes_append, attn_decode_tree,
+ * attn_tree_accept and the attn_pages_* calls take it:
+ *   kpages, vpages  [num_pages, Hkv, page_size, d] bf16
+ *   page_table      [B, max_pages] int32: the page that holds rows
+ *                   [i page_size, (i + 1) page_size) of sequence b is
+ *                   page_table[b, i].  A value outside [0, num_pages) is no page:
+ *                   keys there do not exist, rows for it are not stored.
+ *   page_size       a power of two from 16 to 65536; max_pages * page_size is a
+ *                   sequence's capacity, at most 2^30.
+ * page_table = NULL is a contiguous cache [B, Hkv, page_size, d] of any
+ * page_size: sequence b's only page is b, max_pages is 1 and num_pages B.
+ * Sequences may share pages that are only read (attn_pages_fork); a page that
+ * rows are stored to belongs to one sequence (attn_pages_extend sees to it).
+ */
+
+/*
+ * attn_rope_append by positions with several axes, into pages or contiguous
+ * caches: T new tokens per sequence, q rotated into q_out, k rotated and v copied
+ * into the rows behind each sequence's last.  Unlike attn_rope_append's, the
+ * tokens' positions need not count on from each other: the drafted tokens of a
+ * tree have their depths (attn_tree_mask), an image's its grid.
+ *   positions  as in attn_rope_axes, or NULL: token t has position seqlens[b] + t
+ *              on every axis
+ *   seqlens, new_lens, seqlens_out  as in attn_rope_append (capacity max_pages *
+ *              page_size)
+ *   num_axes, axes  as in attn_rope_axes;  rotary_dim may be 0 (inv_freq NULL)
+ * Other arguments, what may overlap, and errors as attn_rope_append.  Rows that
+ * no token goes to are left as they were.  One kernel on `stream`.
+ */
+int attn_rope_axes_append(const void *q, void *q_out, const void *k, const void *v, void *kpages, void *vpages,
+                          const int *page_table, const int *seqlens, const int *positions, long long axis_stride,
+                          long long position_stride, int num_axes, const int *new_lens, int *seqlens_out,
+                          const double *inv_freq, const int *axes, int B, int Hq, int Hkv, int T, int d, int rotary_dim,
+                          int interleaved, float out_scale, int num_pages, int page_size, int max_pages,
+                          const long long *strides, attn_stream_t stream);
 
 /*
  * Decode for a batch whose sequences share a prefix (one query row per

@@ -1,0 +1,87 @@
+"""CPU-only checks of the entry points of the paged cache and of drafted tokens:
+refusals come from the host before any CUDA call, and the torch helpers refuse
+tensors whose addresses alone would not tell.  No kernel runs."""
+import ctypes
+
+import pytest
+import torch
+
+import attention_fa2_fwd_sm_gb300 as attn
+from attention_fa2_fwd_sm_gb300 import _build
+
+A16 = 0x10000  # a fake 16-byte-aligned address: never dereferenced by these calls
+ARG, UNSUP, WS = attn.ATTN_ERR_ARG, attn.ATTN_ERR_UNSUPPORTED, attn.ATTN_ERR_WORKSPACE
+MB = 1 << 20
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _built():
+    _build.build()
+    attn.lib()
+
+
+def _axes(**kw):
+    a = dict(q=A16, q_out=A16 + MB, k=A16 + 2 * MB, k_out=A16 + 3 * MB, pos=A16, axis_stride=48, pos_stride=16, A=2, freqs=A16,
+             axes=A16, B=3, Hq=2, Hkv=2, N=16, d=64, r=64, inter=0, scale=1.0, inverse=0, strides=None)
+    a.update(kw)
+    return attn.attn_rope_axes(*a.values(), stream=0)
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(q=None), ARG), (dict(q=A16 + 8), ARG), (dict(q_out=None), ARG), (dict(k_out=None), ARG), (dict(k=None), ARG),
+    (dict(pos=None), ARG), (dict(pos=A16 + 2), ARG), (dict(axis_stride=-1), ARG), (dict(pos_stride=-1), ARG), (dict(A=0), ARG),
+    (dict(A=5), ARG), (dict(axes=A16 + 1), ARG), (dict(freqs=None), ARG), (dict(freqs=A16 + 4), ARG), (dict(B=0), ARG),
+    (dict(Hq=0), ARG), (dict(Hkv=0), ARG), (dict(N=0), ARG), (dict(r=0), ARG), (dict(r=63), ARG), (dict(r=66), ARG),
+    (dict(scale=float("nan")), ARG), (dict(d=60, r=32), UNSUP), (dict(d=520), UNSUP), (dict(q_out=A16 + 2 * MB), ARG),
+    (dict(k_out=A16 + MB), ARG),
+    (dict(strides=(ctypes.c_longlong * 12)(2048, 1024, 64, 2048, 1024, 60, *(2048, 1024, 64) * 2)), ARG),
+])
+def test_rope_axes_refusals(kw, code):
+    assert _axes(**kw) == code
+
+
+KP, VP = A16 + 16 * MB, A16 + 64 * MB
+
+
+def _append(**kw):
+    a = dict(q=A16, q_out=A16 + MB, k=A16 + 2 * MB, v=A16 + 3 * MB, kp=KP, vp=VP, table=A16 + 4 * MB, lens=A16, pos=None,
+             axis_stride=0, pos_stride=0, A=1, new=None, out=A16 + 64, freqs=A16, axes=None, B=3, Hq=2, Hkv=2, T=1, d=64, r=64,
+             inter=0, scale=1.0, pages=20, page=16, per=4, strides=None)
+    a.update(kw)
+    return attn.attn_rope_axes_append(*a.values(), stream=0)
+
+
+PAGED = [
+    (dict(page=24), ARG), (dict(page=8), ARG), (dict(page=1 << 17), ARG), (dict(page=0), ARG), (dict(per=0), ARG),
+    (dict(pages=0), ARG), (dict(per=1 << 27), ARG), (dict(pages=1 << 30), ARG), (dict(B=0), ARG),
+    (dict(table=A16 + 4 * MB + 2), ARG), (dict(table=None), ARG), (dict(table=None, pages=3), ARG), (dict(table=None, per=1), ARG),
+]
+
+
+@pytest.mark.parametrize("kw,code", PAGED + [
+    (dict(q=None), ARG), (dict(k=A16 + 8), ARG), (dict(v=None), ARG), (dict(kp=None), ARG), (dict(vp=KP), ARG),
+    (dict(vp=VP + 4), ARG), (dict(k=KP), ARG), (dict(v=VP), ARG), (dict(q_out=KP + 16 * 64 * 2 * 2 * 19), ARG),
+    (dict(lens=None), ARG), (dict(lens=A16 + 1), ARG), (dict(out=A16), ARG), (dict(out=A16 + 8), ARG),
+    (dict(out=A16 + 4 * MB + 16), ARG), (dict(new=A16 + 72), ARG), (dict(pos=A16 + 2), ARG), (dict(A=5), ARG), (dict(A=0), ARG),
+    (dict(T=0), ARG), (dict(r=64, freqs=None), ARG), (dict(d=12), UNSUP), (dict(scale=-float("inf")), ARG),
+])
+def test_append_refusals(kw, code):
+    assert _append(**kw) == code
+
+
+def test_sections():
+    assert attn.rope_sections((2, 3), device="cpu").tolist() == [0, 0, 1, 1, 1]
+    assert attn.rope_sections((2, 3, 1), cycled=True, device="cpu").tolist() == [0, 1, 2, 0, 1, 1]
+    for bad in ((), (1,) * 5, (0, 0), (3, -1)):
+        with pytest.raises(attn.AttnError):
+            attn.rope_sections(bad, device="cpu")
+
+
+def test_helpers_refuse_cpu_tensors():
+    x = torch.zeros((1, 2, 3, 64), dtype=torch.bfloat16)
+    f, lens = torch.ones(32, dtype=torch.float64), torch.zeros(1, dtype=torch.int32)
+    for call in (lambda: attn.rope_axes(x, x, f, None, torch.zeros(3, dtype=torch.int32)),
+                 lambda: attn.rope_axes_append(x, x, x, x, x, lens, f)):
+        with pytest.raises(attn.AttnError) as e:
+            call()
+        assert e.value.code == ARG
