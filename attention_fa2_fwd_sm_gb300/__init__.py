@@ -75,6 +75,13 @@ SIGNATURES = {
     "attn_decode_prefix_segment": (_I, [_I] * 6 + [_LL] + [_I] * 3 + [_IP]),
     "attn_cache_evict": (_I, [_P] * 11 + [_I] * 7 + [_P, _SZ, _P]),
     "attn_cache_evict_workspace_bytes": (_SZ, [_I] * 5),
+    "attn_tree_mask": (_I, [_P] * 5 + [_I, _I, _P]),
+    "attn_tree_accept": (_I, [_P] * 7 + [_I] * 8 + [_P]),
+    "attn_pages_extend": (_I, [_P] * 4 + [_I] + [_P] * 3 + [_I] * 7 + [_P, _SZ, _P]),
+    "attn_pages_fork": (_I, [_P] * 6 + [_I] * 4 + [_P]),
+    "attn_pages_trim": (_I, [_P] * 5 + [_I] * 4 + [_P]),
+    "attn_pages_compact": (_I, [_P] * 5 + [_I] * 7 + [_P, _SZ, _P]),
+    "attn_pages_workspace_bytes": (_SZ, [_I, _I]),
     "attn_tile_map": (_I, [_I, _I, _I, _I, _I, _I, _LL, _IP, _IP, _IP]),
     "attn_tile_map_die_split": (_I, [_I, _I, _I, _I, _I, _I, _LL, _IP, _IP, _IP]),
     "attn_bwd_tile_map": (_I, [_I, _I, _I, _I, _I, _I, _LL, _IP, _IP, _IP]),
@@ -410,6 +417,48 @@ def attn_cache_evict(kcache, vcache, weights, cache_pos, seqlens, cur_pos, kout,
 
 def attn_cache_evict_workspace_bytes(B, Hkv, max_seqlen, keep, in_place) -> int:
     return lib().attn_cache_evict_workspace_bytes(B, Hkv, max_seqlen, keep, int(bool(in_place)))
+
+
+def attn_tree_mask(parents, seqlens, draft_lens, mask, positions, B, T, stream=None) -> int:
+    return lib().attn_tree_mask(_ptr(parents), _ptr(seqlens), _ptr(draft_lens), _ptr(mask), _ptr(positions), B, T,
+                                _stream(stream))
+
+
+def attn_tree_accept(kpages, vpages, page_table, seqlens, mask, last, seqlens_out, layers, B, Hkv, T, d, num_pages,
+                     page_size, max_pages, stream=None) -> int:
+    return lib().attn_tree_accept(_ptr(kpages), _ptr(vpages), _ptr(page_table), _ptr(seqlens), _ptr(mask), _ptr(last),
+                                  _ptr(seqlens_out), layers, B, Hkv, T, d, num_pages, page_size, max_pages,
+                                  _stream(stream))
+
+
+def attn_pages_extend(page_table, refs, seqlens, new_lens, T, kpages, vpages, info, layers, B, Hkv, d, num_pages,
+                      page_size, max_pages, workspace, workspace_bytes, stream=None) -> int:
+    return lib().attn_pages_extend(_ptr(page_table), _ptr(refs), _ptr(seqlens), _ptr(new_lens), T, _ptr(kpages),
+                                   _ptr(vpages), _ptr(info), layers, B, Hkv, d, num_pages, page_size, max_pages,
+                                   _ptr(workspace), workspace_bytes, _stream(stream))
+
+
+def attn_pages_fork(page_table, page_table_out, refs, seqlens, seqlens_out, parent, B, num_pages, page_size, max_pages,
+                    stream=None) -> int:
+    return lib().attn_pages_fork(_ptr(page_table), _ptr(page_table_out), _ptr(refs), _ptr(seqlens), _ptr(seqlens_out),
+                                 _ptr(parent), B, num_pages, page_size, max_pages, _stream(stream))
+
+
+def attn_pages_trim(page_table, refs, seqlens, seqlens_out, keep_lens, B, num_pages, page_size, max_pages,
+                    stream=None) -> int:
+    return lib().attn_pages_trim(_ptr(page_table), _ptr(refs), _ptr(seqlens), _ptr(seqlens_out), _ptr(keep_lens), B,
+                                 num_pages, page_size, max_pages, _stream(stream))
+
+
+def attn_pages_compact(page_table, refs, kpages, vpages, info, layers, B, Hkv, d, num_pages, page_size, max_pages,
+                       workspace, workspace_bytes, stream=None) -> int:
+    return lib().attn_pages_compact(_ptr(page_table), _ptr(refs), _ptr(kpages), _ptr(vpages), _ptr(info), layers, B,
+                                    Hkv, d, num_pages, page_size, max_pages, _ptr(workspace), workspace_bytes,
+                                    _stream(stream))
+
+
+def attn_pages_workspace_bytes(B, num_pages) -> int:
+    return lib().attn_pages_workspace_bytes(B, num_pages)
 
 
 def attn_rope_freqs(rotary_dim, base=10000.0, rule=0, factor=1.0, low=1.0, high=4.0, trained_len=8192.0):
@@ -891,6 +940,229 @@ def cache_evict(kcache, vcache, weights, seqlens, keep, recent=0, cache_pos=None
     if rc:
         check(rc, "attn_cache_evict")
     return seqlens_out, workspace
+
+
+def tree_mask(parents, seqlens=None, draft_lens=None, with_positions=True, stream=None):
+    """What each node of the drafted trees ``[B, T]`` int32 `parents` sees, by
+    attn_tree_mask; returns ``(mask, positions)``: int64 ``[B, T, ceil(T / 64)]`` for
+    `decode_tree` and `tree_accept`, and int32 ``[B, T]`` (`seqlens` plus the node's
+    depth) for `rope_axes_append`, or None."""
+    import torch
+    what, i32 = "tree_mask", torch.int32
+    gpu = parents.get_device()
+    if stream is not None or gpu < 0 or gpu != torch._C._cuda_getDevice():
+        with _elsewhere(what, gpu, stream):
+            got = tree_mask(parents, seqlens, draft_lens, with_positions)
+        _lend(stream, parents, seqlens, draft_lens)
+        return got
+    if parents.dim() != 2:
+        raise AttnError(ATTN_ERR_ARG, "tree_mask: parents has to be [B, T]")
+    B, T = shape = parents.shape
+    _fits(parents, i32, shape, gpu) or _refuse(what, "parents", parents, i32, shape)
+    seqlens is None or _fits(seqlens, i32, (B,), gpu) or _refuse(what, "seqlens", seqlens, i32, (B,))
+    draft_lens is None or _fits(draft_lens, i32, (B,), gpu) or _refuse(what, "draft_lens", draft_lens, i32, (B,))
+    mask = torch.empty((B, T, (T + 63) // 64), dtype=torch.int64, device=parents.device)
+    positions = torch.empty_like(parents) if with_positions else None
+    rc = lib().attn_tree_mask(parents.data_ptr(), None if seqlens is None else seqlens.data_ptr(),
+                              None if draft_lens is None else draft_lens.data_ptr(), mask.data_ptr(),
+                              None if positions is None else positions.data_ptr(), B, T,
+                              torch._C._cuda_getCurrentRawStream(gpu))
+    if rc:
+        check(rc, "attn_tree_mask")
+    return mask, positions
+
+
+def _layers(what, kcache, vcache, gpu):
+    """(layers, pages, Hkv, page size, d) of pools with or without a leading dimension of layers."""
+    import torch
+    if kcache.dim() not in (4, 5):
+        raise AttnError(ATTN_ERR_ARG, f"{what}: the caches have to be [pages, Hkv, page_size, d], with the layers before it or not")
+    shape = kcache.shape
+    _fits(kcache, torch.bfloat16, shape, gpu) or _refuse(what, "kcache", kcache, torch.bfloat16, shape)
+    _fits(vcache, torch.bfloat16, shape, gpu) or _refuse(what, "vcache", vcache, torch.bfloat16, shape)
+    return shape if len(shape) == 5 else (1, *shape)
+
+
+def tree_accept(kcache, vcache, seqlens, mask, last, page_table=None, seqlens_out=None, stream=None):
+    """Move the rows of the accepted path, which ends at node `last` ``[B]``
+    int32 (-1: nothing is accepted), behind the cached keys by attn_tree_accept;
+    returns the new lengths.  Caches ``[B, Hkv, slots, d]`` or, with `page_table`, pages
+    ``[pages, Hkv, page_size, d]``, either with a leading dimension of layers.  `mask`
+    as from `tree_mask`, or None: a chain, which has no rows to move."""
+    import torch
+    what, i32 = "tree_accept", torch.int32
+    gpu = kcache.get_device()
+    if stream is not None or gpu < 0 or gpu != torch._C._cuda_getDevice():
+        with _elsewhere(what, gpu, stream):
+            got = tree_accept(kcache, vcache, seqlens, mask, last, page_table, seqlens_out)
+        _lend(stream, kcache, vcache, seqlens, mask, last, page_table, seqlens_out)
+        return got
+    layers, pages, Hkv, page, d = _layers(what, kcache, vcache, gpu)
+    if seqlens is None or seqlens.dim() != 1:
+        raise AttnError(ATTN_ERR_ARG, "tree_accept: seqlens has to be [B]")
+    B, per, T = seqlens.shape[0], 1, 256
+    if page_table is not None:
+        per = page_table.shape[-1]
+        _fits(page_table, i32, (B, per), gpu) or _refuse(what, "page_table", page_table, i32, (B, per))
+    _fits(seqlens, i32, (B,), gpu) or _refuse(what, "seqlens", seqlens, i32, (B,))
+    _fits(last, i32, (B,), gpu) or _refuse(what, "last", last, i32, (B,))
+    if mask is not None:
+        T = mask.shape[1] if mask.dim() == 3 else 0
+        shape = (B, T, (T + 63) // 64)
+        _fits(mask, torch.int64, shape, gpu) or _refuse(what, "mask", mask, torch.int64, shape)
+    if seqlens_out is None:
+        seqlens_out = torch.empty_like(seqlens)
+    else:
+        _fits(seqlens_out, i32, (B,), gpu) or _refuse(what, "seqlens_out", seqlens_out, i32, (B,))
+    rc = lib().attn_tree_accept(kcache.data_ptr(), vcache.data_ptr(), None if page_table is None else page_table.data_ptr(),
+                                seqlens.data_ptr(), None if mask is None else mask.data_ptr(), last.data_ptr(),
+                                seqlens_out.data_ptr(), layers, B, Hkv, T, d, pages, page, per,
+                                torch._C._cuda_getCurrentRawStream(gpu))
+    if rc:
+        check(rc, "attn_tree_accept")
+    return seqlens_out
+
+
+def _tables(what, page_table, refs, gpu):
+    import torch
+    i32 = torch.int32
+    if page_table.dim() != 2 or refs is None or refs.dim() != 1:
+        raise AttnError(ATTN_ERR_ARG, f"{what}: page_table has to be [B, max_pages], refs [pages]")
+    _fits(page_table, i32, page_table.shape, gpu) or _refuse(what, "page_table", page_table, i32, page_table.shape)
+    _fits(refs, i32, refs.shape, gpu) or _refuse(what, "refs", refs, i32, refs.shape)
+    return (*page_table.shape, refs.shape[0])
+
+
+def _pages_workspace(what, workspace, B, pages, device, gpu):
+    import torch
+    if workspace is not None:
+        return workspace, _held(what, workspace, gpu)
+    nbytes = attn_pages_workspace_bytes(B, pages)
+    return torch.empty(max(nbytes, 16), dtype=torch.uint8, device=device), nbytes
+
+
+def pages_extend(page_table, refs, seqlens, new, kpages, vpages, workspace=None, info=None, stream=None):
+    """Give every sequence pages of its own for `new` more keys (a number, or
+    ``[B]`` int32) behind `seqlens`, by attn_pages_extend: missing ones are taken,
+    shared ones copied.  Pools ``[pages, Hkv, page_size, d]``, with a leading dimension
+    of layers or not; `page_table` ``[B, max_pages]`` and `refs` ``[pages]`` int32 are
+    updated.  Returns ``(info, workspace)``: int32 ``[2]``, pages taken and pages
+    missing (then nothing has been changed)."""
+    import torch
+    what, i32 = "pages_extend", torch.int32
+    gpu = page_table.get_device()
+    if stream is not None or gpu < 0 or gpu != torch._C._cuda_getDevice():
+        with _elsewhere(what, gpu, stream):
+            got = pages_extend(page_table, refs, seqlens, new, kpages, vpages, workspace, info)
+        _lend(stream, page_table, refs, seqlens, new if torch.is_tensor(new) else None, kpages, vpages, workspace, info)
+        return got
+    B, per, pages = _tables(what, page_table, refs, gpu)
+    layers, n, Hkv, page, d = _layers(what, kpages, vpages, gpu)
+    if n != pages:
+        raise AttnError(ATTN_ERR_ARG, f"pages_extend: {n} pages and {pages} counts")
+    _fits(seqlens, i32, (B,), gpu) or _refuse(what, "seqlens", seqlens, i32, (B,))
+    each = None
+    if torch.is_tensor(new):
+        each, new = new, 0
+        _fits(each, i32, (B,), gpu) or _refuse(what, "new", each, i32, (B,))
+    if info is None:
+        info = torch.empty(2, dtype=i32, device=page_table.device)
+    else:
+        _fits(info, i32, (2,), gpu) or _refuse(what, "info", info, i32, (2,))
+    workspace, nbytes = _pages_workspace(what, workspace, B, pages, page_table.device, gpu)
+    rc = lib().attn_pages_extend(page_table.data_ptr(), refs.data_ptr(), seqlens.data_ptr(),
+                                 None if each is None else each.data_ptr(), new, kpages.data_ptr(), vpages.data_ptr(),
+                                 info.data_ptr(), layers, B, Hkv, d, pages, page, per, workspace.data_ptr(), nbytes,
+                                 torch._C._cuda_getCurrentRawStream(gpu))
+    if rc:
+        check(rc, "attn_pages_extend")
+    return info, workspace
+
+
+def pages_fork(page_table, refs, seqlens, parent, page_size, page_table_out=None, seqlens_out=None, stream=None):
+    """Let every sequence go on as sequence `parent` ``[B]`` int32 (-1: it
+    ends), sharing its pages, by attn_pages_fork; `refs` is updated.  Returns
+    ``(page_table_out, seqlens_out)``, which replace the old ones."""
+    import torch
+    what, i32 = "pages_fork", torch.int32
+    gpu = page_table.get_device()
+    if stream is not None or gpu < 0 or gpu != torch._C._cuda_getDevice():
+        with _elsewhere(what, gpu, stream):
+            got = pages_fork(page_table, refs, seqlens, parent, page_size, page_table_out, seqlens_out)
+        _lend(stream, page_table, refs, seqlens, parent, page_table_out, seqlens_out)
+        return got
+    B, per, pages = _tables(what, page_table, refs, gpu)
+    _fits(seqlens, i32, (B,), gpu) or _refuse(what, "seqlens", seqlens, i32, (B,))
+    _fits(parent, i32, (B,), gpu) or _refuse(what, "parent", parent, i32, (B,))
+    if page_table_out is None:
+        page_table_out = torch.empty_like(page_table)
+    else:
+        _fits(page_table_out, i32, (B, per), gpu) or _refuse(what, "page_table_out", page_table_out, i32, (B, per))
+    if seqlens_out is None:
+        seqlens_out = torch.empty_like(seqlens)
+    else:
+        _fits(seqlens_out, i32, (B,), gpu) or _refuse(what, "seqlens_out", seqlens_out, i32, (B,))
+    rc = lib().attn_pages_fork(page_table.data_ptr(), page_table_out.data_ptr(), refs.data_ptr(), seqlens.data_ptr(),
+                               seqlens_out.data_ptr(), parent.data_ptr(), B, pages, page_size, per,
+                               torch._C._cuda_getCurrentRawStream(gpu))
+    if rc:
+        check(rc, "attn_pages_fork")
+    return page_table_out, seqlens_out
+
+
+def pages_trim(page_table, refs, seqlens, keep, page_size, seqlens_out=None, stream=None):
+    """Free the pages behind the first `keep` ``[B]`` int32 keys of every
+    sequence by attn_pages_trim; `page_table` and `refs` are updated.  Returns the new
+    lengths (`seqlens_out` may be `seqlens`)."""
+    import torch
+    what, i32 = "pages_trim", torch.int32
+    gpu = page_table.get_device()
+    if stream is not None or gpu < 0 or gpu != torch._C._cuda_getDevice():
+        with _elsewhere(what, gpu, stream):
+            got = pages_trim(page_table, refs, seqlens, keep, page_size, seqlens_out)
+        _lend(stream, page_table, refs, seqlens, keep, seqlens_out)
+        return got
+    B, per, pages = _tables(what, page_table, refs, gpu)
+    _fits(seqlens, i32, (B,), gpu) or _refuse(what, "seqlens", seqlens, i32, (B,))
+    _fits(keep, i32, (B,), gpu) or _refuse(what, "keep", keep, i32, (B,))
+    if seqlens_out is None:
+        seqlens_out = torch.empty_like(seqlens)
+    else:
+        _fits(seqlens_out, i32, (B,), gpu) or _refuse(what, "seqlens_out", seqlens_out, i32, (B,))
+    rc = lib().attn_pages_trim(page_table.data_ptr(), refs.data_ptr(), seqlens.data_ptr(), seqlens_out.data_ptr(),
+                               keep.data_ptr(), B, pages, page_size, per, torch._C._cuda_getCurrentRawStream(gpu))
+    if rc:
+        check(rc, "attn_pages_trim")
+    return seqlens_out
+
+
+def pages_compact(page_table, refs, kpages, vpages, workspace=None, info=None, stream=None):
+    """Move the pages in use to the front of the pool by attn_pages_compact;
+    pools, `page_table` and `refs` as in `pages_extend`, all updated.  Returns
+    ``(info, workspace)``: int32 ``[2]``, pages in use and pages moved."""
+    import torch
+    what, i32 = "pages_compact", torch.int32
+    gpu = page_table.get_device()
+    if stream is not None or gpu < 0 or gpu != torch._C._cuda_getDevice():
+        with _elsewhere(what, gpu, stream):
+            got = pages_compact(page_table, refs, kpages, vpages, workspace, info)
+        _lend(stream, page_table, refs, kpages, vpages, workspace, info)
+        return got
+    B, per, pages = _tables(what, page_table, refs, gpu)
+    layers, n, Hkv, page, d = _layers(what, kpages, vpages, gpu)
+    if n != pages:
+        raise AttnError(ATTN_ERR_ARG, f"pages_compact: {n} pages and {pages} counts")
+    if info is None:
+        info = torch.empty(2, dtype=i32, device=page_table.device)
+    else:
+        _fits(info, i32, (2,), gpu) or _refuse(what, "info", info, i32, (2,))
+    workspace, nbytes = _pages_workspace(what, workspace, B, pages, page_table.device, gpu)
+    rc = lib().attn_pages_compact(page_table.data_ptr(), refs.data_ptr(), kpages.data_ptr(), vpages.data_ptr(),
+                                  info.data_ptr(), layers, B, Hkv, d, pages, page, per, workspace.data_ptr(), nbytes,
+                                  torch._C._cuda_getCurrentRawStream(gpu))
+    if rc:
+        check(rc, "attn_pages_compact")
+    return info, workspace
 
 
 def forward(q, k, v, causal=False, scale=None, tile_order=ORDER_HEAD_FIRST, with_lse=True,

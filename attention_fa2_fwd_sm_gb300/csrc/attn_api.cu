@@ -1127,6 +1127,214 @@ int attn_cache_evict(const void *kcache, const void *vcache, const float *weight
     return evict_launch(a, reinterpret_cast<cudaStream_t>(stream));
 }
 
+// Trees of drafted tokens.
+static bool aligned8(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 7u) == 0; }
+constexpr int kMaxDraft = 256;
+
+int attn_tree_mask(const int *parents, const int *seqlens, const int *draft_lens, long long *mask, int *positions, int B,
+                   int T, attn_stream_t stream) {
+    if (B <= 0 || T <= 0 || T > kMaxDraft || !parents || !mask || !aligned8(mask)) return ATTN_ERR_ARG;
+    if (!aligned4(parents) || !aligned4(seqlens) || !aligned4(draft_lens) || !aligned4(positions)) return ATTN_ERR_ARG;
+    const size_t nodes = size_t(B) * T * 4, lens = size_t(B) * 4, bits = size_t(B) * T * ((T + 63) / 64) * 8;
+    const struct {
+        const void *p;
+        size_t n;
+    } ins[] = {{parents, nodes}, {seqlens, lens}, {draft_lens, lens}};
+    for (const auto &in : ins)
+        if (bytes_overlap(mask, bits, in.p, in.n) || bytes_overlap(positions, nodes, in.p, in.n)) return ATTN_ERR_ARG;
+    if (bytes_overlap(mask, bits, positions, nodes)) return ATTN_ERR_ARG;
+    TreeLaunch a;
+    a.parents = parents;
+    a.seqlens = seqlens;
+    a.draft_lens = draft_lens;
+    a.mask_out = reinterpret_cast<unsigned long long *>(mask);
+    a.positions = positions;
+    a.B = B;
+    a.T = T;
+    return tree_mask_launch(a, reinterpret_cast<cudaStream_t>(stream));
+}
+
+// Pools of all layers [layers, num_pages, Hkv, page_size, d].
+static int pools(const void *k, const void *v, int layers, int Hkv, int d, int num_pages, int page_size, size_t *bytes) {
+    if (layers <= 0 || Hkv <= 0) return ATTN_ERR_ARG;
+    if (d <= 0 || d % 8 || d > 512) return ATTN_ERR_UNSUPPORTED;
+    if (!aligned16(k) || !aligned16(v)) return ATTN_ERR_ARG;
+    if ((double)layers * num_pages * Hkv * ((double)page_size * d) >= 4.0e18) return ATTN_ERR_ARG;
+    if ((long long)layers * 2 * Hkv * (d / 8) > 0x3fffffffLL) return ATTN_ERR_ARG;  // counted in 32 bits
+    *bytes = (size_t)layers * num_pages * Hkv * page_size * d * 2;
+    return bytes_overlap(k, *bytes, v, *bytes) ? ATTN_ERR_ARG : ATTN_OK;
+}
+
+int attn_tree_accept(void *kpages, void *vpages, const int *page_table, const int *seqlens, const long long *mask,
+                     const int *last, int *seqlens_out, int layers, int B, int Hkv, int T, int d, int num_pages,
+                     int page_size, int max_pages, attn_stream_t stream) {
+    int rc = paged_sizes(page_table, B, Hkv, num_pages, page_size, max_pages);
+    if (rc != ATTN_OK) return rc;
+    size_t bytes = 0;
+    rc = pools(kpages, vpages, layers, Hkv, d, num_pages, page_size, &bytes);
+    if (rc != ATTN_OK) return rc;
+    if (T <= 0 || T > kMaxDraft || !seqlens || !last) return ATTN_ERR_ARG;
+    if (!aligned4(seqlens) || !aligned4(last) || !aligned4(seqlens_out) || !aligned8(mask)) return ATTN_ERR_ARG;
+    const size_t lens = size_t(B) * 4;
+    const struct {
+        const void *p;
+        size_t n;
+    } ins[] = {{seqlens, lens}, {last, lens}, {mask, size_t(B) * T * ((T + 63) / 64) * 8}, {page_table, lens * max_pages}};
+    for (const auto &in : ins)
+        for (void *out : {kpages, vpages, (void *)seqlens_out})
+            if (bytes_overlap(out, out == seqlens_out ? lens : bytes, in.p, in.n)) return ATTN_ERR_ARG;
+    if (bytes_overlap(seqlens_out, lens, kpages, bytes) || bytes_overlap(seqlens_out, lens, vpages, bytes)) return ATTN_ERR_ARG;
+    TreeLaunch a;
+    a.kpages = kpages;
+    a.vpages = vpages;
+    a.table = page_table;
+    a.seqlens = seqlens;
+    a.mask = reinterpret_cast<const unsigned long long *>(mask);
+    a.last = last;
+    a.lens_out = seqlens_out;
+    a.layers = layers;
+    a.B = B;
+    a.Hkv = Hkv;
+    a.T = T;
+    a.d = d;
+    a.num_pages = num_pages;
+    a.page_size = page_size;
+    a.page_shift = page_shift_of(page_table, page_size);
+    a.max_pages = max_pages;
+    return tree_accept_launch(a, reinterpret_cast<cudaStream_t>(stream));
+}
+
+// The pages of a cache.
+static int tables(const int *page_table, const int *refs, int B, int num_pages, int page_size, int max_pages) {
+    if (!page_table || !refs || !aligned4(refs)) return ATTN_ERR_ARG;
+    const int rc = paged_sizes(page_table, B, 1, num_pages, page_size, max_pages);
+    if (rc != ATTN_OK) return rc;
+    return (long long)B * max_pages > (1 << 30) || num_pages > (1 << 30) ? ATTN_ERR_ARG : ATTN_OK;
+}
+
+// Whether any two of the arrays share a byte (null ones do not).
+struct Span {
+    const void *p;
+    size_t n;
+};
+static bool any_overlap(const Span *s, int n) {
+    for (int i = 0; i < n; ++i)
+        for (int j = 0; j < i; ++j)
+            if (bytes_overlap(s[i].p, s[i].n, s[j].p, s[j].n)) return true;
+    return false;
+}
+
+size_t attn_pages_workspace_bytes(int B, int num_pages) {
+    return B <= 0 || num_pages <= 0 || B > (1 << 30) || num_pages > (1 << 30) ? 0 : pages_workspace_bytes(B, num_pages);
+}
+
+static int pages_moves(PagesLaunch *a, int *page_table, int *refs, void *kpages, void *vpages, int *info, int layers, int B,
+                       int Hkv, int d, int num_pages, int page_size, int max_pages, const int *seqlens,
+                       const int *new_lens, void *workspace, size_t workspace_bytes) {
+    int rc = tables(page_table, refs, B, num_pages, page_size, max_pages);
+    if (rc == ATTN_OK) rc = paged_sizes(page_table, B, Hkv, num_pages, page_size, max_pages);
+    if (rc != ATTN_OK) return rc;
+    size_t bytes = 0;
+    rc = pools(kpages, vpages, layers, Hkv, d, num_pages, page_size, &bytes);
+    if (rc != ATTN_OK) return rc;
+    if (!info || !aligned4(info) || !aligned4(seqlens) || !aligned4(new_lens)) return ATTN_ERR_ARG;
+    const size_t need = pages_workspace_bytes(B, num_pages), lens = size_t(B) * 4;
+    if (!workspace || !aligned16(workspace) || workspace_bytes < need) return ATTN_ERR_WORKSPACE;
+    const Span arrays[] = {{page_table, lens * max_pages}, {refs, size_t(num_pages) * 4}, {info, 8}, {seqlens, lens},
+                           {kpages, bytes}, {vpages, bytes}, {workspace, need}};
+    if (any_overlap(arrays, int(sizeof(arrays) / sizeof(Span)))) return ATTN_ERR_ARG;
+    for (const Span &s : arrays)  // (the two lengths are only read)
+        if (s.p != seqlens && bytes_overlap(new_lens, lens, s.p, s.n)) return ATTN_ERR_ARG;
+    a->table = page_table;
+    a->refs = refs;
+    a->seqlens = seqlens;
+    a->new_lens = new_lens;
+    a->kpages = kpages;
+    a->vpages = vpages;
+    a->info = info;
+    a->layers = layers;
+    a->B = B;
+    a->Hkv = Hkv;
+    a->d = d;
+    a->num_pages = num_pages;
+    a->page_size = page_size;
+    a->max_pages = max_pages;
+    a->workspace = static_cast<char *>(workspace);
+    a->num_sms = current_num_sms();
+    return a->num_sms <= 0 ? note_cuda_error(cudaErrorNoDevice, "device query") : ATTN_OK;
+}
+
+int attn_pages_extend(int *page_table, int *refs, const int *seqlens, const int *new_lens, int T, void *kpages,
+                      void *vpages, int *info, int layers, int B, int Hkv, int d, int num_pages, int page_size,
+                      int max_pages, void *workspace, size_t workspace_bytes, attn_stream_t stream) {
+    if (!seqlens || T < 0) return ATTN_ERR_ARG;
+    PagesLaunch a;
+    const int rc = pages_moves(&a, page_table, refs, kpages, vpages, info, layers, B, Hkv, d, num_pages, page_size,
+                               max_pages, seqlens, new_lens, workspace, workspace_bytes);
+    if (rc != ATTN_OK) return rc;
+    a.T = T;
+    return pages_extend_launch(a, reinterpret_cast<cudaStream_t>(stream));
+}
+
+int attn_pages_compact(int *page_table, int *refs, void *kpages, void *vpages, int *info, int layers, int B, int Hkv,
+                       int d, int num_pages, int page_size, int max_pages, void *workspace, size_t workspace_bytes,
+                       attn_stream_t stream) {
+    PagesLaunch a;
+    const int rc = pages_moves(&a, page_table, refs, kpages, vpages, info, layers, B, Hkv, d, num_pages, page_size,
+                               max_pages, nullptr, nullptr, workspace, workspace_bytes);
+    if (rc != ATTN_OK) return rc;
+    return pages_compact_launch(a, reinterpret_cast<cudaStream_t>(stream));
+}
+
+int attn_pages_fork(const int *page_table, int *page_table_out, int *refs, const int *seqlens, int *seqlens_out,
+                    const int *parent, int B, int num_pages, int page_size, int max_pages, attn_stream_t stream) {
+    const int rc = tables(page_table, refs, B, num_pages, page_size, max_pages);
+    if (rc != ATTN_OK) return rc;
+    if (!page_table_out || !seqlens || !seqlens_out || !parent) return ATTN_ERR_ARG;
+    for (const int *ptr : {(const int *)page_table_out, seqlens, (const int *)seqlens_out, parent})
+        if (!aligned4(ptr)) return ATTN_ERR_ARG;
+    const size_t lens = size_t(B) * 4;
+    const Span arrays[] = {{page_table, lens * max_pages}, {page_table_out, lens * max_pages}, {refs, size_t(num_pages) * 4},
+                           {seqlens, lens}, {seqlens_out, lens}, {parent, lens}};
+    if (any_overlap(arrays, int(sizeof(arrays) / sizeof(Span)))) return ATTN_ERR_ARG;
+    PagesLaunch a;
+    a.table = const_cast<int *>(page_table);
+    a.table_out = page_table_out;
+    a.refs = refs;
+    a.seqlens = seqlens;
+    a.lens_out = seqlens_out;
+    a.parent = parent;
+    a.B = B;
+    a.num_pages = num_pages;
+    a.page_size = page_size;
+    a.max_pages = max_pages;
+    return pages_fork_launch(a, reinterpret_cast<cudaStream_t>(stream));
+}
+
+int attn_pages_trim(int *page_table, int *refs, const int *seqlens, int *seqlens_out, const int *keep_lens, int B,
+                    int num_pages, int page_size, int max_pages, attn_stream_t stream) {
+    const int rc = tables(page_table, refs, B, num_pages, page_size, max_pages);
+    if (rc != ATTN_OK) return rc;
+    if (!seqlens || !keep_lens || !aligned4(seqlens) || !aligned4(seqlens_out) || !aligned4(keep_lens)) return ATTN_ERR_ARG;
+    const size_t lens = size_t(B) * 4;
+    const Span arrays[] = {{page_table, lens * max_pages}, {refs, size_t(num_pages) * 4},
+                           {seqlens_out == seqlens ? nullptr : seqlens, lens}, {seqlens_out, lens}};
+    if (any_overlap(arrays, int(sizeof(arrays) / sizeof(Span)))) return ATTN_ERR_ARG;
+    for (const Span &s : {arrays[0], arrays[1], arrays[3]})
+        if (bytes_overlap(keep_lens, lens, s.p, s.n)) return ATTN_ERR_ARG;
+    PagesLaunch a;
+    a.table = page_table;
+    a.refs = refs;
+    a.seqlens = seqlens;
+    a.lens_out = seqlens_out;
+    a.new_lens = keep_lens;
+    a.B = B;
+    a.num_pages = num_pages;
+    a.page_size = page_size;
+    a.max_pages = max_pages;
+    return pages_trim_launch(a, reinterpret_cast<cudaStream_t>(stream));
+}
+
 int attn_device_status(attn_stream_t stream) {
     if (cudaStreamSynchronize(reinterpret_cast<cudaStream_t>(stream)) != cudaSuccess)
         return ATTN_ERR_CUDA;

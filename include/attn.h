@@ -663,6 +663,109 @@ int attn_cache_evict(const void *kcache, const void *vcache, const float *weight
  * max_seqlen - keep <= 64).  Pure host code. */
 size_t attn_cache_evict_workspace_bytes(int B, int Hkv, int max_seqlen, int keep, int in_place);
 
+/*
+ * What each node of a tree of drafted tokens sees: itself and the nodes on its
+ * way to the root.
+ *   parents    [B, T] int32: the node's parent, a node before it; any other
+ *              value (-1) makes it a root, whose parent is the last cached key
+ *   seqlens    [B] int32 position of a root, or NULL: 0
+ *   draft_lens [B] int32 nodes of each tree (clamped to [0, T]), or NULL: all T
+ *   mask       [B, T, W] int64 (written), W = ceil(T / 64): bit u % 64 of word u / 64
+ *              of row t says that node t sees node u; nodes past draft_lens see
+ *              nothing and are seen by none.  8-byte aligned.
+ *   positions  [B, T] int32 (written), or NULL: a root's position plus the node's
+ *              depth, which attn_rope_axes_append takes
+ *   1 <= T <= 256.  One kernel on `stream`.
+ */
+int attn_tree_mask(const int *parents, const int *seqlens, const int *draft_lens, long long *mask, int *positions, int B,
+                   int T, attn_stream_t stream);
+
+/*
+ * The accepted path of a drafted tree becomes part of the cache: the rows of
+ * the nodes that mask[b, last[b]] names, behind row seqlens[b] as
+ * attn_rope_axes_append stored them, are moved to rows seqlens[b], seqlens[b] + 1,
+ * ... in the nodes' order, for every KV head and layer.
+ *   kpages, vpages  [layers, num_pages, Hkv, page_size, d] bf16; page_table as for
+ *              one layer (the same for all), or NULL: contiguous caches
+ *   seqlens    [B] int32 keys cached before the draft, clamped to the capacity
+ *   mask       [B, T, W] int64 as attn_tree_mask writes it (bits from T on count
+ *              as 0), or NULL: a chain, whose rows are in their places
+ *   last       [B] int32: the last accepted node; a value outside [0, T): none
+ *   seqlens_out [B] int32, min(seqlens[b] + accepted nodes, capacity), or NULL; must
+ *              not overlap seqlens or last
+ *   d a multiple of 8, at most 512; 1 <= T <= 256.
+ * Rows behind the accepted ones keep what they hold.  A row that lies on no page is
+ * not moved, and nothing is moved to one.  One kernel on `stream`.
+ */
+int attn_tree_accept(void *kpages, void *vpages, const int *page_table, const int *seqlens, const long long *mask,
+                     const int *last, int *seqlens_out, int layers, int B, int Hkv, int T, int d, int num_pages,
+                     int page_size, int max_pages, attn_stream_t stream);
+
+/*
+ * The pages of a cache.  One page_table [B, max_pages] int32 and one array refs
+ * [num_pages] int32, the number of table entries that hold each page (0: free),
+ * serve all layers; both belong to the caller, who starts with entries of -1 and
+ * counts of 0.  Everything is decided on the device, without host synchronisation,
+ * and does not depend on any order of execution.  B * max_pages and num_pages are
+ * at most 2^30; page_size a power of two from 16 to 65536, max_pages * page_size at most
+ * 2^30.  None of a call's int32 arrays may overlap another, unless said.
+ *
+ * attn_pages_extend: room for new keys.  For every sequence, the slots that rows
+ * [seqlens[b], seqlens[b] + new) reach (cut at the capacity) get a page of their
+ * own: where the entry is no page, and where the page is shared with others, in
+ * which case the keys in use in it are copied (K and V, all heads and layers).  Where
+ * all holders of a shared page are among the writers, the one of the highest b
+ * keeps it.  Pages are taken lowest first, in the order of the sequences and slots.
+ *   new_lens   [B] int32 new keys of each (below 0: 0), or NULL: T for all
+ *   kpages, vpages  [layers, num_pages, Hkv, page_size, d] bf16, d a multiple of 8, at most 512
+ *   info       [2] int32 (written): pages taken, pages missing.  If pages are
+ *              missing, nothing else is changed.
+ *   workspace  attn_pages_workspace_bytes(B, num_pages) bytes, 16-byte aligned
+ * Two kernels on `stream`.
+ */
+int attn_pages_extend(int *page_table, int *refs, const int *seqlens, const int *new_lens, int T, void *kpages,
+                      void *vpages, int *info, int layers, int B, int Hkv, int d, int num_pages, int page_size,
+                      int max_pages, void *workspace, size_t workspace_bytes, attn_stream_t stream);
+
+/*
+ * attn_pages_fork: every sequence b goes on as parent[b] (a beam search's step; a
+ * prompt's samples; parent[b] = b: as itself; outside [0, B): it ends, and its
+ * pages are freed as far as nobody else holds them).  Pages are shared, not copied.
+ * A sequence that stays itself keeps all of its entries; another one's get the
+ * entries that parent's keys reach, the rest becomes -1.
+ *   page_table_out  [B, max_pages] int32 (written), seqlens_out [B] int32
+ *              (written): the parent's length, 0 for none; not the inputs
+ *   refs       updated
+ * One kernel on `stream`.
+ */
+int attn_pages_fork(const int *page_table, int *page_table_out, int *refs, const int *seqlens, int *seqlens_out,
+                    const int *parent, int B, int num_pages, int page_size, int max_pages, attn_stream_t stream);
+
+/*
+ * attn_pages_trim: frees the pages behind the first keep_lens[b] keys (clamped to
+ * [0, capacity]) of every sequence; 0 frees all of them.
+ *   seqlens_out [B] int32, min(seqlens[b], keep_lens[b]), or NULL; may be seqlens
+ * One kernel on `stream`.
+ */
+int attn_pages_trim(int *page_table, int *refs, const int *seqlens, int *seqlens_out, const int *keep_lens, int B,
+                    int num_pages, int page_size, int max_pages, attn_stream_t stream);
+
+/*
+ * attn_pages_compact: moves the n pages in use to the first n of the pool.  Used
+ * pages below n stay; the i-th free one below n receives the i-th used one from n on,
+ * in all layers; tables and counts follow.  The pages from n on keep what they
+ * held, and are free.
+ *   info       [2] int32 (written): n, pages moved
+ * Other arguments as attn_pages_extend.  Two kernels on `stream`.
+ */
+int attn_pages_compact(int *page_table, int *refs, void *kpages, void *vpages, int *info, int layers, int B, int Hkv,
+                       int d, int num_pages, int page_size, int max_pages, void *workspace, size_t workspace_bytes,
+                       attn_stream_t stream);
+
+/* Workspace bytes of attn_pages_extend and attn_pages_compact (0 for bad
+ * sizes).  Pure host code. */
+size_t attn_pages_workspace_bytes(int B, int num_pages);
+
 /* Host-side view of the forward scheduler: unit `unit` of the order maps to
  * (*b, *h, *m) where m is the index of a 256-row block.  Pure host code; the
  * same function runs inside the kernel.  Orders 0-2 only (the die-split order

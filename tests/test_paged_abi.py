@@ -85,3 +85,114 @@ def test_helpers_refuse_cpu_tensors():
         with pytest.raises(attn.AttnError) as e:
             call()
         assert e.value.code == ARG
+
+
+def _mask(**kw):
+    a = dict(parents=A16, lens=A16 + MB, live=None, mask=A16 + 2 * MB, pos=A16 + 3 * MB, B=3, T=70)
+    a.update(kw)
+    return attn.attn_tree_mask(*a.values(), stream=0)
+
+
+@pytest.mark.parametrize("kw", [
+    dict(parents=None), dict(parents=A16 + 2), dict(lens=A16 + 1), dict(live=A16 + 3), dict(mask=None), dict(mask=A16 + 4),
+    dict(pos=A16 + 2), dict(B=0), dict(T=0), dict(T=257), dict(mask=A16), dict(pos=A16 + 3 * 70 * 4 - 4), dict(pos=A16 + MB),
+    dict(mask=A16 + MB), dict(pos=A16 + 2 * MB + 3 * 70 * 16 - 4), dict(live=A16 + 2 * MB),
+])
+def test_mask_refusals(kw):
+    assert _mask(**kw) == ARG
+
+
+def _accept(**kw):
+    a = dict(kp=KP, vp=VP, table=A16 + 4 * MB, lens=A16, mask=A16 + MB, last=A16 + 2 * MB, out=A16 + 3 * MB, layers=2, B=3,
+             Hkv=2, T=70, d=64, pages=20, page=16, per=4)
+    a.update(kw)
+    return attn.attn_tree_accept(*a.values(), stream=0)
+
+
+@pytest.mark.parametrize("kw,code", PAGED + [
+    (dict(kp=None), ARG), (dict(vp=None), ARG), (dict(kp=KP + 8), ARG), (dict(vp=KP + 2 * 20 * 2 * 16 * 64 * 2 - 16), ARG),
+    (dict(lens=None), ARG), (dict(last=None), ARG), (dict(lens=A16 + 2), ARG), (dict(last=A16 + 1), ARG), (dict(out=A16 + 3), ARG),
+    (dict(mask=A16 + 4), ARG), (dict(T=0), ARG), (dict(T=257), ARG), (dict(layers=0), ARG), (dict(d=60), UNSUP), (dict(d=520), UNSUP),
+    (dict(out=A16), ARG), (dict(out=A16 + 2 * MB + 8), ARG), (dict(out=A16 + MB), ARG), (dict(out=A16 + 4 * MB), ARG), (dict(out=KP), ARG),
+    (dict(lens=KP), ARG), (dict(last=VP + 64), ARG), (dict(mask=KP), ARG), (dict(layers=1 << 27, pages=1, B=1, per=1), ARG),
+])
+def test_accept_refusals(kw, code):
+    assert _accept(**kw) == code
+
+
+def _extend(**kw):
+    a = dict(table=A16, refs=A16 + MB, lens=A16 + 2 * MB, new=None, T=1, kp=KP, vp=VP, info=A16 + 3 * MB, layers=2, B=3, Hkv=2,
+             d=64, pages=20, page=16, per=4, ws=A16 + 4 * MB, bytes=1 << 20)
+    a.update(kw)
+    return attn.attn_pages_extend(*a.values(), stream=0)
+
+
+def _compact(**kw):
+    a = dict(table=A16, refs=A16 + MB, kp=KP, vp=VP, info=A16 + 3 * MB, layers=2, B=3, Hkv=2, d=64, pages=20, page=16, per=4,
+             ws=A16 + 4 * MB, bytes=1 << 20)
+    a.update(kw)
+    return attn.attn_pages_compact(*a.values(), stream=0)
+
+
+def _fork(**kw):
+    a = dict(table=A16, out=A16 + MB, refs=A16 + 2 * MB, lens=A16 + 3 * MB, lens_out=A16 + 4 * MB, parent=A16 + 5 * MB, B=3,
+             pages=20, page=16, per=4)
+    a.update(kw)
+    return attn.attn_pages_fork(*a.values(), stream=0)
+
+
+def _trim(**kw):
+    a = dict(table=A16, refs=A16 + MB, lens=A16 + 2 * MB, lens_out=A16 + 3 * MB, keep=A16 + 4 * MB, B=3, pages=20, page=16, per=4)
+    a.update(kw)
+    return attn.attn_pages_trim(*a.values(), stream=0)
+
+
+SIZES = [(kw, code) for kw, code in PAGED if "table" not in kw]
+
+
+@pytest.mark.parametrize("call", [_extend, _compact, _fork, _trim])
+@pytest.mark.parametrize("kw,code", SIZES + [(dict(table=None), ARG), (dict(table=A16 + 2), ARG), (dict(refs=None), ARG),
+                                             (dict(refs=A16 + 1), ARG), (dict(refs=A16 + 44), ARG)])
+def test_pages_sizes_and_tables(call, kw, code):
+    assert call(**kw) == code
+
+
+@pytest.mark.parametrize("call", [_extend, _compact])
+@pytest.mark.parametrize("kw,code", [
+    (dict(kp=None), ARG), (dict(vp=VP + 8), ARG), (dict(vp=KP), ARG), (dict(info=None), ARG), (dict(info=A16 + 2), ARG),
+    (dict(info=A16 + MB), ARG), (dict(info=A16 + 47), ARG), (dict(layers=0), ARG), (dict(Hkv=0), ARG), (dict(d=60), UNSUP),
+    (dict(d=520), UNSUP), (dict(ws=None), WS), (dict(ws=A16 + 4 * MB + 8), WS), (dict(bytes=16), WS), (dict(ws=A16), ARG),
+    (dict(ws=KP), ARG), (dict(table=KP), ARG), (dict(refs=VP), ARG),
+])
+def test_pages_move_refusals(call, kw, code):
+    assert call(**kw) == code
+
+
+@pytest.mark.parametrize("call,kw", [
+    (_extend, dict(lens=None)), (_extend, dict(lens=A16 + 2)), (_extend, dict(new=A16 + 1)), (_extend, dict(T=-1)),
+    (_extend, dict(lens=A16)), (_extend, dict(new=A16 + MB)), (_extend, dict(new=KP)),
+    (_fork, dict(out=None)), (_fork, dict(out=A16)), (_fork, dict(out=A16 + 44)), (_fork, dict(lens=None)),
+    (_fork, dict(lens_out=None)), (_fork, dict(lens_out=A16 + 3 * MB)), (_fork, dict(parent=None)), (_fork, dict(parent=A16 + 2)),
+    (_fork, dict(parent=A16 + 2 * MB)), (_fork, dict(lens=A16 + 3)),
+    (_trim, dict(lens=None)), (_trim, dict(keep=None)), (_trim, dict(keep=A16)), (_trim, dict(lens_out=A16 + 4 * MB)),
+    (_trim, dict(lens_out=A16 + MB)), (_trim, dict(keep=A16 + 4 * MB + 2)),
+])
+def test_pages_other_refusals(call, kw):
+    assert call(**kw) == ARG
+
+
+def test_pages_workspace():
+    f = attn.attn_pages_workspace_bytes
+    assert f(0, 5) == f(5, 0) == f(-1, 5) == f(1, (1 << 30) + 1) == 0
+    assert f(1, 1) >= 16 and f(64, 1000) >= 4 * 4 * 1000 + 20 * 64
+
+
+def test_page_helpers_refuse_cpu_tensors():
+    t, r, n = torch.zeros((2, 3), dtype=torch.int32), torch.zeros(5, dtype=torch.int32), torch.zeros(2, dtype=torch.int32)
+    k = torch.zeros((5, 1, 16, 8), dtype=torch.bfloat16)
+    for call in (lambda: attn.tree_mask(t), lambda: attn.tree_accept(k, k, n, None, n, page_table=t),
+                 lambda: attn.pages_extend(t, r, n, 1, k, k), lambda: attn.pages_fork(t, r, n, n, 16),
+                 lambda: attn.pages_trim(t, r, n, n, 16), lambda: attn.pages_compact(t, r, k, k)):
+        with pytest.raises(attn.AttnError) as e:
+            call()
+        assert e.value.code == ARG
