@@ -76,6 +76,8 @@ SIGNATURES = {
     "attn_cache_evict": (_I, [_P] * 11 + [_I] * 7 + [_P, _SZ, _P]),
     "attn_cache_evict_workspace_bytes": (_SZ, [_I] * 5),
     "attn_tree_mask": (_I, [_P] * 5 + [_I, _I, _P]),
+    "attn_decode_tree": (_I, [_P] * 9 + [_I] * 5 + [_F] + [_I] * 3 + [_P, _SZ, _P]),
+    "attn_decode_tree_workspace_bytes": (_SZ, [_I] * 7),
     "attn_tree_accept": (_I, [_P] * 7 + [_I] * 8 + [_P]),
     "attn_pages_extend": (_I, [_P] * 4 + [_I] + [_P] * 3 + [_I] * 7 + [_P, _SZ, _P]),
     "attn_pages_fork": (_I, [_P] * 6 + [_I] * 4 + [_P]),
@@ -422,6 +424,17 @@ def attn_cache_evict_workspace_bytes(B, Hkv, max_seqlen, keep, in_place) -> int:
 def attn_tree_mask(parents, seqlens, draft_lens, mask, positions, B, T, stream=None) -> int:
     return lib().attn_tree_mask(_ptr(parents), _ptr(seqlens), _ptr(draft_lens), _ptr(mask), _ptr(positions), B, T,
                                 _stream(stream))
+
+
+def attn_decode_tree(q, kpages, vpages, page_table, seqlens, mask, draft_lens, o, lse, B, Hq, Hkv, T, d, scale,
+                     num_pages, page_size, max_pages, workspace, workspace_bytes, stream=None) -> int:
+    return lib().attn_decode_tree(_ptr(q), _ptr(kpages), _ptr(vpages), _ptr(page_table), _ptr(seqlens), _ptr(mask),
+                                  _ptr(draft_lens), _ptr(o), _ptr(lse), B, Hq, Hkv, T, d, scale, num_pages, page_size,
+                                  max_pages, _ptr(workspace), workspace_bytes, _stream(stream))
+
+
+def attn_decode_tree_workspace_bytes(B, Hq, Hkv, T, d, page_size, max_pages) -> int:
+    return lib().attn_decode_tree_workspace_bytes(B, Hq, Hkv, T, d, page_size, max_pages)
 
 
 def attn_tree_accept(kpages, vpages, page_table, seqlens, mask, last, seqlens_out, layers, B, Hkv, T, d, num_pages,
@@ -970,6 +983,54 @@ def tree_mask(parents, seqlens=None, draft_lens=None, with_positions=True, strea
     if rc:
         check(rc, "attn_tree_mask")
     return mask, positions
+
+
+def decode_tree(q, kcache, vcache, seqlens, mask=None, draft_lens=None, page_table=None, scale=None, workspace=None,
+                with_lse=True, stream=None):
+    """Attention of the drafted tokens q ``[B, Hq, T, d]`` over the `seqlens`
+    cached keys and the drafted ones behind them, by attn_decode_tree: contiguous
+    caches ``[B, Hkv, slots, d]`` or, with `page_table` ``[B, max_pages]`` int32, pages
+    ``[pages, Hkv, page_size, d]``.  `mask` as from `tree_mask` (None: a chain).
+    Allocates the outputs, and a workspace when none is given
+    (attn_decode_tree_workspace_bytes says how large one has to be); returns ``(o, lse,
+    workspace)``."""
+    import torch
+    what, i32 = "decode_tree", torch.int32
+    gpu = q.get_device()
+    if stream is not None or gpu < 0 or gpu != torch._C._cuda_getDevice():
+        with _elsewhere(what, gpu, stream):
+            got = decode_tree(q, kcache, vcache, seqlens, mask, draft_lens, page_table, scale, workspace, with_lse)
+        _lend(stream, q, kcache, vcache, seqlens, mask, draft_lens, page_table, workspace)
+        return got
+    if q.dim() != 4:
+        raise AttnError(ATTN_ERR_ARG, "decode_tree: q has to be [B, Hq, T, d]")
+    B, Hq, T, d = shape = q.shape
+    Hkv, cols, pages, page, per = _paged(what, kcache, vcache, page_table, B, gpu)
+    if cols != d:
+        raise AttnError(ATTN_ERR_ARG, f"decode_tree: heads of {d} columns and caches of {cols}")
+    _fits(q, torch.bfloat16, shape, gpu) or _refuse(what, "q", q, torch.bfloat16, shape)
+    _fits(seqlens, i32, (B,), gpu) or _refuse(what, "seqlens", seqlens, i32, (B,))
+    draft_lens is None or _fits(draft_lens, i32, (B,), gpu) or _refuse(what, "draft_lens", draft_lens, i32, (B,))
+    if mask is not None:
+        bits = (B, T, (T + 63) // 64)
+        _fits(mask, torch.int64, bits, gpu) or _refuse(what, "mask", mask, torch.int64, bits)
+    if workspace is None:
+        nbytes = attn_decode_tree_workspace_bytes(B, Hq, Hkv, T, d, page, per)
+        workspace = torch.empty(max(nbytes, 16), dtype=torch.uint8, device=q.device)
+    else:
+        nbytes = _held(what, workspace, gpu)
+    o = torch.empty_like(q)
+    lse = torch.empty((B, Hq, T), dtype=torch.float32, device=q.device) if with_lse else None
+    rc = lib().attn_decode_tree(q.data_ptr(), kcache.data_ptr(), vcache.data_ptr(),
+                                None if page_table is None else page_table.data_ptr(), seqlens.data_ptr(),
+                                None if mask is None else mask.data_ptr(),
+                                None if draft_lens is None else draft_lens.data_ptr(), o.data_ptr(),
+                                lse.data_ptr() if with_lse else None, B, Hq, Hkv, T, d,
+                                d ** -0.5 if scale is None else scale, pages, page, per, workspace.data_ptr(), nbytes,
+                                torch._C._cuda_getCurrentRawStream(gpu))
+    if rc:
+        check(rc, "attn_decode_tree")
+    return o, lse, workspace
 
 
 def _layers(what, kcache, vcache, gpu):

@@ -1127,6 +1127,18 @@ int attn_cache_evict(const void *kcache, const void *vcache, const float *weight
     return evict_launch(a, reinterpret_cast<cudaStream_t>(stream));
 }
 
+// Whether any two of the arrays share a byte (null ones do not).
+struct Span {
+    const void *p;
+    size_t n;
+};
+static bool any_overlap(const Span *s, int n) {
+    for (int i = 0; i < n; ++i)
+        for (int j = 0; j < i; ++j)
+            if (bytes_overlap(s[i].p, s[i].n, s[j].p, s[j].n)) return true;
+    return false;
+}
+
 // Trees of drafted tokens.
 static bool aligned8(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 7u) == 0; }
 constexpr int kMaxDraft = 256;
@@ -1152,6 +1164,73 @@ int attn_tree_mask(const int *parents, const int *seqlens, const int *draft_lens
     a.B = B;
     a.T = T;
     return tree_mask_launch(a, reinterpret_cast<cudaStream_t>(stream));
+}
+
+static int decode_tree_sizes(int B, int Hq, int Hkv, int T, int d, int page_size, int max_pages) {
+    if (B <= 0 || Hq <= 0 || Hkv <= 0 || T <= 0 || Hq % Hkv || page_size <= 0 || max_pages <= 0) return ATTN_ERR_ARG;
+    if (d != 64 && d != 128) return ATTN_ERR_UNSUPPORTED;
+    if (Hq / Hkv > kDecodeMaxGroup || T > kMaxDraft) return ATTN_ERR_UNSUPPORTED;
+    const long long cap = (long long)page_size * max_pages;
+    if (cap > (1 << 30) || (long long)B * Hkv > 0x7fffffffLL) return ATTN_ERR_ARG;
+    return (double)B * Hkv * (double)((cap + 127) / 128) < 2147483648.0 ? ATTN_OK : ATTN_ERR_ARG;
+}
+
+size_t attn_decode_tree_workspace_bytes(int B, int Hq, int Hkv, int T, int d, int page_size, int max_pages) {
+    if (decode_tree_sizes(B, Hq, Hkv, T, d, page_size, max_pages) != ATTN_OK) return 0;
+    const int sms = current_num_sms();
+    return sms <= 0 ? 0 : decode_tree_workspace_bytes(B, Hq / Hkv, Hkv, T, d, (long long)page_size * max_pages, sms);
+}
+
+int attn_decode_tree(const void *q, const void *kpages, const void *vpages, const int *page_table, const int *seqlens,
+                     const long long *mask, const int *draft_lens, void *o, float *lse, int B, int Hq, int Hkv, int T,
+                     int d, float scale, int num_pages, int page_size, int max_pages, void *workspace,
+                     size_t workspace_bytes, attn_stream_t stream) {
+    int rc = decode_tree_sizes(B, Hq, Hkv, T, d, page_size, max_pages);
+    if (rc == ATTN_OK) rc = paged_sizes(page_table, B, Hkv, num_pages, page_size, max_pages);
+    if (rc != ATTN_OK) return rc;
+    if (!aligned16(q) || !aligned16(kpages) || !aligned16(vpages) || !aligned16(o) || !seqlens) return ATTN_ERR_ARG;
+    if (!aligned4(seqlens) || !aligned4(draft_lens) || !aligned4(lse) || !aligned8(mask)) return ATTN_ERR_ARG;
+    if (!(scale > 0.f) || !std::isfinite(scale)) return ATTN_ERR_ARG;
+    // tensor-map limits
+    if ((long long)page_size * d * 2 >= (1LL << 39) || (long long)(Hq / Hkv) * T * d * 2 >= (1LL << 39)) return ATTN_ERR_ARG;
+    if (!workspace || !aligned16(workspace)) return ATTN_ERR_WORKSPACE;
+    const int sms = current_num_sms();
+    if (sms <= 0) return note_cuda_error(cudaErrorNoDevice, "device query");
+    const size_t need = decode_tree_workspace_bytes(B, Hq / Hkv, Hkv, T, d, (long long)page_size * max_pages, sms);
+    if (workspace_bytes < need) return ATTN_ERR_WORKSPACE;
+    // An output may overlap no input, nor the workspace.
+    const size_t rows = size_t(B) * Hq * T, cache = size_t(num_pages) * Hkv * page_size * d * 2, lens = size_t(B) * 4;
+    const Span outs[] = {{o, rows * d * 2}, {lse, rows * 4}, {workspace, need}};
+    const Span ins[] = {{q, rows * d * 2}, {kpages, cache}, {vpages, cache}, {page_table, lens * max_pages}, {seqlens, lens},
+                        {draft_lens, lens}, {mask, size_t(B) * T * ((T + 63) / 64) * 8}};
+    if (any_overlap(outs, 3)) return ATTN_ERR_ARG;
+    for (const Span &x : outs)
+        for (const Span &y : ins)
+            if (bytes_overlap(x.p, x.n, y.p, y.n)) return ATTN_ERR_ARG;
+    DecodeTreeLaunch a;
+    a.q = q;
+    a.kpages = kpages;
+    a.vpages = vpages;
+    a.table = page_table;
+    a.seqlens = seqlens;
+    a.draft_lens = draft_lens;
+    a.mask = reinterpret_cast<const unsigned long long *>(mask);
+    a.o = o;
+    a.lse = lse;
+    a.B = B;
+    a.Hq = Hq;
+    a.Hkv = Hkv;
+    a.T = T;
+    a.d = d;
+    a.num_pages = num_pages;
+    a.page_size = page_size;
+    a.page_shift = page_shift_of(page_table, page_size);
+    a.max_pages = max_pages;
+    a.scale = scale;
+    a.workspace = static_cast<char *>(workspace);
+    a.wait_ns = (unsigned long long)g_wait_ns.load();
+    a.num_sms = sms;
+    return decode_tree_launch(a, reinterpret_cast<cudaStream_t>(stream));
 }
 
 // Pools of all layers [layers, num_pages, Hkv, page_size, d].
@@ -1210,18 +1289,6 @@ static int tables(const int *page_table, const int *refs, int B, int num_pages, 
     const int rc = paged_sizes(page_table, B, 1, num_pages, page_size, max_pages);
     if (rc != ATTN_OK) return rc;
     return (long long)B * max_pages > (1 << 30) || num_pages > (1 << 30) ? ATTN_ERR_ARG : ATTN_OK;
-}
-
-// Whether any two of the arrays share a byte (null ones do not).
-struct Span {
-    const void *p;
-    size_t n;
-};
-static bool any_overlap(const Span *s, int n) {
-    for (int i = 0; i < n; ++i)
-        for (int j = 0; j < i; ++j)
-            if (bytes_overlap(s[i].p, s[i].n, s[j].p, s[j].n)) return true;
-    return false;
 }
 
 size_t attn_pages_workspace_bytes(int B, int num_pages) {
@@ -1338,13 +1405,13 @@ int attn_pages_trim(int *page_table, int *refs, const int *seqlens, int *seqlens
 int attn_device_status(attn_stream_t stream) {
     if (cudaStreamSynchronize(reinterpret_cast<cudaStream_t>(stream)) != cudaSuccess)
         return ATTN_ERR_CUDA;
-    int a = 0, b = 0, c = 0, e = 0, f = 0, g = 0, h = 0;
+    int a = 0, b = 0, c = 0, e = 0, f = 0, g = 0, h = 0, i = 0;
     if (fwd_take_status(&a) != cudaSuccess || decode_take_status(&b) != cudaSuccess ||
         bwd_take_status(&c) != cudaSuccess || fwd_pair_take_status(&e) != cudaSuccess ||
         fwd_split_take_status(&f) != cudaSuccess || decode_prefix_take_status(&g) != cudaSuccess ||
-        own_take_status(&h) != cudaSuccess)
+        own_take_status(&h) != cudaSuccess || decode_tree_take_status(&i) != cudaSuccess)
         return ATTN_ERR_CUDA;
-    return (a | b | c | e | f | g | h) ? ATTN_ERR_TIMEOUT : ATTN_OK;
+    return (a | b | c | e | f | g | h | i) ? ATTN_ERR_TIMEOUT : ATTN_OK;
 }
 
 }  // extern "C"

@@ -199,6 +199,22 @@ struct TreeLaunch {
     const int *table = nullptr;
     int B, T, layers = 1, Hkv = 1, d = 8, num_pages = 0, page_size = 0, page_shift = 0, max_pages = 0;
 };
+// Attention of drafted tokens over a cache (decode_tree_sm103.cu).
+struct DecodeTreeLaunch {
+    const void *q, *kpages, *vpages;
+    const int *table, *seqlens, *draft_lens;  // table, draft_lens: may be null
+    const unsigned long long *mask;           // may be null: a chain
+    void *o;
+    float *lse;  // may be null
+    int B, Hq, Hkv, T, d, num_pages, page_size, page_shift, max_pages;
+    float scale;
+    char *workspace;
+    unsigned long long wait_ns;
+    int num_sms;
+};
+size_t decode_tree_workspace_bytes(int B, int G, int Hkv, int T, int d, long long cap, int num_sms);
+int decode_tree_launch(const DecodeTreeLaunch &a, cudaStream_t stream);
+cudaError_t decode_tree_take_status(int *bits);
 int tree_mask_launch(const TreeLaunch &a, cudaStream_t stream);
 int tree_accept_launch(const TreeLaunch &a, cudaStream_t stream);
 

@@ -681,6 +681,46 @@ int attn_tree_mask(const int *parents, const int *seqlens, const int *draft_lens
                    int T, attn_stream_t stream);
 
 /*
+ * Attention of T drafted tokens per sequence over a cache that holds their keys
+ * too: token t of sequence b attends the first seqlens[b] keys and, of the drafted
+ * tokens, whose keys are in the rows behind (attn_rope_axes_append put them
+ * there), those that its row of the mask names:
+ *     s_j = scale * <q, k_j>,  L = log(sum_j exp(s_j)),  o = sum_j exp(s_j - L) v_j,
+ *     lse = L over the keys that it attends.
+ * T = 1 is a decode step over pages.  The keys are read once for all T tokens and
+ * all query heads of a KV head.
+ *   q, o       [B, Hq, T, d] bf16, contiguous
+ *   kpages, vpages, page_table, num_pages, page_size, max_pages  a cache in pages,
+ *              or contiguous caches [B, Hkv, page_size, d] (page_table NULL), as
+ *              above.  The values of keys that a token does not attend do not
+ *              matter, whatever they are, nor do rows behind the last key.
+ *   seqlens    [B] int32 keys before the drafted ones, clamped to [0, capacity]
+ *   mask       [B, T, W] int64, W = ceil(T / 64), as attn_tree_mask writes it: bit u
+ *              of row t says that token t attends drafted token u (any pattern; bits
+ *              from draft_lens[b] on count as 0).  NULL: a chain, token t attends the
+ *              drafted tokens 0 .. t.  8-byte aligned.
+ *   draft_lens [B] int32 drafted tokens of each (clamped to [0, T]), or NULL: all T.
+ *              Rows past it get o = 0, lse = -inf.
+ *   lse        [B, Hq, T] fp32 (natural log), or NULL.  A token that attends no key
+ *              (or none whose score is above -inf) gets o = 0, lse = -inf.
+ *   Drafted tokens whose row is at or past the capacity have no key.
+ *   d in {64, 128}; 1 <= Hq / Hkv <= 16; 1 <= T <= 256; B * Hkv * ceil(capacity /
+ *   128) < 2^31.
+ *   workspace  at least attn_decode_tree_workspace_bytes(...) bytes, 16-byte
+ *              aligned.  Nothing in it outlives the call.
+ * Up to two kernels run on `stream`, with no host synchronisation.  No atomics:
+ * equal calls give equal bits.
+ */
+int attn_decode_tree(const void *q, const void *kpages, const void *vpages, const int *page_table, const int *seqlens,
+                     const long long *mask, const int *draft_lens, void *o, float *lse, int B, int Hq, int Hkv, int T,
+                     int d, float scale, int num_pages, int page_size, int max_pages, void *workspace,
+                     size_t workspace_bytes, attn_stream_t stream);
+
+/* Workspace bytes attn_decode_tree needs on the current device (0 for sizes that
+ * it refuses, or when the device cannot be queried). */
+size_t attn_decode_tree_workspace_bytes(int B, int Hq, int Hkv, int T, int d, int page_size, int max_pages);
+
+/*
  * The accepted path of a drafted tree becomes part of the cache: the rows of
  * the nodes that mask[b, last[b]] names, behind row seqlens[b] as
  * attn_rope_axes_append stored them, are moved to rows seqlens[b], seqlens[b] + 1,

@@ -196,3 +196,29 @@ def test_page_helpers_refuse_cpu_tensors():
         with pytest.raises(attn.AttnError) as e:
             call()
         assert e.value.code == ARG
+
+
+def _tree(**kw):
+    a = dict(q=A16, kp=KP, vp=VP, table=A16 + MB, lens=A16 + 2 * MB, mask=A16 + 3 * MB, live=None, o=A16 + 4 * MB, lse=A16 + 5 * MB,
+             B=3, Hq=4, Hkv=2, T=70, d=64, scale=0.1, pages=20, page=16, per=4, ws=A16 + 128 * MB, bytes=1 << 30)
+    a.update(kw)
+    return attn.attn_decode_tree(*a.values(), stream=0)
+
+
+@pytest.mark.parametrize("kw,code", [(kw, code) for kw, code in PAGED if kw != dict(table=A16 + 4 * MB + 2)] + [
+    (dict(q=None), ARG), (dict(q=A16 + 8), ARG), (dict(kp=None), ARG), (dict(vp=VP + 8), ARG), (dict(o=None), ARG),
+    (dict(o=A16 + 4), ARG), (dict(lens=None), ARG), (dict(lens=A16 + 1), ARG), (dict(mask=A16 + 4), ARG), (dict(live=A16 + 2), ARG),
+    (dict(lse=A16 + 2), ARG), (dict(scale=0.0), ARG), (dict(scale=float("inf")), ARG), (dict(scale=float("nan")), ARG),
+    (dict(Hq=5), ARG), (dict(Hq=34), UNSUP), (dict(T=0), ARG), (dict(T=257), UNSUP), (dict(d=56), UNSUP), (dict(d=256), UNSUP),
+    (dict(table=A16 + MB + 2), ARG), (dict(ws=None), WS), (dict(ws=A16 + 128 * MB + 8), WS),
+    (dict(B=1 << 20, Hkv=64, Hq=64, per=1 << 20), ARG),
+])
+def test_decode_tree_refusals(kw, code):
+    assert _tree(**kw) == code
+
+
+def test_decode_tree_workspace():
+    f = attn.attn_decode_tree_workspace_bytes
+    for bad in ((0, 4, 2, 1, 64, 16, 4), (1, 5, 2, 1, 64, 16, 4), (1, 4, 2, 0, 64, 16, 4), (1, 4, 2, 257, 64, 16, 4),
+                (1, 4, 2, 1, 56, 16, 4), (1, 4, 2, 1, 64, 0, 4), (1, 4, 2, 1, 64, 1 << 20, 1 << 20)):
+        assert f(*bad) == 0
