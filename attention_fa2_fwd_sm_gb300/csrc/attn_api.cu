@@ -1172,7 +1172,7 @@ static int decode_tree_sizes(int B, int Hq, int Hkv, int T, int d, int page_size
     if (Hq / Hkv > kDecodeMaxGroup || T > kMaxDraft) return ATTN_ERR_UNSUPPORTED;
     const long long cap = (long long)page_size * max_pages;
     if (cap > (1 << 30) || (long long)B * Hkv > 0x7fffffffLL) return ATTN_ERR_ARG;
-    return (double)B * Hkv * (double)((cap + 127) / 128) < 2147483648.0 ? ATTN_OK : ATTN_ERR_ARG;
+    return (double)B * Hkv * (double)((cap + 63) / 64) < 2147483648.0 ? ATTN_OK : ATTN_ERR_ARG;
 }
 
 size_t attn_decode_tree_workspace_bytes(int B, int Hq, int Hkv, int T, int d, int page_size, int max_pages) {

@@ -53,7 +53,7 @@ static __device__ int g_tree_status;
 
 namespace dtree {
 
-constexpr int kTileM = 128, kBlock = 128;  // rows of a tile, keys of a block
+constexpr int kTileM = 128;  // rows of a tile
 constexpr int kThreads = 384;
 // As in fwd_kernel.cuh: 384 threads x 168 registers at launch are shared out anew.
 constexpr int kLaunchRegs = 168, kCtrlRegs = 120, kSoftmaxRegs = 192;
@@ -63,12 +63,17 @@ constexpr int kTurnStride = 20, kTurnFloats = 32 * kTurnStride;
 constexpr int kMaskWords = 8;  // 32-bit words of a row's mask: 256 drafted tokens
 constexpr int kMergeWarps = 4;
 
+// Keys of a block.  Where the chains take turns, HBM is what they wait for, and small
+// blocks hold less of the ring while they are worked on.
+constexpr int block_keys(bool keys) { return keys ? 64 : 128; }
+
 template <int D, bool kKeys>
 struct Cfg {
-    static constexpr int kChunks = D / 64, kChunkBytes = 128 * 128;
+    static constexpr int kBlock = block_keys(kKeys);
+    static constexpr int kChunks = D / 64, kQChunkBytes = kTileM * 128, kChunkBytes = kBlock * 128;
     static constexpr int kQTiles = kKeys ? 1 : 2;
     static constexpr int kQBytes = kTileM * D * 2, kKVBytes = kBlock * D * 2;
-    static constexpr int kStages = (D == 128 ? 1 : 2) * (kKeys ? 5 : 4);
+    static constexpr int kStages = (D == 128 ? 1 : 2) * (kKeys ? 10 : 4);
     static constexpr int kOCol = 2 * kTileM;
     static constexpr int kDataBytes = kQTiles * kQBytes + kStages * kKVBytes;
     static constexpr int kTurnOffset = kDataBytes, kStateOffset = kTurnOffset + 8 * kTurnFloats * 4;
@@ -110,15 +115,19 @@ __device__ __forceinline__ void load_sequence(const Params &p, int b, int &len, 
 __device__ __forceinline__ int keys_of(const Params &p, int len, int tb) {
     return tb > 0 ? int(min((long long)len + tb, (long long)p.cap)) : 0;
 }
-__device__ __forceinline__ int blocks_of(int keys) { return (keys + kBlock - 1) / kBlock; }
+template <int kBlock>
+__device__ __forceinline__ int blocks_of(int keys) {
+    return (keys + kBlock - 1) / kBlock;
+}
 
 // Blocks of all pairs (all lanes of the calling warp).
+template <int kBlock>
 __device__ __forceinline__ long long all_blocks(const Params &p) {
     long long n = 0;
     for (int b = threadIdx.x & 31; b < p.B; b += 32) {
         int len, tb;
         load_sequence(p, b, len, tb);
-        n += blocks_of(keys_of(p, len, tb));
+        n += blocks_of<kBlock>(keys_of(p, len, tb));
     }
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) n += __shfl_xor_sync(0xffffffffu, n, off);
@@ -126,6 +135,7 @@ __device__ __forceinline__ long long all_blocks(const Params &p) {
 }
 
 // The pair of block x, and which of its blocks x is (j0); all lanes of the calling warp.
+template <int kBlock>
 __device__ __forceinline__ Unit find_block(const Params &p, long long x) {
     const int lane = threadIdx.x & 31;
     Unit u = {};
@@ -136,7 +146,7 @@ __device__ __forceinline__ Unit find_block(const Params &p, long long x) {
             load_sequence(p, first + lane, len, tb);
             keys = keys_of(p, len, tb);
         }
-        const long long n = (long long)blocks_of(keys) * p.Hkv;
+        const long long n = (long long)blocks_of<kBlock>(keys) * p.Hkv;
         long long upto = n;
 #pragma unroll
         for (int off = 1; off < 32; off <<= 1) {
@@ -151,7 +161,7 @@ __device__ __forceinline__ Unit find_block(const Params &p, long long x) {
             u.len = __shfl_sync(0xffffffffu, len, src);
             u.tb = __shfl_sync(0xffffffffu, tb, src);
             u.keys = __shfl_sync(0xffffffffu, keys, src);
-            u.nb = blocks_of(u.keys);
+            u.nb = blocks_of<kBlock>(u.keys);
             const unsigned rem = unsigned(x - __shfl_sync(0xffffffffu, base, src));
             u.g = int(rem / unsigned(u.nb));
             u.j0 = int(rem - unsigned(u.g) * unsigned(u.nb));
@@ -176,7 +186,7 @@ __device__ __forceinline__ uint32_t mask_bits(const uint32_t (&m)[kMaskWords], i
 
 // A row of V in shared memory (128 bytes of each chunk; the swizzle stays within them), of key `key`: zeros behind
 // the last key; in a drafted row, zeros for what is not finite, and whether there was any.
-template <int kChunks>
+template <int kChunks, int kBlock>
 __device__ __forceinline__ bool clean_row(uint8_t *v, int key, int len, int keys) {
     bool found = false;
     if (key >= len)
@@ -214,6 +224,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     tree_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                 const __grid_constant__ CUtensorMap tmV, const Params p) {
     using C = Cfg<D, kKeys>;
+    constexpr int kBlock = C::kBlock;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint8_t *sQ = smem, *sKV = smem + C::kQTiles * C::kQBytes;
@@ -263,11 +274,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         tmem_relinquish();
     }
     if (warp == 2 || warp == 3) {
-        const long long total = all_blocks(p), S = (total + p.shares - 1) / p.shares, lo = share * S;
+        const long long total = all_blocks<kBlock>(p), S = (total + p.shares - 1) / p.shares, lo = share * S;
         const int left = int(lo < total ? min(S, total - lo) : 0);
         if (warp == 2) {
             Unit u = {};
-            if (left > 0) u = find_block(p, lo);
+            if (left > 0) u = find_block<kBlock>(p, lo);
             if (lane == 0) {
                 start[0] = u.b;
                 start[1] = u.g;
@@ -279,7 +290,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             // whose waits run out leaves the merge wrong numbers but no wrong addresses.
             int4 cut = make_int4(0, 0, 0, 0);
             if (left > 0) {
-                const Unit u = find_block(p, lo + left - 1);
+                const Unit u = find_block<kBlock>(p, lo + left - 1);
                 const int rest = u.nb - u.j0 - 1;
                 if (u.j0 < left && rest > 0) cut = make_int4(u.b, u.g, 1 + int((rest + S - 1) / S), u.tb);
             }
@@ -295,7 +306,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kCtrlRegs));
         if (warp == 0) {
             // -------------------------------------------------------- producer
-            long long fills = 0;
+            uint32_t fills = 0;
             int q_loads = 0;  // per tile (both are loaded for every unit that has them)
             bool ok = true;
             Unit u = {};
@@ -306,7 +317,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (left > 0) {
                 load_sequence(p, u.b, u.len, u.tb);
                 u.keys = keys_of(p, u.len, u.tb);
-                u.nb = blocks_of(u.keys);
+                u.nb = blocks_of<kBlock>(u.keys);
             }
             const bool second = !kKeys && (2 * m + 1) * kTileM < p.rows;
             const int boxes = p.table && p.page_size < kBlock ? kBlock / p.page_size : 1;
@@ -337,7 +348,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (lane == 0) {
                         mbar_arrive_expect_tx(bar(C::kQFull + t), C::kQBytes);
                         for (int c = 0; c < C::kChunks; ++c)
-                            tma_load_3d(smem_u32(sQ + t * C::kQBytes + c * C::kChunkBytes), &tmQ, bar(C::kQFull + t), c * 64,
+                            tma_load_3d(smem_u32(sQ + t * C::kQBytes + c * C::kQChunkBytes), &tmQ, bar(C::kQFull + t), c * 64,
                                         (2 * m + t) * kTileM, u.b * p.Hkv + u.g);
                     }
                     __syncwarp();
@@ -365,10 +376,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                     const int plane = page >= 0 && page < p.num_pages ? page * p.Hkv + u.g : p.num_pages * p.Hkv;
                     for (int kv = 0; kv < 2; ++kv) {
-                        const int slot = int(fills % C::kStages);
-                        const long long round = fills / C::kStages;
+                        const uint32_t slot = fills % C::kStages, round = fills / C::kStages;
                         if (round > 0) {
-                            ok = mbar_wait_warp(bar(C::kKVEmpty + slot), uint32_t((round - 1) & 1), p.wait_ns, abort_flag, status);
+                            ok = mbar_wait_warp(bar(C::kKVEmpty + slot), (round - 1) & 1, p.wait_ns, abort_flag, status);
                             if (!ok) break;
                         }
                         const uint32_t fb = bar(C::kKVFull + slot);
@@ -390,7 +400,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         load_sequence(p, ++u.b, u.len, u.tb);
                         u.keys = keys_of(p, u.len, u.tb);
                     } while (u.keys == 0);
-                    u.nb = blocks_of(u.keys);
+                    u.nb = blocks_of<kBlock>(u.keys);
                 }
             }
             __syncwarp();
@@ -398,10 +408,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                 // The last copy into every slot has to land before the CTA goes (bounded).
                 const unsigned long long drain_ns = 1000000000ull;
                 volatile int no_abort = 0;
-                for (int s = 0; s < C::kStages; ++s) {
+                for (uint32_t s = 0; s < C::kStages; ++s) {
                     if (fills <= s) continue;
-                    const long long last = (fills - 1 - s) / C::kStages;  // round of the slot's last fill
-                    if (!mbar_wait_bounded(bar(C::kKVFull + s), uint32_t(last & 1), drain_ns, &no_abort, status))
+                    const uint32_t last = (fills - 1 - s) / C::kStages;  // round of the slot's last fill
+                    if (!mbar_wait_bounded(bar(C::kKVFull + s), last & 1, drain_ns, &no_abort, status))
                         atomicOr(status, kStatusDrainTimeout);
                 }
                 for (int t = 0; t < (second ? 2 : 1); ++t)
@@ -412,33 +422,32 @@ __global__ void __launch_bounds__(kThreads, 1)
         } else if (warp == 1) {
             // ------------------------------------------------------ MMA issuer
             constexpr uint32_t kIdescQK = idesc_bf16_f32(kTileM, kBlock, 0), kIdescPV = idesc_bf16_f32(kTileM, D, 1);
-            long long fills = 0;
-            int q_used = 0, p_waits[2] = {0, 0}, done[2] = {0, 0};
+            uint32_t fills = 0;
+            uint32_t q_used = 0;
+            uint32_t p_odd = 0, o_odd = 0, used = 0;  // a bit a chain: waits for P, units done, whether there was one
             bool ok = true;
             const int chains = kKeys || (2 * m + 1) * kTileM < p.rows ? 2 : 1;
-            auto wait_slot = [&](long long f) {
-                return mbar_wait_warp(bar(C::kKVFull + int(f % C::kStages)), uint32_t((f / C::kStages) & 1), p.wait_ns, abort_flag,
-                                      status);
+            auto wait_slot = [&](uint32_t f) {
+                return mbar_wait_warp(bar(C::kKVFull + f % C::kStages), (f / C::kStages) & 1, p.wait_ns, abort_flag, status);
             };
             const uint64_t dQ = smem_desc_sw128(smem_u32(sQ), 16, 1024);
             const uint64_t dK = smem_desc_sw128(smem_u32(sKV), 16, 1024);
             const uint64_t dV = smem_desc_sw128(smem_u32(sKV), C::kChunkBytes, 1024);
-            auto slot_off = [&](long long f) { return uint64_t(int(f % C::kStages) * (C::kKVBytes >> 4)); };
-            auto issue_qk = [&](int t, long long fK) {
+            auto slot_off = [&](uint32_t f) { return uint64_t(f % C::kStages * (C::kKVBytes >> 4)); };
+            auto issue_qk = [&](int t, uint32_t fK) {
                 const uint64_t a0 = dQ + uint64_t((kKeys ? 0 : t) * (C::kQBytes >> 4)), b0 = dK + slot_off(fK);
 #pragma unroll
                 for (int g = 0; g < D / 64; ++g) {
                     uint64_t a[4], b[4];
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
-                        const uint64_t off = uint64_t((g * C::kChunkBytes + i * 32) >> 4);
-                        a[i] = a0 + off;
-                        b[i] = b0 + off;
+                        a[i] = a0 + uint64_t((g * C::kQChunkBytes + i * 32) >> 4);
+                        b[i] = b0 + uint64_t((g * C::kChunkBytes + i * 32) >> 4);
                     }
                     tc_mma_ss_x4_elect(tmem_base + t * kTileM, a, b, kIdescQK, g > 0 ? 1u : 0u);
                 }
             };
-            auto issue_pv = [&](int t, long long fV, bool acc) {
+            auto issue_pv = [&](int t, uint32_t fV, bool acc) {
                 const uint64_t b0 = dV + slot_off(fV);
 #pragma unroll
                 for (int g = 0; g < kBlock / 64; ++g) {
@@ -461,7 +470,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int n = __shfl_sync(0xffffffffu, int(e[3]), 0);
                 mbar_arrive_elect(bar(C::kUEmpty + qs));
                 if (n == 0) break;
-                const long long f0 = fills;  // K_j at f0 + 2 j, V_j behind it
+                const uint32_t f0 = fills;  // K_j at f0 + 2 j, V_j behind it
                 // The first product of each chain.
                 for (int t = 0; ok && t < chains; ++t) {
                     const int j = kKeys ? t : 0;
@@ -475,15 +484,18 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 ++q_used;
                 for (int j = 0; ok && j < n; ++j) {
-                    const long long fV = f0 + 2 * j + 1;
+                    const uint32_t fV = f0 + 2 * j + 1;
                     bool v_ready = false;
-                    for (int t = kKeys ? j & 1 : 0; ok && t < (kKeys ? (j & 1) + 1 : chains); ++t) {
-                        ok = mbar_wait_warp(bar(C::kPFull + t), p_waits[t] & 1, p.wait_ns, abort_flag, status);
+#pragma unroll
+                    for (int i = 0; i < (kKeys ? 1 : 2); ++i) {
+                        const int t = kKeys ? j & 1 : i;
+                        if (!kKeys && i >= chains) break;
+                        ok = mbar_wait_warp(bar(C::kPFull + t), p_odd >> t & 1, p.wait_ns, abort_flag, status);
                         if (!ok) break;
-                        ++p_waits[t];
+                        p_odd ^= 1u << t;
                         const bool first = kKeys ? j < 2 : j == 0;
-                        if (first && done[t] > 0) {
-                            ok = mbar_wait_warp(bar(C::kOEmpty + t), (done[t] - 1) & 1, p.wait_ns, abort_flag, status);
+                        if (first && (used >> t & 1)) {
+                            ok = mbar_wait_warp(bar(C::kOEmpty + t), ~(o_odd >> t) & 1, p.wait_ns, abort_flag, status);
                             if (!ok) break;
                         }
                         if (!v_ready) {
@@ -493,7 +505,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         }
                         tc_fence_after();
                         issue_pv(t, fV, !first);
-                        if (kKeys || t == chains - 1) tc_commit_elect(bar(C::kKVEmpty + int(fV % C::kStages)));
+                        if (kKeys || t == chains - 1) tc_commit_elect(bar(C::kKVEmpty + fV % C::kStages));
                         const int next = j + (kKeys ? 2 : 1);
                         if (next < n) {
                             ok = wait_slot(f0 + 2 * next);
@@ -503,11 +515,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                         } else {
                             tc_commit_elect(bar(C::kOFull + t));
                             if (!kKeys || j == n - 1) tc_commit_elect(bar(C::kQEmpty + (kKeys ? 0 : t)));
-                            ++done[t];
+                            o_odd ^= 1u << t;
+                            used |= 1u << t;
                         }
                     }
                 }
-                fills = f0 + 2 * (long long)n;
+                fills = f0 + 2 * n;
             }
             tc_commit_elect(bar(C::kDrain));
             volatile int no_abort = 0;
@@ -542,8 +555,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int limit = p.rows - row0;  // rows of the tile in use, if below 128
         float *turn = reinterpret_cast<float *>(smem + C::kTurnOffset) + (warp - 4) * kTurnFloats;
         float2 *states = reinterpret_cast<float2 *>(smem + C::kStateOffset);  // [unit parity][chain][row]
-        int s_waits = 0, o_waits[2] = {0, 0};
-        long long kv_base = 0;
+        uint32_t s_waits = 0, o_waits = 0, o_waits1 = 0;
+        uint32_t kv_base = 0;
         bool ok = true;
         for (long long qi = 0; ok; ++qi) {
             const int qs = int(qi & 1);
@@ -555,8 +568,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             __syncwarp();
             mbar_arrive_elect(bar(C::kUEmpty + qs));
             if (u.n == 0) break;
-            const long long f0 = kv_base;
-            kv_base += 2 * (long long)u.n;
+            const uint32_t f0 = kv_base;
+            kv_base += 2 * u.n;
             if (!has_tile) continue;
             const bool live = row < p.rows && token < u.tb;
             // What the row sees of the drafted tokens.
@@ -584,7 +597,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int i = (((u.j0 + j) * kBlock) >> p.shift) + lane;
                 return table && lane < boxes && i < used && j < u.n ? table[i] : -1;
             };
-            constexpr int kStep = kKeys ? 2 : 1;
+            constexpr int kStep = kKeys ? 2 : 1, kQuads = kBlock / 32;
             const int jt = kKeys ? t : 0;
             int ahead = page_of(jt);
             float m_run = -INFINITY, l_run = 0.f;
@@ -599,23 +612,23 @@ __global__ void __launch_bounds__(kThreads, 1)
                 ++s_waits;
                 // S complete: so are all products before it, and K's slot is free once the last chain to use it says so.
                 if (quarter == 0 && (kKeys || t == (second ? 1 : 0)))
-                    mbar_arrive_elect(bar(C::kKVEmpty + int((f0 + 2 * j) % C::kStages)));
+                    mbar_arrive_elect(bar(C::kKVEmpty + (f0 + 2 * j) % C::kStages));
                 if (has_rows) {
                     tc_fence_after();
-                    uint32_t sr[4][32];
+                    uint32_t sr[kQuads][32];
 #pragma unroll
-                    for (int c = 0; c < 4; ++c) tmem_ld32(tS + c * 32, sr[c]);
+                    for (int c = 0; c < kQuads; ++c) tmem_ld32(tS + c * 32, sr[c]);
                     tmem_wait_ld();
-                    float s[128];
+                    float s[kBlock];
 #pragma unroll
-                    for (int c = 0; c < 4; ++c)
+                    for (int c = 0; c < kQuads; ++c)
 #pragma unroll
                         for (int i = 0; i < 32; ++i) s[c * 32 + i] = __uint_as_float(sr[c][i]);
                     const int kv0 = (u.j0 + j) * kBlock;
                     const uint32_t all = boxes >= 32 ? ~0u : (1u << boxes) - 1;
                     if (kv0 + kBlock > u.len || (table && (on_page & all) != all)) {
 #pragma unroll
-                        for (int c = 0; c < 4; ++c) {
+                        for (int c = 0; c < kQuads; ++c) {
                             uint32_t bits = mask_bits(seen, kv0 + 32 * c - u.len);
                             if (table) {
                                 const int per = 32 / (p.page_size < 32 ? p.page_size : 32);  // pages in 32 keys: 1 or 2
@@ -629,20 +642,21 @@ __global__ void __launch_bounds__(kThreads, 1)
                         }
                     }
                     auto block_max = [&]() {
-                        float mq[4];
+                        float mq[kQuads];
 #pragma unroll
-                        for (int c = 0; c < 4; ++c) {
+                        for (int c = 0; c < kQuads; ++c) {
                             float x = fmax3(s[32 * c], s[32 * c + 1], s[32 * c + 2]);
 #pragma unroll
                             for (int i = 3; i < 31; i += 2) x = fmax3(x, s[32 * c + i], s[32 * c + i + 1]);
                             mq[c] = fmaxf(x, s[32 * c + 31]);
                         }
-                        return fmax3(mq[0], mq[1], fmaxf(mq[2], mq[3]));
+                        if constexpr (kQuads == 2) return fmaxf(mq[0], mq[1]);
+                        else return fmax3(mq[0], mq[1], fmaxf(mq[2], mq[3]));
                     };
                     auto exp_block = [&](float neg_m) {
                         float ls[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-                        for (int c = 0; c < 4; ++c) {
+                        for (int c = 0; c < kQuads; ++c) {
                             uint32_t pk[16];
 #pragma unroll
                             for (int i = 0; i < 16; ++i) {
@@ -688,11 +702,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 if ((u.j0 + j + 1) * kBlock > u.len && (kKeys || t == 0)) {
                     // (the other chain's product of this block is issued behind this one's)
-                    const long long fV = f0 + 2 * j + 1;
-                    const int slot = int(fV % C::kStages);
-                    ok = mbar_wait_warp(bar(C::kKVFull + slot), uint32_t((fV / C::kStages) & 1), p.wait_ns, abort_flag, status);
+                    const uint32_t fV = f0 + 2 * j + 1, slot = fV % C::kStages;
+                    ok = mbar_wait_warp(bar(C::kKVFull + slot), (fV / C::kStages) & 1, p.wait_ns, abort_flag, status);
                     if (!ok) break;
-                    if (clean_row<C::kChunks>(sKV + slot * C::kKVBytes + r * 128, (u.j0 + j) * kBlock + r, u.len, u.keys)) {
+                    if (r < kBlock && clean_row<C::kChunks, kBlock>(sKV + slot * C::kKVBytes + r * 128, (u.j0 + j) * kBlock + r, u.len, u.keys)) {
                         const int x = (u.j0 + j) * kBlock + r - u.len;
                         atomicOr(odd_rows + (qi & 3) * kMaskWords + (x >> 5), 1u << (x & 31));
                     }
@@ -715,11 +728,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                 __syncwarp();
                 mbar_arrive_elect(bar(C::kStateFull));
                 ok = mbar_wait_warp(bar(C::kStateFull), uint32_t(qi & 1), p.wait_ns, abort_flag, status);
-                if (ok) ok = mbar_wait_warp(bar(C::kOFull), o_waits[0] & 1, p.wait_ns, abort_flag, status);
-                if (ok && has1) ok = mbar_wait_warp(bar(C::kOFull + 1), o_waits[1] & 1, p.wait_ns, abort_flag, status);
+                if (ok) ok = mbar_wait_warp(bar(C::kOFull), o_waits & 1, p.wait_ns, abort_flag, status);
+                if (ok && has1) ok = mbar_wait_warp(bar(C::kOFull + 1), o_waits1 & 1, p.wait_ns, abort_flag, status);
                 if (!ok) break;
-                ++o_waits[0];
-                if (has1) ++o_waits[1];
+                ++o_waits;
+                if (has1) ++o_waits1;
                 const float2 a = mine[r], c = mine[kTileM + r];
                 const float top = fmaxf(a.x, c.x), ref = top == -INFINITY ? 0.f : top;
                 f[0] = fast_exp2(a.x - ref);
@@ -729,11 +742,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                 f[0] /= sum;
                 f[1] /= sum;
             } else {
-                ok = mbar_wait_warp(bar(C::kOFull + t), o_waits[t] & 1, p.wait_ns, abort_flag, status);
+                ok = mbar_wait_warp(bar(C::kOFull + t), o_waits & 1, p.wait_ns, abort_flag, status);
                 if (!ok) break;
-                ++o_waits[t];
+                ++o_waits;
                 sum = l_run;
-                f[t] = 1.f / sum;
+                f[0] = 1.f / sum;
                 L = m_run + __log2f(sum);
             }
             tc_fence_after();
@@ -760,7 +773,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     tmem_ld32(tO + (kKeys ? 0 : t * D) + col, ov);
                     tmem_wait_ld();
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) x[i] = __uint_as_float(ov[i]) * f[kKeys ? 0 : t];
+                    for (int i = 0; i < 32; ++i) x[i] = __uint_as_float(ov[i]) * f[0];
                     if (has1) {
                         tmem_ld32(tO + D + col, ov);
                         tmem_wait_ld();
@@ -877,7 +890,8 @@ Layout layout_of(int B, int G, int Hkv, int T, int d, long long cap, int num_sms
     Layout l;
     const size_t rows = size_t(G) * T;
     l.mt = int((rows + 2 * kTileM - 1) / (2 * kTileM));
-    const long long most = (long long)B * Hkv * ((cap + kBlock - 1) / kBlock);
+    const int block = block_keys(rows <= kTileM);
+    const long long most = (long long)B * Hkv * ((cap + block - 1) / block);
     const int groups = num_sms / l.mt > 0 ? num_sms / l.mt : 1;
     l.shares = int(most < groups ? most : groups);
     auto up = [](size_t n) { return (n + 255) / 256 * 256; };
@@ -893,7 +907,7 @@ int launch(const DecodeTreeLaunch &a, const Layout &l, cudaStream_t stream) {
     using C = Cfg<D, kKeys>;
     const int G = a.Hq / a.Hkv;
     CUtensorMap mq, mk, mv;
-    const uint32_t box = uint32_t(a.table && a.page_size < kBlock ? a.page_size : kBlock);
+    const uint32_t box = uint32_t(a.table && a.page_size < C::kBlock ? a.page_size : C::kBlock);
     const uint64_t planes = uint64_t(a.num_pages) * a.Hkv;
     if (!encode_bf16_3d(&mq, a.q, D, uint64_t(G) * a.T, uint64_t(a.B) * a.Hkv, 64, kTileM) ||
         !encode_bf16_3d(&mk, a.kpages, D, uint64_t(a.page_size), planes, 64, box) ||

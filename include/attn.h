@@ -705,7 +705,7 @@ int attn_tree_mask(const int *parents, const int *seqlens, const int *draft_lens
  *              (or none whose score is above -inf) gets o = 0, lse = -inf.
  *   Drafted tokens whose row is at or past the capacity have no key.
  *   d in {64, 128}; 1 <= Hq / Hkv <= 16; 1 <= T <= 256; B * Hkv * ceil(capacity /
- *   128) < 2^31.
+ *   64) < 2^31.
  *   workspace  at least attn_decode_tree_workspace_bytes(...) bytes, 16-byte
  *              aligned.  Nothing in it outlives the call.
  * Up to two kernels run on `stream`, with no host synchronisation.  No atomics:
