@@ -15,9 +15,10 @@
 //   kRows (R > 128): the chains hold two tiles of rows, and both visit every key
 //     block; units of 256 rows, `mt` units a KV head, side by side on mt SMs so
 //     that all but one find the keys in L2.
-//   kKeys (R <= 128): one tile; the chains take turns with the key blocks, and
-//     their softmax states are merged in the epilogue, where each of them adds up half of the
-//     columns from both accumulators.
+//   kKeys (R <= 128): one tile; the chains take turns with the key blocks (of 64
+//     keys), each with two score buffers, so that the products' latency is not in a
+//     chain's way; their softmax states are merged in the epilogue, where each of
+//     them adds up half of the columns from both accumulators.
 // The blocks of all (sequence, KV head) pairs, in that order, are cut into equal
 // shares, one a CTA (group of mt): nothing depends on how ragged the lengths are.  A
 // pair that lies in one share is written out at once; one that is cut goes through
@@ -63,6 +64,8 @@ constexpr int kTurnStride = 20, kTurnFloats = 32 * kTurnStride;
 constexpr int kMaskWords = 8;  // 32-bit words of a row's mask: 256 drafted tokens
 constexpr int kMergeWarps = 4;
 
+constexpr int kUnitInts = 12;  // of a unit in the queue
+
 // Keys of a block.  Where the chains take turns, HBM is what they wait for, and small
 // blocks hold less of the ring while they are worked on.
 constexpr int block_keys(bool keys) { return keys ? 64 : 128; }
@@ -80,11 +83,13 @@ struct Cfg {
     static constexpr int kOddOffset = kStateOffset + (kKeys ? 2 * 2 * kTileM * 8 : 0);
     static constexpr int kBarOffset = kOddOffset + 4 * kMaskWords * 4;
     // barriers
-    static constexpr int kQFull = 0, kQEmpty = 2, kSFull = 4, kPFull = 6, kOFull = 8, kOEmpty = 10, kStateFull = 12,
-                         kDrain = 13, kUFull = 14, kUEmpty = 16, kKVFull = 18, kKVEmpty = 18 + kStages,
-                         kNumBars = 18 + 2 * kStages;
+    // (S and P: [chain][buffer])
+    static constexpr int kBuffers = kKeys ? 2 : 1;
+    static constexpr int kQFull = 0, kQEmpty = 2, kSFull = 4, kPFull = 8, kOFull = 12, kOEmpty = 14, kStateFull = 16,
+                         kDrain = 17, kUFull = 18, kUEmpty = 20, kKVFull = 22, kKVEmpty = 22 + kStages,
+                         kNumBars = 22 + 2 * kStages;
     static constexpr int kUnitOffset = (kBarOffset + kNumBars * 8 + 15) / 16 * 16;
-    static constexpr int kSmemBytes = kUnitOffset + 2 * 32 + 64 + 1024;  // units, start, tmem, abort; alignment
+    static constexpr int kSmemBytes = kUnitOffset + 2 * kUnitInts * 4 + 16 + 1024;  // units, tmem, abort; alignment
     static_assert(kSmemBytes <= 227 * 1024, "shared memory");
 };
 
@@ -103,9 +108,16 @@ struct Params {
     unsigned long long wait_ns;
 };
 
-// A piece of work: blocks [j0, j0 + n) of the nb blocks of pair (b, g); n = 0: the end.
+// A piece of work: blocks [j0, j0 + n) of the nb blocks of pair (b, g); n = 0: the end.  holes: some of its entries may be
+// no page.
 struct Unit {
-    int b, g, j0, n, nb, len, tb, keys;
+    int b, g, j0, n, nb, len, tb, keys, holes;
+    __device__ __forceinline__ void put(volatile int *e) const {
+        e[0] = b, e[1] = g, e[2] = j0, e[3] = n, e[4] = nb, e[5] = len, e[6] = tb, e[7] = keys, e[8] = holes;
+    }
+    __device__ __forceinline__ void get(const volatile int *e) {
+        b = e[0], g = e[1], j0 = e[2], n = e[3], nb = e[4], len = e[5], tb = e[6], keys = e[7], holes = e[8];
+    }
 };
 
 __device__ __forceinline__ void load_sequence(const Params &p, int b, int &len, int &tb) {
@@ -120,14 +132,29 @@ __device__ __forceinline__ int blocks_of(int keys) {
     return (keys + kBlock - 1) / kBlock;
 }
 
-// Blocks of all pairs (all lanes of the calling warp).
+// The lengths of 256 sequences from `first` on, eight a lane.
+constexpr int kRound = 8;
+struct Lengths {
+    int len[kRound], tb[kRound];
+    __device__ __forceinline__ void load(const Params &p, int first) {
+#pragma unroll
+        for (int k = 0; k < kRound; ++k) {
+            const int i = first + 32 * k + int(threadIdx.x & 31);
+            len[k] = tb[k] = 0;
+            if (i < p.B) load_sequence(p, i, len[k], tb[k]);
+        }
+    }
+};
+
+// Blocks of all pairs (all lanes of the calling warp); leaves the first 256 lengths in l.  The host bounds the sum, and
+// all places in it, below 2^31.
 template <int kBlock>
-__device__ __forceinline__ long long all_blocks(const Params &p) {
-    long long n = 0;
-    for (int b = threadIdx.x & 31; b < p.B; b += 32) {
-        int len, tb;
-        load_sequence(p, b, len, tb);
-        n += blocks_of<kBlock>(keys_of(p, len, tb));
+__device__ __forceinline__ unsigned all_blocks(const Params &p, Lengths &l) {
+    unsigned n = 0;
+    for (int first = (p.B - 1) / (32 * kRound) * (32 * kRound); first >= 0; first -= 32 * kRound) {
+        l.load(p, first);
+#pragma unroll
+        for (int k = 0; k < kRound; ++k) n += blocks_of<kBlock>(keys_of(p, l.len[k], l.tb[k]));
     }
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) n += __shfl_xor_sync(0xffffffffu, n, off);
@@ -136,38 +163,39 @@ __device__ __forceinline__ long long all_blocks(const Params &p) {
 
 // The pair of block x, and which of its blocks x is (j0); all lanes of the calling warp.
 template <int kBlock>
-__device__ __forceinline__ Unit find_block(const Params &p, long long x) {
+__device__ __forceinline__ Unit find_block(const Params &p, Lengths &l, unsigned x) {
     const int lane = threadIdx.x & 31;
     Unit u = {};
-    long long before = 0;
-    for (int first = 0; first < p.B; first += 32) {
-        int len = 0, tb = 0, keys = 0;
-        if (first + lane < p.B) {
-            load_sequence(p, first + lane, len, tb);
-            keys = keys_of(p, len, tb);
-        }
-        const long long n = (long long)blocks_of<kBlock>(keys) * p.Hkv;
-        long long upto = n;
+    unsigned before = 0;
+    for (int first = 0; first < p.B; first += 32 * kRound) {
+        if (first > 0) l.load(p, first);
 #pragma unroll
-        for (int off = 1; off < 32; off <<= 1) {
-            const long long y = __shfl_up_sync(0xffffffffu, upto, off);
-            if (lane >= off) upto += y;
+        for (int k = 0; k < kRound; ++k) {
+            if (first + 32 * k >= p.B) break;
+            const int keys = keys_of(p, l.len[k], l.tb[k]);
+            const unsigned n = unsigned(blocks_of<kBlock>(keys)) * p.Hkv;
+            unsigned upto = n;
+#pragma unroll
+            for (int off = 1; off < 32; off <<= 1) {
+                const unsigned y = __shfl_up_sync(0xffffffffu, upto, off);
+                if (lane >= off) upto += y;
+            }
+            const unsigned base = before + upto - n;
+            const uint32_t hit = __ballot_sync(0xffffffffu, x >= base && x < base + n);
+            if (hit) {
+                const int src = __ffs(hit) - 1;
+                u.b = first + 32 * k + src;
+                u.len = __shfl_sync(0xffffffffu, l.len[k], src);
+                u.tb = __shfl_sync(0xffffffffu, l.tb[k], src);
+                u.keys = __shfl_sync(0xffffffffu, keys, src);
+                u.nb = blocks_of<kBlock>(u.keys);
+                const unsigned rem = x - __shfl_sync(0xffffffffu, base, src);
+                u.g = int(rem / unsigned(u.nb));
+                u.j0 = int(rem - unsigned(u.g) * unsigned(u.nb));
+                return u;
+            }
+            before += __shfl_sync(0xffffffffu, upto, 31);
         }
-        const long long base = before + upto - n;
-        const uint32_t hit = __ballot_sync(0xffffffffu, x >= base && x < base + n);
-        if (hit) {
-            const int src = __ffs(hit) - 1;
-            u.b = first + src;
-            u.len = __shfl_sync(0xffffffffu, len, src);
-            u.tb = __shfl_sync(0xffffffffu, tb, src);
-            u.keys = __shfl_sync(0xffffffffu, keys, src);
-            u.nb = blocks_of<kBlock>(u.keys);
-            const unsigned rem = unsigned(x - __shfl_sync(0xffffffffu, base, src));
-            u.g = int(rem / unsigned(u.nb));
-            u.j0 = int(rem - unsigned(u.g) * unsigned(u.nb));
-            return u;
-        }
-        before += __shfl_sync(0xffffffffu, upto, 31);
     }
     return u;
 }
@@ -184,15 +212,18 @@ __device__ __forceinline__ uint32_t mask_bits(const uint32_t (&m)[kMaskWords], i
     return __funnelshift_r(lo, hi, u & 31);
 }
 
-// A row of V in shared memory (128 bytes of each chunk; the swizzle stays within them), of key `key`: zeros behind
-// the last key; in a drafted row, zeros for what is not finite, and whether there was any.
+// V rows [first, kBlock) of a block in shared memory, by the four warps of a chain (`warp` of them; the swizzle stays
+// within a row's 128 bytes of a chunk, which eight lanes take): rows from `end` on become zeros; in the drafted rows
+// before it, of which row `first` is number `u0`, elements that are not finite do, and the row's bit in `odd` is set.
 template <int kChunks, int kBlock>
-__device__ __forceinline__ bool clean_row(uint8_t *v, int key, int len, int keys) {
-    bool found = false;
-    if (key >= len)
-        for (int i = 0; i < kChunks * 8; ++i) {
-            uint4 *at = reinterpret_cast<uint4 *>(v + (i >> 3) * (kBlock * 128) + (i & 7) * 16);
-            if (key >= keys) {
+__device__ __forceinline__ void clean_rows(uint8_t *v, int warp, int first, int end, int u0, uint32_t *odd) {
+    const int lane = threadIdx.x & 31;
+    for (int row = first + warp * 4 + (lane >> 3); row < kBlock; row += 16) {
+        bool found = false;
+#pragma unroll
+        for (int c = 0; c < kChunks; ++c) {
+            uint4 *at = reinterpret_cast<uint4 *>(v + c * (kBlock * 128) + row * 128 + (lane & 7) * 16);
+            if (row >= end) {
                 *at = make_uint4(0, 0, 0, 0);
                 continue;
             }
@@ -207,7 +238,9 @@ __device__ __forceinline__ bool clean_row(uint8_t *v, int key, int len, int keys
             if (here) *at = x;
             found |= here;
         }
-    return found;
+        const int u = u0 + row - first;
+        if (found) atomicOr(odd + (u >> 5), 1u << (u & 31));
+    }
 }
 
 // x += the elements of 32 columns of V that are not finite.
@@ -229,13 +262,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint8_t *sQ = smem, *sKV = smem + C::kQTiles * C::kQBytes;
     uint64_t *bars = reinterpret_cast<uint64_t *>(smem + C::kBarOffset);
-    volatile int *units = reinterpret_cast<volatile int *>(smem + C::kUnitOffset);  // two entries of 8
-    volatile int *start = units + 16;  // the first unit of the share, and the blocks left (8)
+    volatile int *units = reinterpret_cast<volatile int *>(smem + C::kUnitOffset);  // two entries
     // Drafted V rows of a unit that are not finite everywhere; of four units in turn, since the other chain may still
     // read the last one's, and the next one's has to be empty by then.
     uint32_t *odd_rows = reinterpret_cast<uint32_t *>(smem + C::kOddOffset);
     static_assert(4 * kMaskWords == 32, "one warp clears them");
-    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + C::kUnitOffset + 96);
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + C::kUnitOffset + 2 * kUnitInts * 4);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int share = blockIdx.x / p.mt, m = blockIdx.x - share * p.mt;
@@ -247,12 +279,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int t = 0; t < 2; ++t) {
             mbar_init(bar(C::kQFull + t), 1);
             mbar_init(bar(C::kQEmpty + t), 1);
-            mbar_init(bar(C::kSFull + t), 1);
-            mbar_init(bar(C::kPFull + t), 4);
+            for (int i = 0; i < 2; ++i) {
+                mbar_init(bar(C::kSFull + 2 * t + i), 1);
+                mbar_init(bar(C::kPFull + 2 * t + i), 4);
+            }
             mbar_init(bar(C::kOFull + t), 1);
             mbar_init(bar(C::kOEmpty + t), kKeys ? 8 : 4);
             mbar_init(bar(C::kUFull + t), 1);
-            mbar_init(bar(C::kUEmpty + t), 1 + 8);
+            mbar_init(bar(C::kUEmpty + t), 3 + 8);  // the K, V and MMA warps, the softmax warps
         }
         mbar_init(bar(C::kStateFull), 8);
         mbar_init(bar(C::kDrain), 1);
@@ -273,26 +307,23 @@ __global__ void __launch_bounds__(kThreads, 1)
         tmem_alloc(smem_u32(tmem_slot), kTmemCols);
         tmem_relinquish();
     }
+    // The share [lo, lo + left) of the blocks: warp 3 finds its first unit, warp 2 what lies behind it.
+    Unit u = {};
+    int left = 0;
     if (warp == 2 || warp == 3) {
-        const long long total = all_blocks<kBlock>(p), S = (total + p.shares - 1) / p.shares, lo = share * S;
-        const int left = int(lo < total ? min(S, total - lo) : 0);
-        if (warp == 2) {
-            Unit u = {};
-            if (left > 0) u = find_block<kBlock>(p, lo);
-            if (lane == 0) {
-                start[0] = u.b;
-                start[1] = u.g;
-                start[2] = u.j0;
-                start[3] = left;
-            }
+        Lengths l;
+        const unsigned total = all_blocks<kBlock>(p, l), S = (total + p.shares - 1) / p.shares, lo = share * S;
+        left = int(lo < total ? min(S, total - lo) : 0);
+        if (warp == 3) {
+            if (left > 0) u = find_block<kBlock>(p, l, lo);
         } else if (m == 0) {
             // Where the merge finds the pair that goes on behind this share: from the lengths alone, so that a launch
             // whose waits run out leaves the merge wrong numbers but no wrong addresses.
             int4 cut = make_int4(0, 0, 0, 0);
             if (left > 0) {
-                const Unit u = find_block<kBlock>(p, lo + left - 1);
-                const int rest = u.nb - u.j0 - 1;
-                if (u.j0 < left && rest > 0) cut = make_int4(u.b, u.g, 1 + int((rest + S - 1) / S), u.tb);
+                const Unit at = find_block<kBlock>(p, l, lo + left - 1);
+                const int rest = at.nb - at.j0 - 1;
+                if (at.j0 < left && rest > 0) cut = make_int4(at.b, at.g, 1 + int((rest + S - 1) / S), at.tb);
             }
             if (lane == 0) p.cuts[share] = cut;
         }
@@ -304,44 +335,36 @@ __global__ void __launch_bounds__(kThreads, 1)
 
     if (warp < 4) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kCtrlRegs));
-        if (warp == 0) {
-            // -------------------------------------------------------- producer
-            uint32_t fills = 0;
-            int q_loads = 0;  // per tile (both are loaded for every unit that has them)
+        const bool second = !kKeys && (2 * m + 1) * kTileM < p.rows;  // a second tile
+        const uint64_t drain_ns = 1000000000ull;
+        volatile int no_abort = 0;
+        if (warp == 3) {
+            // -------------------------------------------- planner: the units, and Q
+            uint32_t q_loads = 0;  // per tile (both are loaded for every unit that has them)
             bool ok = true;
-            Unit u = {};
-            u.b = start[0];
-            u.g = start[1];
-            u.j0 = start[2];
-            int left = start[3];
-            if (left > 0) {
-                load_sequence(p, u.b, u.len, u.tb);
-                u.keys = keys_of(p, u.len, u.tb);
-                u.nb = blocks_of<kBlock>(u.keys);
-            }
-            const bool second = !kKeys && (2 * m + 1) * kTileM < p.rows;
-            const int boxes = p.table && p.page_size < kBlock ? kBlock / p.page_size : 1;
-            const int box_bytes = C::kChunkBytes / boxes;
-            const int my_box = lane / C::kChunks, my_chunk = lane % C::kChunks;
+            u.holes = p.table != nullptr;  // (the first unit's entries are looked at block by block)
             for (long long qi = 0; ok; ++qi) {
-                u.n = min(left, u.nb - u.j0);
                 const int qs = int(qi & 1);
+                u.n = left > 0 ? min(left, u.nb - u.j0) : 0;
+                if (p.table && qi > 0) {
+                    // Ahead of the other warps: whether the unit needs looking at all.
+                    const int *table = p.table + (size_t)u.b * p.max_pages;
+                    const int last = min(u.keys, (u.j0 + u.n) * kBlock) - 1;
+                    bool hole = false;
+                    for (int i = ((u.j0 * kBlock) >> p.shift) + lane; u.n > 0 && i <= last >> p.shift; i += 32) {
+                        const int page = table[i];
+                        hole |= page < 0 || page >= p.num_pages;
+                    }
+                    u.holes = __any_sync(0xffffffffu, hole);
+                }
                 if (qi >= 2) ok = mbar_wait_warp(bar(C::kUEmpty + qs), uint32_t(((qi >> 1) - 1) & 1), p.wait_ns, abort_flag, status);
                 if (!ok) break;
                 if (lane == 0) {
-                    volatile int *e = units + 8 * qs;
-                    e[0] = u.b;
-                    e[1] = u.g;
-                    e[2] = u.j0;
-                    e[3] = left > 0 ? u.n : 0;
-                    e[4] = u.nb;
-                    e[5] = u.len;
-                    e[6] = u.tb;
-                    e[7] = u.keys;
+                    u.put(units + kUnitInts * qs);
                     mbar_arrive(bar(C::kUFull + qs));
                 }
                 __syncwarp();
-                if (left <= 0) break;
+                if (u.n == 0) break;
                 for (int t = 0; t < (second ? 2 : 1); ++t) {
                     if (q_loads > 0) ok = mbar_wait_warp(bar(C::kQEmpty + t), (q_loads - 1) & 1, p.wait_ns, abort_flag, status);
                     if (!ok) break;
@@ -355,42 +378,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 if (!ok) break;
                 ++q_loads;
-                // Lane i holds entry base + i of the table, and the one 32 behind it.
-                const int *table = p.table ? p.table + (size_t)u.b * p.max_pages : nullptr;
-                const int used = (u.keys + p.page_size - 1) >> p.shift;
-                auto entry = [&](int i) { return table && i < used ? table[i] : -1; };
-                int base = (u.j0 * kBlock) >> p.shift;
-                int cur = entry(base + lane), nxt = entry(base + 32 + lane);
-                for (int j = 0; ok && j < u.n; ++j) {
-                    const int key = (u.j0 + j) * kBlock;
-                    int page = u.b, row = key;
-                    if (table) {
-                        const int first = key >> p.shift;
-                        if (first >= base + 32) {
-                            base += 32;
-                            cur = nxt;
-                            nxt = entry(base + 32 + lane);
-                        }
-                        page = __shfl_sync(0xffffffffu, cur, (first - base + my_box) & 31);
-                        row = boxes > 1 ? 0 : key & (p.page_size - 1);
-                    }
-                    const int plane = page >= 0 && page < p.num_pages ? page * p.Hkv + u.g : p.num_pages * p.Hkv;
-                    for (int kv = 0; kv < 2; ++kv) {
-                        const uint32_t slot = fills % C::kStages, round = fills / C::kStages;
-                        if (round > 0) {
-                            ok = mbar_wait_warp(bar(C::kKVEmpty + slot), (round - 1) & 1, p.wait_ns, abort_flag, status);
-                            if (!ok) break;
-                        }
-                        const uint32_t fb = bar(C::kKVFull + slot);
-                        if (lane == 0) mbar_arrive_expect_tx(fb, C::kKVBytes);
-                        __syncwarp();
-                        if (my_box < boxes)
-                            tma_load_3d(smem_u32(sKV + slot * C::kKVBytes + my_chunk * C::kChunkBytes + my_box * box_bytes),
-                                        kv == 0 ? &tmK : &tmV, fb, my_chunk * 64, row, plane);
-                        ++fills;
-                    }
-                }
-                if (!ok) break;
                 left -= u.n;
                 if (left <= 0) continue;
                 u.j0 = 0;
@@ -404,21 +391,83 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
             }
             __syncwarp();
-            if (!ok && lane == 0) {
-                // The last copy into every slot has to land before the CTA goes (bounded).
-                const unsigned long long drain_ns = 1000000000ull;
-                volatile int no_abort = 0;
-                for (uint32_t s = 0; s < C::kStages; ++s) {
-                    if (fills <= s) continue;
-                    const uint32_t last = (fills - 1 - s) / C::kStages;  // round of the slot's last fill
-                    if (!mbar_wait_bounded(bar(C::kKVFull + s), last & 1, drain_ns, &no_abort, status))
-                        atomicOr(status, kStatusDrainTimeout);
-                }
+            // Copies have to land before the CTA goes (bounded), whatever became of the other warps.
+            if (!ok && lane == 0)
                 for (int t = 0; t < (second ? 2 : 1); ++t)
                     if (q_loads > 0 && !mbar_wait_bounded(bar(C::kQFull + t), (q_loads - 1) & 1, drain_ns, &no_abort, status))
                         atomicOr(status, kStatusDrainTimeout);
+            __syncwarp();
+        } else if (warp == 0 || warp == 2) {
+            // ------------------------------------- producers: warp 0 K, warp 2 V
+            // Blocks alternate in the ring, K at even fills and V at odd ones; neither warp waits for the other's slots.
+            const uint32_t kv = warp == 0 ? 0 : 1;
+            const CUtensorMap *map = warp == 0 ? &tmK : &tmV;
+            uint32_t blocks = 0;  // loaded so far
+            bool ok = true;
+            const int boxes = p.table && p.page_size < kBlock ? kBlock / p.page_size : 1;
+            const int box_bytes = C::kChunkBytes / boxes;
+            for (long long qi = 0; ok; ++qi) {
+                const int qs = int(qi & 1);
+                ok = mbar_wait_warp(bar(C::kUFull + qs), uint32_t((qi >> 1) & 1), p.wait_ns, abort_flag, status);
+                if (!ok) break;
+                u.get(units + kUnitInts * qs);
+                __syncwarp();
+                mbar_arrive_elect(bar(C::kUEmpty + qs));
+                if (u.n == 0) break;
+                // Lane i holds entry base + i of the table, and the one 32 behind it.
+                const int *table = p.table ? p.table + (size_t)u.b * p.max_pages : nullptr;
+                const int used = (u.keys + p.page_size - 1) >> p.shift;
+                auto entry = [&](int i) { return table && i < used ? table[i] : -1; };
+                int base = (u.j0 * kBlock) >> p.shift;
+                int cur = entry(base + lane), nxt = entry(base + 32 + lane);
+                for (int j = 0; j < u.n; ++j) {
+                    const uint32_t fill = 2 * blocks + kv, slot = fill % C::kStages, round = fill / C::kStages;
+                    if (round > 0) ok = mbar_wait_warp(bar(C::kKVEmpty + slot), (round - 1) & 1, p.wait_ns, abort_flag, status);
+                    if (!ok) break;
+                    const uint32_t fb = bar(C::kKVFull + slot), to = smem_u32(sKV + slot * C::kKVBytes);
+                    if (lane == 0) mbar_arrive_expect_tx(fb, C::kKVBytes);
+                    const int key = (u.j0 + j) * kBlock, first = key >> p.shift;
+                    if (table && first >= base + 32) {
+                        base += 32;
+                        cur = nxt;
+                        nxt = entry(base + 32 + lane);
+                    }
+                    for (int i = 0; i < boxes; ++i) {
+                        const int page = table ? __shfl_sync(0xffffffffu, cur, (first - base + i) & 31) : u.b;
+                        const int row = !table ? key : boxes > 1 ? 0 : key & (p.page_size - 1);
+                        const int plane = page >= 0 && page < p.num_pages ? page * p.Hkv + u.g : p.num_pages * p.Hkv;
+                        if (lane == 0)
+#pragma unroll
+                            for (int c = 0; c < C::kChunks; ++c)
+                                tma_load_3d(to + c * C::kChunkBytes + i * box_bytes, map, fb, c * 64, row, plane);
+                    }
+                    __syncwarp();
+                    ++blocks;
+                }
             }
             __syncwarp();
+            if (!ok && lane == 0)
+                for (uint32_t s = kv; s < C::kStages; s += 2) {
+                    if (2 * blocks <= s) continue;  // fills below 2 blocks + kv are out
+                    const uint32_t last = (2 * blocks - 2 + kv - s) / C::kStages;  // round of the slot's last fill
+                    if (!mbar_wait_bounded(bar(C::kKVFull + s), last & 1, drain_ns, &no_abort, status))
+                        atomicOr(status, kStatusDrainTimeout);
+                }
+            __syncwarp();
+            if (warp == 2) {
+                // Sequences without a token: zeros, and a log-sum-exp of nothing.
+                for (int b = blockIdx.x; b < p.B; b += gridDim.x) {
+                    int len, tb;
+                    load_sequence(p, b, len, tb);
+                    if (tb > 0) continue;
+                    const size_t rows = (size_t)p.Hkv * p.rows, units16 = rows * (D / 8);
+                    uint4 *o = reinterpret_cast<uint4 *>(p.o + (size_t)b * rows * D);
+                    for (size_t i = lane; i < units16; i += 32) o[i] = make_uint4(0, 0, 0, 0);
+                    if (p.lse)
+                        for (size_t i = lane; i < rows; i += 32) p.lse[(size_t)b * rows + i] = -INFINITY;
+                }
+                __syncwarp();
+            }
         } else if (warp == 1) {
             // ------------------------------------------------------ MMA issuer
             constexpr uint32_t kIdescQK = idesc_bf16_f32(kTileM, kBlock, 0), kIdescPV = idesc_bf16_f32(kTileM, D, 1);
@@ -426,7 +475,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             uint32_t q_used = 0;
             uint32_t p_odd = 0, o_odd = 0, used = 0;  // a bit a chain: waits for P, units done, whether there was one
             bool ok = true;
-            const int chains = kKeys || (2 * m + 1) * kTileM < p.rows ? 2 : 1;
+            const int chains = second ? 2 : 1;  // (kRows)
             auto wait_slot = [&](uint32_t f) {
                 return mbar_wait_warp(bar(C::kKVFull + f % C::kStages), (f / C::kStages) & 1, p.wait_ns, abort_flag, status);
             };
@@ -434,7 +483,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const uint64_t dK = smem_desc_sw128(smem_u32(sKV), 16, 1024);
             const uint64_t dV = smem_desc_sw128(smem_u32(sKV), C::kChunkBytes, 1024);
             auto slot_off = [&](uint32_t f) { return uint64_t(f % C::kStages * (C::kKVBytes >> 4)); };
-            auto issue_qk = [&](int t, uint32_t fK) {
+            auto issue_qk = [&](int t, int buf, uint32_t fK) {
                 const uint64_t a0 = dQ + uint64_t((kKeys ? 0 : t) * (C::kQBytes >> 4)), b0 = dK + slot_off(fK);
 #pragma unroll
                 for (int g = 0; g < D / 64; ++g) {
@@ -444,10 +493,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                         a[i] = a0 + uint64_t((g * C::kQChunkBytes + i * 32) >> 4);
                         b[i] = b0 + uint64_t((g * C::kChunkBytes + i * 32) >> 4);
                     }
-                    tc_mma_ss_x4_elect(tmem_base + t * kTileM, a, b, kIdescQK, g > 0 ? 1u : 0u);
+                    tc_mma_ss_x4_elect(tmem_base + t * kTileM + buf * kBlock, a, b, kIdescQK, g > 0 ? 1u : 0u);
                 }
             };
-            auto issue_pv = [&](int t, uint32_t fV, bool acc) {
+            auto issue_pv = [&](int t, int buf, uint32_t fV, bool acc) {
                 const uint64_t b0 = dV + slot_off(fV);
 #pragma unroll
                 for (int g = 0; g < kBlock / 64; ++g) {
@@ -456,7 +505,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         const int kk = g * 4 + i;
-                        a[i] = tmem_base + t * kTileM + kk * 8;
+                        a[i] = tmem_base + t * kTileM + buf * kBlock + kk * 8;
                         b[i] = b0 + uint64_t((kk * 16 * 128) >> 4);
                     }
                     tc_mma_ts_x4_elect(tmem_base + C::kOCol + t * D, a, b, kIdescPV, (acc || g > 0) ? 1u : 0u);
@@ -466,21 +515,23 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int qs = int(qi & 1);
                 ok = mbar_wait_warp(bar(C::kUFull + qs), uint32_t((qi >> 1) & 1), p.wait_ns, abort_flag, status);
                 if (!ok) break;
-                const volatile int *e = units + 8 * qs;
-                const int n = __shfl_sync(0xffffffffu, int(e[3]), 0);
+                const int n = __shfl_sync(0xffffffffu, int(units[kUnitInts * qs + 3]), 0);
                 mbar_arrive_elect(bar(C::kUEmpty + qs));
                 if (n == 0) break;
                 const uint32_t f0 = fills;  // K_j at f0 + 2 j, V_j behind it
-                // The first product of each chain.
-                for (int t = 0; ok && t < chains; ++t) {
-                    const int j = kKeys ? t : 0;
-                    if (j >= n) continue;
+                // The first product of each chain and buffer.
+                ok = mbar_wait_warp(bar(C::kQFull), q_used & 1, p.wait_ns, abort_flag, status);
+                if (ok && !kKeys && second) ok = mbar_wait_warp(bar(C::kQFull + 1), q_used & 1, p.wait_ns, abort_flag, status);
+#pragma unroll
+                for (int i = 0; i < (kKeys ? 4 : 2); ++i) {
+                    const int j = kKeys ? i : 0, t = i & 1, buf = kKeys ? i >> 1 : 0;
+                    if (!ok || j >= n || (!kKeys && t >= chains)) break;
                     ok = wait_slot(f0 + 2 * j);
-                    if (ok && (t == 0 || !kKeys)) ok = mbar_wait_warp(bar(C::kQFull + t), q_used & 1, p.wait_ns, abort_flag, status);
                     if (!ok) break;
                     tc_fence_after();
-                    issue_qk(t, f0 + 2 * j);
-                    tc_commit_elect(bar(C::kSFull + t));
+                    issue_qk(t, buf, f0 + 2 * j);
+                    tc_commit_elect(bar(C::kSFull + 2 * t + buf));
+                    if (j == n - 1) tc_commit_elect(bar(C::kQEmpty + (kKeys ? 0 : t)));  // Q's last product
                 }
                 ++q_used;
                 for (int j = 0; ok && j < n; ++j) {
@@ -488,11 +539,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                     bool v_ready = false;
 #pragma unroll
                     for (int i = 0; i < (kKeys ? 1 : 2); ++i) {
-                        const int t = kKeys ? j & 1 : i;
+                        const int t = kKeys ? j & 1 : i, buf = kKeys ? j >> 1 & 1 : 0, tb = 2 * t + buf;
                         if (!kKeys && i >= chains) break;
-                        ok = mbar_wait_warp(bar(C::kPFull + t), p_odd >> t & 1, p.wait_ns, abort_flag, status);
+                        ok = mbar_wait_warp(bar(C::kPFull + tb), p_odd >> tb & 1, p.wait_ns, abort_flag, status);
                         if (!ok) break;
-                        p_odd ^= 1u << t;
+                        p_odd ^= 1u << tb;
                         const bool first = kKeys ? j < 2 : j == 0;
                         if (first && (used >> t & 1)) {
                             ok = mbar_wait_warp(bar(C::kOEmpty + t), ~(o_odd >> t) & 1, p.wait_ns, abort_flag, status);
@@ -504,17 +555,18 @@ __global__ void __launch_bounds__(kThreads, 1)
                             v_ready = true;
                         }
                         tc_fence_after();
-                        issue_pv(t, fV, !first);
+                        issue_pv(t, buf, fV, !first);
                         if (kKeys || t == chains - 1) tc_commit_elect(bar(C::kKVEmpty + fV % C::kStages));
-                        const int next = j + (kKeys ? 2 : 1);
+                        const int next = j + (kKeys ? 4 : 1);  // into the buffer that P has been read from
                         if (next < n) {
                             ok = wait_slot(f0 + 2 * next);
                             if (!ok) break;
-                            issue_qk(t, f0 + 2 * next);
-                            tc_commit_elect(bar(C::kSFull + t));
-                        } else {
+                            issue_qk(t, buf, f0 + 2 * next);
+                            tc_commit_elect(bar(C::kSFull + tb));
+                            if (next == n - 1) tc_commit_elect(bar(C::kQEmpty + (kKeys ? 0 : t)));
+                        }
+                        if (j + (kKeys ? 2 : 1) >= n) {  // the chain's last block
                             tc_commit_elect(bar(C::kOFull + t));
-                            if (!kKeys || j == n - 1) tc_commit_elect(bar(C::kQEmpty + (kKeys ? 0 : t)));
                             o_odd ^= 1u << t;
                             used |= 1u << t;
                         }
@@ -523,48 +575,33 @@ __global__ void __launch_bounds__(kThreads, 1)
                 fills = f0 + 2 * n;
             }
             tc_commit_elect(bar(C::kDrain));
-            volatile int no_abort = 0;
-            if (!mbar_wait_warp(bar(C::kDrain), 0, 1000000000ull, &no_abort, status) && lane == 0)
+            if (!mbar_wait_warp(bar(C::kDrain), 0, drain_ns, &no_abort, status) && lane == 0)
                 atomicOr(status, kStatusDrainTimeout);
             __syncwarp();
-        } else if (warp == 3) {
-            // Sequences without a token: zeros, and a log-sum-exp of nothing.
-            for (int b = blockIdx.x; b < p.B; b += gridDim.x) {
-                int len, tb;
-                load_sequence(p, b, len, tb);
-                if (tb > 0) continue;
-                const size_t rows = (size_t)p.Hkv * p.rows, units16 = rows * (D / 8);
-                uint4 *o = reinterpret_cast<uint4 *>(p.o + (size_t)b * rows * D);
-                for (size_t i = lane; i < units16; i += 32) o[i] = make_uint4(0, 0, 0, 0);
-                if (p.lse)
-                    for (size_t i = lane; i < rows; i += 32) p.lse[(size_t)b * rows + i] = -INFINITY;
-            }
         }
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
         // ------------------------------------------------- softmax / epilogue
         const int t = (warp - 4) >> 2, quarter = warp & 3, r = quarter * 32 + lane;
         const uint32_t lane_off = uint32_t(quarter * 32) << 16;
-        const uint32_t tS = tmem_base + lane_off + t * kTileM, tO = tmem_base + lane_off + C::kOCol;
+        const uint32_t tS0 = tmem_base + lane_off + t * kTileM, tO = tmem_base + lane_off + C::kOCol;
         const int row0 = kKeys ? 0 : (2 * m + t) * kTileM, row = row0 + r;
         const int token = row % p.T;
         const bool has_rows = row0 + quarter * 32 < p.rows;  // of this warp; the others only keep step
         const bool has_tile = row0 < p.rows;
-        const bool second = kKeys || (2 * m + 1) * kTileM < p.rows;  // whether chain 1 is at work
+        const bool both = kKeys || (2 * m + 1) * kTileM < p.rows;  // whether chain 1 is at work
         const float sl2 = p.scale_log2;
         const int limit = p.rows - row0;  // rows of the tile in use, if below 128
         float *turn = reinterpret_cast<float *>(smem + C::kTurnOffset) + (warp - 4) * kTurnFloats;
         float2 *states = reinterpret_cast<float2 *>(smem + C::kStateOffset);  // [unit parity][chain][row]
-        uint32_t s_waits = 0, o_waits = 0, o_waits1 = 0;
+        uint32_t s_odd = 0, o_waits = 0, o_waits1 = 0;  // s_odd: a bit a buffer
         uint32_t kv_base = 0;
         bool ok = true;
         for (long long qi = 0; ok; ++qi) {
             const int qs = int(qi & 1);
             ok = mbar_wait_warp(bar(C::kUFull + qs), uint32_t((qi >> 1) & 1), p.wait_ns, abort_flag, status);
             if (!ok) break;
-            const volatile int *e = units + 8 * qs;
-            Unit u;
-            u.b = e[0], u.g = e[1], u.j0 = e[2], u.n = e[3], u.nb = e[4], u.len = e[5], u.tb = e[6], u.keys = e[7];
+            u.get(units + kUnitInts * qs);
             __syncwarp();
             mbar_arrive_elect(bar(C::kUEmpty + qs));
             if (u.n == 0) break;
@@ -589,7 +626,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     seen[2 * w + 1] = uint32_t(x >> 32);
                 }
             }
-            const int *table = p.table ? p.table + (size_t)u.b * p.max_pages : nullptr;
+            const int *table = u.holes ? p.table + (size_t)u.b * p.max_pages : nullptr;  // null: nothing to look at
             const int boxes = p.page_size < kBlock ? kBlock / p.page_size : 1;  // (with a table only)
             const int used = (u.keys + p.page_size - 1) >> p.shift;
             // Lane i looks at entry i of a block's pages, one block ahead.
@@ -607,11 +644,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                     on_page = __ballot_sync(0xffffffffu, ahead >= 0 && ahead < p.num_pages);
                     ahead = page_of(j + kStep);
                 }
-                ok = mbar_wait_warp(bar(C::kSFull + t), s_waits & 1, p.wait_ns, abort_flag, status);
+                const int buf = kKeys ? j >> 1 & 1 : 0;
+                const uint32_t tS = tS0 + buf * kBlock;
+                ok = mbar_wait_warp(bar(C::kSFull + 2 * t + buf), s_odd >> buf & 1, p.wait_ns, abort_flag, status);
                 if (!ok) break;
-                ++s_waits;
+                s_odd ^= 1u << buf;
                 // S complete: so are all products before it, and K's slot is free once the last chain to use it says so.
-                if (quarter == 0 && (kKeys || t == (second ? 1 : 0)))
+                if (quarter == 0 && (kKeys || t == (both ? 1 : 0)))
                     mbar_arrive_elect(bar(C::kKVEmpty + (f0 + 2 * j) % C::kStages));
                 if (has_rows) {
                     tc_fence_after();
@@ -685,6 +724,15 @@ __global__ void __launch_bounds__(kThreads, 1)
                         tmem_wait_st();
                         l_blk = exp_block(m_run == -INFINITY ? 0.f : -m_run);
                         if (j > jt && __any_sync(0xffffffffu, corr != 1.f)) {
+                            if constexpr (kKeys) {
+                                // S(j) was issued ahead of the chain's last product into O: wait for that (its V slot, which
+                                // nobody can have filled and freed again before this block's P).
+                                const uint32_t f = f0 + 2 * (j - kStep) + 1;
+                                ok = mbar_wait_warp(bar(C::kKVEmpty + f % C::kStages), (f / C::kStages) & 1, p.wait_ns, abort_flag,
+                                                    status);
+                                if (!ok) break;
+                                tc_fence_after();
+                            }
 #pragma unroll
                             for (int c = 0; c < D / 32; ++c) {
                                 uint32_t ov[32];
@@ -705,14 +753,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const uint32_t fV = f0 + 2 * j + 1, slot = fV % C::kStages;
                     ok = mbar_wait_warp(bar(C::kKVFull + slot), (fV / C::kStages) & 1, p.wait_ns, abort_flag, status);
                     if (!ok) break;
-                    if (r < kBlock && clean_row<C::kChunks, kBlock>(sKV + slot * C::kKVBytes + r * 128, (u.j0 + j) * kBlock + r, u.len, u.keys)) {
-                        const int x = (u.j0 + j) * kBlock + r - u.len;
-                        atomicOr(odd_rows + (qi & 3) * kMaskWords + (x >> 5), 1u << (x & 31));
-                    }
+                    const int kv0 = (u.j0 + j) * kBlock, at = max(u.len - kv0, 0);
+                    clean_rows<C::kChunks, kBlock>(sKV + slot * C::kKVBytes, quarter, at, u.keys - kv0, kv0 + at - u.len,
+                                                   odd_rows + (qi & 3) * kMaskWords);
                     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                 }
                 __syncwarp();
-                mbar_arrive_elect(bar(C::kPFull + t));
+                mbar_arrive_elect(bar(C::kPFull + 2 * t + buf));
             }
             if (!ok) break;
 
@@ -760,58 +807,68 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (t == 0 && quarter == 0 && lane < kMaskWords) odd_rows[((qi + 2) & 3) * kMaskWords + lane] = 0;
             if (has_rows) {
                 const bool any = live && sum != 0.f;  // (NaN stays NaN)
-                // A thread holds a row; the warp turns 32 rows x 16 columns at a time through shared memory, so that
-                // four lanes store one row's 16 columns.
+                // A thread holds a row; the warp turns 64 bytes of each of its 32 rows at a time through shared memory, so
+                // that four lanes store them.
                 const int first = quarter * 32 + (lane >> 2);
                 constexpr int kCols = kKeys ? D / 2 : D;  // of this warp
                 const int col0 = kKeys ? t * kCols : 0;
 #pragma unroll
                 for (int c = 0; c < kCols / 32; ++c) {
                     const int col = col0 + c * 32;
-                    uint32_t ov[32];
+                    uint32_t ov[32], ow[32];
                     float x[32];
                     tmem_ld32(tO + (kKeys ? 0 : t * D) + col, ov);
+                    if (has1) tmem_ld32(tO + D + col, ow);
                     tmem_wait_ld();
 #pragma unroll
                     for (int i = 0; i < 32; ++i) x[i] = __uint_as_float(ov[i]) * f[0];
-                    if (has1) {
-                        tmem_ld32(tO + D + col, ov);
-                        tmem_wait_ld();
+                    if (has1)
 #pragma unroll
-                        for (int i = 0; i < 32; ++i) x[i] += __uint_as_float(ov[i]) * f[1];
-                    }
+                        for (int i = 0; i < 32; ++i) x[i] += __uint_as_float(ow[i]) * f[1];
                     if (any_odd) {
 #pragma unroll
                         for (int w = 0; w < kMaskWords; ++w)
                             for (uint32_t bits = odd[w]; bits; bits &= bits - 1) {
                                 const int key = u.len + 32 * w + __ffs(bits) - 1;
-                                const int page = table ? table[key >> p.shift] : u.b;
-                                const int in = table ? key & (p.page_size - 1) : key;
+                                const int page = p.table ? p.table[(size_t)u.b * p.max_pages + (key >> p.shift)] : u.b;
+                                const int in = p.table ? key & (p.page_size - 1) : key;
                                 if (page >= 0 && page < p.num_pages)
                                     add_odd(x, p.v + (((size_t)page * p.Hkv + u.g) * p.page_size + in) * D + col);
                             }
                     }
+                    if (!any)
 #pragma unroll
-                    for (int half = 0; half < 2; ++half) {
+                        for (int i = 0; i < 32; ++i) x[i] = 0.f;
+                    if (whole) {
+                        uint4 pk[4];
+#pragma unroll
+                        for (int g = 0; g < 4; ++g)
+                            pk[g] = make_uint4(pack_bf16x2(x[8 * g], x[8 * g + 1]), pack_bf16x2(x[8 * g + 2], x[8 * g + 3]),
+                                               pack_bf16x2(x[8 * g + 4], x[8 * g + 5]), pack_bf16x2(x[8 * g + 6], x[8 * g + 7]));
                         __syncwarp();
 #pragma unroll
-                        for (int g = 0; g < 4; ++g) {
-                            const float *y = x + half * 16 + g * 4;
-                            *reinterpret_cast<float4 *>(turn + lane * kTurnStride + g * 4) =
-                                any ? make_float4(y[0], y[1], y[2], y[3]) : make_float4(0.f, 0.f, 0.f, 0.f);
-                        }
+                        for (int g = 0; g < 4; ++g) *reinterpret_cast<uint4 *>(turn + lane * kTurnStride + g * 4) = pk[g];
                         __syncwarp();
-                        const int to = col + half * 16 + (lane & 3) * 4;
 #pragma unroll
-                        for (int k = 0; k < 4; ++k) {
-                            const float4 v =
-                                *reinterpret_cast<const float4 *>(turn + (8 * k + (lane >> 2)) * kTurnStride + (lane & 3) * 4);
-                            if (first + 8 * k >= limit) continue;
-                            if (whole)
-                                *reinterpret_cast<uint2 *>(p.o + (out_row + first + 8 * k) * D + to) =
-                                    make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
-                            else
-                                *reinterpret_cast<float4 *>(p.part_o + (part_row + first + 8 * k) * D + to) = v;
+                        for (int k = 0; k < 4; ++k)
+                            if (first + 8 * k < limit)
+                                *reinterpret_cast<uint4 *>(p.o + (out_row + first + 8 * k) * D + col + (lane & 3) * 8) =
+                                    *reinterpret_cast<const uint4 *>(turn + (8 * k + (lane >> 2)) * kTurnStride + (lane & 3) * 4);
+                    } else {
+#pragma unroll
+                        for (int half = 0; half < 2; ++half) {
+                            __syncwarp();
+#pragma unroll
+                            for (int g = 0; g < 4; ++g) {
+                                const float *y = x + half * 16 + g * 4;
+                                *reinterpret_cast<float4 *>(turn + lane * kTurnStride + g * 4) = make_float4(y[0], y[1], y[2], y[3]);
+                            }
+                            __syncwarp();
+#pragma unroll
+                            for (int k = 0; k < 4; ++k)
+                                if (first + 8 * k < limit)
+                                    *reinterpret_cast<float4 *>(p.part_o + (part_row + first + 8 * k) * D + col + half * 16 + (lane & 3) * 4) =
+                                        *reinterpret_cast<const float4 *>(turn + (8 * k + (lane >> 2)) * kTurnStride + (lane & 3) * 4);
                         }
                     }
                 }
