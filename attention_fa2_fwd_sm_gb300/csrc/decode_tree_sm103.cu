@@ -54,6 +54,27 @@ static __device__ int g_tree_status;
 
 namespace dtree {
 
+// mbar_wait_warp in fewer instructions: the waits are many, and a unit of few blocks
+// runs most of the kernel's code once, out of a cold instruction cache.  The clock is
+// read every 16th time around.
+__device__ __forceinline__ bool wait_warp(uint32_t bar, uint32_t parity, uint64_t limit_ns, volatile int *abort) {
+    if (__all_sync(0xffffffffu, mbar_test_wait(bar, parity))) return true;
+    uint64_t t0 = 0;
+    for (uint32_t it = 1; limit_ns > 0; ++it) {
+        if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+        if (it & 15u) continue;
+        const uint64_t now = global_timer_ns();
+        if (t0 == 0) t0 = now;
+        if (__any_sync(0xffffffffu, *abort != 0 || now - t0 > limit_ns)) break;
+    }
+    if ((threadIdx.x & 31) == 0) {
+        *abort = 1;
+        atomicOr(&g_tree_status, kStatusTimeout);
+    }
+    __syncwarp();
+    return false;
+}
+
 constexpr int kTileM = 128;  // rows of a tile
 constexpr int kThreads = 384;
 // As in fwd_kernel.cuh: 384 threads x 168 registers at launch are shared out anew.
@@ -132,70 +153,57 @@ __device__ __forceinline__ int blocks_of(int keys) {
     return (keys + kBlock - 1) / kBlock;
 }
 
-// The lengths of 256 sequences from `first` on, eight a lane.
-constexpr int kRound = 8;
-struct Lengths {
-    int len[kRound], tb[kRound];
-    __device__ __forceinline__ void load(const Params &p, int first) {
-#pragma unroll
-        for (int k = 0; k < kRound; ++k) {
-            const int i = first + 32 * k + int(threadIdx.x & 31);
-            len[k] = tb[k] = 0;
-            if (i < p.B) load_sequence(p, i, len[k], tb[k]);
-        }
-    }
-};
-
-// Blocks of all pairs (all lanes of the calling warp); leaves the first 256 lengths in l.  The host bounds the sum, and
-// all places in it, below 2^31.
+// Blocks of all pairs (all lanes of the calling warp).  The host bounds the sum, and all places in it, below 2^31.
 template <int kBlock>
-__device__ __forceinline__ unsigned all_blocks(const Params &p, Lengths &l) {
+__device__ __forceinline__ unsigned all_blocks(const Params &p) {
     unsigned n = 0;
-    for (int first = (p.B - 1) / (32 * kRound) * (32 * kRound); first >= 0; first -= 32 * kRound) {
-        l.load(p, first);
-#pragma unroll
-        for (int k = 0; k < kRound; ++k) n += blocks_of<kBlock>(keys_of(p, l.len[k], l.tb[k]));
+#pragma unroll 4
+    for (int b = threadIdx.x & 31; b < p.B; b += 32) {
+        int len, tb;
+        load_sequence(p, b, len, tb);
+        n += blocks_of<kBlock>(keys_of(p, len, tb));
     }
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) n += __shfl_xor_sync(0xffffffffu, n, off);
     return n * p.Hkv;
 }
 
-// The pair of block x, and which of its blocks x is (j0); all lanes of the calling warp.
+// The pair of block x, and which of its blocks x is (j0); all lanes of the calling warp.  (The lengths are in the L1
+// by now.)
 template <int kBlock>
-__device__ __forceinline__ Unit find_block(const Params &p, Lengths &l, unsigned x) {
+__device__ __forceinline__ Unit find_block(const Params &p, unsigned x) {
     const int lane = threadIdx.x & 31;
     Unit u = {};
     unsigned before = 0;
-    for (int first = 0; first < p.B; first += 32 * kRound) {
-        if (first > 0) l.load(p, first);
-#pragma unroll
-        for (int k = 0; k < kRound; ++k) {
-            if (first + 32 * k >= p.B) break;
-            const int keys = keys_of(p, l.len[k], l.tb[k]);
-            const unsigned n = unsigned(blocks_of<kBlock>(keys)) * p.Hkv;
-            unsigned upto = n;
-#pragma unroll
-            for (int off = 1; off < 32; off <<= 1) {
-                const unsigned y = __shfl_up_sync(0xffffffffu, upto, off);
-                if (lane >= off) upto += y;
-            }
-            const unsigned base = before + upto - n;
-            const uint32_t hit = __ballot_sync(0xffffffffu, x >= base && x < base + n);
-            if (hit) {
-                const int src = __ffs(hit) - 1;
-                u.b = first + 32 * k + src;
-                u.len = __shfl_sync(0xffffffffu, l.len[k], src);
-                u.tb = __shfl_sync(0xffffffffu, l.tb[k], src);
-                u.keys = __shfl_sync(0xffffffffu, keys, src);
-                u.nb = blocks_of<kBlock>(u.keys);
-                const unsigned rem = x - __shfl_sync(0xffffffffu, base, src);
-                u.g = int(rem / unsigned(u.nb));
-                u.j0 = int(rem - unsigned(u.g) * unsigned(u.nb));
-                return u;
-            }
-            before += __shfl_sync(0xffffffffu, upto, 31);
+#pragma unroll 1
+    for (int first = 0; first < p.B; first += 32) {
+        int len = 0, tb = 0, keys = 0;
+        if (first + lane < p.B) {
+            load_sequence(p, first + lane, len, tb);
+            keys = keys_of(p, len, tb);
         }
+        const unsigned n = unsigned(blocks_of<kBlock>(keys)) * p.Hkv;
+        unsigned upto = n;
+#pragma unroll
+        for (int off = 1; off < 32; off <<= 1) {
+            const unsigned y = __shfl_up_sync(0xffffffffu, upto, off);
+            if (lane >= off) upto += y;
+        }
+        const unsigned base = before + upto - n;
+        const uint32_t hit = __ballot_sync(0xffffffffu, x >= base && x < base + n);
+        if (hit) {
+            const int src = __ffs(hit) - 1;
+            u.b = first + src;
+            u.len = __shfl_sync(0xffffffffu, len, src);
+            u.tb = __shfl_sync(0xffffffffu, tb, src);
+            u.keys = __shfl_sync(0xffffffffu, keys, src);
+            u.nb = blocks_of<kBlock>(u.keys);
+            const unsigned rem = x - __shfl_sync(0xffffffffu, base, src);
+            u.g = int(rem / unsigned(u.nb));
+            u.j0 = int(rem - unsigned(u.g) * unsigned(u.nb));
+            return u;
+        }
+        before += __shfl_sync(0xffffffffu, upto, 31);
     }
     return u;
 }
@@ -243,12 +251,12 @@ __device__ __forceinline__ void clean_rows(uint8_t *v, int warp, int first, int 
     }
 }
 
-// x += the elements of 32 columns of V that are not finite.
-__device__ __forceinline__ void add_odd(float (&x)[32], const __nv_bfloat16 *v) {
-#pragma unroll
-    for (int i = 0; i < 32; ++i) {
+// Adds to n columns of a stored row the elements of V that are not finite.
+template <typename T>
+__device__ __noinline__ void add_odd(T *to, const __nv_bfloat16 *v, int n) {
+    for (int i = 0; i < n; ++i) {
         const float y = __bfloat162float(v[i]);
-        if (!isfinite(y)) x[i] += y;
+        if (!isfinite(y)) to[i] = T(float(to[i]) + y);
     }
 }
 
@@ -311,17 +319,16 @@ __global__ void __launch_bounds__(kThreads, 1)
     Unit u = {};
     int left = 0;
     if (warp == 2 || warp == 3) {
-        Lengths l;
-        const unsigned total = all_blocks<kBlock>(p, l), S = (total + p.shares - 1) / p.shares, lo = share * S;
+        const unsigned total = all_blocks<kBlock>(p), S = (total + p.shares - 1) / p.shares, lo = share * S;
         left = int(lo < total ? min(S, total - lo) : 0);
         if (warp == 3) {
-            if (left > 0) u = find_block<kBlock>(p, l, lo);
+            if (left > 0) u = find_block<kBlock>(p, lo);
         } else if (m == 0) {
             // Where the merge finds the pair that goes on behind this share: from the lengths alone, so that a launch
             // whose waits run out leaves the merge wrong numbers but no wrong addresses.
             int4 cut = make_int4(0, 0, 0, 0);
             if (left > 0) {
-                const Unit at = find_block<kBlock>(p, l, lo + left - 1);
+                const Unit at = find_block<kBlock>(p, lo + left - 1);
                 const int rest = at.nb - at.j0 - 1;
                 if (at.j0 < left && rest > 0) cut = make_int4(at.b, at.g, 1 + int((rest + S - 1) / S), at.tb);
             }
@@ -343,8 +350,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             uint32_t q_loads = 0;  // per tile (both are loaded for every unit that has them)
             bool ok = true;
             u.holes = p.table != nullptr;  // (the first unit's entries are looked at block by block)
-            for (long long qi = 0; ok; ++qi) {
-                const int qs = int(qi & 1);
+            for (uint32_t qi = 0; ok; ++qi) {
+                const uint32_t qs = qi & 1;
                 u.n = left > 0 ? min(left, u.nb - u.j0) : 0;
                 if (p.table && qi > 0) {
                     // Ahead of the other warps: whether the unit needs looking at all.
@@ -357,7 +364,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                     u.holes = __any_sync(0xffffffffu, hole);
                 }
-                if (qi >= 2) ok = mbar_wait_warp(bar(C::kUEmpty + qs), uint32_t(((qi >> 1) - 1) & 1), p.wait_ns, abort_flag, status);
+                if (qi >= 2) ok = wait_warp(bar(C::kUEmpty + qs), ((qi >> 1) - 1) & 1, p.wait_ns, abort_flag);
                 if (!ok) break;
                 if (lane == 0) {
                     u.put(units + kUnitInts * qs);
@@ -366,7 +373,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 __syncwarp();
                 if (u.n == 0) break;
                 for (int t = 0; t < (second ? 2 : 1); ++t) {
-                    if (q_loads > 0) ok = mbar_wait_warp(bar(C::kQEmpty + t), (q_loads - 1) & 1, p.wait_ns, abort_flag, status);
+                    if (q_loads > 0) ok = wait_warp(bar(C::kQEmpty + t), (q_loads - 1) & 1, p.wait_ns, abort_flag);
                     if (!ok) break;
                     if (lane == 0) {
                         mbar_arrive_expect_tx(bar(C::kQFull + t), C::kQBytes);
@@ -406,9 +413,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             bool ok = true;
             const int boxes = p.table && p.page_size < kBlock ? kBlock / p.page_size : 1;
             const int box_bytes = C::kChunkBytes / boxes;
-            for (long long qi = 0; ok; ++qi) {
-                const int qs = int(qi & 1);
-                ok = mbar_wait_warp(bar(C::kUFull + qs), uint32_t((qi >> 1) & 1), p.wait_ns, abort_flag, status);
+            for (uint32_t qi = 0; ok; ++qi) {
+                const uint32_t qs = qi & 1;
+                ok = wait_warp(bar(C::kUFull + qs), (qi >> 1) & 1, p.wait_ns, abort_flag);
                 if (!ok) break;
                 u.get(units + kUnitInts * qs);
                 __syncwarp();
@@ -422,7 +429,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 int cur = entry(base + lane), nxt = entry(base + 32 + lane);
                 for (int j = 0; j < u.n; ++j) {
                     const uint32_t fill = 2 * blocks + kv, slot = fill % C::kStages, round = fill / C::kStages;
-                    if (round > 0) ok = mbar_wait_warp(bar(C::kKVEmpty + slot), (round - 1) & 1, p.wait_ns, abort_flag, status);
+                    if (round > 0) ok = wait_warp(bar(C::kKVEmpty + slot), (round - 1) & 1, p.wait_ns, abort_flag);
                     if (!ok) break;
                     const uint32_t fb = bar(C::kKVFull + slot), to = smem_u32(sKV + slot * C::kKVBytes);
                     if (lane == 0) mbar_arrive_expect_tx(fb, C::kKVBytes);
@@ -477,7 +484,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             bool ok = true;
             const int chains = second ? 2 : 1;  // (kRows)
             auto wait_slot = [&](uint32_t f) {
-                return mbar_wait_warp(bar(C::kKVFull + f % C::kStages), (f / C::kStages) & 1, p.wait_ns, abort_flag, status);
+                return wait_warp(bar(C::kKVFull + f % C::kStages), (f / C::kStages) & 1, p.wait_ns, abort_flag);
             };
             const uint64_t dQ = smem_desc_sw128(smem_u32(sQ), 16, 1024);
             const uint64_t dK = smem_desc_sw128(smem_u32(sKV), 16, 1024);
@@ -511,18 +518,18 @@ __global__ void __launch_bounds__(kThreads, 1)
                     tc_mma_ts_x4_elect(tmem_base + C::kOCol + t * D, a, b, kIdescPV, (acc || g > 0) ? 1u : 0u);
                 }
             };
-            for (long long qi = 0; ok; ++qi) {
-                const int qs = int(qi & 1);
-                ok = mbar_wait_warp(bar(C::kUFull + qs), uint32_t((qi >> 1) & 1), p.wait_ns, abort_flag, status);
+            for (uint32_t qi = 0; ok; ++qi) {
+                const uint32_t qs = qi & 1;
+                ok = wait_warp(bar(C::kUFull + qs), (qi >> 1) & 1, p.wait_ns, abort_flag);
                 if (!ok) break;
                 const int n = __shfl_sync(0xffffffffu, int(units[kUnitInts * qs + 3]), 0);
                 mbar_arrive_elect(bar(C::kUEmpty + qs));
                 if (n == 0) break;
                 const uint32_t f0 = fills;  // K_j at f0 + 2 j, V_j behind it
                 // The first product of each chain and buffer.
-                ok = mbar_wait_warp(bar(C::kQFull), q_used & 1, p.wait_ns, abort_flag, status);
-                if (ok && !kKeys && second) ok = mbar_wait_warp(bar(C::kQFull + 1), q_used & 1, p.wait_ns, abort_flag, status);
-#pragma unroll
+                ok = wait_warp(bar(C::kQFull), q_used & 1, p.wait_ns, abort_flag);
+                if (ok && !kKeys && second) ok = wait_warp(bar(C::kQFull + 1), q_used & 1, p.wait_ns, abort_flag);
+#pragma unroll 1
                 for (int i = 0; i < (kKeys ? 4 : 2); ++i) {
                     const int j = kKeys ? i : 0, t = i & 1, buf = kKeys ? i >> 1 : 0;
                     if (!ok || j >= n || (!kKeys && t >= chains)) break;
@@ -537,16 +544,16 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int j = 0; ok && j < n; ++j) {
                     const uint32_t fV = f0 + 2 * j + 1;
                     bool v_ready = false;
-#pragma unroll
+#pragma unroll 1
                     for (int i = 0; i < (kKeys ? 1 : 2); ++i) {
                         const int t = kKeys ? j & 1 : i, buf = kKeys ? j >> 1 & 1 : 0, tb = 2 * t + buf;
                         if (!kKeys && i >= chains) break;
-                        ok = mbar_wait_warp(bar(C::kPFull + tb), p_odd >> tb & 1, p.wait_ns, abort_flag, status);
+                        ok = wait_warp(bar(C::kPFull + tb), p_odd >> tb & 1, p.wait_ns, abort_flag);
                         if (!ok) break;
                         p_odd ^= 1u << tb;
                         const bool first = kKeys ? j < 2 : j == 0;
                         if (first && (used >> t & 1)) {
-                            ok = mbar_wait_warp(bar(C::kOEmpty + t), ~(o_odd >> t) & 1, p.wait_ns, abort_flag, status);
+                            ok = wait_warp(bar(C::kOEmpty + t), ~(o_odd >> t) & 1, p.wait_ns, abort_flag);
                             if (!ok) break;
                         }
                         if (!v_ready) {
@@ -575,7 +582,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 fills = f0 + 2 * n;
             }
             tc_commit_elect(bar(C::kDrain));
-            if (!mbar_wait_warp(bar(C::kDrain), 0, drain_ns, &no_abort, status) && lane == 0)
+            if (!wait_warp(bar(C::kDrain), 0, drain_ns, &no_abort) && lane == 0)
                 atomicOr(status, kStatusDrainTimeout);
             __syncwarp();
         }
@@ -597,9 +604,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         uint32_t s_odd = 0, o_waits = 0, o_waits1 = 0;  // s_odd: a bit a buffer
         uint32_t kv_base = 0;
         bool ok = true;
-        for (long long qi = 0; ok; ++qi) {
-            const int qs = int(qi & 1);
-            ok = mbar_wait_warp(bar(C::kUFull + qs), uint32_t((qi >> 1) & 1), p.wait_ns, abort_flag, status);
+        for (uint32_t qi = 0; ok; ++qi) {
+            const uint32_t qs = qi & 1;
+            ok = wait_warp(bar(C::kUFull + qs), (qi >> 1) & 1, p.wait_ns, abort_flag);
             if (!ok) break;
             u.get(units + kUnitInts * qs);
             __syncwarp();
@@ -646,7 +653,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 const int buf = kKeys ? j >> 1 & 1 : 0;
                 const uint32_t tS = tS0 + buf * kBlock;
-                ok = mbar_wait_warp(bar(C::kSFull + 2 * t + buf), s_odd >> buf & 1, p.wait_ns, abort_flag, status);
+                ok = wait_warp(bar(C::kSFull + 2 * t + buf), s_odd >> buf & 1, p.wait_ns, abort_flag);
                 if (!ok) break;
                 s_odd ^= 1u << buf;
                 // S complete: so are all products before it, and K's slot is free once the last chain to use it says so.
@@ -712,36 +719,38 @@ __global__ void __launch_bounds__(kThreads, 1)
                     };
                     // The reference maximum is exact for the first block that shows the row a key, and kept while the
                     // exponentials cannot overflow (their sum below 2^60); see fwd_kernel.cuh.
-                    float corr = 1.f;
-                    if (m_run == -INFINITY) m_run = block_max() * sl2;
-                    float l_blk = exp_block(m_run == -INFINITY ? 0.f : -m_run);
-                    if (__any_sync(0xffffffffu, !(l_blk < 0x1p60f))) {
-                        const float m_new = fmaxf(m_run, block_max() * sl2);
-                        if (m_new > m_run) {
-                            corr = fast_exp2(m_run - m_new);
+                    float corr = 1.f, l_blk;
+                    bool again = false, twice = false;
+                    do {
+                        if (m_run == -INFINITY || again) {
+                            const float m_new = fmaxf(m_run, block_max() * sl2);
+                            if (again && m_new > m_run) corr = fast_exp2(m_run - m_new);
                             m_run = m_new;
                         }
-                        tmem_wait_st();
                         l_blk = exp_block(m_run == -INFINITY ? 0.f : -m_run);
-                        if (j > jt && __any_sync(0xffffffffu, corr != 1.f)) {
-                            if constexpr (kKeys) {
-                                // S(j) was issued ahead of the chain's last product into O: wait for that (its V slot, which
-                                // nobody can have filled and freed again before this block's P).
-                                const uint32_t f = f0 + 2 * (j - kStep) + 1;
-                                ok = mbar_wait_warp(bar(C::kKVEmpty + f % C::kStages), (f / C::kStages) & 1, p.wait_ns, abort_flag,
-                                                    status);
-                                if (!ok) break;
-                                tc_fence_after();
-                            }
+                        again = !again && __any_sync(0xffffffffu, !(l_blk < 0x1p60f));
+                        if (again) {
+                            tmem_wait_st();
+                            twice = true;
+                        }
+                    } while (again);
+                    if (twice && j > jt && __any_sync(0xffffffffu, corr != 1.f)) {
+                        if constexpr (kKeys) {
+                            // S(j) was issued ahead of the chain's last product into O: wait for that (its V slot, which
+                            // nobody can have filled and freed again before this block's P).
+                            const uint32_t f = f0 + 2 * (j - kStep) + 1;
+                            ok = wait_warp(bar(C::kKVEmpty + f % C::kStages), (f / C::kStages) & 1, p.wait_ns, abort_flag);
+                            if (!ok) break;
+                            tc_fence_after();
+                        }
+#pragma unroll 1
+                        for (int c = 0; c < D / 32; ++c) {
+                            uint32_t ov[32];
+                            tmem_ld32(tO + t * D + c * 32, ov);
+                            tmem_wait_ld();
 #pragma unroll
-                            for (int c = 0; c < D / 32; ++c) {
-                                uint32_t ov[32];
-                                tmem_ld32(tO + t * D + c * 32, ov);
-                                tmem_wait_ld();
-#pragma unroll
-                                for (int i = 0; i < 32; ++i) ov[i] = __float_as_uint(__uint_as_float(ov[i]) * corr);
-                                tmem_st32(tO + t * D + c * 32, ov);
-                            }
+                            for (int i = 0; i < 32; ++i) ov[i] = __float_as_uint(__uint_as_float(ov[i]) * corr);
+                            tmem_st32(tO + t * D + c * 32, ov);
                         }
                     }
                     l_run = l_run * corr + l_blk;
@@ -751,7 +760,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if ((u.j0 + j + 1) * kBlock > u.len && (kKeys || t == 0)) {
                     // (the other chain's product of this block is issued behind this one's)
                     const uint32_t fV = f0 + 2 * j + 1, slot = fV % C::kStages;
-                    ok = mbar_wait_warp(bar(C::kKVFull + slot), (fV / C::kStages) & 1, p.wait_ns, abort_flag, status);
+                    ok = wait_warp(bar(C::kKVFull + slot), (fV / C::kStages) & 1, p.wait_ns, abort_flag);
                     if (!ok) break;
                     const int kv0 = (u.j0 + j) * kBlock, at = max(u.len - kv0, 0);
                     clean_rows<C::kChunks, kBlock>(sKV + slot * C::kKVBytes, quarter, at, u.keys - kv0, kv0 + at - u.len,
@@ -774,9 +783,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                 mine[t * kTileM + r] = make_float2(m_run, l_run);
                 __syncwarp();
                 mbar_arrive_elect(bar(C::kStateFull));
-                ok = mbar_wait_warp(bar(C::kStateFull), uint32_t(qi & 1), p.wait_ns, abort_flag, status);
-                if (ok) ok = mbar_wait_warp(bar(C::kOFull), o_waits & 1, p.wait_ns, abort_flag, status);
-                if (ok && has1) ok = mbar_wait_warp(bar(C::kOFull + 1), o_waits1 & 1, p.wait_ns, abort_flag, status);
+                ok = wait_warp(bar(C::kStateFull), qi & 1, p.wait_ns, abort_flag);
+                if (ok) ok = wait_warp(bar(C::kOFull), o_waits & 1, p.wait_ns, abort_flag);
+                if (ok && has1) ok = wait_warp(bar(C::kOFull + 1), o_waits1 & 1, p.wait_ns, abort_flag);
                 if (!ok) break;
                 ++o_waits;
                 if (has1) ++o_waits1;
@@ -789,7 +798,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 f[0] /= sum;
                 f[1] /= sum;
             } else {
-                ok = mbar_wait_warp(bar(C::kOFull + t), o_waits & 1, p.wait_ns, abort_flag, status);
+                ok = wait_warp(bar(C::kOFull + t), o_waits & 1, p.wait_ns, abort_flag);
                 if (!ok) break;
                 ++o_waits;
                 sum = l_run;
@@ -797,13 +806,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 L = m_run + __log2f(sum);
             }
             tc_fence_after();
-            uint32_t odd[kMaskWords], any_odd = 0;
-#pragma unroll
-            for (int w = 0; w < kMaskWords; ++w) {
-                odd[w] = odd_rows[(qi & 3) * kMaskWords + w];
-                any_odd |= odd[w];
-                odd[w] &= live ? seen[w] : 0u;
-            }
+            const uint32_t *odd = odd_rows + (qi & 3) * kMaskWords;
+            const bool any_odd = __any_sync(0xffffffffu, lane < kMaskWords && odd[lane & 7] != 0);
             if (t == 0 && quarter == 0 && lane < kMaskWords) odd_rows[((qi + 2) & 3) * kMaskWords + lane] = 0;
             if (has_rows) {
                 const bool any = live && sum != 0.f;  // (NaN stays NaN)
@@ -812,7 +816,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int first = quarter * 32 + (lane >> 2);
                 constexpr int kCols = kKeys ? D / 2 : D;  // of this warp
                 const int col0 = kKeys ? t * kCols : 0;
-#pragma unroll
+#pragma unroll 1
                 for (int c = 0; c < kCols / 32; ++c) {
                     const int col = col0 + c * 32;
                     uint32_t ov[32], ow[32];
@@ -825,17 +829,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (has1)
 #pragma unroll
                         for (int i = 0; i < 32; ++i) x[i] += __uint_as_float(ow[i]) * f[1];
-                    if (any_odd) {
-#pragma unroll
-                        for (int w = 0; w < kMaskWords; ++w)
-                            for (uint32_t bits = odd[w]; bits; bits &= bits - 1) {
-                                const int key = u.len + 32 * w + __ffs(bits) - 1;
-                                const int page = p.table ? p.table[(size_t)u.b * p.max_pages + (key >> p.shift)] : u.b;
-                                const int in = p.table ? key & (p.page_size - 1) : key;
-                                if (page >= 0 && page < p.num_pages)
-                                    add_odd(x, p.v + (((size_t)page * p.Hkv + u.g) * p.page_size + in) * D + col);
-                            }
-                    }
                     if (!any)
 #pragma unroll
                         for (int i = 0; i < 32; ++i) x[i] = 0.f;
@@ -871,6 +864,19 @@ __global__ void __launch_bounds__(kThreads, 1)
                                         *reinterpret_cast<const float4 *>(turn + (8 * k + (lane >> 2)) * kTurnStride + (lane & 3) * 4);
                         }
                     }
+                }
+                if (any_odd) {
+                    __syncwarp();  // behind the warp's stores
+#pragma unroll 1
+                    for (int w = 0; w < kMaskWords; ++w)
+                        for (uint32_t bits = any ? odd[w] & mask_bits(seen, 32 * w) : 0u; bits; bits &= bits - 1) {
+                            const int key = u.len + 32 * w + __ffs(bits) - 1;
+                            const int page = p.table ? p.table[(size_t)u.b * p.max_pages + (key >> p.shift)] : u.b;
+                            const int in = p.table ? key & (p.page_size - 1) : key;
+                            const __nv_bfloat16 *v = p.v + (((size_t)page * p.Hkv + u.g) * p.page_size + in) * D + col0;
+                            if (whole) add_odd(p.o + (out_row + r) * D + col0, v, kCols);
+                            else add_odd(p.part_o + (part_row + r) * D + col0, v, kCols);
+                        }
                 }
                 if ((!kKeys || t == 0) && r < limit) {
                     if (!whole) p.part_lse[part_row + r] = any ? L : -INFINITY;
