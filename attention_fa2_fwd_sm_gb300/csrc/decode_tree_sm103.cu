@@ -7,33 +7,33 @@
 //     s = scale q k^T  (-inf where the mask hides the key),  o = softmax(s) v.
 // The keys are read once for all rows.  With R = G T rows a key costs 4 d bytes and
 // 4 d R flops: below some 280 rows HBM bounds it, above that the tensor cores.  So
-// S = Q K^T and P V are tcgen05 products of 128 rows and 128 keys whatever R is;
-// a tile of few rows is idle for the most part, but still faster than HBM.
+// S = Q K^T and P V are tcgen05 products of 128 rows whatever R is; a tile of few rows
+// is idle for the most part, but still faster than HBM.
 //
-// A CTA an SM, persistent, as in fwd_kernel.cuh: a TMA warp, an issuing warp, and
-// two chains of four softmax warps, whose products and exponentials overlap.
-//   kRows (R > 128): the chains hold two tiles of rows, and both visit every key
-//     block; units of 256 rows, `mt` units a KV head, side by side on mt SMs so
-//     that all but one find the keys in L2.
-//   kKeys (R <= 128): one tile; the chains take turns with the key blocks (of 64
-//     keys), each with two score buffers, so that the products' latency is not in a
-//     chain's way; their softmax states are merged in the epilogue, where each of
-//     them adds up half of the columns from both accumulators.
+// A CTA an SM, persistent: warps that load, issue MMAs and plan, and two chains of
+// four softmax warps, as in fwd_kernel.cuh.
+//   pairs_kernel (R <= 128): each chain is a pipeline of its own, with a loading and
+//     an issuing warp, a ring of 64-key blocks, and two score buffers, so that the
+//     products' latency is not in its way.  The chains work on different keys; when
+//     one starts or ends a pair, the other one keeps the memory busy.
+//   rows_kernel (R > 128): the chains hold two tiles of rows, and both visit every
+//     block of 128 keys in the ring; units of 256 rows, `mt` units a KV head, side by
+//     side on mt SMs so that all but one find the keys in L2.
 // The blocks of all (sequence, KV head) pairs, in that order, are cut into equal
-// shares, one a CTA (group of mt): nothing depends on how ragged the lengths are.  A
-// pair that lies in one share is written out at once; one that is cut goes through
-// partials: share s writes its first segment's to slot 2 s (a pair that began
-// before) and its last one's to 2 s + 1 (a pair that goes on), and merge_kernel adds
-// up slot 2 s + 1, 2 (s + 1), 2 (s + 2), ...
+// shares, one a chain or a group of mt CTAs: nothing depends on how ragged the
+// lengths are.  A pair that lies in one share is written out at once; one that is cut
+// goes through partials: share s writes its first segment's to slot 2 s (a pair
+// that began before) and its last one's to 2 s + 1 (a pair that goes on), and
+// merge_kernel adds up slot 2 s + 1, 2 (s + 1), 2 (s + 2), ...
 //
-// Pages: a block of 128 keys is 128 / page_size boxes, each from the page that the
-// table names; a box on no page is filled with zeros by coordinates past the end.
-// Columns past the last key, on no page, or hidden by the mask become -inf before the
-// softmax.  A probability of 0 does not hide a V of infinity or NaN from the product,
-// so the softmax warps clean the blocks that hold drafted keys before they hand P
-// over: rows behind the last key, which may hold anything, become zeros, and so do
-// elements of drafted rows that are not finite, which the epilogue then adds to the
-// rows that see them.
+// Pages: a block of keys is one box, or several where pages are smaller, each from
+// the page that the table names; a box on no page is filled with zeros by coordinates
+// past the end.  Columns past the last key, on no page, or hidden by the mask become
+// -inf before the softmax.  A probability of 0 does not hide a V of infinity or NaN
+// from the product, so the softmax warps clean the blocks that hold drafted keys
+// before they hand P over: rows behind the last key, which may hold anything, become
+// zeros, and so do elements of drafted rows that are not finite, which the epilogue
+// then adds to the rows that see them.
 //
 // Precision: scores, maxima, sums, partials in fp32; probabilities are rounded to
 // bf16 for the product with V, because the instruction takes both operands in one
@@ -83,36 +83,10 @@ static_assert(128 * kCtrlRegs + 256 * kSoftmaxRegs <= kThreads * kLaunchRegs, "r
 constexpr int kTmemCols = 512;
 constexpr int kTurnStride = 20, kTurnFloats = 32 * kTurnStride;
 constexpr int kMaskWords = 8;  // 32-bit words of a row's mask: 256 drafted tokens
-constexpr int kMergeWarps = 4;
-
 constexpr int kUnitInts = 12;  // of a unit in the queue
-
-// Keys of a block.  Where the chains take turns, HBM is what they wait for, and small
-// blocks hold less of the ring while they are worked on.
-constexpr int block_keys(bool keys) { return keys ? 64 : 128; }
-
-template <int D, bool kKeys>
-struct Cfg {
-    static constexpr int kBlock = block_keys(kKeys);
-    static constexpr int kChunks = D / 64, kQChunkBytes = kTileM * 128, kChunkBytes = kBlock * 128;
-    static constexpr int kQTiles = kKeys ? 1 : 2;
-    static constexpr int kQBytes = kTileM * D * 2, kKVBytes = kBlock * D * 2;
-    static constexpr int kStages = (D == 128 ? 1 : 2) * (kKeys ? 10 : 4);
-    static constexpr int kOCol = 2 * kTileM;
-    static constexpr int kDataBytes = kQTiles * kQBytes + kStages * kKVBytes;
-    static constexpr int kTurnOffset = kDataBytes, kStateOffset = kTurnOffset + 8 * kTurnFloats * 4;
-    static constexpr int kOddOffset = kStateOffset + (kKeys ? 2 * 2 * kTileM * 8 : 0);
-    static constexpr int kBarOffset = kOddOffset + 4 * kMaskWords * 4;
-    // barriers
-    // (S and P: [chain][buffer])
-    static constexpr int kBuffers = kKeys ? 2 : 1;
-    static constexpr int kQFull = 0, kQEmpty = 2, kSFull = 4, kPFull = 8, kOFull = 12, kOEmpty = 14, kStateFull = 16,
-                         kDrain = 17, kUFull = 18, kUEmpty = 20, kKVFull = 22, kKVEmpty = 22 + kStages,
-                         kNumBars = 22 + 2 * kStages;
-    static constexpr int kUnitOffset = (kBarOffset + kNumBars * 8 + 15) / 16 * 16;
-    static constexpr int kSmemBytes = kUnitOffset + 2 * kUnitInts * 4 + 16 + 1024;  // units, tmem, abort; alignment
-    static_assert(kSmemBytes <= 227 * 1024, "shared memory");
-};
+constexpr int kMergeWarps = 4;
+constexpr uint64_t kDrainNs = 1000000000ull;  // for copies and products in flight when a CTA gives up
+constexpr int kSmemMax = 227 * 1024;
 
 struct Params {
     const int *seqlens, *draft_lens, *table;
@@ -122,9 +96,10 @@ struct Params {
     float *lse;                // natural log, or null
     float *part_o, *part_lse;  // [2 shares][rows][D], [2 shares][rows] (log2 units)
     int4 *cuts;                // [shares]: {b, g, partials, drafted tokens} of the pair that goes on behind a share
-    int B, Hkv, G, T, rows;
+    int B, Hkv, T, rows;
     int num_pages, page_size, shift, cap, max_pages;
     int mt, shares;
+    int q_rows, stages;  // pairs_kernel: rows of Q in shared memory, blocks of a chain's ring
     float scale_log2;
     unsigned long long wait_ns;
 };
@@ -208,6 +183,122 @@ __device__ __forceinline__ Unit find_block(const Params &p, unsigned x) {
     return u;
 }
 
+// A share [lo, lo + left) of the blocks, S in a full one.
+struct Share {
+    unsigned lo, S;
+    int left;
+};
+template <int kBlock>
+__device__ __forceinline__ Share share_of(const Params &p, int share) {
+    const unsigned total = all_blocks<kBlock>(p);
+    Share s;
+    s.S = (total + p.shares - 1) / p.shares;
+    s.lo = share * s.S;
+    s.left = s.lo < total ? int(min(s.S, total - s.lo)) : 0;
+    return s;
+}
+
+// Where the merge finds the pair that goes on behind a share: from the lengths alone, so that a launch whose waits run out
+// leaves the merge wrong numbers but no wrong addresses.
+template <int kBlock>
+__device__ __forceinline__ void write_cut(const Params &p, int share, const Share &s) {
+    int4 cut = make_int4(0, 0, 0, 0);
+    if (s.left > 0) {
+        const Unit at = find_block<kBlock>(p, s.lo + s.left - 1);
+        const int rest = at.nb - at.j0 - 1;
+        if (at.j0 < s.left && rest > 0) cut = make_int4(at.b, at.g, 1 + int((rest + s.S - 1) / s.S), at.tb);
+    }
+    if ((threadIdx.x & 31) == 0) p.cuts[share] = cut;
+}
+
+// On to the pair behind; call only while a block is left.
+template <int kBlock>
+__device__ __forceinline__ void next_pair(const Params &p, Unit &u) {
+    u.j0 = 0;
+    if (++u.g < p.Hkv) return;
+    u.g = 0;
+    do {
+        load_sequence(p, ++u.b, u.len, u.tb);
+        u.keys = keys_of(p, u.len, u.tb);
+    } while (u.keys == 0);
+    u.nb = blocks_of<kBlock>(u.keys);
+}
+
+// Whether an entry of the unit's blocks is no page (all lanes of the calling warp).
+template <int kBlock>
+__device__ __forceinline__ bool look_for_holes(const Params &p, const Unit &u) {
+    const int *table = p.table + (size_t)u.b * p.max_pages;
+    const int last = (min(u.keys, (u.j0 + u.n) * kBlock) - 1) >> p.shift;
+    bool hole = false;
+    for (int i = ((u.j0 * kBlock) >> p.shift) + int(threadIdx.x & 31); u.n > 0 && i <= last; i += 32) {
+        const int page = table[i];
+        hole |= page < 0 || page >= p.num_pages;
+    }
+    return __any_sync(0xffffffffu, hole);
+}
+
+// Where a unit's blocks lie: lane i holds entry base + i of its row of the table, and the one 32 behind it.
+template <int kBlock>
+struct Pages {
+    const int *table;
+    int base, used, cur, nxt;
+    __device__ __forceinline__ void start(const Params &p, const Unit &u) {
+        table = p.table ? p.table + (size_t)u.b * p.max_pages : nullptr;
+        used = (u.keys + p.page_size - 1) >> p.shift;
+        base = (u.j0 * kBlock) >> p.shift;
+        cur = entry(base);
+        nxt = entry(base + 32);
+    }
+    __device__ __forceinline__ int entry(int first) const {
+        const int i = first + int(threadIdx.x & 31);
+        return table && i < used ? table[i] : -1;
+    }
+    // The block that starts at `key`, chunk by chunk to `to`; all lanes of the warp, in the blocks' order.
+    template <int kChunks>
+    __device__ __forceinline__ void load(const Params &p, const Unit &u, int key, const CUtensorMap *map, uint32_t full,
+                                         uint32_t to) {
+        constexpr int kChunkBytes = kBlock * 128;
+        const int lane = threadIdx.x & 31;
+        const int none = p.num_pages * p.Hkv;
+        if (!table || p.page_size >= kBlock) {
+            int plane = u.b * p.Hkv + u.g, row = key;
+            if (table) {
+                const int page = take(p, key);
+                plane = page >= 0 && page < p.num_pages ? page * p.Hkv + u.g : none;
+                row = key & (p.page_size - 1);
+            }
+            if (lane == 0)
+#pragma unroll
+                for (int c = 0; c < kChunks; ++c) tma_load_3d(to + c * kChunkBytes, map, full, c * 64, row, plane);
+        } else {
+            const int boxes = kBlock / p.page_size, bytes = p.page_size * 128;
+            take(p, key);
+            const int mine = cur >= 0 && cur < p.num_pages ? cur * p.Hkv + u.g : none;
+            const int at = ((key >> p.shift) - base) & 31;
+#pragma unroll 4
+            for (int i = 0; i < boxes; ++i) {
+                const int plane = __shfl_sync(0xffffffffu, mine, at + i);
+                if (lane == 0)
+#pragma unroll
+                    for (int c = 0; c < kChunks; ++c)
+                        tma_load_3d(to + c * kChunkBytes + i * bytes, map, full, c * 64, 0, plane);
+            }
+        }
+        __syncwarp();
+    }
+
+  private:
+    __device__ __forceinline__ int take(const Params &p, int key) {
+        const int first = key >> p.shift;
+        if (first >= base + 32) {
+            base += 32;
+            cur = nxt;
+            nxt = entry(base + 32);
+        }
+        return __shfl_sync(0xffffffffu, cur, (first - base) & 31);
+    }
+};
+
 // Bits [u, u + 32) of a row's mask; keys before the drafted ones (u < 0) are seen by all.
 __device__ __forceinline__ uint32_t mask_bits(const uint32_t (&m)[kMaskWords], int u) {
     const int i = u >> 5;  // rounds down
@@ -219,6 +310,28 @@ __device__ __forceinline__ uint32_t mask_bits(const uint32_t (&m)[kMaskWords], i
     }
     return __funnelshift_r(lo, hi, u & 31);
 }
+
+// What a row sees of a unit's drafted tokens, 64 a word; loaded ahead, looked at where the blocks end.
+struct Seen {
+    unsigned long long w[kMaskWords / 2];
+    __device__ __forceinline__ void load(const Params &p, const Unit &u, int token, bool want) {
+        const int words = (p.T + 63) / 64;
+        const unsigned long long *row = p.mask && want ? p.mask + ((size_t)u.b * p.T + token) * words : nullptr;
+#pragma unroll
+        for (int i = 0; i < kMaskWords / 2; ++i) w[i] = row && i < words ? row[i] : 0ull;
+    }
+    // As 32-bit words, without keys that do not exist; without a mask, a chain sees what is before it.
+    __device__ __forceinline__ void bits(const Params &p, const Unit &u, int token, bool live, uint32_t (&out)[kMaskWords]) const {
+        const int drafted = u.keys - u.len, end = !live ? 0 : p.mask ? drafted : min(drafted, token + 1);
+#pragma unroll
+        for (int i = 0; i < kMaskWords / 2; ++i) {
+            unsigned long long x = p.mask ? w[i] : ~0ull;
+            if (end < 64 * i + 64) x = end <= 64 * i ? 0ull : x & ((1ull << (end - 64 * i)) - 1);
+            out[2 * i] = uint32_t(x);
+            out[2 * i + 1] = uint32_t(x >> 32);
+        }
+    }
+};
 
 // V rows [first, kBlock) of a block in shared memory, by the four warps of a chain (`warp` of them; the swizzle stays
 // within a row's 128 bytes of a chunk, which eight lanes take): rows from `end` on become zeros; in the drafted rows
@@ -260,43 +373,617 @@ __device__ __noinline__ void add_odd(T *to, const __nv_bfloat16 *v, int n) {
     }
 }
 
-template <int D, bool kKeys>
+// One row's scores of a block, at tS in TMEM, become probabilities in their place.
+template <int kBlock>
+struct Scores {
+    static constexpr int kQuads = kBlock / 32;
+    float s[kBlock];
+    __device__ __forceinline__ void load(uint32_t tS) {
+        uint32_t sr[kQuads][32];
+#pragma unroll
+        for (int c = 0; c < kQuads; ++c) tmem_ld32(tS + c * 32, sr[c]);
+        tmem_wait_ld();
+#pragma unroll
+        for (int c = 0; c < kQuads; ++c)
+#pragma unroll
+            for (int i = 0; i < 32; ++i) s[c * 32 + i] = __uint_as_float(sr[c][i]);
+    }
+    // Keys from `key` on, of which the row sees `seen` from key `len` on; on_page: a bit a page of the block.
+    __device__ __forceinline__ void hide(const Params &p, const uint32_t (&seen)[kMaskWords], int key, int len, bool pages,
+                                         uint32_t on_page) {
+#pragma unroll
+        for (int c = 0; c < kQuads; ++c) {
+            uint32_t bits = mask_bits(seen, key + 32 * c - len);
+            if (pages) {
+                const bool halves = p.page_size == 16;  // two pages in 32 keys
+                const int at = p.page_size < kBlock ? 32 * c / p.page_size : 0;
+                if (!(on_page >> at & 1)) bits &= halves ? 0xffff0000u : 0u;
+                if (halves && !(on_page >> (at + 1) & 1)) bits &= 0x0000ffffu;
+            }
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+                if (!(bits >> i & 1)) s[c * 32 + i] = -INFINITY;
+        }
+    }
+    __device__ __forceinline__ float top() const {
+        float m[kQuads];
+#pragma unroll
+        for (int c = 0; c < kQuads; ++c) {
+            float x = fmax3(s[32 * c], s[32 * c + 1], s[32 * c + 2]);
+#pragma unroll
+            for (int i = 3; i < 31; i += 2) x = fmax3(x, s[32 * c + i], s[32 * c + i + 1]);
+            m[c] = fmaxf(x, s[32 * c + 31]);
+        }
+        if constexpr (kQuads == 2) return fmaxf(m[0], m[1]);
+        else return fmax3(m[0], m[1], fmaxf(m[2], m[3]));
+    }
+    // 2^(s scale - m) in bf16 to tS; their sum.
+    __device__ __forceinline__ float exponentials(uint32_t tS, float sl2, float neg_m) const {
+        float ls[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int c = 0; c < kQuads; ++c) {
+            uint32_t pk[16];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                float x0, x1;
+                ffma2(x0, x1, s[c * 32 + 2 * i], s[c * 32 + 2 * i + 1], sl2, sl2, neg_m, neg_m);
+                const float p0 = fast_exp2(x0), p1 = fast_exp2(x1);
+                const int a = (i & 3) * 2;
+                fadd2(ls[a], ls[a + 1], p0, p1);
+                pk[i] = pack_bf16x2(p0, p1);
+            }
+            tmem_st16(tS + c * 16, pk);
+        }
+        return ((ls[0] + ls[1]) + (ls[2] + ls[3])) + ((ls[4] + ls[5]) + (ls[6] + ls[7]));
+    }
+};
+
+// A row's running softmax.  The reference maximum is exact for the first block that shows the row a key, and kept while
+// the exponentials cannot overflow (their sum below 2^60); see fwd_kernel.cuh.
+struct State {
+    float m, l, corr;
+    __device__ __forceinline__ void clear() { m = -INFINITY, l = 0.f; }
+    // Adds a block; true (for all lanes) if the maximum of a row moved, so that its output has to be scaled by corr.
+    // Rows past the last one (`use` false) hold anything.
+    template <int kBlock>
+    __device__ __forceinline__ bool add(const Scores<kBlock> &s, uint32_t tS, float sl2, bool use) {
+        float sum;
+        bool again = false, twice = false;
+        corr = 1.f;
+        do {
+            if (m == -INFINITY || again) {
+                const float to = fmaxf(m, s.top() * sl2);
+                if (again && to > m) corr = fast_exp2(m - to);
+                m = to;
+            }
+            sum = s.exponentials(tS, sl2, m == -INFINITY ? 0.f : -m);
+            again = !again && __any_sync(0xffffffffu, use && !(sum < 0x1p60f));
+            if (again) {
+                tmem_wait_st();
+                twice = true;
+            }
+        } while (again);
+        l = l * corr + sum;
+        return twice && __any_sync(0xffffffffu, corr != 1.f);
+    }
+};
+
+template <int D>
+__device__ __forceinline__ void scale_output(uint32_t tO, float corr) {
+#pragma unroll 1
+    for (int c = 0; c < D / 32; ++c) {
+        uint32_t x[32];
+        tmem_ld32(tO + c * 32, x);
+        tmem_wait_ld();
+#pragma unroll
+        for (int i = 0; i < 32; ++i) x[i] = __float_as_uint(__uint_as_float(x[i]) * corr);
+        tmem_st32(tO + c * 32, x);
+    }
+}
+
+// A warp's 32 rows of a finished unit, rows [row0, row0 + 32) of the pair, from the accumulator tO in TMEM: to the
+// outputs where the unit is all of the pair, else to the partial of share `share`.  A thread holds a row; the warp turns
+// 64 bytes of each row at a time through shared memory, so that four lanes store them.
+template <int D>
+__device__ __forceinline__ void store_rows(const Params &p, const Unit &u, int share, int row0, uint32_t tO, const State &st,
+                                           bool live, int token, const Seen &mask, const uint32_t *odd, float *turn) {
+    const int lane = threadIdx.x & 31;
+    const bool whole = u.n == u.nb;
+    const size_t row = whole ? ((size_t)u.b * p.Hkv + u.g) * p.rows + row0
+                             : (size_t)(2 * share + (u.j0 > 0 ? 0 : 1)) * p.rows + row0;
+    const int rows = p.rows - row0;  // in use, if below 32
+    const bool any = live && st.l != 0.f;  // (NaN stays NaN)
+    const float f = 1.f / st.l;
+#pragma unroll 1
+    for (int col = 0; col < D; col += 32) {
+        uint32_t x[32];
+        tmem_ld32(tO + col, x);
+        tmem_wait_ld();
+        float y[32];
+#pragma unroll
+        for (int i = 0; i < 32; ++i) y[i] = any ? __uint_as_float(x[i]) * f : 0.f;
+        if (whole) {
+            __syncwarp();
+#pragma unroll
+            for (int g = 0; g < 4; ++g)
+                *reinterpret_cast<uint4 *>(turn + lane * kTurnStride + g * 4) =
+                    make_uint4(pack_bf16x2(y[8 * g], y[8 * g + 1]), pack_bf16x2(y[8 * g + 2], y[8 * g + 3]),
+                               pack_bf16x2(y[8 * g + 4], y[8 * g + 5]), pack_bf16x2(y[8 * g + 6], y[8 * g + 7]));
+            __syncwarp();
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const int r = 8 * k + (lane >> 2);
+                if (r < rows)
+                    *reinterpret_cast<uint4 *>(p.o + (row + r) * D + col + (lane & 3) * 8) =
+                        *reinterpret_cast<const uint4 *>(turn + r * kTurnStride + (lane & 3) * 4);
+            }
+        } else {
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+                __syncwarp();
+#pragma unroll
+                for (int g = 0; g < 4; ++g) {
+                    const float *z = y + half * 16 + g * 4;
+                    *reinterpret_cast<float4 *>(turn + lane * kTurnStride + g * 4) = make_float4(z[0], z[1], z[2], z[3]);
+                }
+                __syncwarp();
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const int r = 8 * k + (lane >> 2);
+                    if (r < rows)
+                        *reinterpret_cast<float4 *>(p.part_o + (row + r) * D + col + half * 16 + (lane & 3) * 4) =
+                            *reinterpret_cast<const float4 *>(turn + r * kTurnStride + (lane & 3) * 4);
+                }
+            }
+        }
+    }
+    if (lane < rows) {
+        const float L = any ? st.m + __log2f(st.l) : -INFINITY;
+        if (!whole) p.part_lse[row + lane] = L;
+        else if (p.lse) p.lse[row + lane] = L * 0.69314718055994531f;
+    }
+    if (__any_sync(0xffffffffu, lane < kMaskWords && odd[lane & (kMaskWords - 1)] != 0)) {  // behind the warp's stores
+        uint32_t seen[kMaskWords];
+        mask.bits(p, u, token, any, seen);
+#pragma unroll 1
+        for (int w = 0; w < kMaskWords; ++w)
+            for (uint32_t bits = odd[w] & mask_bits(seen, 32 * w); bits; bits &= bits - 1) {
+                const int key = u.len + 32 * w + __ffs(bits) - 1;
+                const int page = p.table ? p.table[(size_t)u.b * p.max_pages + (key >> p.shift)] : u.b;
+                const int in = p.table ? key & (p.page_size - 1) : key;
+                const __nv_bfloat16 *v = p.v + (((size_t)page * p.Hkv + u.g) * p.page_size + in) * D;
+                if (whole) add_odd(p.o + (row + lane) * D, v, D);
+                else add_odd(p.part_o + (row + lane) * D, v, D);
+            }
+        __syncwarp();
+    }
+}
+
+// A softmax warp's look at the pages of a unit's blocks, one block ahead: lane i at page i of the block.
+template <int kBlock>
+struct Holes {
+    const int *table;  // null: nothing to look at
+    int boxes, used, ahead;
+    __device__ __forceinline__ void start(const Params &p, const Unit &u) {
+        table = u.holes ? p.table + (size_t)u.b * p.max_pages : nullptr;
+        boxes = p.page_size < kBlock ? kBlock / p.page_size : 1;
+        used = (u.keys + p.page_size - 1) >> p.shift;
+        look(p, u, 0);
+    }
+    __device__ __forceinline__ void look(const Params &p, const Unit &u, int j) {
+        const int lane = threadIdx.x & 31, i = (((u.j0 + j) * kBlock) >> p.shift) + lane;
+        ahead = table && lane < boxes && i < used && j < u.n ? table[i] : -1;
+    }
+    // The bits of block j's pages; then looks at the next one.
+    __device__ __forceinline__ uint32_t next(const Params &p, const Unit &u, int j) {
+        if (!table) return ~0u;
+        const uint32_t on = __ballot_sync(0xffffffffu, ahead >= 0 && ahead < p.num_pages);
+        look(p, u, j + 1);
+        return on | ~((1u << boxes) - 1);
+    }
+};
+
+// Sequences without a token: zeros, and a log-sum-exp of nothing (one warp of every CTA).
+template <int D>
+__device__ __forceinline__ void clear_idle(const Params &p) {
+    const int lane = threadIdx.x & 31;
+#pragma unroll 1
+    for (int b = blockIdx.x; b < p.B; b += gridDim.x) {
+        int len, tb;
+        load_sequence(p, b, len, tb);
+        if (tb > 0) continue;
+        const size_t rows = (size_t)p.Hkv * p.rows, units16 = rows * (D / 8);
+        uint4 *o = reinterpret_cast<uint4 *>(p.o + (size_t)b * rows * D);
+#pragma unroll 1
+        for (size_t i = lane; i < units16; i += 32) o[i] = make_uint4(0, 0, 0, 0);
+#pragma unroll 1
+        for (size_t i = lane; p.lse && i < rows; i += 32) p.lse[(size_t)b * rows + i] = -INFINITY;
+    }
+    __syncwarp();
+}
+
+// MMAs of one block: S (columns of `keys` keys) = Q K^T, four steps of 16 columns a chunk; O += P V, steps of 16 keys.
+template <int D>
+__device__ __forceinline__ void issue_qk(uint32_t tS, uint64_t q, uint32_t q_chunk, uint64_t k, uint32_t k_chunk, uint32_t idesc) {
+#pragma unroll
+    for (int g = 0; g < D / 64; ++g) {
+        uint64_t a[4], b[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            a[i] = q + uint64_t((g * q_chunk + i * 32) >> 4);
+            b[i] = k + uint64_t((g * k_chunk + i * 32) >> 4);
+        }
+        tc_mma_ss_x4_elect(tS, a, b, idesc, g > 0 ? 1u : 0u);
+    }
+}
+template <int kBlock>
+__device__ __forceinline__ void issue_pv(uint32_t tO, uint32_t tP, uint64_t v, uint32_t idesc, bool acc) {
+#pragma unroll
+    for (int g = 0; g < kBlock / 64; ++g) {
+        uint32_t a[4];
+        uint64_t b[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int kk = g * 4 + i;
+            a[i] = tP + kk * 8;
+            b[i] = v + uint64_t((kk * 16 * 128) >> 4);
+        }
+        tc_mma_ts_x4_elect(tO, a, b, idesc, (acc || g > 0) ? 1u : 0u);
+    }
+}
+
+// ------------------------------------------------------------------ few rows
+// Shared memory: Q and the ring of each chain, then the rest.  Q has p.q_rows rows; the MMAs read on behind them, in what
+// is shared memory all the same, and make rows that nobody looks at.
+template <int D>
+struct PairCfg {
+    static constexpr int kBlock = 64, kChunks = D / 64, kChunkBytes = kBlock * 128, kKVBytes = kBlock * D * 2;
+    static constexpr int kMaxStages = 12;
+    // barriers of a chain (S and P: a buffer each)
+    static constexpr int kQFull = 0, kQEmpty = 1, kSFull = 2, kPFull = 4, kOFull = 6, kOEmpty = 7, kUFull = 8, kUEmpty = 10,
+                         kDrain = 12, kKVFull = 13, kKVEmpty = 13 + kMaxStages, kNumBars = 13 + 2 * kMaxStages;
+    static constexpr int kTurnBytes = 8 * kTurnFloats * 4, kOddBytes = 2 * 4 * kMaskWords * 4;
+    static constexpr int kBarOffset = kTurnBytes + kOddBytes, kUnitOffset = (kBarOffset + 2 * kNumBars * 8 + 15) / 16 * 16;
+    static constexpr int kFixedBytes = kUnitOffset + 2 * 2 * kUnitInts * 4 + 16;
+    static __host__ __device__ int q_bytes(int q_rows) { return q_rows * 128 * kChunks; }
+    static __host__ __device__ int chain_bytes(int q_rows, int stages) { return q_bytes(q_rows) + stages * kKVBytes; }
+    static int stages_for(int q_rows) {
+        const int n = ((kSmemMax - 1024 - kFixedBytes) / 2 - q_bytes(q_rows)) / kKVBytes;
+        return n < kMaxStages ? n : kMaxStages;
+    }
+    static int smem_bytes(int q_rows, int stages) { return 2 * chain_bytes(q_rows, stages) + kFixedBytes + 1024; }
+};
+
+// A place in a ring, and the parity of the round.
+struct Place {
+    uint32_t slot = 0, odd = 0;
+    __device__ __forceinline__ void next(uint32_t stages) {
+        if (++slot == stages) slot = 0, odd ^= 1;
+    }
+};
+
+template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
-    tree_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
-                const __grid_constant__ CUtensorMap tmV, const Params p) {
-    using C = Cfg<D, kKeys>;
+    pairs_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
+                 const __grid_constant__ CUtensorMap tmV, const Params p) {
+    using C = PairCfg<D>;
     constexpr int kBlock = C::kBlock;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    uint8_t *sQ = smem, *sKV = smem + C::kQTiles * C::kQBytes;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int t = warp < 4 ? warp >> 1 : (warp - 4) >> 2;  // chain
+    const int share = t * gridDim.x + blockIdx.x;
+    const uint32_t stages = p.stages;
+    const int q_bytes = C::q_bytes(p.q_rows), chain_bytes = C::chain_bytes(p.q_rows, p.stages);
+    uint8_t *sQ = smem + t * chain_bytes, *ring = sQ + q_bytes, *rest = smem + 2 * chain_bytes;
+    uint32_t *odd_rows = reinterpret_cast<uint32_t *>(rest + C::kTurnBytes) + t * 4 * kMaskWords;  // of four units in turn
+    uint64_t *all_bars = reinterpret_cast<uint64_t *>(rest + C::kBarOffset);
+    volatile int *units = reinterpret_cast<volatile int *>(rest + C::kUnitOffset) + t * 2 * kUnitInts;
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(rest + C::kUnitOffset + 2 * 2 * kUnitInts * 4);
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
+    auto bar = [&](int i) { return smem_u32(all_bars + t * C::kNumBars + i); };
+
+    griddep_launch_dependents();  // the merge waits for this grid to end
+    if (threadIdx.x == 0) {
+        for (int c = 0; c < 2; ++c) {
+            auto init = [&](int i, int n) { mbar_init(smem_u32(all_bars + c * C::kNumBars + i), n); };
+            init(C::kQFull, 1);
+            init(C::kQEmpty, 1);
+            for (int i = 0; i < 2; ++i) {
+                init(C::kSFull + i, 1);
+                init(C::kPFull + i, 4);
+                init(C::kUFull + i, 1);
+                init(C::kUEmpty + i, 1 + 4);
+            }
+            init(C::kOFull, 1);
+            init(C::kOEmpty, 4);
+            init(C::kDrain, 1);
+            for (uint32_t s = 0; s < stages; ++s) {
+                init(C::kKVFull + s, 1);
+                init(C::kKVEmpty + s, 1);
+            }
+        }
+        *abort_flag = 0;
+        fence_mbar_init();
+    }
+    if (warp == 4 || warp == 8) odd_rows[lane] = 0;
+    static_assert(4 * kMaskWords == 32, "one warp clears them");
+    if (warp == 1) {
+        tmem_alloc(smem_u32(tmem_slot), kTmemCols);
+        tmem_relinquish();
+    }
+    Unit u = {};
+    int left = 0;
+    if (warp == 0 || warp == 2) {
+        if (lane == 0) {
+            tma_prefetch_desc(&tmQ);
+            tma_prefetch_desc(&tmK);
+            tma_prefetch_desc(&tmV);
+        }
+        const Share s = share_of<kBlock>(p, share);
+        left = share < p.shares ? s.left : 0;
+        if (left > 0) u = find_block<kBlock>(p, s.lo);
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot + t * 256;  // scores at [0, 64) and [64, 128), the output from 128 on
+
+    if (warp < 4) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kCtrlRegs));
+        volatile int no_abort = 0;
+        if ((warp & 1) == 0) {
+            // ------------------------------------- loader: the units, Q, K and V
+            Place at;
+            uint32_t fills = 0, q_loads = 0;
+            bool ok = true;
+            u.holes = p.table != nullptr;  // (the first unit's entries are looked at block by block)
+            for (uint32_t qi = 0; ok; ++qi) {
+                const uint32_t qs = qi & 1;
+                u.n = left > 0 ? min(left, u.nb - u.j0) : 0;
+                Pages<kBlock> pages;
+                if (u.n > 0) pages.start(p, u);
+                if (p.table && qi > 0) u.holes = look_for_holes<kBlock>(p, u);
+                if (qi >= 2) ok = wait_warp(bar(C::kUEmpty + qs), ((qi >> 1) - 1) & 1, p.wait_ns, abort_flag);
+                if (!ok) break;
+                if (lane == 0) {
+                    u.put(units + kUnitInts * qs);
+                    mbar_arrive(bar(C::kUFull + qs));
+                }
+                __syncwarp();
+                if (u.n == 0) break;
+                Pages<kBlock> same = pages;  // of V, one block behind in the prefetched entries at most
+                for (int j = 0; ok && j < u.n; ++j)
+#pragma unroll 1
+                    for (int kv = 0; kv < 2; ++kv) {
+                        if (fills >= stages) ok = wait_warp(bar(C::kKVEmpty + at.slot), at.odd ^ 1, p.wait_ns, abort_flag);
+                        if (!ok) break;
+                        const uint32_t full = bar(C::kKVFull + at.slot), to = smem_u32(ring + at.slot * C::kKVBytes);
+                        if (lane == 0) mbar_arrive_expect_tx(full, C::kKVBytes);
+                        (kv ? same : pages).template load<C::kChunks>(p, u, (u.j0 + j) * kBlock, kv ? &tmV : &tmK, full, to);
+                        ++fills;
+                        at.next(stages);
+                        if (j + kv == 0) {
+                            if (q_loads > 0) ok = wait_warp(bar(C::kQEmpty), (q_loads - 1) & 1, p.wait_ns, abort_flag);
+                            if (!ok) break;
+                            if (lane == 0) {
+                                mbar_arrive_expect_tx(bar(C::kQFull), q_bytes);
+                                for (int c = 0; c < C::kChunks; ++c)
+                                    tma_load_3d(smem_u32(sQ + c * p.q_rows * 128), &tmQ, bar(C::kQFull), c * 64, 0, u.b * p.Hkv + u.g);
+                            }
+                            __syncwarp();
+                            ++q_loads;
+                        }
+                    }
+                left -= u.n;
+                if (ok && left > 0) next_pair<kBlock>(p, u);
+            }
+            __syncwarp();
+            // Copies have to land before the CTA goes (bounded), whatever became of the other warps: the last one into
+            // every slot.
+            if (!ok && lane == 0) {
+                Place back = at;
+                for (uint32_t s = 0; s < min(fills, stages); ++s) {
+                    back.slot = back.slot == 0 ? (back.odd ^= 1, stages - 1) : back.slot - 1;
+                    if (!mbar_wait_bounded(bar(C::kKVFull + back.slot), back.odd, kDrainNs, &no_abort, &g_tree_status))
+                        atomicOr(&g_tree_status, kStatusDrainTimeout);
+                }
+                if (q_loads > 0 && !mbar_wait_bounded(bar(C::kQFull), (q_loads - 1) & 1, kDrainNs, &no_abort, &g_tree_status))
+                    atomicOr(&g_tree_status, kStatusDrainTimeout);
+            }
+            __syncwarp();
+            if (warp == 0) clear_idle<D>(p);
+        } else {
+            // ------------------------------------------------------ MMA issuer
+            if (share < p.shares) write_cut<kBlock>(p, share, share_of<kBlock>(p, share));
+            constexpr uint32_t kIdescQK = idesc_bf16_f32(kTileM, kBlock, 0), kIdescPV = idesc_bf16_f32(kTileM, D, 1);
+            const uint64_t dQ = smem_desc_sw128(smem_u32(sQ), 16, 1024), dK = smem_desc_sw128(smem_u32(ring), 16, 1024),
+                           dV = smem_desc_sw128(smem_u32(ring), C::kChunkBytes, 1024);
+            const uint32_t q_chunk = p.q_rows * 128;
+            Place k, v;  // of the next K and V
+            v.next(stages);
+            uint32_t p_odd = 0, done = 0;  // p_odd: a bit a buffer
+            bool ok = true;
+            auto qk = [&](int buf) {
+                ok = wait_warp(bar(C::kKVFull + k.slot), k.odd, p.wait_ns, abort_flag);
+                if (!ok) return;
+                tc_fence_after();
+                issue_qk<D>(tmem + buf * kBlock, dQ, q_chunk, dK + uint64_t(k.slot * (C::kKVBytes >> 4)), C::kChunkBytes, kIdescQK);
+                tc_commit_elect(bar(C::kSFull + buf));
+                k.next(stages);
+                k.next(stages);
+            };
+            for (uint32_t qi = 0; ok; ++qi) {
+                const uint32_t qs = qi & 1;
+                ok = wait_warp(bar(C::kUFull + qs), (qi >> 1) & 1, p.wait_ns, abort_flag);
+                if (!ok) break;
+                const int n = __shfl_sync(0xffffffffu, int(units[kUnitInts * qs + 3]), 0);
+                mbar_arrive_elect(bar(C::kUEmpty + qs));
+                if (n == 0) break;
+                ok = wait_warp(bar(C::kQFull), qi & 1, p.wait_ns, abort_flag);
+                // S(0), S(1); then P(j) V and S(j + 2) into the buffer that P(j) has been read from.
+#pragma unroll 1
+                for (int j = -2; ok && j < n; ++j) {
+                    const int buf = j & 1;
+                    if (j >= 0) {
+                        ok = wait_warp(bar(C::kPFull + buf), p_odd >> buf & 1, p.wait_ns, abort_flag);
+                        if (ok && j == 0 && done > 0) ok = wait_warp(bar(C::kOEmpty), (done - 1) & 1, p.wait_ns, abort_flag);
+                        if (ok) ok = wait_warp(bar(C::kKVFull + v.slot), v.odd, p.wait_ns, abort_flag);
+                        if (!ok) break;
+                        p_odd ^= 1u << buf;
+                        tc_fence_after();
+                        issue_pv<kBlock>(tmem + 128, tmem + buf * kBlock, dV + uint64_t(v.slot * (C::kKVBytes >> 4)), kIdescPV, j > 0);
+                        tc_commit_elect(bar(C::kKVEmpty + v.slot));
+                        v.next(stages);
+                        v.next(stages);
+                        if (j == n - 1) tc_commit_elect(bar(C::kOFull));
+                    }
+                    if (j + 2 < n) {
+                        qk(buf);
+                        if (ok && j + 2 == n - 1) tc_commit_elect(bar(C::kQEmpty));  // Q's last product
+                    }
+                }
+                ++done;
+            }
+            tc_commit_elect(bar(C::kDrain));
+            if (!wait_warp(bar(C::kDrain), 0, kDrainNs, &no_abort) && lane == 0) atomicOr(&g_tree_status, kStatusDrainTimeout);
+            __syncwarp();
+        }
+    } else {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
+        // ------------------------------------------------- softmax / epilogue
+        const int quarter = warp & 3, row = quarter * 32 + lane, token = row % p.T;
+        const uint32_t lanes = uint32_t(quarter * 32) << 16, tS0 = tmem + lanes, tO = tmem + lanes + 128;
+        const bool has_rows = quarter * 32 < p.rows;  // of this warp; the others only keep step
+        float *turn = reinterpret_cast<float *>(rest) + (warp - 4) * kTurnFloats;
+        Place at;  // of the next block's K
+        uint32_t s_odd = 0;
+        bool ok = true;
+        for (uint32_t qi = 0; ok; ++qi) {
+            const uint32_t qs = qi & 1;
+            ok = wait_warp(bar(C::kUFull + qs), (qi >> 1) & 1, p.wait_ns, abort_flag);
+            if (!ok) break;
+            u.get(units + kUnitInts * qs);
+            __syncwarp();
+            mbar_arrive_elect(bar(C::kUEmpty + qs));
+            if (u.n == 0) break;
+            const bool live = row < p.rows && token < u.tb;
+            Seen mask;
+            mask.load(p, u, token, live && (u.j0 + u.n) * kBlock > u.len);
+            Holes<kBlock> holes;
+            holes.start(p, u);
+            uint32_t *odd = odd_rows + (qi & 3) * kMaskWords;
+            State st;
+            st.clear();
+            Place last = at;  // of the last block's V
+            for (int j = 0; j < u.n; ++j) {
+                const int buf = j & 1, key = (u.j0 + j) * kBlock;
+                const uint32_t on_page = holes.next(p, u, j);
+                ok = wait_warp(bar(C::kSFull + buf), s_odd >> buf & 1, p.wait_ns, abort_flag);
+                if (!ok) break;
+                s_odd ^= 1u << buf;
+                if (quarter == 0) mbar_arrive_elect(bar(C::kKVEmpty + at.slot));  // S complete: K's slot is free
+                at.next(stages);
+                if (has_rows) {
+                    const uint32_t tS = tS0 + buf * kBlock;
+                    tc_fence_after();
+                    Scores<kBlock> s;
+                    s.load(tS);
+                    if (key + kBlock > u.len || on_page != ~0u) {
+                        uint32_t seen[kMaskWords];
+                        mask.bits(p, u, token, live, seen);
+                        s.hide(p, seen, key, u.len, holes.table != nullptr, on_page);
+                    }
+                    if (st.add(s, tS, p.scale_log2, row < p.rows) && j > 0) {
+                        // S(j) was issued ahead of the last product into O: wait for that, by its V slot, which nobody can
+                        // have filled and freed again before this block's P.
+                        ok = wait_warp(bar(C::kKVEmpty + last.slot), last.odd, p.wait_ns, abort_flag);
+                        if (!ok) break;
+                        tc_fence_after();
+                        scale_output<D>(tO, st.corr);
+                    }
+                    tmem_wait_st();
+                    tc_fence_before();
+                }
+                if (key + kBlock > u.len) {
+                    ok = wait_warp(bar(C::kKVFull + at.slot), at.odd, p.wait_ns, abort_flag);
+                    if (!ok) break;
+                    const int first = max(u.len - key, 0);
+                    clean_rows<C::kChunks, kBlock>(ring + at.slot * C::kKVBytes, quarter, first, u.keys - key, key + first - u.len, odd);
+                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                }
+                last = at;
+                at.next(stages);
+                __syncwarp();
+                mbar_arrive_elect(bar(C::kPFull + buf));
+            }
+            if (ok) ok = wait_warp(bar(C::kOFull), qi & 1, p.wait_ns, abort_flag);
+            if (!ok) break;
+            tc_fence_after();
+            // (the next unit but one has none yet, and this warp's mates are all past the last one)
+            if (quarter == 0 && lane < kMaskWords) odd_rows[((qi + 2) & 3) * kMaskWords + lane] = 0;
+            if (has_rows) store_rows<D>(p, u, share, quarter * 32, tO, st, live, token, mask, odd, turn);
+            tc_fence_before();
+            __syncwarp();
+            mbar_arrive_elect(bar(C::kOEmpty));
+        }
+    }
+
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc(*tmem_slot, kTmemCols);
+    }
+}
+
+// ----------------------------------------------------------------- many rows
+template <int D>
+struct RowsCfg {
+    static constexpr int kBlock = 128, kChunks = D / 64, kChunkBytes = 128 * 128;
+    static constexpr int kQBytes = kTileM * D * 2, kKVBytes = kBlock * D * 2;
+    static constexpr int kStages = D == 128 ? 4 : 8;
+    static constexpr int kOCol = 2 * kTileM;
+    static constexpr int kTurnOffset = 2 * kQBytes + kStages * kKVBytes, kOddOffset = kTurnOffset + 8 * kTurnFloats * 4;
+    static constexpr int kBarOffset = kOddOffset + 4 * kMaskWords * 4;
+    static constexpr int kQFull = 0, kQEmpty = 2, kSFull = 4, kPFull = 6, kOFull = 8, kOEmpty = 10, kUFull = 12, kUEmpty = 14,
+                         kDrain = 16, kKVFull = 17, kKVEmpty = 17 + kStages, kNumBars = 17 + 2 * kStages;
+    static constexpr int kUnitOffset = (kBarOffset + kNumBars * 8 + 15) / 16 * 16;
+    static constexpr int kSmemBytes = kUnitOffset + 2 * kUnitInts * 4 + 16 + 1024;  // units, tmem, abort; alignment
+    static_assert(kSmemBytes <= kSmemMax, "shared memory");
+};
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1)
+    rows_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
+                const __grid_constant__ CUtensorMap tmV, const Params p) {
+    using C = RowsCfg<D>;
+    constexpr int kBlock = C::kBlock;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    uint8_t *sQ = smem, *sKV = smem + 2 * C::kQBytes;
+    uint32_t *odd_rows = reinterpret_cast<uint32_t *>(smem + C::kOddOffset);  // of four units in turn
     uint64_t *bars = reinterpret_cast<uint64_t *>(smem + C::kBarOffset);
     volatile int *units = reinterpret_cast<volatile int *>(smem + C::kUnitOffset);  // two entries
-    // Drafted V rows of a unit that are not finite everywhere; of four units in turn, since the other chain may still
-    // read the last one's, and the next one's has to be empty by then.
-    uint32_t *odd_rows = reinterpret_cast<uint32_t *>(smem + C::kOddOffset);
-    static_assert(4 * kMaskWords == 32, "one warp clears them");
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + C::kUnitOffset + 2 * kUnitInts * 4);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int share = blockIdx.x / p.mt, m = blockIdx.x - share * p.mt;
+    const bool second = (2 * m + 1) * kTileM < p.rows;  // a second tile
     auto bar = [&](int i) { return smem_u32(bars + i); };
-    int *status = &g_tree_status;
 
     griddep_launch_dependents();  // the merge waits for this grid to end
     if (threadIdx.x == 0) {
         for (int t = 0; t < 2; ++t) {
             mbar_init(bar(C::kQFull + t), 1);
             mbar_init(bar(C::kQEmpty + t), 1);
-            for (int i = 0; i < 2; ++i) {
-                mbar_init(bar(C::kSFull + 2 * t + i), 1);
-                mbar_init(bar(C::kPFull + 2 * t + i), 4);
-            }
+            mbar_init(bar(C::kSFull + t), 1);
+            mbar_init(bar(C::kPFull + t), 4);
             mbar_init(bar(C::kOFull + t), 1);
-            mbar_init(bar(C::kOEmpty + t), kKeys ? 8 : 4);
+            mbar_init(bar(C::kOEmpty + t), 4);
             mbar_init(bar(C::kUFull + t), 1);
             mbar_init(bar(C::kUEmpty + t), 3 + 8);  // the K, V and MMA warps, the softmax warps
         }
-        mbar_init(bar(C::kStateFull), 8);
         mbar_init(bar(C::kDrain), 1);
         for (int s = 0; s < C::kStages; ++s) {
             mbar_init(bar(C::kKVFull + s), 1);
@@ -315,55 +1002,30 @@ __global__ void __launch_bounds__(kThreads, 1)
         tmem_alloc(smem_u32(tmem_slot), kTmemCols);
         tmem_relinquish();
     }
-    // The share [lo, lo + left) of the blocks: warp 3 finds its first unit, warp 2 what lies behind it.
     Unit u = {};
     int left = 0;
-    if (warp == 2 || warp == 3) {
-        const unsigned total = all_blocks<kBlock>(p), S = (total + p.shares - 1) / p.shares, lo = share * S;
-        left = int(lo < total ? min(S, total - lo) : 0);
-        if (warp == 3) {
-            if (left > 0) u = find_block<kBlock>(p, lo);
-        } else if (m == 0) {
-            // Where the merge finds the pair that goes on behind this share: from the lengths alone, so that a launch
-            // whose waits run out leaves the merge wrong numbers but no wrong addresses.
-            int4 cut = make_int4(0, 0, 0, 0);
-            if (left > 0) {
-                const Unit at = find_block<kBlock>(p, lo + left - 1);
-                const int rest = at.nb - at.j0 - 1;
-                if (at.j0 < left && rest > 0) cut = make_int4(at.b, at.g, 1 + int((rest + S - 1) / S), at.tb);
-            }
-            if (lane == 0) p.cuts[share] = cut;
-        }
+    if (warp == 3) {
+        const Share s = share_of<kBlock>(p, share);
+        left = s.left;
+        if (left > 0) u = find_block<kBlock>(p, s.lo);
     }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem_base = *tmem_slot;
+    const uint32_t tmem = *tmem_slot;
 
     if (warp < 4) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kCtrlRegs));
-        const bool second = !kKeys && (2 * m + 1) * kTileM < p.rows;  // a second tile
-        const uint64_t drain_ns = 1000000000ull;
         volatile int no_abort = 0;
         if (warp == 3) {
             // -------------------------------------------- planner: the units, and Q
-            uint32_t q_loads = 0;  // per tile (both are loaded for every unit that has them)
+            uint32_t q_loads = 0;  // per tile (both are loaded for every unit)
             bool ok = true;
             u.holes = p.table != nullptr;  // (the first unit's entries are looked at block by block)
             for (uint32_t qi = 0; ok; ++qi) {
                 const uint32_t qs = qi & 1;
                 u.n = left > 0 ? min(left, u.nb - u.j0) : 0;
-                if (p.table && qi > 0) {
-                    // Ahead of the other warps: whether the unit needs looking at all.
-                    const int *table = p.table + (size_t)u.b * p.max_pages;
-                    const int last = min(u.keys, (u.j0 + u.n) * kBlock) - 1;
-                    bool hole = false;
-                    for (int i = ((u.j0 * kBlock) >> p.shift) + lane; u.n > 0 && i <= last >> p.shift; i += 32) {
-                        const int page = table[i];
-                        hole |= page < 0 || page >= p.num_pages;
-                    }
-                    u.holes = __any_sync(0xffffffffu, hole);
-                }
+                if (p.table && qi > 0) u.holes = look_for_holes<kBlock>(p, u);
                 if (qi >= 2) ok = wait_warp(bar(C::kUEmpty + qs), ((qi >> 1) - 1) & 1, p.wait_ns, abort_flag);
                 if (!ok) break;
                 if (lane == 0) {
@@ -372,13 +1034,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 __syncwarp();
                 if (u.n == 0) break;
+#pragma unroll 1
                 for (int t = 0; t < (second ? 2 : 1); ++t) {
                     if (q_loads > 0) ok = wait_warp(bar(C::kQEmpty + t), (q_loads - 1) & 1, p.wait_ns, abort_flag);
                     if (!ok) break;
                     if (lane == 0) {
                         mbar_arrive_expect_tx(bar(C::kQFull + t), C::kQBytes);
                         for (int c = 0; c < C::kChunks; ++c)
-                            tma_load_3d(smem_u32(sQ + t * C::kQBytes + c * C::kQChunkBytes), &tmQ, bar(C::kQFull + t), c * 64,
+                            tma_load_3d(smem_u32(sQ + t * C::kQBytes + c * C::kChunkBytes), &tmQ, bar(C::kQFull + t), c * 64,
                                         (2 * m + t) * kTileM, u.b * p.Hkv + u.g);
                     }
                     __syncwarp();
@@ -386,33 +1049,22 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (!ok) break;
                 ++q_loads;
                 left -= u.n;
-                if (left <= 0) continue;
-                u.j0 = 0;
-                if (++u.g == p.Hkv) {
-                    u.g = 0;
-                    do {
-                        load_sequence(p, ++u.b, u.len, u.tb);
-                        u.keys = keys_of(p, u.len, u.tb);
-                    } while (u.keys == 0);
-                    u.nb = blocks_of<kBlock>(u.keys);
-                }
+                if (left > 0) next_pair<kBlock>(p, u);
             }
             __syncwarp();
             // Copies have to land before the CTA goes (bounded), whatever became of the other warps.
             if (!ok && lane == 0)
                 for (int t = 0; t < (second ? 2 : 1); ++t)
-                    if (q_loads > 0 && !mbar_wait_bounded(bar(C::kQFull + t), (q_loads - 1) & 1, drain_ns, &no_abort, status))
-                        atomicOr(status, kStatusDrainTimeout);
+                    if (q_loads > 0 && !mbar_wait_bounded(bar(C::kQFull + t), (q_loads - 1) & 1, kDrainNs, &no_abort, &g_tree_status))
+                        atomicOr(&g_tree_status, kStatusDrainTimeout);
             __syncwarp();
-        } else if (warp == 0 || warp == 2) {
-            // ------------------------------------- producers: warp 0 K, warp 2 V
+        } else if (warp != 1) {
+            // ------------------------------------- loaders: warp 0 K, warp 2 V
             // Blocks alternate in the ring, K at even fills and V at odd ones; neither warp waits for the other's slots.
             const uint32_t kv = warp == 0 ? 0 : 1;
-            const CUtensorMap *map = warp == 0 ? &tmK : &tmV;
+            if (warp == 2 && m == 0) write_cut<kBlock>(p, share, share_of<kBlock>(p, share));
             uint32_t blocks = 0;  // loaded so far
             bool ok = true;
-            const int boxes = p.table && p.page_size < kBlock ? kBlock / p.page_size : 1;
-            const int box_bytes = C::kChunkBytes / boxes;
             for (uint32_t qi = 0; ok; ++qi) {
                 const uint32_t qs = qi & 1;
                 ok = wait_warp(bar(C::kUFull + qs), (qi >> 1) & 1, p.wait_ns, abort_flag);
@@ -421,34 +1073,16 @@ __global__ void __launch_bounds__(kThreads, 1)
                 __syncwarp();
                 mbar_arrive_elect(bar(C::kUEmpty + qs));
                 if (u.n == 0) break;
-                // Lane i holds entry base + i of the table, and the one 32 behind it.
-                const int *table = p.table ? p.table + (size_t)u.b * p.max_pages : nullptr;
-                const int used = (u.keys + p.page_size - 1) >> p.shift;
-                auto entry = [&](int i) { return table && i < used ? table[i] : -1; };
-                int base = (u.j0 * kBlock) >> p.shift;
-                int cur = entry(base + lane), nxt = entry(base + 32 + lane);
+                Pages<kBlock> pages;
+                pages.start(p, u);
                 for (int j = 0; j < u.n; ++j) {
                     const uint32_t fill = 2 * blocks + kv, slot = fill % C::kStages, round = fill / C::kStages;
                     if (round > 0) ok = wait_warp(bar(C::kKVEmpty + slot), (round - 1) & 1, p.wait_ns, abort_flag);
                     if (!ok) break;
-                    const uint32_t fb = bar(C::kKVFull + slot), to = smem_u32(sKV + slot * C::kKVBytes);
-                    if (lane == 0) mbar_arrive_expect_tx(fb, C::kKVBytes);
-                    const int key = (u.j0 + j) * kBlock, first = key >> p.shift;
-                    if (table && first >= base + 32) {
-                        base += 32;
-                        cur = nxt;
-                        nxt = entry(base + 32 + lane);
-                    }
-                    for (int i = 0; i < boxes; ++i) {
-                        const int page = table ? __shfl_sync(0xffffffffu, cur, (first - base + i) & 31) : u.b;
-                        const int row = !table ? key : boxes > 1 ? 0 : key & (p.page_size - 1);
-                        const int plane = page >= 0 && page < p.num_pages ? page * p.Hkv + u.g : p.num_pages * p.Hkv;
-                        if (lane == 0)
-#pragma unroll
-                            for (int c = 0; c < C::kChunks; ++c)
-                                tma_load_3d(to + c * C::kChunkBytes + i * box_bytes, map, fb, c * 64, row, plane);
-                    }
-                    __syncwarp();
+                    const uint32_t full = bar(C::kKVFull + slot);
+                    if (lane == 0) mbar_arrive_expect_tx(full, C::kKVBytes);
+                    pages.template load<C::kChunks>(p, u, (u.j0 + j) * kBlock, kv ? &tmV : &tmK, full,
+                                                    smem_u32(sKV + slot * C::kKVBytes));
                     ++blocks;
                 }
             }
@@ -457,66 +1091,22 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (uint32_t s = kv; s < C::kStages; s += 2) {
                     if (2 * blocks <= s) continue;  // fills below 2 blocks + kv are out
                     const uint32_t last = (2 * blocks - 2 + kv - s) / C::kStages;  // round of the slot's last fill
-                    if (!mbar_wait_bounded(bar(C::kKVFull + s), last & 1, drain_ns, &no_abort, status))
-                        atomicOr(status, kStatusDrainTimeout);
+                    if (!mbar_wait_bounded(bar(C::kKVFull + s), last & 1, kDrainNs, &no_abort, &g_tree_status))
+                        atomicOr(&g_tree_status, kStatusDrainTimeout);
                 }
             __syncwarp();
-            if (warp == 2) {
-                // Sequences without a token: zeros, and a log-sum-exp of nothing.
-                for (int b = blockIdx.x; b < p.B; b += gridDim.x) {
-                    int len, tb;
-                    load_sequence(p, b, len, tb);
-                    if (tb > 0) continue;
-                    const size_t rows = (size_t)p.Hkv * p.rows, units16 = rows * (D / 8);
-                    uint4 *o = reinterpret_cast<uint4 *>(p.o + (size_t)b * rows * D);
-                    for (size_t i = lane; i < units16; i += 32) o[i] = make_uint4(0, 0, 0, 0);
-                    if (p.lse)
-                        for (size_t i = lane; i < rows; i += 32) p.lse[(size_t)b * rows + i] = -INFINITY;
-                }
-                __syncwarp();
-            }
-        } else if (warp == 1) {
+            if (warp == 2) clear_idle<D>(p);
+        } else {
             // ------------------------------------------------------ MMA issuer
             constexpr uint32_t kIdescQK = idesc_bf16_f32(kTileM, kBlock, 0), kIdescPV = idesc_bf16_f32(kTileM, D, 1);
-            uint32_t fills = 0;
-            uint32_t q_used = 0;
-            uint32_t p_odd = 0, o_odd = 0, used = 0;  // a bit a chain: waits for P, units done, whether there was one
+            const uint64_t dQ = smem_desc_sw128(smem_u32(sQ), 16, 1024), dK = smem_desc_sw128(smem_u32(sKV), 16, 1024),
+                           dV = smem_desc_sw128(smem_u32(sKV), C::kChunkBytes, 1024);
+            const int tiles = second ? 2 : 1;
+            uint32_t fills = 0, blocks = 0, done = 0;
             bool ok = true;
-            const int chains = second ? 2 : 1;  // (kRows)
+            auto slot_off = [&](uint32_t f) { return uint64_t(f % C::kStages * (C::kKVBytes >> 4)); };
             auto wait_slot = [&](uint32_t f) {
                 return wait_warp(bar(C::kKVFull + f % C::kStages), (f / C::kStages) & 1, p.wait_ns, abort_flag);
-            };
-            const uint64_t dQ = smem_desc_sw128(smem_u32(sQ), 16, 1024);
-            const uint64_t dK = smem_desc_sw128(smem_u32(sKV), 16, 1024);
-            const uint64_t dV = smem_desc_sw128(smem_u32(sKV), C::kChunkBytes, 1024);
-            auto slot_off = [&](uint32_t f) { return uint64_t(f % C::kStages * (C::kKVBytes >> 4)); };
-            auto issue_qk = [&](int t, int buf, uint32_t fK) {
-                const uint64_t a0 = dQ + uint64_t((kKeys ? 0 : t) * (C::kQBytes >> 4)), b0 = dK + slot_off(fK);
-#pragma unroll
-                for (int g = 0; g < D / 64; ++g) {
-                    uint64_t a[4], b[4];
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        a[i] = a0 + uint64_t((g * C::kQChunkBytes + i * 32) >> 4);
-                        b[i] = b0 + uint64_t((g * C::kChunkBytes + i * 32) >> 4);
-                    }
-                    tc_mma_ss_x4_elect(tmem_base + t * kTileM + buf * kBlock, a, b, kIdescQK, g > 0 ? 1u : 0u);
-                }
-            };
-            auto issue_pv = [&](int t, int buf, uint32_t fV, bool acc) {
-                const uint64_t b0 = dV + slot_off(fV);
-#pragma unroll
-                for (int g = 0; g < kBlock / 64; ++g) {
-                    uint32_t a[4];
-                    uint64_t b[4];
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const int kk = g * 4 + i;
-                        a[i] = tmem_base + t * kTileM + buf * kBlock + kk * 8;
-                        b[i] = b0 + uint64_t((kk * 16 * 128) >> 4);
-                    }
-                    tc_mma_ts_x4_elect(tmem_base + C::kOCol + t * D, a, b, kIdescPV, (acc || g > 0) ? 1u : 0u);
-                }
             };
             for (uint32_t qi = 0; ok; ++qi) {
                 const uint32_t qs = qi & 1;
@@ -525,84 +1115,56 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int n = __shfl_sync(0xffffffffu, int(units[kUnitInts * qs + 3]), 0);
                 mbar_arrive_elect(bar(C::kUEmpty + qs));
                 if (n == 0) break;
-                const uint32_t f0 = fills;  // K_j at f0 + 2 j, V_j behind it
-                // The first product of each chain and buffer.
-                ok = wait_warp(bar(C::kQFull), q_used & 1, p.wait_ns, abort_flag);
-                if (ok && !kKeys && second) ok = wait_warp(bar(C::kQFull + 1), q_used & 1, p.wait_ns, abort_flag);
+                // S(t, 0); then P(t, j) V and S(t, j + 1), so that the commit that announces S(t, j + 1) says that P(t, j) V
+                // is complete too.
+                for (int j = -1; ok && j < n; ++j) {
+                    const uint32_t fV = fills + 2 * j + 1, fK = fV + 1;
 #pragma unroll 1
-                for (int i = 0; i < (kKeys ? 4 : 2); ++i) {
-                    const int j = kKeys ? i : 0, t = i & 1, buf = kKeys ? i >> 1 : 0;
-                    if (!ok || j >= n || (!kKeys && t >= chains)) break;
-                    ok = wait_slot(f0 + 2 * j);
-                    if (!ok) break;
-                    tc_fence_after();
-                    issue_qk(t, buf, f0 + 2 * j);
-                    tc_commit_elect(bar(C::kSFull + 2 * t + buf));
-                    if (j == n - 1) tc_commit_elect(bar(C::kQEmpty + (kKeys ? 0 : t)));  // Q's last product
-                }
-                ++q_used;
-                for (int j = 0; ok && j < n; ++j) {
-                    const uint32_t fV = f0 + 2 * j + 1;
-                    bool v_ready = false;
-#pragma unroll 1
-                    for (int i = 0; i < (kKeys ? 1 : 2); ++i) {
-                        const int t = kKeys ? j & 1 : i, buf = kKeys ? j >> 1 & 1 : 0, tb = 2 * t + buf;
-                        if (!kKeys && i >= chains) break;
-                        ok = wait_warp(bar(C::kPFull + tb), p_odd >> tb & 1, p.wait_ns, abort_flag);
-                        if (!ok) break;
-                        p_odd ^= 1u << tb;
-                        const bool first = kKeys ? j < 2 : j == 0;
-                        if (first && (used >> t & 1)) {
-                            ok = wait_warp(bar(C::kOEmpty + t), ~(o_odd >> t) & 1, p.wait_ns, abort_flag);
+                    for (int t = 0; t < tiles; ++t) {
+                        if (j >= 0) {
+                            ok = wait_warp(bar(C::kPFull + t), blocks & 1, p.wait_ns, abort_flag);
+                            if (ok && j == 0 && done > 0) ok = wait_warp(bar(C::kOEmpty + t), (done - 1) & 1, p.wait_ns, abort_flag);
+                            if (ok && t == 0) ok = wait_slot(fV);
+                            if (!ok) break;
+                            tc_fence_after();
+                            issue_pv<kBlock>(tmem + C::kOCol + t * D, tmem + t * kTileM, dV + slot_off(fV), kIdescPV, j > 0);
+                            if (t == tiles - 1) tc_commit_elect(bar(C::kKVEmpty + fV % C::kStages));
+                        } else {
+                            ok = wait_warp(bar(C::kQFull + t), done & 1, p.wait_ns, abort_flag);
                             if (!ok) break;
                         }
-                        if (!v_ready) {
-                            ok = wait_slot(fV);
+                        if (j + 1 < n) {
+                            if (t == 0) ok = wait_slot(fK);
                             if (!ok) break;
-                            v_ready = true;
-                        }
-                        tc_fence_after();
-                        issue_pv(t, buf, fV, !first);
-                        if (kKeys || t == chains - 1) tc_commit_elect(bar(C::kKVEmpty + fV % C::kStages));
-                        const int next = j + (kKeys ? 4 : 1);  // into the buffer that P has been read from
-                        if (next < n) {
-                            ok = wait_slot(f0 + 2 * next);
-                            if (!ok) break;
-                            issue_qk(t, buf, f0 + 2 * next);
-                            tc_commit_elect(bar(C::kSFull + tb));
-                            if (next == n - 1) tc_commit_elect(bar(C::kQEmpty + (kKeys ? 0 : t)));
-                        }
-                        if (j + (kKeys ? 2 : 1) >= n) {  // the chain's last block
+                            tc_fence_after();
+                            issue_qk<D>(tmem + t * kTileM, dQ + uint64_t(t * (C::kQBytes >> 4)), C::kChunkBytes, dK + slot_off(fK),
+                                        C::kChunkBytes, kIdescQK);
+                            tc_commit_elect(bar(C::kSFull + t));
+                            if (j + 1 == n - 1) tc_commit_elect(bar(C::kQEmpty + t));  // Q's last product
+                        } else {
                             tc_commit_elect(bar(C::kOFull + t));
-                            o_odd ^= 1u << t;
-                            used |= 1u << t;
                         }
                     }
+                    if (j >= 0) ++blocks;
                 }
-                fills = f0 + 2 * n;
+                fills += 2 * n;
+                ++done;
             }
             tc_commit_elect(bar(C::kDrain));
-            if (!wait_warp(bar(C::kDrain), 0, drain_ns, &no_abort) && lane == 0)
-                atomicOr(status, kStatusDrainTimeout);
+            if (!wait_warp(bar(C::kDrain), 0, kDrainNs, &no_abort) && lane == 0) atomicOr(&g_tree_status, kStatusDrainTimeout);
             __syncwarp();
         }
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
         // ------------------------------------------------- softmax / epilogue
-        const int t = (warp - 4) >> 2, quarter = warp & 3, r = quarter * 32 + lane;
-        const uint32_t lane_off = uint32_t(quarter * 32) << 16;
-        const uint32_t tS0 = tmem_base + lane_off + t * kTileM, tO = tmem_base + lane_off + C::kOCol;
-        const int row0 = kKeys ? 0 : (2 * m + t) * kTileM, row = row0 + r;
-        const int token = row % p.T;
-        const bool has_rows = row0 + quarter * 32 < p.rows;  // of this warp; the others only keep step
-        const bool has_tile = row0 < p.rows;
-        const bool both = kKeys || (2 * m + 1) * kTileM < p.rows;  // whether chain 1 is at work
-        const float sl2 = p.scale_log2;
-        const int limit = p.rows - row0;  // rows of the tile in use, if below 128
+        const int t = (warp - 4) >> 2, quarter = warp & 3;
+        const int row0 = (2 * m + t) * kTileM + quarter * 32, row = row0 + lane, token = row % p.T;
+        const uint32_t lanes = uint32_t(quarter * 32) << 16;
+        const uint32_t tS = tmem + lanes + t * kTileM, tO = tmem + lanes + C::kOCol + t * D;
+        const bool has_rows = row0 < p.rows;  // of this warp; the others only keep step
+        const bool frees = quarter == 0 && t == (second ? 1 : 0);  // K's slots: the last chain to see S
         float *turn = reinterpret_cast<float *>(smem + C::kTurnOffset) + (warp - 4) * kTurnFloats;
-        float2 *states = reinterpret_cast<float2 *>(smem + C::kStateOffset);  // [unit parity][chain][row]
-        uint32_t s_odd = 0, o_waits = 0, o_waits1 = 0;  // s_odd: a bit a buffer
-        uint32_t kv_base = 0;
+        uint32_t blocks = 0, fills = 0;
         bool ok = true;
         for (uint32_t qi = 0; ok; ++qi) {
             const uint32_t qs = qi & 1;
@@ -612,281 +1174,55 @@ __global__ void __launch_bounds__(kThreads, 1)
             __syncwarp();
             mbar_arrive_elect(bar(C::kUEmpty + qs));
             if (u.n == 0) break;
-            const uint32_t f0 = kv_base;
-            kv_base += 2 * u.n;
-            if (!has_tile) continue;
+            if (t > 0 && !second) continue;
             const bool live = row < p.rows && token < u.tb;
-            // What the row sees of the drafted tokens.
-            uint32_t seen[kMaskWords];
-#pragma unroll
-            for (int w = 0; w < kMaskWords; ++w) seen[w] = 0;
-            if ((u.j0 + u.n) * (long long)kBlock > u.len && live) {
-                const int words = (p.T + 63) / 64;
-                const unsigned long long *mrow = p.mask ? p.mask + ((size_t)u.b * p.T + token) * words : nullptr;
-                const int end = u.keys - u.len;  // drafted keys that exist
-#pragma unroll
-                for (int w = 0; w < kMaskWords / 2; ++w) {
-                    const int in = mrow ? end : min(end, token + 1);  // a chain sees what is before it
-                    unsigned long long x = !mrow ? ~0ull : w < words ? mrow[w] : 0ull;
-                    if (in < 64 * w + 64) x = in <= 64 * w ? 0ull : x & ((1ull << (in - 64 * w)) - 1);
-                    seen[2 * w] = uint32_t(x);
-                    seen[2 * w + 1] = uint32_t(x >> 32);
-                }
-            }
-            const int *table = u.holes ? p.table + (size_t)u.b * p.max_pages : nullptr;  // null: nothing to look at
-            const int boxes = p.page_size < kBlock ? kBlock / p.page_size : 1;  // (with a table only)
-            const int used = (u.keys + p.page_size - 1) >> p.shift;
-            // Lane i looks at entry i of a block's pages, one block ahead.
-            auto page_of = [&](int j) {
-                const int i = (((u.j0 + j) * kBlock) >> p.shift) + lane;
-                return table && lane < boxes && i < used && j < u.n ? table[i] : -1;
-            };
-            constexpr int kStep = kKeys ? 2 : 1, kQuads = kBlock / 32;
-            const int jt = kKeys ? t : 0;
-            int ahead = page_of(jt);
-            float m_run = -INFINITY, l_run = 0.f;
-            for (int j = jt; j < u.n; j += kStep) {
-                uint32_t on_page = ~0u;
-                if (table) {
-                    on_page = __ballot_sync(0xffffffffu, ahead >= 0 && ahead < p.num_pages);
-                    ahead = page_of(j + kStep);
-                }
-                const int buf = kKeys ? j >> 1 & 1 : 0;
-                const uint32_t tS = tS0 + buf * kBlock;
-                ok = wait_warp(bar(C::kSFull + 2 * t + buf), s_odd >> buf & 1, p.wait_ns, abort_flag);
+            Seen mask;
+            mask.load(p, u, token, live && (u.j0 + u.n) * kBlock > u.len);
+            Holes<kBlock> holes;
+            holes.start(p, u);
+            uint32_t *odd = odd_rows + (qi & 3) * kMaskWords;
+            State st;
+            st.clear();
+            for (int j = 0; j < u.n; ++j, ++blocks, fills += 2) {
+                const int key = (u.j0 + j) * kBlock;
+                const uint32_t on_page = holes.next(p, u, j);
+                ok = wait_warp(bar(C::kSFull + t), blocks & 1, p.wait_ns, abort_flag);
                 if (!ok) break;
-                s_odd ^= 1u << buf;
-                // S complete: so are all products before it, and K's slot is free once the last chain to use it says so.
-                if (quarter == 0 && (kKeys || t == (both ? 1 : 0)))
-                    mbar_arrive_elect(bar(C::kKVEmpty + (f0 + 2 * j) % C::kStages));
+                if (frees) mbar_arrive_elect(bar(C::kKVEmpty + fills % C::kStages));
                 if (has_rows) {
                     tc_fence_after();
-                    uint32_t sr[kQuads][32];
-#pragma unroll
-                    for (int c = 0; c < kQuads; ++c) tmem_ld32(tS + c * 32, sr[c]);
-                    tmem_wait_ld();
-                    float s[kBlock];
-#pragma unroll
-                    for (int c = 0; c < kQuads; ++c)
-#pragma unroll
-                        for (int i = 0; i < 32; ++i) s[c * 32 + i] = __uint_as_float(sr[c][i]);
-                    const int kv0 = (u.j0 + j) * kBlock;
-                    const uint32_t all = boxes >= 32 ? ~0u : (1u << boxes) - 1;
-                    if (kv0 + kBlock > u.len || (table && (on_page & all) != all)) {
-#pragma unroll
-                        for (int c = 0; c < kQuads; ++c) {
-                            uint32_t bits = mask_bits(seen, kv0 + 32 * c - u.len);
-                            if (table) {
-                                const int per = 32 / (p.page_size < 32 ? p.page_size : 32);  // pages in 32 keys: 1 or 2
-                                const int at = p.page_size < kBlock ? 32 * c / p.page_size : 0;
-                                if (!(on_page >> at & 1)) bits &= per == 2 ? 0xffff0000u : 0u;
-                                if (per == 2 && !(on_page >> (at + 1) & 1)) bits &= 0x0000ffffu;
-                            }
-#pragma unroll
-                            for (int i = 0; i < 32; ++i)
-                                if (!(bits >> i & 1)) s[c * 32 + i] = -INFINITY;
-                        }
+                    Scores<kBlock> s;
+                    s.load(tS);
+                    if (key + kBlock > u.len || on_page != ~0u) {
+                        uint32_t seen[kMaskWords];
+                        mask.bits(p, u, token, live, seen);
+                        s.hide(p, seen, key, u.len, holes.table != nullptr, on_page);
                     }
-                    auto block_max = [&]() {
-                        float mq[kQuads];
-#pragma unroll
-                        for (int c = 0; c < kQuads; ++c) {
-                            float x = fmax3(s[32 * c], s[32 * c + 1], s[32 * c + 2]);
-#pragma unroll
-                            for (int i = 3; i < 31; i += 2) x = fmax3(x, s[32 * c + i], s[32 * c + i + 1]);
-                            mq[c] = fmaxf(x, s[32 * c + 31]);
-                        }
-                        if constexpr (kQuads == 2) return fmaxf(mq[0], mq[1]);
-                        else return fmax3(mq[0], mq[1], fmaxf(mq[2], mq[3]));
-                    };
-                    auto exp_block = [&](float neg_m) {
-                        float ls[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-                        for (int c = 0; c < kQuads; ++c) {
-                            uint32_t pk[16];
-#pragma unroll
-                            for (int i = 0; i < 16; ++i) {
-                                float x0, x1;
-                                ffma2(x0, x1, s[c * 32 + 2 * i], s[c * 32 + 2 * i + 1], sl2, sl2, neg_m, neg_m);
-                                const float p0 = fast_exp2(x0), p1 = fast_exp2(x1);
-                                const int a = (i & 3) * 2;
-                                fadd2(ls[a], ls[a + 1], p0, p1);
-                                pk[i] = pack_bf16x2(p0, p1);
-                            }
-                            tmem_st16(tS + c * 16, pk);
-                        }
-                        return ((ls[0] + ls[1]) + (ls[2] + ls[3])) + ((ls[4] + ls[5]) + (ls[6] + ls[7]));
-                    };
-                    // The reference maximum is exact for the first block that shows the row a key, and kept while the
-                    // exponentials cannot overflow (their sum below 2^60); see fwd_kernel.cuh.
-                    float corr = 1.f, l_blk;
-                    bool again = false, twice = false;
-                    do {
-                        if (m_run == -INFINITY || again) {
-                            const float m_new = fmaxf(m_run, block_max() * sl2);
-                            if (again && m_new > m_run) corr = fast_exp2(m_run - m_new);
-                            m_run = m_new;
-                        }
-                        l_blk = exp_block(m_run == -INFINITY ? 0.f : -m_run);
-                        again = !again && __any_sync(0xffffffffu, !(l_blk < 0x1p60f));
-                        if (again) {
-                            tmem_wait_st();
-                            twice = true;
-                        }
-                    } while (again);
-                    if (twice && j > jt && __any_sync(0xffffffffu, corr != 1.f)) {
-                        if constexpr (kKeys) {
-                            // S(j) was issued ahead of the chain's last product into O: wait for that (its V slot, which
-                            // nobody can have filled and freed again before this block's P).
-                            const uint32_t f = f0 + 2 * (j - kStep) + 1;
-                            ok = wait_warp(bar(C::kKVEmpty + f % C::kStages), (f / C::kStages) & 1, p.wait_ns, abort_flag);
-                            if (!ok) break;
-                            tc_fence_after();
-                        }
-#pragma unroll 1
-                        for (int c = 0; c < D / 32; ++c) {
-                            uint32_t ov[32];
-                            tmem_ld32(tO + t * D + c * 32, ov);
-                            tmem_wait_ld();
-#pragma unroll
-                            for (int i = 0; i < 32; ++i) ov[i] = __float_as_uint(__uint_as_float(ov[i]) * corr);
-                            tmem_st32(tO + t * D + c * 32, ov);
-                        }
-                    }
-                    l_run = l_run * corr + l_blk;
+                    if (st.add(s, tS, p.scale_log2, row < p.rows) && j > 0) scale_output<D>(tO, st.corr);
                     tmem_wait_st();
                     tc_fence_before();
                 }
-                if ((u.j0 + j + 1) * kBlock > u.len && (kKeys || t == 0)) {
-                    // (the other chain's product of this block is issued behind this one's)
-                    const uint32_t fV = f0 + 2 * j + 1, slot = fV % C::kStages;
-                    ok = wait_warp(bar(C::kKVFull + slot), (fV / C::kStages) & 1, p.wait_ns, abort_flag);
+                if (key + kBlock > u.len && t == 0) {
+                    // (the other tile's product of this block is issued behind this one's)
+                    const uint32_t slot = (fills + 1) % C::kStages;
+                    ok = wait_warp(bar(C::kKVFull + slot), ((fills + 1) / C::kStages) & 1, p.wait_ns, abort_flag);
                     if (!ok) break;
-                    const int kv0 = (u.j0 + j) * kBlock, at = max(u.len - kv0, 0);
-                    clean_rows<C::kChunks, kBlock>(sKV + slot * C::kKVBytes, quarter, at, u.keys - kv0, kv0 + at - u.len,
-                                                   odd_rows + (qi & 3) * kMaskWords);
+                    const int first = max(u.len - key, 0);
+                    clean_rows<C::kChunks, kBlock>(sKV + slot * C::kKVBytes, quarter, first, u.keys - key, key + first - u.len, odd);
                     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                 }
                 __syncwarp();
-                mbar_arrive_elect(bar(C::kPFull + 2 * t + buf));
+                mbar_arrive_elect(bar(C::kPFull + t));
             }
+            if (ok) ok = wait_warp(bar(C::kOFull + t), qi & 1, p.wait_ns, abort_flag);
             if (!ok) break;
-
-            // Epilogue: to the outputs where the unit is all of the pair, else to a partial.
-            const bool whole = u.n == u.nb;
-            const size_t out_row = ((size_t)u.b * p.Hkv + u.g) * p.rows + row0;
-            const size_t part_row = (size_t)(2 * share + (u.j0 > 0 ? 0 : 1)) * p.rows + row0;
-            const bool has1 = kKeys && u.n > 1;  // whether chain 1 has an accumulator of this unit
-            float f[2] = {0.f, 0.f}, L, sum;      // factors of the accumulators; the row's log-sum-exp (log2) and sum
-            if constexpr (kKeys) {
-                float2 *mine = states + (qi & 1) * 2 * kTileM;
-                mine[t * kTileM + r] = make_float2(m_run, l_run);
-                __syncwarp();
-                mbar_arrive_elect(bar(C::kStateFull));
-                ok = wait_warp(bar(C::kStateFull), qi & 1, p.wait_ns, abort_flag);
-                if (ok) ok = wait_warp(bar(C::kOFull), o_waits & 1, p.wait_ns, abort_flag);
-                if (ok && has1) ok = wait_warp(bar(C::kOFull + 1), o_waits1 & 1, p.wait_ns, abort_flag);
-                if (!ok) break;
-                ++o_waits;
-                if (has1) ++o_waits1;
-                const float2 a = mine[r], c = mine[kTileM + r];
-                const float top = fmaxf(a.x, c.x), ref = top == -INFINITY ? 0.f : top;
-                f[0] = fast_exp2(a.x - ref);
-                f[1] = fast_exp2(c.x - ref);
-                sum = f[0] * a.y + f[1] * c.y;
-                L = top + __log2f(sum);
-                f[0] /= sum;
-                f[1] /= sum;
-            } else {
-                ok = wait_warp(bar(C::kOFull + t), o_waits & 1, p.wait_ns, abort_flag);
-                if (!ok) break;
-                ++o_waits;
-                sum = l_run;
-                f[0] = 1.f / sum;
-                L = m_run + __log2f(sum);
-            }
             tc_fence_after();
-            const uint32_t *odd = odd_rows + (qi & 3) * kMaskWords;
-            const bool any_odd = __any_sync(0xffffffffu, lane < kMaskWords && odd[lane & 7] != 0);
+            // (the next unit but one has none yet; of the last one's, the other tile is past its products, hence its stores)
             if (t == 0 && quarter == 0 && lane < kMaskWords) odd_rows[((qi + 2) & 3) * kMaskWords + lane] = 0;
-            if (has_rows) {
-                const bool any = live && sum != 0.f;  // (NaN stays NaN)
-                // A thread holds a row; the warp turns 64 bytes of each of its 32 rows at a time through shared memory, so
-                // that four lanes store them.
-                const int first = quarter * 32 + (lane >> 2);
-                constexpr int kCols = kKeys ? D / 2 : D;  // of this warp
-                const int col0 = kKeys ? t * kCols : 0;
-#pragma unroll 1
-                for (int c = 0; c < kCols / 32; ++c) {
-                    const int col = col0 + c * 32;
-                    uint32_t ov[32], ow[32];
-                    float x[32];
-                    tmem_ld32(tO + (kKeys ? 0 : t * D) + col, ov);
-                    if (has1) tmem_ld32(tO + D + col, ow);
-                    tmem_wait_ld();
-#pragma unroll
-                    for (int i = 0; i < 32; ++i) x[i] = __uint_as_float(ov[i]) * f[0];
-                    if (has1)
-#pragma unroll
-                        for (int i = 0; i < 32; ++i) x[i] += __uint_as_float(ow[i]) * f[1];
-                    if (!any)
-#pragma unroll
-                        for (int i = 0; i < 32; ++i) x[i] = 0.f;
-                    if (whole) {
-                        uint4 pk[4];
-#pragma unroll
-                        for (int g = 0; g < 4; ++g)
-                            pk[g] = make_uint4(pack_bf16x2(x[8 * g], x[8 * g + 1]), pack_bf16x2(x[8 * g + 2], x[8 * g + 3]),
-                                               pack_bf16x2(x[8 * g + 4], x[8 * g + 5]), pack_bf16x2(x[8 * g + 6], x[8 * g + 7]));
-                        __syncwarp();
-#pragma unroll
-                        for (int g = 0; g < 4; ++g) *reinterpret_cast<uint4 *>(turn + lane * kTurnStride + g * 4) = pk[g];
-                        __syncwarp();
-#pragma unroll
-                        for (int k = 0; k < 4; ++k)
-                            if (first + 8 * k < limit)
-                                *reinterpret_cast<uint4 *>(p.o + (out_row + first + 8 * k) * D + col + (lane & 3) * 8) =
-                                    *reinterpret_cast<const uint4 *>(turn + (8 * k + (lane >> 2)) * kTurnStride + (lane & 3) * 4);
-                    } else {
-#pragma unroll
-                        for (int half = 0; half < 2; ++half) {
-                            __syncwarp();
-#pragma unroll
-                            for (int g = 0; g < 4; ++g) {
-                                const float *y = x + half * 16 + g * 4;
-                                *reinterpret_cast<float4 *>(turn + lane * kTurnStride + g * 4) = make_float4(y[0], y[1], y[2], y[3]);
-                            }
-                            __syncwarp();
-#pragma unroll
-                            for (int k = 0; k < 4; ++k)
-                                if (first + 8 * k < limit)
-                                    *reinterpret_cast<float4 *>(p.part_o + (part_row + first + 8 * k) * D + col + half * 16 + (lane & 3) * 4) =
-                                        *reinterpret_cast<const float4 *>(turn + (8 * k + (lane >> 2)) * kTurnStride + (lane & 3) * 4);
-                        }
-                    }
-                }
-                if (any_odd) {
-                    __syncwarp();  // behind the warp's stores
-#pragma unroll 1
-                    for (int w = 0; w < kMaskWords; ++w)
-                        for (uint32_t bits = any ? odd[w] & mask_bits(seen, 32 * w) : 0u; bits; bits &= bits - 1) {
-                            const int key = u.len + 32 * w + __ffs(bits) - 1;
-                            const int page = p.table ? p.table[(size_t)u.b * p.max_pages + (key >> p.shift)] : u.b;
-                            const int in = p.table ? key & (p.page_size - 1) : key;
-                            const __nv_bfloat16 *v = p.v + (((size_t)page * p.Hkv + u.g) * p.page_size + in) * D + col0;
-                            if (whole) add_odd(p.o + (out_row + r) * D + col0, v, kCols);
-                            else add_odd(p.part_o + (part_row + r) * D + col0, v, kCols);
-                        }
-                }
-                if ((!kKeys || t == 0) && r < limit) {
-                    if (!whole) p.part_lse[part_row + r] = any ? L : -INFINITY;
-                    else if (p.lse) p.lse[out_row + r] = any ? L * 0.69314718055994531f : -INFINITY;
-                }
-            }
+            if (has_rows) store_rows<D>(p, u, share, row0, tO, st, live, token, mask, odd, turn);
             tc_fence_before();
             __syncwarp();
-            mbar_arrive_elect(bar(C::kOEmpty + (kKeys ? 0 : t)));
-            if (has1) mbar_arrive_elect(bar(C::kOEmpty + 1));
+            mbar_arrive_elect(bar(C::kOEmpty + t));
         }
     }
 
@@ -894,7 +1230,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncthreads();
     if (warp == 1) {
         tc_fence_after();
-        tmem_dealloc(tmem_base, kTmemCols);
+        tmem_dealloc(tmem, kTmemCols);
     }
 }
 
@@ -952,10 +1288,11 @@ struct Layout {
 Layout layout_of(int B, int G, int Hkv, int T, int d, long long cap, int num_sms) {
     Layout l;
     const size_t rows = size_t(G) * T;
-    l.mt = int((rows + 2 * kTileM - 1) / (2 * kTileM));
-    const int block = block_keys(rows <= kTileM);
+    const bool few = rows <= size_t(kTileM);
+    l.mt = few ? 1 : int((rows + 2 * kTileM - 1) / (2 * kTileM));
+    const int block = few ? 64 : 128;
     const long long most = (long long)B * Hkv * ((cap + block - 1) / block);
-    const int groups = num_sms / l.mt > 0 ? num_sms / l.mt : 1;
+    const int groups = few ? 2 * num_sms : num_sms / l.mt > 0 ? num_sms / l.mt : 1;
     l.shares = int(most < groups ? most : groups);
     auto up = [](size_t n) { return (n + 255) / 256 * 256; };
     l.cuts = 0;
@@ -965,14 +1302,15 @@ Layout layout_of(int B, int G, int Hkv, int T, int d, long long cap, int num_sms
     return l;
 }
 
-template <int D, bool kKeys>
+template <int D>
 int launch(const DecodeTreeLaunch &a, const Layout &l, cudaStream_t stream) {
-    using C = Cfg<D, kKeys>;
-    const int G = a.Hq / a.Hkv;
+    const int G = a.Hq / a.Hkv, rows = G * a.T;
+    const bool few = rows <= kTileM;
+    const int block = few ? PairCfg<D>::kBlock : RowsCfg<D>::kBlock, q_rows = few ? (rows + 7) / 8 * 8 : kTileM;
     CUtensorMap mq, mk, mv;
-    const uint32_t box = uint32_t(a.table && a.page_size < C::kBlock ? a.page_size : C::kBlock);
+    const uint32_t box = uint32_t(a.table && a.page_size < block ? a.page_size : block);
     const uint64_t planes = uint64_t(a.num_pages) * a.Hkv;
-    if (!encode_bf16_3d(&mq, a.q, D, uint64_t(G) * a.T, uint64_t(a.B) * a.Hkv, 64, kTileM) ||
+    if (!encode_bf16_3d(&mq, a.q, D, uint64_t(rows), uint64_t(a.B) * a.Hkv, 64, uint32_t(q_rows)) ||
         !encode_bf16_3d(&mk, a.kpages, D, uint64_t(a.page_size), planes, 64, box) ||
         !encode_bf16_3d(&mv, a.vpages, D, uint64_t(a.page_size), planes, 64, box))
         return note_cuda_error(cudaErrorInvalidValue, "cuTensorMapEncodeTiled (drafted tokens)");
@@ -989,9 +1327,8 @@ int launch(const DecodeTreeLaunch &a, const Layout &l, cudaStream_t stream) {
     p.part_lse = reinterpret_cast<float *>(a.workspace + l.part_lse);
     p.B = a.B;
     p.Hkv = a.Hkv;
-    p.G = G;
     p.T = a.T;
-    p.rows = G * a.T;
+    p.rows = rows;
     p.num_pages = a.num_pages;
     p.page_size = a.page_size;
     p.shift = a.page_shift;
@@ -999,26 +1336,30 @@ int launch(const DecodeTreeLaunch &a, const Layout &l, cudaStream_t stream) {
     p.max_pages = a.max_pages;
     p.mt = l.mt;
     p.shares = l.shares;
+    p.q_rows = q_rows;
+    p.stages = PairCfg<D>::stages_for(q_rows);
     p.scale_log2 = a.scale * 1.4426950408889634f;
     p.wait_ns = a.wait_ns;
-    auto kernel = tree_kernel<D, kKeys>;
-    static bool attr_set[kMaxDevices] = {};
+    auto kernel = few ? pairs_kernel<D> : rows_kernel<D>;
+    const int smem = few ? PairCfg<D>::smem_bytes(q_rows, p.stages) : RowsCfg<D>::kSmemBytes;
+    static bool attr_set[2][kMaxDevices] = {};
     const int dev = slot_for_device();
-    if (dev < 0 || !attr_set[dev]) {
+    if (dev < 0 || !attr_set[few][dev]) {
         cudaFuncAttributes fa;
         cudaError_t e = cudaFuncGetAttributes(&fa, kernel);
-        if (e != cudaSuccess) return note_cuda_error(e, "cudaFuncGetAttributes(tree_kernel)");
+        if (e != cudaSuccess) return note_cuda_error(e, "cudaFuncGetAttributes(drafted tokens)");
         if (fa.numRegs != kLaunchRegs || fa.maxThreadsPerBlock < kThreads)
-            return note_cuda_error(cudaErrorInvalidConfiguration, "tree_kernel register count differs from the setmaxnreg split");
-        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes);
-        if (e != cudaSuccess) return note_cuda_error(e, "cudaFuncSetAttribute(tree_kernel)");
-        if (dev >= 0) attr_set[dev] = true;
+            return note_cuda_error(cudaErrorInvalidConfiguration, "register count differs from the setmaxnreg split (drafted tokens)");
+        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemMax);
+        if (e != cudaSuccess) return note_cuda_error(e, "cudaFuncSetAttribute(drafted tokens)");
+        if (dev >= 0) attr_set[few][dev] = true;
     }
-    kernel<<<dim3(unsigned(l.shares * l.mt)), dim3(kThreads), C::kSmemBytes, stream>>>(mq, mk, mv, p);
+    const int ctas = few ? (l.shares < a.num_sms ? l.shares : a.num_sms) : l.shares * l.mt;
+    kernel<<<dim3(unsigned(ctas)), dim3(kThreads), smem, stream>>>(mq, mk, mv, p);
     cudaError_t e = cudaGetLastError();
-    if (e != cudaSuccess) return note_cuda_error(e, "tree_kernel launch");
+    if (e != cudaSuccess) return note_cuda_error(e, "kernel launch (drafted tokens)");
     if (l.shares == 1) return 0;  // nothing is cut
-    e = dec::launch_programmatic(merge_kernel<D>, dim3(unsigned(l.shares), unsigned((p.rows + kMergeWarps - 1) / kMergeWarps)),
+    e = dec::launch_programmatic(merge_kernel<D>, dim3(unsigned(l.shares), unsigned((rows + kMergeWarps - 1) / kMergeWarps)),
                                  dim3(kMergeWarps * 32), 0, stream, p);
     return e == cudaSuccess ? 0 : note_cuda_error(e, "merge_kernel (drafted tokens) launch");
 }
@@ -1033,9 +1374,7 @@ int decode_tree_launch(const DecodeTreeLaunch &a, cudaStream_t stream) {
     using namespace dtree;
     const int G = a.Hq / a.Hkv;
     const Layout l = layout_of(a.B, G, a.Hkv, a.T, a.d, (long long)a.page_size * a.max_pages, a.num_sms);
-    const bool keys = G * a.T <= kTileM;
-    if (a.d == 64) return keys ? launch<64, true>(a, l, stream) : launch<64, false>(a, l, stream);
-    return keys ? launch<128, true>(a, l, stream) : launch<128, false>(a, l, stream);
+    return a.d == 64 ? launch<64>(a, l, stream) : launch<128>(a, l, stream);
 }
 
 cudaError_t decode_tree_take_status(int *bits) {
