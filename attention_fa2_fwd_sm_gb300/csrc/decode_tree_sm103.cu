@@ -42,6 +42,7 @@
 #include <cuda_runtime.h>
 
 #include <cmath>
+#include <type_traits>
 
 #include "../../include/attn.h"
 #include "attn_internal.h"
@@ -81,10 +82,9 @@ constexpr int kThreads = 384;
 constexpr int kLaunchRegs = 168, kCtrlRegs = 120, kSoftmaxRegs = 192;
 static_assert(128 * kCtrlRegs + 256 * kSoftmaxRegs <= kThreads * kLaunchRegs, "register split");
 constexpr int kTmemCols = 512;
-constexpr int kTurnStride = 20, kTurnFloats = 32 * kTurnStride;
 constexpr int kMaskWords = 8;  // 32-bit words of a row's mask: 256 drafted tokens
 constexpr int kUnitInts = 12;  // of a unit in the queue
-constexpr int kMergeWarps = 4;
+constexpr int kMergeWarps = 8;
 constexpr uint64_t kDrainNs = 1000000000ull;  // for copies and products in flight when a CTA gives up
 constexpr int kSmemMax = 227 * 1024;
 
@@ -99,6 +99,7 @@ struct Params {
     int B, Hkv, T, rows;
     int num_pages, page_size, shift, cap, max_pages;
     int mt, shares;
+    bool wide;           // outputs and partials are 32-byte aligned
     int q_rows, stages;  // pairs_kernel: rows of Q in shared memory, blocks of a chain's ring
     float scale_log2;
     unsigned long long wait_ns;
@@ -313,12 +314,16 @@ __device__ __forceinline__ uint32_t mask_bits(const uint32_t (&m)[kMaskWords], i
 
 // What a row sees of a unit's drafted tokens, 64 a word; loaded ahead, looked at where the blocks end.
 struct Seen {
-    unsigned long long w[kMaskWords / 2];
-    __device__ __forceinline__ void load(const Params &p, const Unit &u, int token, bool want) {
+    unsigned long long w[kMaskWords / 2] = {};
+    int b = -1;  // whose they are: the KV heads of a sequence have the same
+    __device__ __forceinline__ void load(const Params &p, const Unit &u, int token) {
+        if (!p.mask || b == u.b) return;
+        b = u.b;
         const int words = (p.T + 63) / 64;
-        const unsigned long long *row = p.mask && want ? p.mask + ((size_t)u.b * p.T + token) * words : nullptr;
+        const unsigned long long *row = p.mask + ((size_t)u.b * p.T + token) * words;
 #pragma unroll
-        for (int i = 0; i < kMaskWords / 2; ++i) w[i] = row && i < words ? row[i] : 0ull;
+        for (int i = 0; i < kMaskWords / 2; ++i)
+            if (i < words) w[i] = row[i];
     }
     // As 32-bit words, without keys that do not exist; without a mask, a chain sees what is before it.
     __device__ __forceinline__ void bits(const Params &p, const Unit &u, int token, bool live, uint32_t (&out)[kMaskWords]) const {
@@ -481,12 +486,24 @@ __device__ __forceinline__ void scale_output(uint32_t tO, float corr) {
     }
 }
 
-// A warp's 32 rows of a finished unit, rows [row0, row0 + 32) of the pair, from the accumulator tO in TMEM: to the
-// outputs where the unit is all of the pair, else to the partial of share `share`.  A thread holds a row; the warp turns
-// 64 bytes of each row at a time through shared memory, so that four lanes store them.
+// 32 bytes to global memory: whole sectors, so that lanes that hold a row each need no help from one another to store it;
+// in two halves where the tensors are only 16-byte aligned.
+__device__ __forceinline__ void store_32(void *to, const uint32_t (&x)[8], bool wide) {
+    if (wide) {
+        asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(to), "r"(x[0]), "r"(x[1]), "r"(x[2]),
+                     "r"(x[3]), "r"(x[4]), "r"(x[5]), "r"(x[6]), "r"(x[7])
+                     : "memory");
+    } else {
+        reinterpret_cast<uint4 *>(to)[0] = make_uint4(x[0], x[1], x[2], x[3]);
+        reinterpret_cast<uint4 *>(to)[1] = make_uint4(x[4], x[5], x[6], x[7]);
+    }
+}
+
+// A warp's 32 rows of a finished unit, rows [row0, row0 + 32) of the pair, a thread each, from the accumulator tO in TMEM:
+// to the outputs where the unit is all of the pair, else to the partial of share `share`.
 template <int D>
 __device__ __forceinline__ void store_rows(const Params &p, const Unit &u, int share, int row0, uint32_t tO, const State &st,
-                                           bool live, int token, const Seen &mask, const uint32_t *odd, float *turn) {
+                                           bool live, int token, const Seen &mask, const uint32_t *odd) {
     const int lane = threadIdx.x & 31;
     const bool whole = u.n == u.nb;
     const size_t row = whole ? ((size_t)u.b * p.Hkv + u.g) * p.rows + row0
@@ -495,46 +512,39 @@ __device__ __forceinline__ void store_rows(const Params &p, const Unit &u, int s
     const bool any = live && st.l != 0.f;  // (NaN stays NaN)
     const float f = 1.f / st.l;
 #pragma unroll 1
-    for (int col = 0; col < D; col += 32) {
-        uint32_t x[32];
-        tmem_ld32(tO + col, x);
+    for (int col = 0; col < D; col += 64) {
+        uint32_t x[2][32];
+        tmem_ld32(tO + col, x[0]);
+        tmem_ld32(tO + col + 32, x[1]);
         tmem_wait_ld();
-        float y[32];
 #pragma unroll
-        for (int i = 0; i < 32; ++i) y[i] = any ? __uint_as_float(x[i]) * f : 0.f;
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int i = 0; i < 32; ++i) x[h][i] = any ? __float_as_uint(__uint_as_float(x[h][i]) * f) : 0u;
+        if (lane >= rows) continue;
         if (whole) {
-            __syncwarp();
+            __nv_bfloat16 *to = p.o + (row + lane) * D + col;
 #pragma unroll
-            for (int g = 0; g < 4; ++g)
-                *reinterpret_cast<uint4 *>(turn + lane * kTurnStride + g * 4) =
-                    make_uint4(pack_bf16x2(y[8 * g], y[8 * g + 1]), pack_bf16x2(y[8 * g + 2], y[8 * g + 3]),
-                               pack_bf16x2(y[8 * g + 4], y[8 * g + 5]), pack_bf16x2(y[8 * g + 6], y[8 * g + 7]));
-            __syncwarp();
+            for (int h = 0; h < 2; ++h)
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                const int r = 8 * k + (lane >> 2);
-                if (r < rows)
-                    *reinterpret_cast<uint4 *>(p.o + (row + r) * D + col + (lane & 3) * 8) =
-                        *reinterpret_cast<const uint4 *>(turn + r * kTurnStride + (lane & 3) * 4);
-            }
+                for (int g = 0; g < 2; ++g) {
+                    uint32_t y[8];
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        y[i] = pack_bf16x2(__uint_as_float(x[h][16 * g + 2 * i]), __uint_as_float(x[h][16 * g + 2 * i + 1]));
+                    store_32(to + 32 * h + 16 * g, y, p.wide);
+                }
         } else {
+            float *to = p.part_o + (row + lane) * D + col;
 #pragma unroll
-            for (int half = 0; half < 2; ++half) {
-                __syncwarp();
+            for (int h = 0; h < 2; ++h)
 #pragma unroll
                 for (int g = 0; g < 4; ++g) {
-                    const float *z = y + half * 16 + g * 4;
-                    *reinterpret_cast<float4 *>(turn + lane * kTurnStride + g * 4) = make_float4(z[0], z[1], z[2], z[3]);
-                }
-                __syncwarp();
+                    uint32_t y[8];
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    const int r = 8 * k + (lane >> 2);
-                    if (r < rows)
-                        *reinterpret_cast<float4 *>(p.part_o + (row + r) * D + col + half * 16 + (lane & 3) * 4) =
-                            *reinterpret_cast<const float4 *>(turn + r * kTurnStride + (lane & 3) * 4);
+                    for (int i = 0; i < 8; ++i) y[i] = x[h][8 * g + i];
+                    store_32(to + 32 * h + 8 * g, y, p.wide);
                 }
-            }
         }
     }
     if (lane < rows) {
@@ -542,7 +552,7 @@ __device__ __forceinline__ void store_rows(const Params &p, const Unit &u, int s
         if (!whole) p.part_lse[row + lane] = L;
         else if (p.lse) p.lse[row + lane] = L * 0.69314718055994531f;
     }
-    if (__any_sync(0xffffffffu, lane < kMaskWords && odd[lane & (kMaskWords - 1)] != 0)) {  // behind the warp's stores
+    if (__any_sync(0xffffffffu, lane < kMaskWords && odd[lane & (kMaskWords - 1)] != 0)) {
         uint32_t seen[kMaskWords];
         mask.bits(p, u, token, any, seen);
 #pragma unroll 1
@@ -642,8 +652,7 @@ struct PairCfg {
     // barriers of a chain (S and P: a buffer each)
     static constexpr int kQFull = 0, kQEmpty = 1, kSFull = 2, kPFull = 4, kOFull = 6, kOEmpty = 7, kUFull = 8, kUEmpty = 10,
                          kDrain = 12, kKVFull = 13, kKVEmpty = 13 + kMaxStages, kNumBars = 13 + 2 * kMaxStages;
-    static constexpr int kTurnBytes = 8 * kTurnFloats * 4, kOddBytes = 2 * 4 * kMaskWords * 4;
-    static constexpr int kBarOffset = kTurnBytes + kOddBytes, kUnitOffset = (kBarOffset + 2 * kNumBars * 8 + 15) / 16 * 16;
+    static constexpr int kBarOffset = 2 * 4 * kMaskWords * 4, kUnitOffset = (kBarOffset + 2 * kNumBars * 8 + 15) / 16 * 16;
     static constexpr int kFixedBytes = kUnitOffset + 2 * 2 * kUnitInts * 4 + 16;
     static __host__ __device__ int q_bytes(int q_rows) { return q_rows * 128 * kChunks; }
     static __host__ __device__ int chain_bytes(int q_rows, int stages) { return q_bytes(q_rows) + stages * kKVBytes; }
@@ -676,7 +685,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t stages = p.stages;
     const int q_bytes = C::q_bytes(p.q_rows), chain_bytes = C::chain_bytes(p.q_rows, p.stages);
     uint8_t *sQ = smem + t * chain_bytes, *ring = sQ + q_bytes, *rest = smem + 2 * chain_bytes;
-    uint32_t *odd_rows = reinterpret_cast<uint32_t *>(rest + C::kTurnBytes) + t * 4 * kMaskWords;  // of four units in turn
+    uint32_t *odd_rows = reinterpret_cast<uint32_t *>(rest) + t * 4 * kMaskWords;  // of four units in turn
     uint64_t *all_bars = reinterpret_cast<uint64_t *>(rest + C::kBarOffset);
     volatile int *units = reinterpret_cast<volatile int *>(rest + C::kUnitOffset) + t * 2 * kUnitInts;
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(rest + C::kUnitOffset + 2 * 2 * kUnitInts * 4);
@@ -684,28 +693,16 @@ __global__ void __launch_bounds__(kThreads, 1)
     auto bar = [&](int i) { return smem_u32(all_bars + t * C::kNumBars + i); };
 
     griddep_launch_dependents();  // the merge waits for this grid to end
-    if (threadIdx.x == 0) {
-        for (int c = 0; c < 2; ++c) {
-            auto init = [&](int i, int n) { mbar_init(smem_u32(all_bars + c * C::kNumBars + i), n); };
-            init(C::kQFull, 1);
-            init(C::kQEmpty, 1);
-            for (int i = 0; i < 2; ++i) {
-                init(C::kSFull + i, 1);
-                init(C::kPFull + i, 4);
-                init(C::kUFull + i, 1);
-                init(C::kUEmpty + i, 1 + 4);
-            }
-            init(C::kOFull, 1);
-            init(C::kOEmpty, 4);
-            init(C::kDrain, 1);
-            for (uint32_t s = 0; s < stages; ++s) {
-                init(C::kKVFull + s, 1);
-                init(C::kKVEmpty + s, 1);
-            }
+    if (threadIdx.x >= 128) {  // a barrier a thread
+        const int i = int(threadIdx.x) - 128;
+        if (i < 2 * C::kNumBars) {
+            const int k = i % C::kNumBars;
+            mbar_init(smem_u32(all_bars + i), k == C::kPFull || k == C::kPFull + 1 || k == C::kOEmpty ? 4 : k == C::kUEmpty || k == C::kUEmpty + 1 ? 5 : 1);
         }
-        *abort_flag = 0;
+        if (i == 0) *abort_flag = 0;
         fence_mbar_init();
     }
+    static_assert(2 * C::kNumBars <= kThreads - 128, "one thread each");
     if (warp == 4 || warp == 8) odd_rows[lane] = 0;
     static_assert(4 * kMaskWords == 32, "one warp clears them");
     if (warp == 1) {
@@ -713,6 +710,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         tmem_relinquish();
     }
     Unit u = {};
+    Pages<kBlock> pages = {};
     int left = 0;
     if (warp == 0 || warp == 2) {
         if (lane == 0) {
@@ -722,7 +720,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         const Share s = share_of<kBlock>(p, share);
         left = share < p.shares ? s.left : 0;
-        if (left > 0) u = find_block<kBlock>(p, s.lo);
+        if (left > 0) {
+            u = find_block<kBlock>(p, s.lo);
+            pages.start(p, u);
+        }
     }
     tc_fence_before();
     __syncthreads();
@@ -741,8 +742,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (uint32_t qi = 0; ok; ++qi) {
                 const uint32_t qs = qi & 1;
                 u.n = left > 0 ? min(left, u.nb - u.j0) : 0;
-                Pages<kBlock> pages;
-                if (u.n > 0) pages.start(p, u);
+                if (u.n > 0 && qi > 0) pages.start(p, u);
                 if (p.table && qi > 0) u.holes = look_for_holes<kBlock>(p, u);
                 if (qi >= 2) ok = wait_warp(bar(C::kUEmpty + qs), ((qi >> 1) - 1) & 1, p.wait_ns, abort_flag);
                 if (!ok) break;
@@ -855,8 +855,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int quarter = warp & 3, row = quarter * 32 + lane, token = row % p.T;
         const uint32_t lanes = uint32_t(quarter * 32) << 16, tS0 = tmem + lanes, tO = tmem + lanes + 128;
         const bool has_rows = quarter * 32 < p.rows;  // of this warp; the others only keep step
-        float *turn = reinterpret_cast<float *>(rest) + (warp - 4) * kTurnFloats;
         Place at;  // of the next block's K
+        Seen mask;
         uint32_t s_odd = 0;
         bool ok = true;
         for (uint32_t qi = 0; ok; ++qi) {
@@ -868,8 +868,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_arrive_elect(bar(C::kUEmpty + qs));
             if (u.n == 0) break;
             const bool live = row < p.rows && token < u.tb;
-            Seen mask;
-            mask.load(p, u, token, live && (u.j0 + u.n) * kBlock > u.len);
+            if ((u.j0 + u.n) * kBlock > u.len) mask.load(p, u, token);
             Holes<kBlock> holes;
             holes.start(p, u);
             uint32_t *odd = odd_rows + (qi & 3) * kMaskWords;
@@ -922,7 +921,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             tc_fence_after();
             // (the next unit but one has none yet, and this warp's mates are all past the last one)
             if (quarter == 0 && lane < kMaskWords) odd_rows[((qi + 2) & 3) * kMaskWords + lane] = 0;
-            if (has_rows) store_rows<D>(p, u, share, quarter * 32, tO, st, live, token, mask, odd, turn);
+            if (has_rows) store_rows<D>(p, u, share, quarter * 32, tO, st, live, token, mask, odd);
             tc_fence_before();
             __syncwarp();
             mbar_arrive_elect(bar(C::kOEmpty));
@@ -944,7 +943,7 @@ struct RowsCfg {
     static constexpr int kQBytes = kTileM * D * 2, kKVBytes = kBlock * D * 2;
     static constexpr int kStages = D == 128 ? 4 : 8;
     static constexpr int kOCol = 2 * kTileM;
-    static constexpr int kTurnOffset = 2 * kQBytes + kStages * kKVBytes, kOddOffset = kTurnOffset + 8 * kTurnFloats * 4;
+    static constexpr int kOddOffset = 2 * kQBytes + kStages * kKVBytes;
     static constexpr int kBarOffset = kOddOffset + 4 * kMaskWords * 4;
     static constexpr int kQFull = 0, kQEmpty = 2, kSFull = 4, kPFull = 6, kOFull = 8, kOEmpty = 10, kUFull = 12, kUEmpty = 14,
                          kDrain = 16, kKVFull = 17, kKVEmpty = 17 + kStages, kNumBars = 17 + 2 * kStages;
@@ -973,23 +972,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     auto bar = [&](int i) { return smem_u32(bars + i); };
 
     griddep_launch_dependents();  // the merge waits for this grid to end
-    if (threadIdx.x == 0) {
-        for (int t = 0; t < 2; ++t) {
-            mbar_init(bar(C::kQFull + t), 1);
-            mbar_init(bar(C::kQEmpty + t), 1);
-            mbar_init(bar(C::kSFull + t), 1);
-            mbar_init(bar(C::kPFull + t), 4);
-            mbar_init(bar(C::kOFull + t), 1);
-            mbar_init(bar(C::kOEmpty + t), 4);
-            mbar_init(bar(C::kUFull + t), 1);
-            mbar_init(bar(C::kUEmpty + t), 3 + 8);  // the K, V and MMA warps, the softmax warps
+    if (threadIdx.x >= 128) {  // a barrier a thread
+        const int i = int(threadIdx.x) - 128;
+        if (i < C::kNumBars) {
+            const bool four = (i >= C::kPFull && i < C::kPFull + 2) || (i >= C::kOEmpty && i < C::kOEmpty + 2);
+            // (a unit's slot: the K, V and MMA warps, the softmax warps)
+            mbar_init(bar(i), four ? 4 : i >= C::kUEmpty && i < C::kUEmpty + 2 ? 3 + 8 : 1);
         }
-        mbar_init(bar(C::kDrain), 1);
-        for (int s = 0; s < C::kStages; ++s) {
-            mbar_init(bar(C::kKVFull + s), 1);
-            mbar_init(bar(C::kKVEmpty + s), 1);
-        }
-        *abort_flag = 0;
+        if (i == 0) *abort_flag = 0;
         fence_mbar_init();
     }
     if (warp == 4) odd_rows[lane] = 0;
@@ -1163,8 +1153,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t tS = tmem + lanes + t * kTileM, tO = tmem + lanes + C::kOCol + t * D;
         const bool has_rows = row0 < p.rows;  // of this warp; the others only keep step
         const bool frees = quarter == 0 && t == (second ? 1 : 0);  // K's slots: the last chain to see S
-        float *turn = reinterpret_cast<float *>(smem + C::kTurnOffset) + (warp - 4) * kTurnFloats;
         uint32_t blocks = 0, fills = 0;
+        Seen mask;
         bool ok = true;
         for (uint32_t qi = 0; ok; ++qi) {
             const uint32_t qs = qi & 1;
@@ -1176,8 +1166,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (u.n == 0) break;
             if (t > 0 && !second) continue;
             const bool live = row < p.rows && token < u.tb;
-            Seen mask;
-            mask.load(p, u, token, live && (u.j0 + u.n) * kBlock > u.len);
+            if ((u.j0 + u.n) * kBlock > u.len) mask.load(p, u, token);
             Holes<kBlock> holes;
             holes.start(p, u);
             uint32_t *odd = odd_rows + (qi & 3) * kMaskWords;
@@ -1219,7 +1208,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             tc_fence_after();
             // (the next unit but one has none yet; of the last one's, the other tile is past its products, hence its stores)
             if (t == 0 && quarter == 0 && lane < kMaskWords) odd_rows[((qi + 2) & 3) * kMaskWords + lane] = 0;
-            if (has_rows) store_rows<D>(p, u, share, row0, tO, st, live, token, mask, odd, turn);
+            if (has_rows) store_rows<D>(p, u, share, row0, tO, st, live, token, mask, odd);
             tc_fence_before();
             __syncwarp();
             mbar_arrive_elect(bar(C::kOEmpty + t));
@@ -1234,51 +1223,82 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
 }
 
-// The rows of the pair that goes on behind share blockIdx.x, a warp each: their
-// partials (2 x + 1, 2 (x + 1), 2 (x + 2), ...) by the log-sum-exps' weights.
-template <int D>
+// Rows of the pair that goes on behind share blockIdx.x: their partials (2 x + 1, 2 (x + 1), 2 (x + 2), ...) by the
+// log-sum-exps' weights.  A warp takes kRows rows at once, with the loads of all of them in flight; kSplit warps share
+// the partials of the same rows.
+template <int D, int kSplit>
 __global__ void __launch_bounds__(kMergeWarps * 32) merge_kernel(const Params p) {
-    constexpr int kCols = D / 32, kAhead = 8;
+    constexpr int kCols = D / 32, kRows = 4, kAhead = 2;
+    using Vec = typename std::conditional<kCols == 4, float4, float2>::type;
+    __shared__ float acc_sh[kSplit > 1 ? kSplit : 1][kRows][D], sum_sh[kSplit > 1 ? kSplit : 1][kRows];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, part = warp % kSplit;
+    const int row0 = (blockIdx.y * (kMergeWarps / kSplit) + warp / kSplit) * kRows;
     griddep_wait();
     const int4 cut = p.cuts[blockIdx.x];
-    const int row = blockIdx.y * kMergeWarps + (threadIdx.x >> 5), lane = threadIdx.x & 31;
-    if (cut.z == 0 || row >= p.rows) return;
-    auto at = [&](int i) { return (size_t)(2 * (blockIdx.x + i) + (i == 0 ? 1 : 0)) * p.rows + row; };
-    auto lse = [&](int i) { return i < cut.z ? p.part_lse[at(i)] : -INFINITY; };
-    float top = -INFINITY, sum = 0.f, acc[kCols] = {};
-    for (int i = lane; i < cut.z; i += 32) top = fmaxf(top, lse(i));
+    if (cut.z == 0 || (kSplit == 1 && row0 >= p.rows)) return;
+    const int rows = min(kRows, p.rows - row0);  // (below 1: none, but the warp keeps step)
+    auto at = [&](int i, int r) { return (size_t)(2 * (blockIdx.x + i) + (i == 0 ? 1 : 0)) * p.rows + row0 + r; };
+    // Lane 8 r + k: row r's partials k, k + 8, ...
+    const int r8 = lane >> 3, k8 = lane & 7;
+    float top = -INFINITY;
+    for (int i = k8; i < cut.z; i += 8)
+        if (r8 < rows) top = fmaxf(top, p.part_lse[at(i, r8)]);
 #pragma unroll
-    for (int off = 16; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
+    for (int off = 4; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
     const float ref = top == -INFINITY ? 0.f : top;
-    for (int i0 = 0; i0 < cut.z; i0 += kAhead) {
-        float v[kAhead][kCols], w[kAhead];
+    float acc[kRows][kCols] = {}, sum = 0.f;
+    for (int i0 = part * kAhead; i0 < cut.z; i0 += kSplit * kAhead) {
+        Vec v[kAhead][kRows];
 #pragma unroll
-        for (int k = 0; k < kAhead; ++k) {
-            w[k] = lse(i0 + k);
-            if (i0 + k < cut.z) {
-                const float *x = p.part_o + at(i0 + k) * D + lane * kCols;
+        for (int k = 0; k < kAhead; ++k)
 #pragma unroll
-                for (int c = 0; c < kCols; ++c) v[k][c] = x[c];
+            for (int r = 0; r < kRows; ++r)
+                if (i0 + k < cut.z && r < rows) v[k][r] = reinterpret_cast<const Vec *>(p.part_o + at(i0 + k, r) * D)[lane];
+        const float w = k8 < kAhead && i0 + k8 < cut.z && r8 < rows ? fast_exp2(p.part_lse[at(i0 + k8, r8)] - ref) : 0.f;
+        sum += w;
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k)
+#pragma unroll
+            for (int r = 0; r < kRows; ++r) {
+                const float f = __shfl_sync(0xffffffffu, w, 8 * r + k);
+                if (f == 0.f) continue;  // an empty partial adds nothing (and one past the last is not there)
+                const float *x = reinterpret_cast<const float *>(&v[k][r]);
+#pragma unroll
+                for (int c = 0; c < kCols; ++c) acc[r][c] += f * x[c];
             }
-        }
+    }
 #pragma unroll
-        for (int k = 0; k < kAhead; ++k) {
-            w[k] = fast_exp2(w[k] - ref);
-            sum += w[k];
-            if (i0 + k < cut.z)
+    for (int off = 4; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
+    if constexpr (kSplit > 1) {
 #pragma unroll
-                for (int c = 0; c < kCols; ++c) acc[c] += w[k] * v[k][c];
+        for (int r = 0; r < kRows; ++r) reinterpret_cast<Vec *>(acc_sh[part][r])[lane] = *reinterpret_cast<Vec *>(acc[r]);
+        if (k8 == 0) sum_sh[part][r8] = sum;
+        __syncthreads();
+        if (part > 0) return;
+        for (int w = 1; w < kSplit; ++w) {
+            sum += sum_sh[w][r8];
+#pragma unroll
+            for (int r = 0; r < kRows; ++r) {
+                const Vec x = reinterpret_cast<const Vec *>(acc_sh[w][r])[lane];
+#pragma unroll
+                for (int c = 0; c < kCols; ++c) acc[r][c] += reinterpret_cast<const float *>(&x)[c];
+            }
         }
     }
     const float inv = sum == 0.f ? 0.f : 1.f / sum;  // NaN stays NaN
-    const size_t out = ((size_t)cut.x * p.Hkv + cut.y) * p.rows + row;
-    uint32_t packed[kCols / 2];
+    const size_t out = ((size_t)cut.x * p.Hkv + cut.y) * p.rows + row0;
 #pragma unroll
-    for (int c = 0; c < kCols / 2; ++c) packed[c] = pack_bf16x2(acc[2 * c] * inv, acc[2 * c + 1] * inv);
-    __nv_bfloat16 *o = p.o + out * D + lane * kCols;
-    if constexpr (kCols == 4) *reinterpret_cast<uint2 *>(o) = make_uint2(packed[0], packed[1]);
-    else *reinterpret_cast<uint32_t *>(o) = packed[0];
-    if (lane == 0 && p.lse) p.lse[out] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * 0.69314718055994531f;
+    for (int r = 0; r < kRows; ++r) {
+        const float f = __shfl_sync(0xffffffffu, inv, 8 * r);
+        if (r >= rows) continue;
+        uint32_t packed[kCols / 2];
+#pragma unroll
+        for (int c = 0; c < kCols / 2; ++c) packed[c] = pack_bf16x2(acc[r][2 * c] * f, acc[r][2 * c + 1] * f);
+        __nv_bfloat16 *o = p.o + (out + r) * D + lane * kCols;
+        if constexpr (kCols == 4) *reinterpret_cast<uint2 *>(o) = make_uint2(packed[0], packed[1]);
+        else *reinterpret_cast<uint32_t *>(o) = packed[0];
+    }
+    if (k8 == 0 && r8 < rows && p.lse) p.lse[out + r8] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * 0.69314718055994531f;
 }
 
 struct Layout {
@@ -1336,6 +1356,7 @@ int launch(const DecodeTreeLaunch &a, const Layout &l, cudaStream_t stream) {
     p.max_pages = a.max_pages;
     p.mt = l.mt;
     p.shares = l.shares;
+    p.wide = ((reinterpret_cast<uintptr_t>(a.o) | reinterpret_cast<uintptr_t>(a.workspace)) & 31u) == 0;
     p.q_rows = q_rows;
     p.stages = PairCfg<D>::stages_for(q_rows);
     p.scale_log2 = a.scale * 1.4426950408889634f;
@@ -1359,8 +1380,11 @@ int launch(const DecodeTreeLaunch &a, const Layout &l, cudaStream_t stream) {
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return note_cuda_error(e, "kernel launch (drafted tokens)");
     if (l.shares == 1) return 0;  // nothing is cut
-    e = dec::launch_programmatic(merge_kernel<D>, dim3(unsigned(l.shares), unsigned((rows + kMergeWarps - 1) / kMergeWarps)),
-                                 dim3(kMergeWarps * 32), 0, stream, p);
+    // Few pairs are cut into many partials each: then all warps of a block take a part of them.
+    const bool split = l.shares >= 8LL * a.B * a.Hkv;
+    const int per = split ? 4 : 4 * kMergeWarps;
+    e = dec::launch_programmatic(split ? merge_kernel<D, kMergeWarps> : merge_kernel<D, 1>,
+                                 dim3(unsigned(l.shares), unsigned((rows + per - 1) / per)), dim3(kMergeWarps * 32), 0, stream, p);
     return e == cudaSuccess ? 0 : note_cuda_error(e, "merge_kernel (drafted tokens) launch");
 }
 
