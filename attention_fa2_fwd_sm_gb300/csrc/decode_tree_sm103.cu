@@ -517,11 +517,10 @@ __device__ __forceinline__ void store_rows(const Params &p, const Unit &u, int s
         tmem_ld32(tO + col, x[0]);
         tmem_ld32(tO + col + 32, x[1]);
         tmem_wait_ld();
-#pragma unroll
-        for (int h = 0; h < 2; ++h)
-#pragma unroll
-            for (int i = 0; i < 32; ++i) x[h][i] = any ? __float_as_uint(__uint_as_float(x[h][i]) * f) : 0u;
         if (lane >= rows) continue;
+        auto scaled = [&](int h, int i, float &a, float &b) {
+            ffma2(a, b, __uint_as_float(x[h][i]), __uint_as_float(x[h][i + 1]), f, f, -0.f, -0.f);
+        };
         if (whole) {
             __nv_bfloat16 *to = p.o + (row + lane) * D + col;
 #pragma unroll
@@ -530,8 +529,11 @@ __device__ __forceinline__ void store_rows(const Params &p, const Unit &u, int s
                 for (int g = 0; g < 2; ++g) {
                     uint32_t y[8];
 #pragma unroll
-                    for (int i = 0; i < 8; ++i)
-                        y[i] = pack_bf16x2(__uint_as_float(x[h][16 * g + 2 * i]), __uint_as_float(x[h][16 * g + 2 * i + 1]));
+                    for (int i = 0; i < 8; ++i) {
+                        float a, b;
+                        scaled(h, 16 * g + 2 * i, a, b);
+                        y[i] = any ? pack_bf16x2(a, b) : 0u;
+                    }
                     store_32(to + 32 * h + 16 * g, y, p.wide);
                 }
         } else {
@@ -542,7 +544,12 @@ __device__ __forceinline__ void store_rows(const Params &p, const Unit &u, int s
                 for (int g = 0; g < 4; ++g) {
                     uint32_t y[8];
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) y[i] = x[h][8 * g + i];
+                    for (int i = 0; i < 8; i += 2) {
+                        float a, b;
+                        scaled(h, 8 * g + i, a, b);
+                        y[i] = any ? __float_as_uint(a) : 0u;
+                        y[i + 1] = any ? __float_as_uint(b) : 0u;
+                    }
                     store_32(to + 32 * h + 8 * g, y, p.wide);
                 }
         }
@@ -810,6 +817,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tc_fence_after();
                 issue_qk<D>(tmem + buf * kBlock, dQ, q_chunk, dK + uint64_t(k.slot * (C::kKVBytes >> 4)), C::kChunkBytes, kIdescQK);
                 tc_commit_elect(bar(C::kSFull + buf));
+                tc_commit_elect(bar(C::kKVEmpty + k.slot));
                 k.next(stages);
                 k.next(stages);
             };
@@ -881,7 +889,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                 ok = wait_warp(bar(C::kSFull + buf), s_odd >> buf & 1, p.wait_ns, abort_flag);
                 if (!ok) break;
                 s_odd ^= 1u << buf;
-                if (quarter == 0) mbar_arrive_elect(bar(C::kKVEmpty + at.slot));  // S complete: K's slot is free
                 at.next(stages);
                 if (has_rows) {
                     const uint32_t tS = tS0 + buf * kBlock;
@@ -1238,30 +1245,49 @@ __global__ void __launch_bounds__(kMergeWarps * 32) merge_kernel(const Params p)
     if (cut.z == 0 || (kSplit == 1 && row0 >= p.rows)) return;
     const int rows = min(kRows, p.rows - row0);  // (below 1: none, but the warp keeps step)
     auto at = [&](int i, int r) { return (size_t)(2 * (blockIdx.x + i) + (i == 0 ? 1 : 0)) * p.rows + row0 + r; };
-    // Lane 8 r + k: row r's partials k, k + 8, ...
+    // Lane 8 r + k: row r's partials k, k + 8, ...; the first kHeld of them stay in registers.
+    constexpr int kHeld = 5;
     const int r8 = lane >> 3, k8 = lane & 7;
-    float top = -INFINITY;
-    for (int i = k8; i < cut.z; i += 8)
+    Vec v[kAhead][kRows];
+    auto fetch = [&](int i0) {
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k)
+#pragma unroll
+            for (int r = 0; r < kRows; ++r)
+                if (i0 + k < cut.z && r < rows) v[k][r] = reinterpret_cast<const Vec *>(p.part_o + at(i0 + k, r) * D)[lane];
+    };
+    float held[kHeld], top = -INFINITY;
+#pragma unroll
+    for (int q = 0; q < kHeld; ++q) held[q] = k8 + 8 * q < cut.z && r8 < rows ? p.part_lse[at(k8 + 8 * q, r8)] : -INFINITY;
+    fetch(part * kAhead);  // (does not depend on the weights)
+#pragma unroll
+    for (int q = 0; q < kHeld; ++q) top = fmaxf(top, held[q]);
+    for (int i = k8 + 8 * kHeld; i < cut.z; i += 8)
         if (r8 < rows) top = fmaxf(top, p.part_lse[at(i, r8)]);
 #pragma unroll
     for (int off = 4; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
     const float ref = top == -INFINITY ? 0.f : top;
     float acc[kRows][kCols] = {}, sum = 0.f;
     for (int i0 = part * kAhead; i0 < cut.z; i0 += kSplit * kAhead) {
-        Vec v[kAhead][kRows];
+        if (i0 > part * kAhead) fetch(i0);
+        // The weight of partial i0 + k is with lane (i0 + k) % 8 of the row's eight.
+        const int mine = i0 + ((k8 - i0) & 7);
+        float w = -INFINITY;
+        if (mine < i0 + kAhead && mine < cut.z) {
+            const int q = mine >> 3;
 #pragma unroll
-        for (int k = 0; k < kAhead; ++k)
-#pragma unroll
-            for (int r = 0; r < kRows; ++r)
-                if (i0 + k < cut.z && r < rows) v[k][r] = reinterpret_cast<const Vec *>(p.part_o + at(i0 + k, r) * D)[lane];
-        const float w = k8 < kAhead && i0 + k8 < cut.z && r8 < rows ? fast_exp2(p.part_lse[at(i0 + k8, r8)] - ref) : 0.f;
+            for (int h = 0; h < kHeld; ++h)
+                if (q == h) w = held[h];
+            if (q >= kHeld && r8 < rows) w = p.part_lse[at(mine, r8)];
+        }
+        w = fast_exp2(w - ref);
         sum += w;
 #pragma unroll
         for (int k = 0; k < kAhead; ++k)
 #pragma unroll
             for (int r = 0; r < kRows; ++r) {
-                const float f = __shfl_sync(0xffffffffu, w, 8 * r + k);
-                if (f == 0.f) continue;  // an empty partial adds nothing (and one past the last is not there)
+                const float f = __shfl_sync(0xffffffffu, w, 8 * r + ((i0 + k) & 7));
+                if (f == 0.f || i0 + k >= cut.z) continue;  // an empty partial adds nothing
                 const float *x = reinterpret_cast<const float *>(&v[k][r]);
 #pragma unroll
                 for (int c = 0; c < kCols; ++c) acc[r][c] += f * x[c];
