@@ -12,15 +12,17 @@
 //
 // A CTA an SM, persistent: warps that load, issue MMAs and plan, and two chains of
 // four softmax warps, as in fwd_kernel.cuh.
-//   pairs_kernel (R <= 128): each chain is a pipeline of its own, with a loading and
-//     an issuing warp, a ring of 64-key blocks, and two score buffers, so that the
-//     products' latency is not in its way.  The chains work on different keys; when
-//     one starts or ends a pair, the other one keeps the memory busy.
+//   pairs_kernel (R <= 128): each chain is a pipeline of its own, with loading and
+//     issuing warps, a ring of 64-key blocks, and two score buffers, so that the
+//     products' latency is not in its way.  The chains take the two halves of the CTA's
+//     share, one from its begin on, one from its end back: when one starts or ends a
+//     pair, the other one keeps the memory busy, and the pair that both have a part of
+//     comes last in both, so that they add up their states in the CTA.
 //   rows_kernel (R > 128): the chains hold two tiles of rows, and both visit every
 //     block of 128 keys in the ring; units of 256 rows, `mt` units a KV head, side by
 //     side on mt SMs so that all but one find the keys in L2.
 // The blocks of all (sequence, KV head) pairs, in that order, are cut into equal
-// shares, one a chain or a group of mt CTAs: nothing depends on how ragged the
+// shares, one a CTA or group of mt CTAs: nothing depends on how ragged the
 // lengths are.  A pair that lies in one share is written out at once; one that is cut
 // goes through partials: share s writes its first segment's to slot 2 s (a pair
 // that began before) and its last one's to 2 s + 1 (a pair that goes on), and
@@ -107,13 +109,14 @@ struct Params {
 
 // A piece of work: blocks [j0, j0 + n) of the nb blocks of pair (b, g); n = 0: the end.  holes: some of its entries may be
 // no page.
+// joint: the other chain has the rest of the CTA's part of the pair.
 struct Unit {
-    int b, g, j0, n, nb, len, tb, keys, holes;
+    int b, g, j0, n, nb, len, tb, keys, holes, joint;
     __device__ __forceinline__ void put(volatile int *e) const {
-        e[0] = b, e[1] = g, e[2] = j0, e[3] = n, e[4] = nb, e[5] = len, e[6] = tb, e[7] = keys, e[8] = holes;
+        e[0] = b, e[1] = g, e[2] = j0, e[3] = n, e[4] = nb, e[5] = len, e[6] = tb, e[7] = keys, e[8] = holes, e[9] = joint;
     }
     __device__ __forceinline__ void get(const volatile int *e) {
-        b = e[0], g = e[1], j0 = e[2], n = e[3], nb = e[4], len = e[5], tb = e[6], keys = e[7], holes = e[8];
+        b = e[0], g = e[1], j0 = e[2], n = e[3], nb = e[4], len = e[5], tb = e[6], keys = e[7], holes = e[8], joint = e[9];
     }
 };
 
@@ -223,6 +226,20 @@ __device__ __forceinline__ void next_pair(const Params &p, Unit &u) {
         u.keys = keys_of(p, u.len, u.tb);
     } while (u.keys == 0);
     u.nb = blocks_of<kBlock>(u.keys);
+}
+
+// Back to the end of the pair before; call only while a block is left there.
+template <int kBlock>
+__device__ __forceinline__ void previous_pair(const Params &p, Unit &u) {
+    if (--u.g < 0) {
+        u.g = p.Hkv - 1;
+        do {
+            load_sequence(p, --u.b, u.len, u.tb);
+            u.keys = keys_of(p, u.len, u.tb);
+        } while (u.keys == 0);
+        u.nb = blocks_of<kBlock>(u.keys);
+    }
+    u.j0 = u.nb;
 }
 
 // Whether an entry of the unit's blocks is no page (all lanes of the calling warp).
@@ -448,6 +465,8 @@ struct Scores {
 struct State {
     float m, l, corr;
     __device__ __forceinline__ void clear() { m = -INFINITY, l = 0.f; }
+    // Log-sum-exp in log2 units; -inf for a row without a key.
+    __device__ __forceinline__ float total(bool live) const { return live && l != 0.f ? m + __log2f(l) : -INFINITY; }
     // Adds a block; true (for all lanes) if the maximum of a row moved, so that its output has to be scaled by corr.
     // Rows past the last one (`use` false) hold anything.
     template <int kBlock>
@@ -499,32 +518,35 @@ __device__ __forceinline__ void store_32(void *to, const uint32_t (&x)[8], bool 
     }
 }
 
-// A warp's 32 rows of a finished unit, rows [row0, row0 + 32) of the pair, a thread each, from the accumulator tO in TMEM:
-// to the outputs where the unit is all of the pair, else to the partial of share `share`.
-template <int D>
-__device__ __forceinline__ void store_rows(const Params &p, const Unit &u, int share, int row0, uint32_t tO, const State &st,
-                                           bool live, int token, const Seen &mask, const uint32_t *odd) {
+// A warp's 32 rows of a finished unit, rows [row0, row0 + 32) of the pair, a thread each: columns [col0, col0 + kCols) of
+// the accumulator at tO in TMEM or, where there are two (kTwo), of both, kOther columns apart, times f (and f2): to the
+// outputs where the unit is all of the pair (`whole`), else to row `part` and so on of the partials.  L: the row's
+// log-sum-exp in log2 units, -inf if it has none; odd: drafted rows with elements left out.
+template <int kCols, int D, bool kTwo, int kOther>
+__device__ __forceinline__ void store_rows(const Params &p, const Unit &u, bool whole, size_t part, int row0, uint32_t tO,
+                                           int col0, float f, float f2, float L, int token, bool live, const Seen &mask,
+                                           const uint32_t *odd, const uint32_t *odd2) {
     const int lane = threadIdx.x & 31;
-    const bool whole = u.n == u.nb;
-    const size_t row = whole ? ((size_t)u.b * p.Hkv + u.g) * p.rows + row0
-                             : (size_t)(2 * share + (u.j0 > 0 ? 0 : 1)) * p.rows + row0;
+    const size_t row = whole ? ((size_t)u.b * p.Hkv + u.g) * p.rows + row0 : part + row0;
     const int rows = p.rows - row0;  // in use, if below 32
-    const bool any = live && st.l != 0.f;  // (NaN stays NaN)
-    const float f = 1.f / st.l;
+    const bool any = L != -INFINITY;  // (NaN stays NaN)
 #pragma unroll 1
-    for (int col = 0; col < D; col += 64) {
+    for (int col = col0; col < col0 + kCols; col += 32 * (kTwo || kCols < 64 ? 1 : 2)) {
+        constexpr int kHalves = kTwo || kCols < 64 ? 1 : 2;
         uint32_t x[2][32];
         tmem_ld32(tO + col, x[0]);
-        tmem_ld32(tO + col + 32, x[1]);
+        if constexpr (kTwo || kHalves == 2) tmem_ld32(tO + col + (kTwo ? kOther : 32), x[1]);
         tmem_wait_ld();
         if (lane >= rows) continue;
         auto scaled = [&](int h, int i, float &a, float &b) {
-            ffma2(a, b, __uint_as_float(x[h][i]), __uint_as_float(x[h][i + 1]), f, f, -0.f, -0.f);
+            float c = -0.f, d = -0.f;
+            if constexpr (kTwo) ffma2(c, d, __uint_as_float(x[1][i]), __uint_as_float(x[1][i + 1]), f2, f2, -0.f, -0.f);
+            ffma2(a, b, __uint_as_float(x[h][i]), __uint_as_float(x[h][i + 1]), f, f, c, d);
         };
         if (whole) {
             __nv_bfloat16 *to = p.o + (row + lane) * D + col;
 #pragma unroll
-            for (int h = 0; h < 2; ++h)
+            for (int h = 0; h < kHalves; ++h)
 #pragma unroll
                 for (int g = 0; g < 2; ++g) {
                     uint32_t y[8];
@@ -539,7 +561,7 @@ __device__ __forceinline__ void store_rows(const Params &p, const Unit &u, int s
         } else {
             float *to = p.part_o + (row + lane) * D + col;
 #pragma unroll
-            for (int h = 0; h < 2; ++h)
+            for (int h = 0; h < kHalves; ++h)
 #pragma unroll
                 for (int g = 0; g < 4; ++g) {
                     uint32_t y[8];
@@ -554,26 +576,31 @@ __device__ __forceinline__ void store_rows(const Params &p, const Unit &u, int s
                 }
         }
     }
-    if (lane < rows) {
-        const float L = any ? st.m + __log2f(st.l) : -INFINITY;
+    if (lane < rows && col0 == 0) {
         if (!whole) p.part_lse[row + lane] = L;
         else if (p.lse) p.lse[row + lane] = L * 0.69314718055994531f;
     }
-    if (__any_sync(0xffffffffu, lane < kMaskWords && odd[lane & (kMaskWords - 1)] != 0)) {
+    const uint32_t here = lane < kMaskWords ? odd[lane] | odd2[lane] : 0u;
+    if (__any_sync(0xffffffffu, here != 0)) {
         uint32_t seen[kMaskWords];
-        mask.bits(p, u, token, any, seen);
+        mask.bits(p, u, token, live && any, seen);
 #pragma unroll 1
         for (int w = 0; w < kMaskWords; ++w)
-            for (uint32_t bits = odd[w] & mask_bits(seen, 32 * w); bits; bits &= bits - 1) {
+            for (uint32_t bits = (odd[w] | odd2[w]) & mask_bits(seen, 32 * w); bits; bits &= bits - 1) {
                 const int key = u.len + 32 * w + __ffs(bits) - 1;
                 const int page = p.table ? p.table[(size_t)u.b * p.max_pages + (key >> p.shift)] : u.b;
                 const int in = p.table ? key & (p.page_size - 1) : key;
-                const __nv_bfloat16 *v = p.v + (((size_t)page * p.Hkv + u.g) * p.page_size + in) * D;
-                if (whole) add_odd(p.o + (row + lane) * D, v, D);
-                else add_odd(p.part_o + (row + lane) * D, v, D);
+                const __nv_bfloat16 *v = p.v + (((size_t)page * p.Hkv + u.g) * p.page_size + in) * D + col0;
+                if (whole) add_odd(p.o + (row + lane) * D + col0, v, kCols);
+                else add_odd(p.part_o + (row + lane) * D + col0, v, kCols);
             }
         __syncwarp();
     }
+}
+
+// Row of the partials that a cut unit of share `share`, whose first block is j0, begins at.
+__device__ __forceinline__ size_t part_row(const Params &p, int share, int j0) {
+    return (size_t)(2 * share + (j0 > 0 ? 0 : 1)) * p.rows;
 }
 
 // A softmax warp's look at the pages of a unit's blocks, one block ahead: lane i at page i of the block.
@@ -658,8 +685,12 @@ struct PairCfg {
     static constexpr int kMaxStages = 12;
     // barriers of a chain (S and P: a buffer each)
     static constexpr int kQFull = 0, kQEmpty = 1, kSFull = 2, kPFull = 4, kOFull = 6, kOEmpty = 7, kUFull = 8, kUEmpty = 10,
-                         kDrain = 12, kKVFull = 13, kKVEmpty = 13 + kMaxStages, kNumBars = 13 + 2 * kMaxStages;
-    static constexpr int kBarOffset = 2 * 4 * kMaskWords * 4, kUnitOffset = (kBarOffset + 2 * kNumBars * 8 + 15) / 16 * 16;
+                         kDrain = 12, kJoint = 13, kKVFull = 14, kKVEmpty = 14 + kMaxStages, kNumBars = 14 + 2 * kMaxStages;
+    // 16 warps: 512 threads x 128 registers at launch are shared out anew.
+    static constexpr int kThreads = 512, kCtrlRegs = 88, kSoftmaxRegs = 160;
+    static_assert(256 * kCtrlRegs + 256 * kSoftmaxRegs <= 512 * 128, "register split");
+    static constexpr int kStateOffset = 2 * 4 * kMaskWords * 4;  // the chains' states of a joint unit, and its parts
+    static constexpr int kBarOffset = kStateOffset + 2 * kTileM * 8 + 32, kUnitOffset = (kBarOffset + 2 * kNumBars * 8 + 15) / 16 * 16;
     static constexpr int kFixedBytes = kUnitOffset + 2 * 2 * kUnitInts * 4 + 16;
     static __host__ __device__ int q_bytes(int q_rows) { return q_rows * 128 * kChunks; }
     static __host__ __device__ int chain_bytes(int q_rows, int stages) { return q_bytes(q_rows) + stages * kKVBytes; }
@@ -679,7 +710,7 @@ struct Place {
 };
 
 template <int D>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(PairCfg<D>::kThreads, 1)
     pairs_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                  const __grid_constant__ CUtensorMap tmV, const Params p) {
     using C = PairCfg<D>;
@@ -687,12 +718,17 @@ __global__ void __launch_bounds__(kThreads, 1)
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int t = warp < 4 ? warp >> 1 : (warp - 4) >> 2;  // chain
-    const int share = t * gridDim.x + blockIdx.x;
+    // Per chain: warps that plan and load Q and K, that load V, that issue MMAs, one to spare; then the softmax warps.
+    const int t = warp >> 2 & 1, role = warp < 8 ? warp & 3 : 4;
+    enum { kLoadK, kLoadV, kIssue, kSpare, kSoftmax };
+    const int share = blockIdx.x;
     const uint32_t stages = p.stages;
     const int q_bytes = C::q_bytes(p.q_rows), chain_bytes = C::chain_bytes(p.q_rows, p.stages);
     uint8_t *sQ = smem + t * chain_bytes, *ring = sQ + q_bytes, *rest = smem + 2 * chain_bytes;
-    uint32_t *odd_rows = reinterpret_cast<uint32_t *>(rest) + t * 4 * kMaskWords;  // of four units in turn
+    uint32_t *all_odd = reinterpret_cast<uint32_t *>(rest);  // [chain][four units in turn]
+    uint32_t *odd_rows = all_odd + t * 4 * kMaskWords;
+    float2 *states = reinterpret_cast<float2 *>(rest + C::kStateOffset);  // [chain][row]
+    volatile int *parts = reinterpret_cast<volatile int *>(states + 2 * kTileM);  // [chain]: first block, blocks, which of the four units in turn
     uint64_t *all_bars = reinterpret_cast<uint64_t *>(rest + C::kBarOffset);
     volatile int *units = reinterpret_cast<volatile int *>(rest + C::kUnitOffset) + t * 2 * kUnitInts;
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(rest + C::kUnitOffset + 2 * 2 * kUnitInts * 4);
@@ -700,98 +736,138 @@ __global__ void __launch_bounds__(kThreads, 1)
     auto bar = [&](int i) { return smem_u32(all_bars + t * C::kNumBars + i); };
 
     griddep_launch_dependents();  // the merge waits for this grid to end
-    if (threadIdx.x >= 128) {  // a barrier a thread
-        const int i = int(threadIdx.x) - 128;
+    if (threadIdx.x >= 256) {  // a barrier a thread
+        const int i = int(threadIdx.x) - 256;
         if (i < 2 * C::kNumBars) {
             const int k = i % C::kNumBars;
-            mbar_init(smem_u32(all_bars + i), k == C::kPFull || k == C::kPFull + 1 || k == C::kOEmpty ? 4 : k == C::kUEmpty || k == C::kUEmpty + 1 ? 5 : 1);
+            const bool four = k == C::kPFull || k == C::kPFull + 1 || k == C::kOEmpty;
+            // (a unit's slot: the V and MMA warps, the softmax warps)
+            mbar_init(smem_u32(all_bars + i), four ? 4 : k == C::kUEmpty || k == C::kUEmpty + 1 ? 2 + 4 : k == C::kJoint ? 8 : 1);
         }
         if (i == 0) *abort_flag = 0;
         fence_mbar_init();
     }
-    static_assert(2 * C::kNumBars <= kThreads - 128, "one thread each");
-    if (warp == 4 || warp == 8) odd_rows[lane] = 0;
+    static_assert(2 * C::kNumBars <= 256, "one thread each");
+    if (role == kSoftmax && (warp & 3) == 0) odd_rows[lane] = 0;
     static_assert(4 * kMaskWords == 32, "one warp clears them");
-    if (warp == 1) {
+    if (role == kIssue && t == 0) {
         tmem_alloc(smem_u32(tmem_slot), kTmemCols);
         tmem_relinquish();
     }
     Unit u = {};
     Pages<kBlock> pages = {};
     int left = 0;
-    if (warp == 0 || warp == 2) {
+    bool two = false;  // whether both chains have blocks
+    if (role == kLoadK) {
         if (lane == 0) {
             tma_prefetch_desc(&tmQ);
             tma_prefetch_desc(&tmK);
             tma_prefetch_desc(&tmV);
         }
+        // Chain 0 takes the share's first half, from its begin on, chain 1 the other one, from its end back.
         const Share s = share_of<kBlock>(p, share);
-        left = share < p.shares ? s.left : 0;
+        const int half = (s.left + 1) / 2;
+        left = t == 0 ? half : s.left - half;
+        two = s.left > 1;
         if (left > 0) {
-            u = find_block<kBlock>(p, s.lo);
+            u = find_block<kBlock>(p, t == 0 ? s.lo : s.lo + s.left - 1);
+            if (t > 0) ++u.j0;  // (there: the block behind the unit)
+            u.n = t == 0 ? min(left, u.nb - u.j0) : min(left, u.j0);
+            if (t > 0) u.j0 -= u.n;
+            // The halves meet inside a pair.
+            u.joint = u.n == left && (t == 0 ? two && u.j0 + u.n < u.nb : u.j0 > 0);
             pages.start(p, u);
         }
     }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem = *tmem_slot + t * 256;  // scores at [0, 64) and [64, 128), the output from 128 on
+    const uint32_t tmem_all = *tmem_slot, tmem = tmem_all + t * 256;  // scores at [0, 64) and [64, 128), the output behind
 
-    if (warp < 4) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kCtrlRegs));
+    if (role != kSoftmax) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kCtrlRegs));
         volatile int no_abort = 0;
-        if ((warp & 1) == 0) {
-            // ------------------------------------- loader: the units, Q, K and V
+        if (role == kLoadK || role == kLoadV) {
+            // ------------------------- loaders: the units, Q and K; V from what the other one says
+            // K and V alternate in the ring.
+            const bool is_k = role == kLoadK;
             Place at;
-            uint32_t fills = 0, q_loads = 0;
+            if (!is_k) at.next(stages);
+            uint32_t fills = is_k ? 0 : 1, q_loads = 0;  // fills: the number of the next one in the ring
             bool ok = true;
             u.holes = p.table != nullptr;  // (the first unit's entries are looked at block by block)
             for (uint32_t qi = 0; ok; ++qi) {
                 const uint32_t qs = qi & 1;
-                u.n = left > 0 ? min(left, u.nb - u.j0) : 0;
-                if (u.n > 0 && qi > 0) pages.start(p, u);
-                if (p.table && qi > 0) u.holes = look_for_holes<kBlock>(p, u);
-                if (qi >= 2) ok = wait_warp(bar(C::kUEmpty + qs), ((qi >> 1) - 1) & 1, p.wait_ns, abort_flag);
-                if (!ok) break;
-                if (lane == 0) {
-                    u.put(units + kUnitInts * qs);
-                    mbar_arrive(bar(C::kUFull + qs));
-                }
-                __syncwarp();
-                if (u.n == 0) break;
-                Pages<kBlock> same = pages;  // of V, one block behind in the prefetched entries at most
-                for (int j = 0; ok && j < u.n; ++j)
-#pragma unroll 1
-                    for (int kv = 0; kv < 2; ++kv) {
-                        if (fills >= stages) ok = wait_warp(bar(C::kKVEmpty + at.slot), at.odd ^ 1, p.wait_ns, abort_flag);
-                        if (!ok) break;
-                        const uint32_t full = bar(C::kKVFull + at.slot), to = smem_u32(ring + at.slot * C::kKVBytes);
-                        if (lane == 0) mbar_arrive_expect_tx(full, C::kKVBytes);
-                        (kv ? same : pages).template load<C::kChunks>(p, u, (u.j0 + j) * kBlock, kv ? &tmV : &tmK, full, to);
-                        ++fills;
-                        at.next(stages);
-                        if (j + kv == 0) {
-                            if (q_loads > 0) ok = wait_warp(bar(C::kQEmpty), (q_loads - 1) & 1, p.wait_ns, abort_flag);
-                            if (!ok) break;
-                            if (lane == 0) {
-                                mbar_arrive_expect_tx(bar(C::kQFull), q_bytes);
-                                for (int c = 0; c < C::kChunks; ++c)
-                                    tma_load_3d(smem_u32(sQ + c * p.q_rows * 128), &tmQ, bar(C::kQFull), c * 64, 0, u.b * p.Hkv + u.g);
-                            }
-                            __syncwarp();
-                            ++q_loads;
-                        }
+                if (is_k) {
+                    if (p.table && qi > 0) u.holes = look_for_holes<kBlock>(p, u);
+                    if (qi >= 2) ok = wait_warp(bar(C::kUEmpty + qs), ((qi >> 1) - 1) & 1, p.wait_ns, abort_flag);
+                    if (!ok) break;
+                    if (lane == 0) {
+                        u.put(units + kUnitInts * qs);
+                        mbar_arrive(bar(C::kUFull + qs));
                     }
-                left -= u.n;
-                if (ok && left > 0) next_pair<kBlock>(p, u);
+                    __syncwarp();
+                } else {
+                    ok = wait_warp(bar(C::kUFull + qs), (qi >> 1) & 1, p.wait_ns, abort_flag);
+                    if (!ok) break;
+                    u.get(units + kUnitInts * qs);
+                    __syncwarp();
+                    mbar_arrive_elect(bar(C::kUEmpty + qs));
+                    if (u.n > 0) pages.start(p, u);
+                }
+                if (u.n == 0) break;
+#pragma unroll 1
+                for (int j = 0; j < u.n; ++j) {
+                    if (fills >= stages) ok = wait_warp(bar(C::kKVEmpty + at.slot), at.odd ^ 1, p.wait_ns, abort_flag);
+                    if (!ok) break;
+                    const uint32_t full = bar(C::kKVFull + at.slot);
+                    if (lane == 0) mbar_arrive_expect_tx(full, C::kKVBytes);
+                    pages.template load<C::kChunks>(p, u, (u.j0 + j) * kBlock, is_k ? &tmK : &tmV, full,
+                                                    smem_u32(ring + at.slot * C::kKVBytes));
+                    fills += 2;
+                    at.next(stages);
+                    at.next(stages);
+                    if (is_k && j == 0) {
+                        if (q_loads > 0) ok = wait_warp(bar(C::kQEmpty), (q_loads - 1) & 1, p.wait_ns, abort_flag);
+                        if (!ok) break;
+                        if (lane == 0) {
+                            mbar_arrive_expect_tx(bar(C::kQFull), q_bytes);
+                            for (int c = 0; c < C::kChunks; ++c)
+                                tma_load_3d(smem_u32(sQ + c * p.q_rows * 128), &tmQ, bar(C::kQFull), c * 64, 0, u.b * p.Hkv + u.g);
+                        }
+                        __syncwarp();
+                        ++q_loads;
+                    }
+                }
+                if (!ok) break;
+                if (is_k) {
+                    left -= u.n;
+                    if (left == 0) {
+                        u.n = 0;
+                        continue;
+                    }
+                    if (t == 0) {
+                        next_pair<kBlock>(p, u);
+                        u.n = min(left, u.nb);
+                    } else {
+                        previous_pair<kBlock>(p, u);
+                        u.n = min(left, u.nb);
+                        u.j0 -= u.n;
+                    }
+                    u.joint = u.n == left && (t == 0 ? two && u.n < u.nb : u.j0 > 0);
+                    pages.start(p, u);
+                }
             }
             __syncwarp();
-            // Copies have to land before the CTA goes (bounded), whatever became of the other warps: the last one into
-            // every slot.
+            // Copies have to land before the CTA goes (bounded), whatever became of the other warps: this warp's last one
+            // into every slot.
             if (!ok && lane == 0) {
                 Place back = at;
-                for (uint32_t s = 0; s < min(fills, stages); ++s) {
-                    back.slot = back.slot == 0 ? (back.odd ^= 1, stages - 1) : back.slot - 1;
+                for (uint32_t f = fills; f >= 2 && f + stages > fills; f -= 2) {
+                    for (int i = 0; i < 2; ++i) {
+                        if (back.slot == 0) back.slot = stages, back.odd ^= 1;
+                        --back.slot;
+                    }
                     if (!mbar_wait_bounded(bar(C::kKVFull + back.slot), back.odd, kDrainNs, &no_abort, &g_tree_status))
                         atomicOr(&g_tree_status, kStatusDrainTimeout);
                 }
@@ -799,10 +875,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                     atomicOr(&g_tree_status, kStatusDrainTimeout);
             }
             __syncwarp();
-            if (warp == 0) clear_idle<D>(p);
+        } else if (role == kSpare) {
+            if (t == 0) write_cut<kBlock>(p, share, share_of<kBlock>(p, share));
+            else clear_idle<D>(p);
         } else {
             // ------------------------------------------------------ MMA issuer
-            if (share < p.shares) write_cut<kBlock>(p, share, share_of<kBlock>(p, share));
             constexpr uint32_t kIdescQK = idesc_bf16_f32(kTileM, kBlock, 0), kIdescPV = idesc_bf16_f32(kTileM, D, 1);
             const uint64_t dQ = smem_desc_sw128(smem_u32(sQ), 16, 1024), dK = smem_desc_sw128(smem_u32(ring), 16, 1024),
                            dV = smem_desc_sw128(smem_u32(ring), C::kChunkBytes, 1024);
@@ -811,16 +888,6 @@ __global__ void __launch_bounds__(kThreads, 1)
             v.next(stages);
             uint32_t p_odd = 0, done = 0;  // p_odd: a bit a buffer
             bool ok = true;
-            auto qk = [&](int buf) {
-                ok = wait_warp(bar(C::kKVFull + k.slot), k.odd, p.wait_ns, abort_flag);
-                if (!ok) return;
-                tc_fence_after();
-                issue_qk<D>(tmem + buf * kBlock, dQ, q_chunk, dK + uint64_t(k.slot * (C::kKVBytes >> 4)), C::kChunkBytes, kIdescQK);
-                tc_commit_elect(bar(C::kSFull + buf));
-                tc_commit_elect(bar(C::kKVEmpty + k.slot));
-                k.next(stages);
-                k.next(stages);
-            };
             for (uint32_t qi = 0; ok; ++qi) {
                 const uint32_t qs = qi & 1;
                 ok = wait_warp(bar(C::kUFull + qs), (qi >> 1) & 1, p.wait_ns, abort_flag);
@@ -847,8 +914,15 @@ __global__ void __launch_bounds__(kThreads, 1)
                         if (j == n - 1) tc_commit_elect(bar(C::kOFull));
                     }
                     if (j + 2 < n) {
-                        qk(buf);
-                        if (ok && j + 2 == n - 1) tc_commit_elect(bar(C::kQEmpty));  // Q's last product
+                        ok = wait_warp(bar(C::kKVFull + k.slot), k.odd, p.wait_ns, abort_flag);
+                        if (!ok) break;
+                        tc_fence_after();
+                        issue_qk<D>(tmem + buf * kBlock, dQ, q_chunk, dK + uint64_t(k.slot * (C::kKVBytes >> 4)), C::kChunkBytes, kIdescQK);
+                        tc_commit_elect(bar(C::kSFull + buf));
+                        tc_commit_elect(bar(C::kKVEmpty + k.slot));
+                        k.next(stages);
+                        k.next(stages);
+                        if (j + 2 == n - 1) tc_commit_elect(bar(C::kQEmpty));  // Q's last product
                     }
                 }
                 ++done;
@@ -858,7 +932,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             __syncwarp();
         }
     } else {
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::kSoftmaxRegs));
         // ------------------------------------------------- softmax / epilogue
         const int quarter = warp & 3, row = quarter * 32 + lane, token = row % p.T;
         const uint32_t lanes = uint32_t(quarter * 32) << 16, tS0 = tmem + lanes, tO = tmem + lanes + 128;
@@ -876,13 +950,14 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_arrive_elect(bar(C::kUEmpty + qs));
             if (u.n == 0) break;
             const bool live = row < p.rows && token < u.tb;
-            if ((u.j0 + u.n) * kBlock > u.len) mask.load(p, u, token);
+            if ((u.j0 + u.n) * kBlock > u.len || u.joint) mask.load(p, u, token);
             Holes<kBlock> holes;
             holes.start(p, u);
             uint32_t *odd = odd_rows + (qi & 3) * kMaskWords;
             State st;
             st.clear();
             Place last = at;  // of the last block's V
+#pragma unroll 1
             for (int j = 0; j < u.n; ++j) {
                 const int buf = j & 1, key = (u.j0 + j) * kBlock;
                 const uint32_t on_page = holes.next(p, u, j);
@@ -926,9 +1001,33 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (ok) ok = wait_warp(bar(C::kOFull), qi & 1, p.wait_ns, abort_flag);
             if (!ok) break;
             tc_fence_after();
+            if (u.joint) {
+                // The last unit of both chains: each has the other's state and stores half of the columns.
+                states[t * kTileM + row] = make_float2(st.m, st.l);
+                if (quarter == 0 && lane == 0) parts[3 * t] = u.j0, parts[3 * t + 1] = u.n, parts[3 * t + 2] = int(qi & 3);
+                tc_fence_before();
+                __syncwarp();
+                mbar_arrive_elect(smem_u32(all_bars + C::kJoint));
+                ok = wait_warp(smem_u32(all_bars + C::kJoint), 0, p.wait_ns, abort_flag);
+                if (!ok) break;
+                tc_fence_after();
+                const float2 a = states[row], c = states[kTileM + row];
+                const float top = fmaxf(a.x, c.x), ref = top == -INFINITY ? 0.f : top;
+                const float f = fast_exp2(a.x - ref), f2 = fast_exp2(c.x - ref), sum = f * a.y + f2 * c.y;
+                const bool whole = parts[1] + parts[4] == u.nb;
+                const uint32_t *other = all_odd + ((1 - t) * 4 + parts[3 * (1 - t) + 2]) * kMaskWords;
+                if (has_rows)
+                    store_rows<D / 2, D, true, 256>(p, u, whole, part_row(p, share, parts[0]), quarter * 32,
+                                                    tmem_all + lanes + 128, t * (D / 2), f / sum, f2 / sum,
+                                                    live && sum != 0.f ? top + __log2f(sum) : -INFINITY, token, live, mask, odd, other);
+                tc_fence_before();
+                break;
+            }
             // (the next unit but one has none yet, and this warp's mates are all past the last one)
             if (quarter == 0 && lane < kMaskWords) odd_rows[((qi + 2) & 3) * kMaskWords + lane] = 0;
-            if (has_rows) store_rows<D>(p, u, share, quarter * 32, tO, st, live, token, mask, odd);
+            if (has_rows)
+                store_rows<D, D, false, 0>(p, u, u.n == u.nb, part_row(p, share, u.j0), quarter * 32, tO, 0, 1.f / st.l, 0.f,
+                                           st.total(live), token, live, mask, odd, odd);
             tc_fence_before();
             __syncwarp();
             mbar_arrive_elect(bar(C::kOEmpty));
@@ -937,9 +1036,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 
     tc_fence_before();
     __syncthreads();
-    if (warp == 1) {
+    if (role == kIssue && t == 0) {
         tc_fence_after();
-        tmem_dealloc(*tmem_slot, kTmemCols);
+        tmem_dealloc(tmem_all, kTmemCols);
     }
 }
 
@@ -1215,7 +1314,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             tc_fence_after();
             // (the next unit but one has none yet; of the last one's, the other tile is past its products, hence its stores)
             if (t == 0 && quarter == 0 && lane < kMaskWords) odd_rows[((qi + 2) & 3) * kMaskWords + lane] = 0;
-            if (has_rows) store_rows<D>(p, u, share, row0, tO, st, live, token, mask, odd);
+            if (has_rows)
+                store_rows<D, D, false, 0>(p, u, u.n == u.nb, part_row(p, share, u.j0), row0, tO, 0, 1.f / st.l, 0.f,
+                                           st.total(live), token, live, mask, odd, odd);
             tc_fence_before();
             __syncwarp();
             mbar_arrive_elect(bar(C::kOEmpty + t));
@@ -1338,7 +1439,7 @@ Layout layout_of(int B, int G, int Hkv, int T, int d, long long cap, int num_sms
     l.mt = few ? 1 : int((rows + 2 * kTileM - 1) / (2 * kTileM));
     const int block = few ? 64 : 128;
     const long long most = (long long)B * Hkv * ((cap + block - 1) / block);
-    const int groups = few ? 2 * num_sms : num_sms / l.mt > 0 ? num_sms / l.mt : 1;
+    const int groups = num_sms / l.mt > 0 ? num_sms / l.mt : 1;
     l.shares = int(most < groups ? most : groups);
     auto up = [](size_t n) { return (n + 255) / 256 * 256; };
     l.cuts = 0;
@@ -1388,6 +1489,7 @@ int launch(const DecodeTreeLaunch &a, const Layout &l, cudaStream_t stream) {
     p.scale_log2 = a.scale * 1.4426950408889634f;
     p.wait_ns = a.wait_ns;
     auto kernel = few ? pairs_kernel<D> : rows_kernel<D>;
+    const int threads = few ? PairCfg<D>::kThreads : kThreads;
     const int smem = few ? PairCfg<D>::smem_bytes(q_rows, p.stages) : RowsCfg<D>::kSmemBytes;
     static bool attr_set[2][kMaxDevices] = {};
     const int dev = slot_for_device();
@@ -1395,14 +1497,13 @@ int launch(const DecodeTreeLaunch &a, const Layout &l, cudaStream_t stream) {
         cudaFuncAttributes fa;
         cudaError_t e = cudaFuncGetAttributes(&fa, kernel);
         if (e != cudaSuccess) return note_cuda_error(e, "cudaFuncGetAttributes(drafted tokens)");
-        if (fa.numRegs != kLaunchRegs || fa.maxThreadsPerBlock < kThreads)
+        if (fa.numRegs != (few ? 65536 / PairCfg<D>::kThreads : kLaunchRegs) || fa.maxThreadsPerBlock < threads)
             return note_cuda_error(cudaErrorInvalidConfiguration, "register count differs from the setmaxnreg split (drafted tokens)");
         e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemMax);
         if (e != cudaSuccess) return note_cuda_error(e, "cudaFuncSetAttribute(drafted tokens)");
         if (dev >= 0) attr_set[few][dev] = true;
     }
-    const int ctas = few ? (l.shares < a.num_sms ? l.shares : a.num_sms) : l.shares * l.mt;
-    kernel<<<dim3(unsigned(ctas)), dim3(kThreads), smem, stream>>>(mq, mk, mv, p);
+    kernel<<<dim3(unsigned(l.shares * l.mt)), dim3(unsigned(threads)), smem, stream>>>(mq, mk, mv, p);
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return note_cuda_error(e, "kernel launch (drafted tokens)");
     if (l.shares == 1) return 0;  // nothing is cut
