@@ -26,7 +26,8 @@
 // lengths are.  A pair that lies in one share is written out at once; one that is cut
 // goes through partials: share s writes its first segment's to slot 2 s (a pair
 // that began before) and its last one's to 2 s + 1 (a pair that goes on), and
-// merge_kernel adds up slot 2 s + 1, 2 (s + 1), 2 (s + 2), ...
+// merge_kernel adds up slot 2 s + 1, 2 (s + 1), 2 (s + 2), ...  Where no pair has many
+// blocks, shares end with pairs instead, and there is nothing to merge.
 //
 // Pages: a block of keys is one box, or several where pages are smaller, each from
 // the page that the table names; a box on no page is filled with zeros by coordinates
@@ -101,6 +102,7 @@ struct Params {
     int B, Hkv, T, rows;
     int num_pages, page_size, shift, cap, max_pages;
     int mt, shares;
+    bool whole;          // shares end with pairs
     bool wide;           // outputs and partials are 32-byte aligned
     int q_rows, stages;  // pairs_kernel: rows of Q in shared memory, blocks of a chain's ring
     float scale_log2;
@@ -197,8 +199,18 @@ __device__ __forceinline__ Share share_of(const Params &p, int share) {
     const unsigned total = all_blocks<kBlock>(p);
     Share s;
     s.S = (total + p.shares - 1) / p.shares;
-    s.lo = share * s.S;
-    s.left = s.lo < total ? int(min(s.S, total - s.lo)) : 0;
+    s.lo = min(share * s.S, total);
+    unsigned end = min(s.lo + s.S, total);
+    if (p.whole) {  // on to the pairs' ends
+        auto up = [&](unsigned x) {
+            if (x == total) return x;
+            const Unit u = find_block<kBlock>(p, x);
+            return u.j0 > 0 ? x + u.nb - u.j0 : x;
+        };
+        s.lo = up(s.lo);
+        end = up(end);
+    }
+    s.left = int(end - s.lo);
     return s;
 }
 
@@ -472,16 +484,17 @@ struct State {
     template <int kBlock>
     __device__ __forceinline__ bool add(const Scores<kBlock> &s, uint32_t tS, float sl2, bool use) {
         float sum;
-        bool again = false, twice = false;
+        bool again = false, twice = false, over = false;  // over: this row's sum; the others keep theirs to the bit
         corr = 1.f;
         do {
-            if (m == -INFINITY || again) {
+            if (m == -INFINITY || over) {
                 const float to = fmaxf(m, s.top() * sl2);
-                if (again && to > m) corr = fast_exp2(m - to);
+                if (over && to > m) corr = fast_exp2(m - to);
                 m = to;
             }
             sum = s.exponentials(tS, sl2, m == -INFINITY ? 0.f : -m);
-            again = !again && __any_sync(0xffffffffu, use && !(sum < 0x1p60f));
+            over = use && !(sum < 0x1p60f);
+            again = !again && __any_sync(0xffffffffu, over);
             if (again) {
                 tmem_wait_st();
                 twice = true;
@@ -876,8 +889,8 @@ __global__ void __launch_bounds__(PairCfg<D>::kThreads, 1)
             }
             __syncwarp();
         } else if (role == kSpare) {
-            if (t == 0) write_cut<kBlock>(p, share, share_of<kBlock>(p, share));
-            else clear_idle<D>(p);
+            if (t > 0) clear_idle<D>(p);
+            else if (!p.whole) write_cut<kBlock>(p, share, share_of<kBlock>(p, share));
         } else {
             // ------------------------------------------------------ MMA issuer
             constexpr uint32_t kIdescQK = idesc_bf16_f32(kTileM, kBlock, 0), kIdescPV = idesc_bf16_f32(kTileM, D, 1);
@@ -1158,7 +1171,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             // ------------------------------------- loaders: warp 0 K, warp 2 V
             // Blocks alternate in the ring, K at even fills and V at odd ones; neither warp waits for the other's slots.
             const uint32_t kv = warp == 0 ? 0 : 1;
-            if (warp == 2 && m == 0) write_cut<kBlock>(p, share, share_of<kBlock>(p, share));
+            if (warp == 2 && m == 0 && !p.whole) write_cut<kBlock>(p, share, share_of<kBlock>(p, share));
             uint32_t blocks = 0;  // loaded so far
             bool ok = true;
             for (uint32_t qi = 0; ok; ++qi) {
@@ -1428,8 +1441,19 @@ __global__ void __launch_bounds__(kMergeWarps * 32) merge_kernel(const Params p)
     if (k8 == 0 && r8 < rows && p.lse) p.lse[out + r8] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * 0.69314718055994531f;
 }
 
+// Shares end with pairs where a pair can have at most this many keys.  In us, d = 128, with shares of equal length and
+// with whole pairs, few rows (8 tokens x 8 heads): 1 x 8 pairs of 512 keys 12.5, 14.4 (and a launch less); 8 x 8 of 512
+// 16.4, 14.4, of 1024 21.8, 17.4, of 2048 24.6, 24.6; 32 x 8 of 1024 40.9, 34.2, of 2048 59.6, 53.7; 128 x 8 of 256
+// 53.7, 44.9.  Many rows: 8 x 8 pairs x 256 rows of 512 keys 22.6, 20.6, of 1024 24.8, 26.7; 32 x 8 x 512 of 1024 88, 85,
+// of 2048 134, 137; 8 x 256 of 1024 20.5, 24.7.
+long long whole_keys(bool few, long long pairs, int num_sms) {
+    if (few) return pairs >= num_sms ? 2048 : 4 * pairs >= num_sms ? 1024 : 512;
+    return pairs >= num_sms ? 1024 : 512;
+}
+
 struct Layout {
     int mt, shares;
+    bool whole;
     size_t cuts, part_o, part_lse, bytes;
 };
 Layout layout_of(int B, int G, int Hkv, int T, int d, long long cap, int num_sms) {
@@ -1441,6 +1465,7 @@ Layout layout_of(int B, int G, int Hkv, int T, int d, long long cap, int num_sms
     const long long most = (long long)B * Hkv * ((cap + block - 1) / block);
     const int groups = num_sms / l.mt > 0 ? num_sms / l.mt : 1;
     l.shares = int(most < groups ? most : groups);
+    l.whole = cap <= whole_keys(few, (long long)B * Hkv, num_sms);
     auto up = [](size_t n) { return (n + 255) / 256 * 256; };
     l.cuts = 0;
     l.part_o = up(size_t(l.shares) * sizeof(int4));
@@ -1483,6 +1508,7 @@ int launch(const DecodeTreeLaunch &a, const Layout &l, cudaStream_t stream) {
     p.max_pages = a.max_pages;
     p.mt = l.mt;
     p.shares = l.shares;
+    p.whole = l.whole;
     p.wide = ((reinterpret_cast<uintptr_t>(a.o) | reinterpret_cast<uintptr_t>(a.workspace)) & 31u) == 0;
     p.q_rows = q_rows;
     p.stages = PairCfg<D>::stages_for(q_rows);
@@ -1506,7 +1532,7 @@ int launch(const DecodeTreeLaunch &a, const Layout &l, cudaStream_t stream) {
     kernel<<<dim3(unsigned(l.shares * l.mt)), dim3(unsigned(threads)), smem, stream>>>(mq, mk, mv, p);
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return note_cuda_error(e, "kernel launch (drafted tokens)");
-    if (l.shares == 1) return 0;  // nothing is cut
+    if (l.shares == 1 || l.whole) return 0;  // nothing is cut
     // Few pairs are cut into many partials each: then all warps of a block take a part of them.
     const bool split = l.shares >= 8LL * a.B * a.Hkv;
     const int per = split ? 4 : 4 * kMergeWarps;
