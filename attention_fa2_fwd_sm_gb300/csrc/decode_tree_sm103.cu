@@ -33,10 +33,10 @@
 // the page that the table names; a box on no page is filled with zeros by coordinates
 // past the end.  Columns past the last key, on no page, or hidden by the mask become
 // -inf before the softmax.  A probability of 0 does not hide a V of infinity or NaN
-// from the product, so a warp cleans the blocks of V that hold drafted keys as soon as
-// they land, and only then are they full: rows behind the last key, which may hold
-// anything, become zeros, and so do elements of drafted rows that are not finite,
-// which the epilogue then adds to the rows that see them.
+// from the product, so the softmax warps clean the blocks that hold drafted keys
+// before they hand P over: rows behind the last key, which may hold anything, become
+// zeros, and so do elements of drafted rows that are not finite, which the epilogue
+// then adds to the rows that see them.
 //
 // Precision: scores, maxima, sums, partials in fp32; probabilities are rounded to
 // bf16 for the product with V, because the instruction takes both operands in one
@@ -367,71 +367,36 @@ struct Seen {
     }
 };
 
-// A unit's blocks of V that hold drafted keys, by one warp as they land (on barrier land + slot, of which `odd_land` keeps
-// a parity a slot): rows behind the last key become zeros; in drafted rows, elements that are not finite do, and the row's
-// bit in `odd` is set.  The swizzle stays within a row's 128 bytes of a chunk, which eight lanes take.  Block 0's V is fill
-// `fill` of the ring.
+// V rows [first, kBlock) of a block in shared memory, by the four warps of a chain (`warp` of them; the swizzle stays
+// within a row's 128 bytes of a chunk, which eight lanes take): rows from `end` on become zeros; in the drafted rows
+// before it, of which row `first` is number `u0`, elements that are not finite do, and the row's bit in `odd` is set.
 template <int kChunks, int kBlock>
-__device__ __forceinline__ bool clean_unit(const Params &p, const Unit &u, uint32_t fill, uint32_t stages, uint8_t *ring,
-                                           uint64_t *bars, int land, int full, uint32_t &odd_land, uint32_t *odd,
-                                           volatile int *abort) {
+__device__ __forceinline__ void clean_rows(uint8_t *v, int warp, int first, int end, int u0, uint32_t *odd) {
     const int lane = threadIdx.x & 31;
-#pragma unroll 1
-    for (int j = max(u.len / kBlock - u.j0, 0); j < u.n; ++j) {
-        const uint32_t slot = (fill + 2 * j) % stages;
-        if (!wait_warp(smem_u32(bars + land + slot), odd_land >> slot & 1, p.wait_ns, abort)) return false;
-        odd_land ^= 1u << slot;
-        uint8_t *v = ring + slot * (kChunks * kBlock * 128);
-        const int key = (u.j0 + j) * kBlock;
-#pragma unroll 1
-        for (int row = max(u.len - key, 0) + (lane >> 3); row < kBlock; row += 4) {
-            bool found = false;
+    for (int row = first + warp * 4 + (lane >> 3); row < kBlock; row += 16) {
+        bool found = false;
 #pragma unroll
-            for (int c = 0; c < kChunks; ++c) {
-                uint4 *at = reinterpret_cast<uint4 *>(v + c * (kBlock * 128) + row * 128 + (lane & 7) * 16);
-                if (key + row >= u.keys) {
-                    *at = make_uint4(0, 0, 0, 0);
-                    continue;
-                }
-                uint4 x = *at;
-                uint32_t *w = &x.x;
-                bool here = false;
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    if ((w[k] & 0x7f80u) == 0x7f80u) w[k] &= 0xffff0000u, here = true;
-                    if ((w[k] & 0x7f800000u) == 0x7f800000u) w[k] &= 0x0000ffffu, here = true;
-                }
-                if (here) *at = x;
-                found |= here;
+        for (int c = 0; c < kChunks; ++c) {
+            uint4 *at = reinterpret_cast<uint4 *>(v + c * (kBlock * 128) + row * 128 + (lane & 7) * 16);
+            if (row >= end) {
+                *at = make_uint4(0, 0, 0, 0);
+                continue;
             }
-            const int draft = key + row - u.len;
-            if (found) atomicOr(odd + (draft >> 5), 1u << (draft & 31));
+            uint4 x = *at;
+            uint32_t *w = &x.x;
+            bool here = false;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                if ((w[k] & 0x7f80u) == 0x7f80u) w[k] &= 0xffff0000u, here = true;
+                if ((w[k] & 0x7f800000u) == 0x7f800000u) w[k] &= 0x0000ffffu, here = true;
+            }
+            if (here) *at = x;
+            found |= here;
         }
-        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-        __syncwarp();
-        mbar_arrive_elect(smem_u32(bars + full + slot));
+        const int u = u0 + row - first;
+        if (found) atomicOr(odd + (u >> 5), 1u << (u & 31));
     }
-    return true;
 }
-
-// The V loader's side of it: which barrier a fill of V lands on, and after a launch that gave up, the wait for the last
-// one of a slot.
-struct Landing {
-    uint32_t masked = 0, odd = 0;  // a bit a slot: the last fill holds drafted keys; parity of the next such fill
-    __device__ __forceinline__ int bar(uint32_t slot, bool drafted, int land, int full) {
-        masked = drafted ? masked | 1u << slot : masked & ~(1u << slot);
-        if (!drafted) return full + slot;
-        odd ^= 1u << slot;
-        return land + slot;
-    }
-    __device__ __forceinline__ void drain(uint64_t *bars, uint32_t slot, uint32_t round_odd, int land, int full) const {
-        volatile int no_abort = 0;
-        const bool m = masked >> slot & 1;
-        if (!mbar_wait_bounded(smem_u32(bars + (m ? land : full) + slot), m ? ~(odd >> slot) & 1 : round_odd, kDrainNs, &no_abort,
-                               &g_tree_status))
-            atomicOr(&g_tree_status, kStatusDrainTimeout);
-    }
-};
 
 // Adds to n columns of a stored row the elements of V that are not finite.
 template <typename T>
@@ -469,7 +434,6 @@ struct Scores {
                 if (!(on_page >> at & 1)) bits &= halves ? 0xffff0000u : 0u;
                 if (halves && !(on_page >> (at + 1) & 1)) bits &= 0x0000ffffu;
             }
-            if (__all_sync(0xffffffffu, bits == ~0u)) continue;
 #pragma unroll
             for (int i = 0; i < 32; ++i)
                 if (!(bits >> i & 1)) s[c * 32 + i] = -INFINITY;
@@ -734,8 +698,7 @@ struct PairCfg {
     static constexpr int kMaxStages = 12;
     // barriers of a chain (S and P: a buffer each)
     static constexpr int kQFull = 0, kQEmpty = 1, kSFull = 2, kPFull = 4, kOFull = 6, kOEmpty = 7, kUFull = 8, kUEmpty = 10,
-                         kDrain = 12, kJoint = 13, kKVFull = 14, kKVEmpty = kKVFull + kMaxStages, kLand = kKVEmpty + kMaxStages,
-                         kNumBars = kLand + kMaxStages;
+                         kDrain = 12, kJoint = 13, kKVFull = 14, kKVEmpty = 14 + kMaxStages, kNumBars = 14 + 2 * kMaxStages;
     // 16 warps: 512 threads x 128 registers at launch are shared out anew.
     static constexpr int kThreads = 512, kCtrlRegs = 88, kSoftmaxRegs = 160;
     static_assert(256 * kCtrlRegs + 256 * kSoftmaxRegs <= 512 * 128, "register split");
@@ -768,9 +731,9 @@ __global__ void __launch_bounds__(PairCfg<D>::kThreads, 1)
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    // Per chain: warps that plan and load Q and K, that load V, that issue MMAs, that clean V; then the softmax warps.
+    // Per chain: warps that plan and load Q and K, that load V, that issue MMAs, one to spare; then the softmax warps.
     const int t = warp >> 2 & 1, role = warp < 8 ? warp & 3 : 4;
-    enum { kLoadK, kLoadV, kIssue, kClean, kSoftmax };
+    enum { kLoadK, kLoadV, kIssue, kSpare, kSoftmax };
     const int share = blockIdx.x;
     const uint32_t stages = p.stages;
     const int q_bytes = C::q_bytes(p.q_rows), chain_bytes = C::chain_bytes(p.q_rows, p.stages);
@@ -779,7 +742,7 @@ __global__ void __launch_bounds__(PairCfg<D>::kThreads, 1)
     uint32_t *odd_rows = all_odd + t * 4 * kMaskWords;
     float2 *states = reinterpret_cast<float2 *>(rest + C::kStateOffset);  // [chain][row]
     volatile int *parts = reinterpret_cast<volatile int *>(states + 2 * kTileM);  // [chain]: first block, blocks, which of the four units in turn
-    uint64_t *all_bars = reinterpret_cast<uint64_t *>(rest + C::kBarOffset), *bars = all_bars + t * C::kNumBars;
+    uint64_t *all_bars = reinterpret_cast<uint64_t *>(rest + C::kBarOffset);
     volatile int *units = reinterpret_cast<volatile int *>(rest + C::kUnitOffset) + t * 2 * kUnitInts;
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(rest + C::kUnitOffset + 2 * 2 * kUnitInts * 4);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
@@ -791,13 +754,15 @@ __global__ void __launch_bounds__(PairCfg<D>::kThreads, 1)
         if (i < 2 * C::kNumBars) {
             const int k = i % C::kNumBars;
             const bool four = k == C::kPFull || k == C::kPFull + 1 || k == C::kOEmpty;
-            // (a unit's slot: the V, MMA and cleaning warps, the softmax warps)
-            mbar_init(smem_u32(all_bars + i), four ? 4 : k == C::kUEmpty || k == C::kUEmpty + 1 ? 3 + 4 : k == C::kJoint ? 8 : 1);
+            // (a unit's slot: the V and MMA warps, the softmax warps)
+            mbar_init(smem_u32(all_bars + i), four ? 4 : k == C::kUEmpty || k == C::kUEmpty + 1 ? 2 + 4 : k == C::kJoint ? 8 : 1);
         }
         if (i == 0) *abort_flag = 0;
         fence_mbar_init();
     }
     static_assert(2 * C::kNumBars <= 256, "one thread each");
+    if (role == kSoftmax && (warp & 3) == 0) odd_rows[lane] = 0;
+    static_assert(4 * kMaskWords == 32, "one warp clears them");
     if (role == kIssue && t == 0) {
         tmem_alloc(smem_u32(tmem_slot), kTmemCols);
         tmem_relinquish();
@@ -842,7 +807,6 @@ __global__ void __launch_bounds__(PairCfg<D>::kThreads, 1)
             Place at;
             if (!is_k) at.next(stages);
             uint32_t fills = is_k ? 0 : 1, q_loads = 0;  // fills: the number of the next one in the ring
-            Landing landing;
             bool ok = true;
             u.holes = p.table != nullptr;  // (the first unit's entries are looked at block by block)
             for (uint32_t qi = 0; ok; ++qi) {
@@ -851,9 +815,6 @@ __global__ void __launch_bounds__(PairCfg<D>::kThreads, 1)
                     if (p.table && qi > 0) u.holes = look_for_holes<kBlock>(p, u);
                     if (qi >= 2) ok = wait_warp(bar(C::kUEmpty + qs), ((qi >> 1) - 1) & 1, p.wait_ns, abort_flag);
                     if (!ok) break;
-                    // (the softmax warps have begun the last unit but one: they are done with the one before it)
-                    if (lane < kMaskWords) odd_rows[(qi & 3) * kMaskWords + lane] = 0;
-                    __syncwarp();
                     if (lane == 0) {
                         u.put(units + kUnitInts * qs);
                         mbar_arrive(bar(C::kUFull + qs));
@@ -872,10 +833,10 @@ __global__ void __launch_bounds__(PairCfg<D>::kThreads, 1)
                 for (int j = 0; j < u.n; ++j) {
                     if (fills >= stages) ok = wait_warp(bar(C::kKVEmpty + at.slot), at.odd ^ 1, p.wait_ns, abort_flag);
                     if (!ok) break;
-                    const int key = (u.j0 + j) * kBlock;
-                    const uint32_t full = bar(landing.bar(at.slot, !is_k && key + kBlock > u.len, C::kLand, C::kKVFull));
+                    const uint32_t full = bar(C::kKVFull + at.slot);
                     if (lane == 0) mbar_arrive_expect_tx(full, C::kKVBytes);
-                    pages.template load<C::kChunks>(p, u, key, is_k ? &tmK : &tmV, full, smem_u32(ring + at.slot * C::kKVBytes));
+                    pages.template load<C::kChunks>(p, u, (u.j0 + j) * kBlock, is_k ? &tmK : &tmV, full,
+                                                    smem_u32(ring + at.slot * C::kKVBytes));
                     fills += 2;
                     at.next(stages);
                     at.next(stages);
@@ -920,30 +881,16 @@ __global__ void __launch_bounds__(PairCfg<D>::kThreads, 1)
                         if (back.slot == 0) back.slot = stages, back.odd ^= 1;
                         --back.slot;
                     }
-                    landing.drain(bars, back.slot, back.odd, C::kLand, C::kKVFull);
+                    if (!mbar_wait_bounded(bar(C::kKVFull + back.slot), back.odd, kDrainNs, &no_abort, &g_tree_status))
+                        atomicOr(&g_tree_status, kStatusDrainTimeout);
                 }
                 if (q_loads > 0 && !mbar_wait_bounded(bar(C::kQFull), (q_loads - 1) & 1, kDrainNs, &no_abort, &g_tree_status))
                     atomicOr(&g_tree_status, kStatusDrainTimeout);
             }
             __syncwarp();
-        } else if (role == kClean) {
-            // ------------------------------------------------------ cleaner of V
-            if (t == 0 && !p.whole) write_cut<kBlock>(p, share, share_of<kBlock>(p, share));
-            uint32_t blocks = 0, odd_land = 0;
-            bool ok = true;
-            for (uint32_t qi = 0; ok; ++qi) {
-                const uint32_t qs = qi & 1;
-                ok = wait_warp(bar(C::kUFull + qs), (qi >> 1) & 1, p.wait_ns, abort_flag);
-                if (!ok) break;
-                u.get(units + kUnitInts * qs);
-                __syncwarp();
-                mbar_arrive_elect(bar(C::kUEmpty + qs));
-                if (u.n == 0) break;
-                ok = clean_unit<C::kChunks, kBlock>(p, u, 2 * blocks + 1, stages, ring, bars, C::kLand, C::kKVFull, odd_land,
-                                                    odd_rows + (qi & 3) * kMaskWords, abort_flag);
-                blocks += u.n;
-            }
+        } else if (role == kSpare) {
             if (t > 0) clear_idle<D>(p);
+            else if (!p.whole) write_cut<kBlock>(p, share, share_of<kBlock>(p, share));
         } else {
             // ------------------------------------------------------ MMA issuer
             constexpr uint32_t kIdescQK = idesc_bf16_f32(kTileM, kBlock, 0), kIdescPV = idesc_bf16_f32(kTileM, D, 1);
@@ -1052,6 +999,13 @@ __global__ void __launch_bounds__(PairCfg<D>::kThreads, 1)
                     tmem_wait_st();
                     tc_fence_before();
                 }
+                if (key + kBlock > u.len) {
+                    ok = wait_warp(bar(C::kKVFull + at.slot), at.odd, p.wait_ns, abort_flag);
+                    if (!ok) break;
+                    const int first = max(u.len - key, 0);
+                    clean_rows<C::kChunks, kBlock>(ring + at.slot * C::kKVBytes, quarter, first, u.keys - key, key + first - u.len, odd);
+                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                }
                 last = at;
                 at.next(stages);
                 __syncwarp();
@@ -1082,6 +1036,8 @@ __global__ void __launch_bounds__(PairCfg<D>::kThreads, 1)
                 tc_fence_before();
                 break;
             }
+            // (the next unit but one has none yet, and this warp's mates are all past the last one)
+            if (quarter == 0 && lane < kMaskWords) odd_rows[((qi + 2) & 3) * kMaskWords + lane] = 0;
             if (has_rows)
                 store_rows<D, D, false, 0>(p, u, u.n == u.nb, part_row(p, share, u.j0), quarter * 32, tO, 0, 1.f / st.l, 0.f,
                                            st.total(live), token, live, mask, odd, odd);
@@ -1109,7 +1065,7 @@ struct RowsCfg {
     static constexpr int kOddOffset = 2 * kQBytes + kStages * kKVBytes;
     static constexpr int kBarOffset = kOddOffset + 4 * kMaskWords * 4;
     static constexpr int kQFull = 0, kQEmpty = 2, kSFull = 4, kPFull = 6, kOFull = 8, kOEmpty = 10, kUFull = 12, kUEmpty = 14,
-                         kDrain = 16, kKVFull = 17, kKVEmpty = kKVFull + kStages, kLand = kKVEmpty + kStages, kNumBars = kLand + kStages;
+                         kDrain = 16, kKVFull = 17, kKVEmpty = 17 + kStages, kNumBars = 17 + 2 * kStages;
     static constexpr int kUnitOffset = (kBarOffset + kNumBars * 8 + 15) / 16 * 16;
     static constexpr int kSmemBytes = kUnitOffset + 2 * kUnitInts * 4 + 16 + 1024;  // units, tmem, abort; alignment
     static_assert(kSmemBytes <= kSmemMax, "shared memory");
@@ -1145,6 +1101,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (i == 0) *abort_flag = 0;
         fence_mbar_init();
     }
+    if (warp == 4) odd_rows[lane] = 0;
     if (warp == 0 && lane == 0) {
         tma_prefetch_desc(&tmQ);
         tma_prefetch_desc(&tmK);
@@ -1170,10 +1127,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kCtrlRegs));
         volatile int no_abort = 0;
         if (warp == 3) {
-            // ------------------------- planner: the units, and Q; meanwhile it cleans V of the last one
+            // -------------------------------------------- planner: the units, and Q
             uint32_t q_loads = 0;  // per tile (both are loaded for every unit)
-            uint32_t blocks = 0, odd_land = 0;
-            Unit before = {};
             bool ok = true;
             u.holes = p.table != nullptr;  // (the first unit's entries are looked at block by block)
             for (uint32_t qi = 0; ok; ++qi) {
@@ -1182,21 +1137,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (p.table && qi > 0) u.holes = look_for_holes<kBlock>(p, u);
                 if (qi >= 2) ok = wait_warp(bar(C::kUEmpty + qs), ((qi >> 1) - 1) & 1, p.wait_ns, abort_flag);
                 if (!ok) break;
-                // (the softmax warps have begun the last unit but one: they are done with the one before it)
-                if (lane < kMaskWords) odd_rows[(qi & 3) * kMaskWords + lane] = 0;
-                __syncwarp();
                 if (lane == 0) {
                     u.put(units + kUnitInts * qs);
                     mbar_arrive(bar(C::kUFull + qs));
                 }
                 __syncwarp();
-                if (qi > 0) {
-                    ok = clean_unit<C::kChunks, kBlock>(p, before, 2 * blocks + 1, C::kStages, sKV, bars, C::kLand, C::kKVFull, odd_land,
-                                                        odd_rows + ((qi - 1) & 3) * kMaskWords, abort_flag);
-                    blocks += before.n;
-                    if (!ok) break;
-                }
-                before = u;
                 if (u.n == 0) break;
 #pragma unroll 1
                 for (int t = 0; t < (second ? 2 : 1); ++t) {
@@ -1228,7 +1173,6 @@ __global__ void __launch_bounds__(kThreads, 1)
             const uint32_t kv = warp == 0 ? 0 : 1;
             if (warp == 2 && m == 0 && !p.whole) write_cut<kBlock>(p, share, share_of<kBlock>(p, share));
             uint32_t blocks = 0;  // loaded so far
-            Landing landing;
             bool ok = true;
             for (uint32_t qi = 0; ok; ++qi) {
                 const uint32_t qs = qi & 1;
@@ -1244,10 +1188,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const uint32_t fill = 2 * blocks + kv, slot = fill % C::kStages, round = fill / C::kStages;
                     if (round > 0) ok = wait_warp(bar(C::kKVEmpty + slot), (round - 1) & 1, p.wait_ns, abort_flag);
                     if (!ok) break;
-                    const int key = (u.j0 + j) * kBlock;
-                    const uint32_t full = bar(landing.bar(slot, kv && key + kBlock > u.len, C::kLand, C::kKVFull));
+                    const uint32_t full = bar(C::kKVFull + slot);
                     if (lane == 0) mbar_arrive_expect_tx(full, C::kKVBytes);
-                    pages.template load<C::kChunks>(p, u, key, kv ? &tmV : &tmK, full, smem_u32(sKV + slot * C::kKVBytes));
+                    pages.template load<C::kChunks>(p, u, (u.j0 + j) * kBlock, kv ? &tmV : &tmK, full,
+                                                    smem_u32(sKV + slot * C::kKVBytes));
                     ++blocks;
                 }
             }
@@ -1256,7 +1200,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (uint32_t s = kv; s < C::kStages; s += 2) {
                     if (2 * blocks <= s) continue;  // fills below 2 blocks + kv are out
                     const uint32_t last = (2 * blocks - 2 + kv - s) / C::kStages;  // round of the slot's last fill
-                    landing.drain(bars, s, last & 1, C::kLand, C::kKVFull);
+                    if (!mbar_wait_bounded(bar(C::kKVFull + s), last & 1, kDrainNs, &no_abort, &g_tree_status))
+                        atomicOr(&g_tree_status, kStatusDrainTimeout);
                 }
             __syncwarp();
             if (warp == 2) clear_idle<D>(p);
@@ -1365,12 +1310,23 @@ __global__ void __launch_bounds__(kThreads, 1)
                     tmem_wait_st();
                     tc_fence_before();
                 }
+                if (key + kBlock > u.len && t == 0) {
+                    // (the other tile's product of this block is issued behind this one's)
+                    const uint32_t slot = (fills + 1) % C::kStages;
+                    ok = wait_warp(bar(C::kKVFull + slot), ((fills + 1) / C::kStages) & 1, p.wait_ns, abort_flag);
+                    if (!ok) break;
+                    const int first = max(u.len - key, 0);
+                    clean_rows<C::kChunks, kBlock>(sKV + slot * C::kKVBytes, quarter, first, u.keys - key, key + first - u.len, odd);
+                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                }
                 __syncwarp();
                 mbar_arrive_elect(bar(C::kPFull + t));
             }
             if (ok) ok = wait_warp(bar(C::kOFull + t), qi & 1, p.wait_ns, abort_flag);
             if (!ok) break;
             tc_fence_after();
+            // (the next unit but one has none yet; of the last one's, the other tile is past its products, hence its stores)
+            if (t == 0 && quarter == 0 && lane < kMaskWords) odd_rows[((qi + 2) & 3) * kMaskWords + lane] = 0;
             if (has_rows)
                 store_rows<D, D, false, 0>(p, u, u.n == u.nb, part_row(p, share, u.j0), row0, tO, 0, 1.f / st.l, 0.f,
                                            st.total(live), token, live, mask, odd, odd);
