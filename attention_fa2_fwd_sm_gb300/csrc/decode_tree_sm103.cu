@@ -104,7 +104,7 @@ struct Params {
     int mt, shares;
     bool whole;          // shares end with pairs
     bool wide;           // outputs and partials are 32-byte aligned
-    int q_rows, stages;  // pairs_kernel: rows of Q in shared memory, blocks of a chain's ring
+    int q_rows;          // pairs_kernel: rows of Q in shared memory
     float scale_log2;
     unsigned long long wait_ns;
 };
@@ -695,10 +695,15 @@ __device__ __forceinline__ void issue_pv(uint32_t tO, uint32_t tP, uint64_t v, u
 template <int D>
 struct PairCfg {
     static constexpr int kBlock = 64, kChunks = D / 64, kChunkBytes = kBlock * 128, kKVBytes = kBlock * D * 2;
-    static constexpr int kMaxStages = 12;
+    // Blocks of a chain's ring.  64 KB on their way are enough for a chain, and more are not better: 64 users of 8001 .. 16001
+    // keys, one token, d = 128, 4 stages 431 us, 5 433, 6 452, 12 451 (7.3 and 7.0 TB/s); d = 64 the same with 4 as with 12.
+    // An even number, so that K and V have slots of their own: a loader that waits for a slot has then waited for the
+    // round before it too, and no parity is taken for the one of two rounds ago.
+    static constexpr int kStages = 4;
+    static_assert(kStages >= 4 && kStages % 2 == 0, "see above; the next but one K is issued ahead of V");
     // barriers of a chain (S and P: a buffer each)
     static constexpr int kQFull = 0, kQEmpty = 1, kSFull = 2, kPFull = 4, kOFull = 6, kOEmpty = 7, kUFull = 8, kUEmpty = 10,
-                         kDrain = 12, kJoint = 13, kKVFull = 14, kKVEmpty = 14 + kMaxStages, kNumBars = 14 + 2 * kMaxStages;
+                         kDrain = 12, kJoint = 13, kKVFull = 14, kKVEmpty = 14 + kStages, kNumBars = 14 + 2 * kStages;
     // 16 warps: 512 threads x 128 registers at launch are shared out anew.
     static constexpr int kThreads = 512, kCtrlRegs = 88, kSoftmaxRegs = 160;
     static_assert(256 * kCtrlRegs + 256 * kSoftmaxRegs <= 512 * 128, "register split");
@@ -706,12 +711,9 @@ struct PairCfg {
     static constexpr int kBarOffset = kStateOffset + 2 * kTileM * 8 + 32, kUnitOffset = (kBarOffset + 2 * kNumBars * 8 + 15) / 16 * 16;
     static constexpr int kFixedBytes = kUnitOffset + 2 * 2 * kUnitInts * 4 + 16;
     static __host__ __device__ int q_bytes(int q_rows) { return q_rows * 128 * kChunks; }
-    static __host__ __device__ int chain_bytes(int q_rows, int stages) { return q_bytes(q_rows) + stages * kKVBytes; }
-    static int stages_for(int q_rows) {
-        const int n = ((kSmemMax - 1024 - kFixedBytes) / 2 - q_bytes(q_rows)) / kKVBytes;
-        return n < kMaxStages ? n : kMaxStages;
-    }
-    static int smem_bytes(int q_rows, int stages) { return 2 * chain_bytes(q_rows, stages) + kFixedBytes + 1024; }
+    static __host__ __device__ int chain_bytes(int q_rows) { return q_bytes(q_rows) + kStages * kKVBytes; }
+    static int smem_bytes(int q_rows) { return 2 * chain_bytes(q_rows) + kFixedBytes + 1024; }
+    static_assert(2 * (kTileM * D * 2 + kStages * kKVBytes) + kFixedBytes + 1024 <= kSmemMax, "shared memory");
 };
 
 // A place in a ring, and the parity of the round.
@@ -735,8 +737,8 @@ __global__ void __launch_bounds__(PairCfg<D>::kThreads, 1)
     const int t = warp >> 2 & 1, role = warp < 8 ? warp & 3 : 4;
     enum { kLoadK, kLoadV, kIssue, kSpare, kSoftmax };
     const int share = blockIdx.x;
-    const uint32_t stages = p.stages;
-    const int q_bytes = C::q_bytes(p.q_rows), chain_bytes = C::chain_bytes(p.q_rows, p.stages);
+    constexpr uint32_t stages = C::kStages;
+    const int q_bytes = C::q_bytes(p.q_rows), chain_bytes = C::chain_bytes(p.q_rows);
     uint8_t *sQ = smem + t * chain_bytes, *ring = sQ + q_bytes, *rest = smem + 2 * chain_bytes;
     uint32_t *all_odd = reinterpret_cast<uint32_t *>(rest);  // [chain][four units in turn]
     uint32_t *odd_rows = all_odd + t * 4 * kMaskWords;
@@ -1511,12 +1513,11 @@ int launch(const DecodeTreeLaunch &a, const Layout &l, cudaStream_t stream) {
     p.whole = l.whole;
     p.wide = ((reinterpret_cast<uintptr_t>(a.o) | reinterpret_cast<uintptr_t>(a.workspace)) & 31u) == 0;
     p.q_rows = q_rows;
-    p.stages = PairCfg<D>::stages_for(q_rows);
     p.scale_log2 = a.scale * 1.4426950408889634f;
     p.wait_ns = a.wait_ns;
     auto kernel = few ? pairs_kernel<D> : rows_kernel<D>;
     const int threads = few ? PairCfg<D>::kThreads : kThreads;
-    const int smem = few ? PairCfg<D>::smem_bytes(q_rows, p.stages) : RowsCfg<D>::kSmemBytes;
+    const int smem = few ? PairCfg<D>::smem_bytes(q_rows) : RowsCfg<D>::kSmemBytes;
     static bool attr_set[2][kMaxDevices] = {};
     const int dev = slot_for_device();
     if (dev < 0 || !attr_set[few][dev]) {
