@@ -944,6 +944,10 @@ int attn_rope_axes_append(const void *q, void *q_out, const void *k, const void 
     if (seqlens_out && page_table &&
         bytes_overlap(seqlens_out, size_t(B) * 4, page_table, size_t(B) * max_pages * 4))
         return ATTN_ERR_ARG;
+    if (seqlens_out && positions) {  // other blocks still read them
+        const size_t n = size_t(num_axes - 1) * axis_stride + size_t(B - 1) * position_stride + T;
+        if (bytes_overlap(seqlens_out, size_t(B) * 4, positions, n * 4)) return ATTN_ERR_ARG;
+    }
     if (!aligned16(kpages) || !aligned16(vpages)) return ATTN_ERR_ARG;
     const long long row = (long long)page_size * d;
     if ((double)num_pages * Hkv * (double)row >= 9.0e18) return ATTN_ERR_ARG;
@@ -1304,6 +1308,7 @@ static int pages_moves(PagesLaunch *a, int *page_table, int *refs, void *kpages,
     size_t bytes = 0;
     rc = pools(kpages, vpages, layers, Hkv, d, num_pages, page_size, &bytes);
     if (rc != ATTN_OK) return rc;
+    if ((long long)Hkv * page_size * (d / 8) >= 0x7fffffffLL) return ATTN_ERR_ARG;  // a page's 16-byte units, in 32 bits
     if (!info || !aligned4(info) || !aligned4(seqlens) || !aligned4(new_lens)) return ATTN_ERR_ARG;
     const size_t need = pages_workspace_bytes(B, num_pages), lens = size_t(B) * 4;
     if (!workspace || !aligned16(workspace) || workspace_bytes < need) return ATTN_ERR_WORKSPACE;

@@ -115,8 +115,8 @@ __device__ __forceinline__ Reach reach_of(const Params &p, int b) {
 }
 
 // One CTA.  A slot of the reach needs a page where its entry is none, or is a page
-// that others hold too -- unless all that hold it are about to write (then the last
-// of them by number keeps it).
+// that other entries hold too -- unless all that hold it are about to be written to
+// (then the last of them, by sequence and slot, keeps it).
 __global__ void __launch_bounds__(kPlanThreads) extend_kernel(const Params p) {
     __shared__ int counts[kRound + 1][kPlanWarps];
     __shared__ int warp_sums[kPlanWarps], num_shared;
@@ -146,16 +146,16 @@ __global__ void __launch_bounds__(kPlanThreads) extend_kernel(const Params p) {
                 const int e = *entry(b, s);
                 if (is_page(p, e) && p.refs[e] > 1) {
                     atomicAdd(p.writers + e, 1);
-                    atomicMax(p.latest + e, b);
+                    atomicMax(p.latest + e, b * p.max_pages + s);
                 }
             }
         }
         __syncthreads();
     }
-    auto needs = [&](int b, int e) {
+    auto needs = [&](int b, int slot, int e) {
         if (!is_page(p, e)) return true;
         const int refs = __ldcg(p.refs + e);
-        return refs > 1 && !(__ldcg(p.writers + e) == refs && __ldcg(p.latest + e) == b);
+        return refs > 1 && !(__ldcg(p.writers + e) == refs && __ldcg(p.latest + e) == b * p.max_pages + slot);
     };
     // Pages needed by each sequence, then by all before it.
     int before = 0;
@@ -166,8 +166,8 @@ __global__ void __launch_bounds__(kPlanThreads) extend_kernel(const Params p) {
             const Reach r = reach_of(p, b);
             for (int s = r.lo + sub; s < r.hi; s += kLanes) {
                 const int e = *entry(b, s);
-                n += needs(b, e) ? 1 : 0;
-                if (is_page(p, e) && p.refs[e] > 1 && __ldcg(p.latest + e) == b) {
+                n += needs(b, s, e) ? 1 : 0;
+                if (is_page(p, e) && p.refs[e] > 1 && __ldcg(p.latest + e) == b * p.max_pages + s) {
                     // One of its writers puts it down (in any order: only its own count is changed by it).
                     const int i = atomicAdd(&num_shared, 1);
                     if (i < p.num_pages) p.shared[i] = e;
@@ -211,7 +211,7 @@ __global__ void __launch_bounds__(kPlanThreads) extend_kernel(const Params p) {
             const int s = s0 + sub;
             int *at = entry(b, s);
             const int e = s < r.hi ? *at : 0;
-            const bool need = s < r.hi && needs(b, e);
+            const bool need = s < r.hi && needs(b, s, e);
             const uint32_t vote = __ballot_sync(mates, need) & mates;
             if (need) {
                 const int page = p.list[next + __popc(vote & ((1u << lane) - 1))];

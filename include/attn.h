@@ -752,12 +752,13 @@ int attn_tree_accept(void *kpages, void *vpages, const int *page_table, const in
  *
  * attn_pages_extend: room for new keys.  For every sequence, the slots that rows
  * [seqlens[b], seqlens[b] + new) reach (cut at the capacity) get a page of their
- * own: where the entry is no page, and where the page is shared with others, in
- * which case the keys in use in it are copied (K and V, all heads and layers).  Where
- * all holders of a shared page are among the writers, the one of the highest b
- * keeps it.  Pages are taken lowest first, in the order of the sequences and slots.
+ * own: where the entry is no page, and where the page is shared with other entries,
+ * in which case the keys in use in it are copied (K and V, all heads and layers).
+ * Where all entries that hold a shared page are about to be written to, the last of
+ * them (of the highest b) keeps it.  Pages are taken lowest first, in the order of the sequences and slots.
  *   new_lens   [B] int32 new keys of each (below 0: 0), or NULL: T for all
- *   kpages, vpages  [layers, num_pages, Hkv, page_size, d] bf16, d a multiple of 8, at most 512
+ *   kpages, vpages  [layers, num_pages, Hkv, page_size, d] bf16, d a multiple of 8, at most 512; a page
+ *              of one layer has less than 2^35 bytes of K
  *   info       [2] int32 (written): pages taken, pages missing.  If pages are
  *              missing, nothing else is changed.
  *   workspace  attn_pages_workspace_bytes(B, num_pages) bytes, 16-byte aligned

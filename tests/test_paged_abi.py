@@ -222,3 +222,15 @@ def test_decode_tree_workspace():
     for bad in ((0, 4, 2, 1, 64, 16, 4), (1, 5, 2, 1, 64, 16, 4), (1, 4, 2, 0, 64, 16, 4), (1, 4, 2, 257, 64, 16, 4),
                 (1, 4, 2, 1, 56, 16, 4), (1, 4, 2, 1, 64, 0, 4), (1, 4, 2, 1, 64, 1 << 20, 1 << 20)):
         assert f(*bad) == 0
+
+
+@pytest.mark.parametrize("call", [_extend, _compact])
+def test_pages_whose_units_are_not_counted_in_32_bits(call):
+    # 8192 heads x 65536 rows x 4 units of 16 bytes are 2^31
+    assert call(pages=1, B=1, per=1, page=65536, Hkv=8192, d=32, layers=1, kp=1 << 40, vp=1 << 44) == ARG
+
+
+@pytest.mark.parametrize("pos", [A16 + 64 - 4, A16 + 64 + 8, A16 + 64 - 100 * 4, A16 + 64 - 8 * 4])
+def test_append_refuses_new_lengths_over_positions(pos):
+    # two axes 100 apart, three entries 4 apart, one token: the last one is at 108
+    assert _append(pos=pos, axis_stride=100, pos_stride=4, A=2) == ARG

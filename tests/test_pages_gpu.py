@@ -257,3 +257,24 @@ def test_in_a_graph_and_on_another_stream(attn):
     pool.compact()
     dev.table, dev.lens = out, olens
     dev.same(pool)
+
+
+def test_a_page_twice_in_a_sequence(attn):
+    """Entries count, not sequences: of two that hold a page and are both written to, the last keeps it; the
+    others get pages of their own, with the keys in use."""
+    page, pages, B = 16, 12, 2
+    k, v = (normal_bf16((pages, 1, page, 64), 40 + i, "cpu") for i in range(2))
+    table = torch.tensor([[5, 5, 3, -1], [3, 7, 7, 7]], dtype=torch.int32, device=DEV)
+    refs = torch.tensor([0, 0, 0, 2, 0, 2, 0, 3, 0, 0, 0, 0], dtype=torch.int32, device=DEV)
+    lens = torch.tensor([10, 20], dtype=torch.int32, device=DEV)
+    kd, vd = k.to(DEV), v.to(DEV)
+    # sequence 0 writes to slots 0 and 1 (both entries of page 5), sequence 1 to slots 1 and 2 (two of the three of page 7)
+    info, _ = attn.pages_extend(table, refs, lens, torch.tensor([20, 20], dtype=torch.int32, device=DEV), kd, vd)
+    assert info.tolist() == [3, 0]
+    assert table.tolist() == [[0, 5, 3, -1], [3, 1, 2, 7]]
+    assert refs.tolist() == [1, 1, 1, 2, 0, 1, 0, 1, 0, 0, 0, 0]
+    for got, was in ((kd.cpu(), k), (vd.cpu(), v)):
+        want = was.clone()
+        want[0, :, :10] = was[5, :, :10]
+        want[1, :, :4] = was[7, :, :4]
+        assert torch.equal(got, want)
