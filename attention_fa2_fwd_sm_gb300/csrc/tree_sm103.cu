@@ -11,7 +11,8 @@
 // least i, rows move towards the front only: taken in order, no row is overwritten
 // before it has been read, so the move needs no second buffer.  A thread owns 16
 // bytes of a head's rows and takes the path in batches, all loads of a batch before
-// its stores.  4 d bytes read and written a row and head: HBM- or launch-bound.
+// its stores.  4 d bytes read and written a row and head: launch- or latency-bound
+// (few rows 4.3 us, 64 users with 8 layers 10.2, of which HBM needs 7.4).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
