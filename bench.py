@@ -995,6 +995,137 @@ def run_decode_cache(args):
     line("rotary positions of a prompt of 8192", 4 * (Hq + Hkv) * 8192 * d, rope_us=timed(lambda: attn.rope(q, kp, f, out=out)))
 
 
+def run_paged_cache(args):
+    """The paged cache's operators (GQA Hq=64, Hkv=8, d=128), one JSON line per
+    workload: one token of every user over pages against attn_decode_varlen on
+    contiguous caches; a step of drafted trees over pages (all of its calls, by graph
+    replay) against the attention alone and against as many single-token steps; the
+    rotary positions of a prompt by three axes; a beam search's step; a pool moved
+    together.  Between calls the L2 is flushed."""
+    import torch
+
+    import attention_fa2_fwd_sm_gb300 as attn
+    from attention_fa2_fwd_sm_gb300 import _build
+    from synthetic_inputs import normal_bf16
+    _build.build()
+    dev = torch.device("cuda", 0)
+    torch.cuda.set_device(dev)
+    peaks, _ = load_peaks()
+    stream = torch.cuda.current_stream(dev)
+    flush = _l2_flush_buffer(torch, dev)
+    Hq, Hkv, d = 64, 8, 128
+    i32 = dict(dtype=torch.int32, device=dev)
+
+    def timed(fn):
+        for _ in range(args.warmup):
+            fn()
+        return round(_time_calls(torch, fn, args.steps, flush, stream) * 1e3, 2)
+
+    def replayed(fn):
+        fn()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            fn()
+        return timed(graph.replay)
+
+    def line(workload, nbytes, **us):
+        print(json.dumps({"mode": "paged-cache", "workload": workload, "Hq": Hq, "Hkv": Hkv, "d": d, "bytes": nbytes,
+                          "hbm_floor_us": round(nbytes / peaks["hbm_gbs"] / 1e3, 2), **us}), flush=True)
+
+    def pool(B, S, page, seed):
+        """Pages of B sequences with room for S keys each, in a random order; their lengths are in (S / 2, S)."""
+        per = -(-S // page)
+        g = torch.Generator().manual_seed(seed)
+        table = torch.randperm(B * per, generator=g).reshape(B, per).to(**i32)
+        lens = torch.randint(S // 2, S + 1, (B,), generator=g).to(**i32)
+        return table, lens, *(normal_bf16((B * per, Hkv, page, d), seed + i, dev) for i in (1, 2))
+
+    B, S = 64, 16384
+    for page in (16, 64, 256):
+        table, lens, kp, vp = pool(B, S, page, 300)
+        q = normal_bf16((B, Hq, 1, d), 303, dev)
+        lens -= 1  # the token's own key is the last one
+        ws = attn.decode_tree(q, kp, vp, lens, page_table=table)[2]
+        us = dict(tree_us=timed(lambda: attn.decode_tree(q, kp, vp, lens, page_table=table, workspace=ws)))
+        whole = lens + 1
+        if page == 256:  # (the same pool's pages, in their order, are contiguous caches of the same lengths)
+            kc, vc = (x.view(B, -1, Hkv, page, d).transpose(1, 2).reshape(B, Hkv, S, d) for x in (kp, vp))
+            q1 = q[:, :, 0].contiguous()
+            wv = attn.decode_varlen(q1, kc, vc, whole)[1]
+            us["varlen_contiguous_us"] = timed(lambda: attn.decode_varlen(q1, kc, vc, whole, workspace=wv))
+            del kc, vc
+        line(f"{B} users, one token, {S // 2}..{S} keys, pages of {page}", 4 * d * Hkv * int(whole.sum()) + 4 * B * Hq * d, **us)
+        del kp, vp, ws
+
+    B, S, T, page = 32, 8192, 16, 64
+    table, lens, kp, vp = pool(B, S, page, 310)
+    lens = (lens - T).clamp_(min=0)
+    refs = torch.ones(kp.shape[0], **i32)
+    q, k, v = (normal_bf16((B, h, T, d), 313 + i, dev) for i, h in enumerate((Hq, Hkv, Hkv)))
+    parents = (torch.arange(T, **i32) - 1).div(2, rounding_mode="floor").expand(B, T).contiguous()
+    last, f = torch.full((B,), T - 1, **i32), attn.rope_freqs(d)
+    mask, pos = attn.tree_mask(parents, lens)
+    ws = attn.decode_tree(q, kp, vp, lens, mask, page_table=table)[2]
+    wp = attn.pages_extend(table, refs, lens, T, kp, vp)[1]
+
+    def step():
+        attn.pages_extend(table, refs, lens, T, kp, vp, workspace=wp)
+        m, p = attn.tree_mask(parents, lens)
+        qr, _ = attn.rope_axes_append(q, k, v, kp, vp, lens, f, positions=p, page_table=table)
+        attn.decode_tree(qr, kp, vp, lens, m, page_table=table, workspace=ws)
+        n = attn.tree_accept(kp, vp, lens, m, last, page_table=table)
+        attn.pages_trim(table, refs, n, n, page)
+
+    # (the trim frees pages, so that a replay's extension takes them again: every step is the same)
+    us = dict(attention_us=timed(lambda: attn.decode_tree(q, kp, vp, lens, mask, page_table=table, workspace=ws)),
+              step_replayed_us=replayed(step))
+    attn.pages_extend(table, refs, lens, T, kp, vp, workspace=wp)
+    q1 = q[:, :, :1].contiguous()
+    us["one_token_us"] = timed(lambda: attn.decode_tree(q1, kp, vp, lens, page_table=table, workspace=ws))
+    line(f"{B} users, trees of {T} tokens, {S // 2}..{S} keys, pages of {page}",
+         4 * d * Hkv * int((lens + T).sum()) + 4 * B * Hq * T * d, **us)
+    del kp, vp, ws
+
+    N = 8192
+    q, k = normal_bf16((1, Hq, N, d), 320, dev), normal_bf16((1, Hkv, N, d), 321, dev)
+    axes = attn.rope_sections((16, 24, 24))
+    at = torch.stack([torch.arange(N) // 1024, torch.arange(N) % 1024 // 32, torch.arange(N) % 32]).to(**i32)
+    out = (torch.empty_like(q), torch.empty_like(k))
+    line(f"rotary positions of {N} tokens by three axes", 4 * (Hq + Hkv) * N * d,
+         axes_us=timed(lambda: attn.rope_axes(q, k, f, axes, at, out=out)))
+
+    B, S, page = 64, 4096, 64
+    table, lens, kp, vp = pool(B, S // 2, page, 330)
+    kp, vp = (torch.cat((x, x)) for x in (kp, vp))
+    own = table.clone(), torch.cat((torch.ones(len(kp) // 2, **i32), torch.zeros(len(kp) // 2, **i32)))
+    table, refs, parent = own[0].clone(), own[1].clone(), torch.arange(B, **i32) // 2
+    wp = attn.pages_extend(table, refs, lens, 0, kp, vp)[1]
+
+    def beams():
+        table.copy_(own[0])
+        refs.copy_(own[1])
+        t, n = attn.pages_fork(table, refs, lens, parent, page)
+        attn.pages_extend(t, refs, n, 1, kp, vp, workspace=wp)
+
+    line(f"{B} beams go on as half of them and get room for a token", 0, fork_extend_replayed_us=replayed(beams))
+
+    gone = torch.arange(B, **i32) % 2 * S  # every other sequence ends
+
+    def together():
+        table.copy_(own[0])
+        refs.copy_(own[1])
+        attn.pages_trim(table, refs, lens, gone, page)
+        attn.pages_compact(table, refs, kp, vp, workspace=wp)
+
+    together()
+    table.copy_(own[0])
+    refs.copy_(own[1])
+    attn.pages_trim(table, refs, lens, gone, page)
+    moved = attn.pages_compact(table, refs, kp, vp, workspace=wp)[0].tolist()[1]
+    line(f"every other of {B} sequences ends, the rest is moved together", 8 * Hkv * page * d * moved,
+         trim_compact_replayed_us=replayed(together))
+
+
 def run_bwd_sweep(args):
     """Backward configurations (MHA, GQA causal and non-causal, DeepSeek-like
     d=56 causal) in the head-first and block-first orders; one JSON line per
@@ -1063,7 +1194,7 @@ def main():
     ap.add_argument("--impl", default="gb300", choices=["gb300", "reference"])
     ap.add_argument("--mode", default="step",
                     choices=["step", "decode-sweep", "decode-one", "decode-floor", "decode-varlen", "fwd-sweep", "fwd-one",
-                             "fwd-splitkv", "decode-cache",
+                             "fwd-splitkv", "decode-cache", "paged-cache",
                              "bwd-one", "bwd-sweep", "die-map"],
                     help="step: the contract's one-line benchmark; the sweeps print one line "
                          "per configuration; fwd-one times one forward configuration")
@@ -1104,6 +1235,8 @@ def main():
         return run_decode_varlen(args)
     if args.mode == "decode-cache":
         return run_decode_cache(args)
+    if args.mode == "paged-cache":
+        return run_paged_cache(args)
     if args.mode == "decode-floor":
         return run_decode_floor(args)
     if args.mode == "fwd-splitkv":
