@@ -42,8 +42,8 @@
 //   one token, 64 users of 8001 .. 16001 keys: 431 us contiguous (7.3 TB/s), 458 in pages of 16;
 //   16 tokens, 32 users of up to 8192 keys, pages of 64: 148 us (5.5 TB/s), of which some 15 are the start, the last
 //     CTAs' late end (they differ by 6%, as the memory serves some SMs better) and the merge;
-//   64 tokens, 16 users of up to 32768 keys: 606 us, 1345 TFLOP/s (all 512 rows of a pair counted), 0.7 of the rate of a
-//     large matrix product, as the forward kernel: exponentials and products take about the same time;
+//   64 tokens, 16 users of up to 32768 keys: 600 us, 1360 TFLOP/s (all 512 rows of a pair counted), 0.7 of the rate of a
+//     large matrix product, as the forward kernel: 3240 clocks a block of 128 keys, of which the products need 2048;
 //   8 tokens, 128 users of 512 keys: 66 us; a pair costs its start and end (4 us) besides its keys.
 // One kernel for both, of 128-key blocks with both chains at every block, took 524 us for the first (pages of 128), 167 for
 // the second and 655 for the third.
@@ -1297,6 +1297,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (u.n == 0) break;
             if (t > 0 && !second) continue;
             const bool live = row < p.rows && token < u.tb;
+            // A warp whose rows have no token leaves its scores as they are: rows that nobody looks at.  (16 users x 32768
+            // keys, 64 tokens, of which 32 are there: 602 -> 566 us.)
+            const bool any_live = __any_sync(0xffffffffu, live);
             if ((u.j0 + u.n) * kBlock > u.len) mask.load(p, u, token);
             Holes<kBlock> holes;
             holes.start(p, u);
@@ -1309,7 +1312,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 ok = wait_warp(bar(C::kSFull + t), blocks & 1, p.wait_ns, abort_flag);
                 if (!ok) break;
                 if (frees) mbar_arrive_elect(bar(C::kKVEmpty + fills % C::kStages));
-                if (has_rows) {
+                if (any_live) {
                     tc_fence_after();
                     Scores<kBlock> s;
                     s.load(tS);
