@@ -482,20 +482,36 @@ struct Scores {
     }
 };
 
-// A row's running softmax.  The reference maximum is exact for the first block that shows the row a key, and kept while
-// the exponentials cannot overflow (their sum below 2^60); see fwd_kernel.cuh.
+// A row's running softmax.  The reference is the maximum of the first block that shows the row a key, and kept until
+// exponentials are some 2^16 times as large: then the row's output is scaled.  Every row decides for itself, so that none
+// depends on another.  kMaxFirst: by the maximum of every block, before its exponentials.  Otherwise by their sum, after
+// which the few blocks that need it take their exponentials again: no maxima, but the scores have to be kept, and the code
+// is twice as long.  In us, by the sum and by the maximum: 128 users of 512 keys, 8 tokens 71, 63; 16 users of up to 32768
+// keys, 64 tokens, d = 64 513, 486; but d = 128, where products and exponentials hold each other up, 600, 604 and in pages
+// of 16 608, 636.
+constexpr float kSlack = 16.f;  // log2 units
+template <bool kMaxFirst>
 struct State {
     float m, l, corr;
     __device__ __forceinline__ void clear() { m = -INFINITY, l = 0.f; }
     // Log-sum-exp in log2 units; -inf for a row without a key.
     __device__ __forceinline__ float total(bool live) const { return live && l != 0.f ? m + __log2f(l) : -INFINITY; }
-    // Adds a block; true (for all lanes) if the maximum of a row moved, so that its output has to be scaled by corr.
+    // Adds a block; true (for all lanes) if the reference of a row moved, so that its output has to be scaled by corr.
     // Rows past the last one (`use` false) hold anything.
     template <int kBlock>
     __device__ __forceinline__ bool add(const Scores<kBlock> &s, uint32_t tS, float sl2, bool use) {
-        float sum;
-        bool again = false, twice = false, over = false;  // over: this row's sum; the others keep theirs to the bit
         corr = 1.f;
+        bool over = false;
+        if constexpr (kMaxFirst) {
+            const float top = s.top() * sl2;
+            if (m == -INFINITY) m = top;
+            over = use && top > m + kSlack;
+            if (over) corr = fast_exp2(m - top), m = top;
+            l = l * corr + s.exponentials(tS, sl2, m == -INFINITY ? 0.f : -m);
+            return __any_sync(0xffffffffu, over);
+        }
+        float sum;
+        bool again = false, twice = false;
         do {
             if (m == -INFINITY || over) {
                 const float to = fmaxf(m, s.top() * sl2);
@@ -503,7 +519,7 @@ struct State {
                 m = to;
             }
             sum = s.exponentials(tS, sl2, m == -INFINITY ? 0.f : -m);
-            over = use && !(sum < 0x1p60f);
+            over = use && !(sum < kBlock * 0x1p16f);
             again = !again && __any_sync(0xffffffffu, over);
             if (again) {
                 tmem_wait_st();
@@ -514,6 +530,7 @@ struct State {
         return twice && __any_sync(0xffffffffu, corr != 1.f);
     }
 };
+static_assert(kSlack == 16.f, "2^16 above");
 
 template <int D>
 __device__ __forceinline__ void scale_output(uint32_t tO, float corr) {
@@ -743,9 +760,13 @@ __global__ void __launch_bounds__(PairCfg<D>::kThreads, 1)
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    // Per chain: warps that plan and load Q and K, that load V, that issue MMAs, one to spare; then the softmax warps.
-    const int t = warp >> 2 & 1, role = warp < 8 ? warp & 3 : 4;
+    // Per chain: warps that plan and load Q and K, that load V, that issue MMAs, one to spare; then the softmax warps.  At
+    // d = 64 the spare one shares its issue slots with the softmax warp of the first 32 rows, which is all there is of few
+    // tokens, instead of the K loader: 64 users, one token, 252 us, now 247; in pages of 16 285, 273; 16 tokens 161 either
+    // way.  (At d = 128, where a block has twice the bytes, 32 users with 16 tokens 148.3 us, and 149.)
     enum { kLoadK, kLoadV, kIssue, kSpare, kSoftmax };
+    const int t = warp >> 2 & 1, place = warp & 3;
+    const int role = warp >= 8 ? kSoftmax : D == 64 && (place == kLoadK || place == kSpare) ? kSpare - place : place;
     const int share = blockIdx.x;
     constexpr uint32_t stages = C::kStages;
     const int q_bytes = C::q_bytes(p.q_rows), chain_bytes = C::chain_bytes(p.q_rows);
@@ -979,7 +1000,7 @@ __global__ void __launch_bounds__(PairCfg<D>::kThreads, 1)
             Holes<kBlock> holes;
             holes.start(p, u);
             uint32_t *odd = odd_rows + (qi & 3) * kMaskWords;
-            State st;
+            State<true> st;
             st.clear();
             Place last = at;  // of the last block's V
 #pragma unroll 1
@@ -1304,7 +1325,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             Holes<kBlock> holes;
             holes.start(p, u);
             uint32_t *odd = odd_rows + (qi & 3) * kMaskWords;
-            State st;
+            State<D == 64> st;
             st.clear();
             for (int j = 0; j < u.n; ++j, ++blocks, fills += 2) {
                 const int key = (u.j0 + j) * kBlock;
