@@ -350,3 +350,18 @@ def test_helper_refusals(attn):
         a.update(bad)
         with pytest.raises(attn.AttnError):
             attn.decode_tree(**a)
+
+
+@pytest.mark.parametrize("Hq,T,d", [(8, 6, 128), (8, 6, 64), (8, 40, 128), (8, 40, 64)])
+def test_rising_scores_and_large_values(attn, Hq, T, d):
+    """Every block's scores are above those of all before it, by up to 300 in all, and values are near 2^90: a reference
+    that is kept too long makes sums that 32 bits do not hold, although the result is no larger than the values."""
+    S = 900
+    k, v, _ = a_cache(2, 1, S, d, 0, 700)
+    base = normal_bf16((d,), 703, DEV).float()
+    rise = torch.arange(S, device=DEV).float() / S * 300 * d ** 0.5 / (base @ base)
+    k = (rise[None, None, :, None] * base + 0.1 * k.float()).bfloat16()
+    v = (v.float() * 2.0 ** 90).bfloat16()
+    q = (base + 0.1 * normal_bf16((2, Hq, T, d), 704, DEV).float()).bfloat16()
+    o, _, _ = run_and_check(attn, q, k, v, None, 0, [800, 450], parents=random_tree(2, T, 3))
+    assert torch.all(torch.isfinite(o))
