@@ -1094,15 +1094,11 @@ struct RowsCfg {
     static constexpr int kBlock = 128, kChunks = D / 64, kChunkBytes = 128 * 128;
     static constexpr int kQBytes = kTileM * D * 2, kKVBytes = kBlock * D * 2;
     static constexpr int kStages = D == 128 ? 4 : 8;
-    // d = 64 leaves room in TMEM for P apart from S: S(j + 1) is made while S(j) becomes P(j), and the chain is the softmax
-    // alone.  16 users of up to 32768 keys, 64 tokens: 486 us, now XXX.
-    static constexpr bool kApart = D == 64;
-    static constexpr int kOCol = 2 * kTileM, kPCol = kOCol + 2 * D;
+    static constexpr int kOCol = 2 * kTileM;
     static constexpr int kOddOffset = 2 * kQBytes + kStages * kKVBytes;
     static constexpr int kBarOffset = kOddOffset + 4 * kMaskWords * 4;
     static constexpr int kQFull = 0, kQEmpty = 2, kSFull = 4, kPFull = 6, kOFull = 8, kOEmpty = 10, kUFull = 12, kUEmpty = 14,
-                         kDrain = 16, kKVFull = 17, kKVEmpty = 17 + kStages;
-    static constexpr int kSTaken = 17 + 2 * kStages, kPDone = kSTaken + 2, kNumBars = kSTaken + (kApart ? 4 : 0);  // where P is apart
+                         kDrain = 16, kKVFull = 17, kKVEmpty = 17 + kStages, kNumBars = 17 + 2 * kStages;
     static constexpr int kUnitOffset = (kBarOffset + kNumBars * 8 + 15) / 16 * 16;
     static constexpr int kSmemBytes = kUnitOffset + 2 * kUnitInts * 4 + 16 + 1024;  // units, tmem, abort; alignment
     static_assert(kSmemBytes <= kSmemMax, "shared memory");
@@ -1131,8 +1127,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (threadIdx.x >= 128) {  // a barrier a thread
         const int i = int(threadIdx.x) - 128;
         if (i < C::kNumBars) {
-            const bool four = (i >= C::kPFull && i < C::kPFull + 2) || (i >= C::kOEmpty && i < C::kOEmpty + 2) ||
-                              (C::kApart && i >= C::kSTaken && i < C::kSTaken + 2);
+            const bool four = (i >= C::kPFull && i < C::kPFull + 2) || (i >= C::kOEmpty && i < C::kOEmpty + 2);
             // (a unit's slot: the K, V and MMA warps, the softmax warps)
             mbar_init(bar(i), four ? 4 : i >= C::kUEmpty && i < C::kUEmpty + 2 ? 3 + 8 : 1);
         }
@@ -1249,7 +1244,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const uint64_t dQ = smem_desc_sw128(smem_u32(sQ), 16, 1024), dK = smem_desc_sw128(smem_u32(sKV), 16, 1024),
                            dV = smem_desc_sw128(smem_u32(sKV), C::kChunkBytes, 1024);
             const int tiles = second ? 2 : 1;
-            uint32_t fills = 0, blocks = 0, done = 0, scores = 0;
+            uint32_t fills = 0, blocks = 0, done = 0;
             bool ok = true;
             auto slot_off = [&](uint32_t f) { return uint64_t(f % C::kStages * (C::kKVBytes >> 4)); };
             auto wait_slot = [&](uint32_t f) {
@@ -1262,70 +1257,37 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int n = __shfl_sync(0xffffffffu, int(units[kUnitInts * qs + 3]), 0);
                 mbar_arrive_elect(bar(C::kUEmpty + qs));
                 if (n == 0) break;
-                if constexpr (C::kApart) {
-                    // S(t, 0); then S(t, j + 1) once S(t, j) has been taken, and P(t, j) V.
-                    for (int j = -1; ok && j < n; ++j) {
-                        const uint32_t fV = fills + 2 * j + 1, fK = fV + 1;
+                // S(t, 0); then P(t, j) V and S(t, j + 1), so that the commit that announces S(t, j + 1) says that P(t, j) V
+                // is complete too.
+                for (int j = -1; ok && j < n; ++j) {
+                    const uint32_t fV = fills + 2 * j + 1, fK = fV + 1;
 #pragma unroll 1
-                        for (int t = 0; t < tiles; ++t) {
-                            if (j + 1 < n) {
-                                if (j < 0) ok = wait_warp(bar(C::kQFull + t), done & 1, p.wait_ns, abort_flag);
-                                if (ok && t == 0) ok = wait_slot(fK);
-                                if (ok && scores > 0) ok = wait_warp(bar(C::kSTaken + t), (scores - 1) & 1, p.wait_ns, abort_flag);
-                                if (!ok) break;
-                                tc_fence_after();
-                                issue_qk<D>(tmem + t * kTileM, dQ + uint64_t(t * (C::kQBytes >> 4)), C::kChunkBytes, dK + slot_off(fK),
-                                            C::kChunkBytes, kIdescQK);
-                                tc_commit_elect(bar(C::kSFull + t));
-                                if (j + 1 == n - 1) tc_commit_elect(bar(C::kQEmpty + t));  // Q's last product
-                            }
-                            if (j < 0) continue;
+                    for (int t = 0; t < tiles; ++t) {
+                        if (j >= 0) {
                             ok = wait_warp(bar(C::kPFull + t), blocks & 1, p.wait_ns, abort_flag);
                             if (ok && j == 0 && done > 0) ok = wait_warp(bar(C::kOEmpty + t), (done - 1) & 1, p.wait_ns, abort_flag);
                             if (ok && t == 0) ok = wait_slot(fV);
                             if (!ok) break;
                             tc_fence_after();
-                            issue_pv<kBlock>(tmem + C::kOCol + t * D, tmem + C::kPCol + t * (kBlock / 2), dV + slot_off(fV), kIdescPV, j > 0);
-                            tc_commit_elect(bar(C::kPDone + t));
+                            issue_pv<kBlock>(tmem + C::kOCol + t * D, tmem + t * kTileM, dV + slot_off(fV), kIdescPV, j > 0);
                             if (t == tiles - 1) tc_commit_elect(bar(C::kKVEmpty + fV % C::kStages));
-                            if (j == n - 1) tc_commit_elect(bar(C::kOFull + t));
+                        } else {
+                            ok = wait_warp(bar(C::kQFull + t), done & 1, p.wait_ns, abort_flag);
+                            if (!ok) break;
                         }
-                        if (j + 1 < n) ++scores;
-                        if (j >= 0) ++blocks;
-                    }
-                } else {
-                    // S(t, 0); then P(t, j) V and S(t, j + 1), so that the commit that announces S(t, j + 1) says that P(t, j) V
-                    // is complete too.
-                    for (int j = -1; ok && j < n; ++j) {
-                        const uint32_t fV = fills + 2 * j + 1, fK = fV + 1;
-#pragma unroll 1
-                        for (int t = 0; t < tiles; ++t) {
-                            if (j >= 0) {
-                                ok = wait_warp(bar(C::kPFull + t), blocks & 1, p.wait_ns, abort_flag);
-                                if (ok && j == 0 && done > 0) ok = wait_warp(bar(C::kOEmpty + t), (done - 1) & 1, p.wait_ns, abort_flag);
-                                if (ok && t == 0) ok = wait_slot(fV);
-                                if (!ok) break;
-                                tc_fence_after();
-                                issue_pv<kBlock>(tmem + C::kOCol + t * D, tmem + t * kTileM, dV + slot_off(fV), kIdescPV, j > 0);
-                                if (t == tiles - 1) tc_commit_elect(bar(C::kKVEmpty + fV % C::kStages));
-                            } else {
-                                ok = wait_warp(bar(C::kQFull + t), done & 1, p.wait_ns, abort_flag);
-                                if (!ok) break;
-                            }
-                            if (j + 1 < n) {
-                                if (t == 0) ok = wait_slot(fK);
-                                if (!ok) break;
-                                tc_fence_after();
-                                issue_qk<D>(tmem + t * kTileM, dQ + uint64_t(t * (C::kQBytes >> 4)), C::kChunkBytes, dK + slot_off(fK),
-                                            C::kChunkBytes, kIdescQK);
-                                tc_commit_elect(bar(C::kSFull + t));
-                                if (j + 1 == n - 1) tc_commit_elect(bar(C::kQEmpty + t));  // Q's last product
-                            } else {
-                                tc_commit_elect(bar(C::kOFull + t));
-                            }
+                        if (j + 1 < n) {
+                            if (t == 0) ok = wait_slot(fK);
+                            if (!ok) break;
+                            tc_fence_after();
+                            issue_qk<D>(tmem + t * kTileM, dQ + uint64_t(t * (C::kQBytes >> 4)), C::kChunkBytes, dK + slot_off(fK),
+                                        C::kChunkBytes, kIdescQK);
+                            tc_commit_elect(bar(C::kSFull + t));
+                            if (j + 1 == n - 1) tc_commit_elect(bar(C::kQEmpty + t));  // Q's last product
+                        } else {
+                            tc_commit_elect(bar(C::kOFull + t));
                         }
-                        if (j >= 0) ++blocks;
                     }
+                    if (j >= 0) ++blocks;
                 }
                 fills += 2 * n;
                 ++done;
@@ -1341,7 +1303,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int row0 = (2 * m + t) * kTileM + quarter * 32, row = row0 + lane, token = row % p.T;
         const uint32_t lanes = uint32_t(quarter * 32) << 16;
         const uint32_t tS = tmem + lanes + t * kTileM, tO = tmem + lanes + C::kOCol + t * D;
-        const uint32_t tP = C::kApart ? tmem + lanes + C::kPCol + t * (kBlock / 2) : tS;
         const bool has_rows = row0 < p.rows;  // of this warp; the others only keep step
         const bool frees = quarter == 0 && t == (second ? 1 : 0);  // K's slots: the last chain to see S
         uint32_t blocks = 0, fills = 0;
@@ -1372,38 +1333,18 @@ __global__ void __launch_bounds__(kThreads, 1)
                 ok = wait_warp(bar(C::kSFull + t), blocks & 1, p.wait_ns, abort_flag);
                 if (!ok) break;
                 if (frees) mbar_arrive_elect(bar(C::kKVEmpty + fills % C::kStages));
-                // Where P is apart, its place is free when the last product has read it (the next S is on its way meanwhile).
-                // Warps without rows wait as well: S(j + 1) may be there before all of P(j), and an arrival for P(j + 1)
-                // must not count for P(j).
-                auto last_read = [&]() {
-                    return !C::kApart || j == 0 || wait_warp(bar(C::kPDone + t), (blocks - 1) & 1, p.wait_ns, abort_flag);
-                };
-                auto taken = [&]() {
-                    if (!C::kApart) return;
-                    tc_fence_before();
-                    __syncwarp();
-                    mbar_arrive_elect(bar(C::kSTaken + t));
-                };
                 if (any_live) {
                     tc_fence_after();
                     Scores<kBlock> s;
                     s.load(tS);
-                    taken();
                     if (key + kBlock > u.len || on_page != ~0u) {
                         uint32_t seen[kMaskWords];
                         mask.bits(p, u, token, live, seen);
                         s.hide(p, seen, key, u.len, holes.table != nullptr, on_page);
                     }
-                    ok = last_read();
-                    if (!ok) break;
-                    if (C::kApart) tc_fence_after();
-                    if (st.add(s, tP, p.scale_log2, row < p.rows) && j > 0) scale_output<D>(tO, st.corr);
+                    if (st.add(s, tS, p.scale_log2, row < p.rows) && j > 0) scale_output<D>(tO, st.corr);
                     tmem_wait_st();
                     tc_fence_before();
-                } else {
-                    taken();
-                    ok = last_read();
-                    if (!ok) break;
                 }
                 if (key + kBlock > u.len && t == 0) {
                     // (the other tile's product of this block is issued behind this one's)
