@@ -32,7 +32,7 @@
 // depth in a tree) and pair i turns by the one that axes[i] names.  The phase of a
 // pair is then its own axis's product; nothing else changes, and nothing else is
 // read but 4 bytes an axis and token: 8192 tokens of 64 + 8 heads by three axes take
-// 51 us (5.9 TB/s of reads and writes; 48 to 49 by one position).  Appending by axes
+// 50 us (6.0 TB/s of reads and writes; 49 to 50 by one position).  Appending by axes
 // also looks the row's page up: a row of a sequence is a row of one of its pages.
 // 4 x 2000 tokens, ragged, into pages of 16: 53.5 us, as into a contiguous cache.
 #include <cuda_bf16.h>
@@ -208,9 +208,11 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const Params p) {
     if constexpr (kLayout == kHalfVec || kLayout == kInterVec) {
         constexpr int kFreqs = kLayout == kHalfVec ? 8 : 4;
         float c[8], s[8];
-        if (turn)
+        auto sines = [&]() {  // while the first heads' loads are in flight (2048 tokens, 32 + 8 heads: 10.3 us, now 8.4)
+            if (turn)
 #pragma unroll
-            for (int i = 0; i < kFreqs; ++i) sin_cos(turns[item * kFreqs + i], pos_of(item * kFreqs + i), p.sign, p.scale, c[i], s[i]);
+                for (int i = 0; i < kFreqs; ++i) sin_cos(turns[item * kFreqs + i], pos_of(item * kFreqs + i), p.sign, p.scale, c[i], s[i]);
+        };
         if (kLayout == kHalfVec && item < p.rot_items) {
             src += item * 8;
             dst += item * 8;
@@ -224,6 +226,7 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const Params p) {
                         x[i] = __ldcs(reinterpret_cast<const uint4 *>(q));
                         y[i] = __ldcs(reinterpret_cast<const uint4 *>(q + half));
                     }
+                if (h == h0) sines();
 #pragma unroll
                 for (int i = 0; i < kBatch; ++i)
                     if (h + i < h1) {
@@ -242,6 +245,7 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const Params p) {
 #pragma unroll
                 for (int i = 0; i < kBatch; ++i)
                     if (h + i < h1) x[i] = __ldcs(reinterpret_cast<const uint4 *>(src + (h + i) * t.in_h));
+                if (h == h0 && kLayout == kInterVec) sines();
 #pragma unroll
                 for (int i = 0; i < kBatch; ++i)
                     if (h + i < h1) {
