@@ -1380,9 +1380,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
 }
 
-// Rows of the pair that goes on behind share blockIdx.x: their partials (2 x + 1, 2 (x + 1), 2 (x + 2), ...) by the
+// Rows of the pair that goes on behind share x: their partials (2 x + 1, 2 (x + 1), 2 (x + 2), ...) by the
 // log-sum-exps' weights.  A warp takes kRows rows at once, with the loads of all of them in flight; kSplit warps share
-// the partials of the same rows.
+// the partials of the same rows.  x is blockIdx.x; or, where pairs are few and rows many, the blockIdx.x-th share that has
+// such a pair, so that no blocks only look and leave.  1 user of up to 8192 keys, both kernels, by blockIdx.x and by
+// search: 2 tokens (16 rows) 18.9 us, 20.6; 4 tokens 20.6, 20.6; 8 tokens (2432 blocks or 128) 22.6, 20.6; 32 tokens 31.6,
+// 26.7.
 template <int D, int kSplit>
 __global__ void __launch_bounds__(kMergeWarps * 32) merge_kernel(const Params p) {
     constexpr int kCols = D / 32, kRows = 4, kAhead = 2;
@@ -1391,10 +1394,36 @@ __global__ void __launch_bounds__(kMergeWarps * 32) merge_kernel(const Params p)
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, part = warp % kSplit;
     const int row0 = (blockIdx.y * (kMergeWarps / kSplit) + warp / kSplit) * kRows;
     griddep_wait();
-    const int4 cut = p.cuts[blockIdx.x];
+    int4 cut = make_int4(0, 0, 0, 0);
+    int x = blockIdx.x;
+    if (kSplit == 1 || gridDim.x == unsigned(p.shares)) {
+        cut = p.cuts[x];
+    } else {
+        __shared__ int4 cut_sh;
+        __shared__ int x_sh, counts[kMergeWarps];
+        if (threadIdx.x == 0) cut_sh = cut;
+        int before = 0;
+        for (int first = 0; first < p.shares; first += kMergeWarps * 32) {
+            const int i = first + int(threadIdx.x);
+            const int4 c = i < p.shares ? p.cuts[i] : make_int4(0, 0, 0, 0);
+            const uint32_t vote = __ballot_sync(0xffffffffu, c.z > 0);
+            if (first > 0) __syncthreads();
+            if (lane == 0) counts[warp] = __popc(vote);
+            __syncthreads();
+            int rank = before + __popc(vote & ((1u << lane) - 1));
+            for (int w = 0; w < kMergeWarps; ++w) {
+                rank += w < warp ? counts[w] : 0;
+                before += counts[w];
+            }
+            if (c.z > 0 && rank == x) cut_sh = c, x_sh = i;
+        }
+        __syncthreads();
+        cut = cut_sh;
+        x = x_sh;
+    }
     if (cut.z == 0 || (kSplit == 1 && row0 >= p.rows)) return;
     const int rows = min(kRows, p.rows - row0);  // (below 1: none, but the warp keeps step)
-    auto at = [&](int i, int r) { return (size_t)(2 * (blockIdx.x + i) + (i == 0 ? 1 : 0)) * p.rows + row0 + r; };
+    auto at = [&](int i, int r) { return (size_t)(2 * (x + i) + (i == 0 ? 1 : 0)) * p.rows + row0 + r; };
     // Lane 8 r + k: row r's partials k, k + 8, ...; the first kHeld of them stay in registers.
     constexpr int kHeld = 5;
     const int r8 = lane >> 3, k8 = lane & 7;
@@ -1570,9 +1599,10 @@ int launch(const DecodeTreeLaunch &a, const Layout &l, cudaStream_t stream) {
     if (l.shares == 1 || l.whole) return 0;  // nothing is cut
     // Few pairs are cut into many partials each: then all warps of a block take a part of them.
     const bool split = l.shares >= 8LL * a.B * a.Hkv;
-    const int per = split ? 4 : 4 * kMergeWarps;
+    const int per = split ? 4 : 4 * kMergeWarps, groups = (rows + per - 1) / per;
+    const bool find = split && groups > 8;  // (see merge_kernel)
     e = dec::launch_programmatic(split ? merge_kernel<D, kMergeWarps> : merge_kernel<D, 1>,
-                                 dim3(unsigned(l.shares), unsigned((rows + per - 1) / per)), dim3(kMergeWarps * 32), 0, stream, p);
+                                 dim3(unsigned(find ? a.B * a.Hkv : l.shares), unsigned(groups)), dim3(kMergeWarps * 32), 0, stream, p);
     return e == cudaSuccess ? 0 : note_cuda_error(e, "merge_kernel (drafted tokens) launch");
 }
 
