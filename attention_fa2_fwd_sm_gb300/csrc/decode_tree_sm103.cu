@@ -42,9 +42,9 @@
 //   one token, 64 users of 8001 .. 16001 keys: 431 us contiguous (7.3 TB/s), 458 in pages of 16;
 //   16 tokens, 32 users of up to 8192 keys, pages of 64: 148 us (5.5 TB/s), of which some 15 are the start, the last
 //     CTAs' late end (they differ by 6%, as the memory serves some SMs better) and the merge;
-//   64 tokens, 16 users of up to 32768 keys: 600 us, 1360 TFLOP/s (all 512 rows of a pair counted), 0.7 of the rate of a
-//     large matrix product, as the forward kernel: 3240 clocks a block of 128 keys, of which the products need 2048;
-//   8 tokens, 128 users of 512 keys: 66 us; a pair costs its start and end (4 us) besides its keys.
+//   64 tokens, 16 users of up to 32768 keys: 591 us, 1380 TFLOP/s (all 512 rows of a pair counted), 0.7 of the rate of a
+//     large matrix product, as the forward kernel: 3200 clocks a block of 128 keys, of which the products need 2048;
+//   8 tokens, 128 users of 512 keys: 60 us; a pair costs its start and end (4 us) besides its keys.
 // One kernel for both, of 128-key blocks with both chains at every block, took 524 us for the first (pages of 128), 167 for
 // the second and 655 for the third.
 //
@@ -96,6 +96,7 @@ constexpr int kLaunchRegs = 168, kCtrlRegs = 120, kSoftmaxRegs = 192;
 static_assert(128 * kCtrlRegs + 256 * kSoftmaxRegs <= kThreads * kLaunchRegs, "register split");
 constexpr int kTmemCols = 512;
 constexpr int kMaskWords = 8;  // 32-bit words of a row's mask: 256 drafted tokens
+constexpr int kLongUnit = 16;  // blocks; a look at the pages of as many is not felt
 constexpr int kUnitInts = 12;  // of a unit in the queue
 constexpr int kMergeWarps = 8;
 constexpr uint64_t kDrainNs = 1000000000ull;  // for copies and products in flight when a CTA gives up
@@ -351,6 +352,41 @@ __device__ __forceinline__ uint32_t mask_bits(const uint32_t (&m)[kMaskWords], i
     return __funnelshift_r(lo, hi, u & 31);
 }
 
+// The 64 scores at tS in TMEM that the row does not see become -inf: keys on no page (on_page: a bit a page of the block),
+// and of the keys from the drafted ones on (u: the number of the first score's; negative: cached) those from `end` on and
+// those without a bit in w.  For pairs_kernel: few of its blocks need it, and the others would carry its code through their
+// loop (128 users of 512 keys, 8 tokens 67 us, now 60; 32 users of up to 16384 keys, 16 tokens, d = 64 162, now 156).  In
+// rows_kernel, where a block has twice the keys, the mask stays in registers (38 users of 64 keys, 64 tokens 37 us, out of
+// line 39), in a loop of its own.
+__device__ __noinline__ void hide_scores(uint32_t tS, int u, int end, unsigned long long w0, unsigned long long w1,
+                                         unsigned long long w2, unsigned long long w3, uint32_t on_page, int page_size) {
+    auto word = [&](int i) {
+        const int left = end - 32 * i;
+        if (i < 0) return ~0u;
+        if (i >= kMaskWords || left <= 0) return 0u;
+        const unsigned long long w = i < 2 ? w0 : i < 4 ? w1 : i < 6 ? w2 : w3;
+        const uint32_t x = uint32_t(i & 1 ? w >> 32 : w);
+        return left < 32 ? x & ((1u << left) - 1) : x;
+    };
+    uint32_t x[2][32];
+    tmem_ld32(tS, x[0]);
+    tmem_ld32(tS + 32, x[1]);
+    tmem_wait_ld();
+#pragma unroll
+    for (int h = 0; h < 2; ++h, u += 32) {
+        uint32_t bits = __funnelshift_r(word(u >> 5), word((u >> 5) + 1), u & 31);
+        // Pages of 16: two in 32 keys.
+        const int at = page_size < 64 ? 32 * h / page_size : 0;
+        if (!(on_page >> at & 1)) bits &= page_size == 16 ? 0xffff0000u : 0u;
+        if (page_size == 16 && !(on_page >> (at + 1) & 1)) bits &= 0x0000ffffu;
+#pragma unroll
+        for (int i = 0; i < 32; ++i)
+            if (!(bits >> i & 1)) x[h][i] = 0xff800000u;  // -inf
+        tmem_st32(tS + 32 * h, x[h]);
+    }
+    tmem_wait_st();
+}
+
 // What a row sees of a unit's drafted tokens, 64 a word; loaded ahead, looked at where the blocks end.
 struct Seen {
     unsigned long long w[kMaskWords / 2] = {};
@@ -364,9 +400,21 @@ struct Seen {
         for (int i = 0; i < kMaskWords / 2; ++i)
             if (i < words) w[i] = row[i];
     }
+    // The first drafted token that the row does not see, nor any behind it.
+    __device__ __forceinline__ int end(const Params &p, const Unit &u, int token, bool live) const {
+        const int drafted = u.keys - u.len;
+        return !live ? 0 : p.mask ? drafted : min(drafted, token + 1);
+    }
+    // The scores of the 64 keys from `key` on, at tS.
+    __device__ __forceinline__ void hide(const Params &p, const Unit &u, int token, bool live, uint32_t tS, int key,
+                                         uint32_t on_page) const {
+        const bool all = !p.mask;
+        hide_scores(tS, key - u.len, end(p, u, token, live), all ? ~0ull : w[0], all ? ~0ull : w[1], all ? ~0ull : w[2],
+                    all ? ~0ull : w[3], on_page, p.page_size);
+    }
     // As 32-bit words, without keys that do not exist; without a mask, a chain sees what is before it.
     __device__ __forceinline__ void bits(const Params &p, const Unit &u, int token, bool live, uint32_t (&out)[kMaskWords]) const {
-        const int drafted = u.keys - u.len, end = !live ? 0 : p.mask ? drafted : min(drafted, token + 1);
+        const int end = this->end(p, u, token, live);
 #pragma unroll
         for (int i = 0; i < kMaskWords / 2; ++i) {
             unsigned long long x = p.mask ? w[i] : ~0ull;
@@ -1014,13 +1062,9 @@ __global__ void __launch_bounds__(PairCfg<D>::kThreads, 1)
                 if (has_rows) {
                     const uint32_t tS = tS0 + buf * kBlock;
                     tc_fence_after();
+                    if (key + kBlock > u.len || on_page != ~0u) mask.hide(p, u, token, live, tS, key, on_page);
                     Scores<kBlock> s;
                     s.load(tS);
-                    if (key + kBlock > u.len || on_page != ~0u) {
-                        uint32_t seen[kMaskWords];
-                        mask.bits(p, u, token, live, seen);
-                        s.hide(p, seen, key, u.len, holes.table != nullptr, on_page);
-                    }
                     if (st.add(s, tS, p.scale_log2, row < p.rows) && j > 0) {
                         // S(j) was issued ahead of the last product into O: wait for that, by its V slot, which nobody can
                         // have filled and freed again before this block's P.
@@ -1163,11 +1207,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             // -------------------------------------------- planner: the units, and Q
             uint32_t q_loads = 0;  // per tile (both are loaded for every unit)
             bool ok = true;
-            u.holes = p.table != nullptr;  // (the first unit's entries are looked at block by block)
+            u.holes = p.table != nullptr;  // (a short first unit's entries are looked at block by block)
             for (uint32_t qi = 0; ok; ++qi) {
                 const uint32_t qs = qi & 1;
                 u.n = left > 0 ? min(left, u.nb - u.j0) : 0;
-                if (p.table && qi > 0) u.holes = look_for_holes<kBlock>(p, u);
+                if (p.table && (qi > 0 || u.n >= kLongUnit)) u.holes = look_for_holes<kBlock>(p, u);
                 if (qi >= 2) ok = wait_warp(bar(C::kUEmpty + qs), ((qi >> 1) - 1) & 1, p.wait_ns, abort_flag);
                 if (!ok) break;
                 if (lane == 0) {
@@ -1327,17 +1371,19 @@ __global__ void __launch_bounds__(kThreads, 1)
             uint32_t *odd = odd_rows + (qi & 3) * kMaskWords;
             State<D == 64> st;
             st.clear();
-            for (int j = 0; j < u.n; ++j, ++blocks, fills += 2) {
+            // A block; masked: keys may be drafted, or on no page.
+            auto step = [&](int j, auto masked) {
+                constexpr bool kMasked = decltype(masked)::value;
                 const int key = (u.j0 + j) * kBlock;
-                const uint32_t on_page = holes.next(p, u, j);
+                const uint32_t on_page = kMasked ? holes.next(p, u, j) : ~0u;
                 ok = wait_warp(bar(C::kSFull + t), blocks & 1, p.wait_ns, abort_flag);
-                if (!ok) break;
+                if (!ok) return;
                 if (frees) mbar_arrive_elect(bar(C::kKVEmpty + fills % C::kStages));
                 if (any_live) {
                     tc_fence_after();
                     Scores<kBlock> s;
                     s.load(tS);
-                    if (key + kBlock > u.len || on_page != ~0u) {
+                    if (kMasked && (key + kBlock > u.len || on_page != ~0u)) {
                         uint32_t seen[kMaskWords];
                         mask.bits(p, u, token, live, seen);
                         s.hide(p, seen, key, u.len, holes.table != nullptr, on_page);
@@ -1346,18 +1392,26 @@ __global__ void __launch_bounds__(kThreads, 1)
                     tmem_wait_st();
                     tc_fence_before();
                 }
-                if (key + kBlock > u.len && t == 0) {
+                if (kMasked && key + kBlock > u.len && t == 0) {
                     // (the other tile's product of this block is issued behind this one's)
                     const uint32_t slot = (fills + 1) % C::kStages;
                     ok = wait_warp(bar(C::kKVFull + slot), ((fills + 1) / C::kStages) & 1, p.wait_ns, abort_flag);
-                    if (!ok) break;
+                    if (!ok) return;
                     const int first = max(u.len - key, 0);
                     clean_rows<C::kChunks, kBlock>(sKV + slot * C::kKVBytes, quarter, first, u.keys - key, key + first - u.len, odd);
                     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                 }
                 __syncwarp();
                 mbar_arrive_elect(bar(C::kPFull + t));
-            }
+                ++blocks;
+                fills += 2;
+            };
+            // The blocks of cached keys alone in a loop without the mask's code: 16 users of up to 32768 keys, 64 tokens, 602
+            // us, now 591; in pages of 16 607, now 590; 4 users of up to 8192, 256 tokens, 176, now 171.
+            const int plain = holes.table ? 0 : min(u.n, max(0, u.len / kBlock - u.j0));
+            int j = 0;
+            for (; ok && j < plain; ++j) step(j, std::false_type{});
+            for (; ok && j < u.n; ++j) step(j, std::true_type{});
             if (ok) ok = wait_warp(bar(C::kOFull + t), qi & 1, p.wait_ns, abort_flag);
             if (!ok) break;
             tc_fence_after();
