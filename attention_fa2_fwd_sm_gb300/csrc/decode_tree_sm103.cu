@@ -39,11 +39,11 @@
 // then adds to the rows that see them.
 //
 // What it measured (kernels alone, d = 128, 64 query and 8 KV heads; the copy rate is 6.75 TB/s):
-//   one token, 64 users of 8001 .. 16001 keys: 431 us contiguous (7.3 TB/s), 458 in pages of 16;
-//   16 tokens, 32 users of up to 8192 keys, pages of 64: 148 us (5.5 TB/s), of which some 15 are the start, the last
+//   one token, 64 users of 8001 .. 16001 keys: 436 us contiguous (7.1 TB/s), 459 in pages of 16 (6.9);
+//   16 tokens, 32 users of up to 8192 keys, pages of 64: 148 us (5.8 TB/s), of which some 15 are the start, the last
 //     CTAs' late end (they differ by 6%, as the memory serves some SMs better) and the merge;
-//   64 tokens, 16 users of up to 32768 keys: 591 us, 1380 TFLOP/s (all 512 rows of a pair counted), 0.7 of the rate of a
-//     large matrix product, as the forward kernel: 3200 clocks a block of 128 keys, of which the products need 2048;
+//   64 tokens, 16 users of up to 32768 keys: 592 us, 1510 TFLOP/s (all 512 rows of a pair counted), 0.8 of the rate of a
+//     large matrix product: some 3000 clocks a block of 128 keys, of which the products need 2048;
 //   8 tokens, 128 users of 512 keys: 60 us; a pair costs its start and end (4 us) besides its keys.
 // One kernel for both, of 128-key blocks with both chains at every block, took 524 us for the first (pages of 128), 167 for
 // the second and 655 for the third.
@@ -771,7 +771,7 @@ template <int D>
 struct PairCfg {
     static constexpr int kBlock = 64, kChunks = D / 64, kChunkBytes = kBlock * 128, kKVBytes = kBlock * D * 2;
     // Blocks of a chain's ring.  64 KB on their way are enough for a chain, and more are not better: 64 users of 8001 .. 16001
-    // keys, one token, d = 128, 4 stages 431 us, 5 433, 6 452, 12 451 (7.3 and 7.0 TB/s); d = 64 the same with 4 as with 12.
+    // keys, one token, d = 128, 4 stages 431 us, 5 433, 6 452, 12 451 (7.2 and 6.9 TB/s); d = 64 the same with 4 as with 12.
     // An even number, so that K and V have slots of their own: a loader that waits for a slot has then waited for the
     // round before it too, and no parity is taken for the one of two rounds ago.
     static constexpr int kStages = 4;
