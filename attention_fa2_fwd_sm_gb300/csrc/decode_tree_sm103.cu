@@ -42,7 +42,7 @@
 //   one token, 64 users of 8001 .. 16001 keys: 436 us contiguous (7.1 TB/s), 459 in pages of 16 (6.9);
 //   16 tokens, 32 users of up to 8192 keys, pages of 64: 148 us (5.8 TB/s), of which some 15 are the start, the last
 //     CTAs' late end (they differ by 6%, as the memory serves some SMs better) and the merge;
-//   64 tokens, 16 users of up to 32768 keys: 592 us, 1510 TFLOP/s (all 512 rows of a pair counted), 0.8 of the rate of a
+//   64 tokens, 16 users of up to 32768 keys: 593 us, 1510 TFLOP/s (all 512 rows of a pair counted), 0.8 of the rate of a
 //     large matrix product: some 3000 clocks a block of 128 keys, of which the products need 2048;
 //   8 tokens, 128 users of 512 keys: 60 us; a pair costs its start and end (4 us) besides its keys.
 // One kernel for both, of 128-key blocks with both chains at every block, took 524 us for the first (pages of 128), 167 for
@@ -530,15 +530,13 @@ struct Scores {
     }
 };
 
-// A row's running softmax.  The reference is the maximum of the first block that shows the row a key, and kept until
-// exponentials are some 2^16 times as large: then the row's output is scaled.  Every row decides for itself, so that none
-// depends on another.  kMaxFirst: by the maximum of every block, before its exponentials.  Otherwise by their sum, after
-// which the few blocks that need it take their exponentials again: no maxima, but the scores have to be kept, and the code
-// is twice as long.  In us, by the sum and by the maximum: 128 users of 512 keys, 8 tokens 71, 63; 16 users of up to 32768
-// keys, 64 tokens, d = 64 513, 486; but d = 128, where products and exponentials hold each other up, 600, 604 and in pages
-// of 16 608, 636.
+// A row's running softmax.  The reference is the maximum of the first block that shows the row a key, and kept until a
+// score is more than 2^16 times as heavy: then the row's output is scaled.  Every row decides for itself, so that none
+// depends on another.  The decision is by the maximum of every block, before its exponentials.  By their sum, after which
+// the few blocks that need it take them again (as in fwd_kernel.cuh), costs no maxima, but the scores have to be kept, and
+// the code is twice as long.  In us, by the sum and by the maximum: 128 users of 512 keys, 8 tokens 71, 63; 16 users of up
+// to 32768 keys, 64 tokens, d = 64 486, 468; d = 128 591, 593, in pages of 16 594, 602.
 constexpr float kSlack = 16.f;  // log2 units
-template <bool kMaxFirst>
 struct State {
     float m, l, corr;
     __device__ __forceinline__ void clear() { m = -INFINITY, l = 0.f; }
@@ -548,40 +546,20 @@ struct State {
     // Rows past the last one (`use` false) hold anything.
     template <int kBlock>
     __device__ __forceinline__ bool add(const Scores<kBlock> &s, uint32_t tS, float sl2, bool use) {
+        const float top = s.top() * sl2;
         corr = 1.f;
-        bool over = false;
-        if constexpr (kMaxFirst) {
-            const float top = s.top() * sl2;
-            if (m == -INFINITY) m = top;
-            over = use && top > m + kSlack;
-            if (over) corr = fast_exp2(m - top), m = top;
-            l = l * corr + s.exponentials(tS, sl2, m == -INFINITY ? 0.f : -m);
-            return __any_sync(0xffffffffu, over);
-        }
-        float sum;
-        bool again = false, twice = false;
-        do {
-            if (m == -INFINITY || over) {
-                const float to = fmaxf(m, s.top() * sl2);
-                if (over && to > m) corr = fast_exp2(m - to);
-                m = to;
-            }
-            sum = s.exponentials(tS, sl2, m == -INFINITY ? 0.f : -m);
-            over = use && !(sum < kBlock * 0x1p16f);
-            again = !again && __any_sync(0xffffffffu, over);
-            if (again) {
-                tmem_wait_st();
-                twice = true;
-            }
-        } while (again);
-        l = l * corr + sum;
-        return twice && __any_sync(0xffffffffu, corr != 1.f);
+        if (m == -INFINITY) m = top;
+        const bool over = use && top > m + kSlack;
+        if (over) corr = fast_exp2(m - top), m = top;
+        l = l * corr + s.exponentials(tS, sl2, m == -INFINITY ? 0.f : -m);
+        return __any_sync(0xffffffffu, over);
     }
 };
-static_assert(kSlack == 16.f, "2^16 above");
 
+// (Out of line: its code is not in the loops' way.  16 users of up to 32768 keys, 64 tokens, 588 us, now 580; d = 64 487,
+// now 469; 32 users of up to 16384 keys, 16 tokens, d = 64 157, now 152.)
 template <int D>
-__device__ __forceinline__ void scale_output(uint32_t tO, float corr) {
+__device__ __noinline__ void scale_output(uint32_t tO, float corr) {
 #pragma unroll 1
     for (int c = 0; c < D / 32; ++c) {
         uint32_t x[32];
@@ -1048,7 +1026,7 @@ __global__ void __launch_bounds__(PairCfg<D>::kThreads, 1)
             Holes<kBlock> holes;
             holes.start(p, u);
             uint32_t *odd = odd_rows + (qi & 3) * kMaskWords;
-            State<true> st;
+            State st;
             st.clear();
             Place last = at;  // of the last block's V
 #pragma unroll 1
@@ -1369,7 +1347,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             Holes<kBlock> holes;
             holes.start(p, u);
             uint32_t *odd = odd_rows + (qi & 3) * kMaskWords;
-            State<D == 64> st;
+            State st;
             st.clear();
             // A block; masked: keys may be drafted, or on no page.
             auto step = [&](int j, auto masked) {
@@ -1407,7 +1385,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 fills += 2;
             };
             // The blocks of cached keys alone in a loop without the mask's code: 16 users of up to 32768 keys, 64 tokens, 602
-            // us, now 591; in pages of 16 607, now 590; 4 users of up to 8192, 256 tokens, 176, now 171.
+            // us, then 591; in pages of 16 607, then 590; 4 users of up to 8192, 256 tokens, 176, then 171.
             const int plain = holes.table ? 0 : min(u.n, max(0, u.len / kBlock - u.j0));
             int j = 0;
             for (; ok && j < plain; ++j) step(j, std::false_type{});
