@@ -42,7 +42,7 @@
 //   one token, 64 users of 8001 .. 16001 keys: 436 us contiguous (7.1 TB/s), 459 in pages of 16 (6.9);
 //   16 tokens, 32 users of up to 8192 keys, pages of 64: 148 us (5.8 TB/s), of which some 15 are the start, the last
 //     CTAs' late end (they differ by 6%, as the memory serves some SMs better) and the merge;
-//   64 tokens, 16 users of up to 32768 keys: 583 to 593 us, 1510 TFLOP/s and more (all 512 rows of a pair counted), 0.8 of the rate of a
+//   64 tokens, 16 users of up to 32768 keys: 573 to 585 us, 1540 TFLOP/s and more (all 512 rows of a pair counted), 0.8 of the rate of a
 //     large matrix product: some 3000 clocks a block of 128 keys, of which the products need 2048;
 //   8 tokens, 128 users of 512 keys: 60 us; a pair costs its start and end (4 us) besides its keys.
 // One kernel for both, of 128-key blocks with both chains at every block, took 524 us for the first (pages of 128), 167 for
@@ -1329,23 +1329,31 @@ __global__ void __launch_bounds__(kThreads, 1)
         const bool frees = quarter == 0 && t == (second ? 1 : 0);  // K's slots: the last chain to see S
         uint32_t blocks = 0, fills = 0;
         Seen mask;
+        Holes<kBlock> holes;
         bool ok = true;
-        for (uint32_t qi = 0; ok; ++qi) {
-            const uint32_t qs = qi & 1;
-            ok = wait_warp(bar(C::kUFull + qs), (qi >> 1) & 1, p.wait_ns, abort_flag);
-            if (!ok) break;
-            u.get(units + kUnitInts * qs);
+        // A unit, and the loads that its blocks need: the next one's before the rows of the last are stored (38 users, 64
+        // tokens, 2048 keys 152 us, now 147; 16 users of up to 32768 keys 581, now 573).
+        auto fetch = [&](uint32_t qi, Unit &x, Seen &seen, Holes<kBlock> &h) {
+            if (!wait_warp(bar(C::kUFull + (qi & 1)), (qi >> 1) & 1, p.wait_ns, abort_flag)) return false;
+            x.get(units + kUnitInts * (qi & 1));
             __syncwarp();
-            mbar_arrive_elect(bar(C::kUEmpty + qs));
+            mbar_arrive_elect(bar(C::kUEmpty + (qi & 1)));
+            if (x.n == 0 || (t > 0 && !second)) return true;
+            if ((x.j0 + x.n) * kBlock > x.len) seen.load(p, x, token);
+            h.start(p, x);
+            return true;
+        };
+        ok = fetch(0, u, mask, holes);
+        for (uint32_t qi = 0; ok; ++qi) {
             if (u.n == 0) break;
-            if (t > 0 && !second) continue;
+            if (t > 0 && !second) {
+                ok = fetch(qi + 1, u, mask, holes);
+                continue;
+            }
             const bool live = row < p.rows && token < u.tb;
             // A warp whose rows have no token leaves its scores as they are: rows that nobody looks at.  (16 users x 32768
             // keys, 64 tokens, of which 32 are there: 602 -> 566 us.)
             const bool any_live = __any_sync(0xffffffffu, live);
-            if ((u.j0 + u.n) * kBlock > u.len) mask.load(p, u, token);
-            Holes<kBlock> holes;
-            holes.start(p, u);
             uint32_t *odd = odd_rows + (qi & 3) * kMaskWords;
             State st;
             st.clear();
@@ -1390,6 +1398,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             int j = 0;
             for (; ok && j < plain; ++j) step(j, std::false_type{});
             for (; ok && j < u.n; ++j) step(j, std::true_type{});
+            Unit next = {};
+            Seen next_mask = mask;
+            if (ok) ok = fetch(qi + 1, next, next_mask, holes);
             if (ok) ok = wait_warp(bar(C::kOFull + t), qi & 1, p.wait_ns, abort_flag);
             if (!ok) break;
             tc_fence_after();
@@ -1401,6 +1412,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             tc_fence_before();
             __syncwarp();
             mbar_arrive_elect(bar(C::kOEmpty + t));
+            u = next;
+            mask = next_mask;
         }
     }
 
