@@ -42,7 +42,7 @@
 //   one token, 64 users of 8001 .. 16001 keys: 436 us contiguous (7.1 TB/s), 459 in pages of 16 (6.9);
 //   16 tokens, 32 users of up to 8192 keys, pages of 64: 148 us (5.8 TB/s), of which some 15 are the start, the last
 //     CTAs' late end (they differ by 6%, as the memory serves some SMs better) and the merge;
-//   64 tokens, 16 users of up to 32768 keys: 573 to 585 us, 1540 TFLOP/s and more (all 512 rows of a pair counted), 0.8 of the rate of a
+//   64 tokens, 16 users of up to 32768 keys: 572 us, 1570 TFLOP/s (all 512 rows of a pair counted), 0.8 of the rate of a
 //     large matrix product: some 3000 clocks a block of 128 keys, of which the products need 2048;
 //   8 tokens, 128 users of 512 keys: 60 us; a pair costs its start and end (4 us) besides its keys.
 // One kernel for both, of 128-key blocks with both chains at every block, took 524 us for the first (pages of 128), 167 for
