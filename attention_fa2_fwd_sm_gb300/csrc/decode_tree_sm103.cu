@@ -369,6 +369,7 @@ __device__ __noinline__ void hide_scores(uint32_t tS, int u, int end, unsigned l
         return left < 32 ? x & ((1u << left) - 1) : x;
     };
     uint32_t x[2][32];
+    __syncwarp();
     tmem_ld32(tS, x[0]);
     tmem_ld32(tS + 32, x[1]);
     tmem_wait_ld();
@@ -382,6 +383,7 @@ __device__ __noinline__ void hide_scores(uint32_t tS, int u, int end, unsigned l
 #pragma unroll
         for (int i = 0; i < 32; ++i)
             if (!(bits >> i & 1)) x[h][i] = 0xff800000u;  // -inf
+        __syncwarp();
         tmem_st32(tS + 32 * h, x[h]);
     }
     tmem_wait_st();
@@ -551,8 +553,9 @@ struct State {
         if (m == -INFINITY) m = top;
         const bool over = use && top > m + kSlack;
         if (over) corr = fast_exp2(m - top), m = top;
+        const bool moved = __any_sync(0xffffffffu, over);  // (brings the lanes together for the stores to TMEM, too)
         l = l * corr + s.exponentials(tS, sl2, m == -INFINITY ? 0.f : -m);
-        return __any_sync(0xffffffffu, over);
+        return moved;
     }
 };
 
@@ -588,6 +591,8 @@ __device__ __forceinline__ void store_32(void *to, const uint32_t (&x)[8], bool 
 // the accumulator at tO in TMEM or, where there are two (kTwo), of both, kOther columns apart, times f (and f2): to the
 // outputs where the unit is all of the pair (`whole`), else to row `part` and so on of the partials.  L: the row's
 // log-sum-exp in log2 units, -inf if it has none; odd: drafted rows with elements left out.
+// (Instructions on TMEM are the whole warp's, here and above: where lanes may have gone apart before one, __syncwarp or a
+// vote brings them together.)
 template <int kCols, int D, bool kTwo, int kOther>
 __device__ __forceinline__ void store_rows(const Params &p, const Unit &u, bool whole, size_t part, int row0, uint32_t tO,
                                            int col0, float f, float f2, float L, int token, bool live, const Seen &mask,
@@ -600,16 +605,16 @@ __device__ __forceinline__ void store_rows(const Params &p, const Unit &u, bool 
     for (int col = col0; col < col0 + kCols; col += 32 * (kTwo || kCols < 64 ? 1 : 2)) {
         constexpr int kHalves = kTwo || kCols < 64 ? 1 : 2;
         uint32_t x[2][32];
+        __syncwarp();  // lanes without a row, that have stored nothing, and the others
         tmem_ld32(tO + col, x[0]);
         if constexpr (kTwo || kHalves == 2) tmem_ld32(tO + col + (kTwo ? kOther : 32), x[1]);
         tmem_wait_ld();
-        if (lane >= rows) continue;
         auto scaled = [&](int h, int i, float &a, float &b) {
             float c = -0.f, d = -0.f;
             if constexpr (kTwo) ffma2(c, d, __uint_as_float(x[1][i]), __uint_as_float(x[1][i + 1]), f2, f2, -0.f, -0.f);
             ffma2(a, b, __uint_as_float(x[h][i]), __uint_as_float(x[h][i + 1]), f, f, c, d);
         };
-        if (whole) {
+        if (lane < rows && whole) {
             __nv_bfloat16 *to = p.o + (row + lane) * D + col;
 #pragma unroll
             for (int h = 0; h < kHalves; ++h)
@@ -624,7 +629,7 @@ __device__ __forceinline__ void store_rows(const Params &p, const Unit &u, bool 
                     }
                     store_32(to + 32 * h + 16 * g, y, p.wide);
                 }
-        } else {
+        } else if (lane < rows) {
             float *to = p.part_o + (row + lane) * D + col;
 #pragma unroll
             for (int h = 0; h < kHalves; ++h)
