@@ -1044,24 +1044,27 @@ def _layers(what, kcache, vcache, gpu):
     return shape if len(shape) == 5 else (1, *shape)
 
 
-def tree_accept(kcache, vcache, seqlens, mask, last, page_table=None, seqlens_out=None, stream=None):
+def tree_accept(kcache, vcache, seqlens, mask, last, page_table=None, seqlens_out=None, stream=None, drafted=None):
     """Move the rows of the accepted path, which ends at node `last` ``[B]``
     int32 (-1: nothing is accepted), behind the cached keys by attn_tree_accept;
     returns the new lengths.  Caches ``[B, Hkv, slots, d]`` or, with `page_table`, pages
     ``[pages, Hkv, page_size, d]``, either with a leading dimension of layers.  `mask`
-    as from `tree_mask`, or None: a chain, which has no rows to move."""
+    as from `tree_mask`, or None: a chain, which has no rows to move.  `drafted` is
+    how many tokens a chain has, as the mask's shape says for a tree: a `last` that is
+    none of them accepts nothing.  Without it any `last` of a draft's largest size, 256,
+    counts, and the caller sees to it that its rows have been appended."""
     import torch
     what, i32 = "tree_accept", torch.int32
     gpu = kcache.get_device()
     if stream is not None or gpu < 0 or gpu != torch._C._cuda_getDevice():
         with _elsewhere(what, gpu, stream):
-            got = tree_accept(kcache, vcache, seqlens, mask, last, page_table, seqlens_out)
+            got = tree_accept(kcache, vcache, seqlens, mask, last, page_table, seqlens_out, drafted=drafted)
         _lend(stream, kcache, vcache, seqlens, mask, last, page_table, seqlens_out)
         return got
     layers, pages, Hkv, page, d = _layers(what, kcache, vcache, gpu)
     if seqlens is None or seqlens.dim() != 1:
         raise AttnError(ATTN_ERR_ARG, "tree_accept: seqlens has to be [B]")
-    B, per, T = seqlens.shape[0], 1, 256
+    B, per, T = seqlens.shape[0], 1, 256 if drafted is None else drafted
     if page_table is not None:
         per = page_table.shape[-1]
         _fits(page_table, i32, (B, per), gpu) or _refuse(what, "page_table", page_table, i32, (B, per))
@@ -1071,6 +1074,8 @@ def tree_accept(kcache, vcache, seqlens, mask, last, page_table=None, seqlens_ou
         T = mask.shape[1] if mask.dim() == 3 else 0
         shape = (B, T, (T + 63) // 64)
         _fits(mask, torch.int64, shape, gpu) or _refuse(what, "mask", mask, torch.int64, shape)
+        if drafted is not None and drafted != T:
+            raise AttnError(ATTN_ERR_ARG, f"tree_accept: {drafted} drafted tokens and a mask of {T}")
     if seqlens_out is None:
         seqlens_out = torch.empty_like(seqlens)
     else:
