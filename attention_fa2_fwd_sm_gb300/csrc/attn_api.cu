@@ -720,6 +720,38 @@ static bool shares_with_itself(const Rows &a) {
     return false;
 }
 
+// An array of whole numbers or frequencies that a call reads (or, the new lengths, writes); null or empty: absent.
+struct Array {
+    const void *p;
+    __int128 bytes;
+};
+
+static bool arrays_meet(const Array &a, const Array &b) {
+    if (!a.p || !b.p) return false;
+    const __int128 apart = (__int128)reinterpret_cast<uintptr_t>(a.p) - (__int128)reinterpret_cast<uintptr_t>(b.p);
+    return apart < b.bytes && -apart < a.bytes;
+}
+
+// Whether a row of the tensor and the array share a byte: rows are whole units, so the array may be taken for the units that
+// it touches, [0, len) from its first one.  A row at distance x meets it if -d < x < len; twice that, less the difference of
+// the two, is what meets() asks for.
+static bool rows_meet(const Rows &a, const Array &b) {
+    if (!a.p || !b.p || b.bytes <= 0) return false;
+    const __int128 at = (__int128)reinterpret_cast<uintptr_t>(b.p), first = at / 16, len = (at + b.bytes + 15) / 16 - first;
+    const __int128 apart = (__int128)reinterpret_cast<uintptr_t>(a.p) / 16 - first;
+    if (apart >= len || apart + a.span <= -a.d) return false;
+    Reach dim[3];
+    int n = 0;
+    for (int k = 0; k < 3; ++k) {
+        if (a.s[k] == 0 || a.n[k] < 2) continue;
+        int i = n++;
+        for (; i > 0 && dim[i - 1].s < 2 * (__int128)a.s[k]; --i) dim[i] = dim[i - 1];
+        dim[i] = {2 * (__int128)a.s[k], 0, a.n[k] - 1};
+    }
+    int budget = 2000;
+    return meets(dim, n, 2 * apart + a.d - len, a.d + len, &budget);
+}
+
 static Rows rows_in(const RopeTensor &t, int B, int N, int d) { return Rows(t.in, {t.in_b, t.in_h, t.in_n}, B, t.heads, N, d); }
 static Rows rows_out(const RopeTensor &t, int B, int N, int d) { return Rows(t.out, {t.out_b, t.out_h, t.out_n}, B, t.heads, N, d); }
 
@@ -900,6 +932,11 @@ static int axes_common(const int *positions, long long axis_stride, long long po
     return ATTN_OK;
 }
 
+// From the first position to the last.
+static __int128 positions_bytes(long long axis_stride, long long position_stride, int num_axes, int B, int N) {
+    return ((__int128)axis_stride * (num_axes - 1) + (__int128)position_stride * (B - 1) + N) * 4;
+}
+
 int attn_rope_axes(const void *q, void *q_out, const void *k, void *k_out, const int *positions, long long axis_stride,
                    long long position_stride, int num_axes, const double *inv_freq, const int *axes, int B, int Hq,
                    int Hkv, int N, int d, int rotary_dim, int interleaved, float out_scale, int inverse,
@@ -911,6 +948,10 @@ int attn_rope_axes(const void *q, void *q_out, const void *k, void *k_out, const
     RopeLaunch a;
     rc = rope_tensors(&a, q, q_out, k, k_out, B, Hq, Hkv, N, d, strides);
     if (rc != ATTN_OK) return rc;
+    const Array arrays[] = {{positions, positions_bytes(axis_stride, position_stride, num_axes, B, N)},
+                            {axes, rotary_dim / 2 * 4}, {inv_freq, rotary_dim / 2 * 8}};
+    for (const Array &x : arrays)  // other blocks still read them
+        if (rows_meet(rows_out(a.t[0], B, N, d), x) || rows_meet(rows_out(a.t[1], B, N, d), x)) return ATTN_ERR_ARG;
     a.inv_freq = inv_freq;
     a.pos = positions;
     a.pos_stride = position_stride;
@@ -940,20 +981,28 @@ int attn_rope_axes_append(const void *q, void *q_out, const void *k, const void 
     if (rc == ATTN_OK) rc = paged_sizes(page_table, B, Hkv, num_pages, page_size, max_pages);
     if (rc != ATTN_OK) return rc;
     if (!seqlens || !aligned4(seqlens) || !aligned4(new_lens) || !aligned4(seqlens_out)) return ATTN_ERR_ARG;
-    if (ints_overlap(seqlens_out, seqlens, B) || ints_overlap(seqlens_out, new_lens, B)) return ATTN_ERR_ARG;
-    if (seqlens_out && page_table &&
-        bytes_overlap(seqlens_out, size_t(B) * 4, page_table, size_t(B) * max_pages * 4))
-        return ATTN_ERR_ARG;
-    if (seqlens_out && positions) {  // other blocks still read them
-        const size_t n = size_t(num_axes - 1) * axis_stride + size_t(B - 1) * position_stride + T;
-        if (bytes_overlap(seqlens_out, size_t(B) * 4, positions, n * 4)) return ATTN_ERR_ARG;
-    }
+    const __int128 lens = (__int128)B * 4;
+    const Array written = {seqlens_out, lens};
+    const Array arrays[] = {{seqlens, lens}, {new_lens, lens}, {page_table, lens * max_pages},
+                            {positions, positions_bytes(axis_stride, position_stride, num_axes, B, T)},
+                            {axes, rotary_dim / 2 * 4}, {inv_freq, rotary_dim / 2 * 8}};
+    for (const Array &x : arrays)  // other blocks still read them
+        if (arrays_meet(x, written)) return ATTN_ERR_ARG;
     if (!aligned16(kpages) || !aligned16(vpages)) return ATTN_ERR_ARG;
     const long long row = (long long)page_size * d;
     if ((double)num_pages * Hkv * (double)row >= 9.0e18) return ATTN_ERR_ARG;
     RopeLaunch a;
     rc = append_tensors(&a, q, q_out, k, v, kpages, vpages, B, Hq, Hkv, T, d, num_pages, page_size, strides);
     if (rc != ATTN_OK) return rc;
+    const Rows outs[] = {rows_out(a.t[0], B, T, d), rows_out(a.t[1], num_pages, page_size, d),
+                         rows_out(a.t[2], num_pages, page_size, d)};
+    for (const Rows &out : outs) {
+        if (rows_meet(out, written)) return ATTN_ERR_ARG;
+        for (const Array &x : arrays)
+            if (rows_meet(out, x)) return ATTN_ERR_ARG;
+    }
+    for (const RopeTensor &t : a.t)
+        if (rows_meet(rows_in(t, B, T, d), written)) return ATTN_ERR_ARG;
     a.inv_freq = inv_freq;
     a.pos = positions;
     a.pos_stride = position_stride;

@@ -516,8 +516,8 @@ int attn_rope_append(const void *q, void *q_out, const void *k, const void *v, v
  *   num_axes   1 to 4
  *   axes       [rotary_dim / 2] int32 device array, or NULL: all 0.  Values are
  *              clamped to [0, num_axes - 1].
- * Other arguments, what may overlap, and errors as attn_rope.  One kernel on
- * `stream`.
+ * Other arguments, what may overlap, and errors as attn_rope; neither output may
+ * overlap positions, axes or inv_freq (refused, too).  One kernel on `stream`.
  */
 int attn_rope_axes(const void *q, void *q_out, const void *k, void *k_out, const int *positions, long long axis_stride,
                    long long position_stride, int num_axes, const double *inv_freq, const int *axes, int B, int Hq,
@@ -551,8 +551,10 @@ int attn_rope_axes(const void *q, void *q_out, const void *k, void *k_out, const
  *   seqlens, new_lens, seqlens_out  as in attn_rope_append (capacity max_pages *
  *              page_size)
  *   num_axes, axes  as in attn_rope_axes;  rotary_dim may be 0 (inv_freq NULL)
- * Other arguments, what may overlap, and errors as attn_rope_append.  Rows that
- * no token goes to are left as they were.  One kernel on `stream`.
+ * Other arguments, what may overlap, and errors as attn_rope_append; q_out,
+ * kpages, vpages and seqlens_out may not overlap any other array of the call but
+ * where q_out is q (refused, too).  Rows that no token goes to are left as they were.
+ * One kernel on `stream`.
  */
 int attn_rope_axes_append(const void *q, void *q_out, const void *k, const void *v, void *kpages, void *vpages,
                           const int *page_table, const int *seqlens, const int *positions, long long axis_stride,
