@@ -501,6 +501,13 @@ def _refuse(what, name, t, dtype, shape):
                                   f"contiguous rows (got {got})")
 
 
+def _present(what, name, t):
+    """ATTN_ERR_ARG for a tensor that the call cannot do without."""
+    if t is None:
+        raise AttnError(ATTN_ERR_ARG, f"{what}: {name} is missing")
+    return t
+
+
 def _elsewhere(what, gpu, stream):
     """The context that makes `stream` (or GPU `gpu`'s current one) the current
     stream.  The helpers below call themselves inside it unless it is current
@@ -559,7 +566,7 @@ def rope(q, k, inv_freq, positions=None, interleaved=False, out_scale=1.0, out=N
     address or a torch.cuda.ExternalStream."""
     import torch
     what, bf16 = "rope", torch.bfloat16
-    gpu = q.get_device()
+    gpu = _present(what, "q", q).get_device()
     if stream is not None or gpu < 0 or gpu != torch._C._cuda_getDevice():
         with _elsewhere(what, gpu, stream):
             got = rope(q, k, inv_freq, positions, interleaved, out_scale, out, inverse)
@@ -568,7 +575,7 @@ def rope(q, k, inv_freq, positions=None, interleaved=False, out_scale=1.0, out=N
     if q.dim() != 4 or (k is not None and k.dim() != 4):
         raise AttnError(ATTN_ERR_ARG, "rope: q and k have to be [B, H, N, d]")
     B, Hq, N, d = q.shape
-    pairs = inv_freq.numel()
+    pairs = _present(what, "inv_freq", inv_freq).numel()
     _fits_rows(q, bf16, q.shape, gpu) or _refuse(what, "q", q, bf16, q.shape)
     _fits(inv_freq, torch.float64, (pairs,), gpu) or _refuse(what, "inv_freq", inv_freq, torch.float64, (pairs,))
     per_entry = 0
@@ -619,7 +626,7 @@ def rope_append(q, k, v, kcache, vcache, seqlens, inv_freq=None, start_pos=None,
     seqlens_out)``."""
     import torch
     what, bf16, i32 = "rope_append", torch.bfloat16, torch.int32
-    gpu = q.get_device()
+    gpu = _present(what, "q", q).get_device()
     if stream is not None or gpu < 0 or gpu != torch._C._cuda_getDevice():
         with _elsewhere(what, gpu, stream):
             got = rope_append(q, k, v, kcache, vcache, seqlens, inv_freq, start_pos, new_lens, interleaved, out_scale,
@@ -627,7 +634,7 @@ def rope_append(q, k, v, kcache, vcache, seqlens, inv_freq=None, start_pos=None,
         _lend(stream, q, k, v, kcache, vcache, seqlens, inv_freq, start_pos, new_lens, cache_pos, weights, q_out,
               seqlens_out)
         return got
-    if q.dim() != 4 or kcache.dim() != 4:
+    if q.dim() != 4 or kcache is None or kcache.dim() != 4:
         raise AttnError(ATTN_ERR_ARG, "rope_append: q has to be [B, Hq, T, d], the caches [B, Hkv, max_seqlen, d]")
     B, Hq, T, d = q.shape
     Hkv, s_max = kcache.shape[1], kcache.shape[2]
@@ -707,7 +714,7 @@ def rope_axes(q, k, inv_freq, axes, positions, interleaved=False, out_scale=1.0,
     single axis, positions ``[N]`` or ``[B, N]``)."""
     import torch
     what, bf16 = "rope_axes", torch.bfloat16
-    gpu = q.get_device()
+    gpu = _present(what, "q", q).get_device()
     if stream is not None or gpu < 0 or gpu != torch._C._cuda_getDevice():
         with _elsewhere(what, gpu, stream):
             got = rope_axes(q, k, inv_freq, axes, positions, interleaved, out_scale, out, inverse)
@@ -716,11 +723,10 @@ def rope_axes(q, k, inv_freq, axes, positions, interleaved=False, out_scale=1.0,
     if q.dim() != 4 or (k is not None and k.dim() != 4):
         raise AttnError(ATTN_ERR_ARG, "rope_axes: q and k have to be [B, H, N, d]")
     B, Hq, N, d = q.shape
-    pairs = inv_freq.numel()
+    pairs = _present(what, "inv_freq", inv_freq).numel()
     _fits_rows(q, bf16, q.shape, gpu) or _refuse(what, "q", q, bf16, q.shape)
     _fits(inv_freq, torch.float64, (pairs,), gpu) or _refuse(what, "inv_freq", inv_freq, torch.float64, (pairs,))
-    if positions is None:
-        raise AttnError(ATTN_ERR_ARG, "rope_axes: positions are missing")
+    _present(what, "positions", positions)
     num_axes, axis_stride, per_entry = _axes_positions(what, positions, axes, pairs, B, N, gpu)
     q_out, k_out = (None, None) if out is None else out
     if out is not None and (q_out is None or (k is None) != (k_out is None)):
@@ -770,9 +776,15 @@ def _paged(what, kcache, vcache, page_table, B, gpu):
         if pages != B:
             raise AttnError(ATTN_ERR_ARG, f"{what}: {pages} caches for {B} sequences, and no page table")
         return Hkv, d, pages, page, 1
-    per = page_table.shape[-1]
-    _fits(page_table, torch.int32, (B, per), gpu) or _refuse(what, "page_table", page_table, torch.int32, (B, per))
-    return Hkv, d, pages, page, per
+    return Hkv, d, pages, page, _pages_each(what, page_table, B, gpu)
+
+
+def _pages_each(what, page_table, B, gpu):
+    """Pages a sequence of a table ``[B, max_pages]``."""
+    import torch
+    shape = (B, page_table.shape[-1] if page_table.dim() else 1)
+    _fits(page_table, torch.int32, shape, gpu) or _refuse(what, "page_table", page_table, torch.int32, shape)
+    return shape[1]
 
 
 def rope_axes_append(q, k, v, kcache, vcache, seqlens, inv_freq=None, axes=None, positions=None, page_table=None,
@@ -785,7 +797,7 @@ def rope_axes_append(q, k, v, kcache, vcache, seqlens, inv_freq=None, axes=None,
     are not given; returns ``(q_out, seqlens_out)``."""
     import torch
     what, bf16, i32 = "rope_axes_append", torch.bfloat16, torch.int32
-    gpu = q.get_device()
+    gpu = _present(what, "q", q).get_device()
     if stream is not None or gpu < 0 or gpu != torch._C._cuda_getDevice():
         with _elsewhere(what, gpu, stream):
             got = rope_axes_append(q, k, v, kcache, vcache, seqlens, inv_freq, axes, positions, page_table, new_lens,
@@ -839,7 +851,7 @@ def decode_prefix(q, kprefix, vprefix, kcache, vcache, seqlens, scale=None, weig
     how large one has to be); returns ``(o, lse, workspace)``."""
     import torch
     what, bf16 = "decode_prefix", torch.bfloat16
-    gpu = q.get_device()
+    gpu = _present(what, "q", q).get_device()
     if stream is not None or gpu < 0 or gpu != torch._C._cuda_getDevice():
         with _elsewhere(what, gpu, stream):
             got = decode_prefix(q, kprefix, vprefix, kcache, vcache, seqlens, scale, weights, workspace, with_lse)
@@ -902,7 +914,7 @@ def cache_evict(kcache, vcache, weights, seqlens, keep, recent=0, cache_pos=None
     ``(seqlens_out, workspace)`` (`workspace` is None where none is needed)."""
     import torch
     what, bf16, i32, f32 = "cache_evict", torch.bfloat16, torch.int32, torch.float32
-    gpu = kcache.get_device()
+    gpu = _present(what, "kcache", kcache).get_device()
     if stream is not None or gpu < 0 or gpu != torch._C._cuda_getDevice():
         with _elsewhere(what, gpu, stream):
             got = cache_evict(kcache, vcache, weights, seqlens, keep, recent, cache_pos, cur_pos, out, seqlens_out,
@@ -962,7 +974,7 @@ def tree_mask(parents, seqlens=None, draft_lens=None, with_positions=True, strea
     depth) for `rope_axes_append`, or None."""
     import torch
     what, i32 = "tree_mask", torch.int32
-    gpu = parents.get_device()
+    gpu = _present(what, "parents", parents).get_device()
     if stream is not None or gpu < 0 or gpu != torch._C._cuda_getDevice():
         with _elsewhere(what, gpu, stream):
             got = tree_mask(parents, seqlens, draft_lens, with_positions)
@@ -996,7 +1008,7 @@ def decode_tree(q, kcache, vcache, seqlens, mask=None, draft_lens=None, page_tab
     workspace)``."""
     import torch
     what, i32 = "decode_tree", torch.int32
-    gpu = q.get_device()
+    gpu = _present(what, "q", q).get_device()
     if stream is not None or gpu < 0 or gpu != torch._C._cuda_getDevice():
         with _elsewhere(what, gpu, stream):
             got = decode_tree(q, kcache, vcache, seqlens, mask, draft_lens, page_table, scale, workspace, with_lse)
@@ -1033,14 +1045,14 @@ def decode_tree(q, kcache, vcache, seqlens, mask=None, draft_lens=None, page_tab
     return o, lse, workspace
 
 
-def _layers(what, kcache, vcache, gpu):
+def _layers(what, names, kcache, vcache, gpu):
     """(layers, pages, Hkv, page size, d) of pools with or without a leading dimension of layers."""
     import torch
-    if kcache.dim() not in (4, 5):
-        raise AttnError(ATTN_ERR_ARG, f"{what}: the caches have to be [pages, Hkv, page_size, d], with the layers before it or not")
+    if kcache is None or kcache.dim() not in (4, 5):
+        raise AttnError(ATTN_ERR_ARG, f"{what}: {names[0]} and {names[1]} have to be [pages, Hkv, page_size, d], with the layers before it or not")
     shape = kcache.shape
-    _fits(kcache, torch.bfloat16, shape, gpu) or _refuse(what, "kcache", kcache, torch.bfloat16, shape)
-    _fits(vcache, torch.bfloat16, shape, gpu) or _refuse(what, "vcache", vcache, torch.bfloat16, shape)
+    _fits(kcache, torch.bfloat16, shape, gpu) or _refuse(what, names[0], kcache, torch.bfloat16, shape)
+    _fits(vcache, torch.bfloat16, shape, gpu) or _refuse(what, names[1], vcache, torch.bfloat16, shape)
     return shape if len(shape) == 5 else (1, *shape)
 
 
@@ -1055,19 +1067,18 @@ def tree_accept(kcache, vcache, seqlens, mask, last, page_table=None, seqlens_ou
     counts, and the caller sees to it that its rows have been appended."""
     import torch
     what, i32 = "tree_accept", torch.int32
-    gpu = kcache.get_device()
+    gpu = _present(what, "kcache", kcache).get_device()
     if stream is not None or gpu < 0 or gpu != torch._C._cuda_getDevice():
         with _elsewhere(what, gpu, stream):
             got = tree_accept(kcache, vcache, seqlens, mask, last, page_table, seqlens_out, drafted=drafted)
         _lend(stream, kcache, vcache, seqlens, mask, last, page_table, seqlens_out)
         return got
-    layers, pages, Hkv, page, d = _layers(what, kcache, vcache, gpu)
+    layers, pages, Hkv, page, d = _layers(what, ("kcache", "vcache"), kcache, vcache, gpu)
     if seqlens is None or seqlens.dim() != 1:
         raise AttnError(ATTN_ERR_ARG, "tree_accept: seqlens has to be [B]")
     B, per, T = seqlens.shape[0], 1, 256 if drafted is None else drafted
     if page_table is not None:
-        per = page_table.shape[-1]
-        _fits(page_table, i32, (B, per), gpu) or _refuse(what, "page_table", page_table, i32, (B, per))
+        per = _pages_each(what, page_table, B, gpu)
     _fits(seqlens, i32, (B,), gpu) or _refuse(what, "seqlens", seqlens, i32, (B,))
     _fits(last, i32, (B,), gpu) or _refuse(what, "last", last, i32, (B,))
     if mask is not None:
@@ -1116,19 +1127,19 @@ def pages_extend(page_table, refs, seqlens, new, kpages, vpages, workspace=None,
     missing (then nothing has been changed)."""
     import torch
     what, i32 = "pages_extend", torch.int32
-    gpu = page_table.get_device()
+    gpu = _present(what, "page_table", page_table).get_device()
     if stream is not None or gpu < 0 or gpu != torch._C._cuda_getDevice():
         with _elsewhere(what, gpu, stream):
             got = pages_extend(page_table, refs, seqlens, new, kpages, vpages, workspace, info)
         _lend(stream, page_table, refs, seqlens, new if torch.is_tensor(new) else None, kpages, vpages, workspace, info)
         return got
     B, per, pages = _tables(what, page_table, refs, gpu)
-    layers, n, Hkv, page, d = _layers(what, kpages, vpages, gpu)
+    layers, n, Hkv, page, d = _layers(what, ("kpages", "vpages"), kpages, vpages, gpu)
     if n != pages:
         raise AttnError(ATTN_ERR_ARG, f"pages_extend: {n} pages and {pages} counts")
     _fits(seqlens, i32, (B,), gpu) or _refuse(what, "seqlens", seqlens, i32, (B,))
     each = None
-    if torch.is_tensor(new):
+    if torch.is_tensor(_present(what, "new", new)):
         each, new = new, 0
         _fits(each, i32, (B,), gpu) or _refuse(what, "new", each, i32, (B,))
     if info is None:
@@ -1151,7 +1162,7 @@ def pages_fork(page_table, refs, seqlens, parent, page_size, page_table_out=None
     ``(page_table_out, seqlens_out)``, which replace the old ones."""
     import torch
     what, i32 = "pages_fork", torch.int32
-    gpu = page_table.get_device()
+    gpu = _present(what, "page_table", page_table).get_device()
     if stream is not None or gpu < 0 or gpu != torch._C._cuda_getDevice():
         with _elsewhere(what, gpu, stream):
             got = pages_fork(page_table, refs, seqlens, parent, page_size, page_table_out, seqlens_out)
@@ -1182,7 +1193,7 @@ def pages_trim(page_table, refs, seqlens, keep, page_size, seqlens_out=None, str
     lengths (`seqlens_out` may be `seqlens`)."""
     import torch
     what, i32 = "pages_trim", torch.int32
-    gpu = page_table.get_device()
+    gpu = _present(what, "page_table", page_table).get_device()
     if stream is not None or gpu < 0 or gpu != torch._C._cuda_getDevice():
         with _elsewhere(what, gpu, stream):
             got = pages_trim(page_table, refs, seqlens, keep, page_size, seqlens_out)
@@ -1208,14 +1219,14 @@ def pages_compact(page_table, refs, kpages, vpages, workspace=None, info=None, s
     ``(info, workspace)``: int32 ``[2]``, pages in use and pages moved."""
     import torch
     what, i32 = "pages_compact", torch.int32
-    gpu = page_table.get_device()
+    gpu = _present(what, "page_table", page_table).get_device()
     if stream is not None or gpu < 0 or gpu != torch._C._cuda_getDevice():
         with _elsewhere(what, gpu, stream):
             got = pages_compact(page_table, refs, kpages, vpages, workspace, info)
         _lend(stream, page_table, refs, kpages, vpages, workspace, info)
         return got
     B, per, pages = _tables(what, page_table, refs, gpu)
-    layers, n, Hkv, page, d = _layers(what, kpages, vpages, gpu)
+    layers, n, Hkv, page, d = _layers(what, ("kpages", "vpages"), kpages, vpages, gpu)
     if n != pages:
         raise AttnError(ATTN_ERR_ARG, f"pages_compact: {n} pages and {pages} counts")
     if info is None:
