@@ -1357,7 +1357,8 @@ static int pages_moves(PagesLaunch *a, int *page_table, int *refs, void *kpages,
     size_t bytes = 0;
     rc = pools(kpages, vpages, layers, Hkv, d, num_pages, page_size, &bytes);
     if (rc != ATTN_OK) return rc;
-    if ((long long)Hkv * page_size * (d / 8) >= 0x7fffffffLL) return ATTN_ERR_ARG;  // a page's 16-byte units, in 32 bits
+    // A page's 16-byte units, rounded up to a warp's 256, are counted in 32 bits.
+    if ((long long)Hkv * page_size * (d / 8) > 0x7fffffffLL - 255) return ATTN_ERR_ARG;
     if (!info || !aligned4(info) || !aligned4(seqlens) || !aligned4(new_lens)) return ATTN_ERR_ARG;
     const size_t need = pages_workspace_bytes(B, num_pages), lens = size_t(B) * 4;
     if (!workspace || !aligned16(workspace) || workspace_bytes < need) return ATTN_ERR_WORKSPACE;

@@ -760,7 +760,7 @@ int attn_tree_accept(void *kpages, void *vpages, const int *page_table, const in
  * them (of the highest b) keeps it.  Pages are taken lowest first, in the order of the sequences and slots.
  *   new_lens   [B] int32 new keys of each (below 0: 0), or NULL: T for all
  *   kpages, vpages  [layers, num_pages, Hkv, page_size, d] bf16, d a multiple of 8, at most 512; a page
- *              of one layer has less than 2^35 bytes of K
+ *              of one layer has at most 2^35 - 4096 bytes of K
  *   info       [2] int32 (written): pages taken, pages missing.  If pages are
  *              missing, nothing else is changed.
  *   workspace  attn_pages_workspace_bytes(B, num_pages) bytes, 16-byte aligned
