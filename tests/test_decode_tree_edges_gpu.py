@@ -35,3 +35,46 @@ def test_rows_that_do_not_fill_a_warp(attn, Hq, T, d):
     run_and_check(attn, q, k, v, table, 16, [cap - T, 0, 1, 64, 127, 200, max(0, cap - 1)], parents=random_tree(7, T, 42))
     k, v, _ = a_cache(1, 1, 21000, d, 0, 43)
     run_and_check(attn, q[:1], k, v, None, 0, [20000 - T], parents=random_tree(1, T, 44))
+
+
+def guarded(shape, dtype, skip, seed):
+    """A tensor `skip` bytes behind the start of an allocation, and all of that, filled with a pattern."""
+    size = torch.empty(0, dtype=dtype).element_size()
+    n = torch.Size(shape).numel()
+    whole = torch.randint(0, 128, (skip + n * size + 256,), generator=torch.Generator().manual_seed(seed), dtype=torch.uint8).to(DEV)
+    return whole[skip:skip + n * size].view(dtype).view(shape), whole
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("B,Hq,T,S,page", [
+    (1, 8, 1, 9000, 0), (1, 8, 5, 9000, 16), (7, 8, 5, 300, 16), (2, 16, 8, 3000, 64), (1, 8, 33, 9000, 0), (3, 16, 20, 300, 16),
+    (2, 16, 40, 3000, 64), (40, 8, 5, 500, 64),
+])
+def test_outputs_and_workspace_on_16_bytes(attn, B, Hq, T, S, page, d):
+    """Outputs, queries and a workspace that are 16-byte aligned and no more: the bits of the call that has them on 256
+    bytes, and not a byte around them changed.  Pairs in one piece, cut ones and those that a CTA's chains share."""
+    k, v, table = a_cache(B, 2, S, d, page, 60)
+    q = normal_bf16((B, Hq, T, d), 61, DEV)
+    table = None if table is None else table.to(DEV)
+    per = 1 if page == 0 else table.shape[1]
+    lens = torch.randint(0, S, (B,), generator=torch.Generator().manual_seed(62)).to(torch.int32)
+    lens[0] = S - T
+    lens = lens.to(DEV)
+    mask, _ = attn.tree_mask(random_tree(B, T, 63).to(DEV))
+    want = attn.decode_tree(q, k, v, lens, mask, page_table=table)
+    nbytes = attn.attn_decode_tree_workspace_bytes(B, Hq, 2, T, d, page or S, per)
+    for q_at, o_at, ws_at in ((0, 16, 0), (0, 0, 16), (16, 16, 48)):
+        o, o_all = guarded((B, Hq, T, d), torch.bfloat16, o_at, 64)
+        lse, lse_all = guarded((B, Hq, T), torch.float32, 4, 65)
+        ws, ws_all = guarded((nbytes,), torch.uint8, ws_at, 66)
+        queries = guarded((B, Hq, T, d), torch.bfloat16, q_at, 67)[0]
+        queries.copy_(q)
+        was = [x.clone() for x in (o_all, lse_all, ws_all)]
+        rc = attn.attn_decode_tree(queries, k, v, table, lens, mask, None, o, lse, B, Hq, 2, T, d, d ** -0.5, k.shape[0],
+                                   page or S, per, ws, nbytes)
+        torch.cuda.synchronize()
+        assert rc == attn.ATTN_OK and attn.attn_device_status() == attn.ATTN_OK
+        assert torch.equal(o, want[0]) and torch.equal(lse, want[1])
+        for part, x, old in ((o, o_all, was[0]), (lse, lse_all, was[1]), (ws, ws_all, was[2])):
+            at, n = part.data_ptr() - x.data_ptr(), part.numel() * part.element_size()
+            assert torch.equal(x[:at], old[:at]) and torch.equal(x[at + n:], old[at + n:])
