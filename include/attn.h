@@ -706,6 +706,12 @@ int attn_tree_mask(const int *parents, const int *seqlens, const int *draft_lens
  *   lse        [B, Hq, T] fp32 (natural log), or NULL.  A token that attends no key
  *              (or none whose score is above -inf) gets o = 0, lse = -inf.
  *   Drafted tokens whose row is at or past the capacity have no key.
+ *   Scores, sums and lse are in fp32; probabilities are rounded to bf16 for the
+ *   product with V (off by at most 2^-8 of each), as in attn_decode, and o once
+ *   more.  A key's weight may stand up to 2^16 above its final one in the sums before
+ *   they are divided, so values have to be below 2^111 over the number of keys that a
+ *   token attends (2^81 always do); above that o may be infinite or NaN although
+ *   the exact one is not.
  *   d in {64, 128}; 1 <= Hq / Hkv <= 16; 1 <= T <= 256; B * Hkv * ceil(capacity /
  *   64) < 2^31.
  *   workspace  at least attn_decode_tree_workspace_bytes(...) bytes, 16-byte

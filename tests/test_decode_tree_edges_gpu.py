@@ -78,3 +78,19 @@ def test_outputs_and_workspace_on_16_bytes(attn, B, Hq, T, S, page, d):
         for part, x, old in ((o, o_all, was[0]), (lse, lse_all, was[1]), (ws, ws_all, was[2])):
             at, n = part.data_ptr() - x.data_ptr(), part.numel() * part.element_size()
             assert torch.equal(x[:at], old[:at]) and torch.equal(x[at + n:], old[at + n:])
+
+
+@pytest.mark.parametrize("Hq,T,d", [(8, 6, 64), (8, 6, 128), (8, 40, 64), (8, 40, 128)])
+@pytest.mark.parametrize("S", [500, 5000])
+def test_values_at_their_limit(attn, Hq, T, d, S):
+    """Values of just below 2^111 over the number of keys, all of one sign, and weights that the reference of a row, which
+    stays at its first block's, lets grow as far as it does: 11 log2(e) = 15.9 of 16 binary orders.  Sums before the
+    division reach 2^15.9 2^111 = 2^126.9, just below what 32 bits hold."""
+    k, v, _ = a_cache(2, 1, S, d, 0, 70)
+    n = S - 9
+    k[...] = 11 / d ** 0.5
+    k[:, :, :128] = 0
+    v = ((0.75 + 0.24 * torch.tanh(v.float())) * (2.0 ** 111 / S)).bfloat16()
+    q = torch.ones((2, Hq, T, d), dtype=torch.bfloat16, device=DEV)
+    o, _, _ = run_and_check(attn, q, k, v, None, 0, [n - T, n // 2], parents=random_tree(2, T, 71))
+    assert torch.all(torch.isfinite(o)) and torch.all(o > 2.0 ** 110 / S)
