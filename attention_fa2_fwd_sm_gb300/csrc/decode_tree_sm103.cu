@@ -42,15 +42,18 @@
 //   one token, 64 users of 8001 .. 16001 keys: 436 us contiguous (7.1 TB/s), 459 in pages of 16 (6.9);
 //   16 tokens, 32 users of up to 8192 keys, pages of 64: 148 us (5.8 TB/s), of which some 15 are the start, the last
 //     CTAs' late end (they differ by 6%, as the memory serves some SMs better) and the merge;
-//   64 tokens, 16 users of up to 32768 keys: 572 us, 1570 TFLOP/s (all 512 rows of a pair counted), 0.8 of the rate of a
+//   64 tokens, 16 users of up to 32768 keys: 569 to 582 us, 1570 TFLOP/s (all 512 rows of a pair counted), 0.8 of the rate of a
 //     large matrix product: some 3000 clocks a block of 128 keys, of which the products need 2048;
-//   8 tokens, 128 users of 512 keys: 60 us; a pair costs its start and end (4 us) besides its keys.
+//   8 tokens, 128 users of 512 keys: 61 to 66 us; a pair costs its start and end (4 us) besides its keys.
 // One kernel for both, of 128-key blocks with both chains at every block, took 524 us for the first (pages of 128), 167 for
 // the second and 655 for the third.
 //
 // Precision: scores, maxima, sums, partials in fp32; probabilities are rounded to
-// bf16 for the product with V, because the instruction takes both operands in one
-// 16-bit type; outputs are rounded once more.
+// bf16 for the product with V, whose instruction takes both operands in one 16-bit type;
+// outputs are rounded once more.  Outputs are 0.0023 off (relative, against 64 bits),
+// with probabilities in 32 bits they would be 0.0017 off, by their own rounding.
+// Probabilities as two bf16 terms would get there, for twice the product with V, and
+// twice what the softmax warps pack and store; not taken, nor measured.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 

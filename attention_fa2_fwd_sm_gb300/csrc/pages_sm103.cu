@@ -1,6 +1,5 @@
 // pages_sm103.cu -- the pages of a cache: taken, copied on write, shared by
-// forked sequences, freed, and moved together; and the accepted path of a tree of
-// drafted tokens, moved to the front of its rows.
+// forked sequences, freed, and moved together.
 //
 // A pool holds `num_pages` pages of K and of V in every layer; one table and one
 // array of reference counts serve all layers.  The rules (attn.h has them in full)
@@ -14,9 +13,11 @@
 // so the plans are latency, a handful of dependent passes by one CTA; the copies
 // are HBM-bound, 4 d bytes a row and head read and as many written.  A warp copies
 // 4 KB at a time with all of its loads in flight.  Compaction of 1 GB in 2 layers:
-// 328 us, 6.6 TB/s read and written, 8 CTAs an SM.  A step of 64 beams (fork, then
-// room for one token with copies on write) takes 20.6 us in four launches, of
-// which the plan of the second call, three passes over the tables, is the longest.
+// 328 us, 6.6 TB/s read and written (a grid of 8 CTAs an SM, of which 4 fit at once).
+// A step of 64 beams (fork, then room for one token with copies on write) takes 17.0 us
+// in three launches: the fork 2.2, the rest the plan, up to four passes over lengths,
+// entries and counts by one CTA, and the copies.  Room for one token where no page is
+// shared 10.7 (the copies' launch finds nothing to do); a trim 1.8.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
